@@ -551,8 +551,134 @@ moe_status moe_backward_dropless_profiled(const moe_config* cfg, const moe_weigh
                                           void* dw_down, void* ws, size_t ws_bytes, void* stream,
                                           void* const* stage_events, int32_t n_events);
 
+/* ------------------------------------------------------------------------
+ * Routing by scores (sigmoid or softmax of every logit), with the balancing
+ * bias in the selection only, an optional group limit, and gates made of the
+ * raw scores:
+ *   s_e = 1 / (1 + exp(-l_e))  or  exp(l_e) / sum over the E logits
+ *   key_e = s_e + bias_e
+ *   group g = experts [g E/G, (g+1) E/G); its score is the sum of its
+ *   group_top largest keys; the top_groups best groups stay (equal: lower
+ *   index); with top_groups == n_groups there is no limit
+ *   the k largest keys of the groups that stay, descending, equal keys by
+ *   lower expert index
+ *   gate_j = scale s_j / (sum over the selected s + 1e-20)   (renormalise)
+ *            scale s_j                                       (else)
+ * Selection compares the keys as real numbers (fp64 where fp32 cannot tell
+ * two apart), so it does not depend on the rounding of an fp32 exponential.
+ * A logit or a bias may be -infinity: such a logit scores 0, and an expert
+ * whose bias is -infinity is taken only when nothing else is left.
+ * ------------------------------------------------------------------------ */
+typedef enum { MOE_SCORE_SOFTMAX = 0, MOE_SCORE_SIGMOID = 1 } moe_score;
+
+typedef struct {
+  int32_t score;       /* moe_score                                        */
+  int32_t n_groups;    /* G: divides E, <= 64; 1 = no groups               */
+  int32_t top_groups;  /* groups kept, 1 .. G; top_groups * E/G >= k       */
+  int32_t group_top;   /* 1 or 2: keys summed for a group's score          */
+  int32_t renormalise; /* 0 or 1                                           */
+  float scale;         /* factor of every gate, finite                     */
+  int32_t reserved;    /* must be 0                                        */
+} moe_scoring;
+
+/* logits (device) [T][E] fp32; bias (device) [E] fp32 or NULL; topk_idx
+   (device, out) [T][k]; gates (device, out) [T][k] fp32.  Only T, n_experts
+   and top_k of *cfg are read, and validated as in moe_route. */
+moe_status moe_route_scored(const moe_config* cfg, const moe_scoring* scoring, const float* logits,
+                            const float* bias, int32_t* topk_idx, float* gates, void* stream);
+
+/* Gradient of the gates with respect to the logits for the selection made:
+   with dg_j = scale d_gates[t][j] and S = sum over the selected s + 1e-20,
+     ds_j = (dg_j - sum_i dg_i s_i / S) / S  (renormalise),  dg_j  (else)
+     sigmoid: d_logits[t][e] = ds_j s_j (1 - s_j) at e = topk_idx[t][j], else 0
+     softmax: d_logits[t][e] = s_e (ds_e [e selected] - sum_j ds_j s_j)
+   d_logits (device, out) [T][E] fp32, written whole.  An id outside [0, E)
+   counts as a score of 0; an id that appears twice adds twice.  The bias and
+   the group choice get no gradient: n_groups, top_groups and group_top are
+   validated and otherwise unused. */
+moe_status moe_route_scored_backward(const moe_config* cfg, const moe_scoring* scoring, const float* logits,
+                                     const int32_t* topk_idx, const float* d_gates, float* d_logits,
+                                     void* stream);
+
+/* ------------------------------------------------------------------------
+ * 8-bit values (e4m3: 1 sign, 4 exponent, 3 mantissa bits, largest 448, no
+ * infinities) with one fp32 scale for a block: value = e4m3 * scale.  Blocks
+ * run along K, the contracted (contiguous) dimension, 128 values each:
+ *   1 x 128 blocks (activations):  scales [ceil(K/128)][R], K block first
+ *   128 x 128 blocks (weights):    scales [ceil(R/128)][ceil(K/128)]
+ * Rows are stored K rounded up to 128 bytes apart; the padding is zero.
+ * ------------------------------------------------------------------------ */
+
+/* Quantise x (device) [rows][cols], ldx elements between rows, dtype MOE_F32
+   or MOE_BF16:  per block, amax = max(|x|, 2^-100), scale = amax / 448,
+   q = 448 x / amax rounded to the nearest e4m3 value, ties to even (the
+   quotient rounded once to fp32 before).  block_rows 1 or 128 as above.
+   transpose 0: R = rows, K = cols; 1: the result is that of x^T (R = cols,
+   K = rows), the operand of a gradient's product.
+   q       (device, out, 16-byte aligned) [R][K rounded up to 128]
+   scales  (device, out) as above
+   An infinity or a NaN makes the values of its block unspecified.
+   MOE_ERR_UNSUPPORTED past 2^30 rows or columns or 2^24 - 1 blocks of 128 x
+   128. */
+moe_status moe_quantize(int64_t rows, int64_t cols, const void* x, int64_t ldx, int32_t dtype,
+                        int32_t block_rows, int32_t transpose, void* q, float* scales, void* stream);
+
+/* C[m][n] = sum over K blocks b of a_scale[b][m] bs[b][n] <A[m], B[n]>_b,
+   <,>_b the product over block b, accumulated in fp32, rounded once to
+   out_dtype.  bs is b_scale[b][n] (b_block_rows 1) or b_scale[n / 128][b]
+   (b_block_rows 128).  A linear layer y = x W^T is
+     y  = A: x        (1 x 128),   B: W     (128 x 128)
+     dx = A: dy       (1 x 128),   B: W^T   (128 x 128, quantised transposed)
+     dW = A: dy^T, B: x^T          (1 x 128, both quantised transposed). */
+typedef struct {
+  int64_t M, N, K;      /* K a multiple of 128, <= 2^23; 0: C is zero       */
+  const void* a;        /* [M][lda] e4m3, 16-byte aligned                   */
+  int64_t lda;          /* bytes, >= K, a multiple of 16                    */
+  const float* a_scale; /* [K/128][a_scale_ld]                              */
+  int64_t a_scale_ld;   /* >= M                                             */
+  const void* b;        /* [N][ldb] e4m3, 16-byte aligned                   */
+  int64_t ldb;          /* bytes, >= K, a multiple of 16                    */
+  const float* b_scale; /* b_block_rows 128: [ceil(N/128)][b_scale_ld];
+                           1: [K/128][b_scale_ld]                           */
+  int64_t b_scale_ld;   /* >= K/128, or >= N                                */
+  void* c;              /* [M][ldc] out_dtype                               */
+  int64_t ldc;          /* elements, >= N                                   */
+  int32_t b_block_rows; /* 1 or 128                                         */
+  int32_t out_dtype;    /* moe_dtype of C                                   */
+  int32_t reserved;     /* must be 0                                        */
+} moe_quant_gemm;
+
+/* Workspace of the product (may be 0: then ws may be NULL); only the sizes,
+   leading dimensions and types of *gemm are read. */
+moe_status moe_gemm_quant_ws_bytes(const moe_quant_gemm* gemm, size_t* bytes);
+moe_status moe_gemm_quant(const moe_quant_gemm* gemm, void* ws, size_t ws_bytes, void* stream);
+
+/* Weights of the routed experts in e4m3 with 128 x 128 scales (device). */
+typedef struct {
+  const void* q_gate;  /* [E][F][L]           */
+  const float* s_gate; /* [E][F/128][L/128]   */
+  const void* q_up;    /* [E][F][L]           */
+  const float* s_up;
+  const void* q_down;  /* [E][L][F]           */
+  const float* s_down; /* [E][L/128][F/128]   */
+} moe_quant_experts;
+
+/* moe_experts_dropless with 8-bit weights: xs (device, bf16 [T*k][L]) is
+   quantised in 1 x 128 blocks, the hidden rows silu(a) * b are quantised
+   the same way from their fp32 values, both products accumulate in fp32 and
+   expert_out (device, bf16 [T*k][L]) is rounded once.  Rows outside every
+   expert's range are not written; offsets are kept inside [0, T*k].
+   bf16 configs with d_latent and d_ff multiples of 128 (MOE_ERR_UNSUPPORTED
+   else).  For a straight-through gradient, moe_experts_backward_dropless
+   takes the bf16 weights that were quantised. */
+moe_status moe_experts_dropless_quant_ws_bytes(const moe_config* cfg, size_t* bytes);
+moe_status moe_experts_dropless_quant(const moe_config* cfg, const void* xs, const int32_t* expert_offsets,
+                                      const moe_quant_experts* w, void* expert_out, void* ws, size_t ws_bytes,
+                                      void* stream);
+
 #ifdef __cplusplus
 }
 #endif
+
 
 #endif /* MOE_H */

@@ -20,7 +20,8 @@ __all__ = ["make_config", "plan", "route", "dispatch", "experts", "combine", "fo
            "dispatch_dropless", "experts_dropless", "combine_dropless", "forward_dropless",
            "combine_backward", "experts_backward", "dispatch_backward", "route_backward",
            "combine_backward_dropless", "experts_backward_dropless", "dispatch_backward_dropless",
-           "BackwardRouted", "library", "MoeError"]
+           "BackwardRouted", "scoring", "route_scored", "route_scored_backward", "quantize", "gemm_quant",
+           "experts_dropless_quant", "library", "MoeError"]
 
 MoeError = abi.MoeError
 _DT = {"f32": abi.MOE_F32, "bf16": abi.MOE_BF16, torch.float32: abi.MOE_F32,
@@ -522,3 +523,186 @@ def dispatch_backward_dropless(cfg, row_of, d_xs, dz=None):
         C.byref(cfg), _ptr(row_of), _ptr(d_xs), _ptr(dz), _stream(dev)))
     return dz
 
+
+# ---------------------------------------------------------- scored routing
+def _check(ok, what):
+    if not ok:
+        raise ValueError(what)
+
+
+def _rows(t, shape, dtype, what, dev=None):
+    """A contiguous device tensor of this shape and type (the entry points take plain pointers)."""
+    _check(isinstance(t, torch.Tensor) and t.dtype == dtype and tuple(t.shape) == tuple(shape) and t.is_contiguous()
+           and t.is_cuda and (dev is None or t.device == dev),
+           f"{what} must be a contiguous {dtype} tensor of shape {tuple(shape)}"
+           + (f" on {dev}" if dev is not None else " on a GPU"))
+    return t
+
+
+class _on:
+    """The tensors' device, made current for the call where it is not."""
+
+    def __init__(self, dev):
+        self.dev, self.prev = dev, None
+
+    def __enter__(self):
+        cur = torch.cuda.current_device()
+        if cur != self.dev.index:
+            self.prev = cur
+            torch.cuda.set_device(self.dev)
+        return C.c_void_p(torch.cuda.current_stream(self.dev).cuda_stream)
+
+    def __exit__(self, *exc):
+        if self.prev is not None:
+            torch.cuda.set_device(self.prev)
+        return False
+
+
+def scoring(score="sigmoid", n_groups=1, top_groups=1, group_top=2, renormalise=True, scale=1.0) -> abi.MoeScoring:
+    """How route_scored makes scores, limits groups and scales gates (moe_scoring)."""
+    _check(score in ("sigmoid", "softmax"), "score is 'sigmoid' or 'softmax'")
+    return abi.MoeScoring(score=abi.MOE_SCORE_SIGMOID if score == "sigmoid" else abi.MOE_SCORE_SOFTMAX,
+                          n_groups=n_groups, top_groups=top_groups, group_top=group_top,
+                          renormalise=int(bool(renormalise)), scale=scale, reserved=0)
+
+
+def route_scored(cfg, sc: abi.MoeScoring, logits: torch.Tensor, bias: Optional[torch.Tensor] = None, out=None):
+    """(topk_idx [T, k] int32, gates [T, k] fp32) by scores (moe_route_scored)."""
+    T, k, E = cfg.T, cfg.top_k, cfg.n_experts
+    dev = _rows(logits, (T, E), torch.float32, "logits").device
+    if bias is not None:
+        _rows(bias, (E,), torch.float32, "bias", dev)
+    topk = torch.empty((T, k), dtype=torch.int32, device=dev) if out is None else \
+        _rows(out["topk_idx"], (T, k), torch.int32, "out['topk_idx']", dev)
+    gates = torch.empty((T, k), dtype=torch.float32, device=dev) if out is None else \
+        _rows(out["gates"], (T, k), torch.float32, "out['gates']", dev)
+    with _on(dev) as stream:
+        abi.check("moe_route_scored", library().moe_route_scored(
+            C.byref(cfg), C.byref(sc), _ptr(logits), _ptr(bias), _ptr(topk), _ptr(gates), stream))
+    return topk, gates
+
+
+def route_scored_backward(cfg, sc: abi.MoeScoring, logits, topk_idx, d_gates, d_logits=None):
+    """d_logits [T, E] fp32 = transpose of route_scored's gates for the selection made."""
+    T, k, E = cfg.T, cfg.top_k, cfg.n_experts
+    dev = _rows(logits, (T, E), torch.float32, "logits").device
+    _rows(topk_idx, (T, k), torch.int32, "topk_idx", dev)
+    _rows(d_gates, (T, k), torch.float32, "d_gates", dev)
+    d_logits = torch.empty_like(logits) if d_logits is None else \
+        _rows(d_logits, (T, E), torch.float32, "d_logits", dev)
+    with _on(dev) as stream:
+        abi.check("moe_route_scored_backward", library().moe_route_scored_backward(
+            C.byref(cfg), C.byref(sc), _ptr(logits), _ptr(topk_idx), _ptr(d_gates), _ptr(d_logits), stream))
+    return d_logits
+
+
+# ------------------------------------------------------- block-scaled e4m3
+def quantize(x: torch.Tensor, block_rows: int = 1, transpose: bool = False, out=None):
+    """(q, scales) of x [rows, cols] (bf16 or fp32; rows may be strided) in
+    e4m3 with one fp32 scale for 1 x 128 or 128 x 128 blocks (moe_quantize).
+    With transpose, of x^T.  q [R, K padded to 128]; scales [K/128, R], or
+    [R/128, K/128] for 128 x 128 blocks."""
+    _check(isinstance(x, torch.Tensor) and x.dim() == 2 and x.is_cuda and x.dtype in (torch.bfloat16, torch.float32),
+           "x must be a two-dimensional bf16 or fp32 tensor on a GPU")
+    _check(x.shape[1] <= 1 or x.stride(1) == 1, "the columns of x must be contiguous")
+    _check(block_rows in (1, 128), "block_rows is 1 or 128")
+    rows, cols = x.shape
+    ld = x.stride(0) if rows > 1 else cols
+    _check(ld >= cols, "the rows of x must not overlap")
+    R, K = (cols, rows) if transpose else (rows, cols)
+    kb = -(-K // 128)
+    dev = x.device
+    qs, ss = (R, kb * 128), ((kb, R) if block_rows == 1 else (-(-R // 128), kb))
+    q = torch.empty(qs, dtype=torch.float8_e4m3fn, device=dev) if out is None else \
+        _rows(out[0], qs, torch.float8_e4m3fn, "out[0]", dev)
+    s = torch.empty(ss, dtype=torch.float32, device=dev) if out is None else \
+        _rows(out[1], ss, torch.float32, "out[1]", dev)
+    with _on(dev) as stream:
+        abi.check("moe_quantize", library().moe_quantize(
+            rows, cols, _ptr(x), ld, _DT[x.dtype], block_rows, int(transpose), _ptr(q), _ptr(s), stream))
+    return q, s
+
+
+def _operand(q, what, dev=None):
+    _check(isinstance(q, torch.Tensor) and q.dim() == 2 and q.is_cuda and q.dtype == torch.float8_e4m3fn
+           and (dev is None or q.device == dev), f"{what} must be a two-dimensional e4m3 tensor on one GPU")
+    _check(q.shape[1] <= 1 or q.stride(1) == 1, f"the columns of {what} must be contiguous")
+    return q.stride(0) if q.shape[0] > 1 else q.shape[1]
+
+
+def _scale_ld(s, shape, what, dev):
+    _check(isinstance(s, torch.Tensor) and s.dtype == torch.float32 and tuple(s.shape) == shape and s.device == dev
+           and (shape[1] <= 1 or s.stride(1) == 1),
+           f"{what} must be an fp32 tensor of shape {shape} with contiguous columns")
+    return s.stride(0) if shape[0] > 1 else max(shape[1], 1)
+
+
+def gemm_quant(a, a_scales, b, b_scales, block_rows: int = 128, out_dtype=torch.bfloat16, out=None, ws=None):
+    """C [M, N] = A B^T of e4m3 operands with block scales (moe_gemm_quant):
+    a [M, K] with a_scales [K/128, M]; b [N, K] with b_scales [N/128, K/128]
+    (block_rows 128) or [K/128, N] (block_rows 1).  Rows may be strided (a
+    slice of a larger batch); C is bf16 or fp32."""
+    lda = _operand(a, "a")
+    dev = a.device
+    ldb = _operand(b, "b", dev)
+    (M, K), N = a.shape, b.shape[0]
+    _check(b.shape[1] == K and K % 128 == 0, "a and b must have the same K, a multiple of 128")
+    _check(block_rows in (1, 128), "block_rows is 1 or 128")
+    _check(out_dtype in (torch.bfloat16, torch.float32), "out_dtype is bfloat16 or float32")
+    kb = K // 128
+    sa = _scale_ld(a_scales, (kb, M), "a_scales", dev)
+    sb = _scale_ld(b_scales, (kb, N) if block_rows == 1 else (-(-N // 128), kb), "b_scales", dev)
+    if out is None:
+        out = torch.empty((M, N), dtype=out_dtype, device=dev)
+    else:
+        _check(tuple(out.shape) == (M, N) and out.dtype == out_dtype and out.device == dev
+               and (N <= 1 or out.stride(1) == 1) and (M <= 1 or out.stride(0) >= N),
+               f"out must be a {out_dtype} tensor of shape {(M, N)} with contiguous columns")
+    g = abi.MoeQuantGemm(M=M, N=N, K=K, a=a.data_ptr(), lda=lda, a_scale=a_scales.data_ptr(), a_scale_ld=sa,
+                         b=b.data_ptr(), ldb=ldb, b_scale=b_scales.data_ptr(), b_scale_ld=sb, c=out.data_ptr(),
+                         ldc=out.stride(0) if M > 1 else N, b_block_rows=block_rows, out_dtype=_DT[out_dtype],
+                         reserved=0)
+    lib = library()
+    n = C.c_size_t(0)
+    abi.check("moe_gemm_quant_ws_bytes", lib.moe_gemm_quant_ws_bytes(C.byref(g), C.byref(n)))
+    if ws is None and n.value:
+        ws = _ws(n.value, dev)
+    with _on(dev) as stream:
+        abi.check("moe_gemm_quant", lib.moe_gemm_quant(
+            C.byref(g), _ptr(ws), ws.numel() if ws is not None else 0, stream))
+    return out
+
+
+def _quant_experts(cfg, w_gate, w_up, w_down, dev):
+    E, L, F = cfg.n_experts, cfg.d_latent, cfg.d_ff
+    f = {}
+    for name, (q, s), r, c in (("gate", w_gate, F, L), ("up", w_up, F, L), ("down", w_down, L, F)):
+        f["q_" + name] = _rows(q, (E, r, c), torch.float8_e4m3fn, f"w_{name}[0]", dev).data_ptr()
+        f["s_" + name] = _rows(s, (E, r // 128, c // 128), torch.float32, f"w_{name}[1]", dev).data_ptr()
+    return abi.MoeQuantExperts(**f)
+
+
+def experts_dropless_quant_ws_bytes(cfg) -> int:
+    n = C.c_size_t(0)
+    abi.check("moe_experts_dropless_quant_ws_bytes",
+              library().moe_experts_dropless_quant_ws_bytes(C.byref(cfg), C.byref(n)))
+    return int(n.value)
+
+
+def experts_dropless_quant(cfg, xs, expert_offsets, w_gate, w_up, w_down, expert_out=None, ws=None):
+    """experts_dropless with e4m3 weights (moe_experts_dropless_quant): each
+    weight a (q [E, out, in], scales [E, out/128, in/128]) pair."""
+    n, L = cfg.T * cfg.top_k, cfg.d_latent
+    nbytes = experts_dropless_quant_ws_bytes(cfg)
+    dev = _rows(xs, (n, L), torch.bfloat16, "xs").device
+    _rows(expert_offsets, (cfg.n_experts + 1,), torch.int32, "expert_offsets", dev)
+    w = _quant_experts(cfg, w_gate, w_up, w_down, dev)
+    expert_out = torch.empty_like(xs) if expert_out is None else \
+        _rows(expert_out, (n, L), torch.bfloat16, "expert_out", dev)
+    if ws is None:
+        ws = _ws(nbytes, dev)
+    with _on(dev) as stream:
+        abi.check("moe_experts_dropless_quant", library().moe_experts_dropless_quant(
+            C.byref(cfg), _ptr(xs), _ptr(expert_offsets), C.byref(w), _ptr(expert_out), _ptr(ws), ws.numel(),
+            stream))
+    return expert_out

@@ -14,6 +14,7 @@ LIB_PATH = os.environ.get("MOE_LIB") or os.path.join(_PKG, "libmoe.so")
 
 MOE_OK, MOE_ERR_INVALID_ARG, MOE_ERR_UNSUPPORTED, MOE_ERR_WORKSPACE, MOE_ERR_HIP = range(5)
 MOE_F32, MOE_BF16 = 0, 1
+MOE_SCORE_SOFTMAX, MOE_SCORE_SIGMOID = 0, 1
 STATUS_NAMES = {0: "MOE_OK", 1: "MOE_ERR_INVALID_ARG", 2: "MOE_ERR_UNSUPPORTED",
                 3: "MOE_ERR_WORKSPACE", 4: "MOE_ERR_HIP"}
 
@@ -61,6 +62,22 @@ class MoeDroplessTaps(C.Structure):
     _fields_ = [(n, C.c_void_p) for n in (
         "logits", "topk_idx", "gates", "row_of", "expert_offsets", "z", "xs", "expert_out",
         "y_latent")]
+
+
+class MoeScoring(C.Structure):
+    _fields_ = [("score", C.c_int32), ("n_groups", C.c_int32), ("top_groups", C.c_int32), ("group_top", C.c_int32),
+                ("renormalise", C.c_int32), ("scale", C.c_float), ("reserved", C.c_int32)]
+
+
+class MoeQuantGemm(C.Structure):
+    _fields_ = [("M", C.c_int64), ("N", C.c_int64), ("K", C.c_int64), ("a", C.c_void_p), ("lda", C.c_int64),
+                ("a_scale", C.c_void_p), ("a_scale_ld", C.c_int64), ("b", C.c_void_p), ("ldb", C.c_int64),
+                ("b_scale", C.c_void_p), ("b_scale_ld", C.c_int64), ("c", C.c_void_p), ("ldc", C.c_int64),
+                ("b_block_rows", C.c_int32), ("out_dtype", C.c_int32), ("reserved", C.c_int32)]
+
+
+class MoeQuantExperts(C.Structure):
+    _fields_ = [(n, C.c_void_p) for n in ("q_gate", "s_gate", "q_up", "s_up", "q_down", "s_down")]
 
 
 # exported symbols and their signatures
@@ -125,6 +142,14 @@ SIGNATURES = {
                                                C.POINTER(MoeTaps), _P, _P, _P, _P, _P, _P, _P,
                                                C.c_size_t, _P, C.POINTER(C.c_void_p),
                                                C.c_int32]),
+    "moe_route_scored": (C.c_int, [C.POINTER(MoeConfig), C.POINTER(MoeScoring), _P, _P, _P, _P, _P]),
+    "moe_route_scored_backward": (C.c_int, [C.POINTER(MoeConfig), C.POINTER(MoeScoring), _P, _P, _P, _P, _P]),
+    "moe_quantize": (C.c_int, [C.c_int64, C.c_int64, _P, C.c_int64, C.c_int32, C.c_int32, C.c_int32, _P, _P, _P]),
+    "moe_gemm_quant_ws_bytes": (C.c_int, [C.POINTER(MoeQuantGemm), C.POINTER(C.c_size_t)]),
+    "moe_gemm_quant": (C.c_int, [C.POINTER(MoeQuantGemm), _P, C.c_size_t, _P]),
+    "moe_experts_dropless_quant_ws_bytes": (C.c_int, [C.POINTER(MoeConfig), C.POINTER(C.c_size_t)]),
+    "moe_experts_dropless_quant": (C.c_int, [C.POINTER(MoeConfig), _P, _P, C.POINTER(MoeQuantExperts), _P, _P,
+                                             C.c_size_t, _P]),
 }
 
 STAGES = ["latent", "router", "topk", "assign", "scatter", "recv_bin", "expert_rows",

@@ -264,4 +264,83 @@ hipError_t launch_bwd_dh(const BwdDgrad& p, int64_t max_entries, hipStream_t s);
 hipError_t launch_bwd_du(const BwdDgrad& p, int64_t max_entries, hipStream_t s);
 hipError_t launch_bwd_wgrad(const BwdWgrad& p, hipStream_t s);
 
+// ---------------------------------------------------------- scored routing
+// Scores, balancing bias, group limit, top-k, gates (route_scored.hip).
+struct ScoreArgs {
+  int64_t T;
+  int E, k;
+  int sigmoid;     // scores: 1 sigmoid, 0 softmax over the E logits
+  int groups;      // contiguous groups of E / groups experts
+  int top_groups;  // groups kept
+  int group_top;   // 1 or 2: keys of a group that its score sums
+  int renorm;
+  float scale;
+};
+hipError_t launch_route_scored(const ScoreArgs& a, const float* logits, const float* bias, int32_t* topk,
+                               float* gates, hipStream_t s);
+hipError_t launch_route_scored_bwd(const ScoreArgs& a, const float* logits, const int32_t* topk,
+                                   const float* d_gates, float* d_logits, hipStream_t s);
+
+// ------------------------------------------------------- block-scaled e4m3
+// K blocks of 128 values share one fp32 scale (quant.hip, gemm_quant.hip).
+constexpr int kQB = 128;
+struct QuantizeArgs {
+  const void* x;
+  int64_t rows, cols, ld;  // source, ld in elements
+  int dt;
+  int block_rows;  // 1 or 128
+  bool transpose;
+  char* q;         // [R][ldq] bytes, R = rows (cols if transposed)
+  int64_t ldq;
+  float* scale;    // block_rows 1: [K blocks][scale_ld]; 128: [R blocks][scale_ld]
+  int64_t scale_ld;
+};
+hipError_t launch_quantize(const QuantizeArgs& a, hipStream_t s);
+
+// C = A B^T over e4m3 rows with scales.  With offsets (grouped): expert e's
+// rows of A and C are [offsets[e], offsets[e+1]), its weights B + e * b_stride.
+struct QuantGemm {
+  const char* A;
+  int64_t lda;            // bytes
+  const float* a_scale;   // [K blocks][a_scale_ld]
+  int64_t a_scale_ld;
+  const char* B;
+  int64_t ldb;            // bytes
+  const float* b_scale;   // b_rows 128: [N blocks][b_scale_ld]; 1: [K blocks][b_scale_ld]
+  int64_t b_scale_ld;
+  int b_rows;
+  int64_t M, N;           // grouped: M = rows of all experts together
+  int K;
+  int out_dt;
+  void* C;
+  int64_t ldc;            // elements
+  const int32_t* offsets; // [E+1] or null
+  int E;
+  int64_t b_stride, b_scale_stride;  // bytes / floats between experts
+};
+int64_t quant_gemm_ws_bytes(const QuantGemm& g);
+hipError_t launch_quant_gemm(const QuantGemm& g, void* ws, hipStream_t s);
+
+// H = quantised silu(A Wg^T) * (A Wu^T): [rows][F] e4m3 with one scale per row
+// and 128 features.  offsets null: every group e takes all M rows and writes
+// its features at column e * F.
+struct QuantGateUp {
+  const char* A;
+  int64_t lda;
+  const float* a_scale;   // [K blocks][a_scale_ld]
+  int64_t a_scale_ld;
+  const char* Wg;         // [E][F][K]
+  const float* sg;        // [E][F / 128][K / 128]
+  const char* Wu;
+  const float* su;
+  int64_t M;
+  int E, F, K;
+  const int32_t* offsets;
+  char* H;
+  int64_t ldh;            // bytes
+  float* h_scale;         // [feature blocks][h_scale_ld]
+  int64_t h_scale_ld;
+};
+hipError_t launch_quant_gate_up(const QuantGateUp& g, hipStream_t s);
+
 }  // namespace moe

@@ -1444,3 +1444,268 @@ MOE_API moe_status moe_backward_dropless_profiled(const moe_config* cfg, const m
   return backward_dropless_impl(cfg, w, saved, dy_latent, dz, d_logits, dw_gate, dw_up, dw_down, ws, ws_bytes,
                                 stream, stage_events, n_events);
 }
+
+// ------------------------------------------------------------------ scored routing
+namespace {
+
+constexpr int kMaxGroups = 64;  // one lane of a wavefront per group
+
+moe_status check_scoring(const moe_config* c, const moe_scoring* sc, moe::ScoreArgs* a) {
+  moe_status st = check_route_shape(c);
+  if (st != MOE_OK) return st;
+  if (!sc || c->top_k > c->n_experts) return MOE_ERR_INVALID_ARG;
+  if (sc->score != MOE_SCORE_SOFTMAX && sc->score != MOE_SCORE_SIGMOID) return MOE_ERR_INVALID_ARG;
+  if (sc->n_groups < 1 || c->n_experts % sc->n_groups || sc->top_groups < 1 || sc->top_groups > sc->n_groups ||
+      sc->group_top < 1 || sc->group_top > 2)
+    return MOE_ERR_INVALID_ARG;
+  if (sc->top_groups * (c->n_experts / sc->n_groups) < c->top_k) return MOE_ERR_INVALID_ARG;
+  if ((sc->renormalise != 0 && sc->renormalise != 1) || sc->reserved != 0) return MOE_ERR_INVALID_ARG;
+  if (!(sc->scale - sc->scale == 0.0f)) return MOE_ERR_INVALID_ARG;  // an infinity or a NaN
+  if (sc->n_groups > kMaxGroups) return MOE_ERR_UNSUPPORTED;
+  a->T = c->T;
+  a->E = c->n_experts;
+  a->k = c->top_k;
+  a->sigmoid = sc->score == MOE_SCORE_SIGMOID;
+  a->groups = sc->top_groups == sc->n_groups ? 1 : sc->n_groups;  // every group kept: no limit
+  a->top_groups = a->groups == 1 ? 1 : sc->top_groups;
+  a->group_top = sc->group_top;
+  a->renorm = sc->renormalise;
+  a->scale = sc->scale;
+  return MOE_OK;
+}
+
+}  // namespace
+
+MOE_API moe_status moe_route_scored(const moe_config* cfg, const moe_scoring* scoring, const float* logits,
+                                    const float* bias, int32_t* topk_idx, float* gates, void* stream) {
+  moe::ScoreArgs a{};
+  moe_status st = check_scoring(cfg, scoring, &a);
+  if (st != MOE_OK) return st;
+  if (cfg->T > 0 && (!logits || !topk_idx || !gates)) return MOE_ERR_INVALID_ARG;
+  return hip_status(moe::launch_route_scored(a, logits, bias, topk_idx, gates, static_cast<hipStream_t>(stream)));
+}
+
+MOE_API moe_status moe_route_scored_backward(const moe_config* cfg, const moe_scoring* scoring, const float* logits,
+                                             const int32_t* topk_idx, const float* d_gates, float* d_logits,
+                                             void* stream) {
+  moe::ScoreArgs a{};
+  moe_status st = check_scoring(cfg, scoring, &a);
+  if (st != MOE_OK) return st;
+  if (cfg->T > 0 && (!logits || !topk_idx || !d_gates || !d_logits)) return MOE_ERR_INVALID_ARG;
+  return hip_status(
+      moe::launch_route_scored_bwd(a, logits, topk_idx, d_gates, d_logits, static_cast<hipStream_t>(stream)));
+}
+
+// ------------------------------------------------------------------ block-scaled e4m3
+namespace {
+
+constexpr int64_t kMaxQuantTiles = (int64_t(1) << 24) - 1;  // 256-thread workgroups of one launch
+constexpr int64_t kMaxQuantRows = int64_t(1) << 30;         // rows of an operand of moe_gemm_quant
+constexpr int64_t kMaxQuantK = int64_t(1) << 23;            // 256 rows of K bytes stay below 2^31
+
+bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15) == 0; }
+bool aligned_to(const void* p, int64_t n) { return reinterpret_cast<uintptr_t>(p) % (uintptr_t)n == 0; }
+int64_t align128(int64_t x) { return (x + 127) & ~int64_t(127); }
+
+moe_status check_gemm_quant(const moe_quant_gemm* q, moe::QuantGemm* g) {
+  if (!q) return MOE_ERR_INVALID_ARG;
+  if (q->M < 0 || q->N < 0 || q->K < 0 || q->reserved != 0) return MOE_ERR_INVALID_ARG;
+  if (q->out_dtype != MOE_F32 && q->out_dtype != MOE_BF16) return MOE_ERR_INVALID_ARG;
+  if (q->b_block_rows != 1 && q->b_block_rows != 128) return MOE_ERR_INVALID_ARG;
+  if (q->K % 128) return MOE_ERR_INVALID_ARG;
+  if (q->M > kMaxQuantRows || q->N > kMaxQuantRows || q->K > kMaxQuantK) return MOE_ERR_UNSUPPORTED;
+  const int64_t kb = q->K / 128;
+  const int64_t nb = q->b_block_rows == 128 ? kb : q->N;
+  if (q->lda < q->K || q->ldb < q->K || q->ldc < q->N || q->a_scale_ld < q->M || q->b_scale_ld < nb)
+    return MOE_ERR_INVALID_ARG;
+  if (q->lda > kMaxQuantK || q->ldb > kMaxQuantK) return MOE_ERR_UNSUPPORTED;
+  if (q->lda % 16 || q->ldb % 16) return MOE_ERR_UNSUPPORTED;
+  g->lda = q->lda;
+  g->a_scale_ld = q->a_scale_ld;
+  g->ldb = q->ldb;
+  g->b_scale_ld = q->b_scale_ld;
+  g->b_rows = q->b_block_rows;
+  g->M = q->M;
+  g->N = q->N;
+  g->K = (int)q->K;
+  g->out_dt = q->out_dtype;
+  g->ldc = q->ldc;
+  return MOE_OK;
+}
+
+// Grouped SwiGLU in e4m3 over expert-ordered bf16 rows: its workspace.
+struct QuantExpertsWs {
+  char* xq;
+  float* xs;
+  char* hq;
+  float* hs;
+  void* gemm;
+};
+int64_t carve_experts_quant(const moe_config* c, int64_t n, void* ws, QuantExpertsWs* w) {
+  const int64_t L = c->d_latent, F = c->d_ff;
+  Carver cv{static_cast<char*>(ws), 0};
+  w->xq = static_cast<char*>(cv.take(n * L));
+  w->xs = static_cast<float*>(cv.take(n * (L / 128) * 4));
+  w->hq = static_cast<char*>(cv.take(n * F));
+  w->hs = static_cast<float*>(cv.take(n * (F / 128) * 4));
+  moe::QuantGemm d{};
+  d.M = n;
+  d.N = L;
+  d.K = (int)F;
+  d.E = c->n_experts;
+  w->gemm = cv.take(moe::quant_gemm_ws_bytes(d));
+  return cv.used;
+}
+
+moe_status check_quant_config(const moe_config* cfg, moe_plan* p) {
+  moe_status st = check_dropless(cfg, p);
+  if (st != MOE_OK) return st;
+  if (cfg->d_latent % 128 || cfg->d_ff % 128) return MOE_ERR_UNSUPPORTED;
+  return MOE_OK;
+}
+
+moe_status run_experts_quant(const moe_config* c, const moe_plan& p, const void* xs, const int32_t* offsets,
+                             const moe_quant_experts* w, void* out, void* ws, hipStream_t s) {
+  const int64_t n = p.dropless_rows, L = c->d_latent, F = c->d_ff;
+  QuantExpertsWs q;
+  carve_experts_quant(c, n, ws, &q);
+  moe::QuantizeArgs z{};
+  z.x = xs;
+  z.rows = n;
+  z.cols = z.ld = z.ldq = L;
+  z.dt = moe::DT_BF16;
+  z.block_rows = 1;
+  z.q = q.xq;
+  z.scale = q.xs;
+  z.scale_ld = n;
+  hipError_t e = moe::launch_quantize(z, s);
+  if (e != hipSuccess) return MOE_ERR_HIP;
+  moe::QuantGateUp u{};
+  u.A = q.xq;
+  u.lda = L;
+  u.a_scale = q.xs;
+  u.a_scale_ld = n;
+  u.Wg = static_cast<const char*>(w->q_gate);
+  u.sg = w->s_gate;
+  u.Wu = static_cast<const char*>(w->q_up);
+  u.su = w->s_up;
+  u.M = n;
+  u.E = c->n_experts;
+  u.F = (int)F;
+  u.K = (int)L;
+  u.offsets = offsets;
+  u.H = q.hq;
+  u.ldh = F;
+  u.h_scale = q.hs;
+  u.h_scale_ld = n;
+  e = moe::launch_quant_gate_up(u, s);
+  if (e != hipSuccess) return MOE_ERR_HIP;
+  moe::QuantGemm d{};
+  d.A = q.hq;
+  d.lda = F;
+  d.a_scale = q.hs;
+  d.a_scale_ld = n;
+  d.B = static_cast<const char*>(w->q_down);
+  d.ldb = F;
+  d.b_scale = w->s_down;
+  d.b_scale_ld = F / 128;
+  d.b_rows = 128;
+  d.M = n;
+  d.N = L;
+  d.K = (int)F;
+  d.out_dt = moe::DT_BF16;
+  d.C = out;
+  d.ldc = L;
+  d.offsets = offsets;
+  d.E = c->n_experts;
+  d.b_stride = L * F;
+  d.b_scale_stride = (L / 128) * (F / 128);
+  return hip_status(moe::launch_quant_gemm(d, q.gemm, s));
+}
+
+bool quant_experts_valid(const moe_quant_experts* w) {
+  return w && w->q_gate && w->s_gate && w->q_up && w->s_up && w->q_down && w->s_down && aligned16(w->q_gate) &&
+         aligned16(w->q_up) && aligned16(w->q_down);
+}
+
+}  // namespace
+
+MOE_API moe_status moe_quantize(int64_t rows, int64_t cols, const void* x, int64_t ldx, int32_t dtype,
+                                int32_t block_rows, int32_t transpose, void* q, float* scales, void* stream) {
+  if (rows < 0 || cols < 0 || ldx < cols) return MOE_ERR_INVALID_ARG;
+  if ((dtype != MOE_F32 && dtype != MOE_BF16) || (block_rows != 1 && block_rows != 128) ||
+      (transpose != 0 && transpose != 1))
+    return MOE_ERR_INVALID_ARG;
+  if (rows > kMaxQuantRows || cols > kMaxQuantRows || ceil_div(rows, 128) * ceil_div(cols, 128) > kMaxQuantTiles)
+    return MOE_ERR_UNSUPPORTED;
+  if (rows == 0 || cols == 0) return MOE_OK;
+  if (!x || !q || !scales || !aligned16(q) || !aligned_to(x, dtype == MOE_BF16 ? 2 : 4) || !aligned_to(scales, 4))
+    return MOE_ERR_INVALID_ARG;
+  moe::QuantizeArgs a{};
+  a.x = x;
+  a.rows = rows;
+  a.cols = cols;
+  a.ld = ldx;
+  a.dt = dtype;
+  a.block_rows = block_rows;
+  a.transpose = transpose != 0;
+  const int64_t R = transpose ? cols : rows, K = transpose ? rows : cols;
+  a.q = static_cast<char*>(q);
+  a.ldq = align128(K);
+  a.scale = scales;
+  a.scale_ld = block_rows == 1 ? R : align128(K) / 128;
+  return hip_status(moe::launch_quantize(a, static_cast<hipStream_t>(stream)));
+}
+
+MOE_API moe_status moe_gemm_quant_ws_bytes(const moe_quant_gemm* gemm, size_t* bytes) {
+  moe::QuantGemm g{};
+  moe_status st = check_gemm_quant(gemm, &g);
+  if (st != MOE_OK) return st;
+  if (!bytes) return MOE_ERR_INVALID_ARG;
+  *bytes = (size_t)align256(moe::quant_gemm_ws_bytes(g));
+  return MOE_OK;
+}
+
+MOE_API moe_status moe_gemm_quant(const moe_quant_gemm* gemm, void* ws, size_t ws_bytes, void* stream) {
+  moe::QuantGemm g{};
+  moe_status st = check_gemm_quant(gemm, &g);
+  if (st != MOE_OK) return st;
+  if (g.M == 0 || g.N == 0) return MOE_OK;
+  if (!gemm->c || !aligned_to(gemm->c, gemm->out_dtype == MOE_BF16 ? 2 : 4)) return MOE_ERR_INVALID_ARG;
+  if (g.K > 0 && (!gemm->a || !gemm->a_scale || !gemm->b || !gemm->b_scale || !aligned16(gemm->a) ||
+                  !aligned16(gemm->b) || !aligned_to(gemm->a_scale, 4) || !aligned_to(gemm->b_scale, 4)))
+    return MOE_ERR_INVALID_ARG;
+  const int64_t need = align256(moe::quant_gemm_ws_bytes(g));
+  if (need > 0 && (!ws || (int64_t)ws_bytes < need || !aligned256(ws))) return MOE_ERR_WORKSPACE;
+  g.A = static_cast<const char*>(gemm->a);
+  g.a_scale = gemm->a_scale;
+  g.B = static_cast<const char*>(gemm->b);
+  g.b_scale = gemm->b_scale;
+  g.C = gemm->c;
+  return hip_status(moe::launch_quant_gemm(g, ws, static_cast<hipStream_t>(stream)));
+}
+
+MOE_API moe_status moe_experts_dropless_quant_ws_bytes(const moe_config* cfg, size_t* bytes) {
+  moe_plan p;
+  moe_status st = check_quant_config(cfg, &p);
+  if (st != MOE_OK) return st;
+  if (!bytes) return MOE_ERR_INVALID_ARG;
+  QuantExpertsWs q;
+  *bytes = (size_t)carve_experts_quant(cfg, p.dropless_rows, nullptr, &q);
+  return MOE_OK;
+}
+
+MOE_API moe_status moe_experts_dropless_quant(const moe_config* cfg, const void* xs, const int32_t* expert_offsets,
+                                              const moe_quant_experts* w, void* expert_out, void* ws,
+                                              size_t ws_bytes, void* stream) {
+  moe_plan p;
+  moe_status st = check_quant_config(cfg, &p);
+  if (st != MOE_OK) return st;
+  if (!expert_offsets || !quant_experts_valid(w)) return MOE_ERR_INVALID_ARG;
+  if (cfg->T == 0) return MOE_OK;
+  if (!xs || !expert_out || !aligned16(xs) || !aligned16(expert_out)) return MOE_ERR_INVALID_ARG;
+  QuantExpertsWs q;
+  if (!ws || (int64_t)ws_bytes < carve_experts_quant(cfg, p.dropless_rows, nullptr, &q) || !aligned256(ws))
+    return MOE_ERR_WORKSPACE;
+  return run_experts_quant(cfg, p, xs, expert_offsets, w, expert_out, ws, static_cast<hipStream_t>(stream));
+}
