@@ -648,6 +648,14 @@ typedef struct {
   int32_t reserved;     /* must be 0                                        */
 } moe_quant_gemm;
 
+/* An fp32 result is summed by bf16 matrix instructions (e4m3 values are bf16
+   values): the 8-bit ones drop the bits of a product that lie far below the
+   largest product they sum, which a bf16 result does not show.
+   MOE_ERR_INVALID_ARG: a size or leading dimension out of range, K not a
+   multiple of 128, a null or misaligned pointer; MOE_ERR_UNSUPPORTED: M or N
+   past 2^30, K, lda or ldb past 2^23 or not a multiple of 16, or more than
+   2^23 - 8 tiles of 128 x 128. */
+
 /* Workspace of the product (may be 0: then ws may be NULL); only the sizes,
    leading dimensions and types of *gemm are read. */
 moe_status moe_gemm_quant_ws_bytes(const moe_quant_gemm* gemm, size_t* bytes);
@@ -668,8 +676,8 @@ typedef struct {
    the same way from their fp32 values, both products accumulate in fp32 and
    expert_out (device, bf16 [T*k][L]) is rounded once.  Rows outside every
    expert's range are not written; offsets are kept inside [0, T*k].
-   bf16 configs with d_latent and d_ff multiples of 128 (MOE_ERR_UNSUPPORTED
-   else).  For a straight-through gradient, moe_experts_backward_dropless
+   bf16 configs with d_latent and d_ff multiples of 128, of at most 2^23 - 8
+   tiles of 64 rows x 128 columns (MOE_ERR_UNSUPPORTED else).  For a straight-through gradient, moe_experts_backward_dropless
    takes the bf16 weights that were quantised. */
 moe_status moe_experts_dropless_quant_ws_bytes(const moe_config* cfg, size_t* bytes);
 moe_status moe_experts_dropless_quant(const moe_config* cfg, const void* xs, const int32_t* expert_offsets,

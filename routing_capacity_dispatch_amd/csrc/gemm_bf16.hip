@@ -29,12 +29,14 @@ namespace {
 using core::Acc;
 using core::acc_col;
 using core::acc_row;
+using core::dense_tile;
 using core::load_col;
 using core::load_row;
 using core::mainloop;
 using core::RowSrc;
 using core::uniform_ptr;
 using core::with_row_blocks;
+using core::xcd_order;
 
 using DenseTile = core::Tile<256, 256, 4, 2, 64, 2>;
 // a third B stage, all 160 KB of LDS: the shared SwiGLU GEMM and single-segment dense GEMMs
@@ -48,27 +50,11 @@ static_assert(ExpertTileTall::BN == ExpertTile::BN, "both expert tiles share the
 // are four N tiles, so the Marin-shaped router GEMM is 512 tiles, two per CU
 using RouterTile = core::Tile<128, 96, 2, 2, 64, 2>;
 
-constexpr int kGroupM = 4;  // M panels per group of the dense tile order (4: measured best of 2, 4, 6, 8, 16)
 constexpr int kStagePad = 16;
 
 template <class TL>
 constexpr int lds_bytes() {
   return TL::MAIN_LDS > TL::BM * (TL::BN * 2 + kStagePad) ? TL::MAIN_LDS : TL::BM * (TL::BN * 2 + kStagePad);
-}
-
-// Linear block index -> index in a sequence in which each XCD owns a
-// contiguous range (grids are padded to a multiple of 8 blocks).
-__device__ __forceinline__ int xcd_order(int bid, int nblocks) { return (bid & 7) * (nblocks >> 3) + (bid >> 3); }
-
-// Dense tile order: groups of kGroupM M panels, N tiles, M fastest.
-__device__ __forceinline__ void dense_tile(int t, int tiles_m, int tiles_n, int& mt, int& nt) {
-  const int per_group = kGroupM * tiles_n;
-  const int g = t / per_group;
-  const int first = g * kGroupM;
-  const int gsz = min(tiles_m - first, kGroupM);
-  const int r = t - g * per_group;
-  mt = first + r % gsz;
-  nt = r / gsz;
 }
 
 // Stage the accumulator tile as bf16 rows of `ld` bytes.

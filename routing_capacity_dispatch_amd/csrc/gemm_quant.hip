@@ -9,6 +9,7 @@
 // the order of K inside a block does not matter as long as it is the same:
 // lane l takes bytes 16 (l >> 4) .. + 15 and 64 + 16 (l >> 4) .. + 15 of row
 // l & 15, which makes each load instruction read 64 contiguous bytes a row.
+#include "gemm_core.h"
 #include "kernels.h"
 #include "quant.h"
 
@@ -33,6 +34,29 @@ __device__ __forceinline__ f32x4_t mfma_block(const Frag8& a, const Frag8& b) {
   return __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(x, y, f32x4_t{0.f, 0.f, 0.f, 0.f}, 0, 0, 0, 0, 0, 0);
 }
 
+typedef __bf16 bf16x2v_t __attribute__((ext_vector_type(2)));
+
+// 8 e4m3 bytes as the 8 bf16 values they stand for (exact).
+__device__ __forceinline__ bf16x8_t widen(uint32_t w0, uint32_t w1) {
+  const bf16x2v_t a = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(w0, 1.0f, false);
+  const bf16x2v_t b = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(w0, 1.0f, true);
+  const bf16x2v_t c = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(w1, 1.0f, false);
+  const bf16x2v_t d = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(w1, 1.0f, true);
+  return bf16x8_t{a[0], a[1], b[0], b[1], c[0], c[1], d[0], d[1]};
+}
+struct Wide {
+  bf16x8_t v[4];
+};
+__device__ __forceinline__ Wide widen(const Frag8& f) {
+  return Wide{{widen(f.lo.x, f.lo.y), widen(f.lo.z, f.lo.w), widen(f.hi.x, f.hi.y), widen(f.hi.z, f.hi.w)}};
+}
+__device__ __forceinline__ f32x4_t mfma_block(const Wide& a, const Wide& b) {
+  f32x4_t p = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+  for (int i = 0; i < 4; ++i) p = __builtin_amdgcn_mfma_f32_16x16x32_bf16(a.v[i], b.v[i], p, 0, 0, 0);
+  return p;
+}
+
 __device__ __forceinline__ void store_out(int out_dt, void* C, int64_t i, float v) {
   if (out_dt == DT_BF16)
     static_cast<uint16_t*>(C)[i] = f32_to_bf16(v);
@@ -52,7 +76,7 @@ __device__ __forceinline__ void expert_range(const int32_t* offsets, int e, int6
 // of K; their sums meet in LDS in a fixed order.
 constexpr int kSkinnyWaves = 4;
 
-template <int KS>
+template <int KS, bool kWide>
 __global__ __launch_bounds__(64 * kSkinnyWaves) void skinny_kernel(QuantGemm g) {
   __shared__ f32x4_t part[kSkinnyWaves][64];
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
@@ -84,7 +108,11 @@ __global__ __launch_bounds__(64 * kSkinnyWaves) void skinny_kernel(QuantGemm g) 
     for (int b = ks; b < nb; b += KS) {
       const Frag8 fa = load_frag(arow + (int64_t)b * kQB, lane), fb = load_frag(brow + (int64_t)b * kQB, lane);
       const float s = sbp[b * sb_step];
-      const f32x4_t p = mfma_block(fa, fb);
+      f32x4_t p;
+      if constexpr (kWide)
+        p = mfma_block(widen(fa), widen(fb));
+      else
+        p = mfma_block(fa, fb);
 #pragma unroll
       for (int r = 0; r < 4; ++r) acc[r] = fmaf(p[r], s * sap[r][b * g.a_scale_ld], acc[r]);
     }
@@ -170,22 +198,474 @@ __global__ __launch_bounds__(512) void skinny_gate_up_kernel(QuantGateUp g) {
   }
 }
 
+// ------------------------------------------------------------ tiles in LDS
+// BM x BN per workgroup; K advances one block of 128 bytes a step, so a tile
+// row is 128 bytes and the row-major tile of gemm_core.h (direct global ->
+// LDS loads, 16-byte chunks XOR-swizzled) serves e4m3 unchanged.  The block's
+// scales come with it: one float per tile row of A and of B.
+using core::acc_col;
+using core::acc_row;
+using core::load_col;
+using core::load_row;
+using core::lds_load16;
+using core::RowSrc;
+using core::uniform_ptr;
+
+enum Mode { kBlockB = 0, kRowB = 1, kGateUp = 2 };
+
+// 4 bytes per lane, global -> LDS: lane l's dword lands at lds_wave_base + 4 l.
+__device__ __forceinline__ void lds_load4(const float* p, char* lds_wave_base) {
+  const uint32_t l = __builtin_amdgcn_readfirstlane(
+      static_cast<uint32_t>(reinterpret_cast<uintptr_t>((MOE_LDS char*)lds_wave_base)));
+  asm volatile("s_mov_b32 m0, %0\n\tglobal_load_lds_dword %1, off" ::"s"(l), "v"(p) : "memory", "m0");
+}
+
+template <class TL>
+struct QTile : TL {
+  static constexpr int SCALES = 64 * TL::NW;  // floats staged per step: one load instruction a wavefront
+  static_assert(TL::BM + TL::BN <= SCALES, "a scale for every tile row");
+  static constexpr int S_BASE = TL::MAIN_LDS;
+  static constexpr int LDS = S_BASE + TL::NS * SCALES * 4;
+};
+
+// Row `r` of a staged operand tile, this lane's 32 bytes.
+template <class TL>
+__device__ __forceinline__ Frag8 lds_frag(const char* st, int row, int lane) {
+  const char* p = st + row * TL::RB;
+  const int sw = TL::swz(row & 15);
+  return Frag8{ld16(p + (((lane >> 4) ^ sw) << 4)), ld16(p + (((4 + (lane >> 4)) ^ sw) << 4))};
+}
+
+template <class TL>
+struct QAcc {
+  f32x4_t v[TL::MI][TL::NI];
+};
+
+// acc += scaled product of the staged block.
+template <class TL, int kMode, bool kWide>
+__device__ __forceinline__ void block_step(const char* sa, const char* sb, const float* sc, QAcc<TL>& acc, int wm,
+                                           int wn, int lane) {
+  Frag8 fb[TL::NI];
+#pragma unroll
+  for (int ni = 0; ni < TL::NI; ++ni) fb[ni] = lds_frag<TL>(sb, wn * TL::WN + ni * 16 + (lane & 15), lane);
+  Wide wb[kWide ? TL::NI : 1];
+  if constexpr (kWide)
+#pragma unroll
+    for (int ni = 0; ni < TL::NI; ++ni) wb[ni] = widen(fb[ni]);
+  // scales of B: one for the wavefront's columns (128 of them share it), one
+  // for its gate and one for its up columns, or one per column
+  const float* scb = sc + TL::BM + wn * TL::WN;
+  float bs[TL::NI];
+#pragma unroll
+  for (int ni = 0; ni < TL::NI; ++ni) {
+    if constexpr (kMode == kRowB)
+      bs[ni] = scb[ni * 16 + (lane & 15)];
+    else
+      bs[ni] = __int_as_float(__builtin_amdgcn_readfirstlane(__float_as_int(scb[kMode == kGateUp ? (ni & 1) * 16 : 0])));
+  }
+#pragma unroll
+  for (int mi = 0; mi < TL::MI; ++mi) {
+    const Frag8 fa = lds_frag<TL>(sa, wm * TL::WM + mi * 16 + (lane & 15), lane);
+    const f32x4_t as = *reinterpret_cast<const f32x4_t*>(sc + wm * TL::WM + mi * 16 + (lane >> 4) * 4);
+    Wide wa;
+    if constexpr (kWide) wa = widen(fa);
+#pragma unroll
+    for (int ni = 0; ni < TL::NI; ++ni) {
+      f32x4_t p;
+      if constexpr (kWide)
+        p = mfma_block(wa, wb[ni]);
+      else
+        p = mfma_block(fa, fb[ni]);
+#pragma unroll
+      for (int r = 0; r < 4; ++r) acc.v[mi][ni][r] = fmaf(p[r], as[r] * bs[ni], acc.v[mi][ni][r]);
+    }
+  }
+}
+
+// Sum over K blocks [0, nb): the next block's loads fly while one is
+// computed.  sp: this lane's scale of block 0, s_step floats to the next.
+// Ends with a barrier, so the caller may reuse the LDS.
+template <class TL, int kMode, bool kWide>
+__device__ __forceinline__ void quant_loop(const RowSrc<TL::A_INS>& a, const RowSrc<TL::B_INS>& b, const float* sp,
+                                           int64_t s_step, int nb, char* lds, QAcc<TL>& acc) {
+  using Q = QTile<TL>;
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+  const int wm = wave / TL::WGN, wn = wave % TL::WGN;
+#pragma unroll
+  for (int mi = 0; mi < TL::MI; ++mi)
+#pragma unroll
+    for (int ni = 0; ni < TL::NI; ++ni) acc.v[mi][ni] = f32x4_t{0.f, 0.f, 0.f, 0.f};
+  auto issue = [&](int kb) {
+    const int st = kb & 1;
+    core::issue_rows<TL>(a, (int64_t)kb * kQB, lds + st * TL::A_BYTES, wave);
+    core::issue_rows<TL>(b, (int64_t)kb * kQB, lds + TL::B_BASE + st * TL::B_BYTES, wave);
+    lds_load4(sp + kb * s_step, lds + Q::S_BASE + (st * Q::SCALES + wave * 64) * 4);
+  };
+  if (nb > 0) issue(0);
+  for (int kb = 0; kb < nb; ++kb) {
+    core::wait_loads<0>();
+    if (kb + 1 < nb) issue(kb + 1);
+    const int st = kb & 1;
+    block_step<TL, kMode, kWide>(lds + st * TL::A_BYTES, lds + TL::B_BASE + st * TL::B_BYTES,
+                                 reinterpret_cast<const float*>(lds + Q::S_BASE) + st * Q::SCALES, acc, wm, wn, lane);
+  }
+  __syncthreads();
+}
+
+// Tile t of the grouped products: the expert that holds it.  Every wavefront
+// finds it from the offsets: 64 experts at a time, a scan of their tile
+// counts.  Each XCD takes an eighth of the tiles, contiguous.  Returns false
+// past the last tile.
+template <int BM>
+__device__ __forceinline__ bool expert_tile(const int32_t* offsets, int E, int64_t M, int tiles_n, int& e, int& mt,
+                                            int& nt, int64_t& row0, int64_t& rows) {
+  const int lane = threadIdx.x & 63;
+  int total = 0;
+  for (int e0 = 0; e0 < E; e0 += 64) {
+    int64_t r0, n;
+    expert_range(offsets, min(e0 + lane, E - 1), M, r0, n);
+    int c = e0 + lane < E && n > 0 ? (int)((n + BM - 1) / BM) : 0;
+    for (int d = 1; d < 64; d <<= 1) c += __shfl_xor(c, d);
+    total += c;
+  }
+  total *= tiles_n;
+  const int per = (total + 7) >> 3;
+  const int local = blockIdx.x >> 3;
+  int t = (blockIdx.x & 7) * per + local;
+  if (local >= per || t >= total) return false;
+  for (int e0 = 0; e0 < E; e0 += 64) {
+    int64_t r0, n;
+    expert_range(offsets, min(e0 + lane, E - 1), M, r0, n);
+    const int c = (e0 + lane < E && n > 0 ? (int)((n + BM - 1) / BM) : 0) * tiles_n;
+    int x = c;
+    for (int d = 1; d < 64; d <<= 1) {
+      const int o = __shfl_up(x, d);
+      if (lane >= d) x += o;
+    }
+    const uint64_t hit = ballot64(x > t);
+    if (hit) {
+      const int l = __builtin_ctzll(hit);
+      e = e0 + l;
+      const int first = __builtin_amdgcn_readlane(x - c, l);
+      const int tm = __builtin_amdgcn_readlane(c, l) / tiles_n;
+      row0 = readlane64(r0, l);
+      rows = readlane64(n, l);
+      t -= first;
+      nt = t / tm;
+      mt = t - nt * tm;
+      return true;
+    }
+    t -= __builtin_amdgcn_readlane(x, 63);
+  }
+  return false;
+}
+
+constexpr int kStagePad = 16;
+
+template <class TL>
+constexpr int product_lds() {
+  constexpr int stage = TL::BM * (TL::BN * 2 + kStagePad);
+  return QTile<TL>::LDS > stage ? QTile<TL>::LDS : stage;
+}
+
+// C tile.  Grouped products have offsets; a dense one may split K: part
+// blockIdx.y of gridDim.y sums its share of the blocks into partial sums
+// [part][M][N] fp32 (g.C with split), which reduce_kernel adds in order.
+template <class TL, int kMode, bool kWide>
+__global__ __launch_bounds__(TL::THREADS) void product_kernel(QuantGemm g, int tiles_m, int tiles_n, float* partial) {
+  __shared__ __attribute__((aligned(1024))) char lds[product_lds<TL>()];
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+  int e = 0, mt, nt;
+  int64_t row0 = 0, rows = g.M;
+  if (g.offsets) {
+    if (!expert_tile<TL::BM>(g.offsets, g.E, g.M, tiles_n, e, mt, nt, row0, rows)) return;
+  } else {
+    const int t = core::xcd_order(blockIdx.x, gridDim.x);
+    if (t >= tiles_m * tiles_n) return;
+    core::dense_tile(t, tiles_m, tiles_n, mt, nt);
+  }
+  const int64_t m0 = (int64_t)mt * TL::BM, n0 = (int64_t)nt * TL::BN;
+  int kb0 = 0, nb = g.K / kQB;
+  if (partial) {
+    const int per = (nb + gridDim.y - 1) / gridDim.y;
+    kb0 = min((int)blockIdx.y * per, nb);
+    nb = min(per, nb - kb0);
+  }
+  RowSrc<TL::A_INS> a;
+  RowSrc<TL::B_INS> b;
+  const char* A = uniform_ptr(g.A + (row0 + m0) * g.lda + (int64_t)kb0 * kQB);
+  const char* B = uniform_ptr(g.B + e * g.b_stride + n0 * g.ldb + (int64_t)kb0 * kQB);
+  const int mlast = (int)min(rows - m0 - 1, (int64_t)TL::BM), nlast = (int)min(g.N - n0 - 1, (int64_t)TL::BN);
+#pragma unroll
+  for (int i = 0; i < TL::A_INS; ++i) {
+    a.base[i] = A;
+    a.off[i] = (uint32_t)(min(load_row<TL>(i, wave, lane), mlast) * (uint32_t)g.lda) + load_col<TL>(lane);
+  }
+#pragma unroll
+  for (int i = 0; i < TL::B_INS; ++i) {
+    b.base[i] = B;
+    b.off[i] = (uint32_t)(min(load_row<TL>(i, wave, lane), nlast) * (uint32_t)g.ldb) + load_col<TL>(lane);
+  }
+  const int j = threadIdx.x;
+  const float* sp;
+  int64_t step;
+  if (j < TL::BM) {
+    sp = g.a_scale + kb0 * g.a_scale_ld + row0 + m0 + min(j, mlast);
+    step = g.a_scale_ld;
+  } else {
+    const int64_t n = n0 + min(j - TL::BM, nlast);
+    const float* sb = g.b_scale + e * g.b_scale_stride;
+    sp = kMode == kRowB ? sb + kb0 * g.b_scale_ld + n : sb + (n >> 7) * g.b_scale_ld + kb0;
+    step = kMode == kRowB ? g.b_scale_ld : 1;
+  }
+  QAcc<TL> acc;
+  quant_loop<TL, kMode, kWide>(a, b, sp, step, nb, lds, acc);
+  const int wm = wave / TL::WGN, wn = wave % TL::WGN;
+  if (partial || g.out_dt == DT_F32) {
+    float* C = partial ? partial + ((int64_t)blockIdx.y * g.M + m0) * g.N + n0
+                       : static_cast<float*>(g.C) + (row0 + m0) * g.ldc + n0;
+    const int64_t ld = partial ? g.N : g.ldc;
+#pragma unroll
+    for (int mi = 0; mi < TL::MI; ++mi)
+#pragma unroll
+      for (int r = 0; r < 4; ++r) {
+        const int row = acc_row<TL>(wm, mi, lane, r);
+#pragma unroll
+        for (int ni = 0; ni < TL::NI; ++ni) {
+          const int col = acc_col<TL>(wn, ni, lane);
+          if (row <= mlast && col <= nlast) C[row * ld + col] = acc.v[mi][ni][r];
+        }
+      }
+    return;
+  }
+  constexpr int ld = TL::BN * 2 + kStagePad;
+#pragma unroll
+  for (int mi = 0; mi < TL::MI; ++mi)
+#pragma unroll
+    for (int ni = 0; ni < TL::NI; ++ni)
+#pragma unroll
+      for (int r = 0; r < 4; ++r)
+        *reinterpret_cast<uint16_t*>(lds + acc_row<TL>(wm, mi, lane, r) * ld + acc_col<TL>(wn, ni, lane) * 2) =
+            f32_to_bf16(acc.v[mi][ni][r]);
+  __syncthreads();
+  uint16_t* C = static_cast<uint16_t*>(g.C) + (row0 + m0) * g.ldc + n0;
+  const bool wide_ok = ((reinterpret_cast<uintptr_t>(g.C) | (uintptr_t)(g.ldc * 2)) & 15) == 0;
+  constexpr int cpr = TL::BN / 8;
+  for (int q = threadIdx.x; q < TL::BM * cpr; q += TL::THREADS) {
+    const int r = q / cpr, c = (q - r * cpr) * 8;
+    if (r > mlast || c > nlast) continue;
+    const char* src = lds + r * ld + c * 2;
+    if (wide_ok && c + 7 <= nlast)
+      st16(C + r * g.ldc + c, ld16(src));
+    else
+      for (int i = 0; i < 8 && c + i <= nlast; ++i) C[r * g.ldc + c + i] = reinterpret_cast<const uint16_t*>(src)[i];
+  }
+}
+
+// C = sum of the partial sums, in order.
+__global__ __launch_bounds__(256) void reduce_kernel(QuantGemm g, const float* __restrict__ partial, int parts) {
+  const int64_t n = g.M * g.N;
+  for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; i < n; i += (int64_t)gridDim.x * 256) {
+    float s = partial[i];
+    for (int p = 1; p < parts; ++p) s += partial[p * n + i];
+    const int64_t r = i / g.N;
+    store_out(g.out_dt, g.C, r * g.ldc + (i - r * g.N), s);
+  }
+}
+
+// Hidden tile: 128 features, gate and up rows interleaved in 16-row blocks,
+// so a lane holds both halves of its features.
+template <class TL>
+__global__ __launch_bounds__(TL::THREADS) void gate_up_kernel(QuantGateUp g, int tiles_m) {
+  static_assert(TL::BN == 2 * kQB, "one feature block per tile");
+  __shared__ __attribute__((aligned(1024))) char lds[QTile<TL>::LDS];
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+  const int tiles_n = g.F / kQB;
+  int e, mt, fb;
+  int64_t row0 = 0, rows = g.M;
+  if (g.offsets) {
+    if (!expert_tile<TL::BM>(g.offsets, g.E, g.M, tiles_n, e, mt, fb, row0, rows)) return;
+  } else {
+    const int t = core::xcd_order(blockIdx.x, gridDim.x);
+    const int per = tiles_m * tiles_n;
+    e = t / per;
+    if (e >= g.E) return;
+    core::dense_tile(t - e * per, tiles_m, tiles_n, mt, fb);
+  }
+  const int64_t m0 = (int64_t)mt * TL::BM;
+  const int nb = g.K / kQB;
+  RowSrc<TL::A_INS> a;
+  RowSrc<TL::B_INS> b;
+  const char* A = uniform_ptr(g.A + (row0 + m0) * g.lda);
+  const int64_t wrow = ((int64_t)e * g.F + fb * kQB) * g.K;
+  const int mlast = (int)min(rows - m0 - 1, (int64_t)TL::BM);
+#pragma unroll
+  for (int i = 0; i < TL::A_INS; ++i) {
+    a.base[i] = A;
+    a.off[i] = (uint32_t)(min(load_row<TL>(i, wave, lane), mlast) * (uint32_t)g.lda) + load_col<TL>(lane);
+  }
+  // tile row r: 16-row blocks alternate gate and up; each load instruction's
+  // 8 rows lie in one block
+  auto feature = [](int r) { return (r >> 5) * 16 + (r & 15); };
+#pragma unroll
+  for (int i = 0; i < TL::B_INS; ++i) {
+    const int r = load_row<TL>(i, wave, lane);
+    b.base[i] = uniform_ptr(((r >> 4) & 1 ? g.Wu : g.Wg) + wrow);
+    b.off[i] = (uint32_t)(feature(r) * (uint32_t)g.K) + load_col<TL>(lane);
+  }
+  const int j = threadIdx.x;
+  const float* sp;
+  int64_t step = 1;
+  if (j < TL::BM) {
+    sp = g.a_scale + row0 + m0 + min(j, mlast);
+    step = g.a_scale_ld;
+  } else {
+    sp = (((j - TL::BM) >> 4) & 1 ? g.su : g.sg) + ((int64_t)e * tiles_n + fb) * nb;
+  }
+  QAcc<TL> acc;
+  quant_loop<TL, kGateUp, false>(a, b, sp, step, nb, lds, acc);
+  // h over the gate registers; its largest magnitude per row: lanes, then
+  // wavefronts of the row
+  const int wm = wave / TL::WGN, wn = wave % TL::WGN;
+  float* part = reinterpret_cast<float*>(lds);  // [BM][WGN]
+  constexpr int ld = kQB + kStagePad;
+  char* stage = lds + TL::BM * TL::WGN * 4;
+#pragma unroll
+  for (int mi = 0; mi < TL::MI; ++mi)
+#pragma unroll
+    for (int r = 0; r < 4; ++r) {
+      float mx = 0.0f;
+#pragma unroll
+      for (int q = 0; q < TL::NI / 2; ++q) {
+        const float h = silu(acc.v[mi][2 * q][r]) * acc.v[mi][2 * q + 1][r];
+        acc.v[mi][2 * q][r] = h;
+        mx = fmaxf(mx, fabsf(h));
+      }
+      for (int d = 1; d < 16; d <<= 1) mx = fmaxf(mx, __shfl_xor(mx, d));
+      if ((lane & 15) == 0) part[acc_row<TL>(wm, mi, lane, r) * TL::WGN + wn] = mx;
+    }
+  __syncthreads();
+  const int64_t col = (g.offsets ? 0 : (int64_t)e * g.F) + fb * kQB;
+#pragma unroll
+  for (int mi = 0; mi < TL::MI; ++mi)
+#pragma unroll
+    for (int r = 0; r < 4; ++r) {
+      const int row = acc_row<TL>(wm, mi, lane, r);
+      float amax = kQuantTiny;
+#pragma unroll
+      for (int w = 0; w < TL::WGN; ++w) amax = fmaxf(amax, part[row * TL::WGN + w]);
+      const BlockQuant bq(amax);
+#pragma unroll
+      for (int q = 0; q < TL::NI / 2; ++q)
+        stage[row * ld + wn * (TL::WN / 2) + q * 16 + (lane & 15)] =
+            (char)(e4m3_quad(bq(acc.v[mi][2 * q][r]), 0.f, 0.f, 0.f) & 0xFF);
+      if (wn == 0 && (lane & 15) == 0 && row <= mlast)
+        g.h_scale[(col / kQB) * g.h_scale_ld + row0 + m0 + row] = block_scale(amax);
+    }
+  __syncthreads();
+  for (int q = threadIdx.x; q < TL::BM * 8; q += TL::THREADS) {
+    const int r = q >> 3, c = (q & 7) * 16;
+    if (r <= mlast) st16(g.H + (row0 + m0 + r) * g.ldh + col + c, ld16(stage + r * ld + c));
+  }
+}
+
+using T256 = core::Tile<256, 256, 2, 4>;
+using T128 = core::Tile<128, 128, 2, 2>;
+using E128 = core::Tile<128, 256, 2, 4>;
+using E64 = core::Tile<64, 256, 1, 8>;
+
 inline int64_t cdiv(int64_t a, int64_t b) { return (a + b - 1) / b; }
+inline unsigned pad8(int64_t n) { return (unsigned)((n + 7) / 8 * 8); }
+
+// How a product runs: few rows straight from memory, or tiles.
+struct Form {
+  bool skinny;
+  bool big;    // 256 x 256 tiles (else 128 x 128)
+  bool wide;   // bf16 matrix instructions on the widened values
+  int parts;   // shares of K
+};
+
+Form product_form(const QuantGemm& g) {
+  Form f{};
+  f.parts = 1;
+  const int64_t rows = g.offsets ? cdiv(g.M, g.E) : g.M;
+  f.wide = g.out_dt == DT_F32;
+  f.skinny = rows <= 32;
+  if (f.skinny) return f;
+  f.big = !f.wide && rows >= 192 && (g.offsets || cdiv(g.M, 256) * cdiv(g.N, 256) >= 128);
+  if (!g.offsets && !f.big) {
+    const int64_t tiles = cdiv(g.M, 128) * cdiv(g.N, 128);
+    int64_t p = 512 / (tiles > 0 ? tiles : 1);  // two 128 x 128 workgroups fit a CU
+    if (p > 8) p = 8;
+    if (p > g.K / kQB / 4) p = g.K / kQB / 4;
+    if (p > 1) f.parts = (int)p;
+  }
+  return f;
+}
 
 }  // namespace
 
-int64_t quant_gemm_ws_bytes(const QuantGemm& g) { return 0; }
+int64_t quant_gemm_ws_bytes(const QuantGemm& g) {
+  const Form f = product_form(g);
+  return f.parts > 1 ? f.parts * g.M * g.N * 4 : 0;
+}
+
+template <class TL, bool kWide>
+void launch_tiles(const QuantGemm& g, int parts, float* partial, hipStream_t s) {
+  const int64_t tn = cdiv(g.N, TL::BN);
+  const int64_t tm = g.offsets ? cdiv(g.M, TL::BM) + g.E : cdiv(g.M, TL::BM);
+  const dim3 grid(pad8(tm * tn), (unsigned)parts);
+  if (g.b_rows == 1)
+    product_kernel<TL, kRowB, kWide><<<grid, TL::THREADS, 0, s>>>(g, (int)tm, (int)tn, partial);
+  else
+    product_kernel<TL, kBlockB, kWide><<<grid, TL::THREADS, 0, s>>>(g, (int)tm, (int)tn, partial);
+}
 
 hipError_t launch_quant_gemm(const QuantGemm& g, void* ws, hipStream_t s) {
   if (g.M <= 0 || g.N <= 0) return hipSuccess;
-  const int64_t rows = g.offsets ? g.E : (cdiv(g.M, 16) < 65535 ? cdiv(g.M, 16) : 65535);
-  skinny_kernel<1><<<dim3((unsigned)cdiv(g.N, 16 * kSkinnyWaves), (unsigned)rows), 64 * kSkinnyWaves, 0, s>>>(g);
+  const Form f = product_form(g);
+  if (f.skinny) {
+    const int64_t rows = g.offsets ? g.E : cdiv(g.M, 16);
+    const dim3 grid((unsigned)cdiv(g.N, 16 * kSkinnyWaves), (unsigned)rows);
+    if (f.wide)
+      skinny_kernel<1, true><<<grid, 64 * kSkinnyWaves, 0, s>>>(g);
+    else
+      skinny_kernel<1, false><<<grid, 64 * kSkinnyWaves, 0, s>>>(g);
+    return hipGetLastError();
+  }
+  float* partial = f.parts > 1 ? static_cast<float*>(ws) : nullptr;
+  if (f.big)
+    launch_tiles<T256, false>(g, f.parts, partial, s);
+  else if (f.wide)
+    launch_tiles<T128, true>(g, f.parts, partial, s);
+  else
+    launch_tiles<T128, false>(g, f.parts, partial, s);
+  if (partial) {
+    const int64_t blocks = cdiv(g.M * g.N, 1024);
+    reduce_kernel<<<(unsigned)(blocks < 4096 ? blocks : 4096), 256, 0, s>>>(g, partial, f.parts);
+  }
   return hipGetLastError();
+}
+
+template <class TL>
+void launch_hidden(const QuantGateUp& g, hipStream_t s) {
+  const int64_t tn = g.F / kQB;
+  const int64_t tm = cdiv(g.M, TL::BM);
+  const int64_t tiles = g.offsets ? (tm + g.E) * tn : tm * tn * g.E;
+  gate_up_kernel<TL><<<pad8(tiles), TL::THREADS, 0, s>>>(g, (int)tm);
 }
 
 hipError_t launch_quant_gate_up(const QuantGateUp& g, hipStream_t s) {
   if (g.M <= 0 || g.E <= 0) return hipSuccess;
-  skinny_gate_up_kernel<<<dim3((unsigned)(g.F / kQB), (unsigned)g.E), 512, 0, s>>>(g);
+  const int64_t rows = g.offsets ? cdiv(g.M, g.E) : g.M;
+  if (rows <= 24)
+    skinny_gate_up_kernel<<<dim3((unsigned)(g.F / kQB), (unsigned)g.E), 512, 0, s>>>(g);
+  else if (rows <= 64)
+    launch_hidden<E64>(g, s);
+  else if (rows <= 160)
+    launch_hidden<E128>(g, s);
+  else
+    launch_hidden<T256>(g, s);
   return hipGetLastError();
 }
 

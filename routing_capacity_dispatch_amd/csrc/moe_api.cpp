@@ -1513,7 +1513,9 @@ moe_status check_gemm_quant(const moe_quant_gemm* q, moe::QuantGemm* g) {
   if (q->out_dtype != MOE_F32 && q->out_dtype != MOE_BF16) return MOE_ERR_INVALID_ARG;
   if (q->b_block_rows != 1 && q->b_block_rows != 128) return MOE_ERR_INVALID_ARG;
   if (q->K % 128) return MOE_ERR_INVALID_ARG;
-  if (q->M > kMaxQuantRows || q->N > kMaxQuantRows || q->K > kMaxQuantK) return MOE_ERR_UNSUPPORTED;
+  if (q->M > kMaxQuantRows || q->N > kMaxQuantRows || q->K > kMaxQuantK ||
+      ceil_div(q->M, 128) * ceil_div(q->N, 128) > kMaxListEntries)
+    return MOE_ERR_UNSUPPORTED;
   const int64_t kb = q->K / 128;
   const int64_t nb = q->b_block_rows == 128 ? kb : q->N;
   if (q->lda < q->K || q->ldb < q->K || q->ldc < q->N || q->a_scale_ld < q->M || q->b_scale_ld < nb)
@@ -1561,6 +1563,9 @@ moe_status check_quant_config(const moe_config* cfg, moe_plan* p) {
   moe_status st = check_dropless(cfg, p);
   if (st != MOE_OK) return st;
   if (cfg->d_latent % 128 || cfg->d_ff % 128) return MOE_ERR_UNSUPPORTED;
+  // tiles of 64 rows x 128 columns at the least
+  const int64_t widest = cfg->d_latent > cfg->d_ff ? cfg->d_latent : cfg->d_ff;
+  if ((ceil_div(p->dropless_rows, 64) + cfg->n_experts) * (widest / 128) > kMaxListEntries) return MOE_ERR_UNSUPPORTED;
   return MOE_OK;
 }
 

@@ -1,0 +1,473 @@
+"""The e4m3 quantiser, the block-scaled product and the 8-bit experts against
+the fp64 oracle.
+
+Tolerances.  Quantised values of bf16 inputs are equal (the fp32 quotient of
+bf16 numbers is a tie only where the real one is).  Of fp32 inputs they are
+equal but where the real quotient lies within 2^-22 of a tie, relatively (two
+fp32 roundings), and there one step off at most.  Scales are the correctly
+rounded fp32 quotient.
+
+A bf16 product: the 8-bit matrix instructions keep, of the products of 8
+consecutive k, the bits down to 2^-13 of the largest, so each of the other 7
+loses at most 2^-13 of it; fp32 sums of K/8 groups and K/128 scaled blocks
+lose 2^-24 of the magnitudes a step; the result is rounded to bf16 (2^-8 at
+most).  An fp32 product has no dropped bits: (K + K/128 + 4) 2^-24 of the
+magnitudes covers any order of its sums."""
+import numpy as np
+import pytest
+import torch
+
+import routing_capacity_dispatch_amd as rcd
+import synth
+from gpu_common import dev, say
+from oracle import block_quant as bq
+
+pytestmark = pytest.mark.gpu
+DROP = 7 * 2.0 ** -13
+
+
+def np64(t):
+    return t.detach().cpu().float().numpy().astype(np.float64)
+
+
+def rand(shape, seed, dtype=torch.float32, spread=0.0):
+    g = torch.Generator(device="cpu").manual_seed(seed)
+    x = torch.randn(shape, generator=g)
+    if spread:
+        x = x * torch.exp(spread * torch.randn((shape[0],) + (1,) * (len(shape) - 1), generator=g))
+    return x.to(dtype)
+
+
+# ------------------------------------------------------------- quantiser
+def check_quantize(x, block, transpose):
+    d = dev()
+    say("quantize", tuple(x.shape), x.dtype, "block", block, "transpose", transpose, "stride", x.stride())
+    q, s = rcd.quantize(x.to(d) if not x.is_cuda else x, block, transpose)
+    torch.cuda.synchronize()
+    xn = np64(x)
+    v, amax = bq.quotients(xn, block, transpose)
+    ref = bq.round_e4m3(v)
+    got = np64(q)
+    assert got.shape == ref.shape
+    if x.dtype == torch.bfloat16:
+        assert np.array_equal(got, ref)
+    else:
+        lo, hi = bq.round_e4m3(v * (1 - 2.0 ** -22)), bq.round_e4m3(np.clip(v * (1 + 2.0 ** -22), -448, 448))
+        assert ((got >= np.minimum(lo, hi)) & (got <= np.maximum(lo, hi))).all()
+    want = amax.astype(np.float32) / np.float32(448)
+    assert np.array_equal(s.cpu().numpy(), want.T if block == 1 else want)
+
+
+@pytest.mark.parametrize("transpose", [False, True])
+@pytest.mark.parametrize("block", [1, 128])
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+@pytest.mark.parametrize("shape", [(1, 1), (1, 128), (3, 129), (128, 128), (130, 257), (257, 1000), (1, 5000), (900, 4),
+                                   (64, 512), (200, 2048)])
+def test_quantize_matches_oracle(shape, dtype, block, transpose):
+    check_quantize(rand(shape, shape[0] * 31 + shape[1], dtype, 1.0), block, transpose)
+
+
+@pytest.mark.parametrize("transpose", [False, True])
+@pytest.mark.parametrize("block", [1, 128])
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+def test_quantize_strided_and_unaligned_rows(dtype, block, transpose):
+    d = dev()
+    big = rand((140, 700), 3, dtype, 1.0).to(d)
+    for x in (big[:, :256], big[5:, 8:264], big[:, 1:130], big[::2, 3:400], big[1:2, 5:700]):
+        check_quantize(x, block, transpose)
+
+
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+@pytest.mark.parametrize("transpose", [False, True])
+@pytest.mark.parametrize("block", [1, 128])
+def test_quantize_extreme_magnitudes_and_ties(dtype, block, transpose):
+    x = torch.zeros((300, 300))
+    x[0, 0] = 3.3e38                           # beside zeros and ordinary values
+    x[0, 1] = 1.0
+    x[129, 129:140] = 2.0 ** -120              # below the smallest block magnitude
+    x[130:140, 150:290] = 1e-30
+    x[200:210, :] = torch.linspace(-3e38, 3e38, 300)
+    # amax 1.75 makes the factor 256: every midpoint between e4m3 values occurs
+    mid = torch.from_numpy((bq.MAGNITUDES[1:] + bq.MAGNITUDES[:-1]) / 512).float()
+    x[256, :126] = mid
+    x[256, 126] = 1.75
+    x[257, :126] = -mid
+    x[257, 127] = 1.75
+    x[258, :128] = torch.arange(128) / 128.0 * 1.0
+    x[258, 127] = 1.0                          # 448 times eighths: ties at another factor
+    x[280, 299] = -0.0
+    check_quantize(x.to(dtype), block, transpose)
+
+
+def test_quantize_nothing():
+    d = dev()
+    q, s = rcd.quantize(torch.empty((0, 256), dtype=torch.bfloat16, device=d))
+    assert q.shape == (0, 256) and s.shape == (2, 0)
+    q, s = rcd.quantize(torch.empty((5, 0), dtype=torch.bfloat16, device=d))
+    assert q.shape == (5, 0) and s.shape == (0, 5)
+
+
+# --------------------------------------------------------------- product
+def operands(M, N, K, block, seed):
+    d = dev()
+    a, sa = rcd.quantize(rand((M, K), seed, spread=0.7).to(d))
+    b, sb = rcd.quantize(rand((N, K), seed + 1, spread=0.3).to(d), block)
+    torch.cuda.synchronize()
+    return a, sa, b, sb
+
+
+def gemm_ref(a, sa, b, sb, block):
+    """(product, its value on magnitudes, the dropped bits' bound) in fp64."""
+    qa, qb = np64(a), np64(b)
+    va = bq.values(qa, np64(sa).T, 1)
+    vb = bq.values(qb, np64(sb).T if block == 1 else np64(sb), block)
+    return va @ vb.T, np.abs(va) @ np.abs(vb).T, (va, vb)
+
+
+def check_gemm(a, sa, b, sb, block, out_dtype, **kw):
+    M, K, N = a.shape[0], a.shape[1], b.shape[0]
+    say("gemm_quant", M, N, K, "block", block, out_dtype)
+    c = rcd.gemm_quant(a, sa, b, sb, block, out_dtype, **kw)
+    torch.cuda.synchronize()
+    assert c.shape == (M, N) and c.dtype == out_dtype
+    ref, mag, (va, vb) = gemm_ref(a, sa, b, sb, block)
+    tol = (K + K // 128 + 4) * 2.0 ** -24 * mag
+    if out_dtype == torch.bfloat16:
+        drop = bq.group_peaks(va, vb) if M * N * K <= 4e7 else mag
+        tol = tol + DROP * drop + 2.0 ** -8 * (np.abs(ref) + DROP * drop)
+    err = np.abs(np64(c) - ref)
+    assert (err <= tol).all(), (err / np.maximum(tol, 1e-300)).max()
+    return c
+
+
+@pytest.mark.parametrize("out_dtype", [torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("block", [1, 128])
+@pytest.mark.parametrize("M,N,K", [(1, 1, 128), (1, 257, 384), (2, 64, 256), (15, 130, 128), (16, 16, 512), (17, 63, 256),
+                                   (33, 128, 384), (64, 200, 1152), (65, 129, 640), (129, 257, 256), (200, 384, 128),
+                                   (300, 520, 384), (1, 1000, 4096), (8, 48, 2176), (48, 300, 1024), (100, 31, 2048)])
+def test_gemm_matches_oracle(M, N, K, block, out_dtype):
+    check_gemm(*operands(M, N, K, block, M + N + K), block, out_dtype)
+
+
+@pytest.mark.parametrize("M,N,K,block,out_dtype", [
+    (2048, 4100, 256, 128, torch.bfloat16), (4000, 2100, 384, 1, torch.bfloat16), (513, 770, 1280, 128, torch.float32),
+    (260, 4097, 128, 1, torch.float32), (2050, 4090, 128, 128, torch.bfloat16)])
+def test_gemm_larger_matches_oracle(M, N, K, block, out_dtype):
+    check_gemm(*operands(M, N, K, block, M), block, out_dtype)
+
+
+@pytest.mark.parametrize("out_dtype", [torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("M", [3, 40, 200])
+def test_gemm_strided_operands_and_output(M, out_dtype):
+    d = dev()
+    a, sa, b, sb = operands(400, 500, 512, 128, 3)
+    # a slice of the batch: its scales are a slice of the scales' columns
+    c0 = check_gemm(a[7:7 + M], sa[:, 7:7 + M], b, sb, 128, out_dtype)
+    # K blocks 1 and 2 of both, every other row of a
+    check_gemm(a[::2, 128:384][:M], sa[1:3, ::2].contiguous()[:, :M], b[:, 128:384], sb[:, 1:3], 128, out_dtype)
+    # rows 256.. of b, their scale blocks
+    check_gemm(a[:M], sa[:, :M], b[256:], sb[2:], 128, out_dtype)
+    # columns 5.. of a wider output: nothing beside them is written
+    for col, width in ((5, 600), (8, 640)):
+        out = torch.full((M, width), 7.0, dtype=out_dtype, device=d)
+        check_gemm(a[7:7 + M], sa[:, 7:7 + M], b, sb, 128, out_dtype, out=out[:, col:col + 500])
+        assert (out[:, :col] == 7).all() and (out[:, col + 500:] == 7).all()
+        assert torch.equal(out[:, col:col + 500], c0)
+
+
+def test_gemm_of_nothing():
+    d = dev()
+    for M, N, K in ((0, 64, 128), (64, 0, 128), (70, 90, 0), (3, 5, 0)):
+        a = torch.empty((M, K), dtype=torch.float8_e4m3fn, device=d)
+        b = torch.empty((N, K), dtype=torch.float8_e4m3fn, device=d)
+        sa = torch.empty((K // 128, M), device=d)
+        sb = torch.empty((-(-N // 128), K // 128), device=d)
+        out = torch.full((M, N), 3.0, dtype=torch.bfloat16, device=d)
+        c = rcd.gemm_quant(a, sa, b, sb, out=out)
+        torch.cuda.synchronize()
+        assert (c == 0).all()
+
+
+@pytest.mark.parametrize("out_dtype", [torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("M,N,K", [(1, 700, 2048), (40, 300, 2048), (300, 400, 4096), (2048, 4096, 256)])
+def test_gemm_is_reproducible(M, N, K, out_dtype):
+    a, sa, b, sb = operands(M, N, K, 128, 5)
+    c = rcd.gemm_quant(a, sa, b, sb, out_dtype=out_dtype)
+    for _ in range(3):
+        assert torch.equal(c, rcd.gemm_quant(a, sa, b, sb, out_dtype=out_dtype))
+
+
+def test_gemm_offsets_past_32_bits():
+    # 2^20 + 100 rows of 4224 bytes: the last rows lie past 4 GiB of a, and
+    # past 2^31 elements of the bf16 output
+    d = dev()
+    M, N, K = (1 << 20) + 100, 2100, 4224
+    g = torch.Generator(device=d).manual_seed(1)
+    a = torch.empty((M, K), dtype=torch.uint8, device=d)
+    for r in range(0, M, 1 << 17):
+        a[r:r + (1 << 17)] = torch.randint(0, 120, a[r:r + (1 << 17)].shape, generator=g, device=d, dtype=torch.uint8)
+    a = a.view(torch.float8_e4m3fn)
+    sa = torch.rand((K // 128, M), generator=g, device=d) + 0.5
+    b, sb = rcd.quantize(torch.randn((N, K), generator=g, device=d), 128)
+    say("gemm_quant past 32 bits", M, N, K)
+    c = rcd.gemm_quant(a, sa, b, sb)
+    torch.cuda.synchronize()
+    for rows in (slice(M - 130, M), slice((1 << 31) // N - 2, (1 << 31) // N + 2), slice(0, 2)):
+        ref, mag, _ = gemm_ref(a[rows], sa[:, rows], b, sb, 128)
+        tol = ((K + 40) * 2.0 ** -24 + DROP) * mag
+        tol = tol + 2.0 ** -8 * (np.abs(ref) + tol)
+        assert (np.abs(np64(c[rows]) - ref) <= tol).all()
+    # ... and the quantiser over as many source elements
+    x = torch.randn((1 << 20, 16), generator=g, device=d).to(torch.bfloat16)
+    wide = x.repeat(1, 132)[:, :2112].contiguous()
+    wide = torch.as_strided(wide, (1 << 20, 2112), (2112, 1))
+    q, s = rcd.quantize(wide)
+    torch.cuda.synchronize()
+    v, amax = bq.quotients(np64(wide[-3:]))
+    assert np.array_equal(np64(q[-3:]), bq.round_e4m3(v))
+
+
+def test_linear_layer_forward_and_gradients():
+    # y = x W^T, dx = dy W, dW = dy^T x from the same quantiser and product,
+    # against the fp64 products of the quantised values, and dL of a step
+    # along each gradient against the difference of L = <y, dy> (linear in x
+    # and in W, so the difference is exact up to the products' tolerance)
+    d = dev()
+    T, I, O = 200, 300, 150
+    x, w, dy = rand((T, I), 1).to(d), rand((O, I), 2).to(d), rand((T, O), 3).to(d)
+    y = check_gemm(*rcd.quantize(x), *rcd.quantize(w, 128), 128, torch.float32)
+    dx = check_gemm(*rcd.quantize(dy), *rcd.quantize(w, 128, transpose=True), 128, torch.float32)
+    dw = check_gemm(*rcd.quantize(dy, 1, True), *rcd.quantize(x, 1, True), 1, torch.float32)
+    assert y.shape == (T, O) and dx.shape == (T, I) and dw.shape == (O, I)
+    x64, w64, dy64 = np64(x), np64(w), np64(dy)
+    # quantisation moves a value by 2^-4 at most (half a step of 3 mantissa
+    # bits), or by half the smallest step, 2^-10 amax / 448, of its block;
+    # amax of these blocks is below 6
+    eps, sub = 2.0 ** -4, 6 * 2.0 ** -10 / 448
+    for got, p, q in ((y, x64, w64.T), (dx, dy64, w64), (dw, dy64.T, x64)):
+        mag = np.abs(p) @ np.abs(q)
+        n = p.shape[1]
+        tol = (2 * eps + eps * eps) * mag + 8 * n * 6 * sub + 1e-5 * mag
+        assert (np.abs(np64(got) - p @ q) <= tol).all()
+    for g, base, step in ((dx, x64, rand((T, I), 4)), (dw, w64, rand((O, I), 5))):
+        st = np64(step)
+        L = lambda a, b: ((a @ b.T) * dy64).sum()  # noqa: E731
+        diff = (L(base + st, w64) - L(base - st, w64)) / 2 if g is dx else (L(x64, base + st) - L(x64, base - st)) / 2
+        # the error of each entry above, as independent signs: 6 standard deviations of a uniform rounding error
+        p, q = (dy64, w64) if g is dx else (dy64.T, x64)
+        sigma = np.sqrt(((st ** 2) * (2 * (eps / np.sqrt(3)) ** 2 * ((p ** 2) @ (q ** 2)))).sum())
+        assert abs((np64(g) * st).sum() - diff) <= 6 * sigma
+
+
+# --------------------------------------------------------------- experts
+def quant_weights(E, L, F, seed):
+    d = dev()
+    out = []
+    for i, (r, c) in enumerate(((F, L), (F, L), (L, F))):
+        q, s = rcd.quantize((rand((E * r, c), seed + i) * c ** -0.5).to(d), 128)
+        out.append((q.view(E, r, c), s.view(E, r // 128, c // 128)))
+    return out
+
+
+def offsets_of(counts):
+    return torch.tensor(np.concatenate([[0], np.cumsum(counts)]), dtype=torch.int32)
+
+
+def expert_rows_ref(x, wg, wu, wd):
+    """(out, bound) of one expert's rows in fp64.  The bound follows the
+    dropped bits and fp32 sums through the SwiGLU and the requantisation: a
+    hidden value may take any e4m3 value its quotient's interval reaches."""
+    u = bq.values(*bq.quantize(x), 1)
+    K = u.shape[1]
+
+    def prod(p, q):
+        mag = np.abs(p) @ np.abs(q).T
+        return p @ q.T, (K + 16) * 2.0 ** -24 * mag + DROP * bq.group_peaks(p, q)
+    a, ea = prod(u, wg)
+    b, eb = prod(u, wu)
+    sa = bq.silu(a)
+    h = sa * b
+    eh = 1.1 * ea * (np.abs(b) + eb) + np.abs(sa) * eb + 2.0 ** -20 * np.abs(h)
+    rows, F = h.shape
+    hb, ehb = h.reshape(rows, -1, 128), eh.reshape(rows, -1, 128)
+    amax = np.maximum(np.abs(hb).max(2, keepdims=True), bq.TINY)
+    eamax = ehb.max(2, keepdims=True)
+    v = hb * 448 / amax
+    ev = 448 * (ehb / amax + np.abs(hb) * eamax / amax ** 2) + 2.0 ** -20 * np.abs(v)
+    q = bq.round_e4m3(v)
+    dq = np.maximum(np.abs(bq.round_e4m3(np.clip(v + ev, -448, 448)) - q), np.abs(bq.round_e4m3(np.clip(v - ev, -448, 448)) - q))
+    s, es = amax / 448, eamax / 448
+    hv = (q * s).reshape(rows, F)
+    dh = (dq * (s + es) + np.abs(q) * es).reshape(rows, F)
+    o = hv @ wd.T
+    e = dh @ np.abs(wd).T + (F + 16) * 2.0 ** -24 * (np.abs(hv) @ np.abs(wd).T)
+    e = e + DROP * bq.group_peaks(np.abs(hv) + dh, wd)
+    return o, e + 2.0 ** -8 * (np.abs(o) + e)
+
+
+def check_experts(E, L, F, counts, seed, per_expert=6, extra=0):
+    d = dev()
+    n = int(np.sum(counts))
+    say("experts_dropless_quant", E, L, F, "rows", list(counts)[:12])
+    k = 1
+    cfg = rcd.make_config(n + extra, 64, L, E, 1, k, F)
+    w = quant_weights(E, L, F, seed)
+    xs = rand((n + extra, L), seed + 9, torch.bfloat16, 0.5).to(d)
+    off = offsets_of(counts).to(d)
+    out = torch.full((n + extra, L), 9.0, dtype=torch.bfloat16, device=d)
+    rcd.experts_dropless_quant(cfg, xs, off, *w, expert_out=out)
+    torch.cuda.synchronize()
+    assert (out[n:] == 9).all()  # rows behind the last expert are left as they were
+    vals = [np.stack([bq.values(np64(q[e]), np64(s[e]), 128) for e in range(E)]) for q, s in w]
+    x, got = np64(xs), np64(out)
+    rng = np.random.default_rng(seed)
+    start = 0
+    for e, c in enumerate(counts):
+        if c:
+            rows = np.unique(np.concatenate([[0, c - 1], rng.integers(0, c, min(per_expert, c))])) + start
+            ref, bound = expert_rows_ref(x[rows], vals[0][e], vals[1][e], vals[2][e])
+            err = np.abs(got[rows] - ref)
+            assert (err <= bound).all(), (e, (err / bound).max())
+            # the bound holds for the worst case: the norm tells a wrong row
+            # (rounding to bf16 2^-9 rms, a few hidden values a step off)
+            assert np.linalg.norm(got[rows] - ref) <= 2.0 ** -6 * np.linalg.norm(ref), e
+        start += c
+    return out
+
+
+@pytest.mark.parametrize("E,L,F,counts", [
+    (1, 128, 128, [1]), (4, 256, 128, [1, 0, 0, 3]), (4, 128, 256, [0, 16, 17, 0]), (8, 256, 256, [0, 0, 0, 0, 0, 0, 0, 5]),
+    (3, 384, 128, [33, 1, 64]), (4, 256, 256, [70, 0, 130, 3]), (2, 128, 384, [300, 40]), (4, 128, 128, [257, 255, 256, 1]),
+    (2, 256, 128, [513, 700]), (70, 128, 128, [3] * 64 + [0, 1, 20, 0, 2, 9]), (5, 128, 256, [2, 2, 400, 0, 1])])
+def test_experts_match_oracle(E, L, F, counts):
+    check_experts(E, L, F, counts, E + L + F)
+
+
+def test_experts_leave_other_rows():
+    check_experts(4, 128, 128, [3, 0, 2, 40], 3, extra=37)
+    check_experts(4, 128, 128, [0, 0, 0, 0], 4, extra=20)
+    check_experts(2, 256, 128, [300, 280], 5, extra=600)
+
+
+def test_experts_keep_bad_offsets_inside_the_rows():
+    # offsets outside [0, rows] or falling: no row outside is touched, and an
+    # expert whose range is sound gets its rows
+    d = dev()
+    E, L, F, n = 4, 128, 128, 50
+    w = quant_weights(E, L, F, 6)
+    xs = rand((n, L), 7, torch.bfloat16).to(d)
+    cfg = rcd.make_config(n, 64, L, E, 1, 1, F)
+    good = rcd.experts_dropless_quant(cfg, xs, offsets_of([20, 10, 10, 10]).to(d), *w)
+    bad = torch.tensor([0, 20, 10, 1 << 30, -7], dtype=torch.int32, device=d)
+    out = torch.full((n + 64, L), 9.0, dtype=torch.bfloat16, device=d)
+    rcd.experts_dropless_quant(cfg, xs, bad, *w, expert_out=out[:n])
+    torch.cuda.synchronize()
+    assert (out[n:] == 9).all() and torch.equal(out[:10], good[:10])
+
+
+def test_experts_rows_do_not_depend_on_their_neighbours():
+    # the same row among few and among many rows of its expert: the form of
+    # the products changes with the number of rows, the sums' order does not
+    d = dev()
+    E, L, F = 2, 256, 256
+    w = quant_weights(E, L, F, 11)
+    xs = rand((1000, L), 12, torch.bfloat16).to(d)
+
+    def run(n0, n1):
+        cfg = rcd.make_config(n0 + n1, 64, L, E, 1, 1, F)
+        x = torch.cat([xs[:n0], xs[500:500 + n1]])
+        o = rcd.experts_dropless_quant(cfg, x, offsets_of([n0, n1]).to(d), *w)
+        torch.cuda.synchronize()
+        return np64(o[:n0]), np64(o[n0:])
+    base = run(500, 400)
+    for n0, n1 in ((3, 5), (40, 30), (100, 120), (200, 300)):
+        for got, ref in zip(run(n0, n1), base):
+            ref = ref[:got.shape[0]]
+            assert np.linalg.norm(got - ref) <= 2.0 ** -7 * np.linalg.norm(ref)
+
+
+def test_two_streams_and_graph_replay():
+    d = dev()
+    E, L, F, n = 8, 256, 256, 300
+    w = quant_weights(E, L, F, 21)
+    rng = np.random.default_rng(3)
+    cases = []
+    for i in range(3):
+        c = rng.multinomial(n, np.ones(E) / E)
+        cases.append((rand((n, L), 30 + i, torch.bfloat16).to(d), offsets_of(c).to(d)))
+    cfg = rcd.make_config(n, 64, L, E, 1, 1, F)
+    want = [rcd.experts_dropless_quant(cfg, x, o, *w) for x, o in cases]
+    torch.cuda.synchronize()
+    # two calls at once on streams of their own, each with its workspace
+    streams = [torch.cuda.Stream() for _ in range(2)]
+    got = []
+    for i, st in enumerate(streams):
+        st.wait_stream(torch.cuda.current_stream())
+        with torch.cuda.stream(st):
+            got.append(rcd.experts_dropless_quant(cfg, *cases[i], *w))
+    torch.cuda.synchronize()
+    assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])
+    # captured once, replayed on other rows and counts
+    x, o = cases[0][0].clone(), cases[0][1].clone()
+    out = torch.empty_like(x)
+    ws = rcd._ws(rcd.experts_dropless_quant_ws_bytes(cfg), d)
+    a, sa, b, sb = operands(n, 300, 512, 128, 40)
+    dense = torch.empty((n, 300), dtype=torch.float32, device=d)
+    ref_dense = rcd.gemm_quant(a, sa, b, sb, out_dtype=torch.float32)
+    gws = torch.empty(64 << 20, dtype=torch.uint8, device=d)
+
+    def call():
+        rcd.experts_dropless_quant(cfg, x, o, *w, expert_out=out, ws=ws)
+        rcd.gemm_quant(a, sa, b, sb, out_dtype=torch.float32, out=dense, ws=gws)
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        call()
+    torch.cuda.current_stream().wait_stream(side)
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        call()
+    for i in (0, 1, 2, 1):
+        x.copy_(cases[i][0])
+        o.copy_(cases[i][1])
+        out.zero_()
+        dense.zero_()
+        ws.fill_(255)  # nothing in a workspace needs clearing
+        torch.cuda.synchronize()
+        graph.replay()
+        torch.cuda.synchronize()
+        assert torch.equal(out, want[i]) and torch.equal(dense, ref_dense)
+
+
+def test_route_dispatch_experts_combine_together():
+    # one layer as it is used: scored routing, dropless dispatch, 8-bit experts, combine
+    from oracle import scored_routing as sr
+    d = dev()
+    w = synth.workload("mid_bf16").replace(T=200)
+    cfg = rcd.config_of(w)
+    T, E, k, L, F = w.T, w.n_experts, w.top_k, w.d_latent, w.d_ff
+    z = rand((T, L), 50, torch.bfloat16).to(d)
+    logits = rand((T, E), 51).to(d)
+    bias = (0.05 * rand((E,), 52)).to(d)
+    wq = quant_weights(E, L, F, 53)
+    sc = rcd.scoring("sigmoid", 8, 4, 2, True, 1.0)
+    topk, gates = rcd.route_scored(cfg, sc, logits, bias)
+    ds = rcd.dispatch_dropless(cfg, topk, z)
+    eo = rcd.experts_dropless_quant(cfg, ds["xs"], ds["expert_offsets"], *wq)
+    y = rcd.combine_dropless(cfg, eo, ds["row_of"], gates)
+    torch.cuda.synchronize()
+    ids = sr.select(logits.cpu().numpy(), bias.cpu().numpy(), k, "sigmoid", 8, 4, 2)
+    assert np.array_equal(topk.cpu().numpy(), ids)
+    g = sr.gates(logits.cpu().numpy(), ids, "sigmoid")
+    vals = [[bq.values(np64(q[e]), np64(s[e]), 128) for e in range(E)] for q, s in wq]
+    x = np64(z)
+    for t in (0, 1, 99, 199):
+        ref, bound = np.zeros(L), np.zeros(L)
+        for j in range(k):
+            e = ids[t, j]
+            o, b = expert_rows_ref(x[t:t + 1], vals[0][e], vals[1][e], vals[2][e])
+            ref += g[t, j] * o[0]
+            bound += g[t, j] * b[0]
+        bound = bound + 2.0 ** -8 * (np.abs(ref) + bound) + 2.0 ** -18 * np.abs(ref)
+        assert (np.abs(np64(y[t]) - ref) <= bound).all()

@@ -1,0 +1,205 @@
+"""route_scored and its gradient against the fp64 oracle.
+
+Tolerances.  A gate is made of fp32 operations on scores: an exponential (one
+ulp, 2^-23), 1 + e (2^-24) and a division (2^-24) put a sigmoid within 2^-22;
+a softmax score also divides by a sum of at most 1024 terms in at most 70
+steps, each 2^-24, so within 2^-17; the renormalising sum and quotient and the
+scale add at most 2^-20.  Gradients are held to the same bound of the formula's
+value on magnitudes (cancellation included).  Ids are equal."""
+import numpy as np
+import pytest
+import torch
+
+import routing_capacity_dispatch_amd as rcd
+from gpu_common import dev, np_i, say
+from oracle import scored_routing as sr
+
+pytestmark = pytest.mark.gpu
+RTOL = {"sigmoid": 2.0 ** -20, "softmax": 2.0 ** -16}
+FLOOR = 2.0 ** -140  # results below fp32's normal range
+
+
+def cfg_of(T, E, k):
+    return rcd.make_config(T, 64, 64, E, 1, k, 64)
+
+
+def check(T, E, k, logits, bias, kind, groups=1, top_groups=1, group_top=2, renorm=True, scale=2.5):
+    d = dev()
+    say("route_scored", T, E, k, kind, groups, top_groups, group_top, renorm)
+    sc = rcd.scoring(kind, groups, top_groups, group_top, renorm, scale)
+    lt = torch.from_numpy(logits).to(d)
+    bt = None if bias is None else torch.from_numpy(bias).to(d)
+    topk, gates = rcd.route_scored(cfg_of(T, E, k), sc, lt, bt)
+    torch.cuda.synchronize()
+    ids = np_i(topk)
+    ref = sr.select(logits, bias, k, kind, groups, top_groups, group_top)
+    assert np.array_equal(ids, ref), np.argwhere(ids != ref)[:5]
+    g = gates.cpu().numpy().astype(np.float64)
+    rg = sr.gates(logits, ref, kind, renorm, scale)
+    assert (np.abs(g - rg) <= RTOL[kind] * np.abs(rg) + FLOOR).all(), np.abs(g - rg).max()
+    # the gradient for this selection
+    dg = np.random.default_rng(T + E).standard_normal((T, k)).astype(np.float32)
+    dl = rcd.route_scored_backward(cfg_of(T, E, k), sc, lt, topk, torch.from_numpy(dg).to(d))
+    torch.cuda.synchronize()
+    rd, mag = sr.backward(logits, ref, dg, kind, renorm, scale)
+    err = np.abs(dl.cpu().numpy().astype(np.float64) - rd)
+    assert (err <= RTOL[kind] * mag + FLOOR).all(), (err / (mag + FLOOR)).max()
+
+
+@pytest.mark.parametrize("kind", ["sigmoid", "softmax"])
+@pytest.mark.parametrize("renorm", [False, True])
+@pytest.mark.parametrize("T,E,k", [(1, 1, 1), (1, 384, 8), (3, 5, 5), (5, 16, 1), (7, 60, 6), (64, 64, 8), (130, 65, 2),
+                                   (33, 128, 4), (100, 384, 8), (17, 1000, 8), (9, 1024, 64), (5, 100, 33),
+                                   (66, 256, 7), (31, 15, 3), (4, 512, 9)])
+def test_matches_oracle(T, E, k, kind, renorm):
+    rng = np.random.default_rng(T * 1000 + E)
+    logits = (1.5 * rng.standard_normal((T, E))).astype(np.float32)
+    bias = (0.05 * rng.standard_normal(E)).astype(np.float32)
+    check(T, E, k, logits, bias if E % 2 else None, kind, renorm=renorm)
+
+
+@pytest.mark.parametrize("kind", ["sigmoid", "softmax"])
+@pytest.mark.parametrize("group_top", [1, 2])
+@pytest.mark.parametrize("T,E,k,G,tg", [(1, 384, 8, 8, 4), (65, 384, 8, 8, 4), (40, 256, 8, 8, 4), (20, 64, 8, 8, 1),
+                                        (30, 60, 6, 4, 2), (12, 12, 3, 12, 3), (10, 64, 2, 64, 40), (9, 1024, 8, 16, 5),
+                                        (25, 160, 6, 8, 3), (11, 384, 20, 8, 4), (21, 96, 4, 3, 1), (8, 70, 5, 7, 2)])
+def test_group_limit_matches_oracle(T, E, k, G, tg, group_top, kind):
+    rng = np.random.default_rng(T * 7 + E + G)
+    logits = (1.5 * rng.standard_normal((T, E))).astype(np.float32)
+    bias = (0.05 * rng.standard_normal(E)).astype(np.float32)
+    check(T, E, k, logits, bias, kind, G, tg, group_top)
+
+
+@pytest.mark.parametrize("kind", ["sigmoid", "softmax"])
+@pytest.mark.parametrize("G,tg", [(1, 1), (8, 3)])
+def test_equal_keys_take_the_lower_index(kind, G, tg):
+    rng = np.random.default_rng(5)
+    # few distinct logits and biases: equal keys within and across groups
+    logits = rng.choice(np.array([-1.0, 0.0, -0.0, 0.5], dtype=np.float32), size=(200, 64))
+    bias = rng.choice(np.array([0.0, 0.25], dtype=np.float32), size=64)
+    check(200, 64, 8, logits, bias, kind, G, tg)
+    check(200, 64, 8, logits, None, kind, G, tg)
+    check(3, 384, 8, np.zeros((3, 384), np.float32), None, kind, G, tg)
+
+
+@pytest.mark.parametrize("kind", ["sigmoid", "softmax"])
+@pytest.mark.parametrize("G,tg", [(1, 1), (4, 2)])
+def test_keys_that_fp32_cannot_tell_apart(kind, G, tg):
+    # logits one fp32 step apart near 6 (a sigmoid's slope there is 2^-9, so
+    # the scores differ by 2^-30) in random order: only fp64 keys order them
+    rng = np.random.default_rng(6)
+    E, T = 64, 150
+    steps = np.stack([rng.permutation(E) for _ in range(T)])
+    logits = (np.float32(6.0) + steps.astype(np.float32) * np.float32(2.0 ** -21)).astype(np.float32)
+    check(T, E, 8, logits, None, kind, G, tg)
+    # ... and scores whose differences the bias nearly cancels
+    l = (1.5 * rng.standard_normal((T, E))).astype(np.float32)
+    l[:] = l[:1]
+    s = sr.scores(l[:1], kind)[0]
+    bias = (0.5 - s).astype(np.float32)  # every key within 2^-25 of 0.5
+    check(T, E, 8, l, bias, kind, G, tg)
+
+
+@pytest.mark.parametrize("kind", ["sigmoid", "softmax"])
+@pytest.mark.parametrize("G,tg", [(1, 1), (4, 2)])
+def test_infinite_and_extreme_logits(kind, G, tg):
+    rng = np.random.default_rng(7)
+    T, E = 40, 48
+    l = (2 * rng.standard_normal((T, E))).astype(np.float32)
+    l[:, ::3] = -np.inf                       # masked experts score 0
+    l[0] = -np.inf                            # nothing left: ids in index order, gates 0
+    l[1] = -np.inf
+    l[1, 17] = 0.5
+    l[2] = -3.4028235e38                      # the type's lowest value
+    l[3, :5] = [80.0, -80.0, 30.0, -30.0, 100.0]
+    l[4] = -200.0                             # sigmoid underflows in fp32
+    check(T, E, 6, l, None, kind, G, tg)
+    check(T, E, 6, l, None, kind, G, tg, renorm=False)
+    bias = np.zeros(E, np.float32)
+    bias[5:30] = -np.inf                      # never selected while others are left
+    check(T, E, 6, (2 * rng.standard_normal((T, E))).astype(np.float32), bias, kind, G, tg)
+
+
+def test_no_tokens():
+    d = dev()
+    sc = rcd.scoring("sigmoid")
+    cfg = cfg_of(0, 16, 2)
+    topk, gates = rcd.route_scored(cfg, sc, torch.empty((0, 16), device=d))
+    assert topk.shape == (0, 2) and gates.shape == (0, 2)
+    assert rcd.route_scored_backward(cfg, sc, torch.empty((0, 16), device=d), topk, gates).shape == (0, 16)
+
+
+@pytest.mark.parametrize("kind", ["sigmoid", "softmax"])
+def test_backward_ids_outside_and_twice(kind):
+    d = dev()
+    rng = np.random.default_rng(8)
+    T, E, k = 30, 40, 4
+    l = rng.standard_normal((T, E)).astype(np.float32)
+    ids = np.stack([rng.permutation(E)[:k] for _ in range(T)])
+    ids[3, 1] = ids[3, 0]
+    ids[4] = ids[4, 0]
+    ids[5, 2], ids[6, 0], ids[7] = -1, E, [-5, 1 << 30, E + 1, -(1 << 31)]
+    dg = rng.standard_normal((T, k)).astype(np.float32)
+    for renorm in (False, True):
+        sc = rcd.scoring(kind, renormalise=renorm, scale=1.5)
+        got = rcd.route_scored_backward(cfg_of(T, E, k), sc, torch.from_numpy(l).to(d),
+                                        torch.from_numpy(ids.astype(np.int32)).to(d), torch.from_numpy(dg).to(d))
+        torch.cuda.synchronize()
+        ref, mag = sr.backward(l, ids, dg, kind, renorm, 1.5)
+        # row 7 has no expert: S is the 1e-20 of the formula and every factor is 0
+        assert (np.abs(got.cpu().numpy() - ref) <= RTOL[kind] * mag + FLOOR).all()
+
+
+def test_large_batch_matches_small_ones():
+    # a batch of every size class gives each token what it gets alone
+    d = dev()
+    g = torch.Generator(device="cpu").manual_seed(9)
+    T, E, k = 5000, 384, 8
+    l = (1.5 * torch.randn((T, E), generator=g)).to(d)
+    b = (0.05 * torch.randn(E, generator=g)).to(d)
+    sc = rcd.scoring("sigmoid", 8, 4, 2, True, 2.5)
+    topk, gates = rcd.route_scored(cfg_of(T, E, k), sc, l, b)
+    for t in (0, 1, 2, 3, 17, 4095, 4999):
+        t1, g1 = rcd.route_scored(cfg_of(1, E, k), sc, l[t:t + 1].contiguous(), b)
+        assert torch.equal(t1[0], topk[t]) and torch.equal(g1[0], gates[t])
+    ln, ref = l.cpu().numpy(), None
+    ref = sr.select(ln[:600], b.cpu().numpy(), k, "sigmoid", 8, 4, 2)
+    assert np.array_equal(np_i(topk)[:600], ref)
+
+
+def test_graph_replays_and_side_stream():
+    d = dev()
+    g = torch.Generator(device="cpu").manual_seed(10)
+    T, E, k = 300, 64, 6
+    cfg, sc = cfg_of(T, E, k), rcd.scoring("softmax", 4, 2, 2, False, 1.0)
+    ls = [torch.randn((T, E), generator=g).to(d) for _ in range(3)]
+    b = (0.05 * torch.randn(E, generator=g)).to(d)
+    dgs = [torch.randn((T, k), generator=g).to(d) for _ in range(3)]
+    x, dg = ls[0].clone(), dgs[0].clone()
+    out = dict(topk_idx=torch.empty((T, k), dtype=torch.int32, device=d), gates=torch.empty((T, k), device=d))
+    dl = torch.empty((T, E), device=d)
+
+    def call():
+        rcd.route_scored(cfg, sc, x, b, out=out)
+        rcd.route_scored_backward(cfg, sc, x, out["topk_idx"], dg, d_logits=dl)
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        call()
+    torch.cuda.current_stream().wait_stream(side)
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        call()
+    for i in (0, 1, 2, 0):
+        x.copy_(ls[i])
+        dg.copy_(dgs[i])
+        for t in (*out.values(), dl):
+            t.zero_()
+        torch.cuda.synchronize()
+        graph.replay()
+        torch.cuda.synchronize()
+        t2, g2 = rcd.route_scored(cfg, sc, ls[i], b)
+        d2 = rcd.route_scored_backward(cfg, sc, ls[i], t2, dgs[i])
+        torch.cuda.synchronize()
+        assert torch.equal(out["topk_idx"], t2) and torch.equal(out["gates"], g2) and torch.equal(dl, d2)
