@@ -65,8 +65,10 @@ def backward(logits, topk_idx, d_gates, kind, renormalise=True, scale=1.0):
     sel = np.where(on, ids, 0).ravel()
     out, bound = np.zeros((T, E)), np.zeros((T, E))
     if kind == "sigmoid":
-        np.add.at(out, (rows, sel), (ds * s * (1 - s)).ravel())
-        np.add.at(bound, (rows, sel), (mag * s * (1 - s)).ravel())
+        # 1 - s as the score of -l: the difference would lose what is below 2^-53
+        rest = np.take_along_axis(scores(-np.asarray(logits, dtype=np.float64), kind), np.where(on, ids, 0), axis=1)
+        np.add.at(out, (rows, sel), (ds * s * rest).ravel())
+        np.add.at(bound, (rows, sel), (mag * s * rest).ravel())
         return out, bound
     np.add.at(out, (rows, sel), ds.ravel())
     np.add.at(bound, (rows, sel), mag.ravel())

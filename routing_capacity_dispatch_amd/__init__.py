@@ -627,7 +627,7 @@ def _operand(q, what, dev=None):
     _check(isinstance(q, torch.Tensor) and q.dim() == 2 and q.is_cuda and q.dtype == torch.float8_e4m3fn
            and (dev is None or q.device == dev), f"{what} must be a two-dimensional e4m3 tensor on one GPU")
     _check(q.shape[1] <= 1 or q.stride(1) == 1, f"the columns of {what} must be contiguous")
-    return q.stride(0) if q.shape[0] > 1 else q.shape[1]
+    return q.stride(0) if q.shape[0] > 1 and q.shape[1] > 0 else q.shape[1]
 
 
 def _scale_ld(s, shape, what, dev):

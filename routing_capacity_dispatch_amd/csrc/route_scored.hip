@@ -159,9 +159,11 @@ __global__ __launch_bounds__(256) void route_scored_bwd_kernel(ScoreArgs a, cons
   const bool on = idx >= 0 && idx < E;
   const float l = row[on ? idx : 0];
   float p[NPER];
-  float s;
+  float s, rest = 0.0f;  // rest: 1 - sigmoid, from its own formula (1 - s loses bits near 1)
   if (a.sigmoid) {
-    s = on ? 1.0f / (1.0f + expf(-l)) : 0.0f;
+    const float x = expf(-fabsf(l)), r = 1.0f / (1.0f + x);
+    s = on ? (l >= 0.0f ? r : x * r) : 0.0f;
+    rest = l >= 0.0f ? x * r : r;
   } else {
     float mx = -3.402823466e38f, sum = 0.0f;
 #pragma unroll
@@ -194,7 +196,7 @@ __global__ __launch_bounds__(256) void route_scored_bwd_kernel(ScoreArgs a, cons
   float base = 0.0f;
   float val;
   if (a.sigmoid) {
-    val = ds * s * (1.0f - s);
+    val = ds * s * rest;
   } else {
     val = ds;
     base = ds * s;

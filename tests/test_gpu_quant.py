@@ -45,17 +45,23 @@ def check_quantize(x, block, transpose):
     q, s = rcd.quantize(x.to(d) if not x.is_cuda else x, block, transpose)
     torch.cuda.synchronize()
     xn = np64(x)
-    v, amax = bq.quotients(xn, block, transpose)
+    with np.errstate(invalid="ignore"):
+        v, amax = bq.quotients(xn, block, transpose)
+    # values of a block with an infinity or a NaN are unspecified
+    fine = np.isfinite(amax)
+    each = np.repeat(np.repeat(fine, block, axis=0)[:v.shape[0]], 128, axis=1)
+    v = np.where(each, v, 0.0)
     ref = bq.round_e4m3(v)
     got = np64(q)
     assert got.shape == ref.shape
     if x.dtype == torch.bfloat16:
-        assert np.array_equal(got, ref)
+        assert np.array_equal(got[each], ref[each])
     else:
         lo, hi = bq.round_e4m3(v * (1 - 2.0 ** -22)), bq.round_e4m3(np.clip(v * (1 + 2.0 ** -22), -448, 448))
-        assert ((got >= np.minimum(lo, hi)) & (got <= np.maximum(lo, hi))).all()
+        assert ((got >= np.minimum(lo, hi)) & (got <= np.maximum(lo, hi)))[each].all()
     want = amax.astype(np.float32) / np.float32(448)
-    assert np.array_equal(s.cpu().numpy(), want.T if block == 1 else want)
+    s = s.cpu().numpy().T if block == 1 else s.cpu().numpy()
+    assert np.array_equal(s[fine], want[fine])
 
 
 @pytest.mark.parametrize("transpose", [False, True])
@@ -86,7 +92,8 @@ def test_quantize_extreme_magnitudes_and_ties(dtype, block, transpose):
     x[0, 1] = 1.0
     x[129, 129:140] = 2.0 ** -120              # below the smallest block magnitude
     x[130:140, 150:290] = 1e-30
-    x[200:210, :] = torch.linspace(-3e38, 3e38, 300)
+    x[200:210, :] = torch.linspace(-3e38, 3e38, 300)  # its fp32 steps overflow: blocks with infinities
+    x[210:215, :] = torch.linspace(-1.0, 1.0, 300) * 3e38
     # amax 1.75 makes the factor 256: every midpoint between e4m3 values occurs
     mid = torch.from_numpy((bq.MAGNITUDES[1:] + bq.MAGNITUDES[:-1]) / 512).float()
     x[256, :126] = mid
