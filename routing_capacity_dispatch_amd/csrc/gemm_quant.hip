@@ -9,6 +9,8 @@
 // the order of K inside a block does not matter as long as it is the same:
 // lane l takes bytes 16 (l >> 4) .. + 15 and 64 + 16 (l >> 4) .. + 15 of row
 // l & 15, which makes each load instruction read 64 contiguous bytes a row.
+#include <type_traits>
+
 #include "gemm_core.h"
 #include "kernels.h"
 #include "quant.h"
@@ -312,6 +314,144 @@ __device__ __forceinline__ void quant_loop(const RowSrc<TL::A_INS>& a, const Row
   __syncthreads();
 }
 
+// The same sum with the steps of consecutive blocks run into one another, so
+// that the matrix cores always have operands in registers.  Per block, each
+// wavefront goes through its MI row blocks: while the MFMAs of one row block
+// run, the fragment of the next is read from LDS, and the results of two
+// MFMAs before are scaled and added.  At the last row block every read of
+// this stage is done: one barrier (the next block has landed; this stage is
+// free), then the loads of the block after next and the next block's first
+// fragments go in among its MFMAs, each B fragment into the registers that
+// its last MFMA has just read.
+template <class TL, int kMode>
+__device__ __forceinline__ void quant_pipe(const RowSrc<TL::A_INS>& a, const RowSrc<TL::B_INS>& b, const float* sp,
+                                           int64_t s_step, int nb, char* lds, QAcc<TL>& acc) {
+  using Q = QTile<TL>;
+  constexpr int MI = TL::MI, NI = TL::NI, NM = MI * NI;
+  constexpr int kLag = 2;
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+  const int wm = wave / TL::WGN, wn = wave % TL::WGN;
+#pragma unroll
+  for (int mi = 0; mi < MI; ++mi)
+#pragma unroll
+    for (int ni = 0; ni < NI; ++ni) acc.v[mi][ni] = f32x4_t{0.f, 0.f, 0.f, 0.f};
+  if (nb <= 0) return;
+  // one load instruction of a block: A rows, B rows, scales
+  constexpr int P = TL::A_INS + TL::B_INS + 1;
+  auto issue = [&](int kb, int i) {
+    const int st = kb & 1;
+    if (i < TL::A_INS)
+      lds_load16(a.base[i] + (int64_t)kb * kQB, a.off[i], lds + st * TL::A_BYTES + (i * TL::NW + wave) * 1024);
+    else if (i < TL::A_INS + TL::B_INS)
+      lds_load16(b.base[i - TL::A_INS] + (int64_t)kb * kQB, b.off[i - TL::A_INS],
+                 lds + TL::B_BASE + st * TL::B_BYTES + ((i - TL::A_INS) * TL::NW + wave) * 1024);
+    else
+      lds_load4(sp + kb * s_step, lds + Q::S_BASE + (st * Q::SCALES + wave * 64) * 4);
+  };
+  // fragment addresses inside a stage: the swizzle depends on the lane only,
+  // so row blocks are immediate offsets
+  const int sw = TL::swz(lane & 15);
+  const int c0 = (((lane >> 4) ^ sw) << 4), c1 = (((4 + (lane >> 4)) ^ sw) << 4);
+  const char* ab = lds + (wm * TL::WM + (lane & 15)) * TL::RB;
+  const char* bb = lds + TL::B_BASE + (wn * TL::WN + (lane & 15)) * TL::RB;
+  const char* asb = lds + Q::S_BASE + (wm * TL::WM + (lane >> 4) * 4) * 4;
+  const char* bsb = lds + Q::S_BASE + (TL::BM + wn * TL::WN + (kMode == kRowB ? lane & 15 : 0)) * 4;
+  auto read_a = [&](int st, int mi) {
+    const char* q = ab + st * TL::A_BYTES + mi * 16 * TL::RB;
+    return Frag8{ld16(q + c0), ld16(q + c1)};
+  };
+  auto read_b = [&](int st, int ni) {
+    const char* q = bb + st * TL::B_BYTES + ni * 16 * TL::RB;
+    return Frag8{ld16(q + c0), ld16(q + c1)};
+  };
+  auto read_as = [&](int st, int mi) {
+    return *reinterpret_cast<const f32x4_t*>(asb + (st * Q::SCALES + mi * 16) * 4);
+  };
+  constexpr int NBS = kMode == kRowB ? NI : kMode == kGateUp ? 2 : 1;
+  auto read_bs = [&](int st, float* v) {
+#pragma unroll
+    for (int i = 0; i < NBS; ++i) v[i] = *reinterpret_cast<const float*>(bsb + (st * Q::SCALES + i * 16) * 4);
+  };
+#pragma unroll
+  for (int i = 0; i < P; ++i) issue(0, i);
+  core::wait_loads<0>();
+  if (nb > 1)
+#pragma unroll
+    for (int i = 0; i < P; ++i) issue(1, i);
+  Frag8 fb[NI], fa[2];
+  f32x4_t as[2];
+  float bs[NBS], bs_next[NBS];
+#pragma unroll
+  for (int ni = 0; ni < NI; ++ni) fb[ni] = read_b(0, ni);
+  fa[0] = read_a(0, 0);
+  as[0] = read_as(0, 0);
+  read_bs(0, bs_next);
+  static_assert(MI % 2 == 0, "fragment registers alternate over row blocks");
+  // one block; kAhead: blocks that follow it (0, 1, or 2 for more), so that
+  // every body is straight-line and the accumulators stay in place
+  auto block = [&](int kb, auto ahead) {
+    constexpr int kAhead = decltype(ahead)::value;
+    const int st = kb & 1;
+#pragma unroll
+    for (int i = 0; i < NBS; ++i)
+      bs[i] = kMode == kRowB ? bs_next[i] : __int_as_float(__builtin_amdgcn_readfirstlane(__float_as_int(bs_next[i])));
+    f32x4_t p[kLag + 1];
+    // scales of a row block, times each of B's (kRowB, with a scale per
+    // column, multiplies the result instead: four registers per column block
+    // would not fit)
+    constexpr int NSC = kMode == kRowB ? 1 : NBS;
+    f32x4_t sc[2][NSC];
+    auto add = [&](int j) {
+      const int mi = j / NI, ni = j % NI;
+      const f32x4_t s = sc[mi & 1][kMode == kGateUp ? ni & 1 : 0];
+#pragma unroll
+      for (int r = 0; r < 4; ++r) {
+        const float x = kMode == kRowB ? p[j % (kLag + 1)][r] * bs[ni % NBS] : p[j % (kLag + 1)][r];
+        acc.v[mi][ni][r] = fmaf(x, s[r], acc.v[mi][ni][r]);
+      }
+    };
+#pragma unroll
+    for (int mi = 0; mi < MI; ++mi) {
+      constexpr bool more = kAhead >= 1, more2 = kAhead >= 2;
+      const bool last = mi == MI - 1;
+#pragma unroll
+      for (int i = 0; i < NSC; ++i)
+#pragma unroll
+        for (int r = 0; r < 4; ++r) sc[mi & 1][i][r] = kMode == kRowB ? as[mi & 1][r] : as[mi & 1][r] * bs[i];
+      if (!last) {
+        fa[(mi + 1) & 1] = read_a(st, mi + 1);
+        as[(mi + 1) & 1] = read_as(st, mi + 1);
+      } else if (more) {
+        core::wait_loads<0>();
+        fa[0] = read_a(st ^ 1, 0);
+        as[0] = read_as(st ^ 1, 0);
+        read_bs(st ^ 1, bs_next);
+      }
+#pragma unroll
+      for (int ni = 0; ni < NI; ++ni) {
+        const int j = mi * NI + ni;
+        p[j % (kLag + 1)] = mfma_block(fa[mi & 1], fb[ni]);
+        if (last) {
+          if (more) fb[ni] = read_b(st ^ 1, ni);
+          if (more2)
+#pragma unroll
+            for (int i = 0; i < P; ++i)
+              if (i * NI / P == ni) issue(kb + 2, i);
+        }
+        if (j >= kLag) add(j - kLag);
+        __builtin_amdgcn_sched_barrier(0);
+      }
+    }
+#pragma unroll
+    for (int j = NM - kLag; j < NM; ++j) add(j);
+  };
+  int kb = 0;
+  for (; kb + 2 < nb; ++kb) block(kb, std::integral_constant<int, 2>{});
+  if (kb + 1 < nb) block(kb++, std::integral_constant<int, 1>{});
+  block(kb, std::integral_constant<int, 0>{});
+  __syncthreads();
+}
+
 // Tile t of the grouped products: the expert that holds it.  Every wavefront
 // finds it from the offsets: 64 experts at a time, a scan of their tile
 // counts.  Each XCD takes an eighth of the tiles, contiguous.  Returns false
@@ -419,7 +559,10 @@ __global__ __launch_bounds__(TL::THREADS) void product_kernel(QuantGemm g, int t
     step = kMode == kRowB ? g.b_scale_ld : 1;
   }
   QAcc<TL> acc;
-  quant_loop<TL, kMode, kWide>(a, b, sp, step, nb, lds, acc);
+  if constexpr (kWide)
+    quant_loop<TL, kMode, true>(a, b, sp, step, nb, lds, acc);
+  else
+    quant_pipe<TL, kMode>(a, b, sp, step, nb, lds, acc);
   const int wm = wave / TL::WGN, wn = wave % TL::WGN;
   if (partial || g.out_dt == DT_F32) {
     float* C = partial ? partial + ((int64_t)blockIdx.y * g.M + m0) * g.N + n0
@@ -523,7 +666,7 @@ __global__ __launch_bounds__(TL::THREADS) void gate_up_kernel(QuantGateUp g, int
     sp = (((j - TL::BM) >> 4) & 1 ? g.su : g.sg) + ((int64_t)e * tiles_n + fb) * nb;
   }
   QAcc<TL> acc;
-  quant_loop<TL, kGateUp, false>(a, b, sp, step, nb, lds, acc);
+  quant_pipe<TL, kGateUp>(a, b, sp, step, nb, lds, acc);
   // h over the gate registers; its largest magnitude per row: lanes, then
   // wavefronts of the row
   const int wm = wave / TL::WGN, wn = wave % TL::WGN;
