@@ -205,8 +205,6 @@ __global__ __launch_bounds__(512) void skinny_gate_up_kernel(QuantGateUp g) {
 // row is 128 bytes and the row-major tile of gemm_core.h (direct global ->
 // LDS loads, 16-byte chunks XOR-swizzled) serves e4m3 unchanged.  The block's
 // scales come with it: one float per tile row of A and of B.
-using core::acc_col;
-using core::acc_row;
 using core::load_col;
 using core::load_row;
 using core::lds_load16;
@@ -230,104 +228,32 @@ struct QTile : TL {
   static constexpr int LDS = S_BASE + TL::NS * SCALES * 4;
 };
 
-// Row `r` of a staged operand tile, this lane's 32 bytes.
-template <class TL>
-__device__ __forceinline__ Frag8 lds_frag(const char* st, int row, int lane) {
-  const char* p = st + row * TL::RB;
-  const int sw = TL::swz(row & 15);
-  return Frag8{ld16(p + (((lane >> 4) ^ sw) << 4)), ld16(p + (((4 + (lane >> 4)) ^ sw) << 4))};
-}
+// Matrix instructions of a tile: the weights are the first operand and the
+// activations the second, so a lane's 4 results belong to one row m of C
+// (lane & 15) and 4 consecutive n: one scale of A per lane and row block,
+// packed stores, and row maxima partly inside a lane.
+constexpr int kMB = 16;  // rows and columns of an instruction's result
 
 template <class TL>
 struct QAcc {
-  f32x4_t v[TL::MI][TL::NI];
+  static constexpr int MI = TL::WM / kMB, NI = TL::WN / kMB;
+  f32x4_t v[MI][NI];
 };
 
-// acc += scaled product of the staged block.
+// Sum over K blocks [0, nb).  sp: this lane's scale of block 0, s_step floats
+// to the next.  The steps of consecutive blocks run into one another, so that
+// the matrix cores always have operands in registers: while the MFMAs of one
+// row block run, the fragment of the next is read from LDS, and the results
+// before are scaled and added.  At the last row block every read of this
+// stage is done: one barrier (the next block has landed; this stage is free),
+// then the loads of the block after next and the next block's first fragments
+// go in among its MFMAs, each B fragment into the registers that its last
+// MFMA has just read.  Ends with a barrier, so the caller may reuse the LDS.
 template <class TL, int kMode, bool kWide>
-__device__ __forceinline__ void block_step(const char* sa, const char* sb, const float* sc, QAcc<TL>& acc, int wm,
-                                           int wn, int lane) {
-  Frag8 fb[TL::NI];
-#pragma unroll
-  for (int ni = 0; ni < TL::NI; ++ni) fb[ni] = lds_frag<TL>(sb, wn * TL::WN + ni * 16 + (lane & 15), lane);
-  Wide wb[kWide ? TL::NI : 1];
-  if constexpr (kWide)
-#pragma unroll
-    for (int ni = 0; ni < TL::NI; ++ni) wb[ni] = widen(fb[ni]);
-  // scales of B: one for the wavefront's columns (128 of them share it), one
-  // for its gate and one for its up columns, or one per column
-  const float* scb = sc + TL::BM + wn * TL::WN;
-  float bs[TL::NI];
-#pragma unroll
-  for (int ni = 0; ni < TL::NI; ++ni) {
-    if constexpr (kMode == kRowB)
-      bs[ni] = scb[ni * 16 + (lane & 15)];
-    else
-      bs[ni] = __int_as_float(__builtin_amdgcn_readfirstlane(__float_as_int(scb[kMode == kGateUp ? (ni & 1) * 16 : 0])));
-  }
-#pragma unroll
-  for (int mi = 0; mi < TL::MI; ++mi) {
-    const Frag8 fa = lds_frag<TL>(sa, wm * TL::WM + mi * 16 + (lane & 15), lane);
-    const f32x4_t as = *reinterpret_cast<const f32x4_t*>(sc + wm * TL::WM + mi * 16 + (lane >> 4) * 4);
-    Wide wa;
-    if constexpr (kWide) wa = widen(fa);
-#pragma unroll
-    for (int ni = 0; ni < TL::NI; ++ni) {
-      f32x4_t p;
-      if constexpr (kWide)
-        p = mfma_block(wa, wb[ni]);
-      else
-        p = mfma_block(fa, fb[ni]);
-#pragma unroll
-      for (int r = 0; r < 4; ++r) acc.v[mi][ni][r] = fmaf(p[r], as[r] * bs[ni], acc.v[mi][ni][r]);
-    }
-  }
-}
-
-// Sum over K blocks [0, nb): the next block's loads fly while one is
-// computed.  sp: this lane's scale of block 0, s_step floats to the next.
-// Ends with a barrier, so the caller may reuse the LDS.
-template <class TL, int kMode, bool kWide>
-__device__ __forceinline__ void quant_loop(const RowSrc<TL::A_INS>& a, const RowSrc<TL::B_INS>& b, const float* sp,
-                                           int64_t s_step, int nb, char* lds, QAcc<TL>& acc) {
-  using Q = QTile<TL>;
-  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-  const int wm = wave / TL::WGN, wn = wave % TL::WGN;
-#pragma unroll
-  for (int mi = 0; mi < TL::MI; ++mi)
-#pragma unroll
-    for (int ni = 0; ni < TL::NI; ++ni) acc.v[mi][ni] = f32x4_t{0.f, 0.f, 0.f, 0.f};
-  auto issue = [&](int kb) {
-    const int st = kb & 1;
-    core::issue_rows<TL>(a, (int64_t)kb * kQB, lds + st * TL::A_BYTES, wave);
-    core::issue_rows<TL>(b, (int64_t)kb * kQB, lds + TL::B_BASE + st * TL::B_BYTES, wave);
-    lds_load4(sp + kb * s_step, lds + Q::S_BASE + (st * Q::SCALES + wave * 64) * 4);
-  };
-  if (nb > 0) issue(0);
-  for (int kb = 0; kb < nb; ++kb) {
-    core::wait_loads<0>();
-    if (kb + 1 < nb) issue(kb + 1);
-    const int st = kb & 1;
-    block_step<TL, kMode, kWide>(lds + st * TL::A_BYTES, lds + TL::B_BASE + st * TL::B_BYTES,
-                                 reinterpret_cast<const float*>(lds + Q::S_BASE) + st * Q::SCALES, acc, wm, wn, lane);
-  }
-  __syncthreads();
-}
-
-// The same sum with the steps of consecutive blocks run into one another, so
-// that the matrix cores always have operands in registers.  Per block, each
-// wavefront goes through its MI row blocks: while the MFMAs of one row block
-// run, the fragment of the next is read from LDS, and the results of two
-// MFMAs before are scaled and added.  At the last row block every read of
-// this stage is done: one barrier (the next block has landed; this stage is
-// free), then the loads of the block after next and the next block's first
-// fragments go in among its MFMAs, each B fragment into the registers that
-// its last MFMA has just read.
-template <class TL, int kMode>
 __device__ __forceinline__ void quant_pipe(const RowSrc<TL::A_INS>& a, const RowSrc<TL::B_INS>& b, const float* sp,
                                            int64_t s_step, int nb, char* lds, QAcc<TL>& acc) {
   using Q = QTile<TL>;
-  constexpr int MI = TL::MI, NI = TL::NI, NM = MI * NI;
+  constexpr int MI = QAcc<TL>::MI, NI = QAcc<TL>::NI, NM = MI * NI;
   constexpr int kLag = 2;
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
   const int wm = wave / TL::WGN, wn = wave % TL::WGN;
@@ -351,26 +277,29 @@ __device__ __forceinline__ void quant_pipe(const RowSrc<TL::A_INS>& a, const Row
   // fragment addresses inside a stage: the swizzle depends on the lane only,
   // so row blocks are immediate offsets
   const int sw = TL::swz(lane & 15);
-  const int c0 = (((lane >> 4) ^ sw) << 4), c1 = (((4 + (lane >> 4)) ^ sw) << 4);
+  const int c0 = ((lane >> 4) ^ sw) << 4, c1 = ((4 + (lane >> 4)) ^ sw) << 4;
   const char* ab = lds + (wm * TL::WM + (lane & 15)) * TL::RB;
   const char* bb = lds + TL::B_BASE + (wn * TL::WN + (lane & 15)) * TL::RB;
-  const char* asb = lds + Q::S_BASE + (wm * TL::WM + (lane >> 4) * 4) * 4;
-  const char* bsb = lds + Q::S_BASE + (TL::BM + wn * TL::WN + (kMode == kRowB ? lane & 15 : 0)) * 4;
+  const char* asb = lds + Q::S_BASE + (wm * TL::WM + (lane & 15)) * 4;
+  const char* bsb = lds + Q::S_BASE + (TL::BM + wn * TL::WN + (kMode == kRowB ? (lane >> 4) * 4 : 0)) * 4;
   auto read_a = [&](int st, int mi) {
-    const char* q = ab + st * TL::A_BYTES + mi * 16 * TL::RB;
+    const char* q = ab + st * TL::A_BYTES + mi * kMB * TL::RB;
     return Frag8{ld16(q + c0), ld16(q + c1)};
   };
   auto read_b = [&](int st, int ni) {
-    const char* q = bb + st * TL::B_BYTES + ni * 16 * TL::RB;
+    const char* q = bb + st * TL::B_BYTES + ni * kMB * TL::RB;
     return Frag8{ld16(q + c0), ld16(q + c1)};
   };
   auto read_as = [&](int st, int mi) {
-    return *reinterpret_cast<const f32x4_t*>(asb + (st * Q::SCALES + mi * 16) * 4);
+    return *reinterpret_cast<const float*>(asb + (st * Q::SCALES + mi * kMB) * 4);
   };
+  // scales of B: one for the wavefront's columns (128 of them share it), one
+  // for its gate and one for its up columns, or one per column
   constexpr int NBS = kMode == kRowB ? NI : kMode == kGateUp ? 2 : 1;
-  auto read_bs = [&](int st, float* v) {
+  using BScale = std::conditional_t<kMode == kRowB, f32x4_t, float>;
+  auto read_bs = [&](int st, BScale* v) {
 #pragma unroll
-    for (int i = 0; i < NBS; ++i) v[i] = *reinterpret_cast<const float*>(bsb + (st * Q::SCALES + i * 16) * 4);
+    for (int i = 0; i < NBS; ++i) v[i] = *reinterpret_cast<const BScale*>(bsb + (st * Q::SCALES + i * kMB) * 4);
   };
 #pragma unroll
   for (int i = 0; i < P; ++i) issue(0, i);
@@ -379,8 +308,8 @@ __device__ __forceinline__ void quant_pipe(const RowSrc<TL::A_INS>& a, const Row
 #pragma unroll
     for (int i = 0; i < P; ++i) issue(1, i);
   Frag8 fb[NI], fa[2];
-  f32x4_t as[2];
-  float bs[NBS], bs_next[NBS];
+  float as[2];
+  BScale bs[NBS], bs_next[NBS];
 #pragma unroll
   for (int ni = 0; ni < NI; ++ni) fb[ni] = read_b(0, ni);
   fa[0] = read_a(0, 0);
@@ -391,33 +320,33 @@ __device__ __forceinline__ void quant_pipe(const RowSrc<TL::A_INS>& a, const Row
   // every body is straight-line and the accumulators stay in place
   auto block = [&](int kb, auto ahead) {
     constexpr int kAhead = decltype(ahead)::value;
+    constexpr bool more = kAhead >= 1, more2 = kAhead >= 2;
     const int st = kb & 1;
+    if constexpr (kMode == kRowB) {
+      read_bs(st, bs);  // not ahead: a second set of 4 NI registers would spill
+    } else {
 #pragma unroll
-    for (int i = 0; i < NBS; ++i)
-      bs[i] = kMode == kRowB ? bs_next[i] : __int_as_float(__builtin_amdgcn_readfirstlane(__float_as_int(bs_next[i])));
+      for (int i = 0; i < NBS; ++i) bs[i] = __int_as_float(__builtin_amdgcn_readfirstlane(__float_as_int(bs_next[i])));
+    }
     f32x4_t p[kLag + 1];
-    // scales of a row block, times each of B's (kRowB, with a scale per
-    // column, multiplies the result instead: four registers per column block
-    // would not fit)
-    constexpr int NSC = kMode == kRowB ? 1 : NBS;
-    f32x4_t sc[2][NSC];
+    float sc[2][2];  // this row block's scale, times each of B's
     auto add = [&](int j) {
       const int mi = j / NI, ni = j % NI;
-      const f32x4_t s = sc[mi & 1][kMode == kGateUp ? ni & 1 : 0];
 #pragma unroll
       for (int r = 0; r < 4; ++r) {
-        const float x = kMode == kRowB ? p[j % (kLag + 1)][r] * bs[ni % NBS] : p[j % (kLag + 1)][r];
-        acc.v[mi][ni][r] = fmaf(x, s[r], acc.v[mi][ni][r]);
+        float s = sc[mi & 1][kMode == kGateUp ? ni & 1 : 0];
+        if constexpr (kMode == kRowB) s *= bs[ni][r];
+        acc.v[mi][ni][r] = fmaf(p[j % (kLag + 1)][r], s, acc.v[mi][ni][r]);
       }
     };
 #pragma unroll
     for (int mi = 0; mi < MI; ++mi) {
-      constexpr bool more = kAhead >= 1, more2 = kAhead >= 2;
       const bool last = mi == MI - 1;
+      if constexpr (kMode == kRowB)
+        sc[mi & 1][0] = as[mi & 1];
+      else
 #pragma unroll
-      for (int i = 0; i < NSC; ++i)
-#pragma unroll
-        for (int r = 0; r < 4; ++r) sc[mi & 1][i][r] = kMode == kRowB ? as[mi & 1][r] : as[mi & 1][r] * bs[i];
+        for (int i = 0; i < NBS; ++i) sc[mi & 1][i] = as[mi & 1] * bs[i];
       if (!last) {
         fa[(mi + 1) & 1] = read_a(st, mi + 1);
         as[(mi + 1) & 1] = read_as(st, mi + 1);
@@ -425,12 +354,17 @@ __device__ __forceinline__ void quant_pipe(const RowSrc<TL::A_INS>& a, const Row
         core::wait_loads<0>();
         fa[0] = read_a(st ^ 1, 0);
         as[0] = read_as(st ^ 1, 0);
-        read_bs(st ^ 1, bs_next);
+        if constexpr (kMode != kRowB) read_bs(st ^ 1, bs_next);
       }
+      Wide wa;
+      if constexpr (kWide) wa = widen(fa[mi & 1]);
 #pragma unroll
       for (int ni = 0; ni < NI; ++ni) {
         const int j = mi * NI + ni;
-        p[j % (kLag + 1)] = mfma_block(fa[mi & 1], fb[ni]);
+        if constexpr (kWide)
+          p[j % (kLag + 1)] = mfma_block(widen(fb[ni]), wa);
+        else
+          p[j % (kLag + 1)] = mfma_block(fb[ni], fa[mi & 1]);
         if (last) {
           if (more) fb[ni] = read_b(st ^ 1, ni);
           if (more2)
@@ -450,6 +384,17 @@ __device__ __forceinline__ void quant_pipe(const RowSrc<TL::A_INS>& a, const Row
   if (kb + 1 < nb) block(kb++, std::integral_constant<int, 1>{});
   block(kb, std::integral_constant<int, 0>{});
   __syncthreads();
+}
+
+// Row of this lane's results of row block mi, and the first of its 4 columns
+// of column block ni.
+template <class TL>
+__device__ __forceinline__ int tile_row(int wm, int mi, int lane) {
+  return wm * TL::WM + mi * kMB + (lane & 15);
+}
+template <class TL>
+__device__ __forceinline__ int tile_col(int wn, int ni, int lane) {
+  return wn * TL::WN + ni * kMB + (lane >> 4) * 4;
 }
 
 // Tile t of the grouped products: the expert that holds it.  Every wavefront
@@ -559,37 +504,41 @@ __global__ __launch_bounds__(TL::THREADS) void product_kernel(QuantGemm g, int t
     step = kMode == kRowB ? g.b_scale_ld : 1;
   }
   QAcc<TL> acc;
-  if constexpr (kWide)
-    quant_loop<TL, kMode, true>(a, b, sp, step, nb, lds, acc);
-  else
-    quant_pipe<TL, kMode>(a, b, sp, step, nb, lds, acc);
+  quant_pipe<TL, kMode, kWide>(a, b, sp, step, nb, lds, acc);
+  constexpr int MI = QAcc<TL>::MI, NI = QAcc<TL>::NI;
   const int wm = wave / TL::WGN, wn = wave % TL::WGN;
   if (partial || g.out_dt == DT_F32) {
     float* C = partial ? partial + ((int64_t)blockIdx.y * g.M + m0) * g.N + n0
                        : static_cast<float*>(g.C) + (row0 + m0) * g.ldc + n0;
     const int64_t ld = partial ? g.N : g.ldc;
+    const bool wide_ok = ((reinterpret_cast<uintptr_t>(C) | (uintptr_t)(ld * 4)) & 15) == 0;
 #pragma unroll
-    for (int mi = 0; mi < TL::MI; ++mi)
+    for (int mi = 0; mi < MI; ++mi) {
+      const int row = tile_row<TL>(wm, mi, lane);
+      if (row > mlast) continue;
 #pragma unroll
-      for (int r = 0; r < 4; ++r) {
-        const int row = acc_row<TL>(wm, mi, lane, r);
+      for (int ni = 0; ni < NI; ++ni) {
+        const int col = tile_col<TL>(wn, ni, lane);
+        if (wide_ok && col + 3 <= nlast) {
+          *reinterpret_cast<f32x4_t*>(C + row * ld + col) = acc.v[mi][ni];
+        } else {
 #pragma unroll
-        for (int ni = 0; ni < TL::NI; ++ni) {
-          const int col = acc_col<TL>(wn, ni, lane);
-          if (row <= mlast && col <= nlast) C[row * ld + col] = acc.v[mi][ni][r];
+          for (int r = 0; r < 4; ++r)
+            if (col + r <= nlast) C[row * ld + col + r] = acc.v[mi][ni][r];
         }
       }
+    }
     return;
   }
   constexpr int ld = TL::BN * 2 + kStagePad;
 #pragma unroll
-  for (int mi = 0; mi < TL::MI; ++mi)
+  for (int mi = 0; mi < MI; ++mi)
 #pragma unroll
-    for (int ni = 0; ni < TL::NI; ++ni)
-#pragma unroll
-      for (int r = 0; r < 4; ++r)
-        *reinterpret_cast<uint16_t*>(lds + acc_row<TL>(wm, mi, lane, r) * ld + acc_col<TL>(wn, ni, lane) * 2) =
-            f32_to_bf16(acc.v[mi][ni][r]);
+    for (int ni = 0; ni < NI; ++ni) {
+      const f32x4_t& v = acc.v[mi][ni];
+      *reinterpret_cast<uint2*>(lds + tile_row<TL>(wm, mi, lane) * ld + tile_col<TL>(wn, ni, lane) * 2) =
+          make_uint2(bf16_pair(v[0], v[1]), bf16_pair(v[2], v[3]));
+    }
   __syncthreads();
   uint16_t* C = static_cast<uint16_t*>(g.C) + (row0 + m0) * g.ldc + n0;
   const bool wide_ok = ((reinterpret_cast<uintptr_t>(g.C) | (uintptr_t)(g.ldc * 2)) & 15) == 0;
@@ -666,45 +615,47 @@ __global__ __launch_bounds__(TL::THREADS) void gate_up_kernel(QuantGateUp g, int
     sp = (((j - TL::BM) >> 4) & 1 ? g.su : g.sg) + ((int64_t)e * tiles_n + fb) * nb;
   }
   QAcc<TL> acc;
-  quant_pipe<TL, kGateUp>(a, b, sp, step, nb, lds, acc);
-  // h over the gate registers; its largest magnitude per row: lanes, then
-  // wavefronts of the row
+  quant_pipe<TL, kGateUp, false>(a, b, sp, step, nb, lds, acc);
+  // column blocks 2 q (gate) and 2 q + 1 (up) hold the same features: h over
+  // the gate registers, and its largest magnitude per row: in the lane, the 4
+  // lanes of the row, then the wavefronts of the row
+  constexpr int MI = QAcc<TL>::MI, NI = QAcc<TL>::NI;
   const int wm = wave / TL::WGN, wn = wave % TL::WGN;
   float* part = reinterpret_cast<float*>(lds);  // [BM][WGN]
   constexpr int ld = kQB + kStagePad;
   char* stage = lds + TL::BM * TL::WGN * 4;
 #pragma unroll
-  for (int mi = 0; mi < TL::MI; ++mi)
+  for (int mi = 0; mi < MI; ++mi) {
+    float mx = 0.0f;
 #pragma unroll
-    for (int r = 0; r < 4; ++r) {
-      float mx = 0.0f;
+    for (int q = 0; q < NI / 2; ++q)
 #pragma unroll
-      for (int q = 0; q < TL::NI / 2; ++q) {
+      for (int r = 0; r < 4; ++r) {
         const float h = silu(acc.v[mi][2 * q][r]) * acc.v[mi][2 * q + 1][r];
         acc.v[mi][2 * q][r] = h;
         mx = fmaxf(mx, fabsf(h));
       }
-      for (int d = 1; d < 16; d <<= 1) mx = fmaxf(mx, __shfl_xor(mx, d));
-      if ((lane & 15) == 0) part[acc_row<TL>(wm, mi, lane, r) * TL::WGN + wn] = mx;
-    }
+    mx = fmaxf(mx, __shfl_xor(mx, 16));
+    mx = fmaxf(mx, __shfl_xor(mx, 32));
+    if (lane < 16) part[tile_row<TL>(wm, mi, lane) * TL::WGN + wn] = mx;
+  }
   __syncthreads();
   const int64_t col = (g.offsets ? 0 : (int64_t)e * g.F) + fb * kQB;
 #pragma unroll
-  for (int mi = 0; mi < TL::MI; ++mi)
+  for (int mi = 0; mi < MI; ++mi) {
+    const int row = tile_row<TL>(wm, mi, lane);
+    float amax = kQuantTiny;
 #pragma unroll
-    for (int r = 0; r < 4; ++r) {
-      const int row = acc_row<TL>(wm, mi, lane, r);
-      float amax = kQuantTiny;
+    for (int w = 0; w < TL::WGN; ++w) amax = fmaxf(amax, part[row * TL::WGN + w]);
+    const BlockQuant bq(amax);
 #pragma unroll
-      for (int w = 0; w < TL::WGN; ++w) amax = fmaxf(amax, part[row * TL::WGN + w]);
-      const BlockQuant bq(amax);
-#pragma unroll
-      for (int q = 0; q < TL::NI / 2; ++q)
-        stage[row * ld + wn * (TL::WN / 2) + q * 16 + (lane & 15)] =
-            (char)(e4m3_quad(bq(acc.v[mi][2 * q][r]), 0.f, 0.f, 0.f) & 0xFF);
-      if (wn == 0 && (lane & 15) == 0 && row <= mlast)
-        g.h_scale[(col / kQB) * g.h_scale_ld + row0 + m0 + row] = block_scale(amax);
+    for (int q = 0; q < NI / 2; ++q) {
+      const f32x4_t& v = acc.v[mi][2 * q];
+      *reinterpret_cast<uint32_t*>(stage + row * ld + wn * (TL::WN / 2) + q * 16 + (lane >> 4) * 4) =
+          e4m3_quad(bq(v[0]), bq(v[1]), bq(v[2]), bq(v[3]));
     }
+    if (wn == 0 && lane < 16 && row <= mlast) g.h_scale[(col / kQB) * g.h_scale_ld + row0 + m0 + row] = block_scale(amax);
+  }
   __syncthreads();
   for (int q = threadIdx.x; q < TL::BM * 8; q += TL::THREADS) {
     const int r = q >> 3, c = (q & 7) * 16;
