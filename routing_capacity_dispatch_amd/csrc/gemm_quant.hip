@@ -66,6 +66,21 @@ __device__ __forceinline__ void store_out(int out_dt, void* C, int64_t i, float 
     static_cast<float*>(C)[i] = v;
 }
 
+// n (1 .. 4) neighbouring results from element i on.
+__device__ __forceinline__ void store_run(int out_dt, void* C, int64_t i, const f32x4_t& v, int n) {
+  char* p = static_cast<char*>(C) + i * (out_dt == DT_BF16 ? 2 : 4);
+  const int64_t align = reinterpret_cast<int64_t>(p);
+  if (n == 4 && out_dt == DT_BF16 && (align & 7) == 0) {
+    *reinterpret_cast<uint2*>(p) = make_uint2(bf16_pair(v[0], v[1]), bf16_pair(v[2], v[3]));
+  } else if (n == 4 && out_dt == DT_F32 && (align & 15) == 0) {
+    *reinterpret_cast<f32x4_t*>(p) = v;
+  } else {
+#pragma unroll
+    for (int r = 0; r < 4; ++r)
+      if (r < n) store_out(out_dt, C, i + r, v[r]);
+  }
+}
+
 // Expert e's rows, kept inside the M rows that exist whatever the offsets say.
 __device__ __forceinline__ void expert_range(const int32_t* offsets, int e, int64_t M, int64_t& row0, int64_t& rows) {
   row0 = min(max((int64_t)offsets[e], (int64_t)0), M);
@@ -73,129 +88,273 @@ __device__ __forceinline__ void expert_range(const int32_t* offsets, int e, int6
 }
 
 // -------------------------------------------------------------- few rows
-// One wavefront: 16 rows x 16 columns, operands straight from memory.  KS
-// wavefronts of the workgroup share a column tile and take every KS-th block
-// of K; their sums meet in LDS in a fixed order.
-constexpr int kSkinnyWaves = 4;
+// Bound by the bytes of the weights, which are read once: a wavefront takes
+// 16 columns (rows of B) and up to 16 MT rows of A, both straight from
+// memory.  The weights are the matrix instruction's first operand, so a lane
+// holds 4 neighbouring columns of one row.  kSpan blocks' loads are in flight
+// together before the first is used: 4 KiB per wavefront and block.
+constexpr int kSpan = 4;
 
-template <int KS, bool kWide>
-__global__ __launch_bounds__(64 * kSkinnyWaves) void skinny_kernel(QuantGemm g) {
-  __shared__ f32x4_t part[kSkinnyWaves][64];
-  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-  const int ks = wave % KS;
-  const int64_t n0 = ((int64_t)blockIdx.x * (kSkinnyWaves / KS) + wave / KS) * 16;
-  const int64_t n = min(n0 + (lane & 15), g.N - 1);
-  int64_t row0 = 0, rows = g.M, first = (int64_t)blockIdx.y * 16, step = (int64_t)gridDim.y * 16;
-  const char* B = g.B;
-  const float* sb = g.b_scale;
-  if (g.offsets) {
-    const int e = blockIdx.y;
-    expert_range(g.offsets, e, g.M, row0, rows);
-    first = 0;
-    step = 16;
-    B += (int64_t)e * g.b_stride;
-    sb += (int64_t)e * g.b_scale_stride;
-  }
-  const char* brow = B + n * g.ldb;
-  const float* sbp = g.b_rows == 1 ? sb + n : sb + (n >> 7) * g.b_scale_ld;
-  const int64_t sb_step = g.b_rows == 1 ? g.b_scale_ld : 1;
-  const int nb = g.K / kQB;
-  for (int64_t m0 = first; m0 < rows; m0 += step) {
-    const char* arow = g.A + (row0 + min(m0 + (lane & 15), rows - 1)) * g.lda;
-    const int64_t mr = m0 + (lane >> 4) * 4;
-    const float* sap[4];
+// Scale of B for this lane's 4 columns: one value, or one each.
+template <bool kRowScale>
+struct BScales {
+  const float* p[kRowScale ? 4 : 1];
+  int64_t step;
+};
+
+// acc[i] += scaled products of blocks [b0, b1): rows i of A at arow[i], their
+// scales at sa[i], a_step floats a block.
+template <int MT, bool kRowScale, bool kWide>
+__device__ __forceinline__ void span_blocks(const char* brow, const BScales<kRowScale>& sb, const char* const* arow,
+                                            const float* const* sa, int64_t a_step, int b0, int b1, int lane,
+                                            f32x4_t* acc) {
+  constexpr int NS = kRowScale ? 4 : 1;
+  for (int b = b0; b < b1; b += kSpan) {
+    Frag8 fb[kSpan], fa[kSpan][MT];
+    float tb[kSpan][NS], ta[kSpan][MT];
 #pragma unroll
-    for (int r = 0; r < 4; ++r) sap[r] = g.a_scale + row0 + min(mr + r, rows - 1);
-    f32x4_t acc = {0.f, 0.f, 0.f, 0.f};
-    for (int b = ks; b < nb; b += KS) {
-      const Frag8 fa = load_frag(arow + (int64_t)b * kQB, lane), fb = load_frag(brow + (int64_t)b * kQB, lane);
-      const float s = sbp[b * sb_step];
-      f32x4_t p;
-      if constexpr (kWide)
-        p = mfma_block(widen(fa), widen(fb));
-      else
-        p = mfma_block(fa, fb);
+    for (int u = 0; u < kSpan; ++u) {
+      const int64_t k = min(b + u, b1 - 1);  // past the end: the last block again, not used
+      fb[u] = load_frag(brow + k * kQB, lane);
 #pragma unroll
-      for (int r = 0; r < 4; ++r) acc[r] = fmaf(p[r], s * sap[r][b * g.a_scale_ld], acc[r]);
+      for (int i = 0; i < MT; ++i) fa[u][i] = load_frag(arow[i] + k * kQB, lane);
+#pragma unroll
+      for (int r = 0; r < NS; ++r) tb[u][r] = sb.p[r][k * sb.step];
+#pragma unroll
+      for (int i = 0; i < MT; ++i) ta[u][i] = sa[i][k * a_step];
     }
-    if constexpr (KS > 1) {
-      __syncthreads();
-      part[wave][lane] = acc;
-      __syncthreads();
-      if (ks == 0) {
+    __builtin_amdgcn_sched_barrier(0);  // no load moves down to its use
 #pragma unroll
-        for (int j = 1; j < KS; ++j)
+    for (int u = 0; u < kSpan; ++u) {
+      if (b + u >= b1) break;
 #pragma unroll
-          for (int r = 0; r < 4; ++r) acc[r] += part[wave + j][lane][r];
+      for (int i = 0; i < MT; ++i) {
+        f32x4_t p;
+        if constexpr (kWide)
+          p = mfma_block(widen(fb[u]), widen(fa[u][i]));
+        else
+          p = mfma_block(fb[u], fa[u][i]);
+#pragma unroll
+        for (int r = 0; r < 4; ++r) acc[i][r] = fmaf(p[r], ta[u][i] * tb[u][kRowScale ? r : 0], acc[i][r]);
       }
-    }
-    if (ks == 0 && n0 + (lane & 15) < g.N) {
-#pragma unroll
-      for (int r = 0; r < 4; ++r)
-        if (mr + r < rows) store_out(g.out_dt, g.C, (row0 + mr + r) * g.ldc + n, acc[r]);
     }
   }
 }
 
-// One workgroup: an expert's 128 features (16 per wavefront, gate and up),
-// 16 rows at a time, so the hidden rows' scale of those features is the
-// maximum over the workgroup.
-__global__ __launch_bounds__(512) void skinny_gate_up_kernel(QuantGateUp g) {
-  __shared__ float part[8][16];
+// A workgroup of kSkinnyWaves wavefronts: kSkinnyWaves / KS column tiles, KS
+// wavefronts on contiguous shares of K each, whose sums meet in LDS in a
+// fixed order.
+constexpr int kSkinnyWaves = 4;
+
+template <int MT, int KS, bool kRowScale, bool kWide>
+__global__ __launch_bounds__(64 * kSkinnyWaves) void skinny_kernel(QuantGemm g) {
+  __shared__ f32x4_t part[kSkinnyWaves][MT][64];
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+  const int ks = wave % KS;
+  const int64_t n0 = ((int64_t)blockIdx.x * (kSkinnyWaves / KS) + wave / KS) * 16;
+  const int64_t n = min(n0 + (lane & 15), g.N - 1);
+  int64_t row0 = 0, rows = g.M;
+  const char* B = g.B;
+  const float* bs = g.b_scale;
+  if (g.offsets) {
+    const int e = blockIdx.y;
+    expert_range(g.offsets, e, g.M, row0, rows);
+    B += (int64_t)e * g.b_stride;
+    bs += (int64_t)e * g.b_scale_stride;
+  }
+  const char* brow = B + n * g.ldb;
+  const int64_t c0 = n0 + (lane >> 4) * 4;  // this lane's columns
+  BScales<kRowScale> sb;
+  if constexpr (kRowScale) {
+#pragma unroll
+    for (int r = 0; r < 4; ++r) sb.p[r] = bs + min(c0 + r, g.N - 1);
+    sb.step = g.b_scale_ld;
+  } else {
+    sb.p[0] = bs + (min(n0, g.N - 1) >> 7) * g.b_scale_ld;
+    sb.step = 1;
+  }
+  const int nb = g.K / kQB, per = (nb + KS - 1) / KS;
+  const int b0 = min(ks * per, nb), b1 = min(b0 + per, nb);
+  for (int64_t m0 = 0; m0 < rows; m0 += 16 * MT) {
+    const char* arow[MT];
+    const float* sa[MT];
+    f32x4_t acc[MT];
+#pragma unroll
+    for (int i = 0; i < MT; ++i) {
+      const int64_t m = row0 + min(m0 + i * 16 + (lane & 15), rows - 1);
+      arow[i] = g.A + m * g.lda;
+      sa[i] = g.a_scale + m;
+      acc[i] = f32x4_t{0.f, 0.f, 0.f, 0.f};
+    }
+    span_blocks<MT, kRowScale, kWide>(brow, sb, arow, sa, g.a_scale_ld, b0, b1, lane, acc);
+    if constexpr (KS > 1) {
+      __syncthreads();
+#pragma unroll
+      for (int i = 0; i < MT; ++i) part[wave][i][lane] = acc[i];
+      __syncthreads();
+      if (ks != 0) continue;
+#pragma unroll
+      for (int i = 0; i < MT; ++i)
+#pragma unroll
+        for (int j = 1; j < KS; ++j) acc[i] += part[wave + j][i][lane];
+    }
+#pragma unroll
+    for (int i = 0; i < MT; ++i) {
+      const int64_t m = m0 + i * 16 + (lane & 15);
+      if (m >= rows || c0 >= g.N) continue;
+      store_run(g.out_dt, g.C, (row0 + m) * g.ldc + c0, acc[i], (int)min(g.N - c0, (int64_t)4));
+    }
+  }
+}
+
+// Experts with few rows, from the bf16 rows to the quantised hidden rows in
+// one launch.  One workgroup: an expert's 128 features (a block of the hidden
+// rows, whose scale is the maximum over them), 16 rows at a time.  Wavefront
+// w takes features 16 (w % 8) .. + 15, gate and up, over half w / 8 of K.  The
+// rows are quantised into LDS by the workgroup itself: the 16 K .. 32 K values
+// are read by each of the F / 128 workgroups of the expert, little beside its
+// 256 K bytes of weights, and a launch and its round trip through memory
+// less; the first span of weights is on its way meanwhile.
+constexpr int kHiddenHalves = 1;  // wavefronts that share a feature's K
+constexpr int kHiddenWaves = 8 * kHiddenHalves;
+constexpr int kHiddenSpan = 4;
+constexpr int kHiddenPad = 16;  // bytes between LDS rows, so that 16 rows' chunks spread over the banks
+
+// kQuantized: A holds e4m3 rows and scales already (K too long for the LDS).
+struct HiddenArgs {
+  QuantGateUp g;
+  const uint16_t* x;  // bf16 rows, or null: g.A
+  int64_t ldx;
+};
+
+template <bool kQuantized>
+__global__ __launch_bounds__(64 * kHiddenWaves) void skinny_gate_up_kernel(HiddenArgs a) {
+  extern __shared__ __attribute__((aligned(16))) char dyn[];
+  __shared__ float part_max[8][16];
+  __shared__ f32x4_t part[kHiddenHalves == 2 ? 8 : 1][2][64];
+  const QuantGateUp& g = a.g;
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+  const int fw = wave & 7, half = wave >> 3;
   const int e = blockIdx.y;
   int64_t row0 = 0, rows = g.M;
-  if (g.offsets) {
-    expert_range(g.offsets, e, g.M, row0, rows);
-  }
-  const int nb = g.K / kQB;
+  if (g.offsets) expert_range(g.offsets, e, g.M, row0, rows);
+  if (rows <= 0) return;
+  const int nb = g.K / kQB, per = (nb + kHiddenHalves - 1) / kHiddenHalves;
+  const int b0 = half * per, b1 = min(b0 + per, nb);
   const int fb = blockIdx.x;
-  const int f = fb * kQB + wave * 16 + (lane & 15);
+  const int f = fb * kQB + fw * 16 + (lane & 15);
   const char* wg = g.Wg + ((int64_t)e * g.F + f) * g.K;
   const char* wu = g.Wu + ((int64_t)e * g.F + f) * g.K;
   const float* sg = g.sg + ((int64_t)e * (g.F / kQB) + fb) * nb;
   const float* su = g.su + ((int64_t)e * (g.F / kQB) + fb) * nb;
   const int64_t col = (g.offsets ? 0 : (int64_t)e * g.F) + fb * kQB;
+  const int ldq = g.K + kHiddenPad;
+  float* xs = reinterpret_cast<float*>(dyn + 16 * ldq);  // [block][16]
+  constexpr int U = kHiddenSpan;
   for (int64_t m0 = 0; m0 < rows; m0 += 16) {
-    const char* arow = g.A + (row0 + min(m0 + (lane & 15), rows - 1)) * g.lda;
-    const int64_t mr = m0 + (lane >> 4) * 4;
-    const float* sap[4];
+    const int left = (int)min(rows - m0, (int64_t)16);
+    if (m0 > 0) __syncthreads();  // the rows and maxima before are read
+    Frag8 w0[U], w1[U];
+    float t0[U], t1[U];
+    auto load_w = [&](int b) {
 #pragma unroll
-    for (int r = 0; r < 4; ++r) sap[r] = g.a_scale + row0 + min(mr + r, rows - 1);
+      for (int u = 0; u < U; ++u) {
+        const int k = max(min(b + u, b1 - 1), 0);
+        w0[u] = load_frag(wg + (int64_t)k * kQB, lane);
+        w1[u] = load_frag(wu + (int64_t)k * kQB, lane);
+        t0[u] = sg[k];
+        t1[u] = su[k];
+      }
+    };
+    load_w(b0);
+    if constexpr (!kQuantized) {
+      // 8 lanes a block of a row, 16 values a lane
+      const int c = threadIdx.x & 7;
+      for (int i = threadIdx.x >> 3; i < left * nb; i += 64 * kHiddenWaves / 8) {
+        const int r = i / nb, b = i - r * nb;
+        const char* src = reinterpret_cast<const char*>(a.x + (row0 + m0 + r) * a.ldx + b * kQB + c * 16);
+        const uint4 v0 = ld16(src), v1 = ld16(src + 16);
+        float x[16];
+        unpack(v0, x, bf16_t{});
+        unpack(v1, x + 8, bf16_t{});
+        float m = kQuantTiny;
+#pragma unroll
+        for (int j = 0; j < 16; ++j) m = fmaxf(m, fabsf(x[j]));
+        for (int d = 1; d < 8; d <<= 1) m = fmaxf(m, __shfl_xor(m, d));
+        const BlockQuant bq(m);
+        uint32_t q[4];
+#pragma unroll
+        for (int j = 0; j < 4; ++j) q[j] = e4m3_quad(bq(x[4 * j]), bq(x[4 * j + 1]), bq(x[4 * j + 2]), bq(x[4 * j + 3]));
+        st16(dyn + r * ldq + b * kQB + c * 16, make_uint4(q[0], q[1], q[2], q[3]));
+        if (c == 0) xs[b * 16 + r] = block_scale(m);
+      }
+      __syncthreads();
+    }
+    const int ar = min(lane & 15, left - 1);
+    const char* arow = kQuantized ? g.A + (row0 + m0 + ar) * g.lda : dyn + ar * ldq;
+    const float* sa = kQuantized ? g.a_scale + row0 + m0 + ar : xs + ar;
+    const int64_t a_step = kQuantized ? g.a_scale_ld : 16;
     f32x4_t ga = {0.f, 0.f, 0.f, 0.f}, ua = {0.f, 0.f, 0.f, 0.f};
-    for (int b = 0; b < nb; ++b) {
-      const int64_t k = (int64_t)b * kQB;
-      const Frag8 fa = load_frag(arow + k, lane), f0 = load_frag(wg + k, lane), f1 = load_frag(wu + k, lane);
-      const f32x4_t p = mfma_block(fa, f0), q = mfma_block(fa, f1);
+    for (int b = b0; b < b1; b += U) {
+      Frag8 c0[U], c1[U];
+      float d0[U], d1[U];
+#pragma unroll
+      for (int u = 0; u < U; ++u) {
+        c0[u] = w0[u];
+        c1[u] = w1[u];
+        d0[u] = t0[u];
+        d1[u] = t1[u];
+      }
+      if (b + U < b1) load_w(b + U);
+      __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+      for (int u = 0; u < U; ++u) {
+        if (b + u >= b1) break;
+        const Frag8 fa = load_frag(arow + (int64_t)(b + u) * kQB, lane);
+        const float s = sa[(b + u) * a_step];
+        const f32x4_t p = mfma_block(c0[u], fa), q = mfma_block(c1[u], fa);
+        const float s0 = s * d0[u], s1 = s * d1[u];
+#pragma unroll
+        for (int r = 0; r < 4; ++r) {
+          ga[r] = fmaf(p[r], s0, ga[r]);
+          ua[r] = fmaf(q[r], s1, ua[r]);
+        }
+      }
+    }
+    // the halves of K meet; lane: row lane & 15, 4 neighbouring features
+    if constexpr (kHiddenHalves == 2) {
+      if (half) {
+        part[fw][0][lane] = ga;
+        part[fw][1][lane] = ua;
+      }
+      __syncthreads();
+    }
+    f32x4_t h;
+    if (!half) {
+      if constexpr (kHiddenHalves == 2) {
+        ga += part[fw][0][lane];
+        ua += part[fw][1][lane];
+      }
+      float mx = 0.0f;
 #pragma unroll
       for (int r = 0; r < 4; ++r) {
-        const float s = sap[r][b * g.a_scale_ld];
-        ga[r] = fmaf(p[r], s * sg[b], ga[r]);
-        ua[r] = fmaf(q[r], s * su[b], ua[r]);
+        h[r] = silu(ga[r]) * ua[r];
+        mx = fmaxf(mx, fabsf(h[r]));
       }
-    }
-    float h[4], mx[4];
-#pragma unroll
-    for (int r = 0; r < 4; ++r) {
-      h[r] = silu(ga[r]) * ua[r];
-      mx[r] = fabsf(h[r]);
-      for (int d = 1; d < 16; d <<= 1) mx[r] = fmaxf(mx[r], __shfl_xor(mx[r], d));
+      mx = fmaxf(mx, __shfl_xor(mx, 16));
+      mx = fmaxf(mx, __shfl_xor(mx, 32));
+      if (lane < 16) part_max[fw][lane] = mx;
     }
     __syncthreads();
-    if ((lane & 15) == 0)
-#pragma unroll
-      for (int r = 0; r < 4; ++r) part[wave][(lane >> 4) * 4 + r] = mx[r];
-    __syncthreads();
-#pragma unroll
-    for (int r = 0; r < 4; ++r) {
+    if (!half && (lane & 15) < left) {
       float amax = kQuantTiny;
 #pragma unroll
-      for (int w = 0; w < 8; ++w) amax = fmaxf(amax, part[w][(lane >> 4) * 4 + r]);
-      if (mr + r < rows) {
-        const BlockQuant bq(amax);
-        g.H[(row0 + mr + r) * g.ldh + col + wave * 16 + (lane & 15)] = (char)(e4m3_quad(bq(h[r]), 0.f, 0.f, 0.f) & 0xFF);
-        if (wave == 0 && (lane & 15) == 0) g.h_scale[(col / kQB) * g.h_scale_ld + row0 + mr + r] = block_scale(amax);
-      }
+      for (int w = 0; w < 8; ++w) amax = fmaxf(amax, part_max[w][lane & 15]);
+      const BlockQuant bq(amax);
+      const int64_t m = row0 + m0 + (lane & 15);
+      *reinterpret_cast<uint32_t*>(g.H + m * g.ldh + col + fw * 16 + (lane >> 4) * 4) =
+          e4m3_quad(bq(h[0]), bq(h[1]), bq(h[2]), bq(h[3]));
+      if (fw == 0 && lane < 16) g.h_scale[(col / kQB) * g.h_scale_ld + m] = block_scale(amax);
     }
   }
 }
@@ -715,16 +874,49 @@ void launch_tiles(const QuantGemm& g, int parts, float* partial, hipStream_t s) 
     product_kernel<TL, kBlockB, kWide><<<grid, TL::THREADS, 0, s>>>(g, (int)tm, (int)tn, partial);
 }
 
+template <int MT, int KS>
+void launch_skinny_as(const QuantGemm& g, const Form& f, hipStream_t s) {
+  const dim3 grid((unsigned)cdiv(g.N, 16 * (kSkinnyWaves / KS)), (unsigned)(g.offsets ? g.E : 1));
+  constexpr int T = 64 * kSkinnyWaves;
+  if (g.b_rows == 1) {
+    if (f.wide)
+      skinny_kernel<MT, KS, true, true><<<grid, T, 0, s>>>(g);
+    else
+      skinny_kernel<MT, KS, true, false><<<grid, T, 0, s>>>(g);
+  } else {
+    if (f.wide)
+      skinny_kernel<MT, KS, false, true><<<grid, T, 0, s>>>(g);
+    else
+      skinny_kernel<MT, KS, false, false><<<grid, T, 0, s>>>(g);
+  }
+}
+
+void launch_skinny(const QuantGemm& g, const Form& f, hipStream_t s) {
+  // one pass over the weights for up to 32 rows; an expert's rows vary about
+  // their mean, so a mean above 8 takes the two row blocks
+  const bool two = g.offsets ? cdiv(g.M, g.E) > 8 : g.M > 16;
+  // wavefronts per column tile: until the chip has 2048 wavefronts or a
+  // share of K is one span
+  const int64_t tiles = cdiv(g.N, 16) * (g.offsets ? (g.M < g.E ? g.M : g.E) : 1);
+  const bool split = tiles < 2048 && g.K / kQB > kSpan;
+  if (two) {
+    if (split)
+      launch_skinny_as<2, 4>(g, f, s);
+    else
+      launch_skinny_as<2, 1>(g, f, s);
+  } else {
+    if (split)
+      launch_skinny_as<1, 4>(g, f, s);
+    else
+      launch_skinny_as<1, 1>(g, f, s);
+  }
+}
+
 hipError_t launch_quant_gemm(const QuantGemm& g, void* ws, hipStream_t s) {
   if (g.M <= 0 || g.N <= 0) return hipSuccess;
   const Form f = product_form(g);
   if (f.skinny) {
-    const int64_t rows = g.offsets ? g.E : cdiv(g.M, 16);
-    const dim3 grid((unsigned)cdiv(g.N, 16 * kSkinnyWaves), (unsigned)rows);
-    if (f.wide)
-      skinny_kernel<1, true><<<grid, 64 * kSkinnyWaves, 0, s>>>(g);
-    else
-      skinny_kernel<1, false><<<grid, 64 * kSkinnyWaves, 0, s>>>(g);
+    launch_skinny(g, f, s);
     return hipGetLastError();
   }
   float* partial = f.parts > 1 ? static_cast<float*>(ws) : nullptr;
@@ -749,17 +941,32 @@ void launch_hidden(const QuantGateUp& g, hipStream_t s) {
   gate_up_kernel<TL><<<pad8(tiles), TL::THREADS, 0, s>>>(g, (int)tm);
 }
 
-hipError_t launch_quant_gate_up(const QuantGateUp& g, hipStream_t s) {
+// Mean rows per expert up to which an expert's rows go straight from memory.
+constexpr int64_t kFewHiddenRows = 24;
+// K whose 16 quantised rows and scales fit the LDS beside the static arrays.
+constexpr int kFusedHiddenK = 8192;
+
+bool quant_gate_up_takes_bf16(const QuantGateUp& g) {
+  return (g.offsets ? cdiv(g.M, g.E) : g.M) <= kFewHiddenRows && g.K <= kFusedHiddenK;
+}
+
+hipError_t launch_quant_gate_up(const QuantGateUp& g, const void* x, int64_t ldx, hipStream_t s) {
   if (g.M <= 0 || g.E <= 0) return hipSuccess;
   const int64_t rows = g.offsets ? cdiv(g.M, g.E) : g.M;
-  if (rows <= 24)
-    skinny_gate_up_kernel<<<dim3((unsigned)(g.F / kQB), (unsigned)g.E), 512, 0, s>>>(g);
-  else if (rows <= 64)
+  const dim3 few((unsigned)(g.F / kQB), (unsigned)g.E);
+  if (x) {
+    const HiddenArgs a{g, static_cast<const uint16_t*>(x), ldx};
+    const size_t lds = 16 * (size_t)(g.K + kHiddenPad) + 16 * 4 * (size_t)(g.K / kQB);
+    skinny_gate_up_kernel<false><<<few, 64 * kHiddenWaves, lds, s>>>(a);
+  } else if (rows <= kFewHiddenRows) {
+    skinny_gate_up_kernel<true><<<few, 64 * kHiddenWaves, 0, s>>>(HiddenArgs{g, nullptr, 0});
+  } else if (rows <= 64) {
     launch_hidden<E64>(g, s);
-  else if (rows <= 160)
+  } else if (rows <= 160) {
     launch_hidden<E128>(g, s);
-  else
+  } else {
     launch_hidden<T256>(g, s);
+  }
   return hipGetLastError();
 }
 

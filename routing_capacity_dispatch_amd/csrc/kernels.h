@@ -341,6 +341,9 @@ struct QuantGateUp {
   float* h_scale;         // [feature blocks][h_scale_ld]
   int64_t h_scale_ld;
 };
-hipError_t launch_quant_gate_up(const QuantGateUp& g, hipStream_t s);
+// x: bf16 rows to quantise on the way (g.A and g.a_scale unused), where
+// quant_gate_up_takes_bf16 (a function of the sizes) says so; else null.
+bool quant_gate_up_takes_bf16(const QuantGateUp& g);
+hipError_t launch_quant_gate_up(const QuantGateUp& g, const void* x, int64_t ldx, hipStream_t s);
 
 }  // namespace moe

@@ -1574,17 +1574,6 @@ moe_status run_experts_quant(const moe_config* c, const moe_plan& p, const void*
   const int64_t n = p.dropless_rows, L = c->d_latent, F = c->d_ff;
   QuantExpertsWs q;
   carve_experts_quant(c, n, ws, &q);
-  moe::QuantizeArgs z{};
-  z.x = xs;
-  z.rows = n;
-  z.cols = z.ld = z.ldq = L;
-  z.dt = moe::DT_BF16;
-  z.block_rows = 1;
-  z.q = q.xq;
-  z.scale = q.xs;
-  z.scale_ld = n;
-  hipError_t e = moe::launch_quantize(z, s);
-  if (e != hipSuccess) return MOE_ERR_HIP;
   moe::QuantGateUp u{};
   u.A = q.xq;
   u.lda = L;
@@ -1603,7 +1592,22 @@ moe_status run_experts_quant(const moe_config* c, const moe_plan& p, const void*
   u.ldh = F;
   u.h_scale = q.hs;
   u.h_scale_ld = n;
-  e = moe::launch_quant_gate_up(u, s);
+  const bool fused = moe::quant_gate_up_takes_bf16(u);
+  hipError_t e = hipSuccess;
+  if (!fused) {
+    moe::QuantizeArgs z{};
+    z.x = xs;
+    z.rows = n;
+    z.cols = z.ld = z.ldq = L;
+    z.dt = moe::DT_BF16;
+    z.block_rows = 1;
+    z.q = q.xq;
+    z.scale = q.xs;
+    z.scale_ld = n;
+    e = moe::launch_quantize(z, s);
+    if (e != hipSuccess) return MOE_ERR_HIP;
+  }
+  e = moe::launch_quant_gate_up(u, fused ? xs : nullptr, L, s);
   if (e != hipSuccess) return MOE_ERR_HIP;
   moe::QuantGemm d{};
   d.A = q.hq;
