@@ -207,154 +207,165 @@ __global__ __launch_bounds__(64 * kSkinnyWaves) void skinny_kernel(QuantGemm g) 
   }
 }
 
-// Experts with few rows, from the bf16 rows to the quantised hidden rows in
-// one launch.  One workgroup: an expert's 128 features (a block of the hidden
-// rows, whose scale is the maximum over them), 16 rows at a time.  Wavefront
-// w takes features 16 (w % 8) .. + 15, gate and up, over half w / 8 of K.  The
-// rows are quantised into LDS by the workgroup itself: the 16 K .. 32 K values
-// are read by each of the F / 128 workgroups of the expert, little beside its
-// 256 K bytes of weights, and a launch and its round trip through memory
-// less; the first span of weights is on its way meanwhile.
-constexpr int kHiddenHalves = 1;  // wavefronts that share a feature's K
-constexpr int kHiddenWaves = 8 * kHiddenHalves;
-constexpr int kHiddenSpan = 4;
-constexpr int kHiddenPad = 16;  // bytes between LDS rows, so that 16 rows' chunks spread over the banks
+// Experts with few rows.  Two launches: the hidden rows h = silu(x Wg^T) *
+// (x Wu^T) in fp32, then their product with the down weights.  Each launch
+// quantises the rows it reads (bf16 x, fp32 h) into LDS itself, every
+// workgroup all K of its expert's rows, 16 at a time: a launch and a round
+// trip through memory less for rows that are few beside the weights, and the
+// hidden rows' blocks of 128 features bind no workgroup, so workgroups are
+// small and spread over all CUs whatever the number of busy experts.
+// kSource: 0 rows in e4m3 with scales (K too long for the LDS), 1 bf16, 2 fp32.
+enum Source { kE4m3 = 0, kBf16 = 1, kF32 = 2 };
+constexpr int kRowPad = 16;  // bytes between LDS rows, so that 16 rows' chunks spread over the banks
 
-// kQuantized: A holds e4m3 rows and scales already (K too long for the LDS).
-struct HiddenArgs {
-  QuantGateUp g;
-  const uint16_t* x;  // bf16 rows, or null: g.A
-  int64_t ldx;
-};
+// 16 values from element i of a row.
+template <int kSource>
+__device__ __forceinline__ void load16(const void* row, int i, float* v) {
+  const char* p = static_cast<const char*>(row) + (int64_t)i * (kSource == kBf16 ? 2 : 4);
+  if constexpr (kSource == kBf16) {
+    unpack(ld16(p), v, bf16_t{});
+    unpack(ld16(p + 16), v + 8, bf16_t{});
+  } else {
+#pragma unroll
+    for (int j = 0; j < 4; ++j) unpack(ld16(p + 16 * j), v + 4 * j, 0.0f);
+  }
+}
 
-template <bool kQuantized>
-__global__ __launch_bounds__(64 * kHiddenWaves) void skinny_gate_up_kernel(HiddenArgs a) {
-  extern __shared__ __attribute__((aligned(16))) char dyn[];
-  __shared__ float part_max[8][16];
-  __shared__ f32x4_t part[kHiddenHalves == 2 ? 8 : 1][2][64];
-  const QuantGateUp& g = a.g;
+// `left` rows of nb blocks into LDS: bytes at q[row][K + kRowPad], scales at
+// sc[block][16].  8 lanes a block of a row.
+template <int kSource>
+__device__ __forceinline__ void stage_rows(const char* x, int64_t row_bytes, int left, int nb, char* q, float* sc) {
+  const int c = threadIdx.x & 7, ldq = nb * kQB + kRowPad;
+  for (int i = threadIdx.x >> 3; i < left * nb; i += 64 * kSkinnyWaves / 8) {
+    const int r = i / nb, b = i - r * nb;
+    float v[16];
+    load16<kSource>(x + r * row_bytes, b * kQB + c * 16, v);
+    float m = kQuantTiny;
+#pragma unroll
+    for (int j = 0; j < 16; ++j) m = fmaxf(m, fabsf(v[j]));
+    for (int d = 1; d < 8; d <<= 1) m = fmaxf(m, __shfl_xor(m, d));
+    const BlockQuant bq(m);
+    uint32_t w[4];
+#pragma unroll
+    for (int j = 0; j < 4; ++j) w[j] = e4m3_quad(bq(v[4 * j]), bq(v[4 * j + 1]), bq(v[4 * j + 2]), bq(v[4 * j + 3]));
+    st16(q + r * ldq + b * kQB + c * 16, make_uint4(w[0], w[1], w[2], w[3]));
+    if (c == 0) sc[b * 16 + r] = block_scale(m);
+  }
+}
+
+template <int KS, int kSource, bool kHidden>
+__global__ __launch_bounds__(64 * kSkinnyWaves) void few_rows_kernel(FewRows g) {
+  extern __shared__ __attribute__((aligned(16))) char dyn[];  // staged rows, then their scales
+  constexpr int W = kHidden ? 2 : 1;
+  constexpr int U = 4 / W;  // blocks whose loads are in flight together
+  __shared__ f32x4_t part[KS > 1 ? kSkinnyWaves : 1][W][64];
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-  const int fw = wave & 7, half = wave >> 3;
-  const int e = blockIdx.y;
+  const int ks = wave % KS, e = blockIdx.y;
   int64_t row0 = 0, rows = g.M;
   if (g.offsets) expert_range(g.offsets, e, g.M, row0, rows);
   if (rows <= 0) return;
-  const int nb = g.K / kQB, per = (nb + kHiddenHalves - 1) / kHiddenHalves;
-  const int b0 = half * per, b1 = min(b0 + per, nb);
-  const int fb = blockIdx.x;
-  const int f = fb * kQB + fw * 16 + (lane & 15);
-  const char* wg = g.Wg + ((int64_t)e * g.F + f) * g.K;
-  const char* wu = g.Wu + ((int64_t)e * g.F + f) * g.K;
-  const float* sg = g.sg + ((int64_t)e * (g.F / kQB) + fb) * nb;
-  const float* su = g.su + ((int64_t)e * (g.F / kQB) + fb) * nb;
-  const int64_t col = (g.offsets ? 0 : (int64_t)e * g.F) + fb * kQB;
-  const int ldq = g.K + kHiddenPad;
-  float* xs = reinterpret_cast<float*>(dyn + 16 * ldq);  // [block][16]
-  constexpr int U = kHiddenSpan;
+  const int nb = g.K / kQB, per = (nb + KS - 1) / KS;
+  const int b0 = min(ks * per, nb), b1 = min(b0 + per, nb);
+  const int n0 = (blockIdx.x * (kSkinnyWaves / KS) + wave / KS) * 16;  // N is a multiple of 128
+  const int64_t wrow = ((int64_t)e * g.N + n0 + (lane & 15)) * g.K;
+  const char* wp[W];
+  const float* sp[W];
+  const int64_t srow = ((int64_t)e * (g.N / kQB) + (n0 >> 7)) * nb;
+  wp[0] = g.W0 + wrow;
+  sp[0] = g.s0 + srow;
+  if constexpr (kHidden) {
+    wp[1] = g.W1 + wrow;
+    sp[1] = g.s1 + srow;
+  }
+  const int ldq = g.K + kRowPad;
+  float* staged_sc = reinterpret_cast<float*>(dyn + 16 * ldq);
   for (int64_t m0 = 0; m0 < rows; m0 += 16) {
     const int left = (int)min(rows - m0, (int64_t)16);
-    if (m0 > 0) __syncthreads();  // the rows and maxima before are read
-    Frag8 w0[U], w1[U];
-    float t0[U], t1[U];
-    auto load_w = [&](int b) {
+    const int64_t first = row0 + m0;
+    Frag8 w[2][U][W];
+    float t[2][U][W];
+    auto load_w = [&](int s, int b) {
 #pragma unroll
       for (int u = 0; u < U; ++u) {
-        const int k = max(min(b + u, b1 - 1), 0);
-        w0[u] = load_frag(wg + (int64_t)k * kQB, lane);
-        w1[u] = load_frag(wu + (int64_t)k * kQB, lane);
-        t0[u] = sg[k];
-        t1[u] = su[k];
+        const int k = max(min(b + u, b1 - 1), 0);  // past the end: the last block again, not used
+#pragma unroll
+        for (int i = 0; i < W; ++i) {
+          w[s][u][i] = load_frag(wp[i] + (int64_t)k * kQB, lane);
+          t[s][u][i] = sp[i][k];
+        }
       }
     };
-    load_w(b0);
-    if constexpr (!kQuantized) {
-      // 8 lanes a block of a row, 16 values a lane
-      const int c = threadIdx.x & 7;
-      for (int i = threadIdx.x >> 3; i < left * nb; i += 64 * kHiddenWaves / 8) {
-        const int r = i / nb, b = i - r * nb;
-        const char* src = reinterpret_cast<const char*>(a.x + (row0 + m0 + r) * a.ldx + b * kQB + c * 16);
-        const uint4 v0 = ld16(src), v1 = ld16(src + 16);
-        float x[16];
-        unpack(v0, x, bf16_t{});
-        unpack(v1, x + 8, bf16_t{});
-        float m = kQuantTiny;
-#pragma unroll
-        for (int j = 0; j < 16; ++j) m = fmaxf(m, fabsf(x[j]));
-        for (int d = 1; d < 8; d <<= 1) m = fmaxf(m, __shfl_xor(m, d));
-        const BlockQuant bq(m);
-        uint32_t q[4];
-#pragma unroll
-        for (int j = 0; j < 4; ++j) q[j] = e4m3_quad(bq(x[4 * j]), bq(x[4 * j + 1]), bq(x[4 * j + 2]), bq(x[4 * j + 3]));
-        st16(dyn + r * ldq + b * kQB + c * 16, make_uint4(q[0], q[1], q[2], q[3]));
-        if (c == 0) xs[b * 16 + r] = block_scale(m);
-      }
-      __syncthreads();
-    }
+    load_w(0, b0);
     const int ar = min(lane & 15, left - 1);
-    const char* arow = kQuantized ? g.A + (row0 + m0 + ar) * g.lda : dyn + ar * ldq;
-    const float* sa = kQuantized ? g.a_scale + row0 + m0 + ar : xs + ar;
-    const int64_t a_step = kQuantized ? g.a_scale_ld : 16;
-    f32x4_t ga = {0.f, 0.f, 0.f, 0.f}, ua = {0.f, 0.f, 0.f, 0.f};
-    for (int b = b0; b < b1; b += U) {
-      Frag8 c0[U], c1[U];
-      float d0[U], d1[U];
+    const char* arow;
+    const float* sa;
+    int64_t a_step;
+    if constexpr (kSource == kE4m3) {
+      arow = static_cast<const char*>(g.x) + (first + ar) * g.ldx;
+      sa = g.x_scale + first + ar;
+      a_step = g.x_scale_ld;
+    } else {
+      constexpr int kBytes = kSource == kBf16 ? 2 : 4;
+      if (m0 > 0) __syncthreads();  // the rows before are read
+      stage_rows<kSource>(static_cast<const char*>(g.x) + first * g.ldx * kBytes, g.ldx * kBytes, left, nb, dyn,
+                          staged_sc);
+      __syncthreads();
+      arow = dyn + ar * ldq;
+      sa = staged_sc + ar;
+      a_step = 16;
+    }
+    f32x4_t acc[W];
 #pragma unroll
-      for (int u = 0; u < U; ++u) {
-        c0[u] = w0[u];
-        c1[u] = w1[u];
-        d0[u] = t0[u];
-        d1[u] = t1[u];
-      }
-      if (b + U < b1) load_w(b + U);
-      __builtin_amdgcn_sched_barrier(0);
+    for (int i = 0; i < W; ++i) acc[i] = f32x4_t{0.f, 0.f, 0.f, 0.f};
+    auto use_w = [&](int s, int b) {
 #pragma unroll
       for (int u = 0; u < U; ++u) {
         if (b + u >= b1) break;
         const Frag8 fa = load_frag(arow + (int64_t)(b + u) * kQB, lane);
-        const float s = sa[(b + u) * a_step];
-        const f32x4_t p = mfma_block(c0[u], fa), q = mfma_block(c1[u], fa);
-        const float s0 = s * d0[u], s1 = s * d1[u];
+        const float x = sa[(b + u) * a_step];
 #pragma unroll
-        for (int r = 0; r < 4; ++r) {
-          ga[r] = fmaf(p[r], s0, ga[r]);
-          ua[r] = fmaf(q[r], s1, ua[r]);
+        for (int i = 0; i < W; ++i) {
+          const f32x4_t p = mfma_block(w[s][u][i], fa);
+          const float y = x * t[s][u][i];
+#pragma unroll
+          for (int r = 0; r < 4; ++r) acc[i][r] = fmaf(p[r], y, acc[i][r]);
         }
       }
+    };
+    // two spans alternate: one on its way while the other is used
+    for (int b = b0; b < b1; b += 2 * U) {
+      load_w(1, b + U);
+      __builtin_amdgcn_sched_barrier(0);
+      use_w(0, b);
+      load_w(0, b + 2 * U);
+      __builtin_amdgcn_sched_barrier(0);
+      use_w(1, b + U);
     }
-    // the halves of K meet; lane: row lane & 15, 4 neighbouring features
-    if constexpr (kHiddenHalves == 2) {
-      if (half) {
-        part[fw][0][lane] = ga;
-        part[fw][1][lane] = ua;
-      }
+    if constexpr (KS > 1) {
+#pragma unroll
+      for (int i = 0; i < W; ++i) part[wave][i][lane] = acc[i];
       __syncthreads();
-    }
-    f32x4_t h;
-    if (!half) {
-      if constexpr (kHiddenHalves == 2) {
-        ga += part[fw][0][lane];
-        ua += part[fw][1][lane];
-      }
-      float mx = 0.0f;
+      if (ks == 0) {
 #pragma unroll
-      for (int r = 0; r < 4; ++r) {
-        h[r] = silu(ga[r]) * ua[r];
-        mx = fmaxf(mx, fabsf(h[r]));
-      }
-      mx = fmaxf(mx, __shfl_xor(mx, 16));
-      mx = fmaxf(mx, __shfl_xor(mx, 32));
-      if (lane < 16) part_max[fw][lane] = mx;
-    }
-    __syncthreads();
-    if (!half && (lane & 15) < left) {
-      float amax = kQuantTiny;
+        for (int i = 0; i < W; ++i)
 #pragma unroll
-      for (int w = 0; w < 8; ++w) amax = fmaxf(amax, part_max[w][lane & 15]);
-      const BlockQuant bq(amax);
-      const int64_t m = row0 + m0 + (lane & 15);
-      *reinterpret_cast<uint32_t*>(g.H + m * g.ldh + col + fw * 16 + (lane >> 4) * 4) =
-          e4m3_quad(bq(h[0]), bq(h[1]), bq(h[2]), bq(h[3]));
-      if (fw == 0 && lane < 16) g.h_scale[(col / kQB) * g.h_scale_ld + m] = block_scale(amax);
+          for (int j = 1; j < KS; ++j) acc[i] += part[wave + j][i][lane];
+      }
+      if (m0 + 16 < rows) __syncthreads();
+    }
+    // lane: row lane & 15, 4 neighbouring columns
+    if (ks == 0 && (lane & 15) < left) {
+      const int64_t m = first + (lane & 15);
+      const int c = n0 + (lane >> 4) * 4;
+      if constexpr (kHidden) {
+        f32x4_t h;
+#pragma unroll
+        for (int r = 0; r < 4; ++r) h[r] = silu(acc[0][r]) * acc[1][r];
+        *reinterpret_cast<f32x4_t*>(static_cast<float*>(g.out) + m * g.ldo + (g.offsets ? 0 : (int64_t)e * g.N) + c) = h;
+      } else {
+        *reinterpret_cast<uint2*>(static_cast<uint16_t*>(g.out) + m * g.ldo + c) =
+            make_uint2(bf16_pair(acc[0][0], acc[0][1]), bf16_pair(acc[0][2], acc[0][3]));
+      }
     }
   }
 }
@@ -941,32 +952,57 @@ void launch_hidden(const QuantGateUp& g, hipStream_t s) {
   gate_up_kernel<TL><<<pad8(tiles), TL::THREADS, 0, s>>>(g, (int)tm);
 }
 
-// Mean rows per expert up to which an expert's rows go straight from memory.
-constexpr int64_t kFewHiddenRows = 24;
-// K whose 16 quantised rows and scales fit the LDS beside the static arrays.
-constexpr int kFusedHiddenK = 8192;
+// Mean rows per expert up to which the experts' rows go straight from memory.
+constexpr int64_t kFewRows = 24;
+// K whose 16 staged rows leave the LDS of a CU to two workgroups.
+constexpr int kStagedK = 4096;
 
-bool quant_gate_up_takes_bf16(const QuantGateUp& g) {
-  return (g.offsets ? cdiv(g.M, g.E) : g.M) <= kFewHiddenRows && g.K <= kFusedHiddenK;
+bool few_rows(int64_t M, int E, bool grouped) { return (grouped ? cdiv(M, E) : M) <= kFewRows; }
+bool few_rows_stage(int K) { return K <= kStagedK; }
+
+template <int KS>
+void launch_few_as(const FewRows& g, bool hidden, bool staged, hipStream_t s) {
+  const dim3 grid((unsigned)(g.N / (16 * (kSkinnyWaves / KS))), (unsigned)g.E);
+  constexpr int T = 64 * kSkinnyWaves;
+  const size_t lds = staged ? 16 * (size_t)(g.K + kRowPad) + 16 * 4 * (size_t)(g.K / kQB) : 0;
+  if (hidden) {
+    if (staged)
+      few_rows_kernel<KS, kBf16, true><<<grid, T, lds, s>>>(g);
+    else
+      few_rows_kernel<KS, kE4m3, true><<<grid, T, 0, s>>>(g);
+  } else {
+    if (staged)
+      few_rows_kernel<KS, kF32, false><<<grid, T, lds, s>>>(g);
+    else
+      few_rows_kernel<KS, kE4m3, false><<<grid, T, 0, s>>>(g);
+  }
 }
 
-hipError_t launch_quant_gate_up(const QuantGateUp& g, const void* x, int64_t ldx, hipStream_t s) {
+hipError_t launch_few_rows(const FewRows& g, bool hidden, bool staged, hipStream_t s) {
+  if (g.M <= 0 || g.E <= 0) return hipSuccess;
+  // wavefronts on one column tile: more while the busy experts (at most one
+  // per row) give the chip fewer than 3 workgroups per CU
+  const int64_t busy = g.offsets && g.M < g.E ? g.M : g.E;
+  const int64_t tiles = busy * (g.N / 16);
+  const int nb = g.K / kQB;
+  if (tiles / kSkinnyWaves >= 768 || nb < 4)
+    launch_few_as<1>(g, hidden, staged, s);
+  else if (tiles * 2 / kSkinnyWaves >= 768 || nb < 8)
+    launch_few_as<2>(g, hidden, staged, s);
+  else
+    launch_few_as<4>(g, hidden, staged, s);
+  return hipGetLastError();
+}
+
+hipError_t launch_quant_gate_up(const QuantGateUp& g, hipStream_t s) {
   if (g.M <= 0 || g.E <= 0) return hipSuccess;
   const int64_t rows = g.offsets ? cdiv(g.M, g.E) : g.M;
-  const dim3 few((unsigned)(g.F / kQB), (unsigned)g.E);
-  if (x) {
-    const HiddenArgs a{g, static_cast<const uint16_t*>(x), ldx};
-    const size_t lds = 16 * (size_t)(g.K + kHiddenPad) + 16 * 4 * (size_t)(g.K / kQB);
-    skinny_gate_up_kernel<false><<<few, 64 * kHiddenWaves, lds, s>>>(a);
-  } else if (rows <= kFewHiddenRows) {
-    skinny_gate_up_kernel<true><<<few, 64 * kHiddenWaves, 0, s>>>(HiddenArgs{g, nullptr, 0});
-  } else if (rows <= 64) {
+  if (rows <= 64)
     launch_hidden<E64>(g, s);
-  } else if (rows <= 160) {
+  else if (rows <= 160)
     launch_hidden<E128>(g, s);
-  } else {
+  else
     launch_hidden<T256>(g, s);
-  }
   return hipGetLastError();
 }
 

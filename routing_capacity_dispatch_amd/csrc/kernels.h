@@ -341,9 +341,29 @@ struct QuantGateUp {
   float* h_scale;         // [feature blocks][h_scale_ld]
   int64_t h_scale_ld;
 };
-// x: bf16 rows to quantise on the way (g.A and g.a_scale unused), where
-// quant_gate_up_takes_bf16 (a function of the sizes) says so; else null.
-bool quant_gate_up_takes_bf16(const QuantGateUp& g);
-hipError_t launch_quant_gate_up(const QuantGateUp& g, const void* x, int64_t ldx, hipStream_t s);
+hipError_t launch_quant_gate_up(const QuantGateUp& g, hipStream_t s);
+
+// The same experts where each has few rows (few_rows): hidden rows in fp32,
+// then the down product, both quantising the rows they read where K allows it
+// (few_rows_stage: x then holds bf16 rows, or fp32 ones for the down product;
+// else e4m3 rows with scales).
+struct FewRows {
+  const void* x;
+  int64_t ldx;             // elements (bytes for e4m3)
+  const float* x_scale;    // e4m3: [K blocks][x_scale_ld]
+  int64_t x_scale_ld;
+  const char* W0;          // [E][N][K] e4m3: gate or down
+  const float* s0;         // [E][N / 128][K / 128]
+  const char* W1;          // up (hidden)
+  const float* s1;
+  int64_t M;
+  int E, N, K;             // N, K multiples of 128
+  const int32_t* offsets;  // null: every group takes all rows, hidden columns from e * N on
+  void* out;               // hidden: fp32 rows, else bf16 rows
+  int64_t ldo;             // elements, a multiple of 4
+};
+bool few_rows(int64_t M, int E, bool grouped);
+bool few_rows_stage(int K);
+hipError_t launch_few_rows(const FewRows& g, bool hidden, bool staged, hipStream_t s);
 
 }  // namespace moe

@@ -1537,25 +1537,21 @@ moe_status check_gemm_quant(const moe_quant_gemm* q, moe::QuantGemm* g) {
 
 // Grouped SwiGLU in e4m3 over expert-ordered bf16 rows: its workspace.
 struct QuantExpertsWs {
-  char* xq;
-  float* xs;
-  char* hq;
+  char* xq;   // quantised rows
+  float* xs;  // and their scales
+  char* hq;   // quantised hidden rows
   float* hs;
-  void* gemm;
+  float* h;   // few rows per expert: hidden rows in fp32
 };
 int64_t carve_experts_quant(const moe_config* c, int64_t n, void* ws, QuantExpertsWs* w) {
   const int64_t L = c->d_latent, F = c->d_ff;
+  const bool few = moe::few_rows(n, c->n_experts, true);
   Carver cv{static_cast<char*>(ws), 0};
   w->xq = static_cast<char*>(cv.take(n * L));
   w->xs = static_cast<float*>(cv.take(n * (L / 128) * 4));
   w->hq = static_cast<char*>(cv.take(n * F));
   w->hs = static_cast<float*>(cv.take(n * (F / 128) * 4));
-  moe::QuantGemm d{};
-  d.M = n;
-  d.N = L;
-  d.K = (int)F;
-  d.E = c->n_experts;
-  w->gemm = cv.take(moe::quant_gemm_ws_bytes(d));
+  w->h = static_cast<float*>(cv.take(few ? n * F * 4 : 0));
   return cv.used;
 }
 
@@ -1574,6 +1570,65 @@ moe_status run_experts_quant(const moe_config* c, const moe_plan& p, const void*
   const int64_t n = p.dropless_rows, L = c->d_latent, F = c->d_ff;
   QuantExpertsWs q;
   carve_experts_quant(c, n, ws, &q);
+  auto quantize = [&](const void* x, int dt, int64_t K, char* to, float* scale) {
+    moe::QuantizeArgs z{};
+    z.x = x;
+    z.rows = n;
+    z.cols = z.ld = z.ldq = K;
+    z.dt = dt;
+    z.block_rows = 1;
+    z.q = to;
+    z.scale = scale;
+    z.scale_ld = n;
+    return moe::launch_quantize(z, s);
+  };
+  hipError_t e;
+  if (moe::few_rows(n, c->n_experts, true)) {
+    const bool stage_x = moe::few_rows_stage((int)L), stage_h = moe::few_rows_stage((int)F);
+    if (!stage_x) {
+      e = quantize(xs, moe::DT_BF16, L, q.xq, q.xs);
+      if (e != hipSuccess) return MOE_ERR_HIP;
+    }
+    moe::FewRows u{};
+    u.x = stage_x ? xs : q.xq;
+    u.ldx = L;
+    u.x_scale = q.xs;
+    u.x_scale_ld = n;
+    u.W0 = static_cast<const char*>(w->q_gate);
+    u.s0 = w->s_gate;
+    u.W1 = static_cast<const char*>(w->q_up);
+    u.s1 = w->s_up;
+    u.M = n;
+    u.E = c->n_experts;
+    u.N = (int)F;
+    u.K = (int)L;
+    u.offsets = offsets;
+    u.out = q.h;
+    u.ldo = F;
+    e = moe::launch_few_rows(u, true, stage_x, s);
+    if (e != hipSuccess) return MOE_ERR_HIP;
+    if (!stage_h) {
+      e = quantize(q.h, moe::DT_F32, F, q.hq, q.hs);
+      if (e != hipSuccess) return MOE_ERR_HIP;
+    }
+    moe::FewRows d{};
+    d.x = stage_h ? static_cast<const void*>(q.h) : q.hq;
+    d.ldx = F;
+    d.x_scale = q.hs;
+    d.x_scale_ld = n;
+    d.W0 = static_cast<const char*>(w->q_down);
+    d.s0 = w->s_down;
+    d.M = n;
+    d.E = c->n_experts;
+    d.N = (int)L;
+    d.K = (int)F;
+    d.offsets = offsets;
+    d.out = out;
+    d.ldo = L;
+    return hip_status(moe::launch_few_rows(d, false, stage_h, s));
+  }
+  e = quantize(xs, moe::DT_BF16, L, q.xq, q.xs);
+  if (e != hipSuccess) return MOE_ERR_HIP;
   moe::QuantGateUp u{};
   u.A = q.xq;
   u.lda = L;
@@ -1592,22 +1647,7 @@ moe_status run_experts_quant(const moe_config* c, const moe_plan& p, const void*
   u.ldh = F;
   u.h_scale = q.hs;
   u.h_scale_ld = n;
-  const bool fused = moe::quant_gate_up_takes_bf16(u);
-  hipError_t e = hipSuccess;
-  if (!fused) {
-    moe::QuantizeArgs z{};
-    z.x = xs;
-    z.rows = n;
-    z.cols = z.ld = z.ldq = L;
-    z.dt = moe::DT_BF16;
-    z.block_rows = 1;
-    z.q = q.xq;
-    z.scale = q.xs;
-    z.scale_ld = n;
-    e = moe::launch_quantize(z, s);
-    if (e != hipSuccess) return MOE_ERR_HIP;
-  }
-  e = moe::launch_quant_gate_up(u, fused ? xs : nullptr, L, s);
+  e = moe::launch_quant_gate_up(u, s);
   if (e != hipSuccess) return MOE_ERR_HIP;
   moe::QuantGemm d{};
   d.A = q.hq;
@@ -1629,7 +1669,7 @@ moe_status run_experts_quant(const moe_config* c, const moe_plan& p, const void*
   d.E = c->n_experts;
   d.b_stride = L * F;
   d.b_scale_stride = (L / 128) * (F / 128);
-  return hip_status(moe::launch_quant_gemm(d, q.gemm, s));
+  return hip_status(moe::launch_quant_gemm(d, nullptr, s));
 }
 
 bool quant_experts_valid(const moe_quant_experts* w) {

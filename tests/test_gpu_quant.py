@@ -350,6 +350,13 @@ def test_experts_match_oracle(E, L, F, counts):
     check_experts(E, L, F, counts, E + L + F)
 
 
+@pytest.mark.parametrize("E,L,F,counts", [(3, 4096, 128, [1, 17, 0]), (2, 4224, 128, [2, 20]), (2, 128, 4096, [5, 3]),
+                                          (3, 128, 4352, [1, 18, 0]), (2, 4224, 4224, [3, 1]), (2, 1152, 640, [16, 32]),
+                                          (2, 2176, 128, [90, 40])])
+def test_experts_of_long_rows_match_oracle(E, L, F, counts):
+    check_experts(E, L, F, counts, E + L + F, per_expert=3)
+
+
 def test_experts_leave_other_rows():
     check_experts(4, 128, 128, [3, 0, 2, 40], 3, extra=37)
     check_experts(4, 128, 128, [0, 0, 0, 0], 4, extra=20)
