@@ -532,10 +532,10 @@ def _check(ok, what):
 
 def _rows(t, shape, dtype, what, dev=None):
     """A contiguous device tensor of this shape and type (the entry points take plain pointers)."""
-    _check(isinstance(t, torch.Tensor) and t.dtype == dtype and tuple(t.shape) == tuple(shape) and t.is_contiguous()
-           and t.is_cuda and (dev is None or t.device == dev),
-           f"{what} must be a contiguous {dtype} tensor of shape {tuple(shape)}"
-           + (f" on {dev}" if dev is not None else " on a GPU"))
+    if not (isinstance(t, torch.Tensor) and t.dtype == dtype and t.shape == shape and t.is_contiguous()
+            and t.is_cuda and (dev is None or t.device == dev)):
+        raise ValueError(f"{what} must be a contiguous {dtype} tensor of shape {tuple(shape)}"
+                         + (f" on {dev}" if dev is not None else " on a GPU"))
     return t
 
 
@@ -624,16 +624,16 @@ def quantize(x: torch.Tensor, block_rows: int = 1, transpose: bool = False, out=
 
 
 def _operand(q, what, dev=None):
-    _check(isinstance(q, torch.Tensor) and q.dim() == 2 and q.is_cuda and q.dtype == torch.float8_e4m3fn
-           and (dev is None or q.device == dev), f"{what} must be a two-dimensional e4m3 tensor on one GPU")
-    _check(q.shape[1] <= 1 or q.stride(1) == 1, f"the columns of {what} must be contiguous")
+    if not (isinstance(q, torch.Tensor) and q.dim() == 2 and q.is_cuda and q.dtype == torch.float8_e4m3fn
+            and (dev is None or q.device == dev) and (q.shape[1] <= 1 or q.stride(1) == 1)):
+        raise ValueError(f"{what} must be a two-dimensional e4m3 tensor with contiguous columns on one GPU")
     return q.stride(0) if q.shape[0] > 1 and q.shape[1] > 0 else q.shape[1]
 
 
 def _scale_ld(s, shape, what, dev):
-    _check(isinstance(s, torch.Tensor) and s.dtype == torch.float32 and tuple(s.shape) == shape and s.device == dev
-           and (shape[1] <= 1 or s.stride(1) == 1),
-           f"{what} must be an fp32 tensor of shape {shape} with contiguous columns")
+    if not (isinstance(s, torch.Tensor) and s.dtype == torch.float32 and s.shape == shape and s.device == dev
+            and (shape[1] <= 1 or s.stride(1) == 1)):
+        raise ValueError(f"{what} must be an fp32 tensor of shape {shape} with contiguous columns")
     return s.stride(0) if shape[0] > 1 else max(shape[1], 1)
 
 
@@ -655,9 +655,9 @@ def gemm_quant(a, a_scales, b, b_scales, block_rows: int = 128, out_dtype=torch.
     if out is None:
         out = torch.empty((M, N), dtype=out_dtype, device=dev)
     else:
-        _check(tuple(out.shape) == (M, N) and out.dtype == out_dtype and out.device == dev
+        _check(out.shape == (M, N) and out.dtype == out_dtype and out.device == dev
                and (N <= 1 or out.stride(1) == 1) and (M <= 1 or out.stride(0) >= N),
-               f"out must be a {out_dtype} tensor of shape {(M, N)} with contiguous columns")
+               "out must be a tensor of C's shape and type with contiguous columns")
     g = abi.MoeQuantGemm(M=M, N=N, K=K, a=a.data_ptr(), lda=lda, a_scale=a_scales.data_ptr(), a_scale_ld=sa,
                          b=b.data_ptr(), ldb=ldb, b_scale=b_scales.data_ptr(), b_scale_ld=sb, c=out.data_ptr(),
                          ldc=out.stride(0) if M > 1 else N, b_block_rows=block_rows, out_dtype=_DT[out_dtype],

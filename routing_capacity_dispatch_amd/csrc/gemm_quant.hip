@@ -210,7 +210,7 @@ __global__ __launch_bounds__(64 * kSkinnyWaves) void skinny_kernel(QuantGemm g) 
 // Experts with few rows.  Two launches: the hidden rows h = silu(x Wg^T) *
 // (x Wu^T) in fp32, then their product with the down weights.  Each launch
 // quantises the rows it reads (bf16 x, fp32 h) into LDS itself, every
-// workgroup all K of its expert's rows, 16 at a time: a launch and a round
+// workgroup all K of its expert's rows, g.chunk (1 .. 16) at a time: a launch and a round
 // trip through memory less for rows that are few beside the weights, and the
 // hidden rows' blocks of 128 features bind no workgroup, so workgroups are
 // small and spread over all CUs whatever the number of busy experts.
@@ -257,7 +257,10 @@ template <int KS, int kSource, bool kHidden>
 __global__ __launch_bounds__(64 * kSkinnyWaves) void few_rows_kernel(FewRows g) {
   extern __shared__ __attribute__((aligned(16))) char dyn[];  // staged rows, then their scales
   constexpr int W = kHidden ? 2 : 1;
-  constexpr int U = 4 / W;  // blocks whose loads are in flight together
+  // blocks of a span (two spans are in flight): fewer registers leave room for
+  // more workgroups, which cover the latency better than longer spans (4 / W
+  // measured 42 us for 4 tokens x 8 of 64 experts, L 2048, F 1024; 2 / W 39)
+  constexpr int U = 2 / W;
   __shared__ f32x4_t part[KS > 1 ? kSkinnyWaves : 1][W][64];
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
   const int ks = wave % KS, e = blockIdx.y;
@@ -278,9 +281,9 @@ __global__ __launch_bounds__(64 * kSkinnyWaves) void few_rows_kernel(FewRows g) 
     sp[1] = g.s1 + srow;
   }
   const int ldq = g.K + kRowPad;
-  float* staged_sc = reinterpret_cast<float*>(dyn + 16 * ldq);
-  for (int64_t m0 = 0; m0 < rows; m0 += 16) {
-    const int left = (int)min(rows - m0, (int64_t)16);
+  float* staged_sc = reinterpret_cast<float*>(dyn + g.chunk * ldq);
+  for (int64_t m0 = 0; m0 < rows; m0 += g.chunk) {
+    const int left = (int)min(rows - m0, (int64_t)g.chunk);
     const int64_t first = row0 + m0;
     Frag8 w[2][U][W];
     float t[2][U][W];
@@ -351,7 +354,7 @@ __global__ __launch_bounds__(64 * kSkinnyWaves) void few_rows_kernel(FewRows g) 
 #pragma unroll
           for (int j = 1; j < KS; ++j) acc[i] += part[wave + j][i][lane];
       }
-      if (m0 + 16 < rows) __syncthreads();
+      if (m0 + g.chunk < rows) __syncthreads();
     }
     // lane: row lane & 15, 4 neighbouring columns
     if (ks == 0 && (lane & 15) < left) {
@@ -964,7 +967,7 @@ template <int KS>
 void launch_few_as(const FewRows& g, bool hidden, bool staged, hipStream_t s) {
   const dim3 grid((unsigned)(g.N / (16 * (kSkinnyWaves / KS))), (unsigned)g.E);
   constexpr int T = 64 * kSkinnyWaves;
-  const size_t lds = staged ? 16 * (size_t)(g.K + kRowPad) + 16 * 4 * (size_t)(g.K / kQB) : 0;
+  const size_t lds = staged ? g.chunk * (size_t)(g.K + kRowPad) + 16 * 4 * (size_t)(g.K / kQB) : 0;
   if (hidden) {
     if (staged)
       few_rows_kernel<KS, kBf16, true><<<grid, T, lds, s>>>(g);

@@ -358,6 +358,7 @@ struct FewRows {
   const float* s1;
   int64_t M;
   int E, N, K;             // N, K multiples of 128
+  int chunk;               // rows taken at once, 1 .. 16
   const int32_t* offsets;  // null: every group takes all rows, hidden columns from e * N on
   void* out;               // hidden: fp32 rows, else bf16 rows
   int64_t ldo;             // elements, a multiple of 4

@@ -1584,6 +1584,9 @@ moe_status run_experts_quant(const moe_config* c, const moe_plan& p, const void*
   };
   hipError_t e;
   if (moe::few_rows(n, c->n_experts, true)) {
+    // a token's ids differ, so an expert has at most T rows (more are taken
+    // in further passes): fewer staged rows leave room for more workgroups
+    const int chunk = (int)(c->T < 16 ? c->T : 16);
     const bool stage_x = moe::few_rows_stage((int)L), stage_h = moe::few_rows_stage((int)F);
     if (!stage_x) {
       e = quantize(xs, moe::DT_BF16, L, q.xq, q.xs);
@@ -1602,6 +1605,7 @@ moe_status run_experts_quant(const moe_config* c, const moe_plan& p, const void*
     u.E = c->n_experts;
     u.N = (int)F;
     u.K = (int)L;
+    u.chunk = chunk;
     u.offsets = offsets;
     u.out = q.h;
     u.ldo = F;
@@ -1622,6 +1626,7 @@ moe_status run_experts_quant(const moe_config* c, const moe_plan& p, const void*
     d.E = c->n_experts;
     d.N = (int)L;
     d.K = (int)F;
+    d.chunk = chunk;
     d.offsets = offsets;
     d.out = out;
     d.ldo = L;

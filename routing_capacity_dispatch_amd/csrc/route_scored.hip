@@ -3,8 +3,11 @@
 // make the gates, renormalised over the selected and scaled on request.
 //
 // Selected ids are whole numbers, so the keys must be ordered as the formula
-// orders them: keys are computed in fp64.  One wavefront per token; lane l
-// holds experts l, l + 64, ...
+// orders them, whatever an fp32 exponential rounds to.  For k <= 8 a token is
+// first selected from fp32 keys by 16 lanes, four tokens to a wavefront; where
+// two keys that matter lie closer than their error bound (about one token in
+// ten thousand on random logits), and for every other shape, one wavefront
+// selects the token from fp64 keys.
 #include "common.h"
 #include "kernels.h"
 
@@ -140,6 +143,309 @@ __global__ __launch_bounds__(256) void route_scored_kernel(ScoreArgs a, const fl
   select_token<NPER>(a, logits + t * a.E, bias, keys[w], topk + t * a.k, gates + t * a.k);
 }
 
+// ------------------------------------------------------- 16 lanes a token
+// Keys as doubles with the expert in the low mantissa bits (an fp32 key
+// leaves 29 free), so that one fp64 maximum carries key and index, the lower
+// index first among equal keys.  A lane reduces its experts to the 8 largest,
+// sorted, by merging sorted lists of 8; four exchanges within the 16 lanes
+// merge those, after which every lane holds the token's 8 largest in order.
+//
+// How far an fp32 key can be from the formula's, u = 2^-24 the rounding unit:
+//   sigmoid: the exponential of l is off by 4 u l + 2 u relatively, which
+//     moves s by s (1 - s) of that (<= 0.23 * 4 u + 0.25 * 2 u); 1 + e and the
+//     reciprocal add 3 u s: within 4.5 u
+//   softmax, d = max - l: e^-d is off by 4 u d + 4 u relatively, d e^-d <=
+//     0.37, so p by 1.5 u + 4 u p; the sum's error (NPER + 4 additions, the
+//     exponentials' own) is a factor common to all p, within (NPER + 24) u,
+//     and turns two keys around only by that factor of their p's difference,
+//     which at a near tie is the difference of two biases
+//   adding the bias: u |key|
+// Two keys closer than both errors are not told apart here.  Without a bias
+// and without groups the logits themselves are the keys: exact, as long as
+// fp64 scores still separate what fp32 logits separate.
+constexpr int kTop = 8;
+
+__device__ __forceinline__ double pack_key(float key, int e) {
+  const float f = fmaxf(key, -3.402823466e38f);  // -inf has no mantissa to carry an index
+  const uint64_t b = (uint64_t)__double_as_longlong((double)f);
+  return __longlong_as_double((long long)(b | (uint32_t)(f < 0.0f ? e : 1023 - e)));
+}
+__device__ __forceinline__ int packed_expert(uint32_t lo, uint32_t hi) {
+  const int i = (int)(lo & 1023);
+  return (hi >> 31) ? i : 1023 - i;
+}
+__device__ __forceinline__ float packed_key(double d) {
+  const uint64_t b = (uint64_t)__double_as_longlong(d) & ~(uint64_t)1023;
+  return (float)__longlong_as_double((long long)b);
+}
+
+__device__ __forceinline__ void order(double& a, double& b) {  // larger first
+  const double x = fmax(a, b), y = fmin(a, b);
+  a = x;
+  b = y;
+}
+
+// Descending sort of 8 (odd-even merge sort, 19 exchanges).
+__device__ __forceinline__ void sort8(double* v) {
+  order(v[0], v[1]); order(v[2], v[3]); order(v[4], v[5]); order(v[6], v[7]);
+  order(v[0], v[2]); order(v[1], v[3]); order(v[4], v[6]); order(v[5], v[7]);
+  order(v[1], v[2]); order(v[5], v[6]);
+  order(v[0], v[4]); order(v[1], v[5]); order(v[2], v[6]); order(v[3], v[7]);
+  order(v[2], v[4]); order(v[3], v[5]);
+  order(v[1], v[2]); order(v[3], v[4]); order(v[5], v[6]);
+}
+
+// v = the 8 largest of two descending lists: their element-wise maximum with
+// one reversed is bitonic.
+__device__ __forceinline__ void merge8(double* v, const double* o) {
+#pragma unroll
+  for (int i = 0; i < 8; ++i) v[i] = fmax(v[i], o[7 - i]);
+#pragma unroll
+  for (int d = 4; d > 0; d >>= 1)
+#pragma unroll
+    for (int i = 0; i < 8; ++i)
+      if ((i & d) == 0) order(v[i], v[i + d]);
+}
+
+// Partner's value in the n-th exchange of 16 lanes: lane ^ 1, lane ^ 2, the
+// mirror within 8, the mirror within 16 (each pairs lanes whose values still
+// differ).
+template <int kStep>
+__device__ __forceinline__ uint32_t partner(uint32_t v) {
+  constexpr int ctrl = kStep == 0 ? 0xB1 : kStep == 1 ? 0x4E : kStep == 2 ? 0x141 : 0x140;
+  return (uint32_t)__builtin_amdgcn_update_dpp(0, (int)v, ctrl, 0xF, 0xF, false);
+}
+template <int kStep>
+__device__ __forceinline__ double partner(double v) {
+  const uint64_t b = (uint64_t)__double_as_longlong(v);
+  const uint64_t lo = partner<kStep>((uint32_t)b), hi = partner<kStep>((uint32_t)(b >> 32));
+  return __longlong_as_double((long long)(lo | (hi << 32)));
+}
+template <int kStep>
+__device__ __forceinline__ float partner(float v) {
+  return __uint_as_float(partner<kStep>(__float_as_uint(v)));
+}
+__device__ __forceinline__ float max16(float v) {
+  v = fmaxf(v, partner<0>(v));
+  v = fmaxf(v, partner<1>(v));
+  v = fmaxf(v, partner<2>(v));
+  return fmaxf(v, partner<3>(v));
+}
+__device__ __forceinline__ float sum16(float v) {
+  v += partner<0>(v);
+  v += partner<1>(v);
+  v += partner<2>(v);
+  return v + partner<3>(v);
+}
+template <int kStep>
+__device__ __forceinline__ void merge_partner(double* v) {
+  double o[8];
+#pragma unroll
+  for (int i = 0; i < 8; ++i) o[i] = partner<kStep>(v[i]);
+  merge8(v, o);
+}
+
+// Where lane c's i-th value lies: expert (i / V) * step + c * lane_step + i %
+// V (V values per load), i below `per`.
+struct LaneMap {
+  int step, lane_step, per;
+};
+
+template <int NPER, int V>
+__device__ __forceinline__ void load_row(const float* __restrict__ row, int E, const LaneMap& m, int c, float* v) {
+#pragma unroll
+  for (int i = 0; i < NPER; i += V) {
+    const int e = min((i / V) * m.step + c * m.lane_step, E - V);  // past the end: unused
+    if constexpr (V == 4) {
+      const f32x4_t x = *reinterpret_cast<const f32x4_t*>(row + e);
+#pragma unroll
+      for (int q = 0; q < 4; ++q) v[i + q] = x[q];
+    } else {
+      v[i] = row[e];
+    }
+  }
+}
+
+template <int NPER, int V>
+__global__ __launch_bounds__(256) void route_top8_kernel(ScoreArgs a, LaneMap map, const float* __restrict__ logits,
+                                                         const float* __restrict__ bias, int32_t* __restrict__ topk,
+                                                         float* __restrict__ gates) {
+  constexpr int NPER64 = (NPER + 3) / 4;  // experts per lane of a whole wavefront
+  __shared__ double keys64[4][NPER64 * 64];
+  const int lane = threadIdx.x & 63, c = lane & 15;
+  const int64_t t0 = ((int64_t)blockIdx.x * 4 + (threadIdx.x >> 6)) * 4;
+  if (t0 >= a.T) return;
+  const int64_t t = min(t0 + (lane >> 4), a.T - 1);
+  const int E = a.E;
+  const float* row = logits + t * E;
+  float v[NPER], key[NPER];
+  load_row<NPER, V>(row, E, map, c, v);
+  bool ok[NPER];
+#pragma unroll
+  for (int i = 0; i < NPER; ++i) ok[i] = i < map.per && (i / V) * map.step + c * map.lane_step + i % V < E;
+  float mx = -3.402823466e38f;
+#pragma unroll
+  for (int i = 0; i < NPER; ++i) mx = fmaxf(mx, ok[i] ? v[i] : mx);
+  mx = max16(mx);
+  float sum = 1.0f;
+  float bmax = 0.0f;  // largest |bias| (softmax)
+  const bool by_logit = bias == nullptr && a.groups == 1;
+  bool unsure = false;
+  if (!a.sigmoid) {
+    sum = 0.0f;
+#pragma unroll
+    for (int i = 0; i < NPER; ++i) {
+      key[i] = ok[i] ? __expf(v[i] - mx) : 0.0f;
+      sum += key[i];
+    }
+    sum = fmaxf(sum16(sum), 1e-37f);
+  }
+  if (by_logit) {
+#pragma unroll
+    for (int i = 0; i < NPER; ++i) key[i] = v[i];
+    // fp64 sigmoids of neighbouring fp32 logits coincide above about 20
+    unsure = !(mx <= 20.0f) && a.sigmoid;
+  } else {
+    if (a.sigmoid) {
+#pragma unroll
+      for (int i = 0; i < NPER; ++i) key[i] = sigmoid(v[i]);
+    } else {
+      const float r = 1.0f / sum;
+#pragma unroll
+      for (int i = 0; i < NPER; ++i) key[i] *= r;
+    }
+    if (bias) {
+      float b[NPER];
+      load_row<NPER, V>(bias, E, map, c, b);
+#pragma unroll
+      for (int i = 0; i < NPER; ++i) key[i] += b[i];
+      if (!a.sigmoid) {
+#pragma unroll
+        for (int i = 0; i < NPER; ++i) bmax = fmaxf(bmax, fabsf(b[i]));
+        bmax = max16(bmax);
+      }
+    }
+  }
+  double top[kTop];
+#pragma unroll
+  for (int i = 0; i < NPER; i += kTop) {
+    double l[kTop];
+#pragma unroll
+    for (int j = 0; j < kTop; ++j) {
+      l[j] = -__builtin_huge_val();
+      if (i + j < NPER) {
+        const int e = ((i + j) / V) * map.step + c * map.lane_step + (i + j) % V;
+        l[j] = ok[i + j] ? pack_key(key[i + j], e) : l[j];
+      }
+    }
+    sort8(l);
+    if (i == 0) {
+#pragma unroll
+      for (int j = 0; j < kTop; ++j) top[j] = l[j];
+    } else {
+      merge8(top, l);
+    }
+  }
+  // difference below which two keys of magnitude up to x are not told apart
+  auto tol = [&](float x) {
+    constexpr float u = 5.9604645e-8f;
+    x = fabsf(x);
+    if (by_logit) return 0x1p-30f * (1.0f + x);  // fp64 scores still differ by it
+    if (a.sigmoid) return 16.0f * u + 4.0f * u * x;
+    return 4.0f * u + 8.0f * u * (x + bmax) + 2.0f * u * x + (NPER + 24) * u * fminf(1.0f, 2.0f * bmax);
+  };
+  bool mine = true;  // this lane's experts can be taken
+  if (a.groups > 1) {
+    // a lane's experts are of one group, groups are 16 / G neighbouring lanes
+    const int span = 16 / a.groups;
+    double t1 = top[0], t2 = top[1];
+    auto join = [&](double o1, double o2) {
+      t2 = fmax(fmin(t1, o1), fmax(t2, o2));
+      t1 = fmax(t1, o1);
+    };
+    if (span > 1) join(partner<0>(t1), partner<0>(t2));
+    if (span > 2) join(partner<1>(t1), partner<1>(t2));
+    if (span > 4) join(partner<2>(t1), partner<2>(t2));
+    const float gsc = a.group_top == 2 && t2 > -1e300 ? packed_key(t1) + packed_key(t2) : packed_key(t1);
+    const int g = c / span;
+    int before = 0;
+    for (int o = 0; o < a.groups; ++o) {
+      const float s = __shfl(gsc, (lane & 48) + o * span);
+      before += (s > gsc || (s == gsc && o < g)) ? 1 : 0;
+      unsure = unsure || (o != g && fabsf(s - gsc) <= 2.0f * tol(fmaxf(fabsf(s), fabsf(gsc))));
+    }
+    mine = before < a.top_groups;
+    if (!mine) {
+#pragma unroll
+      for (int j = 0; j < kTop; ++j) top[j] = -__builtin_huge_val();
+    }
+  }
+  merge_partner<0>(top);
+  merge_partner<1>(top);
+  merge_partner<2>(top);
+  merge_partner<3>(top);
+  // neighbours in order, and the first one not taken: count what lies within
+  // the tolerance of the last taken key
+  float last = 0.0f;
+#pragma unroll
+  for (int j = 0; j < kTop; ++j) {
+    if (j < a.k) {
+      const float x = packed_key(top[j]);
+      if (j > 0) {
+        const float gap = last - x, w = tol(fmaxf(fabsf(last), fabsf(x)));
+        unsure = unsure || (by_logit ? gap > 0.0f && gap <= w : gap <= w);
+      }
+      last = x;
+    }
+  }
+  const float edge = last - tol(last);
+  int near = 0, equal = 0;
+#pragma unroll
+  for (int i = 0; i < NPER; ++i) {
+    near += (ok[i] & mine & (key[i] >= edge)) ? 1 : 0;
+    equal += (ok[i] & mine & (key[i] >= last)) ? 1 : 0;
+  }
+  const float n16 = sum16((float)near), e16 = sum16((float)equal);
+  // equal logits are exact ties: the index decided
+  unsure = unsure || (by_logit ? n16 != e16 : n16 != (float)a.k);
+  // fp64 scores of distant logits underflow and coincide; -inf and NaN too
+  if (by_logit) unsure = unsure || !(last >= (a.sigmoid ? -700.0f : mx - 700.0f));
+  unsure = unsure || !(fabsf(last) < 3.0e38f);
+
+  // lane c < k: the c-th selected expert and its gate
+  uint32_t lo = 0, hi = 0;
+#pragma unroll
+  for (int j = 0; j < kTop; ++j) {
+    const uint64_t b = (uint64_t)__double_as_longlong(top[j]);
+    lo = c == j ? (uint32_t)b : lo;
+    hi = c == j ? (uint32_t)(b >> 32) : hi;
+  }
+  const bool on = c < a.k;
+  const int e = min(packed_expert(lo, hi), E - 1);
+  const float l = on ? row[e] : 0.0f;
+  float s;
+  if (a.sigmoid) {
+    const float x = expf(-fabsf(l)), r = 1.0f / (1.0f + x);
+    s = l >= 0.0f ? r : x * r;
+  } else {
+    s = expf(l - mx) / sum;
+  }
+  s = on ? s : 0.0f;
+  const float S = a.renorm ? sum16(s) + 1e-20f : 1.0f;
+  const uint64_t bad = ballot64(unsure);
+  const bool write = on && t0 + (lane >> 4) < a.T && ((bad >> (lane & 48)) & 0xFFFF) == 0;
+  if (write) {
+    topk[t * a.k + c] = e;
+    gates[t * a.k + c] = s / S * a.scale;
+  }
+  if (bad == 0) return;
+  for (int i = 0; i < 4; ++i) {
+    if (t0 + i >= a.T || ((bad >> (16 * i)) & 0xFFFF) == 0) continue;
+    select_token<NPER64>(a, logits + (t0 + i) * E, bias, keys64[threadIdx.x >> 6], topk + (t0 + i) * a.k,
+                         gates + (t0 + i) * a.k);
+  }
+}
+
 // Gradient: ds_j of the selected scores (lane j), then the row.
 template <int NPER>
 __global__ __launch_bounds__(256) void route_scored_bwd_kernel(ScoreArgs a, const float* __restrict__ logits,
@@ -231,9 +537,40 @@ __global__ __launch_bounds__(256) void route_scored_bwd_kernel(ScoreArgs a, cons
     else { CALL(16); }           \
   } while (0)
 
+template <int V>
+hipError_t launch_top8(const ScoreArgs& a, const LaneMap& m, int nper, const float* logits, const float* bias,
+                       int32_t* topk, float* gates, hipStream_t s) {
+  const dim3 grid((unsigned)((a.T + 15) / 16));
+#define CALL(N) route_top8_kernel<N, V><<<grid, 256, 0, s>>>(a, m, logits, bias, topk, gates)
+  if (nper <= 4) { CALL(4); }
+  else if (nper <= 8) { CALL(8); }
+  else if (nper <= 16) { CALL(16); }
+  else if (nper <= 24) { CALL(24); }
+  else if (nper <= 32) { CALL(32); }
+  else { CALL(64); }
+#undef CALL
+  return hipGetLastError();
+}
+
 hipError_t launch_route_scored(const ScoreArgs& a, const float* logits, const float* bias, int32_t* topk,
                                float* gates, hipStream_t s) {
   if (a.T <= 0) return hipSuccess;
+  const int64_t align = reinterpret_cast<int64_t>(logits) | reinterpret_cast<int64_t>(bias);
+  if (a.k <= kTop) {
+    const int per = (a.E + 15) / 16;
+    if (a.groups == 1) {
+      // 64 experts a load of 16 lanes
+      if (a.E % 4 == 0 && (align & 15) == 0)
+        return launch_top8<4>(a, LaneMap{64, 4, 1 << 20}, (per + 3) / 4 * 4, logits, bias, topk, gates, s);
+      return launch_top8<1>(a, LaneMap{16, 1, 1 << 20}, per, logits, bias, topk, gates, s);
+    }
+    if (16 % a.groups == 0 && a.E % 16 == 0) {
+      // neighbouring experts in a lane, so that a lane's are of one group
+      if (per % 4 == 0 && (align & 15) == 0)
+        return launch_top8<4>(a, LaneMap{4, per, per}, per, logits, bias, topk, gates, s);
+      return launch_top8<1>(a, LaneMap{1, per, per}, per, logits, bias, topk, gates, s);
+    }
+  }
   const dim3 grid((unsigned)((a.T + 3) / 4));
 #define CALL(N) route_scored_kernel<N><<<grid, 256, 0, s>>>(a, logits, bias, topk, gates)
   MOE_BY_EXPERTS(a.E, CALL);
