@@ -179,8 +179,21 @@ __device__ __forceinline__ float packed_key(double d) {
   return (float)__longlong_as_double((long long)b);
 }
 
+// Maximum and minimum as single instructions: packed keys are never NaN, and
+// fmax / fmin would quiet each operand first.
+__device__ __forceinline__ double max64(double a, double b) {
+  double r;
+  asm("v_max_f64 %0, %1, %2" : "=v"(r) : "v"(a), "v"(b));
+  return r;
+}
+__device__ __forceinline__ double min64(double a, double b) {
+  double r;
+  asm("v_min_f64 %0, %1, %2" : "=v"(r) : "v"(a), "v"(b));
+  return r;
+}
+
 __device__ __forceinline__ void order(double& a, double& b) {  // larger first
-  const double x = fmax(a, b), y = fmin(a, b);
+  const double x = max64(a, b), y = min64(a, b);
   a = x;
   b = y;
 }
@@ -199,7 +212,7 @@ __device__ __forceinline__ void sort8(double* v) {
 // one reversed is bitonic.
 __device__ __forceinline__ void merge8(double* v, const double* o) {
 #pragma unroll
-  for (int i = 0; i < 8; ++i) v[i] = fmax(v[i], o[7 - i]);
+  for (int i = 0; i < 8; ++i) v[i] = max64(v[i], o[7 - i]);
 #pragma unroll
   for (int d = 4; d > 0; d >>= 1)
 #pragma unroll
@@ -225,6 +238,12 @@ template <int kStep>
 __device__ __forceinline__ float partner(float v) {
   return __uint_as_float(partner<kStep>(__float_as_uint(v)));
 }
+__device__ __forceinline__ float min16(float v) {
+  v = fminf(v, partner<0>(v));
+  v = fminf(v, partner<1>(v));
+  v = fminf(v, partner<2>(v));
+  return fminf(v, partner<3>(v));
+}
 __device__ __forceinline__ float max16(float v) {
   v = fmaxf(v, partner<0>(v));
   v = fmaxf(v, partner<1>(v));
@@ -246,16 +265,21 @@ __device__ __forceinline__ void merge_partner(double* v) {
 }
 
 // Where lane c's i-th value lies: expert (i / V) * step + c * lane_step + i %
-// V (V values per load), i below `per`.
+// V (V values per load), i below `per`.  full: every lane's NPER values exist.
 struct LaneMap {
   int step, lane_step, per;
+  bool full;
 };
+template <int V>
+__device__ __forceinline__ int mapped(const LaneMap& m, int c, int i) {
+  return (i / V) * m.step + c * m.lane_step + i % V;
+}
 
 template <int NPER, int V>
 __device__ __forceinline__ void load_row(const float* __restrict__ row, int E, const LaneMap& m, int c, float* v) {
 #pragma unroll
   for (int i = 0; i < NPER; i += V) {
-    const int e = min((i / V) * m.step + c * m.lane_step, E - V);  // past the end: unused
+    const int e = min(mapped<V>(m, c, i), E - V);  // past the end: not used
     if constexpr (V == 4) {
       const f32x4_t x = *reinterpret_cast<const f32x4_t*>(row + e);
 #pragma unroll
@@ -265,79 +289,132 @@ __device__ __forceinline__ void load_row(const float* __restrict__ row, int E, c
     }
   }
 }
-
 template <int NPER, int V>
+__device__ __forceinline__ void mask_row(int E, const LaneMap& m, int c, float* v) {
+  if (m.full) return;
+#pragma unroll
+  for (int i = 0; i < NPER; ++i) v[i] = (i < m.per) & (mapped<V>(m, c, i) < E) ? v[i] : -__builtin_huge_valf();
+}
+
+// Tokens whose selection hangs on keys too close for fp32 (`again`, equal in
+// the 16 lanes of a token): the experts whose keys reach `edge`, at most 16,
+// are compared by fp64 keys, one per lane.  cand: 64 ints of LDS of this
+// wavefront.
+template <int NPER, int V, bool kSigmoid>
+__device__ __forceinline__ void select_close(const ScoreArgs& a, const LaneMap& map, const float* __restrict__ row,
+                                             const float* __restrict__ bias, const float* key, float edge, float mx,
+                                             bool again, int* cand, int32_t* topk, float* gates) {
+  const int lane = threadIdx.x & 63, c = lane & 15;
+  int* mine = cand + (lane & 48);
+  int n = 0;
+#pragma unroll
+  for (int i = 0; i < NPER; ++i) {
+    const bool take = again && key[i] >= edge;
+    const uint32_t m = (uint32_t)(ballot64(take) >> (lane & 48)) & 0xFFFF;
+    const int at = n + __popc(m & ((1u << c) - 1));
+    if (take && at < 16) mine[at] = mapped<V>(map, c, i);
+    n += __popc(m);
+  }
+  __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+  const bool on = again && c < min(n, 16);
+  const int e = on ? mine[c] : 0;
+  const float l = row[e];
+  double s;
+  if constexpr (kSigmoid) {
+    s = score64(a, l, 0.0, 1.0);
+  } else {
+    double sum = 0.0;
+    for (int j = c; j < a.E; j += 16) sum += exp((double)row[j] - (double)mx);
+    for (int d = 1; d < 16; d <<= 1) sum += shfl_xor_f64(sum, d);
+    s = score64(a, l, mx, fmax(sum, 1e-300));
+  }
+  const double x = s + (bias ? (double)bias[e] : 0.0);
+  int rank = 0;
+  for (int j = 0; j < 16; ++j) {
+    const int from = (lane & 48) + j;
+    const uint64_t b = (uint64_t)__double_as_longlong(x);
+    const uint64_t lo = __shfl((uint32_t)b, from), hi = __shfl((uint32_t)(b >> 32), from);
+    const double o = __longlong_as_double((long long)(lo | (hi << 32)));
+    const int oe = __shfl(e, from);
+    rank += (j < n && (o > x || (o == x && oe < e))) ? 1 : 0;
+  }
+  const bool sel = on && rank < a.k;
+  double S = 1.0;
+  if (a.renorm) {
+    S = sel ? s : 0.0;
+    for (int d = 1; d < 16; d <<= 1) S += shfl_xor_f64(S, d);
+    S += 1e-20;
+  }
+  if (sel) {
+    topk[rank] = e;
+    gates[rank] = (float)(s / S * (double)a.scale);
+  }
+}
+
+// kLogit: the logits are the keys (no bias, no groups).
+template <int NPER, int V, bool kSigmoid, bool kLogit>
 __global__ __launch_bounds__(256) void route_top8_kernel(ScoreArgs a, LaneMap map, const float* __restrict__ logits,
                                                          const float* __restrict__ bias, int32_t* __restrict__ topk,
                                                          float* __restrict__ gates) {
   constexpr int NPER64 = (NPER + 3) / 4;  // experts per lane of a whole wavefront
   __shared__ double keys64[4][NPER64 * 64];
-  const int lane = threadIdx.x & 63, c = lane & 15;
-  const int64_t t0 = ((int64_t)blockIdx.x * 4 + (threadIdx.x >> 6)) * 4;
+  __shared__ int cand[4][64];
+  const int lane = threadIdx.x & 63, c = lane & 15, wave = threadIdx.x >> 6;
+  const int64_t t0 = ((int64_t)blockIdx.x * 4 + wave) * 4;
   if (t0 >= a.T) return;
-  const int64_t t = min(t0 + (lane >> 4), a.T - 1);
+  const bool exists = t0 + (lane >> 4) < a.T;
+  const int64_t t = exists ? t0 + (lane >> 4) : a.T - 1;
   const int E = a.E;
   const float* row = logits + t * E;
-  float v[NPER], key[NPER];
-  load_row<NPER, V>(row, E, map, c, v);
-  bool ok[NPER];
+  float key[NPER];
+  load_row<NPER, V>(row, E, map, c, key);
+  mask_row<NPER, V>(E, map, c, key);
+  // `hard`: left to the whole wavefront's fp64 selection
+  bool hard = false;
+  float mx = 0.0f, sum = 1.0f, bmax = 0.0f;
+  if (!kSigmoid || kLogit) {
+    mx = -3.402823466e38f;
 #pragma unroll
-  for (int i = 0; i < NPER; ++i) ok[i] = i < map.per && (i / V) * map.step + c * map.lane_step + i % V < E;
-  float mx = -3.402823466e38f;
-#pragma unroll
-  for (int i = 0; i < NPER; ++i) mx = fmaxf(mx, ok[i] ? v[i] : mx);
-  mx = max16(mx);
-  float sum = 1.0f;
-  float bmax = 0.0f;  // largest |bias| (softmax)
-  const bool by_logit = bias == nullptr && a.groups == 1;
-  bool unsure = false;
-  if (!a.sigmoid) {
-    sum = 0.0f;
+    for (int i = 0; i < NPER; ++i) mx = fmaxf(mx, key[i]);
+    mx = max16(mx);
+  }
+  if constexpr (!kSigmoid) {
+    float part[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
     for (int i = 0; i < NPER; ++i) {
-      key[i] = ok[i] ? __expf(v[i] - mx) : 0.0f;
-      sum += key[i];
+      const float p = __expf(key[i] - mx);
+      if constexpr (!kLogit) key[i] = p;
+      part[i & 3] += p;
     }
-    sum = fmaxf(sum16(sum), 1e-37f);
+    sum = fmaxf(sum16((part[0] + part[1]) + (part[2] + part[3])), 1e-37f);
   }
-  if (by_logit) {
-#pragma unroll
-    for (int i = 0; i < NPER; ++i) key[i] = v[i];
+  if constexpr (kLogit) {
     // fp64 sigmoids of neighbouring fp32 logits coincide above about 20
-    unsure = !(mx <= 20.0f) && a.sigmoid;
+    if (kSigmoid) hard = !(mx <= 20.0f);
   } else {
-    if (a.sigmoid) {
+    const float r = 1.0f / sum;
 #pragma unroll
-      for (int i = 0; i < NPER; ++i) key[i] = sigmoid(v[i]);
-    } else {
-      const float r = 1.0f / sum;
-#pragma unroll
-      for (int i = 0; i < NPER; ++i) key[i] *= r;
-    }
+    for (int i = 0; i < NPER; ++i) key[i] = kSigmoid ? sigmoid(key[i]) : key[i] * r;
     if (bias) {
       float b[NPER];
       load_row<NPER, V>(bias, E, map, c, b);
 #pragma unroll
       for (int i = 0; i < NPER; ++i) key[i] += b[i];
-      if (!a.sigmoid) {
+      if constexpr (!kSigmoid) {
 #pragma unroll
         for (int i = 0; i < NPER; ++i) bmax = fmaxf(bmax, fabsf(b[i]));
         bmax = max16(bmax);
       }
     }
+    mask_row<NPER, V>(E, map, c, key);
   }
   double top[kTop];
 #pragma unroll
   for (int i = 0; i < NPER; i += kTop) {
     double l[kTop];
 #pragma unroll
-    for (int j = 0; j < kTop; ++j) {
-      l[j] = -__builtin_huge_val();
-      if (i + j < NPER) {
-        const int e = ((i + j) / V) * map.step + c * map.lane_step + (i + j) % V;
-        l[j] = ok[i + j] ? pack_key(key[i + j], e) : l[j];
-      }
-    }
+    for (int j = 0; j < kTop; ++j)
+      l[j] = i + j < NPER ? pack_key(key[i + j], mapped<V>(map, c, i + j)) : -__builtin_huge_val();
     sort8(l);
     if (i == 0) {
 #pragma unroll
@@ -350,81 +427,82 @@ __global__ __launch_bounds__(256) void route_top8_kernel(ScoreArgs a, LaneMap ma
   auto tol = [&](float x) {
     constexpr float u = 5.9604645e-8f;
     x = fabsf(x);
-    if (by_logit) return 0x1p-30f * (1.0f + x);  // fp64 scores still differ by it
-    if (a.sigmoid) return 16.0f * u + 4.0f * u * x;
+    if constexpr (kLogit) return 0x1p-30f * (1.0f + x);  // fp64 scores still differ by it
+    if constexpr (kSigmoid) return 16.0f * u + 4.0f * u * x;
     return 4.0f * u + 8.0f * u * (x + bmax) + 2.0f * u * x + (NPER + 24) * u * fminf(1.0f, 2.0f * bmax);
   };
-  bool mine = true;  // this lane's experts can be taken
-  if (a.groups > 1) {
-    // a lane's experts are of one group, groups are 16 / G neighbouring lanes
-    const int span = 16 / a.groups;
-    double t1 = top[0], t2 = top[1];
-    auto join = [&](double o1, double o2) {
-      t2 = fmax(fmin(t1, o1), fmax(t2, o2));
-      t1 = fmax(t1, o1);
-    };
-    if (span > 1) join(partner<0>(t1), partner<0>(t2));
-    if (span > 2) join(partner<1>(t1), partner<1>(t2));
-    if (span > 4) join(partner<2>(t1), partner<2>(t2));
-    const float gsc = a.group_top == 2 && t2 > -1e300 ? packed_key(t1) + packed_key(t2) : packed_key(t1);
-    const int g = c / span;
-    int before = 0;
-    for (int o = 0; o < a.groups; ++o) {
-      const float s = __shfl(gsc, (lane & 48) + o * span);
-      before += (s > gsc || (s == gsc && o < g)) ? 1 : 0;
-      unsure = unsure || (o != g && fabsf(s - gsc) <= 2.0f * tol(fmaxf(fabsf(s), fabsf(gsc))));
-    }
-    mine = before < a.top_groups;
-    if (!mine) {
+  float shut = 0.0f;  // -inf where this lane's experts cannot be taken
+  if constexpr (!kLogit) {
+    if (a.groups > 1) {
+      // a lane's experts are of one group, groups are 16 / G neighbouring lanes
+      const int span = 16 / a.groups;
+      double t1 = top[0], t2 = top[1];
+      auto join = [&](double o1, double o2) {
+        t2 = max64(min64(t1, o1), max64(t2, o2));
+        t1 = max64(t1, o1);
+      };
+      if (span > 1) join(partner<0>(t1), partner<0>(t2));
+      if (span > 2) join(partner<1>(t1), partner<1>(t2));
+      if (span > 4) join(partner<2>(t1), partner<2>(t2));
+      const float gsc = a.group_top == 2 && t2 > -1e300 ? packed_key(t1) + packed_key(t2) : packed_key(t1);
+      const int g = c / span;
+      int before = 0;
+      for (int o = 0; o < a.groups; ++o) {
+        const float s = __shfl(gsc, (lane & 48) + o * span);
+        before += (s > gsc || (s == gsc && o < g)) ? 1 : 0;
+      }
+      const bool in = before < a.top_groups;
+      const float low = min16(in ? gsc : 3.402823466e38f), high = max16(in ? -3.402823466e38f : gsc);
+      hard = hard || !(low - high > 2.0f * tol(fmaxf(fabsf(low), fabsf(high))));
+      if (!in) {
+        shut = -__builtin_huge_valf();
 #pragma unroll
-      for (int j = 0; j < kTop; ++j) top[j] = -__builtin_huge_val();
+        for (int j = 0; j < kTop; ++j) top[j] = -__builtin_huge_val();
+      }
     }
   }
   merge_partner<0>(top);
   merge_partner<1>(top);
   merge_partner<2>(top);
   merge_partner<3>(top);
-  // neighbours in order, and the first one not taken: count what lies within
-  // the tolerance of the last taken key
-  float last = 0.0f;
-#pragma unroll
-  for (int j = 0; j < kTop; ++j) {
-    if (j < a.k) {
-      const float x = packed_key(top[j]);
-      if (j > 0) {
-        const float gap = last - x, w = tol(fmaxf(fabsf(last), fabsf(x)));
-        unsure = unsure || (by_logit ? gap > 0.0f && gap <= w : gap <= w);
-      }
-      last = x;
-    }
-  }
-  const float edge = last - tol(last);
-  int near = 0, equal = 0;
-#pragma unroll
-  for (int i = 0; i < NPER; ++i) {
-    near += (ok[i] & mine & (key[i] >= edge)) ? 1 : 0;
-    equal += (ok[i] & mine & (key[i] >= last)) ? 1 : 0;
-  }
-  const float n16 = sum16((float)near), e16 = sum16((float)equal);
-  // equal logits are exact ties: the index decided
-  unsure = unsure || (by_logit ? n16 != e16 : n16 != (float)a.k);
-  // fp64 scores of distant logits underflow and coincide; -inf and NaN too
-  if (by_logit) unsure = unsure || !(last >= (a.sigmoid ? -700.0f : mx - 700.0f));
-  unsure = unsure || !(fabsf(last) < 3.0e38f);
-
-  // lane c < k: the c-th selected expert and its gate
+  // `close`: neighbours in order, or the last one taken and one that is not,
+  // within the tolerance; lane c holds the c-th key
   uint32_t lo = 0, hi = 0;
 #pragma unroll
   for (int j = 0; j < kTop; ++j) {
     const uint64_t b = (uint64_t)__double_as_longlong(top[j]);
-    lo = c == j ? (uint32_t)b : lo;
-    hi = c == j ? (uint32_t)(b >> 32) : hi;
+    lo = (c & 7) == j ? (uint32_t)b : lo;
+    hi = (c & 7) == j ? (uint32_t)(b >> 32) : hi;
   }
+  const float own = packed_key(__longlong_as_double((long long)(((uint64_t)hi << 32) | lo)));
+  const float next = __uint_as_float((uint32_t)__builtin_amdgcn_update_dpp(0, (int)__float_as_uint(own), 0x101, 0xF, 0xF,
+                                                                           false));  // lane c + 1
+  const float last = __shfl(own, (lane & 48) + a.k - 1);
+  const float gap = own - next;
+  bool close = c + 1 < a.k && gap <= tol(fmaxf(fabsf(own), fabsf(next))) && !(kLogit && gap == 0.0f);
+  const float edge = last - tol(last);
+  int near = 0, equal = 0;
+#pragma unroll
+  for (int i = 0; i < NPER; ++i) {
+    near += key[i] + shut >= edge ? 1 : 0;
+    if constexpr (kLogit) equal += key[i] >= last ? 1 : 0;
+  }
+  const float n16 = sum16((float)near);
+  if constexpr (kLogit) {
+    close = close || n16 != sum16((float)equal);  // equal logits are exact ties: the index decided
+    // fp64 scores of distant logits underflow and coincide
+    hard = hard || !(last >= (kSigmoid ? -700.0f : mx - 700.0f));
+  } else {
+    close = close || n16 != (float)a.k;
+  }
+  hard = hard || !(fabsf(last) < 3.0e38f);
+
+  // lane c < k: the c-th selected expert and its gate
   const bool on = c < a.k;
   const int e = min(packed_expert(lo, hi), E - 1);
   const float l = on ? row[e] : 0.0f;
   float s;
-  if (a.sigmoid) {
+  if constexpr (kSigmoid) {
     const float x = expf(-fabsf(l)), r = 1.0f / (1.0f + x);
     s = l >= 0.0f ? r : x * r;
   } else {
@@ -432,17 +510,25 @@ __global__ __launch_bounds__(256) void route_top8_kernel(ScoreArgs a, LaneMap ma
   }
   s = on ? s : 0.0f;
   const float S = a.renorm ? sum16(s) + 1e-20f : 1.0f;
-  const uint64_t bad = ballot64(unsure);
-  const bool write = on && t0 + (lane >> 4) < a.T && ((bad >> (lane & 48)) & 0xFFFF) == 0;
-  if (write) {
+  const uint64_t closes = ballot64(close);
+  const bool token_close = ((closes >> (lane & 48)) & 0xFFFF) != 0;
+  const uint64_t hards = ballot64(hard || (token_close && n16 > 16.0f));
+  const bool token_hard = ((hards >> (lane & 48)) & 0xFFFF) != 0;
+  if (on && exists && !token_hard && !token_close) {
     topk[t * a.k + c] = e;
     gates[t * a.k + c] = s / S * a.scale;
   }
-  if (bad == 0) return;
+  if ((closes | hards) == 0) return;
+  const bool again = exists && token_close && !token_hard;
+  if (ballot64(again) != 0) {
+#pragma unroll
+    for (int i = 0; i < NPER; ++i) key[i] += shut;
+    select_close<NPER, V, kSigmoid>(a, map, row, bias, key, edge, mx, again, cand[wave], topk + t * a.k,
+                                    gates + t * a.k);
+  }
   for (int i = 0; i < 4; ++i) {
-    if (t0 + i >= a.T || ((bad >> (16 * i)) & 0xFFFF) == 0) continue;
-    select_token<NPER64>(a, logits + (t0 + i) * E, bias, keys64[threadIdx.x >> 6], topk + (t0 + i) * a.k,
-                         gates + (t0 + i) * a.k);
+    if (t0 + i >= a.T || ((hards >> (16 * i)) & 0xFFFF) == 0) continue;
+    select_token<NPER64>(a, logits + (t0 + i) * E, bias, keys64[wave], topk + (t0 + i) * a.k, gates + (t0 + i) * a.k);
   }
 }
 
@@ -537,39 +623,55 @@ __global__ __launch_bounds__(256) void route_scored_bwd_kernel(ScoreArgs a, cons
     else { CALL(16); }           \
   } while (0)
 
-template <int V>
-hipError_t launch_top8(const ScoreArgs& a, const LaneMap& m, int nper, const float* logits, const float* bias,
-                       int32_t* topk, float* gates, hipStream_t s) {
+template <int NPER, int V>
+void launch_top8(const ScoreArgs& a, const LaneMap& m, const float* logits, const float* bias, int32_t* topk,
+                 float* gates, hipStream_t s) {
   const dim3 grid((unsigned)((a.T + 15) / 16));
-#define CALL(N) route_top8_kernel<N, V><<<grid, 256, 0, s>>>(a, m, logits, bias, topk, gates)
-  if (nper <= 4) { CALL(4); }
-  else if (nper <= 8) { CALL(8); }
-  else if (nper <= 16) { CALL(16); }
-  else if (nper <= 24) { CALL(24); }
-  else if (nper <= 32) { CALL(32); }
-  else { CALL(64); }
-#undef CALL
-  return hipGetLastError();
+  const bool by_logit = !bias && a.groups == 1;
+  if (a.sigmoid) {
+    if (by_logit)
+      route_top8_kernel<NPER, V, true, true><<<grid, 256, 0, s>>>(a, m, logits, bias, topk, gates);
+    else
+      route_top8_kernel<NPER, V, true, false><<<grid, 256, 0, s>>>(a, m, logits, bias, topk, gates);
+  } else {
+    if (by_logit)
+      route_top8_kernel<NPER, V, false, true><<<grid, 256, 0, s>>>(a, m, logits, bias, topk, gates);
+    else
+      route_top8_kernel<NPER, V, false, false><<<grid, 256, 0, s>>>(a, m, logits, bias, topk, gates);
+  }
 }
 
 hipError_t launch_route_scored(const ScoreArgs& a, const float* logits, const float* bias, int32_t* topk,
                                float* gates, hipStream_t s) {
   if (a.T <= 0) return hipSuccess;
   const int64_t align = reinterpret_cast<int64_t>(logits) | reinterpret_cast<int64_t>(bias);
-  if (a.k <= kTop) {
-    const int per = (a.E + 15) / 16;
-    if (a.groups == 1) {
-      // 64 experts a load of 16 lanes
-      if (a.E % 4 == 0 && (align & 15) == 0)
-        return launch_top8<4>(a, LaneMap{64, 4, 1 << 20}, (per + 3) / 4 * 4, logits, bias, topk, gates, s);
-      return launch_top8<1>(a, LaneMap{16, 1, 1 << 20}, per, logits, bias, topk, gates, s);
+  const int per = (a.E + 15) / 16;
+  // neighbouring experts in a lane, so that a lane's are of one group
+  const bool by_lane = a.groups > 1 && 16 % a.groups == 0 && a.E % 16 == 0;
+  if (a.k <= kTop && (a.groups == 1 || by_lane)) {
+    const bool by4 = a.E % 4 == 0 && (align & 15) == 0 && (!by_lane || per % 4 == 0);
+    LaneMap m = by_lane ? LaneMap{by4 ? 4 : 1, per, per, false} : LaneMap{by4 ? 64 : 16, by4 ? 4 : 1, 1 << 20, false};
+#define CALL(N, V)                                           \
+  do {                                                       \
+    m.full = a.E == 16 * (N);                                \
+    launch_top8<N, V>(a, m, logits, bias, topk, gates, s);   \
+  } while (0)
+    // values per lane: whole loads of 4
+    const int need = by4 && !by_lane ? (per + 3) / 4 * 4 : per;
+    if (by4) {
+      if (need <= 4) CALL(4, 4);
+      else if (need <= 8) CALL(8, 4);
+      else if (need <= 16) CALL(16, 4);
+      else if (need <= 24) CALL(24, 4);
+      else if (need <= 32) CALL(32, 4);
+      else CALL(64, 4);
+    } else {
+      if (need <= 8) CALL(8, 1);
+      else if (need <= 24) CALL(24, 1);
+      else CALL(64, 1);
     }
-    if (16 % a.groups == 0 && a.E % 16 == 0) {
-      // neighbouring experts in a lane, so that a lane's are of one group
-      if (per % 4 == 0 && (align & 15) == 0)
-        return launch_top8<4>(a, LaneMap{4, per, per}, per, logits, bias, topk, gates, s);
-      return launch_top8<1>(a, LaneMap{1, per, per}, per, logits, bias, topk, gates, s);
-    }
+#undef CALL
+    return hipGetLastError();
   }
   const dim3 grid((unsigned)((a.T + 3) / 4));
 #define CALL(N) route_scored_kernel<N><<<grid, 256, 0, s>>>(a, logits, bias, topk, gates)
