@@ -351,6 +351,49 @@ __device__ __forceinline__ void select_close(const ScoreArgs& a, const LaneMap& 
   }
 }
 
+// Whether this lane's group stays, by fp64 keys: those of the lane's 4 largest
+// fp32 keys hold its two largest, unless the fifth is within their tolerance
+// (then, or where a key is no number: `unsettled`).
+template <bool kSigmoid>
+__device__ __forceinline__ bool groups64(const ScoreArgs& a, const float* __restrict__ row,
+                                         const float* __restrict__ bias, float mx, const double* top, float tol, int g,
+                                         int span, bool& unsettled) {
+  const int lane = threadIdx.x & 63, c = lane & 15;
+  double sum = 1.0;
+  if constexpr (!kSigmoid) {
+    sum = 0.0;
+    for (int j = c; j < a.E; j += 16) sum += exp((double)row[j] - (double)mx);
+    for (int d = 1; d < 16; d <<= 1) sum += shfl_xor_f64(sum, d);
+    sum = fmax(sum, 1e-300);
+  }
+  unsettled = packed_key(top[4]) + 2.0f * tol >= packed_key(top[1]) || !(packed_key(top[0]) > -3.0e38f);
+  double t1 = kNone, t2 = kNone;
+#pragma unroll
+  for (int j = 0; j < 4; ++j) {
+    const uint64_t b = (uint64_t)__double_as_longlong(top[j]);
+    const int e = min(packed_expert((uint32_t)b, (uint32_t)(b >> 32)), a.E - 1);
+    double x = score64(a, row[e], mx, sum) + (bias ? (double)bias[e] : 0.0);
+    if (!(packed_key(top[j]) > -3.0e38f)) x = kNone;
+    t2 = fmax(t2, fmin(t1, x));
+    t1 = fmax(t1, x);
+  }
+  for (int d = 1; d < span; d <<= 1) {
+    const double o1 = shfl_xor_f64(t1, d), o2 = shfl_xor_f64(t2, d);
+    t2 = fmax(fmin(t1, o1), fmax(t2, o2));
+    t1 = fmax(t1, o1);
+  }
+  const double s = a.group_top == 2 && a.E > a.groups ? t1 + t2 : t1;
+  int before = 0;
+  for (int o = 0; o < a.groups; ++o) {
+    const int from = (lane & 48) + o * span;
+    const uint64_t b = (uint64_t)__double_as_longlong(s);
+    const uint64_t lo = __shfl((uint32_t)b, from), hi = __shfl((uint32_t)(b >> 32), from);
+    const double x = __longlong_as_double((long long)(lo | (hi << 32)));
+    before += (x > s || (x == s && o < g)) ? 1 : 0;
+  }
+  return before < a.top_groups;
+}
+
 // kLogit: the logits are the keys (no bias, no groups).
 template <int NPER, int V, bool kSigmoid, bool kLogit>
 __global__ __launch_bounds__(256) void route_top8_kernel(ScoreArgs a, LaneMap map, const float* __restrict__ logits,
@@ -451,9 +494,15 @@ __global__ __launch_bounds__(256) void route_top8_kernel(ScoreArgs a, LaneMap ma
         const float s = __shfl(gsc, (lane & 48) + o * span);
         before += (s > gsc || (s == gsc && o < g)) ? 1 : 0;
       }
-      const bool in = before < a.top_groups;
+      bool in = before < a.top_groups;
       const float low = min16(in ? gsc : 3.402823466e38f), high = max16(in ? -3.402823466e38f : gsc);
-      hard = hard || !(low - high > 2.0f * tol(fmaxf(fabsf(low), fabsf(high))));
+      const bool close_groups = !(low - high > 2.0f * tol(fmaxf(fabsf(low), fabsf(high))));
+      if (ballot64(close_groups) != 0) {
+        bool unsettled;
+        const bool in64 = groups64<kSigmoid>(a, row, bias, mx, top, tol(packed_key(top[0])), g, span, unsettled);
+        in = close_groups ? in64 : in;
+        hard = hard || (close_groups && unsettled);
+      }
       if (!in) {
         shut = -__builtin_huge_valf();
 #pragma unroll
@@ -609,6 +658,79 @@ __global__ __launch_bounds__(256) void route_scored_bwd_kernel(ScoreArgs a, cons
     if (i * 64 + lane < E) d_logits[t * E + i * 64 + lane] = a.sigmoid ? out[i] : out[i] * p[i];
 }
 
+// The gradient for k <= 16 and whole 16-byte rows: 16 lanes a token, four
+// tokens to a wavefront, lane c holding the c-th selected expert and columns
+// 64 i + 4 c .. + 3 of the row.
+template <int NPER, bool kSigmoid>
+__global__ __launch_bounds__(256) void route_bwd16_kernel(ScoreArgs a, const float* __restrict__ logits,
+                                                          const int32_t* __restrict__ topk,
+                                                          const float* __restrict__ d_gates,
+                                                          float* __restrict__ d_logits) {
+  const int lane = threadIdx.x & 63, c = lane & 15;
+  const int64_t t0 = ((int64_t)blockIdx.x * 4 + (threadIdx.x >> 6)) * 4;
+  if (t0 >= a.T) return;
+  const bool exists = t0 + (lane >> 4) < a.T;
+  const int64_t t = exists ? t0 + (lane >> 4) : a.T - 1;
+  const int E = a.E;
+  const float* row = logits + t * E;
+  const int idx = c < a.k ? topk[t * a.k + c] : -1;
+  float dg = c < a.k ? d_gates[t * a.k + c] * a.scale : 0.0f;
+  const LaneMap map{64, 4, 1 << 20, false};
+  float p[kSigmoid ? 1 : NPER];
+  if constexpr (!kSigmoid) {
+    load_row<NPER, 4>(row, E, map, c, p);
+    mask_row<NPER, 4>(E, map, c, p);
+  }
+  const bool on = idx >= 0 && idx < E;
+  const float l = row[on ? idx : 0];
+  float s, rest = 0.0f, r = 1.0f;
+  if constexpr (kSigmoid) {
+    const float x = expf(-fabsf(l));
+    r = 1.0f / (1.0f + x);
+    s = on ? (l >= 0.0f ? r : x * r) : 0.0f;
+    rest = l >= 0.0f ? x * r : r;
+  } else {
+    float mx = -3.402823466e38f, sum = 0.0f;
+#pragma unroll
+    for (int i = 0; i < NPER; ++i) mx = fmaxf(mx, p[i]);
+    mx = max16(mx);
+#pragma unroll
+    for (int i = 0; i < NPER; ++i) {
+      p[i] = expf(p[i] - mx);
+      sum += p[i];
+    }
+    r = 1.0f / fmaxf(sum16(sum), 1e-37f);
+    s = on ? expf(l - mx) * r : 0.0f;
+  }
+  if (!on) dg = 0.0f;
+  float ds = dg;
+  if (a.renorm) {
+    const float S = sum16(s) + 1e-20f, dot = sum16(dg * s);  // over all 16 lanes: not inside the selection
+    ds = on ? (dg - dot / S) / S : 0.0f;
+  }
+  const float val = kSigmoid ? ds * s * rest : ds;
+  const float base = kSigmoid ? 0.0f : sum16(ds * s);
+  float out[NPER];
+#pragma unroll
+  for (int i = 0; i < NPER; ++i) out[i] = -base;
+  const int from = lane & 48;
+  for (int j = 0; j < a.k; ++j) {
+    const int e = __shfl(on ? idx : -1, from + j);
+    const float x = __shfl(val, from + j);
+    const int d = e - 4 * c;  // 64 i + q where the expert is this lane's
+#pragma unroll
+    for (int i = 0; i < NPER; ++i) out[i] += d == (i / 4) * 64 + i % 4 ? x : 0.0f;
+  }
+  if (!exists) return;
+#pragma unroll
+  for (int i = 0; i < NPER; i += 4) {
+    const int e = mapped<4>(map, c, i);
+    f32x4_t v = {out[i], out[i + 1], out[i + 2], out[i + 3]};
+    if constexpr (!kSigmoid) v *= f32x4_t{p[i], p[i + 1], p[i + 2], p[i + 3]} * r;
+    if (e < E) *reinterpret_cast<f32x4_t*>(d_logits + t * E + e) = v;
+  }
+}
+
 }  // namespace
 
 // f(NPER) with the smallest instantiated NPER >= ceil(E / 64)
@@ -683,6 +805,25 @@ hipError_t launch_route_scored(const ScoreArgs& a, const float* logits, const fl
 hipError_t launch_route_scored_bwd(const ScoreArgs& a, const float* logits, const int32_t* topk,
                                    const float* d_gates, float* d_logits, hipStream_t s) {
   if (a.T <= 0) return hipSuccess;
+  const int64_t align = reinterpret_cast<int64_t>(logits) | reinterpret_cast<int64_t>(d_logits);
+  if (a.k <= 16 && a.E % 4 == 0 && (align & 15) == 0) {
+    const dim3 grid((unsigned)((a.T + 15) / 16));
+#define CALL(N)                                                                               \
+  do {                                                                                        \
+    if (a.sigmoid)                                                                            \
+      route_bwd16_kernel<N, true><<<grid, 256, 0, s>>>(a, logits, topk, d_gates, d_logits);   \
+    else                                                                                      \
+      route_bwd16_kernel<N, false><<<grid, 256, 0, s>>>(a, logits, topk, d_gates, d_logits);  \
+  } while (0)
+    if (a.E <= 64) CALL(4);
+    else if (a.E <= 128) CALL(8);
+    else if (a.E <= 256) CALL(16);
+    else if (a.E <= 384) CALL(24);
+    else if (a.E <= 512) CALL(32);
+    else CALL(64);
+#undef CALL
+    return hipGetLastError();
+  }
   const dim3 grid((unsigned)((a.T + 3) / 4));
 #define CALL(N) route_scored_bwd_kernel<N><<<grid, 256, 0, s>>>(a, logits, topk, d_gates, d_logits)
   MOE_BY_EXPERTS(a.E, CALL);
