@@ -18,30 +18,75 @@ constexpr int kRun = 16;             // values per thread and block
 constexpr int kLanes = kQB / kRun;   // lanes per row of a block
 constexpr int kGroups = 256 / kLanes;  // rows a workgroup takes at once
 
-// 16 values of the source, as loaded.
+// 16 bytes at an address that is a multiple of kAlign (2 or 4).  No
+// nontemporal hint, though each byte is read once: neighbouring loads share
+// lines, and with the hint each fetches its own (8192 x 4096 fp32: 42 us with
+// it, 26 without).
+typedef u32x4_t u32x4_by2_t __attribute__((aligned(2)));
+typedef u32x4_t u32x4_by4_t __attribute__((aligned(4)));
+template <int kAlign>
+__device__ __forceinline__ uint4 ld16_any(const char* p) {
+  using any_t = std::conditional_t<kAlign == 2, u32x4_by2_t, u32x4_by4_t>;
+  const u32x4_t v = *reinterpret_cast<const any_t*>(p);
+  return make_uint4(v.x, v.y, v.z, v.w);
+}
+
+// 16 values of the source, as loaded: 16-byte loads whatever the rows'
+// alignment (global memory takes any; a row that starts off a 16-byte
+// boundary costs little beside loads of single values).
 template <typename T>
 struct Run {
   static constexpr int kChunks = kRun * (int)sizeof(T) / 16;
   uint4 v[kChunks];
 
-  // inside: 16-byte aligned and every value exists
   __device__ __forceinline__ void load(const char* p) {
 #pragma unroll
-    for (int i = 0; i < kChunks; ++i) v[i] = ld16_stream(p + i * 16);
+    for (int i = 0; i < kChunks; ++i) v[i] = ld16_any<(int)sizeof(T)>(p + i * 16);
   }
-  // n values exist (0 .. 16, any alignment of T); the rest are zeros
-  __device__ __forceinline__ void load_edge(const char* p, int n) {
-    uint32_t w[kChunks * 4] = {};
+  // n values exist (0 .. 16); the rest are zeros.  The 16 bytes are loaded
+  // whole wherever they lie inside [any, end), the source's first byte and
+  // end (past a row's last value lie the next row's, which are cleared): only
+  // the source's last bytes are loaded one by one, and none of those loads
+  // stands behind a branch of its own (past the end the last value again, or
+  // where there is none, the source's first).
+  __device__ __forceinline__ void load_edge(const char* p, int n, const char* any, const char* end_) {
+    const char* w = n > 0 ? p : any;
+    if (w + kRun * (int)sizeof(T) <= end_) {
+      load(w);
+      constexpr int kPer = 4 / (int)sizeof(T);  // values per word
 #pragma unroll
-    for (int i = 0; i < kRun; ++i)
-      if (i < n) {
-        if constexpr (sizeof(T) == 4)
-          w[i] = reinterpret_cast<const uint32_t*>(p)[i];
-        else
-          w[i / 2] |= (uint32_t)reinterpret_cast<const uint16_t*>(p)[i] << (16 * (i & 1));
+      for (int i = 0; i < kChunks; ++i) {
+        uint32_t x[4] = {v[i].x, v[i].y, v[i].z, v[i].w};
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          const int first = (4 * i + j) * kPer;
+          x[j] = n >= first + kPer ? x[j] : n <= first ? 0u : x[j] & 0xFFFFu;
+        }
+        v[i] = make_uint4(x[0], x[1], x[2], x[3]);
       }
+      return;
+    }
+    const char* q = n > 0 ? p : any;
+    const int end = n > 0 ? n - 1 : 0;
+    uint32_t x[kRun];
 #pragma unroll
-    for (int i = 0; i < kChunks; ++i) v[i] = make_uint4(w[4 * i], w[4 * i + 1], w[4 * i + 2], w[4 * i + 3]);
+    for (int i = 0; i < kRun; ++i) {
+      if constexpr (sizeof(T) == 4)
+        x[i] = reinterpret_cast<const uint32_t*>(q)[min(i, end)];
+      else
+        x[i] = reinterpret_cast<const uint16_t*>(q)[min(i, end)];
+    }
+#pragma unroll
+    for (int i = 0; i < kRun; ++i) x[i] = i < n ? x[i] : 0u;
+    if constexpr (sizeof(T) == 4) {
+#pragma unroll
+      for (int i = 0; i < kChunks; ++i) v[i] = make_uint4(x[4 * i], x[4 * i + 1], x[4 * i + 2], x[4 * i + 3]);
+    } else {
+#pragma unroll
+      for (int i = 0; i < kChunks; ++i)
+        v[i] = make_uint4(x[8 * i] | x[8 * i + 1] << 16, x[8 * i + 2] | x[8 * i + 3] << 16,
+                          x[8 * i + 4] | x[8 * i + 5] << 16, x[8 * i + 6] | x[8 * i + 7] << 16);
+    }
   }
   __device__ __forceinline__ void values(float* f) const {
 #pragma unroll
@@ -60,7 +105,7 @@ struct Run {
 struct Source {
   const char* x;
   int64_t rows, cols, ld;  // elements
-  bool aligned;            // base and rows 16-byte aligned
+  const char* end;         // behind the last value
 };
 
 // Largest over the 8 lanes of a block's row (lanes 8 g .. 8 g + 7).
@@ -90,14 +135,14 @@ __global__ __launch_bounds__(256) void quantize_rows_kernel(Source s, char* __re
   const int64_t row = r0 + g, col = k0 + c * kRun;
   const char* p = s.x + (row * s.ld + col) * (int64_t)sizeof(T);
   Run<T> v[NB];
-  if (s.aligned && r0 + kGroups <= s.rows && k0 + NB * kQB <= s.cols) {
+  if (r0 + kGroups <= s.rows && k0 + NB * kQB <= s.cols) {
 #pragma unroll
     for (int i = 0; i < NB; ++i) v[i].load(p + i * (kQB * (int)sizeof(T)));
   } else {
 #pragma unroll
     for (int i = 0; i < NB; ++i) {
       const int64_t left = row < s.rows ? s.cols - (col + i * kQB) : 0;
-      v[i].load_edge(p + i * (kQB * (int)sizeof(T)), (int)max(min(left, (int64_t)kRun), (int64_t)0));
+      v[i].load_edge(p + i * (kQB * (int)sizeof(T)), (int)max(min(left, (int64_t)kRun), (int64_t)0), s.x, s.end);
     }
   }
 #pragma unroll
@@ -127,21 +172,23 @@ __global__ __launch_bounds__(256) void quantize_tile_kernel(Source s, char* __re
                                                             float* __restrict__ scale, int64_t scale_ld, int tiles_k) {
   static_assert(kSquare || kTranspose, "1 x 128 blocks that are not transposed have a kernel of their own");
   __shared__ uint32_t tile[kTranspose ? kQB * kTLd : 1];
-  __shared__ float part[4][kSquare ? 1 : kQB];
+  // kSquare: maxima of the wavefronts; else column maxima of the 16 groups of
+  // 8 rows, then (row 0) of the tile
+  __shared__ __attribute__((aligned(16))) float part[kSquare ? 4 : 16][kSquare ? 1 : kQB];
   const int tr = blockIdx.x / tiles_k, tk = blockIdx.x - tr * tiles_k;
   const int g = threadIdx.x / kLanes, c = threadIdx.x % kLanes, wave = threadIdx.x >> 6;
   const int64_t r0 = (int64_t)tr * kQB, k0 = (int64_t)tk * kQB;
   const int64_t col = k0 + c * kRun;
   const char* p = s.x + ((r0 + g * 4) * s.ld + col) * (int64_t)sizeof(T);
   Run<T> v[4];
-  if (s.aligned && r0 + kQB <= s.rows && k0 + kQB <= s.cols) {
+  if (r0 + kQB <= s.rows && k0 + kQB <= s.cols) {
 #pragma unroll
     for (int i = 0; i < 4; ++i) v[i].load(p + i * s.ld * (int64_t)sizeof(T));
   } else {
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
       const int64_t left = r0 + g * 4 + i < s.rows ? s.cols - col : 0;
-      v[i].load_edge(p + i * s.ld * (int64_t)sizeof(T), (int)max(min(left, (int64_t)kRun), (int64_t)0));
+      v[i].load_edge(p + i * s.ld * (int64_t)sizeof(T), (int)max(min(left, (int64_t)kRun), (int64_t)0), s.x, s.end);
     }
   }
   uint4 w[4];  // bytes of row i
@@ -161,7 +208,7 @@ __global__ __launch_bounds__(256) void quantize_tile_kernel(Source s, char* __re
     if (threadIdx.x == 0) scale[kTranspose ? (k0 / kQB) * scale_ld + r0 / kQB : (r0 / kQB) * scale_ld + k0 / kQB] = block_scale(m);
   } else {
     // a block is a column of the tile: its largest over the thread's rows,
-    // the wavefront's 8 row groups, then the 4 wavefronts
+    // its neighbour 8 lanes on, then over LDS
     float m[kRun];
 #pragma unroll
     for (int j = 0; j < kRun; ++j) m[j] = 0.0f;
@@ -173,16 +220,26 @@ __global__ __launch_bounds__(256) void quantize_tile_kernel(Source s, char* __re
       for (int j = 0; j < kRun; ++j) m[j] = fmaxf(m[j], fabsf(f[j]));
     }
 #pragma unroll
-    for (int j = 0; j < kRun; ++j) {
-      for (int d = kLanes; d < 64; d <<= 1) m[j] = fmaxf(m[j], __shfl_xor(m[j], d));
-      if ((threadIdx.x & 63) < kLanes) part[wave][c * kRun + j] = m[j];
+    for (int j = 0; j < kRun; ++j)  // rotation by 8 within 16 lanes
+      m[j] = fmaxf(m[j], __int_as_float(__builtin_amdgcn_update_dpp(0, __float_as_int(m[j]), 0x128, 0xF, 0xF, false)));
+    if ((threadIdx.x & 15) < kLanes) {
+      f32x4_t* to = reinterpret_cast<f32x4_t*>(&part[threadIdx.x >> 4][c * kRun]);
+#pragma unroll
+      for (int j = 0; j < 4; ++j) to[j] = f32x4_t{m[4 * j], m[4 * j + 1], m[4 * j + 2], m[4 * j + 3]};
+    }
+    __syncthreads();
+    if (threadIdx.x < kQB) {
+      float x = kQuantTiny;
+#pragma unroll
+      for (int i = 0; i < 16; ++i) x = fmaxf(x, part[i][threadIdx.x]);
+      part[0][threadIdx.x] = x;
+      if (k0 + threadIdx.x < s.cols) scale[(r0 / kQB) * scale_ld + k0 + threadIdx.x] = block_scale(x);
     }
     __syncthreads();
 #pragma unroll
     for (int j = 0; j < kRun; ++j) {
       const int n = c * kRun + j;
-      const float amax = fmaxf(fmaxf(fmaxf(part[0][n], part[1][n]), fmaxf(part[2][n], part[3][n])), kQuantTiny);
-      const BlockQuant bq(amax);
+      const BlockQuant bq(part[0][n]);
       float x[4];
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
@@ -191,7 +248,6 @@ __global__ __launch_bounds__(256) void quantize_tile_kernel(Source s, char* __re
         x[i] = bq(f[j]);
       }
       tile[n * kTLd + g] = e4m3_quad(x[0], x[1], x[2], x[3]);
-      if (g == 0 && k0 + n < s.cols) scale[(r0 / kQB) * scale_ld + k0 + n] = block_scale(amax);
     }
   }
   if constexpr (!kTranspose) {
@@ -227,8 +283,8 @@ __global__ __launch_bounds__(256) void quantize_tile_kernel(Source s, char* __re
 
 template <typename T>
 hipError_t launch_typed(const QuantizeArgs& a, hipStream_t st) {
-  Source s{static_cast<const char*>(a.x), a.rows, a.cols, a.ld, false};
-  s.aligned = (reinterpret_cast<uintptr_t>(a.x) & 15) == 0 && (a.ld * (int64_t)sizeof(T)) % 16 == 0;
+  const char* x = static_cast<const char*>(a.x);
+  const Source s{x, a.rows, a.cols, a.ld, x + ((a.rows - 1) * a.ld + a.cols) * (int64_t)sizeof(T)};
   const int64_t tk = (a.cols + kQB - 1) / kQB;
   if (a.block_rows == 1 && !a.transpose) {
     // blocks per thread: as many as leave every CU a few workgroups; 64
