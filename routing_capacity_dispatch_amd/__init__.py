@@ -35,12 +35,9 @@ def library():
 def make_config(T, d_model, d_latent, n_experts, n_pools, top_k, d_ff, n_shared=0,
                 d_ff_shared=0, n_waves=3, dtype="bf16", send_cap=(11, 10), recv_cap=(23, 20),
                 cap_send_rows=0, cap_recv_rows=0) -> abi.MoeConfig:
-    return abi.MoeConfig(
-        T=T, d_model=d_model, d_latent=d_latent, n_experts=n_experts, n_pools=n_pools,
-        top_k=top_k, d_ff=d_ff, n_shared=n_shared, d_ff_shared=d_ff_shared, n_waves=n_waves,
-        send_cap_num=send_cap[0], send_cap_den=send_cap[1], recv_cap_num=recv_cap[0],
-        recv_cap_den=recv_cap[1], cap_send_rows=cap_send_rows, cap_recv_rows=cap_recv_rows,
-        dtype=_DT[dtype], reserved=0)
+    # in the order of the fields
+    return abi.MoeConfig(T, d_model, d_latent, n_experts, n_pools, top_k, d_ff, n_shared, d_ff_shared, n_waves,
+                         send_cap[0], send_cap[1], recv_cap[0], recv_cap[1], cap_send_rows, cap_recv_rows, _DT[dtype], 0)
 
 
 def config_of(w, **over) -> abi.MoeConfig:
@@ -539,31 +536,42 @@ def _rows(t, shape, dtype, what, dev=None):
     return t
 
 
-class _on:
-    """The tensors' device, made current for the call where it is not."""
+def _workspace(ws, nbytes, dev):
+    """The caller's workspace (bytes on the tensors' device), or a new one."""
+    if ws is None:
+        return _ws(nbytes, dev)
+    if not (ws.dtype == torch.uint8 and ws.device == dev and ws.is_contiguous()):
+        raise ValueError(f"ws must be a contiguous uint8 tensor on {dev}")
+    return ws
 
-    def __init__(self, dev):
-        self.dev, self.prev = dev, None
 
-    def __enter__(self):
-        cur = torch.cuda.current_device()
-        if cur != self.dev.index:
-            self.prev = cur
-            torch.cuda.set_device(self.dev)
-        return C.c_void_p(torch.cuda.current_stream(self.dev).cuda_stream)
+# raw handle of the current stream of a device: torch's own accessor where it
+# has one (a Stream object costs a microsecond per call)
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or \
+    (lambda index: torch.cuda.current_stream(index).cuda_stream)
 
-    def __exit__(self, *exc):
-        if self.prev is not None:
-            torch.cuda.set_device(self.prev)
-        return False
+
+def _launch(name, dev, *args):
+    """Call a C entry point on the tensors' device (made current for the call
+    where it is not) and its current stream."""
+    index = dev.index
+    prev = torch.cuda.current_device()
+    if prev != index:
+        torch.cuda.set_device(index)
+    try:
+        status = getattr(library(), name)(*args, _raw_stream(index))
+    finally:
+        if prev != index:
+            torch.cuda.set_device(prev)
+    if status:
+        raise MoeError(name, status)
 
 
 def scoring(score="sigmoid", n_groups=1, top_groups=1, group_top=2, renormalise=True, scale=1.0) -> abi.MoeScoring:
     """How route_scored makes scores, limits groups and scales gates (moe_scoring)."""
     _check(score in ("sigmoid", "softmax"), "score is 'sigmoid' or 'softmax'")
-    return abi.MoeScoring(score=abi.MOE_SCORE_SIGMOID if score == "sigmoid" else abi.MOE_SCORE_SOFTMAX,
-                          n_groups=n_groups, top_groups=top_groups, group_top=group_top,
-                          renormalise=int(bool(renormalise)), scale=scale, reserved=0)
+    return abi.MoeScoring(abi.MOE_SCORE_SIGMOID if score == "sigmoid" else abi.MOE_SCORE_SOFTMAX, n_groups, top_groups,
+                          group_top, int(bool(renormalise)), scale, 0)
 
 
 def route_scored(cfg, sc: abi.MoeScoring, logits: torch.Tensor, bias: Optional[torch.Tensor] = None, out=None):
@@ -576,9 +584,8 @@ def route_scored(cfg, sc: abi.MoeScoring, logits: torch.Tensor, bias: Optional[t
         _rows(out["topk_idx"], (T, k), torch.int32, "out['topk_idx']", dev)
     gates = torch.empty((T, k), dtype=torch.float32, device=dev) if out is None else \
         _rows(out["gates"], (T, k), torch.float32, "out['gates']", dev)
-    with _on(dev) as stream:
-        abi.check("moe_route_scored", library().moe_route_scored(
-            C.byref(cfg), C.byref(sc), _ptr(logits), _ptr(bias), _ptr(topk), _ptr(gates), stream))
+    _launch("moe_route_scored", dev, C.byref(cfg), C.byref(sc), logits.data_ptr(),
+            None if bias is None else bias.data_ptr(), topk.data_ptr(), gates.data_ptr())
     return topk, gates
 
 
@@ -590,9 +597,8 @@ def route_scored_backward(cfg, sc: abi.MoeScoring, logits, topk_idx, d_gates, d_
     _rows(d_gates, (T, k), torch.float32, "d_gates", dev)
     d_logits = torch.empty_like(logits) if d_logits is None else \
         _rows(d_logits, (T, E), torch.float32, "d_logits", dev)
-    with _on(dev) as stream:
-        abi.check("moe_route_scored_backward", library().moe_route_scored_backward(
-            C.byref(cfg), C.byref(sc), _ptr(logits), _ptr(topk_idx), _ptr(d_gates), _ptr(d_logits), stream))
+    _launch("moe_route_scored_backward", dev, C.byref(cfg), C.byref(sc), logits.data_ptr(), topk_idx.data_ptr(),
+            d_gates.data_ptr(), d_logits.data_ptr())
     return d_logits
 
 
@@ -617,9 +623,8 @@ def quantize(x: torch.Tensor, block_rows: int = 1, transpose: bool = False, out=
         _rows(out[0], qs, torch.float8_e4m3fn, "out[0]", dev)
     s = torch.empty(ss, dtype=torch.float32, device=dev) if out is None else \
         _rows(out[1], ss, torch.float32, "out[1]", dev)
-    with _on(dev) as stream:
-        abi.check("moe_quantize", library().moe_quantize(
-            rows, cols, _ptr(x), ld, _DT[x.dtype], block_rows, int(transpose), _ptr(q), _ptr(s), stream))
+    _launch("moe_quantize", dev, rows, cols, x.data_ptr(), ld, _DT[x.dtype], block_rows, int(transpose), q.data_ptr(),
+            s.data_ptr())
     return q, s
 
 
@@ -658,18 +663,16 @@ def gemm_quant(a, a_scales, b, b_scales, block_rows: int = 128, out_dtype=torch.
         _check(out.shape == (M, N) and out.dtype == out_dtype and out.device == dev
                and (N <= 1 or out.stride(1) == 1) and (M <= 1 or out.stride(0) >= N),
                "out must be a tensor of C's shape and type with contiguous columns")
-    g = abi.MoeQuantGemm(M=M, N=N, K=K, a=a.data_ptr(), lda=lda, a_scale=a_scales.data_ptr(), a_scale_ld=sa,
-                         b=b.data_ptr(), ldb=ldb, b_scale=b_scales.data_ptr(), b_scale_ld=sb, c=out.data_ptr(),
-                         ldc=out.stride(0) if M > 1 else N, b_block_rows=block_rows, out_dtype=_DT[out_dtype],
-                         reserved=0)
+    g = abi.MoeQuantGemm(M, N, K, a.data_ptr(), lda, a_scales.data_ptr(), sa, b.data_ptr(), ldb, b_scales.data_ptr(),
+                         sb, out.data_ptr(), out.stride(0) if M > 1 else N, block_rows, _DT[out_dtype], 0)
     lib = library()
     n = C.c_size_t(0)
     abi.check("moe_gemm_quant_ws_bytes", lib.moe_gemm_quant_ws_bytes(C.byref(g), C.byref(n)))
-    if ws is None and n.value:
-        ws = _ws(n.value, dev)
-    with _on(dev) as stream:
-        abi.check("moe_gemm_quant", lib.moe_gemm_quant(
-            C.byref(g), _ptr(ws), ws.numel() if ws is not None else 0, stream))
+    if n.value:
+        ws = _workspace(ws, n.value, dev)
+        _launch("moe_gemm_quant", dev, C.byref(g), ws.data_ptr(), ws.numel())
+    else:
+        _launch("moe_gemm_quant", dev, C.byref(g), None, 0)
     return out
 
 
@@ -699,10 +702,7 @@ def experts_dropless_quant(cfg, xs, expert_offsets, w_gate, w_up, w_down, expert
     w = _quant_experts(cfg, w_gate, w_up, w_down, dev)
     expert_out = torch.empty_like(xs) if expert_out is None else \
         _rows(expert_out, (n, L), torch.bfloat16, "expert_out", dev)
-    if ws is None:
-        ws = _ws(nbytes, dev)
-    with _on(dev) as stream:
-        abi.check("moe_experts_dropless_quant", library().moe_experts_dropless_quant(
-            C.byref(cfg), _ptr(xs), _ptr(expert_offsets), C.byref(w), _ptr(expert_out), _ptr(ws), ws.numel(),
-            stream))
+    ws = _workspace(ws, nbytes, dev)
+    _launch("moe_experts_dropless_quant", dev, C.byref(cfg), xs.data_ptr(), expert_offsets.data_ptr(), C.byref(w),
+            expert_out.data_ptr(), ws.data_ptr(), ws.numel())
     return expert_out
