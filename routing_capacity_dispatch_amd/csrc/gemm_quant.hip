@@ -380,18 +380,39 @@ __global__ __launch_bounds__(64 * kSkinnyWaves) void few_rows_kernel(FewRows g) 
 // scales come with it: one float per tile row of A and of B.
 using core::load_col;
 using core::load_row;
-using core::lds_load16;
-using core::RowSrc;
 using core::uniform_ptr;
 
 enum Mode { kBlockB = 0, kRowB = 1, kGateUp = 2 };
 
-// 4 bytes per lane, global -> LDS: lane l's dword lands at lds_wave_base + 4 l.
-__device__ __forceinline__ void lds_load4(const float* p, char* lds_wave_base) {
-  const uint32_t l = __builtin_amdgcn_readfirstlane(
-      static_cast<uint32_t>(reinterpret_cast<uintptr_t>((MOE_LDS char*)lds_wave_base)));
-  asm volatile("s_mov_b32 m0, %0\n\tglobal_load_lds_dword %1, off" ::"s"(l), "v"(p) : "memory", "m0");
+// Global -> LDS loads of 16 or 4 bytes per lane (lane l's at lds + off + 16 l
+// or 4 l): two instructions each, so that they fit between MFMAs.  Inline
+// assembly for the reason given at core::lds_load16: the loop waits for them
+// itself.
+__device__ __forceinline__ uint32_t lds_address(const void* p) {
+  return __builtin_amdgcn_readfirstlane(static_cast<uint32_t>(reinterpret_cast<uintptr_t>((MOE_LDS const char*)p)));
 }
+template <int kOff>
+__device__ __forceinline__ void stage16(uint32_t lds, const char* sbase, uint32_t voff) {
+  asm volatile("s_add_u32 m0, %0, %3\n\tglobal_load_lds_dwordx4 %1, %2" ::"s"(lds), "v"(voff), "s"(sbase), "n"(kOff)
+               : "memory", "m0", "scc");
+}
+template <int kOff>
+__device__ __forceinline__ void stage4(uint32_t lds, const float* p) {
+  asm volatile("s_add_u32 m0, %0, %2\n\tglobal_load_lds_dword %1, off" ::"s"(lds), "v"(p), "n"(kOff)
+               : "memory", "m0", "scc");
+}
+
+// What a wavefront stages per block: rows of A and of B (one base each, wave-
+// uniform, and per-lane offsets that also pick the swizzled chunk), and one
+// scale per lane.
+template <class TL>
+struct Stager {
+  const char* a;
+  const char* b;
+  const float* s;
+  int64_t s_step;
+  uint32_t a_off[TL::A_INS], b_off[TL::B_INS];
+};
 
 template <class TL>
 struct QTile : TL {
@@ -407,14 +428,23 @@ struct QTile : TL {
 // packed stores, and row maxima partly inside a lane.
 constexpr int kMB = 16;  // rows and columns of an instruction's result
 
+// f(0), f(1), ... with the index as a compile-time constant.
+template <int I, int N, class F>
+__device__ __forceinline__ void for_range(F&& f) {
+  if constexpr (I < N) {
+    f(std::integral_constant<int, I>{});
+    for_range<I + 1, N>(f);
+  }
+}
+
 template <class TL>
 struct QAcc {
   static constexpr int MI = TL::WM / kMB, NI = TL::WN / kMB;
   f32x4_t v[MI][NI];
 };
 
-// Sum over K blocks [0, nb).  sp: this lane's scale of block 0, s_step floats
-// to the next.  The steps of consecutive blocks run into one another, so that
+// Sum over K blocks [0, nb).  The steps of consecutive blocks run into one
+// another, so that
 // the matrix cores always have operands in registers: while the MFMAs of one
 // row block run, the fragment of the next is read from LDS, and the results
 // before are scaled and added.  At the last row block every read of this
@@ -423,8 +453,7 @@ struct QAcc {
 // go in among its MFMAs, each B fragment into the registers that its last
 // MFMA has just read.  Ends with a barrier, so the caller may reuse the LDS.
 template <class TL, int kMode, bool kWide>
-__device__ __forceinline__ void quant_pipe(const RowSrc<TL::A_INS>& a, const RowSrc<TL::B_INS>& b, const float* sp,
-                                           int64_t s_step, int nb, char* lds, QAcc<TL>& acc) {
+__device__ __forceinline__ void quant_pipe(Stager<TL>& src, int nb, char* lds, QAcc<TL>& acc) {
   using Q = QTile<TL>;
   constexpr int MI = QAcc<TL>::MI, NI = QAcc<TL>::NI, NM = MI * NI;
   constexpr int kLag = 2;
@@ -435,18 +464,28 @@ __device__ __forceinline__ void quant_pipe(const RowSrc<TL::A_INS>& a, const Row
 #pragma unroll
     for (int ni = 0; ni < NI; ++ni) acc.v[mi][ni] = f32x4_t{0.f, 0.f, 0.f, 0.f};
   if (nb <= 0) return;
-  // one load instruction of a block: A rows, B rows, scales
+  // load instruction i of the next block, into stage st: A rows, B rows, scales
   constexpr int P = TL::A_INS + TL::B_INS + 1;
-  auto issue = [&](int kb, int i) {
-    const int st = kb & 1;
-    if (i < TL::A_INS)
-      lds_load16(a.base[i] + (int64_t)kb * kQB, a.off[i], lds + st * TL::A_BYTES + (i * TL::NW + wave) * 1024);
-    else if (i < TL::A_INS + TL::B_INS)
-      lds_load16(b.base[i - TL::A_INS] + (int64_t)kb * kQB, b.off[i - TL::A_INS],
-                 lds + TL::B_BASE + st * TL::B_BYTES + ((i - TL::A_INS) * TL::NW + wave) * 1024);
-    else
-      lds_load4(sp + kb * s_step, lds + Q::S_BASE + (st * Q::SCALES + wave * 64) * 4);
+  const uint32_t lds_rows = lds_address(lds + wave * 1024);
+  const uint32_t lds_scales = lds_address(lds + Q::S_BASE + wave * 256);
+  auto issue = [&](int st, auto ins) {
+    constexpr int i = decltype(ins)::value;
+    if constexpr (i < TL::A_INS) {
+      stage16<i * TL::NW * 1024>(lds_rows + st * TL::A_BYTES, src.a, src.a_off[i]);
+    } else if constexpr (i < TL::A_INS + TL::B_INS) {
+      stage16<TL::B_BASE + (i - TL::A_INS) * TL::NW * 1024>(lds_rows + st * TL::B_BYTES, src.b, src.b_off[i - TL::A_INS]);
+    } else {
+      stage4<0>(lds_scales + st * Q::SCALES * 4, src.s);
+      src.a += kQB;
+      src.b += kQB;
+      src.s += src.s_step;
+    }
   };
+  auto issue_range = [&](int st, auto first, auto last) {
+    constexpr int i0 = decltype(first)::value, i1 = decltype(last)::value;
+    for_range<i0, i1>([&](auto i) { issue(st, i); });
+  };
+  using std::integral_constant;
   // fragment addresses inside a stage: the swizzle depends on the lane only,
   // so row blocks are immediate offsets
   const int sw = TL::swz(lane & 15);
@@ -474,12 +513,9 @@ __device__ __forceinline__ void quant_pipe(const RowSrc<TL::A_INS>& a, const Row
 #pragma unroll
     for (int i = 0; i < NBS; ++i) v[i] = *reinterpret_cast<const BScale*>(bsb + (st * Q::SCALES + i * kMB) * 4);
   };
-#pragma unroll
-  for (int i = 0; i < P; ++i) issue(0, i);
+  issue_range(0, integral_constant<int, 0>{}, integral_constant<int, P>{});
   core::wait_loads<0>();
-  if (nb > 1)
-#pragma unroll
-    for (int i = 0; i < P; ++i) issue(1, i);
+  if (nb > 1) issue_range(1, integral_constant<int, 0>{}, integral_constant<int, P>{});
   Frag8 fb[NI], fa[2];
   float as[2];
   BScale bs[NBS], bs_next[NBS];
@@ -503,6 +539,10 @@ __device__ __forceinline__ void quant_pipe(const RowSrc<TL::A_INS>& a, const Row
     }
     f32x4_t p[kLag + 1];
     float sc[2][2];  // this row block's scale, times each of B's
+    Wide wb[kWide ? NI : 1];  // widened once per block, used by every row block
+    if constexpr (kWide)
+#pragma unroll
+      for (int ni = 0; ni < NI; ++ni) wb[ni] = widen(fb[ni]);
     auto add = [&](int j) {
       const int mi = j / NI, ni = j % NI;
 #pragma unroll
@@ -531,23 +571,21 @@ __device__ __forceinline__ void quant_pipe(const RowSrc<TL::A_INS>& a, const Row
       }
       Wide wa;
       if constexpr (kWide) wa = widen(fa[mi & 1]);
-#pragma unroll
-      for (int ni = 0; ni < NI; ++ni) {
+      for_range<0, NI>([&](auto col) {
+        constexpr int ni = decltype(col)::value;
         const int j = mi * NI + ni;
         if constexpr (kWide)
-          p[j % (kLag + 1)] = mfma_block(widen(fb[ni]), wa);
+          p[j % (kLag + 1)] = mfma_block(wb[ni], wa);
         else
           p[j % (kLag + 1)] = mfma_block(fb[ni], fa[mi & 1]);
         if (last) {
           if (more) fb[ni] = read_b(st ^ 1, ni);
-          if (more2)
-#pragma unroll
-            for (int i = 0; i < P; ++i)
-              if (i * NI / P == ni) issue(kb + 2, i);
+          // the block after next: instructions [ni P / NI, (ni + 1) P / NI)
+          if (more2) issue_range(st, integral_constant<int, ni * P / NI>{}, integral_constant<int, (ni + 1) * P / NI>{});
         }
         if (j >= kLag) add(j - kLag);
         __builtin_amdgcn_sched_barrier(0);
-      }
+      });
     }
 #pragma unroll
     for (int j = NM - kLag; j < NM; ++j) add(j);
@@ -649,35 +687,28 @@ __global__ __launch_bounds__(TL::THREADS) void product_kernel(QuantGemm g, int t
     kb0 = min((int)blockIdx.y * per, nb);
     nb = min(per, nb - kb0);
   }
-  RowSrc<TL::A_INS> a;
-  RowSrc<TL::B_INS> b;
-  const char* A = uniform_ptr(g.A + (row0 + m0) * g.lda + (int64_t)kb0 * kQB);
-  const char* B = uniform_ptr(g.B + e * g.b_stride + n0 * g.ldb + (int64_t)kb0 * kQB);
+  Stager<TL> src;
+  src.a = uniform_ptr(g.A + (row0 + m0) * g.lda + (int64_t)kb0 * kQB);
+  src.b = uniform_ptr(g.B + e * g.b_stride + n0 * g.ldb + (int64_t)kb0 * kQB);
   const int mlast = (int)min(rows - m0 - 1, (int64_t)TL::BM), nlast = (int)min(g.N - n0 - 1, (int64_t)TL::BN);
 #pragma unroll
-  for (int i = 0; i < TL::A_INS; ++i) {
-    a.base[i] = A;
-    a.off[i] = (uint32_t)(min(load_row<TL>(i, wave, lane), mlast) * (uint32_t)g.lda) + load_col<TL>(lane);
-  }
+  for (int i = 0; i < TL::A_INS; ++i)
+    src.a_off[i] = (uint32_t)(min(load_row<TL>(i, wave, lane), mlast) * (uint32_t)g.lda) + load_col<TL>(lane);
 #pragma unroll
-  for (int i = 0; i < TL::B_INS; ++i) {
-    b.base[i] = B;
-    b.off[i] = (uint32_t)(min(load_row<TL>(i, wave, lane), nlast) * (uint32_t)g.ldb) + load_col<TL>(lane);
-  }
+  for (int i = 0; i < TL::B_INS; ++i)
+    src.b_off[i] = (uint32_t)(min(load_row<TL>(i, wave, lane), nlast) * (uint32_t)g.ldb) + load_col<TL>(lane);
   const int j = threadIdx.x;
-  const float* sp;
-  int64_t step;
   if (j < TL::BM) {
-    sp = g.a_scale + kb0 * g.a_scale_ld + row0 + m0 + min(j, mlast);
-    step = g.a_scale_ld;
+    src.s = g.a_scale + kb0 * g.a_scale_ld + row0 + m0 + min(j, mlast);
+    src.s_step = g.a_scale_ld;
   } else {
     const int64_t n = n0 + min(j - TL::BM, nlast);
     const float* sb = g.b_scale + e * g.b_scale_stride;
-    sp = kMode == kRowB ? sb + kb0 * g.b_scale_ld + n : sb + (n >> 7) * g.b_scale_ld + kb0;
-    step = kMode == kRowB ? g.b_scale_ld : 1;
+    src.s = kMode == kRowB ? sb + kb0 * g.b_scale_ld + n : sb + (n >> 7) * g.b_scale_ld + kb0;
+    src.s_step = kMode == kRowB ? g.b_scale_ld : 1;
   }
   QAcc<TL> acc;
-  quant_pipe<TL, kMode, kWide>(a, b, sp, step, nb, lds, acc);
+  quant_pipe<TL, kMode, kWide>(src, nb, lds, acc);
   constexpr int MI = QAcc<TL>::MI, NI = QAcc<TL>::NI;
   const int wm = wave / TL::WGN, wn = wave % TL::WGN;
   if (partial || g.out_dt == DT_F32) {
@@ -759,36 +790,33 @@ __global__ __launch_bounds__(TL::THREADS) void gate_up_kernel(QuantGateUp g, int
   }
   const int64_t m0 = (int64_t)mt * TL::BM;
   const int nb = g.K / kQB;
-  RowSrc<TL::A_INS> a;
-  RowSrc<TL::B_INS> b;
-  const char* A = uniform_ptr(g.A + (row0 + m0) * g.lda);
-  const int64_t wrow = ((int64_t)e * g.F + fb * kQB) * g.K;
+  Stager<TL> src;
+  src.a = uniform_ptr(g.A + (row0 + m0) * g.lda);
   const int mlast = (int)min(rows - m0 - 1, (int64_t)TL::BM);
 #pragma unroll
-  for (int i = 0; i < TL::A_INS; ++i) {
-    a.base[i] = A;
-    a.off[i] = (uint32_t)(min(load_row<TL>(i, wave, lane), mlast) * (uint32_t)g.lda) + load_col<TL>(lane);
-  }
-  // tile row r: 16-row blocks alternate gate and up; each load instruction's
-  // 8 rows lie in one block
-  auto feature = [](int r) { return (r >> 5) * 16 + (r & 15); };
+  for (int i = 0; i < TL::A_INS; ++i)
+    src.a_off[i] = (uint32_t)(min(load_row<TL>(i, wave, lane), mlast) * (uint32_t)g.lda) + load_col<TL>(lane);
+  // tile row r: 16-row blocks alternate gate and up.  The 8 rows of a load
+  // instruction lie in one block, and a wavefront's instructions, 8 NW = 64
+  // rows apart, all in gate or all in up blocks
+  static_assert(TL::NW == 8, "64 rows between a wavefront's load instructions");
+  const bool up = (load_row<TL>(0, wave, 0) >> 4) & 1;
+  src.b = uniform_ptr((up ? g.Wu : g.Wg) + ((int64_t)e * g.F + fb * kQB) * g.K);
 #pragma unroll
   for (int i = 0; i < TL::B_INS; ++i) {
     const int r = load_row<TL>(i, wave, lane);
-    b.base[i] = uniform_ptr(((r >> 4) & 1 ? g.Wu : g.Wg) + wrow);
-    b.off[i] = (uint32_t)(feature(r) * (uint32_t)g.K) + load_col<TL>(lane);
+    src.b_off[i] = (uint32_t)(((r >> 5) * 16 + (r & 15)) * (uint32_t)g.K) + load_col<TL>(lane);
   }
   const int j = threadIdx.x;
-  const float* sp;
-  int64_t step = 1;
   if (j < TL::BM) {
-    sp = g.a_scale + row0 + m0 + min(j, mlast);
-    step = g.a_scale_ld;
+    src.s = g.a_scale + row0 + m0 + min(j, mlast);
+    src.s_step = g.a_scale_ld;
   } else {
-    sp = (((j - TL::BM) >> 4) & 1 ? g.su : g.sg) + ((int64_t)e * tiles_n + fb) * nb;
+    src.s = (((j - TL::BM) >> 4) & 1 ? g.su : g.sg) + ((int64_t)e * tiles_n + fb) * nb;
+    src.s_step = 1;
   }
   QAcc<TL> acc;
-  quant_pipe<TL, kGateUp, false>(a, b, sp, step, nb, lds, acc);
+  quant_pipe<TL, kGateUp, false>(src, nb, lds, acc);
   // column blocks 2 q (gate) and 2 q + 1 (up) hold the same features: h over
   // the gate registers, and its largest magnitude per row: in the lane, the 4
   // lanes of the row, then the wavefronts of the row
