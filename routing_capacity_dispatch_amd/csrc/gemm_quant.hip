@@ -452,15 +452,16 @@ struct QAcc {
 // then the loads of the block after next and the next block's first fragments
 // go in among its MFMAs, each B fragment into the registers that its last
 // MFMA has just read.  Ends with a barrier, so the caller may reuse the LDS.
-template <class TL, int kMode, bool kWide>
+// MI: row blocks computed, the wavefront's first ones (see pipe_rows).
+template <class TL, int kMode, bool kWide, int MI = QAcc<TL>::MI>
 __device__ __forceinline__ void quant_pipe(Stager<TL>& src, int nb, char* lds, QAcc<TL>& acc) {
   using Q = QTile<TL>;
-  constexpr int MI = QAcc<TL>::MI, NI = QAcc<TL>::NI, NM = MI * NI;
+  constexpr int NI = QAcc<TL>::NI, NM = MI * NI;
   constexpr int kLag = 2;
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
   const int wm = wave / TL::WGN, wn = wave % TL::WGN;
 #pragma unroll
-  for (int mi = 0; mi < MI; ++mi)
+  for (int mi = 0; mi < QAcc<TL>::MI; ++mi)
 #pragma unroll
     for (int ni = 0; ni < NI; ++ni) acc.v[mi][ni] = f32x4_t{0.f, 0.f, 0.f, 0.f};
   if (nb <= 0) return;
@@ -597,6 +598,22 @@ __device__ __forceinline__ void quant_pipe(Stager<TL>& src, int nb, char* lds, Q
   __syncthreads();
 }
 
+// quant_pipe over the row blocks that hold some of the tile's rows (`last`
+// the last one's index): an expert's last tile is half empty on average, and
+// a wavefront whose band is empty leaves the matrix cores to the one that
+// shares its SIMD.  Loads and barriers are those of every variant.
+template <class TL, int kMode, int M = QAcc<TL>::MI>
+__device__ __forceinline__ void pipe_rows(Stager<TL>& src, int nb, char* lds, QAcc<TL>& acc, int last) {
+  if constexpr (M > 2) {
+    const int band = last + 1 - (int)(threadIdx.x >> 6) / TL::WGN * TL::WM;
+    if (__builtin_amdgcn_readfirstlane(band) <= (M - 2) * kMB) {
+      pipe_rows<TL, kMode, M - 2>(src, nb, lds, acc, last);
+      return;
+    }
+  }
+  quant_pipe<TL, kMode, false, M>(src, nb, lds, acc);
+}
+
 // Row of this lane's results of row block mi, and the first of its 4 columns
 // of column block ni.
 template <class TL>
@@ -667,13 +684,13 @@ constexpr int product_lds() {
 // C tile.  Grouped products have offsets; a dense one may split K: part
 // blockIdx.y of gridDim.y sums its share of the blocks into partial sums
 // [part][M][N] fp32 (g.C with split), which reduce_kernel adds in order.
-template <class TL, int kMode, bool kWide>
+template <class TL, int kMode, bool kWide, bool kGrouped>
 __global__ __launch_bounds__(TL::THREADS) void product_kernel(QuantGemm g, int tiles_m, int tiles_n, float* partial) {
   __shared__ __attribute__((aligned(1024))) char lds[product_lds<TL>()];
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
   int e = 0, mt, nt;
   int64_t row0 = 0, rows = g.M;
-  if (g.offsets) {
+  if constexpr (kGrouped) {
     if (!expert_tile<TL::BM>(g.offsets, g.E, g.M, tiles_n, e, mt, nt, row0, rows)) return;
   } else {
     const int t = core::xcd_order(blockIdx.x, gridDim.x);
@@ -708,7 +725,10 @@ __global__ __launch_bounds__(TL::THREADS) void product_kernel(QuantGemm g, int t
     src.s_step = kMode == kRowB ? g.b_scale_ld : 1;
   }
   QAcc<TL> acc;
-  quant_pipe<TL, kMode, kWide>(src, nb, lds, acc);
+  if constexpr (kGrouped)
+    pipe_rows<TL, kMode>(src, nb, lds, acc, mlast);
+  else
+    quant_pipe<TL, kMode, kWide>(src, nb, lds, acc);
   constexpr int MI = QAcc<TL>::MI, NI = QAcc<TL>::NI;
   const int wm = wave / TL::WGN, wn = wave % TL::WGN;
   if (partial || g.out_dt == DT_F32) {
@@ -816,7 +836,7 @@ __global__ __launch_bounds__(TL::THREADS) void gate_up_kernel(QuantGateUp g, int
     src.s_step = 1;
   }
   QAcc<TL> acc;
-  quant_pipe<TL, kGateUp, false>(src, nb, lds, acc);
+  pipe_rows<TL, kGateUp>(src, nb, lds, acc, mlast);
   // column blocks 2 q (gate) and 2 q + 1 (up) hold the same features: h over
   // the gate registers, and its largest magnitude per row: in the lane, the 4
   // lanes of the row, then the wavefronts of the row
@@ -911,9 +931,11 @@ void launch_tiles(const QuantGemm& g, int parts, float* partial, hipStream_t s) 
   const int64_t tm = g.offsets ? cdiv(g.M, TL::BM) + g.E : cdiv(g.M, TL::BM);
   const dim3 grid(pad8(tm * tn), (unsigned)parts);
   if (g.b_rows == 1)
-    product_kernel<TL, kRowB, kWide><<<grid, TL::THREADS, 0, s>>>(g, (int)tm, (int)tn, partial);
-  else
-    product_kernel<TL, kBlockB, kWide><<<grid, TL::THREADS, 0, s>>>(g, (int)tm, (int)tn, partial);
+    product_kernel<TL, kRowB, kWide, false><<<grid, TL::THREADS, 0, s>>>(g, (int)tm, (int)tn, partial);
+  else if (!g.offsets)
+    product_kernel<TL, kBlockB, kWide, false><<<grid, TL::THREADS, 0, s>>>(g, (int)tm, (int)tn, partial);
+  else if constexpr (!kWide)  // the experts' down product: bf16 results
+    product_kernel<TL, kBlockB, false, true><<<grid, TL::THREADS, 0, s>>>(g, (int)tm, (int)tn, partial);
 }
 
 template <int MT, int KS>
