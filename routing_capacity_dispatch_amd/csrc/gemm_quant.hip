@@ -633,60 +633,63 @@ template <int BM>
 __device__ __forceinline__ bool expert_tile(const int32_t* offsets, int E, int64_t M, int tiles_n, int& e, int& mt,
                                             int& nt, int64_t& row0, int64_t& rows) {
   const int lane = threadIdx.x & 63;
-  int total = 0;
-  for (int e0 = 0; e0 < E; e0 += 64) {
-    int64_t r0, n;
+  int64_t r0, n;
+  int x, c;  // tiles of this lane's expert, and of those up to it in its 64
+  auto scan = [&](int e0) {
     expert_range(offsets, min(e0 + lane, E - 1), M, r0, n);
-    int c = e0 + lane < E && n > 0 ? (int)((n + BM - 1) / BM) : 0;
-    for (int d = 1; d < 64; d <<= 1) c += __shfl_xor(c, d);
-    total += c;
-  }
-  total *= tiles_n;
+    c = e0 + lane < E && n > 0 ? (int)((n + BM - 1) / BM) * tiles_n : 0;
+    x = c;
+    for (int d = 1; d < 64; d <<= 1) {
+      const int o = __shfl_up(x, d);
+      if (lane >= d) x += o;
+    }
+    return __builtin_amdgcn_readlane(x, 63);
+  };
+  int total = scan(0);
+  const int first64 = total;
+  for (int e0 = 64; e0 < E; e0 += 64) total += scan(e0);
   const int per = (total + 7) >> 3;
   const int local = blockIdx.x >> 3;
   int t = (blockIdx.x & 7) * per + local;
   if (local >= per || t >= total) return false;
   for (int e0 = 0; e0 < E; e0 += 64) {
-    int64_t r0, n;
-    expert_range(offsets, min(e0 + lane, E - 1), M, r0, n);
-    const int c = (e0 + lane < E && n > 0 ? (int)((n + BM - 1) / BM) : 0) * tiles_n;
-    int x = c;
-    for (int d = 1; d < 64; d <<= 1) {
-      const int o = __shfl_up(x, d);
-      if (lane >= d) x += o;
-    }
-    const uint64_t hit = ballot64(x > t);
-    if (hit) {
-      const int l = __builtin_ctzll(hit);
+    const int here = E <= 64 ? first64 : scan(e0);
+    if (t < here) {
+      const int l = __builtin_ctzll(ballot64(x > t));
       e = e0 + l;
-      const int first = __builtin_amdgcn_readlane(x - c, l);
       const int tm = __builtin_amdgcn_readlane(c, l) / tiles_n;
+      t -= __builtin_amdgcn_readlane(x - c, l);
       row0 = readlane64(r0, l);
       rows = readlane64(n, l);
-      t -= first;
       nt = t / tm;
       mt = t - nt * tm;
       return true;
     }
-    t -= __builtin_amdgcn_readlane(x, 63);
+    t -= here;
   }
   return false;
 }
 
-constexpr int kStagePad = 16;
-
-template <class TL>
-constexpr int product_lds() {
-  constexpr int stage = TL::BM * (TL::BN * 2 + kStagePad);
-  return QTile<TL>::LDS > stage ? QTile<TL>::LDS : stage;
+// Lanes of 16 exchange between two neighbouring column blocks x and y (one
+// word of each lane's 4 columns): then lanes 0..15 and 32..47 hold the words of
+// x's columns 0..7 and 8..15 (first: 0..3 of them, second: 4..7), lanes 16..31
+// and 48..63 those of y.
+struct Swapped {
+  uint32_t first, second;
+};
+__device__ __forceinline__ Swapped swap_rows(uint32_t x, uint32_t y) {
+  const auto r = __builtin_amdgcn_permlane16_swap(x, y, false, false);
+  return Swapped{r[0], r[1]};
 }
+// First of this lane's 8 columns after the exchange, from the first block's.
+__device__ __forceinline__ int swapped_col(int lane) { return ((lane >> 4) & 1) * kMB + (lane >> 5) * 8; }
 
 // C tile.  Grouped products have offsets; a dense one may split K: part
 // blockIdx.y of gridDim.y sums its share of the blocks into partial sums
 // [part][M][N] fp32 (g.C with split), which reduce_kernel adds in order.
 template <class TL, int kMode, bool kWide, bool kGrouped>
 __global__ __launch_bounds__(TL::THREADS) void product_kernel(QuantGemm g, int tiles_m, int tiles_n, float* partial) {
-  __shared__ __attribute__((aligned(1024))) char lds[product_lds<TL>()];
+  __shared__ __attribute__((aligned(1024))) char lds[QTile<TL>::LDS];
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
   int e = 0, mt, nt;
   int64_t row0 = 0, rows = g.M;
@@ -754,27 +757,30 @@ __global__ __launch_bounds__(TL::THREADS) void product_kernel(QuantGemm g, int t
     }
     return;
   }
-  constexpr int ld = TL::BN * 2 + kStagePad;
-#pragma unroll
-  for (int mi = 0; mi < MI; ++mi)
-#pragma unroll
-    for (int ni = 0; ni < NI; ++ni) {
-      const f32x4_t& v = acc.v[mi][ni];
-      *reinterpret_cast<uint2*>(lds + tile_row<TL>(wm, mi, lane) * ld + tile_col<TL>(wn, ni, lane) * 2) =
-          make_uint2(bf16_pair(v[0], v[1]), bf16_pair(v[2], v[3]));
-    }
-  __syncthreads();
+  // straight from the registers: two column blocks exchange so that a lane
+  // holds 8 neighbouring columns, 4 lanes 64 bytes of a row
   uint16_t* C = static_cast<uint16_t*>(g.C) + (row0 + m0) * g.ldc + n0;
-  const bool wide_ok = ((reinterpret_cast<uintptr_t>(g.C) | (uintptr_t)(g.ldc * 2)) & 15) == 0;
-  constexpr int cpr = TL::BN / 8;
-  for (int q = threadIdx.x; q < TL::BM * cpr; q += TL::THREADS) {
-    const int r = q / cpr, c = (q - r * cpr) * 8;
-    if (r > mlast || c > nlast) continue;
-    const char* src = lds + r * ld + c * 2;
-    if (wide_ok && c + 7 <= nlast)
-      st16(C + r * g.ldc + c, ld16(src));
-    else
-      for (int i = 0; i < 8 && c + i <= nlast; ++i) C[r * g.ldc + c + i] = reinterpret_cast<const uint16_t*>(src)[i];
+  const bool wide_ok = ((reinterpret_cast<uintptr_t>(C) | (uintptr_t)(g.ldc * 2)) & 15) == 0;
+#pragma unroll
+  for (int mi = 0; mi < MI; ++mi) {
+    const int row = tile_row<TL>(wm, mi, lane);
+#pragma unroll
+    for (int ni = 0; ni < NI; ni += 2) {
+      const f32x4_t &u = acc.v[mi][ni], &v = acc.v[mi][ni + 1];
+      const Swapped lo = swap_rows(bf16_pair(u[0], u[1]), bf16_pair(v[0], v[1]));
+      const Swapped hi = swap_rows(bf16_pair(u[2], u[3]), bf16_pair(v[2], v[3]));
+      const int col = wn * TL::WN + ni * kMB + swapped_col(lane);
+      if (row > mlast) continue;
+      uint16_t* dst = C + row * g.ldc + col;
+      const uint32_t w[4] = {lo.first, hi.first, lo.second, hi.second};
+      if (wide_ok && col + 7 <= nlast) {
+        st16(dst, make_uint4(w[0], w[1], w[2], w[3]));
+      } else {
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+          if (col + i <= nlast) dst[i] = (uint16_t)(w[i >> 1] >> (16 * (i & 1)));
+      }
+    }
   }
 }
 
@@ -843,8 +849,6 @@ __global__ __launch_bounds__(TL::THREADS) void gate_up_kernel(QuantGateUp g, int
   constexpr int MI = QAcc<TL>::MI, NI = QAcc<TL>::NI;
   const int wm = wave / TL::WGN, wn = wave % TL::WGN;
   float* part = reinterpret_cast<float*>(lds);  // [BM][WGN]
-  constexpr int ld = kQB + kStagePad;
-  char* stage = lds + TL::BM * TL::WGN * 4;
 #pragma unroll
   for (int mi = 0; mi < MI; ++mi) {
     float mx = 0.0f;
@@ -869,18 +873,25 @@ __global__ __launch_bounds__(TL::THREADS) void gate_up_kernel(QuantGateUp g, int
 #pragma unroll
     for (int w = 0; w < TL::WGN; ++w) amax = fmaxf(amax, part[row * TL::WGN + w]);
     const BlockQuant bq(amax);
+    uint32_t w[NI / 2];
 #pragma unroll
     for (int q = 0; q < NI / 2; ++q) {
       const f32x4_t& v = acc.v[mi][2 * q];
-      *reinterpret_cast<uint32_t*>(stage + row * ld + wn * (TL::WN / 2) + q * 16 + (lane >> 4) * 4) =
-          e4m3_quad(bq(v[0]), bq(v[1]), bq(v[2]), bq(v[3]));
+      w[q] = e4m3_quad(bq(v[0]), bq(v[1]), bq(v[2]), bq(v[3]));
     }
-    if (wn == 0 && lane < 16 && row <= mlast) g.h_scale[(col / kQB) * g.h_scale_ld + row0 + m0 + row] = block_scale(amax);
-  }
-  __syncthreads();
-  for (int q = threadIdx.x; q < TL::BM * 8; q += TL::THREADS) {
-    const int r = q >> 3, c = (q & 7) * 16;
-    if (r <= mlast) st16(g.H + (row0 + m0 + r) * g.ldh + col + c, ld16(stage + r * ld + c));
+    static_assert(NI == 2 || NI == 4, "one or two runs of 16 features per wavefront");
+    if constexpr (NI == 4) {
+      const Swapped x = swap_rows(w[0], w[1]);
+      w[0] = x.first;
+      w[1] = x.second;
+    }
+    if (row > mlast) continue;
+    char* dst = g.H + (row0 + m0 + row) * g.ldh + col + wn * (TL::WN / 2);
+    if constexpr (NI == 4)
+      *reinterpret_cast<uint2*>(dst + swapped_col(lane)) = make_uint2(w[0], w[1]);
+    else
+      *reinterpret_cast<uint32_t*>(dst + (lane >> 4) * 4) = w[0];
+    if (wn == 0 && lane < 16) g.h_scale[(col / kQB) * g.h_scale_ld + row0 + m0 + row] = block_scale(amax);
   }
 }
 
