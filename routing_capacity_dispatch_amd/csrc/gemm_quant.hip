@@ -141,9 +141,9 @@ __device__ __forceinline__ void span_blocks(const char* brow, const BScales<kRow
   }
 }
 
-// A workgroup of kSkinnyWaves wavefronts: kSkinnyWaves / KS column tiles, KS
-// wavefronts on contiguous shares of K each, whose sums meet in LDS in a
-// fixed order.
+// Up to 16 MT rows.  A workgroup of kSkinnyWaves wavefronts: kSkinnyWaves / KS
+// column tiles, KS wavefronts on contiguous shares of K each, whose sums meet
+// in LDS in a fixed order.
 constexpr int kSkinnyWaves = 4;
 
 template <int MT, int KS, bool kRowScale, bool kWide>
@@ -153,16 +153,8 @@ __global__ __launch_bounds__(64 * kSkinnyWaves) void skinny_kernel(QuantGemm g) 
   const int ks = wave % KS;
   const int64_t n0 = ((int64_t)blockIdx.x * (kSkinnyWaves / KS) + wave / KS) * 16;
   const int64_t n = min(n0 + (lane & 15), g.N - 1);
-  int64_t row0 = 0, rows = g.M;
-  const char* B = g.B;
   const float* bs = g.b_scale;
-  if (g.offsets) {
-    const int e = blockIdx.y;
-    expert_range(g.offsets, e, g.M, row0, rows);
-    B += (int64_t)e * g.b_stride;
-    bs += (int64_t)e * g.b_scale_stride;
-  }
-  const char* brow = B + n * g.ldb;
+  const char* brow = g.B + n * g.ldb;
   const int64_t c0 = n0 + (lane >> 4) * 4;  // this lane's columns
   BScales<kRowScale> sb;
   if constexpr (kRowScale) {
@@ -175,35 +167,32 @@ __global__ __launch_bounds__(64 * kSkinnyWaves) void skinny_kernel(QuantGemm g) 
   }
   const int nb = g.K / kQB, per = (nb + KS - 1) / KS;
   const int b0 = min(ks * per, nb), b1 = min(b0 + per, nb);
-  for (int64_t m0 = 0; m0 < rows; m0 += 16 * MT) {
-    const char* arow[MT];
-    const float* sa[MT];
-    f32x4_t acc[MT];
+  const char* arow[MT];
+  const float* sa[MT];
+  f32x4_t acc[MT];
 #pragma unroll
-    for (int i = 0; i < MT; ++i) {
-      const int64_t m = row0 + min(m0 + i * 16 + (lane & 15), rows - 1);
-      arow[i] = g.A + m * g.lda;
-      sa[i] = g.a_scale + m;
-      acc[i] = f32x4_t{0.f, 0.f, 0.f, 0.f};
-    }
-    span_blocks<MT, kRowScale, kWide>(brow, sb, arow, sa, g.a_scale_ld, b0, b1, lane, acc);
-    if constexpr (KS > 1) {
-      __syncthreads();
+  for (int i = 0; i < MT; ++i) {
+    const int64_t m = min((int64_t)(i * 16 + (lane & 15)), g.M - 1);
+    arow[i] = g.A + m * g.lda;
+    sa[i] = g.a_scale + m;
+    acc[i] = f32x4_t{0.f, 0.f, 0.f, 0.f};
+  }
+  span_blocks<MT, kRowScale, kWide>(brow, sb, arow, sa, g.a_scale_ld, b0, b1, lane, acc);
+  if constexpr (KS > 1) {
 #pragma unroll
-      for (int i = 0; i < MT; ++i) part[wave][i][lane] = acc[i];
-      __syncthreads();
-      if (ks != 0) continue;
+    for (int i = 0; i < MT; ++i) part[wave][i][lane] = acc[i];
+    __syncthreads();
+    if (ks != 0) return;
 #pragma unroll
-      for (int i = 0; i < MT; ++i)
+    for (int i = 0; i < MT; ++i)
 #pragma unroll
-        for (int j = 1; j < KS; ++j) acc[i] += part[wave + j][i][lane];
-    }
+      for (int j = 1; j < KS; ++j) acc[i] += part[wave + j][i][lane];
+  }
 #pragma unroll
-    for (int i = 0; i < MT; ++i) {
-      const int64_t m = m0 + i * 16 + (lane & 15);
-      if (m >= rows || c0 >= g.N) continue;
-      store_run(g.out_dt, g.C, (row0 + m) * g.ldc + c0, acc[i], (int)min(g.N - c0, (int64_t)4));
-    }
+  for (int i = 0; i < MT; ++i) {
+    const int64_t m = i * 16 + (lane & 15);
+    if (m >= g.M || c0 >= g.N) continue;
+    store_run(g.out_dt, g.C, m * g.ldc + c0, acc[i], (int)min(g.N - c0, (int64_t)4));
   }
 }
 
@@ -897,7 +886,6 @@ __global__ __launch_bounds__(TL::THREADS) void gate_up_kernel(QuantGateUp g, int
 
 using T256 = core::Tile<256, 256, 2, 4>;
 using T128 = core::Tile<128, 128, 2, 2>;
-using E128 = core::Tile<128, 256, 2, 4>;
 using E64 = core::Tile<64, 256, 1, 8>;
 
 inline int64_t cdiv(int64_t a, int64_t b) { return (a + b - 1) / b; }
@@ -916,7 +904,7 @@ Form product_form(const QuantGemm& g) {
   f.parts = 1;
   const int64_t rows = g.offsets ? cdiv(g.M, g.E) : g.M;
   f.wide = g.out_dt == DT_F32;
-  f.skinny = rows <= 32;
+  f.skinny = !g.offsets && rows <= 32;
   if (f.skinny) return f;
   f.big = !f.wide && rows >= 192 && (g.offsets || cdiv(g.M, 256) * cdiv(g.N, 256) >= 128);
   if (!g.offsets && !f.big) {
@@ -951,7 +939,7 @@ void launch_tiles(const QuantGemm& g, int parts, float* partial, hipStream_t s) 
 
 template <int MT, int KS>
 void launch_skinny_as(const QuantGemm& g, const Form& f, hipStream_t s) {
-  const dim3 grid((unsigned)cdiv(g.N, 16 * (kSkinnyWaves / KS)), (unsigned)(g.offsets ? g.E : 1));
+  const dim3 grid((unsigned)cdiv(g.N, 16 * (kSkinnyWaves / KS)));
   constexpr int T = 64 * kSkinnyWaves;
   if (g.b_rows == 1) {
     if (f.wide)
@@ -967,14 +955,10 @@ void launch_skinny_as(const QuantGemm& g, const Form& f, hipStream_t s) {
 }
 
 void launch_skinny(const QuantGemm& g, const Form& f, hipStream_t s) {
-  // one pass over the weights for up to 32 rows; an expert's rows vary about
-  // their mean, so a mean above 8 takes the two row blocks
-  const bool two = g.offsets ? cdiv(g.M, g.E) > 8 : g.M > 16;
-  // wavefronts per column tile: until the chip has 2048 wavefronts or a
-  // share of K is one span
-  const int64_t tiles = cdiv(g.N, 16) * (g.offsets ? (g.M < g.E ? g.M : g.E) : 1);
-  const bool split = tiles < 2048 && g.K / kQB > kSpan;
-  if (two) {
+  // four wavefronts per column tile while that leaves the chip short of 2048
+  // wavefronts and each a span of K
+  const bool split = cdiv(g.N, 16) < 2048 && g.K / kQB > kSpan;
+  if (g.M > 16) {
     if (split)
       launch_skinny_as<2, 4>(g, f, s);
     else
@@ -1017,7 +1001,9 @@ void launch_hidden(const QuantGateUp& g, hipStream_t s) {
 }
 
 // Mean rows per expert up to which the experts' rows go straight from memory.
-constexpr int64_t kFewRows = 24;
+// 64 experts, L 2048, F 1024, top-8, us for means of 1, 4, 8, 12, 16 rows: this
+// way 57, 78, 97, 121, 138, with tiles 65, 90, 96, 97, 100.
+constexpr int64_t kFewRows = 8;
 // K whose 16 staged rows leave the LDS of a CU to two workgroups.
 constexpr int kStagedK = 4096;
 
@@ -1060,11 +1046,12 @@ hipError_t launch_few_rows(const FewRows& g, bool hidden, bool staged, hipStream
 
 hipError_t launch_quant_gate_up(const QuantGateUp& g, hipStream_t s) {
   if (g.M <= 0 || g.E <= 0) return hipSuccess;
-  const int64_t rows = g.offsets ? cdiv(g.M, g.E) : g.M;
-  if (rows <= 64)
+  // 64-row tiles for means up to 20 rows, 256-row tiles, which compute only the
+  // row blocks that hold rows, above (experts as at kFewRows, us for means of
+  // 16, 24, 32, 48, 64 rows: 100, 115, 118, 127, 132 with the one, 111, 111,
+  // 115, 125, 130 with the other)
+  if ((g.offsets ? cdiv(g.M, g.E) : g.M) <= 20)
     launch_hidden<E64>(g, s);
-  else if (rows <= 160)
-    launch_hidden<E128>(g, s);
   else
     launch_hidden<T256>(g, s);
   return hipGetLastError();
