@@ -906,12 +906,20 @@ Form product_form(const QuantGemm& g) {
   f.wide = g.out_dt == DT_F32;
   f.skinny = !g.offsets && rows <= 32;
   if (f.skinny) return f;
-  f.big = !f.wide && rows >= 192 && (g.offsets || cdiv(g.M, 256) * cdiv(g.N, 256) >= 128);
+  // rounds of the chip: 256 workgroups of 256 x 256 tiles (one per CU) take
+  // 1.92 us a block of K, 512 of 128 x 128 tiles (two per CU) 1.23 us
+  // (8192 x 6144 x 4096: 184 us and 237 us)
+  const int64_t r256 = cdiv(cdiv(g.M, 256) * cdiv(g.N, 256), 256), r128 = cdiv(cdiv(g.M, 128) * cdiv(g.N, 128), 512);
+  f.big = !f.wide && rows >= 192 && (g.offsets || r256 * 192 < r128 * 123);
   if (!g.offsets && !f.big) {
+    // K shared by as many workgroups as give every CU one, 8 blocks each at
+    // the least: more only wait for one another, and the partial sums' way
+    // through memory has a price (N 6144, K 2048, 384 rows, us: 27.6 with two
+    // workgroups per CU, 15.0 with one)
     const int64_t tiles = cdiv(g.M, 128) * cdiv(g.N, 128);
-    int64_t p = 512 / (tiles > 0 ? tiles : 1);  // two 128 x 128 workgroups fit a CU
+    int64_t p = 256 / (tiles > 0 ? tiles : 1);
     if (p > 8) p = 8;
-    if (p > g.K / kQB / 4) p = g.K / kQB / 4;
+    if (p > g.K / kQB / 8) p = g.K / kQB / 8;
     if (p > 1) f.parts = (int)p;
   }
   return f;
