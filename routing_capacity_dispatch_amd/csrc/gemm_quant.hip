@@ -442,12 +442,14 @@ struct QAcc {
 // go in among its MFMAs, each B fragment into the registers that its last
 // MFMA has just read.  Ends with a barrier, so the caller may reuse the LDS.
 // MI: row blocks computed, the wavefront's first ones (see pipe_rows).
-template <class TL, int kMode, bool kWide, int MI = QAcc<TL>::MI>
-__device__ __forceinline__ void quant_pipe(Stager<TL>& src, int nb, char* lds, QAcc<TL>& acc) {
+// KG: groups of wavefronts that share the blocks; src, nb, lds and wave are
+// those of one group, whose blocks lie KG apart.
+template <class TL, int kMode, bool kWide, int MI = QAcc<TL>::MI, int KG = 1>
+__device__ __forceinline__ void quant_pipe(Stager<TL>& src, int nb, char* lds, QAcc<TL>& acc, int wave) {
   using Q = QTile<TL>;
   constexpr int NI = QAcc<TL>::NI, NM = MI * NI;
   constexpr int kLag = 2;
-  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+  const int lane = threadIdx.x & 63;
   const int wm = wave / TL::WGN, wn = wave % TL::WGN;
 #pragma unroll
   for (int mi = 0; mi < QAcc<TL>::MI; ++mi)
@@ -466,8 +468,8 @@ __device__ __forceinline__ void quant_pipe(Stager<TL>& src, int nb, char* lds, Q
       stage16<TL::B_BASE + (i - TL::A_INS) * TL::NW * 1024>(lds_rows + st * TL::B_BYTES, src.b, src.b_off[i - TL::A_INS]);
     } else {
       stage4<0>(lds_scales + st * Q::SCALES * 4, src.s);
-      src.a += kQB;
-      src.b += kQB;
+      src.a += KG * kQB;
+      src.b += KG * kQB;
       src.s += src.s_step;
     }
   };
@@ -600,7 +602,7 @@ __device__ __forceinline__ void pipe_rows(Stager<TL>& src, int nb, char* lds, QA
       return;
     }
   }
-  quant_pipe<TL, kMode, false, M>(src, nb, lds, acc);
+  quant_pipe<TL, kMode, false, M>(src, nb, lds, acc, threadIdx.x >> 6);
 }
 
 // Row of this lane's results of row block mi, and the first of its 4 columns
@@ -673,13 +675,19 @@ __device__ __forceinline__ Swapped swap_rows(uint32_t x, uint32_t y) {
 // First of this lane's 8 columns after the exchange, from the first block's.
 __device__ __forceinline__ int swapped_col(int lane) { return ((lane >> 4) & 1) * kMB + (lane >> 5) * 8; }
 
-// C tile.  Grouped products have offsets; a dense one may split K: part
-// blockIdx.y of gridDim.y sums its share of the blocks into partial sums
-// [part][M][N] fp32 (g.C with split), which reduce_kernel adds in order.
-template <class TL, int kMode, bool kWide, bool kGrouped>
-__global__ __launch_bounds__(TL::THREADS) void product_kernel(QuantGemm g, int tiles_m, int tiles_n, float* partial) {
-  __shared__ __attribute__((aligned(1024))) char lds[QTile<TL>::LDS];
-  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+// C tile.  kGrouped: the tiles of experts' rows.  A dense product may split K:
+// part blockIdx.y of gridDim.y sums its share of the blocks into partial sums
+// [part][M][N] fp32, which reduce_kernel adds in order; and the workgroup's KG
+// groups of wavefronts share the part's blocks, every KG-th one each, with
+// stages of their own, and add their sums at the end.
+template <class TL, int kMode, bool kWide, bool kGrouped, int KG>
+__global__ __launch_bounds__(TL::THREADS* KG) void product_kernel(QuantGemm g, int tiles_m, int tiles_n,
+                                                                 float* partial) {
+  static_assert(KG == 1 || (KG == 2 && !kGrouped), "one or two groups");
+  __shared__ __attribute__((aligned(1024))) char lds[QTile<TL>::LDS * KG];
+  const int lane = threadIdx.x & 63;
+  const int group = KG == 1 ? 0 : __builtin_amdgcn_readfirstlane((int)threadIdx.x / TL::THREADS);
+  const int wave = (threadIdx.x >> 6) - group * TL::NW;
   int e = 0, mt, nt;
   int64_t row0 = 0, rows = g.M;
   if constexpr (kGrouped) {
@@ -696,6 +704,9 @@ __global__ __launch_bounds__(TL::THREADS) void product_kernel(QuantGemm g, int t
     kb0 = min((int)blockIdx.y * per, nb);
     nb = min(per, nb - kb0);
   }
+  const int all = nb;
+  kb0 += group;
+  nb = (all - group + KG - 1) / KG;
   Stager<TL> src;
   src.a = uniform_ptr(g.A + (row0 + m0) * g.lda + (int64_t)kb0 * kQB);
   src.b = uniform_ptr(g.B + e * g.b_stride + n0 * g.ldb + (int64_t)kb0 * kQB);
@@ -706,23 +717,53 @@ __global__ __launch_bounds__(TL::THREADS) void product_kernel(QuantGemm g, int t
 #pragma unroll
   for (int i = 0; i < TL::B_INS; ++i)
     src.b_off[i] = (uint32_t)(min(load_row<TL>(i, wave, lane), nlast) * (uint32_t)g.ldb) + load_col<TL>(lane);
-  const int j = threadIdx.x;
+  const int j = threadIdx.x - group * TL::THREADS;
   if (j < TL::BM) {
     src.s = g.a_scale + kb0 * g.a_scale_ld + row0 + m0 + min(j, mlast);
-    src.s_step = g.a_scale_ld;
+    src.s_step = KG * g.a_scale_ld;
   } else {
     const int64_t n = n0 + min(j - TL::BM, nlast);
     const float* sb = g.b_scale + e * g.b_scale_stride;
     src.s = kMode == kRowB ? sb + kb0 * g.b_scale_ld + n : sb + (n >> 7) * g.b_scale_ld + kb0;
-    src.s_step = kMode == kRowB ? g.b_scale_ld : 1;
+    src.s_step = KG * (kMode == kRowB ? g.b_scale_ld : 1);
   }
   QAcc<TL> acc;
   if constexpr (kGrouped)
     pipe_rows<TL, kMode>(src, nb, lds, acc, mlast);
   else
-    quant_pipe<TL, kMode, kWide>(src, nb, lds, acc);
+    quant_pipe<TL, kMode, kWide, QAcc<TL>::MI, KG>(src, nb, lds + group * QTile<TL>::LDS, acc, wave);
   constexpr int MI = QAcc<TL>::MI, NI = QAcc<TL>::NI;
   const int wm = wave / TL::WGN, wn = wave % TL::WGN;
+  if constexpr (KG == 2) {
+    // a block short (an odd count), or with none at all, this group has met
+    // fewer barriers: one per block, and one more where there is any
+    const int met0 = (all + 1) / 2, met1 = all / 2;
+    if (group == 1)
+      for (int i = met1 + (met1 > 0); i < met0 + (met0 > 0); ++i) __syncthreads();
+    // each group keeps half of the row blocks and hands the other half over
+    f32x4_t* give = reinterpret_cast<f32x4_t*>(lds) + group * (MI / 2 * NI * TL::THREADS) + j;
+    const f32x4_t* take = reinterpret_cast<const f32x4_t*>(lds) + (1 - group) * (MI / 2 * NI * TL::THREADS) + j;
+    static_assert(MI * NI * TL::THREADS * 16 <= QTile<TL>::LDS * KG, "both halves fit the stages");
+#pragma unroll
+    for (int mi = 0; mi < MI; ++mi) {
+      if ((mi < MI / 2) == (group == 0)) continue;
+#pragma unroll
+      for (int ni = 0; ni < NI; ++ni) give[(mi % (MI / 2) * NI + ni) * TL::THREADS] = acc.v[mi][ni];
+    }
+    __syncthreads();
+#pragma unroll
+    for (int mi = 0; mi < MI; ++mi) {
+      if ((mi < MI / 2) != (group == 0)) continue;
+#pragma unroll
+      for (int ni = 0; ni < NI; ++ni) {
+        // group 0's blocks first
+        const f32x4_t o = take[(mi % (MI / 2) * NI + ni) * TL::THREADS];
+        acc.v[mi][ni] += o;
+      }
+    }
+  }
+  // row blocks this group stores
+  auto stores = [&](int mi) { return KG == 1 || (mi < MI / 2) == (group == 0); };
   if (partial || g.out_dt == DT_F32) {
     float* C = partial ? partial + ((int64_t)blockIdx.y * g.M + m0) * g.N + n0
                        : static_cast<float*>(g.C) + (row0 + m0) * g.ldc + n0;
@@ -731,7 +772,7 @@ __global__ __launch_bounds__(TL::THREADS) void product_kernel(QuantGemm g, int t
 #pragma unroll
     for (int mi = 0; mi < MI; ++mi) {
       const int row = tile_row<TL>(wm, mi, lane);
-      if (row > mlast) continue;
+      if (row > mlast || !stores(mi)) continue;
 #pragma unroll
       for (int ni = 0; ni < NI; ++ni) {
         const int col = tile_col<TL>(wn, ni, lane);
@@ -752,6 +793,7 @@ __global__ __launch_bounds__(TL::THREADS) void product_kernel(QuantGemm g, int t
   const bool wide_ok = ((reinterpret_cast<uintptr_t>(C) | (uintptr_t)(g.ldc * 2)) & 15) == 0;
 #pragma unroll
   for (int mi = 0; mi < MI; ++mi) {
+    if (!stores(mi)) continue;
     const int row = tile_row<TL>(wm, mi, lane);
 #pragma unroll
     for (int ni = 0; ni < NI; ni += 2) {
@@ -897,11 +939,12 @@ struct Form {
   bool big;    // 256 x 256 tiles (else 128 x 128)
   bool wide;   // bf16 matrix instructions on the widened values
   int parts;   // shares of K
+  int groups;  // groups of wavefronts in a workgroup that share K again
 };
 
 Form product_form(const QuantGemm& g) {
   Form f{};
-  f.parts = 1;
+  f.parts = f.groups = 1;
   const int64_t rows = g.offsets ? cdiv(g.M, g.E) : g.M;
   f.wide = g.out_dt == DT_F32;
   f.skinny = !g.offsets && rows <= 32;
@@ -912,15 +955,19 @@ Form product_form(const QuantGemm& g) {
   const int64_t r256 = cdiv(cdiv(g.M, 256) * cdiv(g.N, 256), 256), r128 = cdiv(cdiv(g.M, 128) * cdiv(g.N, 128), 512);
   f.big = !f.wide && rows >= 192 && (g.offsets || r256 * 192 < r128 * 123);
   if (!g.offsets && !f.big) {
-    // K shared by as many workgroups as give every CU one, 8 blocks each at
-    // the least: more only wait for one another, and the partial sums' way
-    // through memory has a price (N 6144, K 2048, 384 rows, us: 27.6 with two
-    // workgroups per CU, 15.0 with one)
+    // K shared by as many workgroups as give every CU one (N 6144, K 2048, 384
+    // rows, us: 27.6 with two per CU, 15.0 with one), each with 16 blocks at
+    // the least, 8 of widened values: the partial sums' way through memory and
+    // their own launch have a price (N 6144, K 2048, 128 rows, us: 11.6 with
+    // one share, 15.7 with two; widened 18.4 with either)
     const int64_t tiles = cdiv(g.M, 128) * cdiv(g.N, 128);
     int64_t p = 256 / (tiles > 0 ? tiles : 1);
+    const int64_t most = g.K / kQB / (f.wide ? 8 : 16);
     if (p > 8) p = 8;
-    if (p > g.K / kQB / 8) p = g.K / kQB / 8;
+    if (p > most) p = most;
     if (p > 1) f.parts = (int)p;
+    // one workgroup per CU at the most: two groups of wavefronts in it
+    if (tiles * f.parts <= 256) f.groups = 2;
   }
   return f;
 }
@@ -932,17 +979,22 @@ int64_t quant_gemm_ws_bytes(const QuantGemm& g) {
   return f.parts > 1 ? f.parts * g.M * g.N * 4 : 0;
 }
 
-template <class TL, bool kWide>
-void launch_tiles(const QuantGemm& g, int parts, float* partial, hipStream_t s) {
-  const int64_t tn = cdiv(g.N, TL::BN);
-  const int64_t tm = g.offsets ? cdiv(g.M, TL::BM) + g.E : cdiv(g.M, TL::BM);
+template <class TL, bool kWide, int KG>
+void launch_dense(const QuantGemm& g, int parts, float* partial, hipStream_t s) {
+  const int64_t tm = cdiv(g.M, TL::BM), tn = cdiv(g.N, TL::BN);
   const dim3 grid(pad8(tm * tn), (unsigned)parts);
+  constexpr int T = TL::THREADS * KG;
   if (g.b_rows == 1)
-    product_kernel<TL, kRowB, kWide, false><<<grid, TL::THREADS, 0, s>>>(g, (int)tm, (int)tn, partial);
-  else if (!g.offsets)
-    product_kernel<TL, kBlockB, kWide, false><<<grid, TL::THREADS, 0, s>>>(g, (int)tm, (int)tn, partial);
-  else if constexpr (!kWide)  // the experts' down product: bf16 results
-    product_kernel<TL, kBlockB, false, true><<<grid, TL::THREADS, 0, s>>>(g, (int)tm, (int)tn, partial);
+    product_kernel<TL, kRowB, kWide, false, KG><<<grid, T, 0, s>>>(g, (int)tm, (int)tn, partial);
+  else
+    product_kernel<TL, kBlockB, kWide, false, KG><<<grid, T, 0, s>>>(g, (int)tm, (int)tn, partial);
+}
+
+// The experts' down product: bf16 results, 128 x 128 scales.
+template <class TL>
+void launch_grouped(const QuantGemm& g, hipStream_t s) {
+  const int64_t tm = cdiv(g.M, TL::BM) + g.E, tn = cdiv(g.N, TL::BN);
+  product_kernel<TL, kBlockB, false, true, 1><<<pad8(tm * tn), TL::THREADS, 0, s>>>(g, (int)tm, (int)tn, nullptr);
 }
 
 template <int MT, int KS>
@@ -986,13 +1038,24 @@ hipError_t launch_quant_gemm(const QuantGemm& g, void* ws, hipStream_t s) {
     launch_skinny(g, f, s);
     return hipGetLastError();
   }
+  if (g.offsets) {
+    if (f.big)
+      launch_grouped<T256>(g, s);
+    else
+      launch_grouped<T128>(g, s);
+    return hipGetLastError();
+  }
   float* partial = f.parts > 1 ? static_cast<float*>(ws) : nullptr;
   if (f.big)
-    launch_tiles<T256, false>(g, f.parts, partial, s);
+    launch_dense<T256, false, 1>(g, f.parts, partial, s);
+  else if (f.groups == 1 && f.wide)
+    launch_dense<T128, true, 1>(g, f.parts, partial, s);
+  else if (f.groups == 1)
+    launch_dense<T128, false, 1>(g, f.parts, partial, s);
   else if (f.wide)
-    launch_tiles<T128, true>(g, f.parts, partial, s);
+    launch_dense<T128, true, 2>(g, f.parts, partial, s);
   else
-    launch_tiles<T128, false>(g, f.parts, partial, s);
+    launch_dense<T128, false, 2>(g, f.parts, partial, s);
   if (partial) {
     const int64_t blocks = cdiv(g.M * g.N, 1024);
     reduce_kernel<<<(unsigned)(blocks < 4096 ? blocks : 4096), 256, 0, s>>>(g, partial, f.parts);
