@@ -684,9 +684,45 @@ moe_status moe_experts_dropless_quant(const moe_config* cfg, const void* xs, con
                                       const moe_quant_experts* w, void* expert_out, void* ws, size_t ws_bytes,
                                       void* stream);
 
+/* ------------------------------------------------------------------------
+ * The dropless branch in 8 bits: moe_forward_dropless with scored routing
+ * (moe_route_scored) and every large product on e4m3 operands:
+ *   z      = x W_lat^T                 x quantised 1 x 128, z bf16
+ *   logits = z W_r^T                   bf16 operands, fp32
+ *   ids, gates by scoring; rows ordered by expert; 8-bit experts; combine
+ *   y      = [y_lat | h_1 .. h_S] W_out^T
+ * with y_lat (bf16, combined) and the shared experts' hidden rows h_s =
+ * silu(x Wg_s^T) * (x Wu_s^T) (fp32) quantised 1 x 128 into one operand, and
+ * W_out [D][L + S Fs] the up-projection and the shared down-projections side
+ * by side.  bf16 configs with d_model, d_latent, d_ff and (S > 0) d_ff_shared
+ * multiples of 128 (MOE_ERR_UNSUPPORTED else); top_k <= E, E % 4 == 0.
+ * ------------------------------------------------------------------------ */
+typedef struct {
+  const void* q_latent;     /* [L][D] e4m3, scales [L/128][D/128]             */
+  const float* s_latent;
+  const void* w_router;     /* [E][L] bf16                                    */
+  const float* router_bias; /* [E] fp32 (selection only), or NULL             */
+  moe_quant_experts experts;
+  const void* q_shared_gate; /* [S][Fs][D], scales [S][Fs/128][D/128]         */
+  const float* s_shared_gate;
+  const void* q_shared_up;
+  const float* s_shared_up;
+  const void* q_output;     /* [D][L + S Fs], scales [D/128][(L + S Fs)/128]  */
+  const float* s_output;
+} moe_quant_weights;
+
+/* x (device) [T][D] bf16, 16-byte aligned; y (device, out) [T][D] bf16; taps
+   (host struct, may be NULL) as in moe_forward_dropless, each tap 16-byte
+   aligned; counts (device, out, may be NULL) as there; ws (device) at least
+   moe_forward_dropless_quant_ws_bytes, 256-byte aligned. */
+moe_status moe_forward_dropless_quant_ws_bytes(const moe_config* cfg, size_t* bytes);
+moe_status moe_forward_dropless_quant(const moe_config* cfg, const moe_scoring* scoring,
+                                      const moe_quant_weights* w, const void* x, void* y,
+                                      const moe_dropless_taps* taps, int64_t* counts, void* ws,
+                                      size_t ws_bytes, void* stream);
+
 #ifdef __cplusplus
 }
 #endif
-
 
 #endif /* MOE_H */

@@ -21,7 +21,7 @@ __all__ = ["make_config", "plan", "route", "dispatch", "experts", "combine", "fo
            "combine_backward", "experts_backward", "dispatch_backward", "route_backward",
            "combine_backward_dropless", "experts_backward_dropless", "dispatch_backward_dropless",
            "BackwardRouted", "scoring", "route_scored", "route_scored_backward", "quantize", "gemm_quant",
-           "experts_dropless_quant", "library", "MoeError"]
+           "experts_dropless_quant", "quantize_weights", "ForwardDroplessQuant", "library", "MoeError"]
 
 MoeError = abi.MoeError
 _DT = {"f32": abi.MOE_F32, "bf16": abi.MOE_BF16, torch.float32: abi.MOE_F32,
@@ -706,3 +706,77 @@ def experts_dropless_quant(cfg, xs, expert_offsets, w_gate, w_up, w_down, expert
     _launch("moe_experts_dropless_quant", dev, C.byref(cfg), xs.data_ptr(), expert_offsets.data_ptr(), C.byref(w),
             expert_out.data_ptr(), ws.data_ptr(), ws.numel())
     return expert_out
+
+
+def quantize_weights(cfg, weights: Dict[str, torch.Tensor]) -> Dict:
+    """The weights of a branch (bf16 or fp32, the names of Forward's) in the
+    form ForwardDroplessQuant takes: (q, scales) pairs in 128 x 128 blocks,
+    the up-projection and the shared down-projections side by side as
+    w_output; the router stays bf16."""
+    def blocks(w):
+        q, s = quantize(w.reshape(-1, w.shape[-1]), 128)
+        return q.view(w.shape), s.view(*w.shape[:-2], w.shape[-2] // 128, w.shape[-1] // 128)
+    out = {n: blocks(weights[n]) for n in ("w_latent", "w_gate", "w_up", "w_down")}
+    cols = [weights["w_up_proj"]]
+    if cfg.n_shared:
+        out.update({n: blocks(weights[n]) for n in ("ws_gate", "ws_up")})
+        cols += list(weights["ws_down"])
+    out["w_output"] = blocks(torch.cat(cols, dim=1).contiguous())
+    out["w_router"] = weights["w_router"].to(torch.bfloat16)
+    out["router_bias"] = weights.get("router_bias")
+    return out
+
+
+class ForwardDroplessQuant:
+    """Reusable dropless forward in e4m3 with scored routing
+    (moe_forward_dropless_quant): weights (quantize_weights), workspace and
+    outputs bound once."""
+
+    def __init__(self, cfg, sc: abi.MoeScoring, weights: Dict, device, taps=False):
+        device = torch.device(device)
+        if device.index is None:
+            device = torch.device(device.type, torch.cuda.current_device())
+        self.cfg, self.sc, self.w, self.p = cfg, sc, weights, plan(cfg)
+        n = C.c_size_t(0)
+        abi.check("moe_forward_dropless_quant_ws_bytes",
+                  library().moe_forward_dropless_quant_ws_bytes(C.byref(cfg), C.byref(n)))
+        T, D, L, E, k = cfg.T, cfg.d_model, cfg.d_latent, cfg.n_experts, cfg.top_k
+        S, Fs = cfg.n_shared, cfg.d_ff_shared
+        W = L + S * Fs
+
+        def pair(name, shape):
+            q, s = weights[name]
+            return (_rows(q, shape, torch.float8_e4m3fn, name + "[0]", device).data_ptr(),
+                    _rows(s, (*shape[:-2], shape[-2] // 128, shape[-1] // 128), torch.float32, name + "[1]",
+                          device).data_ptr())
+        f = dict(w_router=_rows(weights["w_router"], (E, L), torch.bfloat16, "w_router", device).data_ptr(),
+                 experts=_quant_experts(cfg, weights["w_gate"], weights["w_up"], weights["w_down"], device))
+        if weights.get("router_bias") is not None:
+            f["router_bias"] = _rows(weights["router_bias"], (E,), torch.float32, "router_bias", device).data_ptr()
+        f["q_latent"], f["s_latent"] = pair("w_latent", (L, D))
+        f["q_output"], f["s_output"] = pair("w_output", (D, W))
+        if S:
+            f["q_shared_gate"], f["s_shared_gate"] = pair("ws_gate", (S, Fs, D))
+            f["q_shared_up"], f["s_shared_up"] = pair("ws_up", (S, Fs, D))
+        self.wstruct = abi.MoeQuantWeights(**f)
+        self.ws = _ws(n.value, device)
+        self.y = torch.empty((T, D), dtype=torch.bfloat16, device=device)
+        self.counts = torch.empty(3, dtype=torch.int64, device=device)
+        self.taps, self.tap_t = None, {}
+        if taps:
+            rows = self.p["dropless_rows"]
+            i32, bf = dict(dtype=torch.int32, device=device), dict(dtype=torch.bfloat16, device=device)
+            self.tap_t = dict(
+                logits=torch.empty((T, E), dtype=torch.float32, device=device), topk_idx=torch.empty((T, k), **i32),
+                gates=torch.empty((T, k), dtype=torch.float32, device=device), row_of=torch.empty((T, k), **i32),
+                expert_offsets=torch.empty(E + 1, **i32), z=torch.empty((T, L), **bf), xs=torch.empty((rows, L), **bf),
+                expert_out=torch.empty((rows, L), **bf), y_latent=torch.empty((T, L), **bf))
+            self.taps = abi.MoeDroplessTaps(**{m: t.data_ptr() for m, t in self.tap_t.items()})
+
+    def __call__(self, x: torch.Tensor):
+        cfg = self.cfg
+        _rows(x, (cfg.T, cfg.d_model), torch.bfloat16, "x", self.y.device)
+        _launch("moe_forward_dropless_quant", self.y.device, C.byref(cfg), C.byref(self.sc), C.byref(self.wstruct),
+                x.data_ptr(), self.y.data_ptr(), C.byref(self.taps) if self.taps is not None else None,
+                self.counts.data_ptr(), self.ws.data_ptr(), self.ws.numel())
+        return self.y

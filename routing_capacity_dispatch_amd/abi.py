@@ -80,6 +80,13 @@ class MoeQuantExperts(C.Structure):
     _fields_ = [(n, C.c_void_p) for n in ("q_gate", "s_gate", "q_up", "s_up", "q_down", "s_down")]
 
 
+class MoeQuantWeights(C.Structure):
+    _fields_ = ([(n, C.c_void_p) for n in ("q_latent", "s_latent", "w_router", "router_bias")]
+                + [("experts", MoeQuantExperts)]
+                + [(n, C.c_void_p) for n in ("q_shared_gate", "s_shared_gate", "q_shared_up", "s_shared_up", "q_output",
+                                             "s_output")])
+
+
 # exported symbols and their signatures
 _P = C.c_void_p
 SIGNATURES = {
@@ -148,6 +155,9 @@ SIGNATURES = {
     "moe_gemm_quant_ws_bytes": (C.c_int, [C.POINTER(MoeQuantGemm), C.POINTER(C.c_size_t)]),
     "moe_gemm_quant": (C.c_int, [C.POINTER(MoeQuantGemm), _P, C.c_size_t, _P]),
     "moe_experts_dropless_quant_ws_bytes": (C.c_int, [C.POINTER(MoeConfig), C.POINTER(C.c_size_t)]),
+    "moe_forward_dropless_quant_ws_bytes": (C.c_int, [C.POINTER(MoeConfig), C.POINTER(C.c_size_t)]),
+    "moe_forward_dropless_quant": (C.c_int, [C.POINTER(MoeConfig), C.POINTER(MoeScoring), C.POINTER(MoeQuantWeights), _P,
+                                             _P, C.POINTER(MoeDroplessTaps), _P, _P, C.c_size_t, _P]),
     "moe_experts_dropless_quant": (C.c_int, [C.POINTER(MoeConfig), _P, _P, C.POINTER(MoeQuantExperts), _P, _P,
                                              C.c_size_t, _P]),
 }

@@ -1763,3 +1763,222 @@ MOE_API moe_status moe_experts_dropless_quant(const moe_config* cfg, const void*
     return MOE_ERR_WORKSPACE;
   return run_experts_quant(cfg, p, xs, expert_offsets, w, expert_out, ws, static_cast<hipStream_t>(stream));
 }
+
+// ------------------------------------------------------------------ dropless forward in e4m3
+namespace {
+
+struct QuantForwardWs {
+  char* xq;       // quantised x and its scales
+  float* xs;
+  char* z;
+  float* logits;
+  int32_t* topk;
+  float* gates;
+  int32_t* row_of;
+  int32_t* offsets;
+  char* rows;     // xs of the dispatch
+  char* expert_out;
+  char* y_lat;
+  char* cat;      // [T][L + S Fs]: quantised y_lat and shared hidden rows
+  float* cat_s;
+  float* h;       // few tokens: shared hidden rows in fp32
+  int64_t* counts;
+  void* dispatch;
+  void* experts;
+  void* gemm;
+};
+
+moe::QuantGemm dense_quant(const char* A, const float* sa, int64_t T, const void* B, const float* sb, int64_t N,
+                           int64_t K, void* C) {
+  moe::QuantGemm g{};
+  g.A = A;
+  g.lda = K;
+  g.a_scale = sa;
+  g.a_scale_ld = T;
+  g.B = static_cast<const char*>(B);
+  g.ldb = K;
+  g.b_scale = sb;
+  g.b_scale_ld = K / 128;
+  g.b_rows = 128;
+  g.M = T;
+  g.N = N;
+  g.K = (int)K;
+  g.out_dt = moe::DT_BF16;
+  g.C = C;
+  g.ldc = N;
+  return g;
+}
+
+int64_t carve_forward_quant(const moe_config* c, const moe_plan& p, const moe_dropless_taps& tp, int64_t* counts,
+                            void* ws, QuantForwardWs* w) {
+  const int64_t T = c->T, D = c->d_model, L = c->d_latent, E = c->n_experts, k = c->top_k, n = p.dropless_rows;
+  const int64_t W = L + (int64_t)c->n_shared * c->d_ff_shared;
+  Carver cv{static_cast<char*>(ws), 0};
+  auto pick = [&](void* tap, int64_t bytes) {
+    void* q = cv.take(bytes);
+    return tap ? tap : q;
+  };
+  w->xq = static_cast<char*>(cv.take(T * D));
+  w->xs = static_cast<float*>(cv.take(T * (D / 128) * 4));
+  w->z = static_cast<char*>(pick(tp.z, T * L * 2));
+  w->logits = static_cast<float*>(pick(tp.logits, T * E * 4));
+  w->topk = static_cast<int32_t*>(pick(tp.topk_idx, T * k * 4));
+  w->gates = static_cast<float*>(pick(tp.gates, T * k * 4));
+  w->row_of = static_cast<int32_t*>(pick(tp.row_of, T * k * 4));
+  w->offsets = static_cast<int32_t*>(pick(tp.expert_offsets, (E + 1) * 4));
+  w->rows = static_cast<char*>(pick(tp.xs, n * L * 2));
+  w->expert_out = static_cast<char*>(pick(tp.expert_out, n * L * 2));
+  w->y_lat = static_cast<char*>(pick(tp.y_latent, T * L * 2));
+  w->cat = static_cast<char*>(cv.take(T * W));
+  w->cat_s = static_cast<float*>(cv.take(T * (W / 128) * 4));
+  w->h = static_cast<float*>(cv.take(moe::few_rows(T, c->n_shared, false) ? T * (W - L) * 4 : 0));
+  w->counts = static_cast<int64_t*>(pick(counts, 3 * 8));
+  w->dispatch = cv.take(p.dropless_dispatch_ws_bytes);
+  QuantExpertsWs x;
+  w->experts = cv.take(carve_experts_quant(c, n, nullptr, &x));
+  const int64_t g0 = moe::quant_gemm_ws_bytes(dense_quant(nullptr, nullptr, T, nullptr, nullptr, L, D, nullptr));
+  const int64_t g1 = moe::quant_gemm_ws_bytes(dense_quant(nullptr, nullptr, T, nullptr, nullptr, D, W, nullptr));
+  w->gemm = cv.take(g0 > g1 ? g0 : g1);
+  return cv.used;
+}
+
+moe_status check_forward_quant(const moe_config* cfg, moe_plan* p) {
+  moe_status st = check_quant_config(cfg, p);
+  if (st != MOE_OK) return st;
+  if (cfg->top_k > cfg->n_experts) return MOE_ERR_INVALID_ARG;
+  if (cfg->n_experts % 4 || cfg->d_model % 128 || (cfg->n_shared > 0 && cfg->d_ff_shared % 128))
+    return MOE_ERR_UNSUPPORTED;
+  // the two dense products and the shared hidden tiles, within the limits of moe_gemm_quant
+  const int64_t W = cfg->d_latent + (int64_t)cfg->n_shared * cfg->d_ff_shared;
+  const int64_t widest = cfg->d_model > W ? cfg->d_model : W;
+  if (widest > kMaxQuantK || cfg->T > kMaxQuantRows || ceil_div(cfg->T, 64) * ceil_div(widest, 128) > kMaxListEntries)
+    return MOE_ERR_UNSUPPORTED;
+  return MOE_OK;
+}
+
+}  // namespace
+
+MOE_API moe_status moe_forward_dropless_quant_ws_bytes(const moe_config* cfg, size_t* bytes) {
+  moe_plan p;
+  moe_status st = check_forward_quant(cfg, &p);
+  if (st != MOE_OK) return st;
+  if (!bytes) return MOE_ERR_INVALID_ARG;
+  QuantForwardWs w;
+  *bytes = (size_t)carve_forward_quant(cfg, p, moe_dropless_taps{}, nullptr, nullptr, &w);
+  return MOE_OK;
+}
+
+MOE_API moe_status moe_forward_dropless_quant(const moe_config* cfg, const moe_scoring* scoring,
+                                              const moe_quant_weights* w, const void* x, void* y,
+                                              const moe_dropless_taps* taps, int64_t* counts, void* ws,
+                                              size_t ws_bytes, void* stream) {
+  moe_plan p;
+  moe_status st = check_forward_quant(cfg, &p);
+  if (st != MOE_OK) return st;
+  moe::ScoreArgs sc{};
+  st = check_scoring(cfg, scoring, &sc);
+  if (st != MOE_OK) return st;
+  if (!w || !w->q_latent || !w->s_latent || !w->w_router || !quant_experts_valid(&w->experts) || !w->q_output ||
+      !w->s_output || !aligned16(w->q_latent) || !aligned16(w->w_router) || !aligned16(w->q_output))
+    return MOE_ERR_INVALID_ARG;
+  if (cfg->n_shared > 0 && (!w->q_shared_gate || !w->s_shared_gate || !w->q_shared_up || !w->s_shared_up ||
+                            !aligned16(w->q_shared_gate) || !aligned16(w->q_shared_up)))
+    return MOE_ERR_INVALID_ARG;
+  if (cfg->T > 0 && (!x || !y || !aligned16(x) || !aligned16(y))) return MOE_ERR_INVALID_ARG;
+  const moe_dropless_taps none{};
+  const moe_dropless_taps& tp = taps ? *taps : none;
+  for (const void* t : {static_cast<const void*>(tp.logits), static_cast<const void*>(tp.z),
+                        static_cast<const void*>(tp.xs), static_cast<const void*>(tp.expert_out),
+                        static_cast<const void*>(tp.y_latent)})
+    if (!aligned16(t)) return MOE_ERR_INVALID_ARG;
+  QuantForwardWs q;
+  if (!ws || !aligned256(ws) || (int64_t)ws_bytes < carve_forward_quant(cfg, p, none, nullptr, nullptr, &q))
+    return MOE_ERR_WORKSPACE;
+  carve_forward_quant(cfg, p, tp, counts, ws, &q);
+
+  hipStream_t s = static_cast<hipStream_t>(stream);
+  const int64_t T = cfg->T, D = cfg->d_model, L = cfg->d_latent, E = cfg->n_experts, S = cfg->n_shared;
+  const int64_t Fs = S > 0 ? cfg->d_ff_shared : 0, W = L + S * Fs;
+  auto quantize = [&](const void* from, int dt, int64_t cols, char* to, int64_t ldq, float* scale) {
+    moe::QuantizeArgs a{};
+    a.x = from;
+    a.rows = T;
+    a.cols = a.ld = cols;
+    a.dt = dt;
+    a.block_rows = 1;
+    a.q = to;
+    a.ldq = ldq;
+    a.scale = scale;
+    a.scale_ld = T;
+    return moe::launch_quantize(a, s);
+  };
+  // z, then the router on it
+  hipError_t e = quantize(x, moe::DT_BF16, D, q.xq, D, q.xs);
+  if (e == hipSuccess)
+    e = moe::launch_quant_gemm(dense_quant(q.xq, q.xs, T, w->q_latent, w->s_latent, L, D, q.z), q.gemm, s);
+  if (e != hipSuccess) return MOE_ERR_HIP;
+  moe::GemmDense r{};
+  r.nseg = 1;
+  r.seg[0] = {q.z, L, w->w_router, L, (int)L};
+  r.C = q.logits;
+  r.ldc = E;
+  r.M = (int)T;
+  r.N = (int)E;
+  e = moe::launch_gemm_dense(moe::DT_BF16, moe::DT_F32, r, s);
+  if (e == hipSuccess) e = moe::launch_route_scored(sc, q.logits, w->router_bias, q.topk, q.gates, s);
+  if (e != hipSuccess) return MOE_ERR_HIP;
+  // the routed path
+  st = run_dispatch_dropless(cfg, p, q.topk, q.z, q.rows, q.row_of, q.offsets, q.counts, q.dispatch, s, nullptr);
+  if (st != MOE_OK) return st;
+  if (T > 0) {
+    st = run_experts_quant(cfg, p, q.rows, q.offsets, &w->experts, q.expert_out, q.experts, s);
+    if (st != MOE_OK) return st;
+  }
+  e = moe::launch_ragged_combine(moe::DT_BF16, q.expert_out, q.row_of, q.gates, T, cfg->top_k, L * 2, q.y_lat, s);
+  if (e == hipSuccess) e = quantize(q.y_lat, moe::DT_BF16, L, q.cat, W, q.cat_s);
+  if (e != hipSuccess) return MOE_ERR_HIP;
+  // shared hidden rows beside it
+  if (S > 0 && T > 0) {
+    if (moe::few_rows(T, (int)S, false)) {
+      moe::FewRows u{};
+      u.x = q.xq;
+      u.ldx = D;
+      u.x_scale = q.xs;
+      u.x_scale_ld = T;
+      u.W0 = static_cast<const char*>(w->q_shared_gate);
+      u.s0 = w->s_shared_gate;
+      u.W1 = static_cast<const char*>(w->q_shared_up);
+      u.s1 = w->s_shared_up;
+      u.M = T;
+      u.E = (int)S;
+      u.N = (int)Fs;
+      u.K = (int)D;
+      u.chunk = 16;
+      u.out = q.h;
+      u.ldo = S * Fs;
+      e = moe::launch_few_rows(u, true, false, s);
+      if (e == hipSuccess) e = quantize(q.h, moe::DT_F32, S * Fs, q.cat + L, W, q.cat_s + (L / 128) * T);
+    } else {
+      moe::QuantGateUp u{};
+      u.A = q.xq;
+      u.lda = D;
+      u.a_scale = q.xs;
+      u.a_scale_ld = T;
+      u.Wg = static_cast<const char*>(w->q_shared_gate);
+      u.sg = w->s_shared_gate;
+      u.Wu = static_cast<const char*>(w->q_shared_up);
+      u.su = w->s_shared_up;
+      u.M = T;
+      u.E = (int)S;
+      u.F = (int)Fs;
+      u.K = (int)D;
+      u.H = q.cat + L;
+      u.ldh = W;
+      u.h_scale = q.cat_s + (L / 128) * T;
+      u.h_scale_ld = T;
+      e = moe::launch_quant_gate_up(u, s);
+    }
+    if (e != hipSuccess) return MOE_ERR_HIP;
+  }
+  return hip_status(moe::launch_quant_gemm(dense_quant(q.cat, q.cat_s, T, w->q_output, w->s_output, D, W, y), q.gemm, s));
+}

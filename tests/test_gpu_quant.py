@@ -485,3 +485,86 @@ def test_route_dispatch_experts_combine_together():
             bound += g[t, j] * b[0]
         bound = bound + 2.0 ** -8 * (np.abs(ref) + bound) + 2.0 ** -18 * np.abs(ref)
         assert (np.abs(np64(y[t]) - ref) <= bound).all()
+
+
+@pytest.mark.parametrize("T,S,taps", [(1, 2, True), (5, 1, False), (8, 2, True), (9, 2, True), (200, 2, True), (300, 0, True),
+                                      (700, 3, True)])
+def test_forward_dropless_quant(T, S, taps):
+    d = dev()
+    say("forward_dropless_quant", T, S)
+    w = synth.workload("mid_bf16").replace(T=T, n_shared=S)
+    cfg = rcd.config_of(w)
+    inp = synth.make_inputs(w, 7, device=d)
+    wq = rcd.quantize_weights(cfg, {k: v for k, v in inp.items() if k != "x"})
+    sc = rcd.scoring("sigmoid", 8, 4, 2, True, 2.5)
+    f = rcd.ForwardDroplessQuant(cfg, sc, wq, d, taps=True)
+    y = f(inp["x"]).clone()
+    torch.cuda.synchronize()
+    t = f.tap_t
+    # every step is the public entry point's, bit for bit
+    xq, xs = rcd.quantize(inp["x"])
+    assert torch.equal(t["z"], rcd.gemm_quant(xq, xs, *wq["w_latent"]))
+    topk, gates = rcd.route_scored(cfg, sc, t["logits"], wq["router_bias"])
+    assert torch.equal(t["topk_idx"], topk) and torch.equal(t["gates"], gates)
+    ds = rcd.dispatch_dropless(cfg, topk, t["z"])
+    assert torch.equal(t["xs"], ds["xs"]) and torch.equal(t["expert_offsets"], ds["expert_offsets"])
+    eo = rcd.experts_dropless_quant(cfg, ds["xs"], ds["expert_offsets"], wq["w_gate"], wq["w_up"], wq["w_down"])
+    assert torch.equal(t["expert_out"], eo)
+    y_lat = rcd.combine_dropless(cfg, eo, ds["row_of"], gates)
+    assert torch.equal(t["y_latent"], y_lat)
+    assert f.counts.tolist() == [T * cfg.top_k, 0, 0]
+    # the output from y_lat and the shared hidden rows, in fp64 on the quantised values
+    parts = [bq.values(*bq.quantize(np64(y_lat)), 1)]
+    x = bq.values(np64(xq), np64(xs).T, 1)
+    for s_ in range(S):
+        a, b = (x @ bq.values(np64(wq[n][0][s_]), np64(wq[n][1][s_]), 128).T for n in ("ws_gate", "ws_up"))
+        parts.append(bq.values(*bq.quantize(bq.silu(a) * b), 1))
+    ref = np.concatenate(parts, axis=1) @ bq.values(np64(wq["w_output"][0]), np64(wq["w_output"][1]), 128).T
+    err = np.linalg.norm(np64(y) - ref, axis=1) / np.linalg.norm(ref, axis=1)
+    # y's own rounding is 2^-9 of it at most.  A hidden value lands one e4m3
+    # step (2^-3 of it at most) off if it lies within the 8-bit products'
+    # dropped bits (2^-12 of the row) of a tie, and ties are 2^-4 of a value
+    # apart or more: less than one in a hundred, 2^-3 sqrt(1/100) = 0.8 2^-6
+    assert (err <= 2.0 ** -6).all(), err.max()
+    # without taps, the same bits
+    g = rcd.ForwardDroplessQuant(cfg, sc, wq, d)
+    assert torch.equal(g(inp["x"]), y)
+
+
+def test_forward_dropless_quant_graph_replays():
+    d = dev()
+    w = synth.workload("mid_bf16").replace(T=96)
+    cfg = rcd.config_of(w)
+    inp = synth.make_inputs(w, 8, device=d)
+    wq = rcd.quantize_weights(cfg, {k: v for k, v in inp.items() if k != "x"})
+    sc = rcd.scoring("softmax", renormalise=False)
+    f, ref = (rcd.ForwardDroplessQuant(cfg, sc, wq, d) for _ in range(2))
+    xs = [synth.make_inputs(w, s, device=d)["x"] for s in (8, 9, 10)]
+    x = xs[0].clone()
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        f(x)
+    torch.cuda.current_stream().wait_stream(side)
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        f(x)
+    for xi in xs + xs[:1]:
+        x.copy_(xi)
+        f.y.zero_()
+        torch.cuda.synchronize()
+        graph.replay()
+        torch.cuda.synchronize()
+        assert torch.equal(f.y, ref(xi)) and torch.equal(f.counts, ref.counts)
+
+
+def test_forward_dropless_quant_without_tokens():
+    d = dev()
+    w = synth.workload("mid_bf16").replace(T=0)
+    inp = synth.make_inputs(w, 7, device=d)
+    cfg = rcd.config_of(w)
+    f = rcd.ForwardDroplessQuant(cfg, rcd.scoring(), rcd.quantize_weights(cfg, {k: v for k, v in inp.items() if k != "x"}), d)
+    assert f(torch.empty((0, cfg.d_model), dtype=torch.bfloat16, device=d)).shape == (0, cfg.d_model)
+    torch.cuda.synchronize()
+    assert f.counts.tolist() == [0, 0, 0]

@@ -203,3 +203,28 @@ def test_graph_replays_and_side_stream():
         d2 = rcd.route_scored_backward(cfg, sc, ls[i], t2, dgs[i])
         torch.cuda.synchronize()
         assert torch.equal(out["topk_idx"], t2) and torch.equal(out["gates"], g2) and torch.equal(dl, d2)
+
+
+@pytest.mark.parametrize("kind", ["sigmoid", "softmax"])
+@pytest.mark.parametrize("lower", [False, True])
+@pytest.mark.parametrize("E,G,tg,k", [(256, 8, 1, 2), (256, 8, 2, 4), (64, 4, 2, 4), (1024, 8, 2, 8)])
+def test_group_boundary_below_fp32(E, G, tg, k, lower, kind):
+    # Equal scores (exact: 1/2, or 1/E), so the bias ranks the groups.  Two
+    # groups' pairs of largest biases sum to 0.375 and 0.375 + 2^-26 (or
+    # - 2^-26): fp32 sums of the keys cannot tell them apart, while the keys
+    # themselves are far from each other.  The other tokens are ordinary.
+    rng = np.random.default_rng(E + tg)
+    size = E // G
+    bias = (-1 - np.arange(E) / E).astype(np.float32)
+    a, b = 1, G - 2  # a would win a tie
+    bias[a * size + 1], bias[a * size + 5] = 0.25, 0.125
+    bias[b * size + 2] = 0.15625
+    bias[b * size + 4] = np.float32(0.21875 + (-1 if lower else 1) * 2.0 ** -26)
+    assert float(bias[b * size + 4]) != 0.21875
+    if tg == 2:  # one group above both
+        bias[0], bias[1] = 0.5, 0.4375
+    logits = np.zeros((21, E), dtype=np.float32)
+    logits[1::3] = rng.standard_normal((7, E))
+    ref = sr.select(logits, bias, k, kind, G, tg, 2)
+    assert (a if lower else b) in ref[0] // size and (b if lower else a) not in ref[0] // size
+    check(21, E, k, logits, bias, kind, G, tg, 2)

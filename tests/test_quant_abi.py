@@ -146,3 +146,38 @@ def test_binding_refuses_tensors_the_kernels_cannot_take():
         rcd.gemm_quant(q, torch.zeros((2, 4)), q, torch.zeros((1, 2)))
     with pytest.raises(ValueError):
         rcd.experts_dropless_quant(rcd.make_config(4, 64, 128, 4, 1, 1, 128), x, None, None, None, None)
+
+
+def test_forward_quant_refusals(lib):
+    assert C.sizeof(abi.MoeQuantWeights) == 16 * 8
+    sc = rcd.scoring("sigmoid", 4, 2)
+
+    def call(cfg, scoring=sc, w=None, x=FAKE, y=FAKE, taps=None, ws=FAKE, n=1 << 40):
+        w = w or weights()
+        return lib.moe_forward_dropless_quant(C.byref(cfg), scoring and C.byref(scoring), C.byref(w), x, y,
+                                              taps and C.byref(taps), NUL, ws, n, NUL)
+
+    def weights(**kw):
+        w = abi.MoeQuantWeights(experts=abi.MoeQuantExperts(*([0x100000] * 6)))
+        for name, _ in w._fields_:
+            if name != "experts":
+                setattr(w, name, kw.get(name, 0x100000))
+        return w
+    shape = dict(T=64, d_model=256, d_latent=128, n_experts=16, n_pools=1, top_k=2, d_ff=128, n_shared=2, d_ff_shared=128)
+    cfg = rcd.make_config(**shape)
+    n = C.c_size_t(0)
+    assert lib.moe_forward_dropless_quant_ws_bytes(C.byref(cfg), C.byref(n)) == OK and n.value % 256 == 0
+    # quantised x and the joined operand, the dispatched rows and the experts' outputs among it
+    assert n.value >= 64 * 256 + 64 * 384 + 2 * 128 * 128 * 2
+    assert lib.moe_forward_dropless_quant_ws_bytes(C.byref(cfg), None) == INV
+    for name in ("q_latent", "s_latent", "w_router", "q_output", "s_output", "q_shared_gate", "s_shared_up"):
+        assert call(cfg, w=weights(**{name: 0})) == INV, name
+    assert call(cfg, w=weights(q_output=0x100008)) == INV
+    assert call(cfg, scoring=None) == INV and call(cfg, x=NUL) == INV and call(cfg, y=C.c_void_p(0x100002)) == INV
+    assert call(cfg, taps=abi.MoeDroplessTaps(z=0x100008)) == INV
+    assert call(cfg, ws=NUL) == WS and call(cfg, n=n.value - 1) == WS and call(cfg, ws=C.c_void_p(0x100010)) == WS
+    for field, value, status in (("d_model", 320, UNS), ("d_latent", 192, UNS), ("d_ff_shared", 64, UNS),
+                                 ("n_experts", 18, UNS), ("top_k", 17, INV)):
+        bad = rcd.make_config(**{**shape, field: value})
+        assert call(bad, scoring=rcd.scoring("sigmoid")) == status, field
+    assert call(rcd.make_config(**shape, dtype="f32")) == UNS
