@@ -433,10 +433,9 @@ struct QAcc {
 };
 
 // Sum over K blocks [0, nb).  The steps of consecutive blocks run into one
-// another, so that
-// the matrix cores always have operands in registers: while the MFMAs of one
-// row block run, the fragment of the next is read from LDS, and the results
-// before are scaled and added.  At the last row block every read of this
+// another, so that the matrix cores always have operands in registers: while
+// the MFMAs of one row block run, the fragment of the next is read from LDS,
+// and the results before are scaled and added.  At the last row block every read of this
 // stage is done: one barrier (the next block has landed; this stage is free),
 // then the loads of the block after next and the next block's first fragments
 // go in among its MFMAs, each B fragment into the registers that its last
@@ -1081,22 +1080,24 @@ constexpr int kStagedK = 4096;
 bool few_rows(int64_t M, int E, bool grouped) { return (grouped ? cdiv(M, E) : M) <= kFewRows; }
 bool few_rows_stage(int K) { return K <= kStagedK; }
 
-template <int KS>
-void launch_few_as(const FewRows& g, bool hidden, bool staged, hipStream_t s) {
+template <int KS, int kSource, bool kHidden>
+hipError_t launch_few_of(const FewRows& g, hipStream_t s) {
   const dim3 grid((unsigned)(g.N / (16 * (kSkinnyWaves / KS))), (unsigned)g.E);
-  constexpr int T = 64 * kSkinnyWaves;
-  const size_t lds = staged ? g.chunk * (size_t)(g.K + kRowPad) + 16 * 4 * (size_t)(g.K / kQB) : 0;
-  if (hidden) {
-    if (staged)
-      few_rows_kernel<KS, kBf16, true><<<grid, T, lds, s>>>(g);
-    else
-      few_rows_kernel<KS, kE4m3, true><<<grid, T, 0, s>>>(g);
-  } else {
-    if (staged)
-      few_rows_kernel<KS, kF32, false><<<grid, T, lds, s>>>(g);
-    else
-      few_rows_kernel<KS, kE4m3, false><<<grid, T, 0, s>>>(g);
+  const size_t lds =
+      kSource == kE4m3 ? 0 : g.chunk * (size_t)(g.K + kRowPad) + 16 * sizeof(float) * (size_t)(g.K / kQB);
+  if (lds >= 64 * 1024) {
+    const hipError_t e = hipFuncSetAttribute(reinterpret_cast<const void*>(few_rows_kernel<KS, kSource, kHidden>),
+                                             hipFuncAttributeMaxDynamicSharedMemorySize, (int)lds);
+    if (e != hipSuccess) return e;
   }
+  few_rows_kernel<KS, kSource, kHidden><<<grid, 64 * kSkinnyWaves, lds, s>>>(g);
+  return hipGetLastError();
+}
+
+template <int KS>
+hipError_t launch_few_as(const FewRows& g, bool hidden, bool staged, hipStream_t s) {
+  if (hidden) return staged ? launch_few_of<KS, kBf16, true>(g, s) : launch_few_of<KS, kE4m3, true>(g, s);
+  return staged ? launch_few_of<KS, kF32, false>(g, s) : launch_few_of<KS, kE4m3, false>(g, s);
 }
 
 hipError_t launch_few_rows(const FewRows& g, bool hidden, bool staged, hipStream_t s) {
@@ -1107,12 +1108,9 @@ hipError_t launch_few_rows(const FewRows& g, bool hidden, bool staged, hipStream
   const int64_t tiles = busy * (g.N / 16);
   const int nb = g.K / kQB;
   if (tiles / kSkinnyWaves >= 768 || nb < 4)
-    launch_few_as<1>(g, hidden, staged, s);
-  else if (tiles * 2 / kSkinnyWaves >= 768 || nb < 8)
-    launch_few_as<2>(g, hidden, staged, s);
-  else
-    launch_few_as<4>(g, hidden, staged, s);
-  return hipGetLastError();
+    return launch_few_as<1>(g, hidden, staged, s);
+  if (tiles * 2 / kSkinnyWaves >= 768 || nb < 8) return launch_few_as<2>(g, hidden, staged, s);
+  return launch_few_as<4>(g, hidden, staged, s);
 }
 
 hipError_t launch_quant_gate_up(const QuantGateUp& g, hipStream_t s) {
