@@ -435,11 +435,14 @@ struct QAcc {
 // Sum over K blocks [0, nb).  The steps of consecutive blocks run into one
 // another, so that the matrix cores always have operands in registers: while
 // the MFMAs of one row block run, the fragment of the next is read from LDS,
-// and the results before are scaled and added.  At the last row block every read of this
-// stage is done: one barrier (the next block has landed; this stage is free),
-// then the loads of the block after next and the next block's first fragments
-// go in among its MFMAs, each B fragment into the registers that its last
-// MFMA has just read.  Ends with a barrier, so the caller may reuse the LDS.
+// and the results before are scaled and added.  All of a block's B fragments
+// are in registers from its start, so after its first row block (one barrier)
+// its B stage takes the block after next, whose loads have nearly two blocks'
+// time.  At the last row block every read of the A stage is done: one barrier
+// (the next block has landed; this A stage is free), then the A loads of the
+// block after next and the next block's first fragments go in among its MFMAs,
+// each B fragment into the registers that its last MFMA has just read.  Ends
+// with a barrier, so the caller may reuse the LDS.
 // MI: row blocks computed, the wavefront's first ones (see pipe_rows).
 // KG: groups of wavefronts that share the blocks; src, nb, lds and wave are
 // those of one group, whose blocks lie KG apart.
@@ -455,7 +458,7 @@ __device__ __forceinline__ void quant_pipe(Stager<TL>& src, int nb, char* lds, Q
 #pragma unroll
     for (int ni = 0; ni < NI; ++ni) acc.v[mi][ni] = f32x4_t{0.f, 0.f, 0.f, 0.f};
   if (nb <= 0) return;
-  // load instruction i of the next block, into stage st: A rows, B rows, scales
+  // load instruction i of a block, into stage st: rows of A, rows of B, scales
   constexpr int P = TL::A_INS + TL::B_INS + 1;
   const uint32_t lds_rows = lds_address(lds + wave * 1024);
   const uint32_t lds_scales = lds_address(lds + Q::S_BASE + wave * 256);
@@ -465,10 +468,10 @@ __device__ __forceinline__ void quant_pipe(Stager<TL>& src, int nb, char* lds, Q
       stage16<i * TL::NW * 1024>(lds_rows + st * TL::A_BYTES, src.a, src.a_off[i]);
     } else if constexpr (i < TL::A_INS + TL::B_INS) {
       stage16<TL::B_BASE + (i - TL::A_INS) * TL::NW * 1024>(lds_rows + st * TL::B_BYTES, src.b, src.b_off[i - TL::A_INS]);
+      if constexpr (i == TL::A_INS + TL::B_INS - 1) src.b += KG * kQB;
     } else {
       stage4<0>(lds_scales + st * Q::SCALES * 4, src.s);
       src.a += KG * kQB;
-      src.b += KG * kQB;
       src.s += src.s_step;
     }
   };
@@ -507,6 +510,14 @@ __device__ __forceinline__ void quant_pipe(Stager<TL>& src, int nb, char* lds, Q
   issue_range(0, integral_constant<int, 0>{}, integral_constant<int, P>{});
   core::wait_loads<0>();
   if (nb > 1) issue_range(1, integral_constant<int, 0>{}, integral_constant<int, P>{});
+  // instructions of A and the scales, in their order
+  constexpr int PA = TL::A_INS + 1;
+  auto issue_a = [&](int st, auto first, auto last) {
+    for_range<decltype(first)::value, decltype(last)::value>([&](auto i) {
+      constexpr int k = decltype(i)::value;
+      issue(st, integral_constant<int, k < TL::A_INS ? k : TL::A_INS + TL::B_INS>{});
+    });
+  };
   Frag8 fb[NI], fa[2];
   float as[2];
   BScale bs[NBS], bs_next[NBS];
@@ -546,6 +557,12 @@ __device__ __forceinline__ void quant_pipe(Stager<TL>& src, int nb, char* lds, Q
 #pragma unroll
     for (int mi = 0; mi < MI; ++mi) {
       const bool last = mi == MI - 1;
+      if (mi == 1 && more2) {
+        // every wavefront holds this block's B fragments: their stage is free
+        __builtin_amdgcn_s_barrier();
+        __builtin_amdgcn_sched_barrier(0);
+        if (last) issue_range(st, integral_constant<int, TL::A_INS>{}, integral_constant<int, TL::A_INS + TL::B_INS>{});
+      }
       if constexpr (kMode == kRowB)
         sc[mi & 1][0] = as[mi & 1];
       else
@@ -555,7 +572,7 @@ __device__ __forceinline__ void quant_pipe(Stager<TL>& src, int nb, char* lds, Q
         fa[(mi + 1) & 1] = read_a(st, mi + 1);
         as[(mi + 1) & 1] = read_as(st, mi + 1);
       } else if (more) {
-        core::wait_loads<0>();
+        core::wait_loads<more2 ? TL::B_INS : 0>();
         fa[0] = read_a(st ^ 1, 0);
         as[0] = read_as(st ^ 1, 0);
         if constexpr (kMode != kRowB) read_bs(st ^ 1, bs_next);
@@ -571,8 +588,10 @@ __device__ __forceinline__ void quant_pipe(Stager<TL>& src, int nb, char* lds, Q
           p[j % (kLag + 1)] = mfma_block(fb[ni], fa[mi & 1]);
         if (last) {
           if (more) fb[ni] = read_b(st ^ 1, ni);
-          // the block after next: instructions [ni P / NI, (ni + 1) P / NI)
-          if (more2) issue_range(st, integral_constant<int, ni * P / NI>{}, integral_constant<int, (ni + 1) * P / NI>{});
+          if (more2) issue_a(st, integral_constant<int, ni * PA / NI>{}, integral_constant<int, (ni + 1) * PA / NI>{});
+        } else if (mi == 1 && more2) {
+          issue_range(st, integral_constant<int, TL::A_INS + ni * TL::B_INS / NI>{},
+                      integral_constant<int, TL::A_INS + (ni + 1) * TL::B_INS / NI>{});
         }
         if (j >= kLag) add(j - kLag);
         __builtin_amdgcn_sched_barrier(0);
@@ -587,6 +606,10 @@ __device__ __forceinline__ void quant_pipe(Stager<TL>& src, int nb, char* lds, Q
   block(kb, std::integral_constant<int, 0>{});
   __syncthreads();
 }
+
+// Barriers of quant_pipe over n blocks: one before the first, one within each
+// but the last two, one at the end of each.
+__device__ __forceinline__ int pipe_barriers(int n) { return n == 0 ? 0 : n + 1 + max(n - 2, 0); }
 
 // quant_pipe over the row blocks that hold some of the tile's rows (`last`
 // the last one's index): an expert's last tile is half empty on average, and
@@ -735,10 +758,9 @@ __global__ __launch_bounds__(TL::THREADS* KG) void product_kernel(QuantGemm g, i
   const int wm = wave / TL::WGN, wn = wave % TL::WGN;
   if constexpr (KG == 2) {
     // a block short (an odd count), or with none at all, this group has met
-    // fewer barriers: one per block, and one more where there is any
-    const int met0 = (all + 1) / 2, met1 = all / 2;
+    // fewer barriers
     if (group == 1)
-      for (int i = met1 + (met1 > 0); i < met0 + (met0 > 0); ++i) __syncthreads();
+      for (int i = pipe_barriers(all / 2); i < pipe_barriers((all + 1) / 2); ++i) __syncthreads();
     // each group keeps half of the row blocks and hands the other half over
     f32x4_t* give = reinterpret_cast<f32x4_t*>(lds) + group * (MI / 2 * NI * TL::THREADS) + j;
     const f32x4_t* take = reinterpret_cast<const f32x4_t*>(lds) + (1 - group) * (MI / 2 * NI * TL::THREADS) + j;
