@@ -296,6 +296,10 @@ struct QuantizeArgs {
   int64_t scale_ld;
 };
 hipError_t launch_quantize(const QuantizeArgs& a, hipStream_t s);
+// Rows t of x (bf16 [T][cols], cols a multiple of 128) quantised 1 x 128 and
+// written as rows row_of[t][0..k) of q ([.][cols] bytes) and scale.
+hipError_t launch_quantize_scatter(const void* x, int64_t T, int cols, const int32_t* row_of, int k, char* q,
+                                   float* scale, int64_t scale_ld, hipStream_t s);
 
 // C = A B^T over e4m3 rows with scales.  With offsets (grouped): expert e's
 // rows of A and C are [offsets[e], offsets[e+1]), its weights B + e * b_stride.

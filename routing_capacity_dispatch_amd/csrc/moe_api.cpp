@@ -798,6 +798,7 @@ moe_status check_dropless(const moe_config* cfg, moe_plan* p) {
   return MOE_OK;
 }
 
+// xs null: only the rows' places are found.
 moe_status run_dispatch_dropless(const moe_config* c, const moe_plan& p, const int32_t* topk, const void* z,
                                  void* xs, int32_t* row_of, int32_t* offsets, int64_t* counts, void* ws,
                                  hipStream_t s, Marks* m) {
@@ -808,7 +809,7 @@ moe_status run_dispatch_dropless(const moe_config* c, const moe_plan& p, const i
   int32_t* base = static_cast<int32_t*>(cv.take(nblk * c->n_experts * 4));
   hipError_t e = moe::launch_ragged_sort(topk, n, c->n_experts, hist, base, offsets, row_of, counts, s);
   if (e == hipSuccess && m) e = m->mark(s);
-  if (e == hipSuccess) e = moe::launch_ragged_scatter(z, row_of, c->T, c->top_k, p.row_bytes, xs, s);
+  if (e == hipSuccess && xs) e = moe::launch_ragged_scatter(z, row_of, c->T, c->top_k, p.row_bytes, xs, s);
   if (e == hipSuccess && m) e = m->mark(s);
   return hip_status(e);
 }
@@ -1565,6 +1566,8 @@ moe_status check_quant_config(const moe_config* cfg, moe_plan* p) {
   return MOE_OK;
 }
 
+// xs null: the workspace's xq and xs hold the quantised rows already (not
+// where few_rows).
 moe_status run_experts_quant(const moe_config* c, const moe_plan& p, const void* xs, const int32_t* offsets,
                              const moe_quant_experts* w, void* out, void* ws, hipStream_t s) {
   const int64_t n = p.dropless_rows, L = c->d_latent, F = c->d_ff;
@@ -1632,7 +1635,7 @@ moe_status run_experts_quant(const moe_config* c, const moe_plan& p, const void*
     d.ldo = L;
     return hip_status(moe::launch_few_rows(d, false, stage_h, s));
   }
-  e = quantize(xs, moe::DT_BF16, L, q.xq, q.xs);
+  e = xs ? quantize(xs, moe::DT_BF16, L, q.xq, q.xs) : hipSuccess;
   if (e != hipSuccess) return MOE_ERR_HIP;
   moe::QuantGateUp u{};
   u.A = q.xq;
@@ -1826,7 +1829,7 @@ int64_t carve_forward_quant(const moe_config* c, const moe_plan& p, const moe_dr
   w->gates = static_cast<float*>(pick(tp.gates, T * k * 4));
   w->row_of = static_cast<int32_t*>(pick(tp.row_of, T * k * 4));
   w->offsets = static_cast<int32_t*>(pick(tp.expert_offsets, (E + 1) * 4));
-  w->rows = static_cast<char*>(pick(tp.xs, n * L * 2));
+  w->rows = static_cast<char*>(pick(tp.xs, moe::few_rows(n, (int)E, true) ? n * L * 2 : 0));
   w->expert_out = static_cast<char*>(pick(tp.expert_out, n * L * 2));
   w->y_lat = static_cast<char*>(pick(tp.y_latent, T * L * 2));
   w->cat = static_cast<char*>(cv.take(T * W));
@@ -1927,11 +1930,21 @@ MOE_API moe_status moe_forward_dropless_quant(const moe_config* cfg, const moe_s
   e = moe::launch_gemm_dense(moe::DT_BF16, moe::DT_F32, r, s);
   if (e == hipSuccess) e = moe::launch_route_scored(sc, q.logits, w->router_bias, q.topk, q.gates, s);
   if (e != hipSuccess) return MOE_ERR_HIP;
-  // the routed path
-  st = run_dispatch_dropless(cfg, p, q.topk, q.z, q.rows, q.row_of, q.offsets, q.counts, q.dispatch, s, nullptr);
+  // the routed path.  Rows are quantised on their way to their experts,
+  // except where the bf16 rows are asked for or where the experts' kernels for
+  // few rows quantise them
+  const bool bf16_rows = tp.xs || moe::few_rows(p.dropless_rows, (int)E, true);
+  st = run_dispatch_dropless(cfg, p, q.topk, q.z, bf16_rows ? q.rows : nullptr, q.row_of, q.offsets, q.counts,
+                             q.dispatch, s, nullptr);
   if (st != MOE_OK) return st;
   if (T > 0) {
-    st = run_experts_quant(cfg, p, q.rows, q.offsets, &w->experts, q.expert_out, q.experts, s);
+    if (!bf16_rows) {
+      QuantExpertsWs x;
+      carve_experts_quant(cfg, p.dropless_rows, q.experts, &x);
+      e = moe::launch_quantize_scatter(q.z, T, (int)L, q.row_of, cfg->top_k, x.xq, x.xs, p.dropless_rows, s);
+      if (e != hipSuccess) return MOE_ERR_HIP;
+    }
+    st = run_experts_quant(cfg, p, bf16_rows ? q.rows : nullptr, q.offsets, &w->experts, q.expert_out, q.experts, s);
     if (st != MOE_OK) return st;
   }
   e = moe::launch_ragged_combine(moe::DT_BF16, q.expert_out, q.row_of, q.gates, T, cfg->top_k, L * 2, q.y_lat, s);
