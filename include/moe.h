@@ -583,7 +583,8 @@ typedef struct {
 
 /* logits (device) [T][E] fp32; bias (device) [E] fp32 or NULL; topk_idx
    (device, out) [T][k]; gates (device, out) [T][k] fp32.  Only T, n_experts
-   and top_k of *cfg are read, and validated as in moe_route. */
+   and top_k of *cfg are read, and validated as in moe_route; T past 2^26 - 4
+   is MOE_ERR_UNSUPPORTED. */
 moe_status moe_route_scored(const moe_config* cfg, const moe_scoring* scoring, const float* logits,
                             const float* bias, int32_t* topk_idx, float* gates, void* stream);
 
@@ -619,7 +620,7 @@ moe_status moe_route_scored_backward(const moe_config* cfg, const moe_scoring* s
    scales  (device, out) as above
    An infinity or a NaN makes the values of its block unspecified.
    MOE_ERR_UNSUPPORTED past 2^30 rows or columns or 2^24 - 1 blocks of 128 x
-   128. */
+   128 (of 32 x 128 with block_rows 1 and no transpose). */
 moe_status moe_quantize(int64_t rows, int64_t cols, const void* x, int64_t ldx, int32_t dtype,
                         int32_t block_rows, int32_t transpose, void* q, float* scales, void* stream);
 
@@ -677,8 +678,9 @@ typedef struct {
    expert_out (device, bf16 [T*k][L]) is rounded once.  Rows outside every
    expert's range are not written; offsets are kept inside [0, T*k].
    bf16 configs with d_latent and d_ff multiples of 128, of at most 2^23 - 8
-   tiles of 64 rows x 128 columns (MOE_ERR_UNSUPPORTED else).  For a straight-through gradient, moe_experts_backward_dropless
-   takes the bf16 weights that were quantised. */
+   tiles of 64 rows x 128 columns (MOE_ERR_UNSUPPORTED else).  For a
+   straight-through gradient, moe_experts_backward_dropless takes the bf16
+   weights that were quantised. */
 moe_status moe_experts_dropless_quant_ws_bytes(const moe_config* cfg, size_t* bytes);
 moe_status moe_experts_dropless_quant(const moe_config* cfg, const void* xs, const int32_t* expert_offsets,
                                       const moe_quant_experts* w, void* expert_out, void* ws, size_t ws_bytes,

@@ -1450,6 +1450,7 @@ MOE_API moe_status moe_backward_dropless_profiled(const moe_config* cfg, const m
 namespace {
 
 constexpr int kMaxGroups = 64;  // one lane of a wavefront per group
+constexpr int64_t kMaxScoredTokens = (int64_t(1) << 26) - 4;  // 64 threads each, below 2^32 in a launch
 
 moe_status check_scoring(const moe_config* c, const moe_scoring* sc, moe::ScoreArgs* a) {
   moe_status st = check_route_shape(c);
@@ -1462,7 +1463,7 @@ moe_status check_scoring(const moe_config* c, const moe_scoring* sc, moe::ScoreA
   if (sc->top_groups * (c->n_experts / sc->n_groups) < c->top_k) return MOE_ERR_INVALID_ARG;
   if ((sc->renormalise != 0 && sc->renormalise != 1) || sc->reserved != 0) return MOE_ERR_INVALID_ARG;
   if (!(sc->scale - sc->scale == 0.0f)) return MOE_ERR_INVALID_ARG;  // an infinity or a NaN
-  if (sc->n_groups > kMaxGroups) return MOE_ERR_UNSUPPORTED;
+  if (sc->n_groups > kMaxGroups || c->T > kMaxScoredTokens) return MOE_ERR_UNSUPPORTED;
   a->T = c->T;
   a->E = c->n_experts;
   a->k = c->top_k;
@@ -1693,7 +1694,9 @@ MOE_API moe_status moe_quantize(int64_t rows, int64_t cols, const void* x, int64
   if ((dtype != MOE_F32 && dtype != MOE_BF16) || (block_rows != 1 && block_rows != 128) ||
       (transpose != 0 && transpose != 1))
     return MOE_ERR_INVALID_ARG;
-  if (rows > kMaxQuantRows || cols > kMaxQuantRows || ceil_div(rows, 128) * ceil_div(cols, 128) > kMaxQuantTiles)
+  // a workgroup's rows: 32 where rows are quantised as they lie
+  const int64_t tile = block_rows == 1 && !transpose ? 32 : 128;
+  if (rows > kMaxQuantRows || cols > kMaxQuantRows || ceil_div(rows, tile) * ceil_div(cols, 128) > kMaxQuantTiles)
     return MOE_ERR_UNSUPPORTED;
   if (rows == 0 || cols == 0) return MOE_OK;
   if (!x || !q || !scales || !aligned16(q) || !aligned_to(x, dtype == MOE_BF16 ? 2 : 4) || !aligned_to(scales, 4))

@@ -181,3 +181,13 @@ def test_forward_quant_refusals(lib):
         bad = rcd.make_config(**{**shape, field: value})
         assert call(bad, scoring=rcd.scoring("sigmoid")) == status, field
     assert call(rcd.make_config(**shape, dtype="f32")) == UNS
+
+
+def test_more_threads_than_a_launch_has(lib):
+    # one column in 2^30 rows: 2^25 workgroups of 32 rows; 2^26 tokens of 64 threads
+    for rows in (1 << 30, (1 << 29) - 31):
+        assert lib.moe_quantize(rows, 1, FAKE, 1, abi.MOE_BF16, 1, 0, FAKE, FAKE, NUL) == UNS
+    sc = rcd.scoring("sigmoid")
+    cfg = rcd.make_config((1 << 26) - 3, 64, 64, 1, 1, 1, 64)
+    assert lib.moe_route_scored(C.byref(cfg), C.byref(sc), FAKE, NUL, FAKE, FAKE, NUL) == UNS
+    assert lib.moe_route_scored_backward(C.byref(cfg), C.byref(sc), FAKE, FAKE, FAKE, FAKE, NUL) == UNS
