@@ -9,6 +9,13 @@
 // the order of K inside a block does not matter as long as it is the same:
 // lane l takes bytes 16 (l >> 4) .. + 15 and 64 + 16 (l >> 4) .. + 15 of row
 // l & 15, which makes each load instruction read 64 contiguous bytes a row.
+//
+// Measured: 1 x 6144 x 2048 4.5 us (2.8 TB/s: a launch and one latency of
+// memory); 8192 x 6144 x 4096 181 us (2.27 PF: matrix cores at the power
+// limit, 156 us without the loads); 1000 x 2056 x 4224 in fp32 35 us (0.5 PF:
+// 136 tiles, and bf16 instructions).  Experts, 64 of L 2048, F 1024: 4 tokens
+// x 8 38 us (4.5 TB/s of weights), 4096 tokens x 8 320 us (quantiser 40,
+// hidden tiles 170, down 105).
 #include <type_traits>
 
 #include "gemm_core.h"
@@ -972,7 +979,7 @@ Form product_form(const QuantGemm& g) {
   if (f.skinny) return f;
   // rounds of the chip: 256 workgroups of 256 x 256 tiles (one per CU) take
   // 1.92 us a block of K, 512 of 128 x 128 tiles (two per CU) 1.23 us
-  // (8192 x 6144 x 4096: 184 us and 237 us)
+  // (8192 x 6144 x 4096 on one card: 192 us and 244 us)
   const int64_t r256 = cdiv(cdiv(g.M, 256) * cdiv(g.N, 256), 256), r128 = cdiv(cdiv(g.M, 128) * cdiv(g.N, 128), 512);
   f.big = !f.wide && rows >= 192 && (g.offsets || r256 * 192 < r128 * 123);
   if (!g.offsets && !f.big) {
@@ -1093,9 +1100,10 @@ void launch_hidden(const QuantGateUp& g, hipStream_t s) {
 }
 
 // Mean rows per expert up to which the experts' rows go straight from memory.
-// 64 experts, L 2048, F 1024, top-8, us for means of 1, 4, 8, 12, 16 rows: this
-// way 57, 78, 97, 121, 138, with tiles 65, 90, 96, 97, 100.
-constexpr int64_t kFewRows = 8;
+// 64 experts, L 2048, F 1024, top-8, us for means of 1, 4, 5, 6, 8, 12 rows:
+// this way 57, 78, 84, 94, 97, 122, with 64-row tiles 59, 84, 88, 90, 92, 93;
+// 16 experts, L 1024, F 2048, top-4, means of 4, 6, 8: 27, 29, 31 and 30, 30, 30.
+constexpr int64_t kFewRows = 6;
 // K whose 16 staged rows leave the LDS of a CU to two workgroups.
 constexpr int kStagedK = 4096;
 
@@ -1137,11 +1145,12 @@ hipError_t launch_few_rows(const FewRows& g, bool hidden, bool staged, hipStream
 
 hipError_t launch_quant_gate_up(const QuantGateUp& g, hipStream_t s) {
   if (g.M <= 0 || g.E <= 0) return hipSuccess;
-  // 64-row tiles for means up to 20 rows, 256-row tiles, which compute only the
-  // row blocks that hold rows, above (experts as at kFewRows, us for means of
-  // 16, 24, 32, 48, 64 rows: 100, 115, 118, 127, 132 with the one, 111, 111,
-  // 115, 125, 130 with the other)
-  if ((g.offsets ? cdiv(g.M, g.E) : g.M) <= 20)
+  // 64-row tiles for means up to 48 rows, 256-row tiles, which compute only the
+  // row blocks that hold rows, above (64 experts, L 2048, F 1024, top-8, us for
+  // means of 16, 32, 48, 64, 96, 192 rows: 94, 108, 115, 120, 138, 202 with the
+  // one, 104, 108, 118, 126, 134, 187 with the other; 128 experts, L 4096,
+  // F 1024, top-4, means of 32, 64: 370, 430 and 381, 411)
+  if ((g.offsets ? cdiv(g.M, g.E) : g.M) <= 48)
     launch_hidden<E64>(g, s);
   else
     launch_hidden<T256>(g, s);

