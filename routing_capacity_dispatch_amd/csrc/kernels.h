@@ -68,6 +68,9 @@ hipError_t launch_expert_down(int dt, const ExpertDown& a, hipStream_t s);
 // bf16 paths on the gfx950 GEMM core (gemm_bf16.hip); the generic dense
 // launchers above dispatch to them for bf16 inputs and outputs.
 hipError_t launch_gemm_dense_bf16(const GemmDense& g, hipStream_t s);
+// One K range of whole runs of 128, N and ldc multiples of 4, 16-byte aligned
+// rows, fp32 output, for at most a few hundred rows.
+hipError_t launch_few_f32out_bf16(const GemmDense& g, hipStream_t s);
 // bf16 operands, fp32 output on the gfx950 core (the router logits), for
 // one K range of whole K tiles and whole 16-byte output chunks.
 bool dense_f32out_supported(const GemmDense& g);

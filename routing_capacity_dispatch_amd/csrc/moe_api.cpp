@@ -1773,6 +1773,8 @@ MOE_API moe_status moe_experts_dropless_quant(const moe_config* cfg, const void*
 // ------------------------------------------------------------------ dropless forward in e4m3
 namespace {
 
+constexpr int64_t kFewLogitRows = 1024;  // rows of the router product up to which the kernel for few is the faster
+
 struct QuantForwardWs {
   char* xq;       // quantised x and its scales
   float* xs;
@@ -1930,7 +1932,7 @@ MOE_API moe_status moe_forward_dropless_quant(const moe_config* cfg, const moe_s
   r.ldc = E;
   r.M = (int)T;
   r.N = (int)E;
-  e = moe::launch_gemm_dense(moe::DT_BF16, moe::DT_F32, r, s);
+  e = T <= kFewLogitRows ? moe::launch_few_f32out_bf16(r, s) : moe::launch_gemm_dense(moe::DT_BF16, moe::DT_F32, r, s);
   if (e == hipSuccess) e = moe::launch_route_scored(sc, q.logits, w->router_bias, q.topk, q.gates, s);
   if (e != hipSuccess) return MOE_ERR_HIP;
   // the routed path.  Rows are quantised on their way to their experts,

@@ -568,3 +568,22 @@ def test_forward_dropless_quant_without_tokens():
     assert f(torch.empty((0, cfg.d_model), dtype=torch.bfloat16, device=d)).shape == (0, cfg.d_model)
     torch.cuda.synchronize()
     assert f.counts.tolist() == [0, 0, 0]
+
+
+@pytest.mark.parametrize("T,E", [(1, 64), (16, 20), (17, 20), (300, 36), (1024, 64), (1025, 64), (1100, 20)])
+def test_forward_dropless_quant_logits(T, E):
+    # both kernels of the router product; each logit is a sum of L = 512
+    # products of bf16 values, exact in fp32 but for the additions, at most
+    # 2^-24 of the magnitudes' sum for each of them in any order
+    d = dev()
+    say("forward_dropless_quant logits", T, E)
+    w = synth.workload("mid_bf16").replace(T=T, n_experts=E, n_pools=4)
+    cfg = rcd.config_of(w)
+    inp = synth.make_inputs(w, 12, device=d)
+    wq = rcd.quantize_weights(cfg, {k: v for k, v in inp.items() if k != "x"})
+    f = rcd.ForwardDroplessQuant(cfg, rcd.scoring("softmax"), wq, d, taps=True)
+    f(inp["x"])
+    torch.cuda.synchronize()
+    z, wr = np64(f.tap_t["z"]), np64(wq["w_router"])
+    err = np.abs(np64(f.tap_t["logits"]) - z @ wr.T)
+    assert (err <= cfg.d_latent * 2.0 ** -24 * (np.abs(z) @ np.abs(wr).T)).all()
