@@ -981,7 +981,12 @@ Form product_form(const QuantGemm& g) {
   // 1.92 us a block of K, 512 of 128 x 128 tiles (two per CU) 1.23 us
   // (8192 x 6144 x 4096 on one card: 192 us and 244 us)
   const int64_t r256 = cdiv(cdiv(g.M, 256) * cdiv(g.N, 256), 256), r128 = cdiv(cdiv(g.M, 128) * cdiv(g.N, 128), 512);
-  f.big = !f.wide && rows >= 192 && (g.offsets || r256 * 192 < r128 * 123);
+  // experts' products: 256 x 256 tiles from a mean of 192 rows on, where they
+  // give most CUs one (64 experts of 2048 x 1024, the whole layer's us for means
+  // of 128, 192, 512 rows: 168, 185, 362 with the small tiles, 166, 179, 353
+  // with these; 16 experts of 1024 x 2048, means of 256, 512: 69, 106 and 77, 103)
+  const int64_t big_tiles = g.offsets ? (cdiv(g.M, 256) + g.E / 2) * cdiv(g.N, 256) : 0;
+  f.big = !f.wide && rows >= 192 && (g.offsets ? big_tiles > 128 : r256 * 192 < r128 * 123);
   if (!g.offsets && !f.big) {
     // K shared by as many workgroups as give every CU one (N 6144, K 2048, 384
     // rows, us: 27.6 with two per CU, 15.0 with one), each with 16 blocks at

@@ -587,3 +587,18 @@ def test_forward_dropless_quant_logits(T, E):
     z, wr = np64(f.tap_t["z"]), np64(wq["w_router"])
     err = np.abs(np64(f.tap_t["logits"]) - z @ wr.T)
     assert (err <= cfg.d_latent * 2.0 ** -24 * (np.abs(z) @ np.abs(wr).T)).all()
+
+
+@pytest.mark.parametrize("L,F,counts", [(2048, 128, [700, 0, 256, 257, 800, 513, 1, 700]),
+                                        (2176, 384, [1300, 255, 600, 900, 0, 17, 40, 500])])
+def test_experts_on_large_tiles_match_oracle(L, F, counts):
+    # both products on 256 x 256 tiles: full ones, last rows, columns past N
+    check_experts(8, L, F, counts, L + F, per_expert=6)
+
+
+@pytest.mark.parametrize("M,N,K,block,out_dtype", [
+    (2100, 4100, 1664, 128, torch.bfloat16), (2100, 4100, 1664, 1, torch.bfloat16),  # 256 x 256 tiles, 13 blocks of K
+    (100, 300, 4224, 128, torch.bfloat16), (100, 300, 4224, 1, torch.float32),       # unequal shares of K
+    (70, 140, 7296, 1, torch.float32), (40, 130, 8576, 128, torch.bfloat16)])        # a short last share
+def test_gemm_of_many_blocks_matches_oracle(M, N, K, block, out_dtype):
+    check_gemm(*operands(M, N, K, block, M + K), block, out_dtype)
