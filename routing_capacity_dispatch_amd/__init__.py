@@ -536,6 +536,11 @@ def _rows(t, shape, dtype, what, dev=None):
     return t
 
 
+def _new(rows, cols, dtype, dev):
+    """A new contiguous [rows, cols] (empty_strided returns sooner than empty)."""
+    return torch.empty_strided((rows, cols), (max(cols, 1), 1), dtype=dtype, device=dev)
+
+
 def _workspace(ws, nbytes, dev):
     """The caller's workspace (bytes on the tensors' device), or a new one."""
     if ws is None:
@@ -580,9 +585,9 @@ def route_scored(cfg, sc: abi.MoeScoring, logits: torch.Tensor, bias: Optional[t
     dev = _rows(logits, (T, E), torch.float32, "logits").device
     if bias is not None:
         _rows(bias, (E,), torch.float32, "bias", dev)
-    topk = torch.empty((T, k), dtype=torch.int32, device=dev) if out is None else \
+    topk = _new(T, k, torch.int32, dev) if out is None else \
         _rows(out["topk_idx"], (T, k), torch.int32, "out['topk_idx']", dev)
-    gates = torch.empty((T, k), dtype=torch.float32, device=dev) if out is None else \
+    gates = _new(T, k, torch.float32, dev) if out is None else \
         _rows(out["gates"], (T, k), torch.float32, "out['gates']", dev)
     _launch("moe_route_scored", dev, C.byref(cfg), C.byref(sc), logits.data_ptr(),
             None if bias is None else bias.data_ptr(), topk.data_ptr(), gates.data_ptr())
@@ -619,9 +624,9 @@ def quantize(x: torch.Tensor, block_rows: int = 1, transpose: bool = False, out=
     kb = -(-K // 128)
     dev = x.device
     qs, ss = (R, kb * 128), ((kb, R) if block_rows == 1 else (-(-R // 128), kb))
-    q = torch.empty(qs, dtype=torch.float8_e4m3fn, device=dev) if out is None else \
+    q = _new(*qs, torch.float8_e4m3fn, dev) if out is None else \
         _rows(out[0], qs, torch.float8_e4m3fn, "out[0]", dev)
-    s = torch.empty(ss, dtype=torch.float32, device=dev) if out is None else \
+    s = _new(*ss, torch.float32, dev) if out is None else \
         _rows(out[1], ss, torch.float32, "out[1]", dev)
     _launch("moe_quantize", dev, rows, cols, x.data_ptr(), ld, _DT[x.dtype], block_rows, int(transpose), q.data_ptr(),
             s.data_ptr())
@@ -658,7 +663,7 @@ def gemm_quant(a, a_scales, b, b_scales, block_rows: int = 128, out_dtype=torch.
     sa = _scale_ld(a_scales, (kb, M), "a_scales", dev)
     sb = _scale_ld(b_scales, (kb, N) if block_rows == 1 else (-(-N // 128), kb), "b_scales", dev)
     if out is None:
-        out = torch.empty((M, N), dtype=out_dtype, device=dev)
+        out = _new(M, N, out_dtype, dev)
     else:
         _check(out.shape == (M, N) and out.dtype == out_dtype and out.device == dev
                and (N <= 1 or out.stride(1) == 1) and (M <= 1 or out.stride(0) >= N),
@@ -714,6 +719,7 @@ def quantize_weights(cfg, weights: Dict[str, torch.Tensor]) -> Dict:
     the up-projection and the shared down-projections side by side as
     w_output; the router stays bf16."""
     def blocks(w):
+        _check(w.shape[-1] % 128 == 0 and w.shape[-2] % 128 == 0, "the weights' sizes must be multiples of 128")
         q, s = quantize(w.reshape(-1, w.shape[-1]), 128)
         return q.view(w.shape), s.view(*w.shape[:-2], w.shape[-2] // 128, w.shape[-1] // 128)
     out = {n: blocks(weights[n]) for n in ("w_latent", "w_gate", "w_up", "w_down")}
