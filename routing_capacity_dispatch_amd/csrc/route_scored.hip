@@ -11,7 +11,7 @@
 //
 // Measured, 16384 tokens of 384 experts, sigmoid, top-8 of the best 4 of 8
 // groups: 13.6 us (1.9 TB/s; the sorting networks' issue, not the bytes'
-// 5 us, bounds it); its gradient 9.5 us (2.8 TB/s); one token 4.4 us, a launch
+// 5 us, bounds it); its gradient 7.5 us (3.6 TB/s); one token 4.4 us, a launch
 // and its chain of exchanges.
 #include "common.h"
 #include "kernels.h"
@@ -671,7 +671,9 @@ __global__ __launch_bounds__(256) void route_bwd16_kernel(ScoreArgs a, const flo
                                                           const int32_t* __restrict__ topk,
                                                           const float* __restrict__ d_gates,
                                                           float* __restrict__ d_logits) {
+  __shared__ __attribute__((aligned(16))) float terms[16][NPER * 16];
   const int lane = threadIdx.x & 63, c = lane & 15;
+  float* mine = terms[threadIdx.x >> 4];
   const int64_t t0 = ((int64_t)blockIdx.x * 4 + (threadIdx.x >> 6)) * 4;
   if (t0 >= a.T) return;
   const bool exists = t0 + (lane >> 4) < a.T;
@@ -715,22 +717,28 @@ __global__ __launch_bounds__(256) void route_bwd16_kernel(ScoreArgs a, const flo
   }
   const float val = kSigmoid ? ds * s * rest : ds;
   const float base = kSigmoid ? 0.0f : sum16(ds * s);
-  float out[NPER];
-#pragma unroll
-  for (int i = 0; i < NPER; ++i) out[i] = -base;
+  // the selected experts' terms go to their columns through LDS (comparing
+  // every column with every id costs NPER k selections a lane: 9.5 us); an id that
+  // appears twice is written once, by its first lane, with the sum of all
   const int from = lane & 48;
+  float total = 0.0f;
+  bool first = on;
   for (int j = 0; j < a.k; ++j) {
     const int e = __shfl(on ? idx : -1, from + j);
     const float x = __shfl(val, from + j);
-    const int d = e - 4 * c;  // 64 i + q where the expert is this lane's
-#pragma unroll
-    for (int i = 0; i < NPER; ++i) out[i] += d == (i / 4) * 64 + i % 4 ? x : 0.0f;
+    total += e == idx ? x : 0.0f;
+    first = first && !(e == idx && j < c);
   }
+#pragma unroll
+  for (int i = 0; i < NPER; i += 4) *reinterpret_cast<f32x4_t*>(mine + mapped<4>(map, c, i)) = f32x4_t{0.f, 0.f, 0.f, 0.f};
+  __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+  if (first) mine[idx] = total;
+  __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
   if (!exists) return;
 #pragma unroll
   for (int i = 0; i < NPER; i += 4) {
     const int e = mapped<4>(map, c, i);
-    f32x4_t v = {out[i], out[i + 1], out[i + 2], out[i + 3]};
+    f32x4_t v = *reinterpret_cast<const f32x4_t*>(mine + e) - base;
     if constexpr (!kSigmoid) v *= f32x4_t{p[i], p[i + 1], p[i + 2], p[i + 3]} * r;
     if (e < E) *reinterpret_cast<f32x4_t*>(d_logits + t * E + e) = v;
   }
