@@ -602,3 +602,51 @@ def test_experts_on_large_tiles_match_oracle(L, F, counts):
     (70, 140, 7296, 1, torch.float32), (40, 130, 8576, 128, torch.bfloat16)])        # a short last share
 def test_gemm_of_many_blocks_matches_oracle(M, N, K, block, out_dtype):
     check_gemm(*operands(M, N, K, block, M + K), block, out_dtype)
+
+
+def test_long_staged_rows_in_a_graph():
+    # 16 staged rows of 4096 and their scales pass 64 KiB of LDS
+    d = dev()
+    E, L, F, n = 4, 4096, 128, 20
+    w = quant_weights(E, L, F, 21)
+    cfg = rcd.make_config(n, 64, L, E, 1, 1, F)
+    off = offsets_of([17, 0, 2, 1]).to(d)
+    xs = [rand((n, L), 30 + i, torch.bfloat16).to(d) for i in range(3)]
+    x, out = xs[0].clone(), torch.empty((n, L), dtype=torch.bfloat16, device=d)
+    ws = torch.empty(rcd.experts_dropless_quant_ws_bytes(cfg), dtype=torch.uint8, device=d)
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        rcd.experts_dropless_quant(cfg, x, off, *w, expert_out=out, ws=ws)
+    torch.cuda.current_stream().wait_stream(side)
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        rcd.experts_dropless_quant(cfg, x, off, *w, expert_out=out, ws=ws)
+    for xi in xs + xs[:1]:
+        x.copy_(xi)
+        out.zero_()
+        torch.cuda.synchronize()
+        graph.replay()
+        torch.cuda.synchronize()
+        assert torch.equal(out, rcd.experts_dropless_quant(cfg, xi, off, *w))
+
+
+@pytest.mark.parametrize("counts", [[3, 2], [40, 60], [400, 300]])
+@pytest.mark.parametrize("bad", [float("nan"), float("inf"), -float("inf")])
+def test_rows_without_numbers_stay_among_themselves(counts, bad):
+    # a row of an expert, and one behind the last expert, hold no numbers: the
+    # others' results are those without them
+    d = dev()
+    L, F, n = 256, 128, sum(counts) + 3
+    w = quant_weights(2, L, F, 22)
+    cfg = rcd.make_config(n, 64, L, 2, 1, 1, F)
+    off = offsets_of(counts).to(d)
+    xs = rand((n, L), 23, torch.bfloat16).to(d)
+    ref = rcd.experts_dropless_quant(cfg, xs, off, *w)
+    xs[1, 5:9] = bad
+    xs[n - 2] = bad
+    got = rcd.experts_dropless_quant(cfg, xs, off, *w)
+    torch.cuda.synchronize()
+    rows = [r for r in range(sum(counts)) if r != 1]
+    assert torch.equal(got[rows], ref[rows])
