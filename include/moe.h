@@ -567,7 +567,9 @@ moe_status moe_backward_dropless_profiled(const moe_config* cfg, const moe_weigh
  * Selection compares the keys as real numbers (fp64 where fp32 cannot tell
  * two apart), so it does not depend on the rounding of an fp32 exponential.
  * A logit or a bias may be -infinity: such a logit scores 0, and an expert
- * whose bias is -infinity is taken only when nothing else is left.
+ * whose bias is -infinity is taken only when nothing else is left.  Where a
+ * logit or a bias is a NaN or +infinity, the ids of that token are k different
+ * ones in [0, E), otherwise unspecified, and so are its gates.
  * ------------------------------------------------------------------------ */
 typedef enum { MOE_SCORE_SOFTMAX = 0, MOE_SCORE_SIGMOID = 1 } moe_score;
 

@@ -76,7 +76,7 @@ __device__ __forceinline__ void select_token(const ScoreArgs& a, const float* __
     key[i] = kNone;
     if (e < E) {
       const double x = score64(a, v[i], m, sum) + (bias ? (double)bias[e] : 0.0);
-      key[i] = x == x ? x : kNone;
+      key[i] = x == x ? fmin(x, 1e300) : kNone;  // so that no sum of two is a NaN
       open |= 1u << i;
     }
   }
@@ -171,7 +171,8 @@ __global__ __launch_bounds__(256) void route_scored_kernel(ScoreArgs a, const fl
 constexpr int kTop = 8;
 
 __device__ __forceinline__ double pack_key(float key, int e) {
-  const float f = fmaxf(key, -3.402823466e38f);  // -inf has no mantissa to carry an index
+  // an infinity has no mantissa to carry an index; a NaN becomes the least
+  const float f = __builtin_amdgcn_fmed3f(key == key ? key : -3.402823466e38f, -3.402823466e38f, 3.402823466e38f);
   const uint64_t b = (uint64_t)__double_as_longlong((double)f);
   return __longlong_as_double((long long)(b | (uint32_t)(f < 0.0f ? e : 1023 - e)));
 }

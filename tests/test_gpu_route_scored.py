@@ -228,3 +228,40 @@ def test_group_boundary_below_fp32(E, G, tg, k, lower, kind):
     ref = sr.select(logits, bias, k, kind, G, tg, 2)
     assert (a if lower else b) in ref[0] // size and (b if lower else a) not in ref[0] // size
     check(21, E, k, logits, bias, kind, G, tg, 2)
+
+
+@pytest.mark.parametrize("kind", ["sigmoid", "softmax"])
+@pytest.mark.parametrize("with_bias", [False, True])
+@pytest.mark.parametrize("E,k,G,tg", [(64, 8, 1, 1), (64, 8, 8, 2), (384, 8, 8, 4), (60, 4, 4, 1), (60, 12, 6, 2), (1024, 64, 1, 1)])
+def test_what_is_no_number_leaves_ids_in_range(E, k, G, tg, with_bias, kind):
+    # ids index the dispatch's rows: they are different and inside [0, E)
+    # whatever the logits are, and the other tokens are not touched
+    rng = np.random.default_rng(E + k)
+    l = rng.standard_normal((40, E)).astype(np.float32)
+    b = (0.05 * rng.standard_normal(E)).astype(np.float32) if with_bias or G > 1 else None
+    ref = sr.select(l, b, k, kind, G, tg, 2)
+    bad = {2: np.nan, 5: np.inf, 11: np.nan, 12: np.inf, 13: -np.inf}
+    for t, v in bad.items():
+        l[t, rng.permutation(E)[:max(E // 2, E - k + 2) if t > 10 else 3]] = v
+    l[17], l[18], l[19] = np.nan, np.inf, -np.inf
+    odd = [*bad, 17, 18, 19]
+    d = dev()
+    sc = rcd.scoring(kind, G, tg, 2)
+
+    def ids(bias):
+        t, _ = rcd.route_scored(cfg_of(40, E, k), sc, torch.from_numpy(l).to(d),
+                                None if bias is None else torch.from_numpy(bias).to(d))
+        torch.cuda.synchronize()
+        t = np_i(t)
+        assert ((t >= 0) & (t < E)).all()
+        assert all(len(set(r)) == k for r in t.tolist())
+        return t
+    keep = [t for t in range(40) if t not in odd]
+    assert np.array_equal(ids(b)[keep], ref[keep])
+    if b is not None:
+        for v in (np.inf, np.nan):
+            c = b.copy()
+            c[[1, E - 2]] = v
+            ids(c)
+        ids(np.full(E, np.nan, dtype=np.float32))
+        ids(np.full(E, np.inf, dtype=np.float32))
