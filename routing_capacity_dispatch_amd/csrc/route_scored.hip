@@ -171,8 +171,10 @@ __global__ __launch_bounds__(256) void route_scored_kernel(ScoreArgs a, const fl
 constexpr int kTop = 8;
 
 __device__ __forceinline__ double pack_key(float key, int e) {
-  // an infinity has no mantissa to carry an index; a NaN becomes the least
-  const float f = __builtin_amdgcn_fmed3f(key == key ? key : -3.402823466e38f, -3.402823466e38f, 3.402823466e38f);
+  // The sum turns -0.0 into the 0.0 it equals (its sign bit would also ask for
+  // the other form of the index) and quiets a NaN, of which the median makes
+  // the least value; an infinity has no mantissa to carry an index.
+  const float f = __builtin_amdgcn_fmed3f(key + 0.0f, -3.402823466e38f, 3.402823466e38f);
   const uint64_t b = (uint64_t)__double_as_longlong((double)f);
   return __longlong_as_double((long long)(b | (uint32_t)(f < 0.0f ? e : 1023 - e)));
 }

@@ -265,3 +265,48 @@ def test_what_is_no_number_leaves_ids_in_range(E, k, G, tg, with_bias, kind):
             ids(c)
         ids(np.full(E, np.nan, dtype=np.float32))
         ids(np.full(E, np.inf, dtype=np.float32))
+
+
+@pytest.mark.parametrize("kind", ["sigmoid", "softmax"])
+@pytest.mark.parametrize("T,E,k", [(1, 64, 8), (3, 384, 8), (40, 60, 6), (33, 61, 7), (9, 8, 8), (5, 1024, 8), (17, 128, 1),
+                                   (6, 100, 12)])
+def test_negative_zeros_are_zeros(T, E, k, kind):
+    # the two zeros are one key: equal ones are taken in index order.  Every
+    # other logit is negative, so that zeros are what is selected: -0.0 alone,
+    # both zeros mixed, one -0.0, and -0.0 as the last key taken
+    rng = np.random.default_rng(T + E + k)
+    l = -np.abs(rng.standard_normal((T, E)).astype(np.float32)) - np.float32(0.1)
+    check(T, E, k, np.full((T, E), -0.0, np.float32), None, kind)
+    check(T, E, k, rng.choice(np.array([0.0, -0.0], np.float32), size=(T, E)), None, kind)
+    check(T, E, k, rng.choice(np.array([-1.0, 0.0, -0.0], np.float32), size=(T, E)), None, kind, renorm=False)
+    one = l.copy()
+    one[np.arange(T), rng.integers(0, E, T)] = -0.0
+    check(T, E, k, one, None, kind)
+    last = l.copy()
+    for t in range(T):
+        at = rng.permutation(E)[:k]
+        last[t, at] = 1.0 + np.arange(k)
+        last[t, at[0]] = -0.0
+    check(T, E, k, last, None, kind)
+    if E % 4 == 0:  # every group kept: no limit
+        check(T, E, k, one, None, kind, 4, 4)
+
+
+@pytest.mark.parametrize("kind", ["sigmoid", "softmax"])
+@pytest.mark.parametrize("E,G,tg", [(64, 1, 1), (61, 1, 1), (64, 8, 2)])
+def test_signalling_nans_are_taken_last(E, G, tg, kind):
+    # a NaN of either kind and sign among finite logits: the ids are different
+    # and in range, and the other tokens are not touched
+    d = dev()
+    rng = np.random.default_rng(E)
+    l = rng.standard_normal((24, E)).astype(np.float32)
+    ref = sr.select(l, None, 6, kind, G, tg, 2)
+    bits = np.array([0x7F800001, 0xFF800001, 0x7FC00000, 0xFFC00000], dtype=np.uint32)
+    for t in range(0, 24, 3):
+        l.view(np.uint32)[t, rng.permutation(E)[:E // 2]] = bits[t // 3 % 4]
+    topk, _ = rcd.route_scored(cfg_of(24, E, 6), rcd.scoring(kind, G, tg, 2), torch.from_numpy(l).to(d))
+    torch.cuda.synchronize()
+    ids = np_i(topk)
+    assert ((ids >= 0) & (ids < E)).all() and all(len(set(r)) == 6 for r in ids.tolist())
+    keep = [t for t in range(24) if t % 3]
+    assert np.array_equal(ids[keep], ref[keep])
