@@ -165,7 +165,9 @@ __global__ __launch_bounds__(256) void route_scored_kernel(ScoreArgs a, const fl
 //     and turns two keys around only by that factor of their p's difference,
 //     which at a near tie is the difference of two biases
 //   adding the bias: u |key|
-// Two keys closer than both errors are not told apart here.  Without a bias
+// Two keys closer than both errors are not told apart here, nor two groups
+// whose scores, each with its keys' errors (those of the keys, which a sum of
+// opposite ones does not show) and its own rounding, overlap.  Without a bias
 // and without groups the logits themselves are the keys: exact, as long as
 // fp64 scores still separate what fp32 logits separate.
 constexpr int kTop = 8;
@@ -360,12 +362,13 @@ __device__ __forceinline__ void select_close(const ScoreArgs& a, const LaneMap& 
 }
 
 // Whether this lane's group stays, by fp64 keys: those of the lane's 4 largest
-// fp32 keys hold its two largest, unless the fifth is within their tolerance
-// (then, or where a key is no number: `unsettled`).
+// fp32 keys hold its two largest, unless the fifth is too close to the second
+// (`margin`: how far those two can be off together) or the lane has no two
+// (`unsettled`).
 template <bool kSigmoid>
 __device__ __forceinline__ bool groups64(const ScoreArgs& a, const float* __restrict__ row,
-                                         const float* __restrict__ bias, float mx, const double* top, float tol, int g,
-                                         int span, bool& unsettled) {
+                                         const float* __restrict__ bias, float mx, const double* top, float margin,
+                                         int g, int span, bool& unsettled) {
   const int lane = threadIdx.x & 63, c = lane & 15;
   double sum = 1.0;
   if constexpr (!kSigmoid) {
@@ -374,7 +377,7 @@ __device__ __forceinline__ bool groups64(const ScoreArgs& a, const float* __rest
     for (int d = 1; d < 16; d <<= 1) sum += shfl_xor_f64(sum, d);
     sum = fmax(sum, 1e-300);
   }
-  unsettled = packed_key(top[4]) + 2.0f * tol >= packed_key(top[1]) || !(packed_key(top[0]) > -3.0e38f);
+  unsettled = !(packed_key(top[1]) - packed_key(top[4]) > margin && packed_key(top[1]) > -3.0e38f);
   double t1 = kNone, t2 = kNone;
 #pragma unroll
   for (int j = 0; j < 4; ++j) {
@@ -474,13 +477,17 @@ __global__ __launch_bounds__(256) void route_top8_kernel(ScoreArgs a, LaneMap ma
       merge8(top, l);
     }
   }
-  // difference below which two keys of magnitude up to x are not told apart
+  // how far an fp32 key x can be off, and the difference below which two keys
+  // of magnitude up to x are not told apart
+  constexpr float u = 5.9604645e-8f;
+  auto off = [&](float x) {
+    x = fminf(fabsf(x), 3.402823466e38f);
+    if constexpr (kSigmoid) return 8.0f * u + 2.0f * u * x;
+    return 2.0f * u + 4.0f * u * (x + bmax) + u * x + 0.5f * (NPER + 24) * u * fminf(1.0f, 2.0f * bmax);
+  };
   auto tol = [&](float x) {
-    constexpr float u = 5.9604645e-8f;
-    x = fabsf(x);
-    if constexpr (kLogit) return 0x1p-30f * (1.0f + x);  // fp64 scores still differ by it
-    if constexpr (kSigmoid) return 16.0f * u + 4.0f * u * x;
-    return 4.0f * u + 8.0f * u * (x + bmax) + 2.0f * u * x + (NPER + 24) * u * fminf(1.0f, 2.0f * bmax);
+    if constexpr (kLogit) return 0x1p-30f * (1.0f + fabsf(x));  // fp64 scores still differ by it
+    return 2.0f * off(x);
   };
   float shut = 0.0f;  // -inf where this lane's experts cannot be taken
   if constexpr (!kLogit) {
@@ -495,7 +502,9 @@ __global__ __launch_bounds__(256) void route_top8_kernel(ScoreArgs a, LaneMap ma
       if (span > 1) join(partner<0>(t1), partner<0>(t2));
       if (span > 2) join(partner<1>(t1), partner<1>(t2));
       if (span > 4) join(partner<2>(t1), partner<2>(t2));
-      const float gsc = a.group_top == 2 && t2 > -1e300 ? packed_key(t1) + packed_key(t2) : packed_key(t1);
+      const bool two = a.group_top == 2 && t2 > -1e300;
+      const float k1 = packed_key(t1), k2 = packed_key(t2), gsc = two ? k1 + k2 : k1;
+      const float gerr = off(k1) + (two ? off(k2) + u * fabsf(gsc) : 0.0f);
       const int g = c / span;
       int before = 0;
       for (int o = 0; o < a.groups; ++o) {
@@ -503,11 +512,12 @@ __global__ __launch_bounds__(256) void route_top8_kernel(ScoreArgs a, LaneMap ma
         before += (s > gsc || (s == gsc && o < g)) ? 1 : 0;
       }
       bool in = before < a.top_groups;
-      const float low = min16(in ? gsc : 3.402823466e38f), high = max16(in ? -3.402823466e38f : gsc);
-      const bool close_groups = !(low - high > 2.0f * tol(fmaxf(fabsf(low), fabsf(high))));
+      const float low = min16(in ? gsc - gerr : 3.402823466e38f), high = max16(in ? -3.402823466e38f : gsc + gerr);
+      const bool close_groups = !(low > high);
       if (ballot64(close_groups) != 0) {
         bool unsettled;
-        const bool in64 = groups64<kSigmoid>(a, row, bias, mx, top, tol(packed_key(top[0])), g, span, unsettled);
+        const float margin = off(packed_key(top[1])) + off(packed_key(top[4]));
+        const bool in64 = groups64<kSigmoid>(a, row, bias, mx, top, margin, g, span, unsettled);
         in = close_groups ? in64 : in;
         hard = hard || (close_groups && unsettled);
       }

@@ -310,3 +310,25 @@ def test_signalling_nans_are_taken_last(E, G, tg, kind):
     assert ((ids >= 0) & (ids < E)).all() and all(len(set(r)) == 6 for r in ids.tolist())
     keep = [t for t in range(24) if t % 3]
     assert np.array_equal(ids[keep], ref[keep])
+
+
+@pytest.mark.parametrize("kind", ["sigmoid", "softmax"])
+@pytest.mark.parametrize("E,G,tg,k", [(64, 8, 4, 8), (256, 8, 3, 6), (64, 4, 1, 2), (128, 16, 5, 4), (60, 6, 2, 3)])
+@pytest.mark.parametrize("size", [128.0, 1000.0, 1e5])
+def test_group_sums_of_large_keys_that_cancel(size, E, G, tg, k, kind):
+    # one bias of +size and the others -size in every group: its two largest
+    # keys nearly cancel, so their sum says nothing of how far the fp32 keys
+    # are off, half a step of theirs (2^-24 size) each.  The two experts'
+    # logits spread the groups' sums over a few such steps (a sigmoid's slope
+    # at 0.3 is 0.24), and the rest of a group lies well below
+    rng = np.random.default_rng(E + G + int(size))
+    gs = E // G
+    first, second = (np.arange(G) * gs + rng.permuted(np.tile(np.arange(gs), (G, 1)), axis=1)[:, :2].T)
+    bias = np.full(E, -size, np.float32)
+    bias[first] = size
+    T = 64
+    l = np.full((T, E), -4.0, np.float32)
+    for t in range(T):
+        for at in (first, second):
+            l[t, at] = 0.3 + size * 2.0 ** (-22 + t % 3) * rng.standard_normal(G)
+    check(T, E, k, l, bias, kind, G, tg, 2)
