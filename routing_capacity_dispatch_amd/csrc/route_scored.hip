@@ -159,12 +159,16 @@ __global__ __launch_bounds__(256) void route_scored_kernel(ScoreArgs a, const fl
 //   sigmoid: the exponential of l is off by 4 u l + 2 u relatively, which
 //     moves s by s (1 - s) of that (<= 0.23 * 4 u + 0.25 * 2 u); 1 + e and the
 //     reciprocal add 3 u s: within 4.5 u
-//   softmax, d = max - l: e^-d is off by 4 u d + 4 u relatively, d e^-d <=
-//     0.37, so p by 1.5 u + 4 u p; the sum's error (NPER + 4 additions, the
-//     exponentials' own) is a factor common to all p, within (NPER + 24) u,
-//     and turns two keys around only by that factor of their p's difference,
-//     which at a near tie is the difference of two biases
-//   adding the bias: u |key|
+//   softmax p = e^-d / S, d = max - l: e^-d is off by 4 u d + 4 u relatively,
+//     the product with 1 / S by u, and p d = p ln(1/(p S)): within u (5 p +
+//     4 m / S), m the largest t ln(1/t) of any t <= p S.  This shrinks with
+//     the score, which a key x bounds by |x| and the largest bias: far from
+//     the largest logit, where most of a sharp softmax lies, keys are told
+//     apart as well as near it.  S itself (NPER + 4 additions, the
+//     exponentials' own errors) is a factor common to all p, within (NPER +
+//     24) u, and turns two keys around only by that factor of their p's
+//     difference, which at a near tie is the difference of two biases
+//   adding the bias: u |key|.  Scores below 2^-126 are flushed to 0.
 // Two keys closer than both errors are not told apart here, nor two groups
 // whose scores, each with its keys' errors (those of the keys, which a sum of
 // opposite ones does not show) and its own rounding, overlap.  Without a bias
@@ -483,7 +487,10 @@ __global__ __launch_bounds__(256) void route_top8_kernel(ScoreArgs a, LaneMap ma
   auto off = [&](float x) {
     x = fminf(fabsf(x), 3.402823466e38f);
     if constexpr (kSigmoid) return 8.0f * u + 2.0f * u * x;
-    return 2.0f * u + 4.0f * u * (x + bmax) + u * x + 0.5f * (NPER + 24) * u * fminf(1.0f, 2.0f * bmax);
+    const float p = fminf(x + bmax, 1.0f / sum);  // at least the score
+    const float t = __builtin_amdgcn_fmed3f(p * sum, 1e-36f, 0.36787944f);
+    return u * (6.0f * p - 5.0f * t * __logf(t) / sum + 1.25f * x) + 1e-36f +
+           0.5f * (NPER + 24) * u * fminf(1.0f, 2.0f * bmax);
   };
   auto tol = [&](float x) {
     if constexpr (kLogit) return 0x1p-30f * (1.0f + fabsf(x));  // fp64 scores still differ by it

@@ -332,3 +332,75 @@ def test_group_sums_of_large_keys_that_cancel(size, E, G, tg, k, kind):
         for at in (first, second):
             l[t, at] = 0.3 + size * 2.0 ** (-22 + t % 3) * rng.standard_normal(G)
     check(T, E, k, l, bias, kind, G, tg, 2)
+
+
+@pytest.mark.parametrize("E,G,tg,k", [(384, 8, 4, 8), (64, 4, 2, 6), (100, 1, 1, 5), (256, 16, 4, 8), (40, 8, 3, 8)])
+@pytest.mark.parametrize("spread", [6.0, 16.0, 60.0, 400.0])
+@pytest.mark.parametrize("kind", ["sigmoid", "softmax"])
+def test_sharp_scores_match_oracle(spread, E, G, tg, k, kind):
+    # Most scores are far below the largest, down to those that fp32 and fp64
+    # exponentials turn to 0; pairs of neighbouring logits among them.
+    # Ids are equal.  Gates and gradients within RTOL of their magnitudes, and
+    # what a score below fp32's normal range, a multiple of 2^-149 and so off
+    # by up to 2 of those (its exponential's and its product's rounding),
+    # makes of it: a gate scale s / S moves by scale 2^-148 / S for its own s
+    # and by at most as much for each of the k in S; a gradient ds s (1 - s)
+    # by |ds| 2^-148 for its own s and, through S and the sum of dg s, by at
+    # most 3 k |ds| (s / S) 2^-148, s / S <= 1, |ds| the largest of the token.
+    def check(T, E, k, logits, bias, kind, groups, top_groups):
+        d = dev()
+        say("sharp", E, k, kind, groups, top_groups, bias is not None)
+        sc = rcd.scoring(kind, groups, top_groups, 2, True, 2.5)
+        lt = torch.from_numpy(logits).to(d)
+        topk, gates = rcd.route_scored(cfg_of(T, E, k), sc, lt, None if bias is None else torch.from_numpy(bias).to(d))
+        torch.cuda.synchronize()
+        ref = sr.select(logits, bias, k, kind, groups, top_groups, 2)
+        assert np.array_equal(np_i(topk), ref)
+        S = np.take_along_axis(sr.scores(logits, kind), ref, axis=1).sum(axis=1, keepdims=True) + 1e-20
+        rg = sr.gates(logits, ref, kind, True, 2.5)
+        err = np.abs(gates.cpu().numpy().astype(np.float64) - rg)
+        assert (err <= RTOL[kind] * rg + FLOOR + (k + 1) * 2.5 * 2.0 ** -148 / S).all()
+        dg = np.random.default_rng(T + E).standard_normal((T, k)).astype(np.float32)
+        dl = rcd.route_scored_backward(cfg_of(T, E, k), sc, lt, topk, torch.from_numpy(dg).to(d))
+        torch.cuda.synchronize()
+        rd, mag = sr.backward(logits, ref, dg, kind, True, 2.5)
+        ds = 2 * 2.5 * np.abs(dg).max(axis=1, keepdims=True) / S
+        err = np.abs(dl.cpu().numpy().astype(np.float64) - rd)
+        assert (err <= RTOL[kind] * mag + FLOOR + (3 * k + 1) * 2.0 ** -148 * ds).all()
+    rng = np.random.default_rng(E + int(spread))
+    l = (spread * rng.standard_normal((50, E))).astype(np.float32)
+    pair = rng.permutation(E)[:E // 4 * 2].reshape(2, -1)
+    l[::2, pair[1]] = np.nextafter(l[::2, pair[0]], np.float32(np.inf))
+    low = l - l.max(axis=1, keepdims=True)
+    tiny = (2.0 ** -20 * rng.standard_normal(E)).astype(np.float32)
+    for x in (l, low, (low - 30).astype(np.float32)):
+        for b in (None, tiny, (0.05 * rng.standard_normal(E)).astype(np.float32)):
+            check(50, E, k, x, b, kind, G, tg)
+
+
+def test_sharp_softmax_scores_keep_the_pace():
+    # errors of fp32 scores shrink with the scores, so a batch of sharp ones
+    # settles its tokens as a batch of flat ones does (the whole-wavefront
+    # fp64 selection of a third of them takes five times as long)
+    d = dev()
+    T, E, k = 16384, 384, 8
+    g = torch.Generator(device=d).manual_seed(3)
+    n = torch.randn((T, E), generator=g, device=d)
+    cfg, sc = cfg_of(T, E, k), rcd.scoring("softmax", 8, 4)
+    out = dict(topk_idx=torch.empty((T, k), dtype=torch.int32, device=d), gates=torch.empty((T, k), device=d))
+
+    def us(l):
+        times = []
+        for _ in range(9):
+            a, b = (torch.cuda.Event(enable_timing=True) for _ in range(2))
+            a.record()
+            for _ in range(20):
+                rcd.route_scored(cfg, sc, l, None, out=out)
+            b.record()
+            torch.cuda.synchronize()
+            times.append(a.elapsed_time(b) * 50)
+        return sorted(times)[4]
+    us(n)
+    flat, sharp = us(1.5 * n), us(16.0 * n)
+    say("softmax scores, flat and sharp, us", flat, sharp)
+    assert sharp <= 2.5 * flat
