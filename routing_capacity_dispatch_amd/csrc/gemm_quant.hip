@@ -10,6 +10,13 @@
 // lane l takes bytes 16 (l >> 4) .. + 15 and 64 + 16 (l >> 4) .. + 15 of row
 // l & 15, which makes each load instruction read 64 contiguous bytes a row.
 //
+// Of 8 consecutive products the 8-bit instruction keeps the bits down to 2^-13
+// of the largest.  Where the weights' bytes bound a kernel (few rows), and for
+// fp32 results, the values are widened to bf16 instead (exact, as are their
+// products in fp32) and four bf16 instructions take a block: no bits are
+// dropped, and few rows cost the same (1 x 6144 x 2048 4.55 and 4.59 us; 4
+// tokens x 8 of 64 experts, L 2048, F 1024, 36 us either way).
+//
 // Measured: 1 x 6144 x 2048 4.5 us (2.8 TB/s: a launch and one latency of
 // memory); 8192 x 6144 x 4096 181 us (2.27 PF: matrix cores at the power
 // limit, 156 us without the loads); 1000 x 2056 x 4224 in fp32 35 us (0.5 PF:
@@ -98,7 +105,7 @@ __device__ __forceinline__ void expert_range(const int32_t* offsets, int e, int6
 // Bound by the bytes of the weights, which are read once: a wavefront takes
 // 16 columns (rows of B) and up to 16 MT rows of A, both straight from
 // memory.  The weights are the matrix instruction's first operand, so a lane
-// holds 4 neighbouring columns of one row.  kSpan blocks' loads are in flight
+// holds 4 neighbouring columns of one row.  Sums drop no bits.  kSpan blocks' loads are in flight
 // together before the first is used: 4 KiB per wavefront and block.
 constexpr int kSpan = 4;
 
@@ -111,7 +118,7 @@ struct BScales {
 
 // acc[i] += scaled products of blocks [b0, b1): rows i of A at arow[i], their
 // scales at sa[i], a_step floats a block.
-template <int MT, bool kRowScale, bool kWide>
+template <int MT, bool kRowScale>
 __device__ __forceinline__ void span_blocks(const char* brow, const BScales<kRowScale>& sb, const char* const* arow,
                                             const float* const* sa, int64_t a_step, int b0, int b1, int lane,
                                             f32x4_t* acc) {
@@ -136,11 +143,7 @@ __device__ __forceinline__ void span_blocks(const char* brow, const BScales<kRow
       if (b + u >= b1) break;
 #pragma unroll
       for (int i = 0; i < MT; ++i) {
-        f32x4_t p;
-        if constexpr (kWide)
-          p = mfma_block(widen(fb[u]), widen(fa[u][i]));
-        else
-          p = mfma_block(fb[u], fa[u][i]);
+        const f32x4_t p = mfma_block(widen(fb[u]), widen(fa[u][i]));
 #pragma unroll
         for (int r = 0; r < 4; ++r) acc[i][r] = fmaf(p[r], ta[u][i] * tb[u][kRowScale ? r : 0], acc[i][r]);
       }
@@ -153,7 +156,7 @@ __device__ __forceinline__ void span_blocks(const char* brow, const BScales<kRow
 // in LDS in a fixed order.
 constexpr int kSkinnyWaves = 4;
 
-template <int MT, int KS, bool kRowScale, bool kWide>
+template <int MT, int KS, bool kRowScale>
 __global__ __launch_bounds__(64 * kSkinnyWaves) void skinny_kernel(QuantGemm g) {
   __shared__ f32x4_t part[kSkinnyWaves][MT][64];
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
@@ -184,7 +187,7 @@ __global__ __launch_bounds__(64 * kSkinnyWaves) void skinny_kernel(QuantGemm g) 
     sa[i] = g.a_scale + m;
     acc[i] = f32x4_t{0.f, 0.f, 0.f, 0.f};
   }
-  span_blocks<MT, kRowScale, kWide>(brow, sb, arow, sa, g.a_scale_ld, b0, b1, lane, acc);
+  span_blocks<MT, kRowScale>(brow, sb, arow, sa, g.a_scale_ld, b0, b1, lane, acc);
   if constexpr (KS > 1) {
 #pragma unroll
     for (int i = 0; i < MT; ++i) part[wave][i][lane] = acc[i];
@@ -320,11 +323,11 @@ __global__ __launch_bounds__(64 * kSkinnyWaves) void few_rows_kernel(FewRows g) 
 #pragma unroll
       for (int u = 0; u < U; ++u) {
         if (b + u >= b1) break;
-        const Frag8 fa = load_frag(arow + (int64_t)(b + u) * kQB, lane);
+        const Wide fa = widen(load_frag(arow + (int64_t)(b + u) * kQB, lane));
         const float x = sa[(b + u) * a_step];
 #pragma unroll
         for (int i = 0; i < W; ++i) {
-          const f32x4_t p = mfma_block(w[s][u][i], fa);
+          const f32x4_t p = mfma_block(widen(w[s][u][i]), fa);
           const float y = x * t[s][u][i];
 #pragma unroll
           for (int r = 0; r < 4; ++r) acc[i][r] = fmaf(p[r], y, acc[i][r]);
@@ -622,16 +625,16 @@ __device__ __forceinline__ int pipe_barriers(int n) { return n == 0 ? 0 : n + 1 
 // the last one's index): an expert's last tile is half empty on average, and
 // a wavefront whose band is empty leaves the matrix cores to the one that
 // shares its SIMD.  Loads and barriers are those of every variant.
-template <class TL, int kMode, int M = QAcc<TL>::MI>
+template <class TL, int kMode, bool kWide, int M = QAcc<TL>::MI>
 __device__ __forceinline__ void pipe_rows(Stager<TL>& src, int nb, char* lds, QAcc<TL>& acc, int last) {
   if constexpr (M > 2) {
     const int band = last + 1 - (int)(threadIdx.x >> 6) / TL::WGN * TL::WM;
     if (__builtin_amdgcn_readfirstlane(band) <= (M - 2) * kMB) {
-      pipe_rows<TL, kMode, M - 2>(src, nb, lds, acc, last);
+      pipe_rows<TL, kMode, kWide, M - 2>(src, nb, lds, acc, last);
       return;
     }
   }
-  quant_pipe<TL, kMode, false, M>(src, nb, lds, acc, threadIdx.x >> 6);
+  quant_pipe<TL, kMode, kWide, M>(src, nb, lds, acc, threadIdx.x >> 6);
 }
 
 // Row of this lane's results of row block mi, and the first of its 4 columns
@@ -758,7 +761,7 @@ __global__ __launch_bounds__(TL::THREADS* KG) void product_kernel(QuantGemm g, i
   }
   QAcc<TL> acc;
   if constexpr (kGrouped)
-    pipe_rows<TL, kMode>(src, nb, lds, acc, mlast);
+    pipe_rows<TL, kMode, kWide>(src, nb, lds, acc, mlast);
   else
     quant_pipe<TL, kMode, kWide, QAcc<TL>::MI, KG>(src, nb, lds + group * QTile<TL>::LDS, acc, wave);
   constexpr int MI = QAcc<TL>::MI, NI = QAcc<TL>::NI;
@@ -856,7 +859,8 @@ __global__ __launch_bounds__(256) void reduce_kernel(QuantGemm g, const float* _
 
 // Hidden tile: 128 features, gate and up rows interleaved in 16-row blocks,
 // so a lane holds both halves of its features.
-template <class TL>
+// kWide: sums without dropped bits.
+template <class TL, bool kWide>
 __global__ __launch_bounds__(TL::THREADS) void gate_up_kernel(QuantGateUp g, int tiles_m) {
   static_assert(TL::BN == 2 * kQB, "one feature block per tile");
   __shared__ __attribute__((aligned(1024))) char lds[QTile<TL>::LDS];
@@ -901,7 +905,7 @@ __global__ __launch_bounds__(TL::THREADS) void gate_up_kernel(QuantGateUp g, int
     src.s_step = 1;
   }
   QAcc<TL> acc;
-  pipe_rows<TL, kGateUp>(src, nb, lds, acc, mlast);
+  pipe_rows<TL, kGateUp, kWide>(src, nb, lds, acc, mlast);
   // column blocks 2 q (gate) and 2 q + 1 (up) hold the same features: h over
   // the gate registers, and its largest magnitude per row: in the lane, the 4
   // lanes of the row, then the wavefronts of the row
@@ -965,7 +969,7 @@ inline unsigned pad8(int64_t n) { return (unsigned)((n + 7) / 8 * 8); }
 struct Form {
   bool skinny;
   bool big;    // 256 x 256 tiles (else 128 x 128)
-  bool wide;   // bf16 matrix instructions on the widened values
+  bool wide;   // tiles: bf16 matrix instructions on the widened values
   int parts;   // shares of K
   int groups;  // groups of wavefronts in a workgroup that share K again
 };
@@ -1031,36 +1035,29 @@ void launch_grouped(const QuantGemm& g, hipStream_t s) {
 }
 
 template <int MT, int KS>
-void launch_skinny_as(const QuantGemm& g, const Form& f, hipStream_t s) {
+void launch_skinny_as(const QuantGemm& g, hipStream_t s) {
   const dim3 grid((unsigned)cdiv(g.N, 16 * (kSkinnyWaves / KS)));
   constexpr int T = 64 * kSkinnyWaves;
-  if (g.b_rows == 1) {
-    if (f.wide)
-      skinny_kernel<MT, KS, true, true><<<grid, T, 0, s>>>(g);
-    else
-      skinny_kernel<MT, KS, true, false><<<grid, T, 0, s>>>(g);
-  } else {
-    if (f.wide)
-      skinny_kernel<MT, KS, false, true><<<grid, T, 0, s>>>(g);
-    else
-      skinny_kernel<MT, KS, false, false><<<grid, T, 0, s>>>(g);
-  }
+  if (g.b_rows == 1)
+    skinny_kernel<MT, KS, true><<<grid, T, 0, s>>>(g);
+  else
+    skinny_kernel<MT, KS, false><<<grid, T, 0, s>>>(g);
 }
 
-void launch_skinny(const QuantGemm& g, const Form& f, hipStream_t s) {
+void launch_skinny(const QuantGemm& g, hipStream_t s) {
   // four wavefronts per column tile while that leaves the chip short of 2048
   // wavefronts and each a span of K
   const bool split = cdiv(g.N, 16) < 2048 && g.K / kQB > kSpan;
   if (g.M > 16) {
     if (split)
-      launch_skinny_as<2, 4>(g, f, s);
+      launch_skinny_as<2, 4>(g, s);
     else
-      launch_skinny_as<2, 1>(g, f, s);
+      launch_skinny_as<2, 1>(g, s);
   } else {
     if (split)
-      launch_skinny_as<1, 4>(g, f, s);
+      launch_skinny_as<1, 4>(g, s);
     else
-      launch_skinny_as<1, 1>(g, f, s);
+      launch_skinny_as<1, 1>(g, s);
   }
 }
 
@@ -1068,7 +1065,7 @@ hipError_t launch_quant_gemm(const QuantGemm& g, void* ws, hipStream_t s) {
   if (g.M <= 0 || g.N <= 0) return hipSuccess;
   const Form f = product_form(g);
   if (f.skinny) {
-    launch_skinny(g, f, s);
+    launch_skinny(g, s);
     return hipGetLastError();
   }
   if (g.offsets) {
@@ -1096,12 +1093,12 @@ hipError_t launch_quant_gemm(const QuantGemm& g, void* ws, hipStream_t s) {
   return hipGetLastError();
 }
 
-template <class TL>
+template <class TL, bool kWide>
 void launch_hidden(const QuantGateUp& g, hipStream_t s) {
   const int64_t tn = g.F / kQB;
   const int64_t tm = cdiv(g.M, TL::BM);
   const int64_t tiles = g.offsets ? (tm + g.E) * tn : tm * tn * g.E;
-  gate_up_kernel<TL><<<pad8(tiles), TL::THREADS, 0, s>>>(g, (int)tm);
+  gate_up_kernel<TL, kWide><<<pad8(tiles), TL::THREADS, 0, s>>>(g, (int)tm);
 }
 
 // Mean rows per expert up to which the experts' rows go straight from memory.
@@ -1154,11 +1151,16 @@ hipError_t launch_quant_gate_up(const QuantGateUp& g, hipStream_t s) {
   // row blocks that hold rows, above (64 experts, L 2048, F 1024, top-8, us for
   // means of 16, 32, 48, 64, 96, 192 rows: 94, 108, 115, 120, 138, 202 with the
   // one, 104, 108, 118, 126, 134, 187 with the other; 128 experts, L 4096,
-  // F 1024, top-4, means of 32, 64: 370, 430 and 381, 411)
+  // F 1024, top-4, means of 32, 64: 370, 430 and 381, 411).  The small tiles sum
+  // by bf16 instructions, so that the rows are requantised from sums without
+  // dropped bits: the weights' bytes bound them (64 experts, L 2048, F 1024,
+  // means of 16, 32, 48: 92, 100, 105 us so, 91, 97, 102 by 8-bit ones).  The
+  // large ones are bound by the matrix cores (mean of 512: 446 us, 314 by 8-bit
+  // ones; error against fp64 0.0017 and 0.0020 of the norm, bf16's rounding 0.0017)
   if ((g.offsets ? cdiv(g.M, g.E) : g.M) <= 48)
-    launch_hidden<E64>(g, s);
+    launch_hidden<E64, true>(g, s);
   else
-    launch_hidden<T256>(g, s);
+    launch_hidden<T256, false>(g, s);
   return hipGetLastError();
 }
 

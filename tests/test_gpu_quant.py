@@ -650,3 +650,64 @@ def test_rows_without_numbers_stay_among_themselves(counts, bad):
     torch.cuda.synchronize()
     rows = [r for r in range(sum(counts)) if r != 1]
     assert torch.equal(got[rows], ref[rows])
+
+
+# ------------------------------------------- sums without dropped bits
+@pytest.mark.parametrize("block", [1, 128])
+@pytest.mark.parametrize("M,N,K", [(1, 400, 2048), (7, 130, 4096), (16, 260, 1280), (17, 64, 384), (32, 300, 2176)])
+def test_gemm_of_few_rows_drops_no_bits(M, N, K, block):
+    # up to 32 rows the bf16 result is the rounded fp32 sum: products are
+    # exact, at most K + K / 128 + 4 roundings of the magnitudes' sum
+    a, sa, b, sb = operands(M, N, K, block, M + K)
+    c = rcd.gemm_quant(a, sa, b, sb, block)
+    torch.cuda.synchronize()
+    ref, mag, _ = gemm_ref(a, sa, b, sb, block)
+    tol = (K + K // 128 + 4) * 2.0 ** -24 * mag
+    assert (np.abs(np64(c) - ref) <= tol + 2.0 ** -8 * (np.abs(ref) + tol)).all()
+    # the same sums, rounded once
+    c32 = rcd.gemm_quant(a, sa, b, sb, block, torch.float32)
+    assert torch.equal(c, c32.to(torch.bfloat16))
+
+
+@pytest.mark.parametrize("E,L,F,counts", [
+    (4, 512, 256, [1, 0, 4, 2]), (2, 2048, 128, [3, 9]), (3, 1024, 1152, [0, 17, 1]), (2, 4224, 256, [2, 3]),  # few rows
+    (2, 128, 4352, [4, 2]), (2, 640, 512, [5, 7]),
+    (2, 512, 256, [40, 9]), (3, 1152, 128, [64, 1, 70]), (2, 2176, 384, [30, 50]), (1, 128, 128, [7])])    # 64-row tiles
+def test_hidden_rows_are_quantised_from_fp32_sums(E, L, F, counts):
+    # Up to 48 rows an expert on average, hidden values are quantised from
+    # sums that drop no bits.  x holds 16, 1 and 2^-6 in neighbouring places
+    # and 448 at each block's end (so its scale is a power of two); gates are
+    # 448 (their sigmoid is 1), ups 16 + 1 + 2^-12 but for the largest of a
+    # block, 448: a hidden value is 17 + 2^-12 of its scale, just above the tie
+    # of 16 and 18, and 16 without the bits of 2^-12 beside 16.  Everything is
+    # exact, also 18 * 448 in bf16.
+    d = dev()
+    n, nb = sum(counts), L // 128
+    x = torch.zeros((n, nb, 128))
+    for g in range(15):
+        x[:, :, 8 * g], x[:, :, 8 * g + 1], x[:, :, 8 * g + 2] = 16.0, 1.0, 2.0 ** -6
+    x[:, :, 127] = 448.0
+    size = 2.0 ** (torch.arange(n) % 5 - 2)  # rows of different magnitude
+    xs = (x.view(n, L) * size[:, None]).to(torch.bfloat16)
+    wg, wu, wd = torch.zeros((F, L)), torch.zeros((F, L)), torch.zeros((L, F))
+    wg[:, 127] = 1.0
+    sign = torch.where(torch.arange(F) % 3 == 1, -1.0, 1.0)
+    for f in range(F):
+        if f % 128 == 0:
+            wu[f, 127] = 1.0
+        else:
+            at = f % nb * 128 + f % 15 * 8
+            wu[f, at], wu[f, at + 1], wu[f, at + 2] = sign[f], sign[f], sign[f] * 2.0 ** -6
+    pick = torch.arange(L) * 7 % F
+    pick = torch.where(pick % 128 == 0, pick + 1, pick)
+    wd[torch.arange(L), pick] = 1.0
+    w = []
+    for v in (wg, wu, wd):
+        q = v.to(torch.float8_e4m3fn)
+        q = q.view(torch.uint8).repeat(E, 1, 1).view(torch.float8_e4m3fn).to(d)
+        w.append((q, torch.ones((E, v.shape[0] // 128, v.shape[1] // 128), device=d)))
+    say("experts, hidden sums near a tie", E, L, F, counts)
+    got = rcd.experts_dropless_quant(rcd.make_config(n, 64, L, E, 1, 1, F), xs.to(d), offsets_of(counts).to(d), *w)
+    torch.cuda.synchronize()
+    want = 18.0 * 448.0 * size[:, None] ** 2 * sign[pick][None, :]
+    assert torch.equal(got.cpu().float(), want)
