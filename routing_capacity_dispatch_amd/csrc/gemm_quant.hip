@@ -1117,7 +1117,9 @@ hipError_t launch_few_of(const FewRows& g, hipStream_t s) {
   const dim3 grid((unsigned)(g.N / (16 * (kSkinnyWaves / KS))), (unsigned)g.E);
   const size_t lds =
       kSource == kE4m3 ? 0 : g.chunk * (size_t)(g.K + kRowPad) + 16 * sizeof(float) * (size_t)(g.K / kQB);
-  if (lds >= 64 * 1024) {
+  // what a launch may have unasked covers the kernel's own LDS too: the partial sums
+  constexpr size_t kOwn = sizeof(f32x4_t) * 64 * (KS > 1 ? kSkinnyWaves : 1) * (kHidden ? 2 : 1);
+  if (lds + kOwn > 64 * 1024) {
     const hipError_t e = hipFuncSetAttribute(reinterpret_cast<const void*>(few_rows_kernel<KS, kSource, kHidden>),
                                              hipFuncAttributeMaxDynamicSharedMemorySize, (int)lds);
     if (e != hipSuccess) return e;

@@ -711,3 +711,11 @@ def test_hidden_rows_are_quantised_from_fp32_sums(E, L, F, counts):
     torch.cuda.synchronize()
     want = 18.0 * 448.0 * size[:, None] ** 2 * sign[pick][None, :]
     assert torch.equal(got.cpu().float(), want)
+
+
+@pytest.mark.parametrize("E,L,F,counts", [(4, 3840, 128, [17, 0, 3, 1]), (4, 128, 3840, [17, 0, 3, 1]),
+                                          (4, 3968, 3584, [1, 18, 2, 0]), (4, 3584, 3968, [16, 2, 0, 4])])
+def test_experts_whose_staged_rows_nearly_fill_64_kib(E, L, F, counts):
+    # 16 staged rows and their scales below 64 KiB of LDS, above it with the
+    # wavefronts' partial sums
+    check_experts(E, L, F, counts, E + L + F, per_expert=3)
