@@ -719,3 +719,129 @@ def test_experts_whose_staged_rows_nearly_fill_64_kib(E, L, F, counts):
     # 16 staged rows and their scales below 64 KiB of LDS, above it with the
     # wavefronts' partial sums
     check_experts(E, L, F, counts, E + L + F, per_expert=3)
+
+
+# ------------------------------------------------------ errors in norm
+def rounding_square(ref):
+    """Mean square sum of the roundings of ref to bf16: uniform within half a step."""
+    half = 2.0 ** (np.floor(np.log2(np.maximum(np.abs(ref), 2.0 ** -100))) - 8)
+    return (half ** 2).sum() / 3
+
+
+@pytest.mark.parametrize("E,L,F,counts,form", [
+    (4, 1024, 512, [1, 0, 12, 7], "few"), (3, 2048, 1024, [5, 9, 4], "few"), (2, 512, 4352, [6, 5], "few"),
+    (3, 1024, 512, [40, 9, 50], "small"), (2, 2048, 384, [64, 30], "small"),
+    (2, 1024, 512, [300, 200], "large"), (8, 2048, 128, [700, 0, 256, 257, 800, 513, 1, 700], "large")])
+def test_experts_error_in_norm(E, L, F, counts, form):
+    # In norm the error is that of rounding the results to bf16 (6 standard
+    # deviations sqrt(0.8 / n) of n squares' mean), and of hidden values a
+    # step off, 2^-3 of the value at most.  Of fp32 sums: one in 10^5 lies
+    # within their 2^-22 or so of a tie (2^-4 apart); three are allowed.  Of
+    # the 8-bit instructions on large tiles: each of 7 products of 8 loses up
+    # to 2^-13 of the largest, about 1.5 of their deviation, so a sum of K is
+    # sqrt(7 / 24) 1.5 2^-13 = 10^-4 of itself off, a product of two sums 1.4
+    # times that, and 2 * 1.4 * 10^-4 / 2^-3.5 = 1/300 lie that near a tie.
+    d = dev()
+    n = sum(counts)
+    w = quant_weights(E, L, F, E + L + F)
+    xs = rand((n, L), L + 9, torch.bfloat16, 0.5).to(d)
+    say("experts in norm", E, L, F, counts)
+    got = np64(rcd.experts_dropless_quant(rcd.make_config(n, 64, L, E, 1, 1, F), xs, offsets_of(counts).to(d), *w))
+    torch.cuda.synchronize()
+    start, square, rounding, norm, size, hidden = 0, 0.0, 0.0, 0.0, 0, 0
+    for e, c in enumerate(counts):
+        if c:
+            rows = np.unique(np.linspace(0, c - 1, 24).astype(int)) + start
+            wg, wu, wd = (bq.values(np64(q[e]), np64(s[e]), 128) for q, s in w)
+            u = bq.values(*bq.quantize(np64(xs)[rows]), 1)
+            ref = bq.values(*bq.quantize(bq.silu(u @ wg.T) * (u @ wu.T)), 1) @ wd.T
+            square += ((got[rows] - ref) ** 2).sum()
+            rounding += rounding_square(ref)
+            norm += (ref ** 2).sum()
+            size += ref.size
+            hidden += len(rows) * F
+        start += c
+    off = 3.0 / hidden if form != "large" else 1.0 / 300
+    say("error over the norm", np.sqrt(square / norm), "of rounding alone", np.sqrt(rounding / norm))
+    assert square <= rounding * (1 + 6 * np.sqrt(0.8 / size)) + (off * 2.0 ** -6 + 2.0 ** -24) * norm
+
+
+@pytest.mark.parametrize("L,F", [(1024, 1152), (4224, 512)])
+def test_forms_of_the_experts_agree(L, F):
+    # the same rows among few (K over up to four wavefronts), among tens and
+    # among hundreds of rows an expert: other orders of the fp32 sums, other
+    # instructions.  Each result is one rounding (2^-8, a third of its square
+    # on average) and few hidden steps from the same value, as above, so two of
+    # them are sqrt(2 (2^-16 / 3 + 2^-6 / 300)) < 2^-6.6 of the norm apart
+    d = dev()
+    w = quant_weights(2, L, F, 11)
+    xs = rand((1100, L), 12, torch.bfloat16).to(d)
+
+    def run(n0, n1):
+        cfg = rcd.make_config(n0 + n1, 64, L, 2, 1, 1, F)
+        o = rcd.experts_dropless_quant(cfg, torch.cat([xs[:n0], xs[600:600 + n1]]), offsets_of([n0, n1]).to(d), *w)
+        torch.cuda.synchronize()
+        return np64(o[:n0]), np64(o[n0:])
+    base = run(600, 500)
+    for n0, n1 in ((3, 5), (6, 6), (40, 30), (100, 120)):
+        for got, ref in zip(run(n0, n1), base):
+            assert np.linalg.norm(got - ref[:got.shape[0]]) <= 2.0 ** -6.6 * np.linalg.norm(ref[:got.shape[0]])
+    # up to 6 rows on average the hidden rows and the outputs are sums of
+    # exact products, whatever shares of K they are added in: a step of bf16
+    # apart at most, and that in few places
+    a, b = run(6, 6)[0][:3], run(3, 9)[0]
+    assert np.array_equal(a, b)
+    assert np.linalg.norm(run(1, 1)[0] - a[:1]) <= 2.0 ** -9 * np.linalg.norm(a[:1])
+
+
+# ------------------------------------------------- straight-through gradient
+def test_training_step_through_8_bit_experts():
+    # scored routing, 8-bit experts and combine forward; backward by
+    # combine_backward_dropless, the bf16 weights that were quantised
+    # (straight through both quantisers), dispatch_backward_dropless and
+    # route_scored_backward, against the formulas in fp64
+    import oracle
+    from gpu_common import TOL_BF16
+    from oracle import scored_routing as sr
+    from _util import rowwise_rel_err
+    d = dev()
+    w = synth.workload("mid_bf16").replace(T=200)
+    cfg = rcd.config_of(w)
+    T, E, k, L, F = w.T, w.n_experts, w.top_k, w.d_latent, w.d_ff
+    z = rand((T, L), 60, torch.bfloat16).to(d)
+    logits, dy = rand((T, E), 61).to(d), rand((T, L), 62, torch.bfloat16).to(d)
+    wb = [(rand((E, r, c), 63 + i) * c ** -0.5).to(torch.bfloat16).to(d) for i, (r, c) in enumerate(((F, L), (F, L), (L, F)))]
+    wq = []
+    for m in wb:
+        q, s = rcd.quantize(m.view(-1, m.shape[2]), 128)
+        wq.append((q.view(m.shape), s.view(E, m.shape[1] // 128, m.shape[2] // 128)))
+    sc = rcd.scoring("sigmoid", 8, 4, 2, True, 1.0)
+    say("training step through 8-bit experts")
+    topk, gates = rcd.route_scored(cfg, sc, logits)
+    ds = rcd.dispatch_dropless(cfg, topk, z)
+    eo = rcd.experts_dropless_quant(cfg, ds["xs"], ds["expert_offsets"], *wq)
+    dg, deo = rcd.combine_backward_dropless(cfg, eo, ds["row_of"], gates, dy)
+    dxs, dw = rcd.experts_backward_dropless(cfg, ds["xs"], ds["expert_offsets"], *wb, deo)
+    dz = rcd.dispatch_backward_dropless(cfg, ds["row_of"], dxs)
+    dl = rcd.route_scored_backward(cfg, sc, logits, topk, dg)
+    torch.cuda.synchronize()
+    ids, g = topk.cpu().numpy(), np64(gates)
+    o = np64(eo)[ds["row_of"].cpu().numpy()]                # [T, k, L]
+    want_dg = (np64(dy)[:, None, :] * o).sum(axis=2)
+    assert rowwise_rel_err(np64(dg), want_dg) <= 2.0 ** -14  # fp32 sums of 512 products
+    rd, mag = sr.backward(logits.cpu().numpy(), ids, np64(dg), "sigmoid", True, 1.0)
+    assert (np.abs(np64(dl) - rd) <= 2.0 ** -20 * mag + 2.0 ** -140).all()
+    w64 = [np64(m) for m in wb]
+    want, wants = np.zeros((T, L)), [np.zeros(m.shape) for m in w64]
+    for e in range(E):
+        rows, js = np.nonzero(ids == e)
+        if len(rows) == 0:
+            assert all(torch.count_nonzero(m[e]) == 0 for m in dw)
+            continue
+        du, *gw = oracle.swiglu_backward(np64(z)[rows], *(m[e] for m in w64), g[rows, js][:, None] * np64(dy)[rows])
+        np.add.at(want, rows, du)
+        for m, x in zip(wants, gw):
+            m[e] = x
+    assert rowwise_rel_err(np64(dz), want) <= TOL_BF16
+    for got, ref in zip(dw, wants):
+        assert np.abs(np64(got) - ref).max() <= TOL_BF16 * np.abs(ref).max()
