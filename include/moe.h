@@ -614,8 +614,9 @@ moe_status moe_route_scored_backward(const moe_config* cfg, const moe_scoring* s
 
 /* Quantise x (device) [rows][cols], ldx elements between rows, dtype MOE_F32
    or MOE_BF16:  per block, amax = max(|x|, 2^-100), scale = amax / 448,
-   q = 448 x / amax rounded to the nearest e4m3 value, ties to even (the
-   quotient rounded once to fp32 before).  block_rows 1 or 128 as above.
+   q = 448 x / amax rounded to the nearest e4m3 value, ties to even; fp32 x
+   whose quotient lies within 2^-22 (relatively) of a tie may take either
+   neighbour.  block_rows 1 or 128 as above.
    transpose 0: R = rows, K = cols; 1: the result is that of x^T (R = cols,
    K = rows), the operand of a gradient's product.
    q       (device, out, 16-byte aligned) [R][K rounded up to 128]

@@ -17,12 +17,14 @@
 // dropped, and few rows cost the same (1 x 6144 x 2048 4.55 and 4.59 us; 4
 // tokens x 8 of 64 experts, L 2048, F 1024, 36 us either way).
 //
-// Measured: 1 x 6144 x 2048 4.5 us (2.8 TB/s: a launch and one latency of
-// memory); 8192 x 6144 x 4096 181 us (2.27 PF: matrix cores at the power
-// limit, 156 us without the loads); 1000 x 2056 x 4224 in fp32 35 us (0.5 PF:
-// 136 tiles, and bf16 instructions).  Experts, 64 of L 2048, F 1024: 4 tokens
-// x 8 38 us (4.5 TB/s of weights), 4096 tokens x 8 320 us (quantiser 40,
-// hidden tiles 170, down 105).
+// Measured: 1 x 6144 x 2048 4.7 us (2.7 TB/s: a launch and one latency of
+// memory), 4 x 6144 x 9216 17.5 us (3.2 TB/s: one span of loads in flight at a
+// time); 8192 x 6144 x 4096 181 us (2.27 PF: matrix cores at the power limit,
+// 156 us without the loads); in fp32 with scales for every row, 6144 x 4096 x
+// 16384 770 us (1.07 PF), 1000 x 2056 x 4224 34 us (0.5 PF: 136 tiles leave 120
+// CUs idle).  Experts, 64 of L 2048, F 1024: 4 tokens x 8 37 us (4.5 TB/s of
+// weights), 4096 tokens x 8 315 to 330 us (quantiser 40, hidden tiles 170, down
+// 105).
 #include <type_traits>
 
 #include "gemm_core.h"

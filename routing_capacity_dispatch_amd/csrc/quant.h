@@ -11,11 +11,14 @@ constexpr float kE4m3Max = 448.0f;
 // scale nor its reciprocal leaves fp32's normal range
 constexpr float kQuantTiny = 7.888609052210118e-31f;  // 2^-100
 
-// Quotients 448 x / amax of one block, each the correctly rounded fp32
-// quotient (one Newton step on the hardware reciprocal) of 7/8 x by amax,
-// times 512: 7/8 x is exact for bf16 x, so a quotient that lies half way
-// between two e4m3 values is met exactly and rounds to even; a product with
-// a rounded 448 / amax would move it off the tie.  amax above 1 is brought
+// Quotients 448 x / amax of one block: 7/8 x by amax, times 512, by one Newton
+// step on the hardware reciprocal, within 2^-23 of the real quotient and equal
+// to it where it is an fp32 number (the step's remainder is then exact).  7/8 x
+// is exact for bf16 x, so a quotient that lies half way between two e4m3
+// values is met exactly and rounds to even, and no other comes that near one;
+// a product with a rounded 448 / amax would move it off the tie.  Of fp32 x
+// 7/8 x is rounded too: quotients within 2^-22 of a tie may take either
+// neighbour.  amax above 1 is brought
 // down by 2^-64 first (exact), so its reciprocal is a normal number.
 struct BlockQuant {
   float c, d, r;

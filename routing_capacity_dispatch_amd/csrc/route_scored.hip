@@ -4,15 +4,21 @@
 //
 // Selected ids are whole numbers, so the keys must be ordered as the formula
 // orders them, whatever an fp32 exponential rounds to.  For k <= 8 a token is
-// first selected from fp32 keys by 16 lanes, four tokens to a wavefront; where
-// two keys that matter lie closer than their error bound (about one token in
-// ten thousand on random logits), and for every other shape, one wavefront
-// selects the token from fp64 keys.
+// first selected from fp32 keys by 16 lanes, four tokens to a wavefront.  Where
+// keys that matter lie closer than their error bound (one token in 500 to 1000
+// for random logits of deviation 1.5, by the bound itself; one in 10^4 for
+// sharp softmax scores), the few near the edge are compared by fp64 keys, one
+// per lane; where they are more than 16, and for every other shape, one
+// wavefront selects the token from fp64 keys.  Sigmoids of many logits far
+// above 10 and no bias are such a batch: fp32 scores all round to 1.
 //
-// Measured, 16384 tokens of 384 experts, sigmoid, top-8 of the best 4 of 8
-// groups: 13.6 us (1.9 TB/s; the sorting networks' issue, not the bytes'
-// 5 us, bounds it); its gradient 7.5 us (3.6 TB/s); one token 4.4 us, a launch
-// and its chain of exchanges.
+// Measured, 16384 tokens of 384 experts, top-8, in us: the best 4 of 8 groups,
+// with a bias, sigmoid 13.7, softmax 17.5 (its error bound's logarithms, the
+// sum and the largest bias); no groups 12.1 and 15.5, no bias either 7.9 and
+// 8.0.  The sorting networks' issue, not the bytes' 5, bounds them.  Saturated
+// sigmoids (logits of deviation 8 and above without a bias): 60 to 90.  k > 8:
+// top-12 of 384 54, top-10 and top-16 of 512 60 and 83.  Gradients: sigmoid 7.6,
+// softmax 10.9.  One token 4.7, a launch and its chain of exchanges.
 #include "common.h"
 #include "kernels.h"
 
