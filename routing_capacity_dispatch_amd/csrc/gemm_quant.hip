@@ -17,14 +17,14 @@
 // dropped, and few rows cost the same (1 x 6144 x 2048 4.55 and 4.59 us; 4
 // tokens x 8 of 64 experts, L 2048, F 1024, 36 us either way).
 //
-// Measured: 1 x 6144 x 2048 4.7 us (2.7 TB/s: a launch and one latency of
-// memory), 4 x 6144 x 9216 17.5 us (3.2 TB/s: one span of loads in flight at a
-// time); 8192 x 6144 x 4096 181 us (2.27 PF: matrix cores at the power limit,
-// 156 us without the loads); in fp32 with scales for every row, 6144 x 4096 x
-// 16384 770 us (1.07 PF), 1000 x 2056 x 4224 34 us (0.5 PF: 136 tiles leave 120
-// CUs idle).  Experts, 64 of L 2048, F 1024: 4 tokens x 8 37 us (4.5 TB/s of
-// weights), 4096 tokens x 8 315 to 330 us (quantiser 40, hidden tiles 170, down
-// 105).
+// Measured: 1 x 6144 x 2048 4.4 us (2.9 TB/s: a launch and one latency of
+// memory), 4 x 6144 x 9216 16.8 us (3.4 TB/s: one span of loads in flight at a
+// time); 8192 x 6144 x 4096 171 to 181 us (2.3 to 2.4 PF: matrix cores at the
+// power limit, 156 us without the loads); in fp32 with scales for every row,
+// 6144 x 4096 x 16384 778 us (1.06 PF), 1000 x 2056 x 4224 32 us (0.54 PF: 136
+// tiles leave 120 CUs idle).  Experts, 64 of L 2048, F 1024: 4 tokens x 8 36 us
+// (4.7 TB/s of weights), 4096 tokens x 8 313 to 331 us (quantiser 40, hidden
+// tiles 170, down 105).
 #include <type_traits>
 
 #include "gemm_core.h"
@@ -1158,7 +1158,8 @@ hipError_t launch_quant_gate_up(const QuantGateUp& g, hipStream_t s) {
   // F 1024, top-4, means of 32, 64: 370, 430 and 381, 411).  The small tiles sum
   // by bf16 instructions, so that the rows are requantised from sums without
   // dropped bits: the weights' bytes bound them (64 experts, L 2048, F 1024,
-  // means of 16, 32, 48: 92, 100, 105 us so, 91, 97, 102 by 8-bit ones).  The
+  // means of 16, 32, 48: 92, 100, 105 us so, 91, 97, 102 by 8-bit ones; the
+  // Marin-shaped layer, mean of 43: this launch 1.57 and 1.47 ms).  The
   // large ones are bound by the matrix cores (mean of 512: 446 us, 314 by 8-bit
   // ones; error against fp64 0.0017 and 0.0020 of the norm, bf16's rounding 0.0017)
   if ((g.offsets ? cdiv(g.M, g.E) : g.M) <= 48)

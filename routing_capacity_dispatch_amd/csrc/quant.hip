@@ -6,9 +6,9 @@
 // or 64 bytes of loads, one 16-byte store), so 8 lanes hold a 1 x 128 block
 // and its maximum is three lane exchanges; several blocks per thread keep
 // that many loads in flight before the first is used.
-// Measured: 16384 x 6144 in 1 x 128 blocks, plain and transposed, bf16 53 and 54
-// us (5.7 TB/s), fp32 93 and 108; in 128 x 128 blocks 49 and 53, 95 and 105; 2056
-// x 4100 fp32, transposed, 128 x 128 10.5 us (4.1 TB/s: two workgroups a CU, so
+// Measured: 16384 x 6144 in 1 x 128 blocks, plain and transposed, bf16 50 and 53
+// us (6.1 TB/s), fp32 92 and 107; in 128 x 128 blocks 48 and 53, 95 and 106; 2056
+// x 4100 fp32, transposed, 128 x 128 10.1 us (4.2 TB/s: two workgroups a CU, so
 // the first loads' latency shows).
 #include <type_traits>
 

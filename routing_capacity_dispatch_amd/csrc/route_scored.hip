@@ -13,12 +13,12 @@
 // above 10 and no bias are such a batch: fp32 scores all round to 1.
 //
 // Measured, 16384 tokens of 384 experts, top-8, in us: the best 4 of 8 groups,
-// with a bias, sigmoid 13.7, softmax 17.5 (its error bound's logarithms, the
-// sum and the largest bias); no groups 12.1 and 15.5, no bias either 7.9 and
-// 8.0.  The sorting networks' issue, not the bytes' 5, bounds them.  Saturated
+// with a bias, sigmoid 12.5, softmax 17.1 (its error bound's logarithms, the
+// sum and the largest bias); no groups 11.2 and 15.2, no bias either 7.3 and
+// 7.7.  The sorting networks' issue, not the bytes' 5, bounds them.  Saturated
 // sigmoids (logits of deviation 8 and above without a bias): 60 to 90.  k > 8:
-// top-12 of 384 54, top-10 and top-16 of 512 60 and 83.  Gradients: sigmoid 7.6,
-// softmax 10.9.  One token 4.7, a launch and its chain of exchanges.
+// top-12 of 384 54, top-10 and top-16 of 512 55 and 79.  Gradients: sigmoid 7.1,
+// softmax 10.6.  One token 4.2, a launch and its chain of exchanges.
 #include "common.h"
 #include "kernels.h"
 
