@@ -404,3 +404,22 @@ def test_sharp_softmax_scores_keep_the_pace():
     flat, sharp = us(1.5 * n), us(16.0 * n)
     say("softmax scores, flat and sharp, us", flat, sharp)
     assert sharp <= 2.5 * flat
+
+
+@pytest.mark.parametrize("kind", ["sigmoid", "softmax"])
+@pytest.mark.parametrize("E,G,tg,k", [(64, 8, 3, 6), (256, 16, 5, 8), (60, 6, 2, 4)])
+def test_group_sums_past_fp32(E, G, tg, k, kind):
+    # two biases of a group whose sum is no fp32 number: still ordered as real
+    # numbers, in both directions
+    rng = np.random.default_rng(E)
+    gs = E // G
+    bias = (0.05 * rng.standard_normal(E)).astype(np.float32)
+    for sign in (1.0, -1.0):
+        b = bias.copy()
+        for g in rng.permutation(G)[:G - 1]:
+            if sign > 0:
+                b[g * gs + rng.permutation(gs)[:2]] = rng.uniform(1.8e38, 2.9e38, 2).astype(np.float32)
+            else:
+                b[g * gs:(g + 1) * gs] = -rng.uniform(1.8e38, 2.9e38, gs).astype(np.float32)
+        l = (1.5 * rng.standard_normal((30, E))).astype(np.float32)
+        check(30, E, k, l, b, kind, G, tg, 2)
