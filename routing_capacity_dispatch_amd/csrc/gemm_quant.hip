@@ -1158,7 +1158,8 @@ hipError_t launch_quant_gate_up(const QuantGateUp& g, hipStream_t s) {
   // F 1024, top-4, means of 32, 64: 370, 430 and 381, 411).  The small tiles sum
   // by bf16 instructions, so that the rows are requantised from sums without
   // dropped bits: the weights' bytes bound them (64 experts, L 2048, F 1024,
-  // means of 16, 32, 48: 92, 100, 105 us so, 91, 97, 102 by 8-bit ones; the
+  // means of 16, 32, 48: 92, 100, 105 us so, 91, 97, 102 by 8-bit ones; 128
+  // experts, L 4096, F 2048, mean of 41: 622 and 593; the
   // Marin-shaped layer, mean of 43: this launch 1.57 and 1.47 ms).  The
   // large ones are bound by the matrix cores (mean of 512: 446 us, 314 by 8-bit
   // ones; error against fp64 0.0017 and 0.0020 of the norm, bf16's rounding 0.0017)
