@@ -732,6 +732,77 @@ moe_status moe_forward_dropless_quant(const moe_config* cfg, const moe_scoring* 
                                       const moe_dropless_taps* taps, int64_t* counts, void* ws,
                                       size_t ws_bytes, void* stream);
 
+/* ------------------------------------------------------------------------
+ * Linear layers with their epilogue, and their gradients: the dense parts
+ * around the routed path (latent projection, up-projection with the block's
+ * residual) as operators of their own.  bf16 operands, fp32 accumulation,
+ * each result rounded once.  Rows may be strided (ld in elements, at least
+ * the row's length, at most 2^22), at any alignment; sizes are any, 0
+ * included.  M up to 2^30, N and K up to 2^22; MOE_ERR_UNSUPPORTED past that
+ * or past 2^23 - 8 tiles of 128 x 128.
+ * ------------------------------------------------------------------------ */
+typedef enum {
+  MOE_ACT_NONE = 0,
+  MOE_ACT_RELU = 1,
+  MOE_ACT_SILU = 2, /* u / (1 + exp(-u))         */
+  MOE_ACT_GELU = 3  /* u (1 + erf(u / sqrt 2)) / 2 */
+} moe_act;
+
+/* u = x W^T + bias;  pre = u;  y = act(u) + residual. */
+typedef struct {
+  int64_t M, N, K;
+  const void* x;        /* [M][ldx] bf16                                     */
+  int64_t ldx;
+  const void* w;        /* [N][ldw] bf16                                     */
+  int64_t ldw;
+  const void* bias;     /* [N] bias_dtype, or NULL                           */
+  const void* residual; /* [M][ldr] out_dtype, or NULL; may be y itself      */
+  int64_t ldr;
+  void* y;              /* (out) [M][ldy] out_dtype                          */
+  int64_t ldy;
+  void* pre;            /* (out) [M][ldp] bf16, or NULL: kept for a backward */
+  int64_t ldp;
+  int32_t act;          /* moe_act                                           */
+  int32_t bias_dtype;   /* moe_dtype                                         */
+  int32_t out_dtype;    /* moe_dtype                                         */
+  int32_t reserved;     /* must be 0                                         */
+} moe_linear_args;
+
+/* Bytes of workspace (may be 0: then ws may be NULL; always 0 up to 64 rows);
+   sizes, leading dimensions, types and the pointers' alignment are read.  All
+   pointers device; ws 256-byte aligned. */
+moe_status moe_linear_ws_bytes(const moe_linear_args* args, size_t* bytes);
+moe_status moe_linear(const moe_linear_args* args, void* ws, size_t ws_bytes, void* stream);
+
+/* Gradients for dy, the gradient of y:  d = dy act'(pre), rounded to bf16 for
+   the two products (not where act is MOE_ACT_NONE and dy is bf16: it is dy),
+     dx = d W,  dw = d^T x,  db = the sum of d (before that rounding) over rows.
+   The residual's gradient is dy.  act'(0) of MOE_ACT_RELU is 0. */
+typedef struct {
+  int64_t M, N, K;
+  const void* dy;   /* [M][lddy] dy_dtype                                 */
+  int64_t lddy;
+  const void* pre;  /* [M][ldp] bf16, as moe_linear kept it; NULL: act is none */
+  int64_t ldp;
+  const void* x;    /* [M][ldx] bf16                                      */
+  int64_t ldx;
+  const void* w;    /* [N][ldw] bf16                                      */
+  int64_t ldw;
+  void* dx;         /* (out) [M][lddx] bf16, or NULL: not computed        */
+  int64_t lddx;
+  void* dw;         /* (out) [N][lddw] bf16, or NULL                      */
+  int64_t lddw;
+  float* db;        /* (out) [N] fp32, or NULL                            */
+  int32_t act;      /* moe_act                                            */
+  int32_t dy_dtype; /* moe_dtype                                          */
+  int32_t reserved; /* must be 0                                          */
+} moe_linear_grad;
+
+/* As above; M up to 4194240 (MOE_ERR_UNSUPPORTED past that).  x may be NULL
+   without dw, w without dx. */
+moe_status moe_linear_backward_ws_bytes(const moe_linear_grad* args, size_t* bytes);
+moe_status moe_linear_backward(const moe_linear_grad* args, void* ws, size_t ws_bytes, void* stream);
+
 #ifdef __cplusplus
 }
 #endif

@@ -21,7 +21,8 @@ __all__ = ["make_config", "plan", "route", "dispatch", "experts", "combine", "fo
            "combine_backward", "experts_backward", "dispatch_backward", "route_backward",
            "combine_backward_dropless", "experts_backward_dropless", "dispatch_backward_dropless",
            "BackwardRouted", "scoring", "route_scored", "route_scored_backward", "quantize", "gemm_quant",
-           "experts_dropless_quant", "quantize_weights", "ForwardDroplessQuant", "library", "MoeError"]
+           "experts_dropless_quant", "quantize_weights", "ForwardDroplessQuant", "linear", "linear_backward",
+           "library", "MoeError"]
 
 MoeError = abi.MoeError
 _DT = {"f32": abi.MOE_F32, "bf16": abi.MOE_BF16, torch.float32: abi.MOE_F32,
@@ -786,3 +787,100 @@ class ForwardDroplessQuant:
                 x.data_ptr(), self.y.data_ptr(), C.byref(self.taps) if self.taps is not None else None,
                 self.counts.data_ptr(), self.ws.data_ptr(), self.ws.numel())
         return self.y
+
+
+# ------------------------------------------------------------- linear layers
+def _matrix(t, shape, dtypes, what, dev=None):
+    """Leading dimension of a two-dimensional tensor of this shape with contiguous columns (rows may be strided)."""
+    if not (isinstance(t, torch.Tensor) and t.shape == shape and t.dtype in dtypes and t.is_cuda
+            and (dev is None or t.device == dev) and (shape[1] <= 1 or t.stride(1) == 1)
+            and (shape[0] <= 1 or t.stride(0) >= shape[1])):
+        raise ValueError(f"{what} must be a {' or '.join(str(d) for d in dtypes)} tensor of shape {tuple(shape)} with "
+                         f"contiguous columns" + (f" on {dev}" if dev is not None else " on a GPU"))
+    return t.stride(0) if shape[0] > 1 else max(shape[1], 1)
+
+
+def _with_workspace(name, dev, args, ws):
+    """Call `name`(args, workspace): with none first where the caller has none, and one of the size asked for if it needs one."""
+    if ws is None:
+        try:
+            return _launch(name, dev, C.byref(args), None, 0)
+        except MoeError as e:
+            if e.status != abi.MOE_ERR_WORKSPACE:
+                raise
+    n = C.c_size_t(0)
+    abi.check(name + "_ws_bytes", getattr(library(), name + "_ws_bytes")(C.byref(args), C.byref(n)))
+    ws = _workspace(ws, n.value, dev)
+    _launch(name, dev, C.byref(args), ws.data_ptr(), ws.numel())
+
+
+_BF16 = (torch.bfloat16,)
+_FLOATS = (torch.bfloat16, torch.float32)
+
+
+def linear(x, w, bias=None, act: str = "none", residual=None, out_dtype=torch.bfloat16, save_pre: bool = False,
+           out=None, ws=None):
+    """y [M, N] = act(x w^T + bias) + residual (moe_linear): x [M, K] and w
+    [N, K] bf16, bias [N] bf16 or fp32, residual and y of out_dtype (bf16 or
+    fp32); residual may be out.  With save_pre, (y, the pre-activation in
+    bf16), which linear_backward takes.  Rows may be strided."""
+    _check(act in abi.ACTS, "act is 'none', 'relu', 'silu' or 'gelu'")
+    _check(isinstance(x, torch.Tensor) and x.dim() == 2 and isinstance(w, torch.Tensor) and w.dim() == 2,
+           "x and w must be two-dimensional tensors")
+    _check(out_dtype in _FLOATS, "out_dtype is bfloat16 or float32")
+    (M, K), N = x.shape, w.shape[0]
+    ldx = _matrix(x, (M, K), _BF16, "x")
+    dev = x.device
+    ldw = _matrix(w, (N, K), _BF16, "w", dev)
+    if bias is not None and not (isinstance(bias, torch.Tensor) and bias.shape == (N,) and bias.dtype in _FLOATS
+                                 and bias.device == dev and bias.is_contiguous()):
+        raise ValueError(f"bias must be a contiguous bf16 or fp32 tensor of shape ({N},) on {dev}")
+    ldr = _matrix(residual, (M, N), (out_dtype,), "residual", dev) if residual is not None else 0
+    if out is None:
+        out, ldy = _new(M, N, out_dtype, dev), max(N, 1)
+    else:
+        ldy = _matrix(out, (M, N), (out_dtype,), "out", dev)
+    pre = _new(M, N, torch.bfloat16, dev) if save_pre else None
+    a = abi.MoeLinearArgs(M, N, K, x.data_ptr(), ldx, w.data_ptr(), ldw, None if bias is None else bias.data_ptr(),
+                          None if residual is None else residual.data_ptr(), ldr, out.data_ptr(), ldy,
+                          None if pre is None else pre.data_ptr(), max(N, 1), abi.ACTS[act],
+                          abi.MOE_F32 if bias is not None and bias.dtype == torch.float32 else abi.MOE_BF16,
+                          _DT[out_dtype], 0)
+    _with_workspace("moe_linear", dev, a, ws)
+    return (out, pre) if save_pre else out
+
+
+def linear_backward(dy, x, w, pre=None, act: str = "none", bias: bool = True, need_dx: bool = True,
+                    need_dw: bool = True, dx=None, dw=None, db=None, ws=None):
+    """(dx [M, K] bf16, dw [N, K] bf16, db [N] fp32) of linear for dy [M, N]
+    (bf16 or fp32) and the pre-activation it kept (moe_linear_backward); None
+    in the place of what need_dx, need_dw and bias leave out.  The residual's
+    gradient is dy."""
+    _check(act in abi.ACTS, "act is 'none', 'relu', 'silu' or 'gelu'")
+    _check(isinstance(x, torch.Tensor) and x.dim() == 2 and isinstance(w, torch.Tensor) and w.dim() == 2,
+           "x and w must be two-dimensional tensors")
+    (M, K), N = x.shape, w.shape[0]
+    ldx = _matrix(x, (M, K), _BF16, "x")
+    dev = x.device
+    ldw = _matrix(w, (N, K), _BF16, "w", dev)
+    lddy = _matrix(dy, (M, N), _FLOATS, "dy", dev)
+    _check(act == "none" or pre is not None, "the pre-activation is needed")
+    ldp = _matrix(pre, (M, N), _BF16, "pre", dev) if act != "none" else 0
+
+    def out(t, rows, what):
+        t = _new(rows, K, torch.bfloat16, dev) if t is None else t
+        return t, _matrix(t, (rows, K), _BF16, what, dev)
+    dx, lddx = out(dx, M, "dx") if need_dx else (None, 0)
+    dw, lddw = out(dw, N, "dw") if need_dw else (None, 0)
+    if not bias:
+        db = None
+    elif db is None:
+        db = torch.empty(N, dtype=torch.float32, device=dev)
+    else:
+        _rows(db, (N,), torch.float32, "db", dev)
+    a = abi.MoeLinearGrad(M, N, K, dy.data_ptr(), lddy, pre.data_ptr() if ldp else None, ldp, x.data_ptr(), ldx,
+                          w.data_ptr(), ldw, None if dx is None else dx.data_ptr(), lddx,
+                          None if dw is None else dw.data_ptr(), lddw, None if db is None else db.data_ptr(),
+                          abi.ACTS[act], _DT[dy.dtype], 0)
+    _with_workspace("moe_linear_backward", dev, a, ws)
+    return dx, dw, db

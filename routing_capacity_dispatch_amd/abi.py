@@ -87,6 +87,22 @@ class MoeQuantWeights(C.Structure):
                                              "s_output")])
 
 
+class MoeLinearArgs(C.Structure):
+    _fields_ = [("M", C.c_int64), ("N", C.c_int64), ("K", C.c_int64), ("x", C.c_void_p), ("ldx", C.c_int64),
+                ("w", C.c_void_p), ("ldw", C.c_int64), ("bias", C.c_void_p), ("residual", C.c_void_p),
+                ("ldr", C.c_int64), ("y", C.c_void_p), ("ldy", C.c_int64), ("pre", C.c_void_p), ("ldp", C.c_int64),
+                ("act", C.c_int32), ("bias_dtype", C.c_int32), ("out_dtype", C.c_int32), ("reserved", C.c_int32)]
+
+
+class MoeLinearGrad(C.Structure):
+    _fields_ = [("M", C.c_int64), ("N", C.c_int64), ("K", C.c_int64), ("dy", C.c_void_p), ("lddy", C.c_int64),
+                ("pre", C.c_void_p), ("ldp", C.c_int64), ("x", C.c_void_p), ("ldx", C.c_int64), ("w", C.c_void_p),
+                ("ldw", C.c_int64), ("dx", C.c_void_p), ("lddx", C.c_int64), ("dw", C.c_void_p), ("lddw", C.c_int64),
+                ("db", C.c_void_p), ("act", C.c_int32), ("dy_dtype", C.c_int32), ("reserved", C.c_int32)]
+
+
+ACTS = {"none": 0, "relu": 1, "silu": 2, "gelu": 3}
+
 # exported symbols and their signatures
 _P = C.c_void_p
 SIGNATURES = {
@@ -160,6 +176,10 @@ SIGNATURES = {
                                              _P, C.POINTER(MoeDroplessTaps), _P, _P, C.c_size_t, _P]),
     "moe_experts_dropless_quant": (C.c_int, [C.POINTER(MoeConfig), _P, _P, C.POINTER(MoeQuantExperts), _P, _P,
                                              C.c_size_t, _P]),
+    "moe_linear_ws_bytes": (C.c_int, [C.POINTER(MoeLinearArgs), C.POINTER(C.c_size_t)]),
+    "moe_linear": (C.c_int, [C.POINTER(MoeLinearArgs), _P, C.c_size_t, _P]),
+    "moe_linear_backward_ws_bytes": (C.c_int, [C.POINTER(MoeLinearGrad), C.POINTER(C.c_size_t)]),
+    "moe_linear_backward": (C.c_int, [C.POINTER(MoeLinearGrad), _P, C.c_size_t, _P]),
 }
 
 STAGES = ["latent", "router", "topk", "assign", "scatter", "recv_bin", "expert_rows",

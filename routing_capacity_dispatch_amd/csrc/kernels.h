@@ -374,4 +374,51 @@ bool few_rows(int64_t M, int E, bool grouped);
 bool few_rows_stage(int K);
 hipError_t launch_few_rows(const FewRows& g, bool hidden, bool staged, hipStream_t s);
 
+// ---------------------------------------------------------- linear layers
+// y = act(x W^T + b) + r and its gradients (linear.hip).
+enum Act : int { ACT_NONE = 0, ACT_RELU = 1, ACT_SILU = 2, ACT_GELU = 3 };
+struct Linear {
+  const void* x;      // [M][ldx] bf16 (K-major: [K][ldx])
+  int64_t ldx;
+  const void* w;      // [N][ldw] bf16 (K-major: [K][ldw])
+  int64_t ldw;
+  int64_t M;
+  int N, K;
+  const void* bias;   // [N] bias_dt, or null
+  int bias_dt;
+  const void* res;    // [M][ldr] out_dt, or null
+  int64_t ldr;
+  void* y;            // [M][ldy] out_dt
+  int64_t ldy;
+  int out_dt;
+  void* pre;          // [M][ldp] bf16, or null
+  int64_t ldp;
+  int act;
+  int vec;            // rows of y, res and pre start on 16 bytes
+  float* part;        // sums of the shares of K
+  // set by the launcher
+  int64_t ldpart;
+  int tiles_m, tiles_n, shares, share_k;
+};
+struct LinearPlan {
+  bool big;
+  int shares, share_k;
+  int64_t part_bytes;
+};
+LinearPlan linear_plan(int64_t M, int64_t N, int64_t K);
+// x and w row-major (with zeros from K to a multiple of 8) or K-major (x only
+// with w), rows on 16 bytes; g.part of linear_plan(...).part_bytes.
+hipError_t launch_linear_tiles(const Linear& g, bool a_kmajor, bool b_kmajor, hipStream_t s);
+// At most 64 rows, both operands row-major, any alignment and K.
+bool linear_skinny(int64_t M);
+hipError_t launch_linear_skinny(const Linear& g, hipStream_t s);
+// bf16 rows into rows of ldd (a multiple of 8) with zeros past cols.
+hipError_t launch_pack_rows(const void* src, int64_t rows, int cols, int64_t ld, void* dst, int64_t ldd,
+                            hipStream_t s);
+// d = dy act'(pre), bf16 rows of ldd with zeros past N (d null: not written);
+// db [N] its sums over rows (null: none) by way of part [slope_blocks(M)][N].
+int64_t slope_blocks(int64_t M);
+hipError_t launch_slope(const void* dy, int64_t ldy, int dy_dt, const void* pre, int64_t ldp, int act, int64_t M,
+                        int N, void* d, int64_t ldd, float* part, float* db, hipStream_t s);
+
 }  // namespace moe

@@ -2000,3 +2000,250 @@ MOE_API moe_status moe_forward_dropless_quant(const moe_config* cfg, const moe_s
   }
   return hip_status(moe::launch_quant_gemm(dense_quant(q.cat, q.cat_s, T, w->q_output, w->s_output, D, W, y), q.gemm, s));
 }
+
+// ------------------------------------------------------------------ linear layers
+namespace {
+
+constexpr int64_t kMaxLd = int64_t(1) << 22;  // 256 rows of 2 bytes stay below 2^31
+constexpr int64_t kMaxLinearRows = int64_t(1) << 30;
+constexpr int64_t kMaxSlopeRows = 65535 * 64;  // one grid row for 64 rows of d
+
+int64_t align8(int64_t x) { return (x + 7) & ~int64_t(7); }
+
+// rows can be read by the tiles as they are
+bool tile_rows(const void* p, int64_t ld) { return aligned16(p) && ld % 8 == 0; }
+
+moe_status check_linear_sizes(int64_t M, int64_t N, int64_t K) {
+  if (M < 0 || N < 0 || K < 0) return MOE_ERR_INVALID_ARG;
+  if (M > kMaxLinearRows || N > kMaxLd || K > kMaxLd) return MOE_ERR_UNSUPPORTED;
+  const int64_t n = N > K ? N : K;
+  if (ceil_div(M, 128) * ceil_div(n, 128) > kMaxListEntries || ceil_div(N, 128) * ceil_div(K, 128) > kMaxListEntries)
+    return MOE_ERR_UNSUPPORTED;
+  return MOE_OK;
+}
+
+moe_status check_ld(int64_t ld, int64_t least) {
+  if (ld < least) return MOE_ERR_INVALID_ARG;
+  return ld > kMaxLd ? MOE_ERR_UNSUPPORTED : MOE_OK;
+}
+
+bool valid_dtype(int32_t d) { return d == MOE_F32 || d == MOE_BF16; }
+bool valid_act(int32_t a) { return a >= MOE_ACT_NONE && a <= MOE_ACT_GELU; }
+bool on_elem(const void* p, int32_t dtype) { return aligned_to(p, dtype == MOE_F32 ? 4 : 2); }
+
+moe_status check_linear(const moe_linear_args* a) {
+  if (!a) return MOE_ERR_INVALID_ARG;
+  if (!valid_dtype(a->bias_dtype) || !valid_dtype(a->out_dtype) || !valid_act(a->act) || a->reserved != 0)
+    return MOE_ERR_INVALID_ARG;
+  moe_status st = check_linear_sizes(a->M, a->N, a->K);
+  if (st == MOE_OK) st = check_ld(a->ldx, a->K);
+  if (st == MOE_OK) st = check_ld(a->ldw, a->K);
+  if (st == MOE_OK) st = check_ld(a->ldy, a->N);
+  if (st == MOE_OK && a->residual) st = check_ld(a->ldr, a->N);
+  if (st == MOE_OK && a->pre) st = check_ld(a->ldp, a->N);
+  if (st != MOE_OK) return st;
+  if (!aligned_to(a->x, 2) || !aligned_to(a->w, 2) || !on_elem(a->bias, a->bias_dtype) ||
+      !on_elem(a->residual, a->out_dtype) || !on_elem(a->y, a->out_dtype) || !aligned_to(a->pre, 2))
+    return MOE_ERR_INVALID_ARG;
+  return MOE_OK;
+}
+
+struct LinearWs {
+  void* x;  // copies in whole 16 bytes, or null
+  void* w;
+  void* part;
+};
+int64_t carve_linear(const moe_linear_args* a, void* ws, LinearWs* w) {
+  Carver cv{static_cast<char*>(ws), 0};
+  *w = LinearWs{};
+  if (moe::linear_skinny(a->M) || a->N == 0 || a->K == 0) return 0;
+  const int64_t K8 = align8(a->K);
+  if (!tile_rows(a->x, a->ldx) || a->K % 8) w->x = cv.take(a->M * K8 * 2);
+  if (!tile_rows(a->w, a->ldw) || a->K % 8) w->w = cv.take(a->N * K8 * 2);
+  const int64_t part = moe::linear_plan(a->M, a->N, K8).part_bytes;
+  if (part) w->part = cv.take(part);
+  return cv.used;
+}
+
+}  // namespace
+
+MOE_API moe_status moe_linear_ws_bytes(const moe_linear_args* args, size_t* bytes) {
+  const moe_status st = check_linear(args);
+  if (st != MOE_OK) return st;
+  if (!bytes) return MOE_ERR_INVALID_ARG;
+  LinearWs w;
+  *bytes = (size_t)carve_linear(args, nullptr, &w);
+  return MOE_OK;
+}
+
+MOE_API moe_status moe_linear(const moe_linear_args* args, void* ws, size_t ws_bytes, void* stream) {
+  const moe_status st = check_linear(args);
+  if (st != MOE_OK) return st;
+  const moe_linear_args& a = *args;
+  if (a.M == 0 || a.N == 0) return MOE_OK;
+  if (!a.y || (a.K > 0 && (!a.x || !a.w))) return MOE_ERR_INVALID_ARG;
+  LinearWs w;
+  const int64_t need = carve_linear(args, nullptr, &w);
+  if (need > 0 && (!ws || !aligned256(ws) || (int64_t)ws_bytes < need)) return MOE_ERR_WORKSPACE;
+  carve_linear(args, need > 0 ? ws : nullptr, &w);
+  hipStream_t s = static_cast<hipStream_t>(stream);
+  moe::Linear g{};
+  g.x = a.x;
+  g.ldx = a.ldx;
+  g.w = a.w;
+  g.ldw = a.ldw;
+  g.M = a.M;
+  g.N = (int)a.N;
+  g.K = (int)a.K;
+  g.bias = a.bias;
+  g.bias_dt = a.bias_dtype;
+  g.res = a.residual;
+  g.ldr = a.ldr;
+  g.y = a.y;
+  g.ldy = a.ldy;
+  g.out_dt = a.out_dtype;
+  g.pre = a.pre;
+  g.ldp = a.ldp;
+  g.act = a.act;
+  const int64_t per16 = a.out_dtype == MOE_F32 ? 4 : 8;
+  g.vec = aligned16(a.y) && a.ldy % per16 == 0 && (!a.residual || (aligned16(a.residual) && a.ldr % per16 == 0)) &&
+          (!a.pre || (aligned16(a.pre) && a.ldp % 8 == 0));
+  if (moe::linear_skinny(a.M)) return hip_status(moe::launch_linear_skinny(g, s));
+  const int64_t K8 = align8(a.K);
+  hipError_t e = hipSuccess;
+  if (w.x) {
+    e = moe::launch_pack_rows(a.x, a.M, g.K, a.ldx, w.x, K8, s);
+    g.x = w.x;
+    g.ldx = K8;
+  }
+  if (e == hipSuccess && w.w) {
+    e = moe::launch_pack_rows(a.w, a.N, g.K, a.ldw, w.w, K8, s);
+    g.w = w.w;
+    g.ldw = K8;
+  }
+  g.K = (int)K8;
+  g.part = static_cast<float*>(w.part);
+  if (e == hipSuccess) e = moe::launch_linear_tiles(g, false, false, s);
+  return hip_status(e);
+}
+
+namespace {
+
+moe_status check_linear_grad(const moe_linear_grad* a) {
+  if (!a) return MOE_ERR_INVALID_ARG;
+  if (!valid_dtype(a->dy_dtype) || !valid_act(a->act) || a->reserved != 0) return MOE_ERR_INVALID_ARG;
+  moe_status st = check_linear_sizes(a->M, a->N, a->K);
+  if (st == MOE_OK && a->M > kMaxSlopeRows) st = MOE_ERR_UNSUPPORTED;
+  if (st == MOE_OK) st = check_ld(a->lddy, a->N);
+  if (st == MOE_OK && a->act != MOE_ACT_NONE) st = check_ld(a->ldp, a->N);
+  if (st == MOE_OK && a->dw) st = check_ld(a->ldx, a->K);
+  if (st == MOE_OK && a->dx) st = check_ld(a->ldw, a->K);
+  if (st == MOE_OK && a->dx) st = check_ld(a->lddx, a->K);
+  if (st == MOE_OK && a->dw) st = check_ld(a->lddw, a->K);
+  if (st != MOE_OK) return st;
+  if (!on_elem(a->dy, a->dy_dtype) || !aligned_to(a->pre, 2) || !aligned_to(a->x, 2) || !aligned_to(a->w, 2) ||
+      !aligned_to(a->dx, 2) || !aligned_to(a->dw, 2) || !aligned_to(a->db, 4))
+    return MOE_ERR_INVALID_ARG;
+  return MOE_OK;
+}
+
+struct LinearGradWs {
+  void* d;      // bf16 [M][N rounded up to 8], or null: dy itself
+  float* sums;  // partial sums of db
+  void* x;      // copies in whole 16 bytes, or null
+  void* w;
+  void* part;
+};
+int64_t carve_linear_grad(const moe_linear_grad* a, void* ws, LinearGradWs* w) {
+  Carver cv{static_cast<char*>(ws), 0};
+  *w = LinearGradWs{};
+  const int64_t N8 = align8(a->N), K8 = align8(a->K);
+  const bool products = (a->dx || a->dw) && a->M > 0 && a->N > 0 && a->K > 0;
+  // dy as it is serves as d where no slope and no rounding is due
+  const bool own = a->act == MOE_ACT_NONE && a->dy_dtype == MOE_BF16 && tile_rows(a->dy, a->lddy) &&
+                   (!a->dx || a->N % 8 == 0);
+  if (products && !own) w->d = cv.take(a->M * N8 * 2);
+  if (a->db && a->M > 0) w->sums = static_cast<float*>(cv.take(moe::slope_blocks(a->M) * a->N * 4));
+  if (products && a->dw && !tile_rows(a->x, a->ldx)) w->x = cv.take(a->M * K8 * 2);
+  if (products && a->dx && !tile_rows(a->w, a->ldw)) w->w = cv.take(a->N * K8 * 2);
+  int64_t part = 0;
+  if (a->dx) part = moe::linear_plan(a->M, a->K, N8).part_bytes;
+  if (a->dw) {
+    const int64_t q = moe::linear_plan(a->N, a->K, a->M).part_bytes;
+    part = q > part ? q : part;
+  }
+  if (products && part) w->part = cv.take(part);
+  return cv.used;
+}
+
+}  // namespace
+
+MOE_API moe_status moe_linear_backward_ws_bytes(const moe_linear_grad* args, size_t* bytes) {
+  const moe_status st = check_linear_grad(args);
+  if (st != MOE_OK) return st;
+  if (!bytes) return MOE_ERR_INVALID_ARG;
+  LinearGradWs w;
+  *bytes = (size_t)carve_linear_grad(args, nullptr, &w);
+  return MOE_OK;
+}
+
+MOE_API moe_status moe_linear_backward(const moe_linear_grad* args, void* ws, size_t ws_bytes, void* stream) {
+  const moe_status st = check_linear_grad(args);
+  if (st != MOE_OK) return st;
+  const moe_linear_grad& a = *args;
+  if (a.M > 0 && a.N > 0) {
+    if ((a.dx || a.dw || a.db) && (!a.dy || (a.act != MOE_ACT_NONE && !a.pre))) return MOE_ERR_INVALID_ARG;
+    if (a.K > 0 && ((a.dx && !a.w) || (a.dw && !a.x))) return MOE_ERR_INVALID_ARG;
+  }
+  LinearGradWs w;
+  const int64_t need = carve_linear_grad(args, nullptr, &w);
+  if (need > 0 && (!ws || !aligned256(ws) || (int64_t)ws_bytes < need)) return MOE_ERR_WORKSPACE;
+  carve_linear_grad(args, need > 0 ? ws : nullptr, &w);
+  hipStream_t s = static_cast<hipStream_t>(stream);
+  const int64_t N8 = align8(a.N), K8 = align8(a.K);
+  hipError_t e = hipSuccess;
+  if (w.d || a.db)
+    e = moe::launch_slope(a.dy, a.lddy, a.dy_dtype, a.pre, a.ldp, a.act, a.M, (int)a.N, w.d, N8, w.sums, a.db, s);
+  const void* d = w.d ? w.d : a.dy;
+  const int64_t ldd = w.d ? N8 : a.lddy;
+  moe::Linear g{};
+  g.part = static_cast<float*>(w.part);
+  g.out_dt = moe::DT_BF16;
+  if (e == hipSuccess && a.dx && a.M > 0 && a.K > 0) {  // d [M][N] by W, K-major along N
+    g.x = d;
+    g.ldx = ldd;
+    g.w = a.w;
+    g.ldw = a.ldw;
+    if (w.w) {
+      e = moe::launch_pack_rows(a.w, a.N, (int)a.K, a.ldw, w.w, K8, s);
+      g.w = w.w;
+      g.ldw = K8;
+    }
+    g.M = a.M;
+    g.N = (int)a.K;
+    g.K = (int)a.N;
+    g.y = a.dx;
+    g.ldy = a.lddx;
+    g.vec = aligned16(a.dx) && a.lddx % 8 == 0;
+    if (e == hipSuccess) e = moe::launch_linear_tiles(g, false, true, s);
+  }
+  if (e == hipSuccess && a.dw && a.N > 0 && a.K > 0) {  // d and x, both K-major along M
+    g.x = d;
+    g.ldx = ldd;
+    g.w = a.x;
+    g.ldw = a.ldx;
+    if (w.x) {
+      e = moe::launch_pack_rows(a.x, a.M, (int)a.K, a.ldx, w.x, K8, s);
+      g.w = w.x;
+      g.ldw = K8;
+    }
+    g.M = a.N;
+    g.N = (int)a.K;
+    g.K = (int)a.M;
+    g.y = a.dw;
+    g.ldy = a.lddw;
+    g.vec = aligned16(a.dw) && a.lddw % 8 == 0;
+    if (e == hipSuccess) e = moe::launch_linear_tiles(g, true, true, s);
+  }
+  return hip_status(e);
+}
