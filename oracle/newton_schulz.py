@@ -1,0 +1,57 @@
+"""Newton-Schulz iteration that moves a matrix's singular values near 1
+(moe_orthogonalize), in fp64: from its definition, and once more with the
+roundings that the GPU's arithmetic makes."""
+import numpy as np
+
+USUAL = (3.4445, -4.7750, 2.0315)
+
+
+def start(g, eps):
+    x = np.asarray(g, dtype=np.float64)
+    x = x.T if x.shape[0] > x.shape[1] else x
+    n = np.sqrt((x * x).sum()) + eps
+    return x / n if n > 0 else np.zeros_like(x)
+
+
+def exact(g, steps=5, coeffs=USUAL, eps=1e-7, scale=1.0):
+    x = start(g, eps)
+    for a, b, c in (coeffs if isinstance(coeffs[0], tuple) else [coeffs] * steps):
+        p = x @ x.T
+        x = a * x + (b * p + c * (p @ p)) @ x
+    return scale * (x.T if np.shape(g)[0] > np.shape(g)[1] else x)
+
+
+def by_singular_values(g, steps=5, coeffs=USUAL, eps=1e-7, scale=1.0):
+    """The same through the singular value decomposition."""
+    x = np.asarray(g, dtype=np.float64)
+    u, s, v = np.linalg.svd(x, full_matrices=False)
+    s = s / (np.sqrt((x * x).sum()) + eps)
+    for a, b, c in (coeffs if isinstance(coeffs[0], tuple) else [coeffs] * steps):
+        s = a * s + b * s ** 3 + c * s ** 5
+    return scale * (u * s) @ v
+
+
+def fp16(x):
+    """x in fp16, scaled by the power of two that takes its largest value to half of fp16's range."""
+    most = np.abs(x).max()
+    e = int(np.floor(np.log2(32768.0 / most))) if most > 0 else 0
+    return np.ldexp(np.ldexp(x, e).astype(np.float16).astype(np.float64), -e)
+
+
+def emulated(g, steps=5, coeffs=USUAL, eps=1e-7, scale=1.0):
+    """X in fp32; the products take X, and A and B off their diagonals, in
+    fp16, X in two fp16 numbers where
+    its smaller side is below 256; sums exact."""
+    x = start(g, eps).astype(np.float32).astype(np.float64)
+    for a, b, c in (coeffs if isinstance(coeffs[0], tuple) else [coeffs] * steps):
+        h = fp16(x)
+        low = fp16(x - h) if min(x.shape) < 256 else np.zeros_like(x)
+        p = h @ h.T + h @ low.T + low @ h.T
+        d = np.diag(p).copy()
+        r = fp16(p - np.diag(d))
+        p2 = r @ r + (d[:, None] + d[None]) * r + np.diag(d * d)
+        q = b * (r + np.diag(d)) + c * p2
+        e = np.diag(q).copy()
+        x = (a + e[:, None]) * x + fp16(q - np.diag(e)) @ (h + low)
+        x = x.astype(np.float32).astype(np.float64)
+    return scale * (x.T if np.shape(g)[0] > np.shape(g)[1] else x)

@@ -10,6 +10,7 @@ BackwardRouted (moe_backward_routed), plus make_config / plan.
 from __future__ import annotations
 
 import ctypes as C
+import functools
 from typing import Dict, Optional
 
 import torch
@@ -22,7 +23,7 @@ __all__ = ["make_config", "plan", "route", "dispatch", "experts", "combine", "fo
            "combine_backward_dropless", "experts_backward_dropless", "dispatch_backward_dropless",
            "BackwardRouted", "scoring", "route_scored", "route_scored_backward", "quantize", "gemm_quant",
            "experts_dropless_quant", "quantize_weights", "ForwardDroplessQuant", "linear", "linear_backward",
-           "library", "MoeError"]
+           "orthogonalize", "library", "MoeError"]
 
 MoeError = abi.MoeError
 _DT = {"f32": abi.MOE_F32, "bf16": abi.MOE_BF16, torch.float32: abi.MOE_F32,
@@ -884,3 +885,47 @@ def linear_backward(dy, x, w, pre=None, act: str = "none", bias: bool = True, ne
                           abi.ACTS[act], _DT[dy.dtype], 0)
     _with_workspace("moe_linear_backward", dev, a, ws)
     return dx, dw, db
+
+
+# --------------------------------------------------- orthogonalised updates
+@functools.lru_cache(maxsize=64)
+def _coefficients(coeffs, steps):
+    """[steps][3] fp32 on the host of one (a, b, c), or of one for each step."""
+    rows = [coeffs] * steps if not isinstance(coeffs[0], tuple) else list(coeffs)
+    _check(len(rows) == steps and all(len(r) == 3 for r in rows), "coeffs is (a, b, c), or one of them for each step")
+    return (C.c_float * (3 * steps))(*[float(v) for r in rows for v in r])
+
+
+def _batch(t, what):
+    """(leading dimension, stride between matrices) of a [B, M, N] tensor with contiguous columns."""
+    B, M, N = t.shape
+    ld = t.stride(1) if M > 1 else max(N, 1)
+    stride = t.stride(0) if B > 1 else M * ld
+    _check((N <= 1 or t.stride(2) == 1) and ld >= N and (B <= 1 or M == 0 or stride >= (M - 1) * ld + N),
+           f"{what} must have contiguous columns and matrices that do not overlap")
+    return ld, stride
+
+
+def orthogonalize(g, steps: int = 5, coeffs=(3.4445, -4.7750, 2.0315), eps: float = 1e-7, scale: float = 1.0, out=None,
+                  ws=None):
+    """scale times the Newton-Schulz iterate of g [M, N] or [B, M, N] (bf16 or
+    fp32; rows and matrices may be strided) in bf16 (moe_orthogonalize): the
+    update of a weight whose singular values lie near 1.  coeffs: (a, b, c)
+    for every step, or a sequence of them, one for each."""
+    _check(isinstance(g, torch.Tensor) and g.dim() in (2, 3) and g.is_cuda and g.dtype in _FLOATS,
+           "g must be a two- or three-dimensional bf16 or fp32 tensor on a GPU")
+    dev = g.device
+    if out is None:
+        out = torch.empty(g.shape, dtype=torch.bfloat16, device=dev)
+    else:
+        _check(isinstance(out, torch.Tensor) and out.shape == g.shape and out.dtype == torch.bfloat16
+               and out.device == dev, f"out must be a bf16 tensor of g's shape on {dev}")
+    g3, o3 = (g, out) if g.dim() == 3 else (g[None], out[None])
+    B, M, N = g3.shape
+    ldg, sg = _batch(g3, "g")
+    ldo, so = _batch(o3, "out")
+    _check(1 <= steps <= 64, "steps is 1 to 64")
+    co = _coefficients(tuple(tuple(c) if isinstance(c, (list, tuple)) else c for c in coeffs), steps)
+    a = abi.MoeOrthoArgs(B, M, N, g.data_ptr(), ldg, sg, out.data_ptr(), ldo, so, co, steps, _DT[g.dtype], eps, scale, 0)
+    _with_workspace("moe_orthogonalize", dev, a, ws)
+    return out

@@ -101,6 +101,13 @@ class MoeLinearGrad(C.Structure):
                 ("db", C.c_void_p), ("act", C.c_int32), ("dy_dtype", C.c_int32), ("reserved", C.c_int32)]
 
 
+class MoeOrthoArgs(C.Structure):
+    _fields_ = [("batch", C.c_int64), ("M", C.c_int64), ("N", C.c_int64), ("g", C.c_void_p), ("ldg", C.c_int64),
+                ("stride_g", C.c_int64), ("out", C.c_void_p), ("ldo", C.c_int64), ("stride_o", C.c_int64),
+                ("coeffs", C.POINTER(C.c_float)), ("steps", C.c_int32), ("dtype", C.c_int32), ("eps", C.c_float),
+                ("scale", C.c_float), ("reserved", C.c_int32)]
+
+
 ACTS = {"none": 0, "relu": 1, "silu": 2, "gelu": 3}
 
 # exported symbols and their signatures
@@ -180,6 +187,8 @@ SIGNATURES = {
     "moe_linear": (C.c_int, [C.POINTER(MoeLinearArgs), _P, C.c_size_t, _P]),
     "moe_linear_backward_ws_bytes": (C.c_int, [C.POINTER(MoeLinearGrad), C.POINTER(C.c_size_t)]),
     "moe_linear_backward": (C.c_int, [C.POINTER(MoeLinearGrad), _P, C.c_size_t, _P]),
+    "moe_orthogonalize_ws_bytes": (C.c_int, [C.POINTER(MoeOrthoArgs), C.POINTER(C.c_size_t)]),
+    "moe_orthogonalize": (C.c_int, [C.POINTER(MoeOrthoArgs), _P, C.c_size_t, _P]),
 }
 
 STAGES = ["latent", "router", "topk", "assign", "scatter", "recv_bin", "expert_rows",

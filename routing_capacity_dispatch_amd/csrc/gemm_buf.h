@@ -45,15 +45,15 @@ struct Rows {
   uint32_t col;       // row-major: first k of this lane's chunk in a K tile
 
   // ptr: the operand; r0: the tile's first row; rows: rows of the operand; ld in elements
-  __device__ __forceinline__ void init(const void* ptr, int64_t r0, int64_t rows, int64_t ld, int K_, int wave,
-                                       int lane) {
+  __device__ __forceinline__ void init(const void* ptr, int r0, int rows, int64_t ld, int K_, int wave, int lane) {
     K = K_;
     if constexpr (kMajor) {
-      base = reinterpret_cast<uint64_t>(ptr) + r0 * 2;
+      base = reinterpret_cast<uint64_t>(ptr) + (int64_t)r0 * 2;
       // up to the end of the 16 bytes that hold the last value (a load is all
       // or nothing per 4 bytes; the columns that follow it are never stored)
-      extent = K > 0 ? (((K - 1) * ld + (rows - r0)) * 2 + 15) & ~int64_t(15) : 0;
+      extent = K > 0 ? (((int64_t)(K - 1) * ld + (rows - r0)) * 2 + 15) & ~int64_t(15) : 0;
       kstep = 64 * ld * 2;
+      in_scalar();
       col = 0;
 #pragma unroll
       for (int i = 0; i < INS; ++i) {
@@ -63,10 +63,11 @@ struct Rows {
         off[i] = r0 + c / 2 < rows ? (uint32_t)(k * ld * 2) + c : kOut;
       }
     } else {
-      base = reinterpret_cast<uint64_t>(ptr) + r0 * ld * 2;
-      const int64_t n = rows - r0 < X ? rows - r0 : X;
-      extent = (((n - 1) * ld + K) * 2 + 15) & ~int64_t(15);
+      base = reinterpret_cast<uint64_t>(ptr) + (int64_t)r0 * ld * 2;
+      const int n = min(rows - r0, X);
+      extent = (((int64_t)(n - 1) * ld + K) * 2 + 15) & ~int64_t(15);
       kstep = TL::RB;
+      in_scalar();
       const int c = core::load_col<TL>(lane);
       col = c / 2;
 #pragma unroll
@@ -76,6 +77,11 @@ struct Rows {
       }
     }
   }
+  // base and extent in scalar registers, so that every descriptor is made there
+  __device__ __forceinline__ void in_scalar() {
+    base = reinterpret_cast<uint64_t>(core::uniform_ptr(reinterpret_cast<const char*>(base)));
+    extent = (int64_t)reinterpret_cast<uint64_t>(core::uniform_ptr(reinterpret_cast<const char*>(extent)));
+  }
   static constexpr uint32_t kOut = 0x80000000u;  // outside every descriptor
   // Descriptor of K tile j, and whether this lane's chunk lies inside K.
   struct TileAt {
@@ -84,11 +90,13 @@ struct Rows {
   };
   __device__ __forceinline__ TileAt tile(int j) const {
     const uint64_t b = base + (int64_t)j * kstep;
-    int64_t left = extent - (int64_t)j * kstep;
-    left = left < 0 ? 0 : left > 0x7FFFFFFF ? 0x7FFFFFFF : left;
+    // made of kernel arguments and block indices in scalar arithmetic (which
+    // has no 64-bit comparison: the bytes left are clamped by their halves)
+    const int64_t left = extent - (int64_t)j * kstep;
+    const int hi = (int)(left >> 32), lo = (int)left;
+    const int bytes = hi < 0 ? 0 : (hi > 0 || lo < 0) ? 0x7FFFFFFF : lo;
     TileAt t;
-    // kernel arguments and block indices only: scalar arithmetic
-    t.rsrc = i32x4_t{(int)(uint32_t)b, (int)((uint32_t)(b >> 32) & 0xFFFFu), (int)(uint32_t)left, 0x00020000};
+    t.rsrc = i32x4_t{(int)(uint32_t)b, (int)((uint32_t)(b >> 32) & 0xFFFFu), bytes, 0x00020000};
     t.in = kMajor || col + j * 64 < (uint32_t)K;
     return t;
   }

@@ -421,4 +421,42 @@ int64_t slope_blocks(int64_t M);
 hipError_t launch_slope(const void* dy, int64_t ldy, int dy_dt, const void* pre, int64_t ldp, int act, int64_t M,
                         int N, void* d, int64_t ldd, float* part, float* db, hipStream_t s);
 
+// ------------------------------------------------- orthogonalised updates
+// Newton-Schulz iteration (orthogonalize.hip).  X is m x n, m <= n, with rows
+// of np = n rounded up to 64 (zeros between); A and B have rows of mp.
+struct Ortho {
+  const void* g;        // [batch][M][ldg]
+  int64_t ldg, stride_g;
+  int dt;
+  int M, N;
+  uint16_t* out;        // bf16 [batch][M][ldo]
+  int64_t ldo, stride_o;
+  int vec_out;          // groups of 4 (tall) or 8 values of a row of out start on 8 or 16 bytes
+  float eps, scale;
+  bool tall;            // M > N: X is G^T
+  int m, n, mp, np;
+  double* norm;         // [group][ortho_norm_chunks()]
+  float* x32;           // [group][m][np]
+  uint16_t* x16[2];     // fp16 X times sx: this step's and the next one's
+  uint16_t* lo16[2];    // ortho_split(m): what that rounding leaves, in fp16
+  uint16_t* a16;        // [group][m][mp] fp16, zero diagonals
+  uint16_t* b16;
+  float* da;            // [group][m]: their diagonals
+  float* db;
+  // set by the launcher
+  int64_t b0;
+  bool split;
+  int count, cur, gram_tiles, tiles_m, tiles_n;
+  float ca, cb, cc, sx, inv_sx, sa, inv_sa, sb, inv_sb, sx_next;
+};
+struct OrthoStep {
+  float a, b, c;        // coefficients
+  float sx, sa, sb;     // powers of two that X, A and B are held in fp16 with
+};
+int ortho_norm_chunks();
+bool ortho_split(int64_t m);
+int64_t ortho_group(int64_t batch, int64_t m, int64_t n);
+hipError_t launch_orthogonalize(const Ortho& p, const OrthoStep* step, int steps, int64_t batch, int64_t group,
+                                hipStream_t s);
+
 }  // namespace moe

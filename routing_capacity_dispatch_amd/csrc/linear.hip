@@ -150,22 +150,21 @@ __global__ __launch_bounds__(TL::THREADS) void linear_tile_kernel(Linear g) {
   if (share >= g.shares) return;
   int mt, nt;
   dense_tile(t - share * tiles, g.tiles_m, g.tiles_n, mt, nt);
-  const int64_t m0 = (int64_t)mt * TL::BM;
-  const int n0 = nt * TL::BN;
+  const int m0 = mt * TL::BM, n0 = nt * TL::BN;
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
   const int k0 = share * g.share_k, kn = min(g.share_k, g.K - k0);
   buf::ARows<TL, AK> a;
   buf::BRows<TL, BK> b;
-  a.init(static_cast<const uint16_t*>(g.x) + (AK ? k0 * g.ldx : k0), m0, g.M, g.ldx, kn, wave, lane);
+  a.init(static_cast<const uint16_t*>(g.x) + (AK ? k0 * g.ldx : k0), m0, (int)g.M, g.ldx, kn, wave, lane);
   b.init(static_cast<const uint16_t*>(g.w) + (BK ? k0 * g.ldw : k0), n0, g.N, g.ldw, kn, wave, lane);
   Acc<TL> acc;
   acc.zero();
   buf::mainloop<TL, AK, BK, false>(a, b, (kn + 63) / 64, lds, acc);
-  const int rows = (int)(g.M - m0 < TL::BM ? g.M - m0 : TL::BM);
+  const int rows = min((int)g.M - m0, TL::BM);
   if (g.shares > 1) {
     float* part = g.part + (int64_t)share * g.M * g.ldpart;
     buf::Epilogue<TL>::run(acc, lds, rows, [&](int r, int c, float* v) {
-      if (n0 + c < g.N) st_vec<8>(part, (m0 + r) * g.ldpart + n0 + c, DT_F32, v);
+      if (n0 + c < g.N) st_vec<8>(part, (int64_t)(m0 + r) * g.ldpart + n0 + c, DT_F32, v);
     });
   } else {
     buf::Epilogue<TL>::run(acc, lds, rows, [&](int r, int c, float* v) { finish<8>(g, m0 + r, n0 + c, v); });
@@ -234,8 +233,7 @@ __global__ __launch_bounds__(64 * kSkinnyWaves) void linear_skinny_kernel(Linear
                                                    0, 0, 0);
   };
   const int whole = g.K & ~127;
-  constexpr int kUnroll = MB > 2 ? 1 : 2;
-#pragma unroll kUnroll
+#pragma unroll 2
   for (int k = wave * 128; k < whole; k += kSkinnyWaves * 128) {
     uint4 a[4], v[MB][4];
 #pragma unroll

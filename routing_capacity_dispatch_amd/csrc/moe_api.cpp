@@ -3,6 +3,7 @@
 #include "moe.h"
 
 #include <hip/hip_runtime.h>
+#include <math.h>
 #include <stdint.h>
 
 #include <mutex>
@@ -2246,4 +2247,152 @@ MOE_API moe_status moe_linear_backward(const moe_linear_grad* args, void* ws, si
     if (e == hipSuccess) e = moe::launch_linear_tiles(g, true, true, s);
   }
   return hip_status(e);
+}
+
+// ------------------------------------------------------------------ orthogonalised updates
+namespace {
+
+constexpr int kMaxOrthoSteps = 64;
+constexpr int64_t kMaxOrthoSide = 65536;
+constexpr int64_t kMaxOrthoLd = int64_t(1) << 30;
+constexpr double kMaxSingular = 1048576.0;
+
+// The largest power of two that takes magnitudes up to `most` to at most half
+// of fp16's range.
+float fp16_scale(double most) {
+  if (!(most > 0.0)) return 1.0f;
+  int e = 0;
+  frexp(32768.0 / most, &e);  // 32768 / most in [2^(e-1), 2^e)
+  e -= 1;
+  return ldexpf(1.0f, e > 60 ? 60 : e);
+}
+
+// Bounds of every step's singular values, from those of X_0 (at most 1, its
+// Frobenius norm), and the scales that follow.  One part in 64 is left to the
+// roundings of a step.
+moe_status ortho_steps(const moe_ortho_args* a, moe::OrthoStep* out) {
+  double m = 1.0;
+  for (int k = 0; k < a->steps; ++k) {
+    const double ca = a->coeffs[3 * k], cb = a->coeffs[3 * k + 1], cc = a->coeffs[3 * k + 2];
+    if (!isfinite(ca) || !isfinite(cb) || !isfinite(cc)) return MOE_ERR_INVALID_ARG;
+    const double y = m * m;
+    // |b y + c y^2| on [0, m^2], and |a s + b s^3 + c s^5| on [0, m]
+    double q = fabs(cb * y + cc * y * y);
+    if (cc != 0.0) {
+      const double t = -cb / (2.0 * cc);
+      if (t > 0.0 && t < y && fabs(cb * t + cc * t * t) > q) q = fabs(cb * t + cc * t * t);
+    }
+    auto poly = [&](double s) { return fabs(s * (ca + s * s * (cb + cc * s * s))); };
+    double p = poly(m);
+    // 5 c t^2 + 3 b t + a = 0 for t = s^2
+    double root[2];
+    int n = 0;
+    if (cc != 0.0) {
+      const double d = 9.0 * cb * cb - 20.0 * ca * cc;
+      if (d >= 0.0) {
+        const double u = -0.5 * (3.0 * cb + (cb < 0.0 ? -sqrt(d) : sqrt(d)));
+        root[n++] = u / (5.0 * cc);
+        if (u != 0.0) root[n++] = ca / u;
+      }
+    } else if (cb != 0.0) {
+      root[n++] = -ca / (3.0 * cb);
+    }
+    for (int i = 0; i < n; ++i)
+      if (root[i] > 0.0 && root[i] < y && poly(sqrt(root[i])) > p) p = poly(sqrt(root[i]));
+    const double slack = 1.0 + 1.0 / 64;
+    out[k].a = (float)ca;
+    out[k].b = (float)cb;
+    out[k].c = (float)cc;
+    out[k].sx = fp16_scale(m * slack);
+    out[k].sa = fp16_scale(y * slack);
+    out[k].sb = fp16_scale(q * slack);
+    m = p * slack;
+    if (!(m < kMaxSingular) || !(q < kMaxSingular * kMaxSingular)) return MOE_ERR_UNSUPPORTED;
+  }
+  return MOE_OK;
+}
+
+moe_status check_ortho(const moe_ortho_args* a, moe::OrthoStep* steps) {
+  if (!a) return MOE_ERR_INVALID_ARG;
+  if (a->batch < 0 || a->M < 0 || a->N < 0 || a->reserved != 0 || !valid_dtype(a->dtype) || !a->coeffs ||
+      a->steps < 1 || a->steps > kMaxOrthoSteps || !(a->eps >= 0.0f) || !isfinite(a->eps) || !isfinite(a->scale))
+    return MOE_ERR_INVALID_ARG;
+  if (a->M > kMaxOrthoSide || a->N > kMaxOrthoSide || a->batch > kI32Max) return MOE_ERR_UNSUPPORTED;
+  if (a->ldg < a->N || a->ldo < a->N) return MOE_ERR_INVALID_ARG;
+  if (a->ldg > kMaxOrthoLd || a->ldo > kMaxOrthoLd) return MOE_ERR_UNSUPPORTED;
+  if (a->batch > 1 && a->M > 0 &&
+      (a->stride_g < (a->M - 1) * a->ldg + a->N || a->stride_o < (a->M - 1) * a->ldo + a->N ||
+       a->stride_g > (int64_t(1) << 46) || a->stride_o > (int64_t(1) << 46)))
+    return MOE_ERR_INVALID_ARG;
+  if (!on_elem(a->g, a->dtype) || !aligned_to(a->out, 2)) return MOE_ERR_INVALID_ARG;
+  return ortho_steps(a, steps);
+}
+
+int64_t align64(int64_t x) { return (x + 63) & ~int64_t(63); }
+
+int64_t carve_ortho(const moe_ortho_args* a, void* ws, moe::Ortho* p, int64_t* group) {
+  const int64_t m = a->M < a->N ? a->M : a->N, n = a->M < a->N ? a->N : a->M, mp = align64(m), np = align64(n);
+  *group = moe::ortho_group(a->batch, m, n);
+  const int64_t g = *group;
+  Carver cv{static_cast<char*>(ws), 0};
+  p->norm = static_cast<double*>(cv.take(g * moe::ortho_norm_chunks() * 8));
+  p->x32 = static_cast<float*>(cv.take(g * m * np * 4));
+  p->x16[0] = static_cast<uint16_t*>(cv.take(g * m * np * 2));
+  p->x16[1] = static_cast<uint16_t*>(cv.take(a->steps > 1 ? g * m * np * 2 : 0));
+  const bool split = moe::ortho_split(m);
+  p->lo16[0] = static_cast<uint16_t*>(cv.take(split ? g * m * np * 2 : 0));
+  p->lo16[1] = static_cast<uint16_t*>(cv.take(split && a->steps > 1 ? g * m * np * 2 : 0));
+  p->a16 = static_cast<uint16_t*>(cv.take(g * m * mp * 2));
+  p->b16 = static_cast<uint16_t*>(cv.take(g * m * mp * 2));
+  p->da = static_cast<float*>(cv.take(g * m * 4));
+  p->db = static_cast<float*>(cv.take(g * m * 4));
+  p->m = (int)m;
+  p->n = (int)n;
+  p->mp = (int)mp;
+  p->np = (int)np;
+  return cv.used;
+}
+
+}  // namespace
+
+MOE_API moe_status moe_orthogonalize_ws_bytes(const moe_ortho_args* args, size_t* bytes) {
+  moe::OrthoStep steps[kMaxOrthoSteps];
+  const moe_status st = check_ortho(args, steps);
+  if (st != MOE_OK) return st;
+  if (!bytes) return MOE_ERR_INVALID_ARG;
+  *bytes = 0;
+  if (args->batch == 0 || args->M == 0 || args->N == 0) return MOE_OK;
+  moe::Ortho p{};
+  int64_t group;
+  *bytes = (size_t)carve_ortho(args, nullptr, &p, &group);
+  return MOE_OK;
+}
+
+MOE_API moe_status moe_orthogonalize(const moe_ortho_args* args, void* ws, size_t ws_bytes, void* stream) {
+  moe::OrthoStep steps[kMaxOrthoSteps];
+  const moe_status st = check_ortho(args, steps);
+  if (st != MOE_OK) return st;
+  const moe_ortho_args& a = *args;
+  if (a.batch == 0 || a.M == 0 || a.N == 0) return MOE_OK;
+  if (!a.g || !a.out) return MOE_ERR_INVALID_ARG;
+  moe::Ortho p{};
+  int64_t group;
+  const int64_t need = carve_ortho(args, nullptr, &p, &group);
+  if (!ws || !aligned256(ws) || (int64_t)ws_bytes < need) return MOE_ERR_WORKSPACE;
+  carve_ortho(args, ws, &p, &group);
+  p.g = a.g;
+  p.ldg = a.ldg;
+  p.stride_g = a.stride_g;
+  p.dt = a.dtype;
+  p.M = (int)a.M;
+  p.N = (int)a.N;
+  p.out = static_cast<uint16_t*>(a.out);
+  p.ldo = a.ldo;
+  p.stride_o = a.stride_o;
+  p.eps = a.eps;
+  p.scale = a.scale;
+  p.tall = a.M > a.N;
+  const int64_t per = p.tall ? 4 : 8;
+  p.vec_out = aligned_to(a.out, per * 2) && a.ldo % per == 0 && (a.batch == 1 || a.stride_o % per == 0);
+  return hip_status(moe::launch_orthogonalize(p, steps, a.steps, a.batch, group, static_cast<hipStream_t>(stream)));
 }
