@@ -840,6 +840,29 @@ typedef struct {
 moe_status moe_orthogonalize_ws_bytes(const moe_ortho_args* args, size_t* bytes);
 moe_status moe_orthogonalize(const moe_ortho_args* args, void* ws, size_t ws_bytes, void* stream);
 
+/* ------------------------------------------------------------------------
+ * The dropless branch for a few tokens (a decoding step): moe_forward_dropless
+ * for T <= 16 with every weight it needs read once and few launches.  The same
+ * weights and the same routing rule (moe_route) on bf16 inputs; z, the hidden
+ * rows, the experts' outputs and y_lat are not rounded to bf16 (they keep 16
+ * bits or more, z all of fp32's where the router reads it), so that logits
+ * and y are nearer to the real ones than moe_forward_dropless's, and close
+ * logits may be ranked otherwise than there.
+ *   y = y_lat W_up^T + sum_s SwiGLU_s(x) (+ residual)
+ * bf16 configs with d_model, d_latent, d_ff and d_ff_shared multiples of 64,
+ * top_k <= E; T past 16: MOE_ERR_UNSUPPORTED.  n_pools, n_waves and the caps
+ * are validated as for moe_make_plan but otherwise unused.
+ *   x, y      (device) [T][D] bf16, 16-byte aligned, as every weight
+ *   residual  (device) [T][D] bf16, 16-byte aligned, or NULL; may be y or x
+ *   logits, topk_idx, gates  (device, out) [T][E] fp32, [T][k] int32, [T][k]
+ *             fp32, or NULL
+ *   ws        (device) >= moe_forward_few_ws_bytes(cfg) bytes, 256-byte
+ *             aligned; nothing in it needs clearing.
+ * ------------------------------------------------------------------------ */
+moe_status moe_forward_few_ws_bytes(const moe_config* cfg, size_t* bytes);
+moe_status moe_forward_few(const moe_config* cfg, const moe_weights* w, const void* x, const void* residual, void* y,
+                           float* logits, int32_t* topk_idx, float* gates, void* ws, size_t ws_bytes, void* stream);
+
 #ifdef __cplusplus
 }
 #endif

@@ -23,7 +23,7 @@ __all__ = ["make_config", "plan", "route", "dispatch", "experts", "combine", "fo
            "combine_backward_dropless", "experts_backward_dropless", "dispatch_backward_dropless",
            "BackwardRouted", "scoring", "route_scored", "route_scored_backward", "quantize", "gemm_quant",
            "experts_dropless_quant", "quantize_weights", "ForwardDroplessQuant", "linear", "linear_backward",
-           "orthogonalize", "library", "MoeError"]
+           "orthogonalize", "ForwardFew", "library", "MoeError"]
 
 MoeError = abi.MoeError
 _DT = {"f32": abi.MOE_F32, "bf16": abi.MOE_BF16, torch.float32: abi.MOE_F32,
@@ -929,3 +929,46 @@ def orthogonalize(g, steps: int = 5, coeffs=(3.4445, -4.7750, 2.0315), eps: floa
     a = abi.MoeOrthoArgs(B, M, N, g.data_ptr(), ldg, sg, out.data_ptr(), ldo, so, co, steps, _DT[g.dtype], eps, scale, 0)
     _with_workspace("moe_orthogonalize", dev, a, ws)
     return out
+
+
+# ------------------------------------------------------- a few tokens
+class ForwardFew:
+    """Reusable dropless forward for at most 16 tokens (moe_forward_few): the
+    weights of ForwardDropless, workspace and outputs bound once."""
+
+    def __init__(self, cfg, weights: Dict[str, torch.Tensor], device, taps=False):
+        device = torch.device(device)
+        if device.index is None:
+            device = torch.device(device.type, torch.cuda.current_device())
+        self.cfg, self.w = cfg, weights
+        n = C.c_size_t(0)
+        abi.check("moe_forward_few_ws_bytes", library().moe_forward_few_ws_bytes(C.byref(cfg), C.byref(n)))
+        T, D, L, E, k, F = cfg.T, cfg.d_model, cfg.d_latent, cfg.n_experts, cfg.top_k, cfg.d_ff
+        shapes = dict(w_latent=(L, D), w_router=(E, L), w_gate=(E, F, L), w_up=(E, F, L), w_down=(E, L, F),
+                      w_up_proj=(D, L))
+        if cfg.n_shared:
+            S, Fs = cfg.n_shared, cfg.d_ff_shared
+            shapes.update(ws_gate=(S, Fs, D), ws_up=(S, Fs, D), ws_down=(S, D, Fs))
+        f = {m: _rows(weights[m], shape, torch.bfloat16, m, device).data_ptr() for m, shape in shapes.items()}
+        if weights.get("router_bias") is not None:
+            f["router_bias"] = _rows(weights["router_bias"], (E,), torch.float32, "router_bias", device).data_ptr()
+        self.wstruct = abi.MoeWeights(**f)
+        self.ws = _ws(n.value, device)
+        self.y = torch.empty((T, D), dtype=torch.bfloat16, device=device)
+        self.tap_t = {}
+        if taps:
+            self.tap_t = dict(logits=torch.empty((T, E), dtype=torch.float32, device=device),
+                              topk_idx=torch.empty((T, k), dtype=torch.int32, device=device),
+                              gates=torch.empty((T, k), dtype=torch.float32, device=device))
+        self._tail = (self.y.data_ptr(), *((self.tap_t[m].data_ptr() if taps else None)
+                                           for m in ("logits", "topk_idx", "gates")),
+                      self.ws.data_ptr(), self.ws.numel())
+
+    def __call__(self, x: torch.Tensor, residual: Optional[torch.Tensor] = None):
+        cfg, dev = self.cfg, self.y.device
+        _rows(x, (cfg.T, cfg.d_model), torch.bfloat16, "x", dev)
+        if residual is not None:
+            _rows(residual, (cfg.T, cfg.d_model), torch.bfloat16, "residual", dev)
+        _launch("moe_forward_few", dev, C.byref(cfg), C.byref(self.wstruct), x.data_ptr(),
+                None if residual is None else residual.data_ptr(), *self._tail)
+        return self.y

@@ -187,6 +187,9 @@ SIGNATURES = {
     "moe_linear": (C.c_int, [C.POINTER(MoeLinearArgs), _P, C.c_size_t, _P]),
     "moe_linear_backward_ws_bytes": (C.c_int, [C.POINTER(MoeLinearGrad), C.POINTER(C.c_size_t)]),
     "moe_linear_backward": (C.c_int, [C.POINTER(MoeLinearGrad), _P, C.c_size_t, _P]),
+    "moe_forward_few_ws_bytes": (C.c_int, [C.POINTER(MoeConfig), C.POINTER(C.c_size_t)]),
+    "moe_forward_few": (C.c_int, [C.POINTER(MoeConfig), C.POINTER(MoeWeights), _P, _P, _P, _P, _P, _P, _P, C.c_size_t,
+                                  _P]),
     "moe_orthogonalize_ws_bytes": (C.c_int, [C.POINTER(MoeOrthoArgs), C.POINTER(C.c_size_t)]),
     "moe_orthogonalize": (C.c_int, [C.POINTER(MoeOrthoArgs), _P, C.c_size_t, _P]),
 }

@@ -1,0 +1,331 @@
+// The dropless branch for at most 16 tokens (moe_forward_few): every weight of
+// the latent projection, the router, the selected experts, the up-projection
+// and the shared experts is read once, straight from memory into matrix
+// instructions.
+//
+// The weights are the first matrix operand (16 rows of one K range a
+// wavefront, the wavefronts of a workgroup sharing K) and the tokens the
+// second: a token picks an expert once, so 16 tokens are at most 16 rows of any
+// expert and one instruction takes them all.  Since the weights' bytes bound
+// the time, the matrix instructions have time to spare, and activations between
+// two products are not rounded to bf16: they are held as the sum of two bf16
+// numbers (16 bits; the router sees three, all of fp32's), each multiplied
+// separately.
+#include "common.h"
+#include "kernels.h"
+#include "select.h"
+
+namespace moe {
+namespace {
+
+constexpr int kWaves = 4;
+constexpr int kThreads = 64 * kWaves;
+
+int64_t cdiv64(int64_t a, int64_t b) { return (a + b - 1) / b; }
+
+__device__ __forceinline__ f32x4_t mfma(const uint4& a, const uint4& b, f32x4_t c) {
+  return __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8_t, a), __builtin_bit_cast(bf16x8_t, b), c, 0,
+                                                 0, 0);
+}
+
+// Sums of one wavefront's share of K (64 values of it at a time, every
+// kWaves-th): W rows of kSets matrices by tokens held in kPlanes bf16 parts.
+// w and x point at this lane's row, 8 (lane >> 4) values in.
+template <int kSets, int kPlanes>
+__device__ __forceinline__ void stream(const uint16_t* const (&w)[kSets], const uint16_t* const (&x)[kPlanes], int K,
+                                       f32x4_t (&acc)[kSets]) {
+  const int wave = threadIdx.x >> 6;
+  auto chunk = [&](int k, uint4 (&a)[kSets][2], uint4 (&b)[kPlanes][2]) {
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+#pragma unroll
+      for (int s = 0; s < kSets; ++s) a[s][i] = ld16(w[s] + k + 32 * i);
+#pragma unroll
+      for (int p = 0; p < kPlanes; ++p) b[p][i] = ld16(x[p] + k + 32 * i);
+    }
+  };
+  auto sums = [&](const uint4 (&a)[kSets][2], const uint4 (&b)[kPlanes][2]) {
+#pragma unroll
+    for (int i = 0; i < 2; ++i)
+#pragma unroll
+      for (int p = kPlanes - 1; p >= 0; --p)
+#pragma unroll
+        for (int s = 0; s < kSets; ++s) acc[s] = mfma(a[s][i], b[p][i], acc[s]);
+  };
+  constexpr int U = 4;  // chunks whose loads are in flight together
+  int k = wave * 64;
+  for (; k + (U - 1) * kWaves * 64 < K; k += U * kWaves * 64) {
+    uint4 a[U][kSets][2], b[U][kPlanes][2];
+#pragma unroll
+    for (int u = 0; u < U; ++u) chunk(k + u * kWaves * 64, a[u], b[u]);
+#pragma unroll
+    for (int u = 0; u < U; ++u) sums(a[u], b[u]);
+  }
+  for (; k < K; k += kWaves * 64) {
+    uint4 a[kSets][2], b[kPlanes][2];
+    chunk(k, a, b);
+    sums(a, b);
+  }
+}
+
+// Sum over the wavefronts; complete in wavefront 0, whose lane holds weight
+// rows 4 (lane >> 4) .. + 3 of token lane & 15.
+template <int kSets>
+__device__ __forceinline__ void join(f32x4_t (&acc)[kSets], f32x4_t* part) {
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+  if (wave > 0) {
+#pragma unroll
+    for (int s = 0; s < kSets; ++s) part[((wave - 1) * kSets + s) * 64 + lane] = acc[s];
+  }
+  __syncthreads();
+  if (wave == 0) {
+#pragma unroll
+    for (int j = 0; j < kWaves - 1; ++j)
+#pragma unroll
+      for (int s = 0; s < kSets; ++s) acc[s] += part[(j * kSets + s) * 64 + lane];
+  }
+}
+
+// 4 neighbouring values as kPlanes bf16 parts, planes `plane` values apart.
+template <int kPlanes>
+__device__ __forceinline__ void store_parts(uint16_t* p, int64_t plane, f32x4_t v) {
+#pragma unroll
+  for (int i = 0; i < kPlanes; ++i) {
+    const uint2 q = make_uint2(bf16_pair(v[0], v[1]), bf16_pair(v[2], v[3]));
+    *reinterpret_cast<uint2*>(p + i * plane) = q;
+    v -= f32x4_t{__uint_as_float(q.x << 16), __uint_as_float(q.x & 0xFFFF0000u), __uint_as_float(q.y << 16),
+                 __uint_as_float(q.y & 0xFFFF0000u)};
+  }
+}
+
+__device__ __forceinline__ f32x4_t zero4() { return f32x4_t{0.f, 0.f, 0.f, 0.f}; }
+
+// z = x W_lat^T: 16 columns.
+__device__ void latent_item(const Few& f, int item, f32x4_t* part) {
+  const int lane = threadIdx.x & 63, at = (lane >> 4) * 8, t = min(lane & 15, f.T - 1);
+  const uint16_t* w[1] = {f.w_latent + (int64_t)(item * 16 + (lane & 15)) * f.D + at};
+  const uint16_t* x[1] = {f.x + (int64_t)t * f.D + at};
+  f32x4_t acc[1] = {zero4()};
+  stream<1, 1>(w, x, f.D, acc);
+  join<1>(acc, part);
+  if (threadIdx.x < 64 && (lane & 15) < f.T)
+    store_parts<3>(f.z + (int64_t)t * f.L + item * 16 + (lane >> 4) * 4, (int64_t)f.T * f.L, acc[0]);
+}
+
+// Hidden values of the shared experts, side by side: 16 of them.
+__device__ void shared_item(const Few& f, int item, f32x4_t* part) {
+  const int lane = threadIdx.x & 63, at = (lane >> 4) * 8, t = min(lane & 15, f.T - 1);
+  const int64_t row = (int64_t)(item * 16 + (lane & 15)) * f.D + at;
+  const uint16_t* w[2] = {f.ws_gate + row, f.ws_up + row};
+  const uint16_t* x[1] = {f.x + (int64_t)t * f.D + at};
+  f32x4_t acc[2] = {zero4(), zero4()};
+  stream<2, 1>(w, x, f.D, acc);
+  join<2>(acc, part);
+  if (threadIdx.x < 64 && (lane & 15) < f.T) {
+    f32x4_t h;
+#pragma unroll
+    for (int r = 0; r < 4; ++r) h[r] = silu(acc[0][r]) * acc[1][r];
+    const int W = f.S * f.Fs;
+    store_parts<2>(f.hs + (int64_t)t * W + item * 16 + (lane >> 4) * 4, (int64_t)f.T * W, h);
+  }
+}
+
+// Router logits of 16 experts.
+__device__ void router_item(const Few& f, int item, f32x4_t* part) {
+  const int lane = threadIdx.x & 63, at = (lane >> 4) * 8, t = min(lane & 15, f.T - 1);
+  const uint16_t* w[1] = {f.w_router + (int64_t)min(item * 16 + (lane & 15), f.E - 1) * f.L + at};
+  const uint16_t* z = f.z + (int64_t)t * f.L + at;
+  const int64_t plane = (int64_t)f.T * f.L;
+  const uint16_t* x[3] = {z, z + plane, z + 2 * plane};
+  f32x4_t acc[1] = {zero4()};
+  stream<1, 3>(w, x, f.L, acc);
+  join<1>(acc, part);
+  if (threadIdx.x < 64 && (lane & 15) < f.T) {
+#pragma unroll
+    for (int r = 0; r < 4; ++r) {
+      const int e = item * 16 + (lane >> 4) * 4 + r;
+      if (e < f.E) f.logits[(int64_t)t * f.E + e] = acc[0][r];
+    }
+  }
+}
+
+// 16 hidden values of the rows of selected expert a.
+__device__ void hidden_item(const Few& f, int a, int item, f32x4_t* part) {
+  const int lane = threadIdx.x & 63, at = (lane >> 4) * 8;
+  const int e = f.act[a], n = f.act_rows[a];
+  const int r = f.rows[a * 16 + min(lane & 15, n - 1)];  // t k + j
+  const int64_t row = ((int64_t)e * f.F + item * 16 + (lane & 15)) * f.L + at;
+  const uint16_t* w[2] = {f.w_gate + row, f.w_up + row};
+  const uint16_t* z = f.z + (int64_t)(r / f.k) * f.L + at;
+  const uint16_t* x[2] = {z, z + (int64_t)f.T * f.L};
+  f32x4_t acc[2] = {zero4(), zero4()};
+  stream<2, 2>(w, x, f.L, acc);
+  join<2>(acc, part);
+  if (threadIdx.x < 64 && (lane & 15) < n) {
+    f32x4_t h;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) h[i] = silu(acc[0][i]) * acc[1][i];
+    store_parts<2>(f.h + (int64_t)r * f.F + item * 16 + (lane >> 4) * 4, (int64_t)f.T * f.k * f.F, h);
+  }
+}
+
+// 16 columns of the outputs of selected expert a.
+__device__ void down_item(const Few& f, int a, int item, f32x4_t* part) {
+  const int lane = threadIdx.x & 63, at = (lane >> 4) * 8;
+  const int e = f.act[a], n = f.act_rows[a];
+  const int r = f.rows[a * 16 + min(lane & 15, n - 1)];
+  const uint16_t* w[1] = {f.w_down + ((int64_t)e * f.L + item * 16 + (lane & 15)) * f.F + at};
+  const uint16_t* h = f.h + (int64_t)r * f.F + at;
+  const uint16_t* x[2] = {h, h + (int64_t)f.T * f.k * f.F};
+  f32x4_t acc[1] = {zero4()};
+  stream<1, 2>(w, x, f.F, acc);
+  join<1>(acc, part);
+  if (threadIdx.x < 64 && (lane & 15) < n)
+    *reinterpret_cast<f32x4_t*>(f.o + (int64_t)r * f.L + item * 16 + (lane >> 4) * 4) = acc[0];
+}
+
+// y_lat = sum over a token's experts, in order: 4 columns a thread.
+__device__ void combine_at(const Few& f, int t, int col) {
+  f32x4_t s = zero4();
+  for (int j = 0; j < f.k; ++j)
+    s += f.gates[t * f.k + j] * *reinterpret_cast<const f32x4_t*>(f.o + (int64_t)(t * f.k + j) * f.L + col);
+  store_parts<2>(f.ylat + (int64_t)t * f.L + col, (int64_t)f.T * f.L, s);
+}
+
+// 16 columns of y: the up-projection, the shared down-projections and the
+// residual.
+__device__ void output_item(const Few& f, int item, f32x4_t* part) {
+  const int lane = threadIdx.x & 63, at = (lane >> 4) * 8, t = min(lane & 15, f.T - 1);
+  const int64_t n = item * 16 + (lane & 15);
+  f32x4_t acc[1] = {zero4()};
+  {
+    const uint16_t* w[1] = {f.w_up_proj + n * f.L + at};
+    const uint16_t* y = f.ylat + (int64_t)t * f.L + at;
+    const uint16_t* x[2] = {y, y + (int64_t)f.T * f.L};
+    stream<1, 2>(w, x, f.L, acc);
+  }
+  const int W = f.S * f.Fs;
+  for (int s = 0; s < f.S; ++s) {
+    const uint16_t* w[1] = {f.ws_down + ((int64_t)s * f.D + n) * f.Fs + at};
+    const uint16_t* h = f.hs + (int64_t)t * W + s * f.Fs + at;
+    const uint16_t* x[2] = {h, h + (int64_t)f.T * W};
+    stream<1, 2>(w, x, f.Fs, acc);
+  }
+  join<1>(acc, part);
+  if (threadIdx.x < 64 && (lane & 15) < f.T) {
+    const int64_t o = (int64_t)t * f.D + item * 16 + (lane >> 4) * 4;
+    f32x4_t v = acc[0];
+    if (f.res) {
+      const uint2 r = *reinterpret_cast<const uint2*>(f.res + o);
+      v += f32x4_t{__uint_as_float(r.x << 16), __uint_as_float(r.x & 0xFFFF0000u), __uint_as_float(r.y << 16),
+                   __uint_as_float(r.y & 0xFFFF0000u)};
+    }
+    *reinterpret_cast<uint2*>(f.y + o) = make_uint2(bf16_pair(v[0], v[1]), bf16_pair(v[2], v[3]));
+  }
+}
+
+// Selection for every token, then the selected experts in ascending order,
+// each with its rows t k + j in token order.  One workgroup.
+__device__ void route_all(const Few& f, uint32_t* mask, int* scan) {
+  const int wave = threadIdx.x >> 6, lane = threadIdx.x & 63;
+  for (int e = threadIdx.x; e < f.E; e += kThreads) mask[e] = 0;
+  __syncthreads();
+  for (int t = wave; t < f.T; t += kWaves) {
+    int mine;
+    float g;
+    select_topk(f.logits + (int64_t)t * f.E, f.bias, f.E, f.k, mine, g);
+    if (lane < f.k) {
+      f.topk[t * f.k + lane] = mine;
+      f.gates[t * f.k + lane] = g;
+      atomicOr(&mask[mine], 1u << t);
+    }
+  }
+  __syncthreads();
+  // rank of every selected expert among the selected: 4 neighbouring experts a thread
+  int n = 0;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const int e = threadIdx.x * 4 + i;
+    n += e < f.E && mask[e] != 0;
+  }
+  int x = n;
+  for (int d = 1; d < 64; d <<= 1) {
+    const int o = __shfl_up(x, d);
+    if (lane >= d) x += o;
+  }
+  if (lane == 63) scan[wave] = x;
+  __syncthreads();
+  int a = x - n;
+  for (int w = 0; w < wave; ++w) a += scan[w];
+  if (threadIdx.x == kThreads - 1) *f.n_act = a + n;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const int e = threadIdx.x * 4 + i;
+    if (e < f.E && mask[e] != 0) {
+      f.act[a] = e;
+      f.act_rows[a] = __popc(mask[e]);
+      mask[e] |= (uint32_t)a << 16;  // T <= 16: the upper half is free
+      ++a;
+    }
+  }
+  __syncthreads();
+  for (int i = threadIdx.x; i < f.T * f.k; i += kThreads) {
+    const int t = i / f.k;
+    const uint32_t m = mask[f.topk[i]];
+    f.rows[(m >> 16) * 16 + __popc(m & ((1u << t) - 1u))] = i;
+  }
+}
+static_assert(kThreads * 4 >= 1024, "the scan covers every expert");
+
+constexpr int kPart = (kWaves - 1) * 2 * 64;
+
+__global__ __launch_bounds__(kThreads) void few_first_kernel(Few f) {
+  __shared__ f32x4_t part[kPart];
+  const int n = f.L / 16;
+  if ((int)blockIdx.x < n)
+    latent_item(f, blockIdx.x, part);
+  else
+    shared_item(f, blockIdx.x - n, part);
+}
+__global__ __launch_bounds__(kThreads) void few_router_kernel(Few f) {
+  __shared__ f32x4_t part[kPart];
+  router_item(f, blockIdx.x, part);
+}
+__global__ __launch_bounds__(kThreads) void few_route_kernel(Few f) {
+  __shared__ uint32_t mask[1024];
+  __shared__ int scan[kWaves];
+  route_all(f, mask, scan);
+}
+__global__ __launch_bounds__(kThreads) void few_hidden_kernel(Few f) {
+  __shared__ f32x4_t part[kPart];
+  if ((int)blockIdx.y < *f.n_act) hidden_item(f, blockIdx.y, blockIdx.x, part);
+}
+__global__ __launch_bounds__(kThreads) void few_down_kernel(Few f) {
+  __shared__ f32x4_t part[kPart];
+  if ((int)blockIdx.y < *f.n_act) down_item(f, blockIdx.y, blockIdx.x, part);
+}
+__global__ __launch_bounds__(kThreads) void few_combine_kernel(Few f) {
+  const int i = blockIdx.x * kThreads + threadIdx.x, per = f.L / 4;
+  if (i < f.T * per) combine_at(f, i / per, i % per * 4);
+}
+__global__ __launch_bounds__(kThreads) void few_output_kernel(Few f) {
+  __shared__ f32x4_t part[kPart];
+  output_item(f, blockIdx.x, part);
+}
+
+}  // namespace
+
+hipError_t launch_few(const Few& f, hipStream_t s) {
+  if (f.T <= 0) return hipSuccess;
+  const unsigned most = (unsigned)(f.T * f.k < f.E ? f.T * f.k : f.E);
+  few_first_kernel<<<(unsigned)(f.L / 16 + f.S * f.Fs / 16), kThreads, 0, s>>>(f);
+  few_router_kernel<<<(unsigned)cdiv64(f.E, 16), kThreads, 0, s>>>(f);
+  few_route_kernel<<<1, kThreads, 0, s>>>(f);
+  few_hidden_kernel<<<dim3(f.F / 16, most), kThreads, 0, s>>>(f);
+  few_down_kernel<<<dim3(f.L / 16, most), kThreads, 0, s>>>(f);
+  few_combine_kernel<<<(unsigned)cdiv64(f.T * (f.L / 4), kThreads), kThreads, 0, s>>>(f);
+  few_output_kernel<<<(unsigned)(f.D / 16), kThreads, 0, s>>>(f);
+  return hipGetLastError();
+}
+
+}  // namespace moe

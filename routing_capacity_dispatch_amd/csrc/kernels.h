@@ -459,4 +459,36 @@ int64_t ortho_group(int64_t batch, int64_t m, int64_t n);
 hipError_t launch_orthogonalize(const Ortho& p, const OrthoStep* step, int steps, int64_t batch, int64_t group,
                                 hipStream_t s);
 
+// ------------------------------------------- the branch for a few tokens
+// few.hip: T <= 16; activations between products as planes of bf16 parts.
+struct Few {
+  int T, D, L, E, k, F, S, Fs;
+  const uint16_t* x;         // [T][D]
+  const uint16_t* res;       // [T][D] or null
+  uint16_t* y;               // [T][D]
+  const uint16_t* w_latent;  // weights as in moe_weights
+  const uint16_t* w_router;
+  const float* bias;
+  const uint16_t* w_gate;
+  const uint16_t* w_up;
+  const uint16_t* w_down;
+  const uint16_t* w_up_proj;
+  const uint16_t* ws_gate;
+  const uint16_t* ws_up;
+  const uint16_t* ws_down;
+  uint16_t* z;               // [3][T][L]
+  uint16_t* hs;              // [2][T][S Fs]
+  float* logits;             // [T][E]
+  int32_t* topk;             // [T][k]
+  float* gates;              // [T][k]
+  int32_t* n_act;            // experts that have rows
+  int32_t* act;              // their numbers, ascending
+  int32_t* act_rows;         // and rows, 1 .. T
+  int32_t* rows;             // [.][16]: t k + j of each
+  uint16_t* h;               // [2][T k][F]
+  float* o;                  // [T k][L]
+  uint16_t* ylat;            // [2][T][L]
+};
+hipError_t launch_few(const Few& f, hipStream_t s);
+
 }  // namespace moe

@@ -2396,3 +2396,95 @@ MOE_API moe_status moe_orthogonalize(const moe_ortho_args* args, void* ws, size_
   p.vec_out = aligned_to(a.out, per * 2) && a.ldo % per == 0 && (a.batch == 1 || a.stride_o % per == 0);
   return hip_status(moe::launch_orthogonalize(p, steps, a.steps, a.batch, group, static_cast<hipStream_t>(stream)));
 }
+
+// ------------------------------------------------------------------ the branch for a few tokens
+namespace {
+
+constexpr int64_t kFewTokens = 16;
+
+moe_status check_few(const moe_config* cfg) {
+  moe_plan p;
+  const moe_status st = check_dropless(cfg, &p);
+  if (st != MOE_OK) return st;
+  if (cfg->top_k > cfg->n_experts) return MOE_ERR_INVALID_ARG;
+  return cfg->T > kFewTokens ? MOE_ERR_UNSUPPORTED : MOE_OK;
+}
+
+int64_t carve_few(const moe_config* c, float* logits, int32_t* topk, float* gates, void* ws, moe::Few* f) {
+  const int64_t T = c->T, L = c->d_latent, E = c->n_experts, k = c->top_k, F = c->d_ff, R = T * k;
+  const int64_t W = c->n_shared > 0 ? (int64_t)c->n_shared * c->d_ff_shared : 0, most = R < E ? R : E;
+  Carver cv{static_cast<char*>(ws), 0};
+  auto pick = [&](void* given, int64_t bytes) {
+    void* q = cv.take(bytes);
+    return given ? given : q;
+  };
+  f->z = static_cast<uint16_t*>(cv.take(3 * T * L * 2));
+  f->hs = static_cast<uint16_t*>(cv.take(2 * T * W * 2));
+  f->logits = static_cast<float*>(pick(logits, T * E * 4));
+  f->topk = static_cast<int32_t*>(pick(topk, R * 4));
+  f->gates = static_cast<float*>(pick(gates, R * 4));
+  f->n_act = static_cast<int32_t*>(cv.take(4));
+  f->act = static_cast<int32_t*>(cv.take(most * 4));
+  f->act_rows = static_cast<int32_t*>(cv.take(most * 4));
+  f->rows = static_cast<int32_t*>(cv.take(most * 16 * 4));
+  f->h = static_cast<uint16_t*>(cv.take(2 * R * F * 2));
+  f->o = static_cast<float*>(cv.take(R * L * 4));
+  f->ylat = static_cast<uint16_t*>(cv.take(2 * T * L * 2));
+  return cv.used;
+}
+
+}  // namespace
+
+MOE_API moe_status moe_forward_few_ws_bytes(const moe_config* cfg, size_t* bytes) {
+  const moe_status st = check_few(cfg);
+  if (st != MOE_OK) return st;
+  if (!bytes) return MOE_ERR_INVALID_ARG;
+  moe::Few f{};
+  *bytes = (size_t)carve_few(cfg, nullptr, nullptr, nullptr, nullptr, &f);
+  return MOE_OK;
+}
+
+MOE_API moe_status moe_forward_few(const moe_config* cfg, const moe_weights* w, const void* x, const void* residual,
+                                   void* y, float* logits, int32_t* topk_idx, float* gates, void* ws, size_t ws_bytes,
+                                   void* stream) {
+  const moe_status st = check_few(cfg);
+  if (st != MOE_OK) return st;
+  if (!w) return MOE_ERR_INVALID_ARG;
+  for (const void* p : {w->w_latent, w->w_router, w->w_gate, w->w_up, w->w_down, w->w_up_proj})
+    if (!p || !aligned16(p)) return MOE_ERR_INVALID_ARG;
+  if (cfg->n_shared > 0)
+    for (const void* p : {w->ws_gate, w->ws_up, w->ws_down})
+      if (!p || !aligned16(p)) return MOE_ERR_INVALID_ARG;
+  if (!aligned_to(w->router_bias, 4) || !aligned16(residual) || !aligned_to(logits, 4) || !aligned_to(topk_idx, 4) ||
+      !aligned_to(gates, 4))
+    return MOE_ERR_INVALID_ARG;
+  if (cfg->T == 0) return MOE_OK;
+  if (!x || !y || !aligned16(x) || !aligned16(y)) return MOE_ERR_INVALID_ARG;
+  moe::Few f{};
+  if (!ws || !aligned256(ws) || (int64_t)ws_bytes < carve_few(cfg, nullptr, nullptr, nullptr, nullptr, &f))
+    return MOE_ERR_WORKSPACE;
+  carve_few(cfg, logits, topk_idx, gates, ws, &f);
+  auto bf16 = [](const void* p) { return static_cast<const uint16_t*>(p); };
+  f.T = (int)cfg->T;
+  f.D = cfg->d_model;
+  f.L = cfg->d_latent;
+  f.E = cfg->n_experts;
+  f.k = cfg->top_k;
+  f.F = cfg->d_ff;
+  f.S = cfg->n_shared;
+  f.Fs = cfg->n_shared > 0 ? cfg->d_ff_shared : 0;
+  f.x = bf16(x);
+  f.res = bf16(residual);
+  f.y = static_cast<uint16_t*>(y);
+  f.w_latent = bf16(w->w_latent);
+  f.w_router = bf16(w->w_router);
+  f.bias = w->router_bias;
+  f.w_gate = bf16(w->w_gate);
+  f.w_up = bf16(w->w_up);
+  f.w_down = bf16(w->w_down);
+  f.w_up_proj = bf16(w->w_up_proj);
+  f.ws_gate = bf16(w->ws_gate);
+  f.ws_up = bf16(w->ws_up);
+  f.ws_down = bf16(w->ws_down);
+  return hip_status(moe::launch_few(f, static_cast<hipStream_t>(stream)));
+}
