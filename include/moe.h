@@ -798,7 +798,7 @@ typedef struct {
   int32_t reserved; /* must be 0                                          */
 } moe_linear_grad;
 
-/* As above; M up to 4194240 (MOE_ERR_UNSUPPORTED past that).  x may be NULL
+/* As above; M up to 2097120 (MOE_ERR_UNSUPPORTED past that).  x may be NULL
    without dw, w without dx. */
 moe_status moe_linear_backward_ws_bytes(const moe_linear_grad* args, size_t* bytes);
 moe_status moe_linear_backward(const moe_linear_grad* args, void* ws, size_t ws_bytes, void* stream);

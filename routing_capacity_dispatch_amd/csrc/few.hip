@@ -14,6 +14,7 @@
 #include "common.h"
 #include "kernels.h"
 #include "select.h"
+#include "stream.h"
 
 namespace moe {
 namespace {
@@ -23,66 +24,28 @@ constexpr int kThreads = 64 * kWaves;
 
 int64_t cdiv64(int64_t a, int64_t b) { return (a + b - 1) / b; }
 
-__device__ __forceinline__ f32x4_t mfma(const uint4& a, const uint4& b, f32x4_t c) {
-  return __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8_t, a), __builtin_bit_cast(bf16x8_t, b), c, 0,
-                                                 0, 0);
-}
-
-// Sums of one wavefront's share of K (64 values of it at a time, every
-// kWaves-th): W rows of kSets matrices by tokens held in kPlanes bf16 parts.
-// w and x point at this lane's row, 8 (lane >> 4) values in.
+// kSets matrices by tokens held in kPlanes bf16 parts, over K values.
 template <int kSets, int kPlanes>
-__device__ __forceinline__ void stream(const uint16_t* const (&w)[kSets], const uint16_t* const (&x)[kPlanes], int K,
-                                       f32x4_t (&acc)[kSets]) {
-  const int wave = threadIdx.x >> 6;
-  auto chunk = [&](int k, uint4 (&a)[kSets][2], uint4 (&b)[kPlanes][2]) {
-#pragma unroll
-    for (int i = 0; i < 2; ++i) {
-#pragma unroll
-      for (int s = 0; s < kSets; ++s) a[s][i] = ld16(w[s] + k + 32 * i);
-#pragma unroll
-      for (int p = 0; p < kPlanes; ++p) b[p][i] = ld16(x[p] + k + 32 * i);
-    }
-  };
-  auto sums = [&](const uint4 (&a)[kSets][2], const uint4 (&b)[kPlanes][2]) {
-#pragma unroll
-    for (int i = 0; i < 2; ++i)
-#pragma unroll
-      for (int p = kPlanes - 1; p >= 0; --p)
-#pragma unroll
-        for (int s = 0; s < kSets; ++s) acc[s] = mfma(a[s][i], b[p][i], acc[s]);
-  };
-  constexpr int U = 4;  // chunks whose loads are in flight together
-  int k = wave * 64;
-  for (; k + (U - 1) * kWaves * 64 < K; k += U * kWaves * 64) {
-    uint4 a[U][kSets][2], b[U][kPlanes][2];
-#pragma unroll
-    for (int u = 0; u < U; ++u) chunk(k + u * kWaves * 64, a[u], b[u]);
-#pragma unroll
-    for (int u = 0; u < U; ++u) sums(a[u], b[u]);
-  }
-  for (; k < K; k += kWaves * 64) {
-    uint4 a[kSets][2], b[kPlanes][2];
-    chunk(k, a, b);
-    sums(a, b);
-  }
+__device__ __forceinline__ void product(const uint16_t* const (&w)[kSets], const uint16_t* const (&x)[kPlanes], int K,
+                                        f32x4_t (&acc)[kSets][1]) {
+  stream<kWaves, kSets, kPlanes, true>(w, x, K / 64, acc, [](const uint16_t* p) { return ld16(p); });
 }
 
 // Sum over the wavefronts; complete in wavefront 0, whose lane holds weight
 // rows 4 (lane >> 4) .. + 3 of token lane & 15.
 template <int kSets>
-__device__ __forceinline__ void join(f32x4_t (&acc)[kSets], f32x4_t* part) {
+__device__ __forceinline__ void join(f32x4_t (&acc)[kSets][1], f32x4_t* part) {
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
   if (wave > 0) {
 #pragma unroll
-    for (int s = 0; s < kSets; ++s) part[((wave - 1) * kSets + s) * 64 + lane] = acc[s];
+    for (int s = 0; s < kSets; ++s) part[((wave - 1) * kSets + s) * 64 + lane] = acc[s][0];
   }
   __syncthreads();
   if (wave == 0) {
 #pragma unroll
     for (int j = 0; j < kWaves - 1; ++j)
 #pragma unroll
-      for (int s = 0; s < kSets; ++s) acc[s] += part[(j * kSets + s) * 64 + lane];
+      for (int s = 0; s < kSets; ++s) acc[s][0] += part[(j * kSets + s) * 64 + lane];
   }
 }
 
@@ -105,11 +68,11 @@ __device__ void latent_item(const Few& f, int item, f32x4_t* part) {
   const int lane = threadIdx.x & 63, at = (lane >> 4) * 8, t = min(lane & 15, f.T - 1);
   const uint16_t* w[1] = {f.w_latent + (int64_t)(item * 16 + (lane & 15)) * f.D + at};
   const uint16_t* x[1] = {f.x + (int64_t)t * f.D + at};
-  f32x4_t acc[1] = {zero4()};
-  stream<1, 1>(w, x, f.D, acc);
+  f32x4_t acc[1][1] = {{zero4()}};
+  product<1, 1>(w, x, f.D, acc);
   join<1>(acc, part);
   if (threadIdx.x < 64 && (lane & 15) < f.T)
-    store_parts<3>(f.z + (int64_t)t * f.L + item * 16 + (lane >> 4) * 4, (int64_t)f.T * f.L, acc[0]);
+    store_parts<3>(f.z + (int64_t)t * f.L + item * 16 + (lane >> 4) * 4, (int64_t)f.T * f.L, acc[0][0]);
 }
 
 // Hidden values of the shared experts, side by side: 16 of them.
@@ -118,13 +81,13 @@ __device__ void shared_item(const Few& f, int item, f32x4_t* part) {
   const int64_t row = (int64_t)(item * 16 + (lane & 15)) * f.D + at;
   const uint16_t* w[2] = {f.ws_gate + row, f.ws_up + row};
   const uint16_t* x[1] = {f.x + (int64_t)t * f.D + at};
-  f32x4_t acc[2] = {zero4(), zero4()};
-  stream<2, 1>(w, x, f.D, acc);
+  f32x4_t acc[2][1] = {{zero4()}, {zero4()}};
+  product<2, 1>(w, x, f.D, acc);
   join<2>(acc, part);
   if (threadIdx.x < 64 && (lane & 15) < f.T) {
     f32x4_t h;
 #pragma unroll
-    for (int r = 0; r < 4; ++r) h[r] = silu(acc[0][r]) * acc[1][r];
+    for (int r = 0; r < 4; ++r) h[r] = silu(acc[0][0][r]) * acc[1][0][r];
     const int W = f.S * f.Fs;
     store_parts<2>(f.hs + (int64_t)t * W + item * 16 + (lane >> 4) * 4, (int64_t)f.T * W, h);
   }
@@ -137,14 +100,14 @@ __device__ void router_item(const Few& f, int item, f32x4_t* part) {
   const uint16_t* z = f.z + (int64_t)t * f.L + at;
   const int64_t plane = (int64_t)f.T * f.L;
   const uint16_t* x[3] = {z, z + plane, z + 2 * plane};
-  f32x4_t acc[1] = {zero4()};
-  stream<1, 3>(w, x, f.L, acc);
+  f32x4_t acc[1][1] = {{zero4()}};
+  product<1, 3>(w, x, f.L, acc);
   join<1>(acc, part);
   if (threadIdx.x < 64 && (lane & 15) < f.T) {
 #pragma unroll
     for (int r = 0; r < 4; ++r) {
       const int e = item * 16 + (lane >> 4) * 4 + r;
-      if (e < f.E) f.logits[(int64_t)t * f.E + e] = acc[0][r];
+      if (e < f.E) f.logits[(int64_t)t * f.E + e] = acc[0][0][r];
     }
   }
 }
@@ -158,13 +121,13 @@ __device__ void hidden_item(const Few& f, int a, int item, f32x4_t* part) {
   const uint16_t* w[2] = {f.w_gate + row, f.w_up + row};
   const uint16_t* z = f.z + (int64_t)(r / f.k) * f.L + at;
   const uint16_t* x[2] = {z, z + (int64_t)f.T * f.L};
-  f32x4_t acc[2] = {zero4(), zero4()};
-  stream<2, 2>(w, x, f.L, acc);
+  f32x4_t acc[2][1] = {{zero4()}, {zero4()}};
+  product<2, 2>(w, x, f.L, acc);
   join<2>(acc, part);
   if (threadIdx.x < 64 && (lane & 15) < n) {
     f32x4_t h;
 #pragma unroll
-    for (int i = 0; i < 4; ++i) h[i] = silu(acc[0][i]) * acc[1][i];
+    for (int i = 0; i < 4; ++i) h[i] = silu(acc[0][0][i]) * acc[1][0][i];
     store_parts<2>(f.h + (int64_t)r * f.F + item * 16 + (lane >> 4) * 4, (int64_t)f.T * f.k * f.F, h);
   }
 }
@@ -177,11 +140,11 @@ __device__ void down_item(const Few& f, int a, int item, f32x4_t* part) {
   const uint16_t* w[1] = {f.w_down + ((int64_t)e * f.L + item * 16 + (lane & 15)) * f.F + at};
   const uint16_t* h = f.h + (int64_t)r * f.F + at;
   const uint16_t* x[2] = {h, h + (int64_t)f.T * f.k * f.F};
-  f32x4_t acc[1] = {zero4()};
-  stream<1, 2>(w, x, f.F, acc);
+  f32x4_t acc[1][1] = {{zero4()}};
+  product<1, 2>(w, x, f.F, acc);
   join<1>(acc, part);
   if (threadIdx.x < 64 && (lane & 15) < n)
-    *reinterpret_cast<f32x4_t*>(f.o + (int64_t)r * f.L + item * 16 + (lane >> 4) * 4) = acc[0];
+    *reinterpret_cast<f32x4_t*>(f.o + (int64_t)r * f.L + item * 16 + (lane >> 4) * 4) = acc[0][0];
 }
 
 // y_lat = sum over a token's experts, in order: 4 columns a thread.
@@ -197,24 +160,24 @@ __device__ void combine_at(const Few& f, int t, int col) {
 __device__ void output_item(const Few& f, int item, f32x4_t* part) {
   const int lane = threadIdx.x & 63, at = (lane >> 4) * 8, t = min(lane & 15, f.T - 1);
   const int64_t n = item * 16 + (lane & 15);
-  f32x4_t acc[1] = {zero4()};
+  f32x4_t acc[1][1] = {{zero4()}};
   {
     const uint16_t* w[1] = {f.w_up_proj + n * f.L + at};
     const uint16_t* y = f.ylat + (int64_t)t * f.L + at;
     const uint16_t* x[2] = {y, y + (int64_t)f.T * f.L};
-    stream<1, 2>(w, x, f.L, acc);
+    product<1, 2>(w, x, f.L, acc);
   }
   const int W = f.S * f.Fs;
   for (int s = 0; s < f.S; ++s) {
     const uint16_t* w[1] = {f.ws_down + ((int64_t)s * f.D + n) * f.Fs + at};
     const uint16_t* h = f.hs + (int64_t)t * W + s * f.Fs + at;
     const uint16_t* x[2] = {h, h + (int64_t)f.T * W};
-    stream<1, 2>(w, x, f.Fs, acc);
+    product<1, 2>(w, x, f.Fs, acc);
   }
   join<1>(acc, part);
   if (threadIdx.x < 64 && (lane & 15) < f.T) {
     const int64_t o = (int64_t)t * f.D + item * 16 + (lane >> 4) * 4;
-    f32x4_t v = acc[0];
+    f32x4_t v = acc[0][0];
     if (f.res) {
       const uint2 r = *reinterpret_cast<const uint2*>(f.res + o);
       v += f32x4_t{__uint_as_float(r.x << 16), __uint_as_float(r.x & 0xFFFF0000u), __uint_as_float(r.y << 16),

@@ -52,7 +52,7 @@ struct Rows {
       // up to the end of the 16 bytes that hold the last value (a load is all
       // or nothing per 4 bytes; the columns that follow it are never stored)
       extent = K > 0 ? (((int64_t)(K - 1) * ld + (rows - r0)) * 2 + 15) & ~int64_t(15) : 0;
-      kstep = 64 * ld * 2;
+      kstep = TL::BK * ld * 2;
       in_scalar();
       col = 0;
 #pragma unroll
@@ -97,7 +97,7 @@ struct Rows {
     const int bytes = hi < 0 ? 0 : (hi > 0 || lo < 0) ? 0x7FFFFFFF : lo;
     TileAt t;
     t.rsrc = i32x4_t{(int)(uint32_t)b, (int)((uint32_t)(b >> 32) & 0xFFFFu), bytes, 0x00020000};
-    t.in = kMajor || col + j * 64 < (uint32_t)K;
+    t.in = kMajor || col + j * TL::BK < (uint32_t)K;
     return t;
   }
   __device__ __forceinline__ void load(const TileAt& t, int i, char* dst) const {
@@ -205,6 +205,186 @@ __device__ __forceinline__ void mainloop(const SA& a, const SB& b, int ktiles, c
   __syncthreads();
 }
 
+// The same with TL::NS stages of both operands, NS - 1 of them in flight, for
+// tiles that leave room for two workgroups a CU (one's epilogue then runs
+// under the other's matrix instructions) or that are few, so that each waits
+// for its loads alone.  One barrier per K tile; the fragments of the next one
+// are read among the matrix instructions of this one.
+template <class TL, bool AK, bool BK, bool kHalf, class SA, class SB>
+__device__ __forceinline__ void mainloop_pipe(const SA& a, const SB& b, int ktiles, char* lds, Acc<TL>& acc) {
+  static_assert(TL::NSB == TL::NS, "as many stages of B as of A");
+  constexpr int P = TL::A_INS + TL::B_INS, NS = TL::NS, KS = TL::KS;
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+  const int wm = wave / TL::WGN, wn = wave % TL::WGN;
+  char* lds_a = lds;
+  char* lds_b = lds + TL::B_BASE;
+  if (ktiles <= 0) return;
+  auto issue = [&](int j, int stage) {
+    const auto ta = a.tile(j);
+    const auto tb = b.tile(j);
+#pragma unroll
+    for (int i = 0; i < TL::A_INS; ++i) a.load(ta, i, lds_a + stage * TL::A_BYTES + (i * TL::NW + wave) * 1024);
+#pragma unroll
+    for (int i = 0; i < TL::B_INS; ++i) b.load(tb, i, lds_b + stage * TL::B_BYTES + (i * TL::NW + wave) * 1024);
+  };
+  // at most `tiles` tiles of this wavefront's loads still in flight, then a barrier
+  auto wait_tiles = [&](int tiles) {
+    if (NS >= 5 && tiles >= 4)
+      core::wait_loads<4 * P>();
+    else if (NS >= 4 && tiles >= 3)
+      core::wait_loads<3 * P>();
+    else if (NS >= 3 && tiles >= 2)
+      core::wait_loads<2 * P>();
+    else if (tiles >= 1)
+      core::wait_loads<P>();
+    else
+      core::wait_loads<0>();
+  };
+#pragma unroll
+  for (int j = 0; j < NS; ++j)
+    if (j < ktiles) issue(j, j);
+  wait_tiles(min(NS - 1, ktiles - 1));
+  Frags<TL> f[2][KS];
+  auto read = [&](int stage, Frags<TL> (&g)[KS]) {
+#pragma unroll
+    for (int ks = 0; ks < KS; ++ks)
+      core::read_frags<TL, AK, BK>(lds_a + stage * TL::A_BYTES, lds_b + stage * TL::B_BYTES, ks, g[ks], wm, wn, lane);
+  };
+  read(0, f[0]);
+  int stage = 0;  // of tile kt
+  auto step = [&](int kt, Frags<TL> (&cur)[KS], Frags<TL> (&nxt)[KS]) {
+    // landed: tile kt + 1; every wavefront has read tile kt
+    wait_tiles(min(NS - 2, ktiles - 2 - kt));
+    core::set_prio<1>();
+    if (kt + NS < ktiles) issue(kt + NS, stage);
+    if (++stage == NS) stage = 0;
+    read(stage, nxt);
+#pragma unroll
+    for (int ks = 0; ks < KS; ++ks) mfma_frags<TL, kHalf>(cur[ks], acc);
+#pragma unroll
+    for (int ks = 0; ks < KS; ++ks) interleave<TL, AK, BK>();
+    core::set_prio<0>();
+  };
+  int kt = 0;
+  for (; kt + 2 < ktiles; kt += 2) {
+    step(kt, f[0], f[1]);
+    step(kt + 1, f[1], f[0]);
+  }
+  if (kt + 1 < ktiles) {
+    step(kt, f[0], f[1]);
+#pragma unroll
+    for (int ks = 0; ks < KS; ++ks) mfma_frags<TL, kHalf>(f[1][ks], acc);
+  } else {
+#pragma unroll
+    for (int ks = 0; ks < KS; ++ks) mfma_frags<TL, kHalf>(f[0][ks], acc);
+  }
+  __builtin_amdgcn_sched_barrier(0);
+  __syncthreads();
+}
+
+typedef u32x4_t u32x4_any_t __attribute__((aligned(2)));
+// 16 bytes at any even address
+__device__ __forceinline__ uint4 ld16_any(const uint16_t* p) {
+  const u32x4_t v = *reinterpret_cast<const u32x4_any_t*>(p);
+  return make_uint4(v.x, v.y, v.z, v.w);
+}
+// 8 values from k on, zeros from K on
+__device__ __forceinline__ uint4 ld8_until(const uint16_t* row, int k, int K) {
+  if (k + 8 <= K) return ld16_any(row + k);
+  uint32_t w[4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const uint32_t lo = k + 2 * i < K ? row[k + 2 * i] : 0, hi = k + 2 * i + 1 < K ? row[k + 2 * i + 1] : 0;
+    w[i] = lo | hi << 16;
+  }
+  return make_uint4(w[0], w[1], w[2], w[3]);
+}
+
+// Rows of one operand at any alignment and of any K, by way of registers.
+template <class TL, int INS, int X, bool kMajor>
+struct RegRows {
+  const uint16_t* ptr;  // the tile's first row (column) at K = 0
+  int64_t ld;
+  int n, K, wave, lane;  // rows of the operand from there on
+  __device__ __forceinline__ void init(const void* p, int r0, int rows, int64_t ld_, int K_, int wave_, int lane_) {
+    ptr = static_cast<const uint16_t*>(p) + (kMajor ? r0 : r0 * ld_);
+    ld = ld_;
+    n = rows - r0;
+    K = K_;
+    wave = wave_;
+    lane = lane_;
+  }
+  // kLast: the last K tile, in which K ends.  Before it, rows past the
+  // operand's are read as its last and columns past it as the first or as what
+  // follows in memory (there is another k-row, and a k-row has at least 8
+  // values): their results are not stored.
+  template <bool kLast>
+  __device__ __forceinline__ uint4 load(int j, int i) const {
+    if constexpr (kMajor) {
+      const int kr = core::kload_row<TL, X>(i, wave, lane), k = j * TL::BK + kr, c = core::kload_col<X>(kr, lane) / 2;
+      if constexpr (!kLast) return ld16_any(ptr + k * ld + (c < n ? c : 0));
+      return k < K ? ld8_until(ptr + k * ld, c, n) : make_uint4(0, 0, 0, 0);
+    } else {
+      const int r = core::load_row<TL>(i, wave, lane), k = j * TL::BK + core::load_col<TL>(lane) / 2;
+      if constexpr (!kLast) return ld16_any(ptr + min(r, n - 1) * ld + k);
+      return r < n ? ld8_until(ptr + r * ld, k, K) : make_uint4(0, 0, 0, 0);
+    }
+  }
+};
+template <class TL, bool kAMajor>
+using ARegs = RegRows<TL, TL::A_INS, TL::BM, kAMajor>;
+template <class TL, bool kBMajor>
+using BRegs = RegRows<TL, TL::B_INS, TL::BN, kBMajor>;
+
+// acc += A B^T over such operands: four K tiles' loads in flight in registers,
+// two stages of LDS, one barrier per K tile.
+template <class TL, bool AK, bool BK, bool kHalf, class SA, class SB>
+__device__ __forceinline__ void mainloop_regs(const SA& a, const SB& b, int ktiles, char* lds, Acc<TL>& acc) {
+  constexpr int D = 4;
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+  const int wm = wave / TL::WGN, wn = wave % TL::WGN;
+  char* lds_a = lds;
+  char* lds_b = lds + TL::B_BASE;
+  uint4 ra[D][TL::A_INS], rb[D][TL::B_INS];
+  auto load = [&](int j, int s) {
+    if (j + 1 < ktiles) {
+#pragma unroll
+      for (int i = 0; i < TL::A_INS; ++i) ra[s][i] = a.template load<false>(j, i);
+#pragma unroll
+      for (int i = 0; i < TL::B_INS; ++i) rb[s][i] = b.template load<false>(j, i);
+    } else if (j < ktiles) {
+#pragma unroll
+      for (int i = 0; i < TL::A_INS; ++i) ra[s][i] = a.template load<true>(j, i);
+#pragma unroll
+      for (int i = 0; i < TL::B_INS; ++i) rb[s][i] = b.template load<true>(j, i);
+    }
+  };
+  auto step = [&](int j, int s) {
+    char* sa = lds_a + (s & 1) * TL::A_BYTES;
+    char* sb = lds_b + (s & 1) * TL::B_BYTES;
+#pragma unroll
+    for (int i = 0; i < TL::A_INS; ++i) st16(sa + (i * TL::NW + wave) * 1024 + lane * 16, ra[s][i]);
+#pragma unroll
+    for (int i = 0; i < TL::B_INS; ++i) st16(sb + (i * TL::NW + wave) * 1024 + lane * 16, rb[s][i]);
+    load(j + D, s);
+    __syncthreads();
+#pragma unroll
+    for (int ks = 0; ks < TL::KS; ++ks) {
+      Frags<TL> f;
+      core::read_frags<TL, AK, BK>(sa, sb, ks, f, wm, wn, lane);
+      mfma_frags<TL, kHalf>(f, acc);
+    }
+  };
+#pragma unroll
+  for (int s = 0; s < D; ++s) load(s, s);
+  for (int j = 0; j < ktiles; j += D) {
+#pragma unroll
+    for (int s = 0; s < D; ++s)
+      if (j + s < ktiles) step(j + s, s);
+  }
+  __syncthreads();
+}
+
 // LDS written by lanes of a wavefront is read by others of the same one.
 __device__ __forceinline__ void wave_sync() {
   __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
@@ -220,17 +400,34 @@ struct Epilogue {
   static constexpr int kRows = 16;
   static constexpr int kLd = TL::WN + 4;  // floats: the 4 row groups of a 16 x 16 block fall on different banks
   static constexpr int kBytes = TL::NW * kRows * kLd * 4;
-  template <class F>
-  __device__ __forceinline__ static void run(const Acc<TL>& acc, char* lds, int rows, F&& f) {
+  static constexpr int kLpr = TL::WN / 8;        // lanes a row
+  static constexpr int kRpi = 64 / kLpr;         // rows at a time
+  static constexpr int kIts = kRows / kRpi;
+  // First of the 8 columns that this lane meets, in every row.
+  __device__ __forceinline__ static int column() {
+    return ((threadIdx.x >> 6) % TL::WGN) * TL::WN + ((threadIdx.x & 63) % kLpr) * 8;
+  }
+  // load(row, column) -> X: what the epilogue reads there, fetched one block
+  // of kRows ahead (before the stores of the last one, which a load issued
+  // later would have to wait for).  f(row, column, 8 values, X).
+  template <class X, class Load, class F>
+  __device__ __forceinline__ static void run(const Acc<TL>& acc, char* lds, int rows, Load&& load, F&& f) {
     const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-    const int wm = wave / TL::WGN, wn = wave % TL::WGN;
+    const int wm = wave / TL::WGN;
     float* mine = reinterpret_cast<float*>(lds) + wave * kRows * kLd;
-    constexpr int LPR = TL::WN / 8;   // lanes a row
-    constexpr int RPI = 64 / LPR;     // rows at a time
+    const int r0 = lane / kLpr, c = (lane % kLpr) * 8, col = column();
+    X x[2][kIts];
+    auto fetch = [&](int mi, X (&to)[kIts]) {
+#pragma unroll
+      for (int i = 0; i < kIts; ++i) {
+        const int row = wm * TL::WM + mi * 16 + i * kRpi + r0;
+        if (row < rows) to[i] = load(row, col);
+      }
+    };
+    fetch(0, x[0]);
 #pragma unroll
     for (int mi = 0; mi < TL::MI; ++mi) {
-      const int row0 = wm * TL::WM + mi * 16;
-      if (row0 >= rows) break;
+      if (mi + 1 < TL::MI) fetch(mi + 1, x[(mi + 1) & 1]);
 #pragma unroll
       for (int ni = 0; ni < TL::NI; ++ni)
 #pragma unroll
@@ -238,15 +435,21 @@ struct Epilogue {
           mine[((lane >> 4) * 4 + r) * kLd + ni * 16 + (lane & 15)] = acc.v[mi][ni][r];
       wave_sync();
 #pragma unroll
-      for (int r = 0; r < kRows; r += RPI) {
-        const int row = r + lane / LPR, c = (lane % LPR) * 8;
+      for (int i = 0; i < kIts; ++i) {
+        const int row = i * kRpi + r0;
         const f32x4_t lo = *reinterpret_cast<const f32x4_t*>(mine + row * kLd + c);
         const f32x4_t hi = *reinterpret_cast<const f32x4_t*>(mine + row * kLd + c + 4);
         float v[8] = {lo[0], lo[1], lo[2], lo[3], hi[0], hi[1], hi[2], hi[3]};
-        if (row0 + row < rows) f(row0 + row, wn * TL::WN + c, v);
+        const int at = wm * TL::WM + mi * 16 + row;
+        if (at < rows) f(at, col, v, x[mi & 1][i]);
       }
       wave_sync();
     }
+  }
+  struct None {};
+  template <class F>
+  __device__ __forceinline__ static void run(const Acc<TL>& acc, char* lds, int rows, F&& f) {
+    run<None>(acc, lds, rows, [](int, int) { return None{}; }, [&](int r, int c, float* v, None) { f(r, c, v); });
   }
 };
 

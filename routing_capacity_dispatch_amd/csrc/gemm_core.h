@@ -203,13 +203,15 @@ typedef short i16x4_t __attribute__((ext_vector_type(4)));
 
 template <int X>
 struct KMajor {
-  static_assert(X == 128 || X == 256, "K-major tiles are 128 or 256 wide");
+  static_assert(X == 64 || X == 128 || X == 256, "K-major tiles are 64, 128 or 256 wide");
   static constexpr int RB = 2 * X;        // bytes per k-row
   static constexpr int CPR = RB / 16;     // 16-byte chunks per k-row
   static constexpr int RPI = 1024 / RB;   // k-rows per load instruction
   // distinct over k & 3 and bits 3.. of k for the 16 k-rows 8 g + 4 h + j
-  // (g < 4, j < 4) of one transposed read
+  // (g < 4, j < 4) of one transposed read (64 wide: a bank line holds two
+  // k-rows, and g alone spreads a read evenly over its 2 cycles)
   __device__ __forceinline__ static int swz(int k) {
+    if (X == 64) return ((k >> 3) & 3) << 1;
     return X == 256 ? (((k & 3) | (((k >> 3) & 3) << 2)) << 1) : (((k & 3) | (((k >> 3) & 1) << 2)) << 1);
   }
 };

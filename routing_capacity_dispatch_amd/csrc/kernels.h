@@ -394,32 +394,56 @@ struct Linear {
   void* pre;          // [M][ldp] bf16, or null
   int64_t ldp;
   int act;
-  int vec;            // rows of y, res and pre start on 16 bytes
   float* part;        // sums of the shares of K
   // set by the launcher
   int64_t ldpart;
   int tiles_m, tiles_n, shares, share_k;
 };
+// Tile sizes of a launch (256, 128 or 64 a side), and the shares of K of one
+// of its products.
+enum TileClass : int { TILE_BIG = 0, TILE_SMALL = 1, TILE_DEEP = 2 };
 struct LinearPlan {
-  bool big;
+  int cls;
   int shares, share_k;
   int64_t part_bytes;
 };
-LinearPlan linear_plan(int64_t M, int64_t N, int64_t K);
-// x and w row-major (with zeros from K to a multiple of 8) or K-major (x only
-// with w), rows on 16 bytes; g.part of linear_plan(...).part_bytes.
-hipError_t launch_linear_tiles(const Linear& g, bool a_kmajor, bool b_kmajor, hipStream_t s);
+// For one product of M0 x N0 results, or two in one launch.
+int linear_class(int64_t M0, int64_t N0, int64_t M1, int64_t N1);
+double linear_units(int cls, int64_t M, int64_t N, int64_t K);
+LinearPlan linear_plan(int cls, int64_t M, int64_t N, int64_t K, double units);
+// Rows of x and w on 16 bytes, with zeros from K to a multiple of 8, or (regs,
+// TILE_DEEP only) at any alignment; g.part of p.part_bytes.
+hipError_t launch_linear_tiles(const Linear& g, const LinearPlan& p, bool regs, hipStream_t s);
+// dw = x^T w with both operands K-major ([K][ldx], [K][ldw]), dx = x w with w
+// K-major (y null: not computed), db[n] = sum of sums[.][n] (null: none).
+struct LinearGrads {
+  Linear dw, dx;
+  int grid_dw, grid_dx;  // set by the launcher
+  const float* sums;     // [sum_blocks][N]
+  int64_t sum_blocks;
+  int N;
+  float* db;
+};
+hipError_t launch_linear_grads(const LinearGrads& g, const LinearPlan& dw, const LinearPlan& dx, bool regs,
+                               hipStream_t s);
 // At most 64 rows, both operands row-major, any alignment and K.
 bool linear_skinny(int64_t M);
 hipError_t launch_linear_skinny(const Linear& g, hipStream_t s);
-// bf16 rows into rows of ldd (a multiple of 8) with zeros past cols.
-hipError_t launch_pack_rows(const void* src, int64_t rows, int cols, int64_t ld, void* dst, int64_t ldd,
-                            hipStream_t s);
-// d = dy act'(pre), bf16 rows of ldd with zeros past N (d null: not written);
-// db [N] its sums over rows (null: none) by way of part [slope_blocks(M)][N].
+// bf16 rows into rows of ldd (a multiple of 8) with zeros past cols; dst null: none.
+struct PackRows {
+  const void* src;
+  int64_t rows;
+  int cols;
+  int64_t ld;
+  void* dst;
+  int64_t ldd;
+};
+hipError_t launch_pack_rows(const PackRows& a, const PackRows& b, hipStream_t s);
+// d = dy act'(pre), bf16 rows of ldd with zeros past N (d null: not written),
+// and its sums over blocks of rows, part [slope_blocks(M)][N] (null: none).
 int64_t slope_blocks(int64_t M);
 hipError_t launch_slope(const void* dy, int64_t ldy, int dy_dt, const void* pre, int64_t ldp, int act, int64_t M,
-                        int N, void* d, int64_t ldd, float* part, float* db, hipStream_t s);
+                        int N, void* d, int64_t ldd, float* part, hipStream_t s);
 
 // ------------------------------------------------- orthogonalised updates
 // Newton-Schulz iteration (orthogonalize.hip).  X is m x n, m <= n, with rows

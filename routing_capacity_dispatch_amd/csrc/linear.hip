@@ -4,13 +4,14 @@
 //
 // Up to kSkinnyRows rows the product is bound by the weights' bytes: they go
 // straight from memory into matrix instructions, the wavefronts of a workgroup
-// sharing K.  More rows take the tiles of gemm_buf.h, K shared by several
-// workgroups where the tiles alone would leave compute units idle.  Operands
-// whose rows do not start on 16 bytes, or end inside 16, are copied into such
-// rows first (tiles only).
+// sharing K.  More rows take the tiles of gemm_buf.h, in three sizes (below),
+// the K of tiles that are few or long shared by several workgroups.  Both
+// products of a backward run in one launch, so that one fills the compute units
+// that the other leaves idle.
 #include "common.h"
 #include "gemm_buf.h"
 #include "kernels.h"
+#include "stream.h"
 
 namespace moe {
 namespace {
@@ -19,9 +20,14 @@ using core::Acc;
 using core::dense_tile;
 using core::xcd_order;
 
-// All 160 KB of LDS, one workgroup a CU; or two of them a CU
+// All 160 KB of LDS, one workgroup a CU: the fastest where every CU has a
+// tile (16384 x 6144 x 6144: 1.02 ms, 128 x 128 tiles 1.35, 64 x 64 2.1)
 using BigTile = core::Tile<256, 256, 4, 2, 64, 2, 3>;
+// Two workgroups a CU (2048 x 2048 x 2048: 33 us, big 59, 64 x 64 36)
 using SmallTile = core::Tile<128, 128, 2, 2, 64, 2, 2>;
+// Two workgroups a CU, five K tiles in flight each: for few tiles, whose time
+// is the loads' (512 x 2048 x 2048: 15 us, 128 x 128 30, or 26 with K shared)
+using DeepTile = core::Tile<64, 64, 2, 2, 64, 5>;
 
 int64_t cdiv64(int64_t a, int64_t b) { return (a + b - 1) / b; }
 
@@ -57,19 +63,22 @@ __device__ __forceinline__ void st_elem(void* p, int64_t i, int dt, float v) {
     static_cast<uint16_t*>(p)[i] = f32_to_bf16(v);
 }
 
-// C neighbouring values of a row, C 4 or 8, on C * size bytes' alignment
+// C neighbouring values of a row, C 4 or 8, at any alignment of an element
+// (the hardware takes wide accesses at any address)
+typedef u32x4_t u32x4_any_t __attribute__((aligned(2)));
+typedef unsigned int u32x2_any_t __attribute__((ext_vector_type(2), aligned(2)));
 template <int C>
 __device__ __forceinline__ void ld_vec(const void* p, int64_t i, int dt, float* v) {
   if (dt == DT_F32) {
-    const float* q = static_cast<const float*>(p) + i;
+    const uint16_t* q = reinterpret_cast<const uint16_t*>(static_cast<const float*>(p) + i);
 #pragma unroll
-    for (int c = 0; c < C; c += 4) unpack(ld16(q + c), v + c, float{});
+    for (int c = 0; c < C; c += 4) unpack(buf::ld16_any(q + 2 * c), v + c, float{});
   } else {
     const uint16_t* q = static_cast<const uint16_t*>(p) + i;
     if constexpr (C == 8) {
-      unpack(ld16(q), v, bf16_t{});
+      unpack(buf::ld16_any(q), v, bf16_t{});
     } else {
-      const uint2 w = *reinterpret_cast<const uint2*>(q);
+      const u32x2_any_t w = *reinterpret_cast<const u32x2_any_t*>(q);
       v[0] = __uint_as_float(w.x << 16);
       v[1] = __uint_as_float(w.x & 0xFFFF0000u);
       v[2] = __uint_as_float(w.y << 16);
@@ -77,32 +86,75 @@ __device__ __forceinline__ void ld_vec(const void* p, int64_t i, int dt, float* 
     }
   }
 }
+__device__ __forceinline__ void st16_any(void* p, const uint4& v) {
+  *static_cast<u32x4_any_t*>(p) = u32x4_t{v.x, v.y, v.z, v.w};
+}
 template <int C>
 __device__ __forceinline__ void st_vec(void* p, int64_t i, int dt, const float* v) {
   if (dt == DT_F32) {
     float* q = static_cast<float*>(p) + i;
 #pragma unroll
-    for (int c = 0; c < C; c += 4) st16(q + c, pack(v + c, float{}));
+    for (int c = 0; c < C; c += 4) st16_any(q + c, pack(v + c, float{}));
   } else {
     uint16_t* q = static_cast<uint16_t*>(p) + i;
-    if constexpr (C == 8)
-      st16(q, pack(v, bf16_t{}));
-    else
-      *reinterpret_cast<uint2*>(q) = make_uint2(bf16_pair(v[0], v[1]), bf16_pair(v[2], v[3]));
+    if constexpr (C == 8) {
+      st16_any(q, pack(v, bf16_t{}));
+    } else {
+      u32x2_any_t w;
+      w.x = bf16_pair(v[0], v[1]);
+      w.y = bf16_pair(v[2], v[3]);
+      *reinterpret_cast<u32x2_any_t*>(q) = w;
+    }
   }
 }
 
-// C neighbouring sums of row m from column n on: bias, pre-activation out,
-// activation, residual, result.  g.vec: every row of y, pre and r starts on 16 bytes.
+// The residual of C neighbouring columns as it lies in memory, fetched before
+// it is needed (where all of them are inside the row).
 template <int C>
-__device__ __forceinline__ void finish(const Linear& g, int64_t m, int n, float* v) {
-  if (n >= g.N) return;
-  const bool whole = g.vec && n + C <= g.N;
-  const int cnt = min(C, g.N - n);
-  if (g.bias) {
+struct Residual {
+  uint4 w[C / 4];  // C fp32, or C bf16 in the first
+};
+template <int C>
+__device__ __forceinline__ Residual<C> fetch(const Linear& g, int64_t m, int n) {
+  Residual<C> r;
+  if (g.res && n + C <= g.N) {
+    const int64_t at = m * g.ldr + n;
+    if (g.out_dt == DT_F32) {
 #pragma unroll
-    for (int c = 0; c < C; ++c) v[c] += ld_elem(g.bias, min(n + c, g.N - 1), g.bias_dt);
+      for (int i = 0; i < C / 4; ++i)
+        r.w[i] = buf::ld16_any(reinterpret_cast<const uint16_t*>(static_cast<const float*>(g.res) + at + 4 * i));
+    } else if constexpr (C == 8) {
+      r.w[0] = buf::ld16_any(static_cast<const uint16_t*>(g.res) + at);
+    } else {
+      const u32x2_any_t q = *reinterpret_cast<const u32x2_any_t*>(static_cast<const uint16_t*>(g.res) + at);
+      r.w[0] = make_uint4(q.x, q.y, 0, 0);
+    }
   }
+  return r;
+}
+
+// C neighbouring sums of row m from column n on: bias, pre-activation out,
+// activation, residual, result.
+template <int C>
+struct Bias {
+  float v[C];
+};
+template <int C>
+__device__ __forceinline__ Bias<C> bias_at(const Linear& g, int n) {
+  Bias<C> b;
+#pragma unroll
+  for (int c = 0; c < C; ++c) b.v[c] = g.bias ? ld_elem(g.bias, min(n + c, g.N - 1), g.bias_dt) : 0.0f;
+  return b;
+}
+
+template <int C>
+__device__ __forceinline__ void finish(const Linear& g, int64_t m, int n, float* v, const Bias<C>& bias,
+                                       const Residual<C>& ahead) {
+  if (n >= g.N) return;
+  const bool whole = n + C <= g.N;
+  const int cnt = min(C, g.N - n);
+#pragma unroll
+  for (int c = 0; c < C; ++c) v[c] += bias.v[c];
   if (g.pre) {
     if (whole) {
       st_vec<C>(g.pre, m * g.ldp + n, DT_BF16, v);
@@ -116,17 +168,20 @@ __device__ __forceinline__ void finish(const Linear& g, int64_t m, int n, float*
 #pragma unroll
     for (int c = 0; c < C; ++c) v[c] = act_of(v[c], g.act);
   }
-  if (g.res) {
-    if (whole) {
-      float r[C];
-      ld_vec<C>(g.res, m * g.ldr + n, g.out_dt, r);
+  if (g.res && whole) {
+    float r[8];
+    if (g.out_dt == DT_F32) {
 #pragma unroll
-      for (int c = 0; c < C; ++c) v[c] += r[c];
+      for (int i = 0; i < C / 4; ++i) unpack(ahead.w[i], r + 4 * i, float{});
     } else {
-#pragma unroll
-      for (int c = 0; c < C; ++c)
-        if (c < cnt) v[c] += ld_elem(g.res, m * g.ldr + n + c, g.out_dt);
+      unpack(ahead.w[0], r, bf16_t{});
     }
+#pragma unroll
+    for (int c = 0; c < C; ++c) v[c] += r[c];
+  } else if (g.res) {
+#pragma unroll
+    for (int c = 0; c < C; ++c)
+      if (c < cnt) v[c] += ld_elem(g.res, m * g.ldr + n + c, g.out_dt);
   }
   if (whole) {
     st_vec<C>(g.y, m * g.ldy + n, g.out_dt, v);
@@ -139,27 +194,37 @@ __device__ __forceinline__ void finish(const Linear& g, int64_t m, int n, float*
 
 // ---------------------------------------------------------------- tiles
 // One tile of C over one share of K; with several shares the fp32 sums go to
-// g.part [shares][M][ldpart] and finish_kernel adds them.
-template <class TL, bool AK, bool BK>
-__global__ __launch_bounds__(TL::THREADS) void linear_tile_kernel(Linear g) {
-  constexpr int kLds = TL::MAIN_LDS > buf::Epilogue<TL>::kBytes ? TL::MAIN_LDS : buf::Epilogue<TL>::kBytes;
-  __shared__ __attribute__((aligned(1024))) char lds[kLds];
-  const int t = xcd_order(blockIdx.x, gridDim.x);
+// g.part [shares][M][ldpart] and linear_finish_kernel adds them.  t: tile and share.
+// kRegs: operands of any alignment, by way of registers.
+template <class TL, bool kRegs, bool AK, bool BK>
+__device__ __forceinline__ void linear_tile(const Linear& g, int t, char* lds) {
   const int tiles = g.tiles_m * g.tiles_n;
   const int share = t / tiles;
-  if (share >= g.shares) return;
   int mt, nt;
   dense_tile(t - share * tiles, g.tiles_m, g.tiles_n, mt, nt);
   const int m0 = mt * TL::BM, n0 = nt * TL::BN;
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-  const int k0 = share * g.share_k, kn = min(g.share_k, g.K - k0);
-  buf::ARows<TL, AK> a;
-  buf::BRows<TL, BK> b;
-  a.init(static_cast<const uint16_t*>(g.x) + (AK ? k0 * g.ldx : k0), m0, (int)g.M, g.ldx, kn, wave, lane);
-  b.init(static_cast<const uint16_t*>(g.w) + (BK ? k0 * g.ldw : k0), n0, g.N, g.ldw, kn, wave, lane);
+  const int k0 = share * g.share_k, kn = min(g.share_k, g.K - k0), ktiles = (kn + TL::BK - 1) / TL::BK;
+  const uint16_t* x = static_cast<const uint16_t*>(g.x) + (AK ? k0 * g.ldx : k0);
+  const uint16_t* w = static_cast<const uint16_t*>(g.w) + (BK ? k0 * g.ldw : k0);
   Acc<TL> acc;
   acc.zero();
-  buf::mainloop<TL, AK, BK, false>(a, b, (kn + 63) / 64, lds, acc);
+  if constexpr (kRegs) {
+    buf::ARegs<TL, AK> a;
+    buf::BRegs<TL, BK> b;
+    a.init(x, m0, (int)g.M, g.ldx, kn, wave, lane);
+    b.init(w, n0, g.N, g.ldw, kn, wave, lane);
+    buf::mainloop_regs<TL, AK, BK, false>(a, b, ktiles, lds, acc);
+  } else {
+    buf::ARows<TL, AK> a;
+    buf::BRows<TL, BK> b;
+    a.init(x, m0, (int)g.M, g.ldx, kn, wave, lane);
+    b.init(w, n0, g.N, g.ldw, kn, wave, lane);
+    if constexpr (TL::NS == 2)
+      buf::mainloop<TL, AK, BK, false>(a, b, ktiles, lds, acc);
+    else
+      buf::mainloop_pipe<TL, AK, BK, false>(a, b, ktiles, lds, acc);
+  }
   const int rows = min((int)g.M - m0, TL::BM);
   if (g.shares > 1) {
     float* part = g.part + (int64_t)share * g.M * g.ldpart;
@@ -167,17 +232,69 @@ __global__ __launch_bounds__(TL::THREADS) void linear_tile_kernel(Linear g) {
       if (n0 + c < g.N) st_vec<8>(part, (int64_t)(m0 + r) * g.ldpart + n0 + c, DT_F32, v);
     });
   } else {
-    buf::Epilogue<TL>::run(acc, lds, rows, [&](int r, int c, float* v) { finish<8>(g, m0 + r, n0 + c, v); });
+    // a lane's columns are the same in every row
+    const Bias<8> bias = bias_at<8>(g, n0 + buf::Epilogue<TL>::column());
+    buf::Epilogue<TL>::template run<Residual<8>>(
+        acc, lds, rows, [&](int r, int c) { return fetch<8>(g, m0 + r, n0 + c); },
+        [&](int r, int c, float* v, const Residual<8>& x) { finish<8>(g, m0 + r, n0 + c, v, bias, x); });
   }
 }
 
+template <class TL>
+constexpr int tile_lds() {
+  return TL::MAIN_LDS > buf::Epilogue<TL>::kBytes ? TL::MAIN_LDS : buf::Epilogue<TL>::kBytes;
+}
+
+template <class TL, bool kRegs>
+__global__ __launch_bounds__(TL::THREADS) void linear_tile_kernel(Linear g) {
+  __shared__ __attribute__((aligned(1024))) char lds[tile_lds<TL>()];
+  const int t = xcd_order(blockIdx.x, gridDim.x);
+  if (t < g.tiles_m * g.tiles_n * g.shares) linear_tile<TL, kRegs, false, false>(g, t, lds);
+}
+
+// db[n] = sum of part[.][n], in order within each of the workgroup's row lanes
+__device__ __forceinline__ void bias_sums(const LinearGrads& p, int block, float* red) {
+  const int c = threadIdx.x & 63, r = threadIdx.x >> 6, lanes = blockDim.x >> 6;
+  const int n = block * 64 + c;
+  float s = 0.0f;
+  if (n < p.N) {
+#pragma unroll 4
+    for (int64_t b = r; b < p.sum_blocks; b += lanes) s += p.sums[b * p.N + n];
+  }
+  red[r * 64 + c] = s;
+  __syncthreads();
+  if (r != 0 || n >= p.N) return;
+  for (int i = 1; i < lanes; ++i) s += red[i * 64 + c];
+  p.db[n] = s;
+}
+
+// dw (both operands K-major, the longer K mostly: first), dx (W K-major), db.
+template <class TL, bool kRegs>
+__global__ __launch_bounds__(TL::THREADS) void linear_grads_kernel(LinearGrads p) {
+  __shared__ __attribute__((aligned(1024))) char lds[tile_lds<TL>()];
+  int b = blockIdx.x;
+  if (b < p.grid_dw) {
+    const int t = xcd_order(b, p.grid_dw);
+    if (t < p.dw.tiles_m * p.dw.tiles_n * p.dw.shares) linear_tile<TL, kRegs, true, true>(p.dw, t, lds);
+    return;
+  }
+  b -= p.grid_dw;
+  if (b < p.grid_dx) {
+    const int t = xcd_order(b, p.grid_dx);
+    if (t < p.dx.tiles_m * p.dx.tiles_n * p.dx.shares) linear_tile<TL, kRegs, false, true>(p.dx, t, lds);
+    return;
+  }
+  bias_sums(p, b - p.grid_dx, reinterpret_cast<float*>(lds));
+}
+
 // Sums of the shares, in their order, then the epilogue: 8 columns a thread.
-__global__ __launch_bounds__(256) void linear_finish_kernel(Linear g) {
+__device__ __forceinline__ void finish_at(const Linear& g, int64_t i) {
   const int64_t chunks = g.ldpart / 8;
-  const int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x;
-  if (i >= g.M * chunks) return;
+  if (g.shares < 2 || i >= g.M * chunks) return;
   const int64_t m = i / chunks;
   const int n = (int)(i - m * chunks) * 8;
+  const Residual<8> ahead = fetch<8>(g, m, n);
+  const Bias<8> bias = bias_at<8>(g, n);
   float v[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
   for (int s = 0; s < g.shares; ++s) {
     float u[8];
@@ -185,30 +302,23 @@ __global__ __launch_bounds__(256) void linear_finish_kernel(Linear g) {
 #pragma unroll
     for (int c = 0; c < 8; ++c) v[c] += u[c];
   }
-  finish<8>(g, m, n, v);
+  finish<8>(g, m, n, v, bias, ahead);
+}
+__global__ __launch_bounds__(256) void linear_finish_kernel(Linear g) {
+  finish_at(g, (int64_t)blockIdx.x * 256 + threadIdx.x);
+}
+__global__ __launch_bounds__(256) void linear_grads_finish_kernel(LinearGrads p, int first) {
+  if ((int)blockIdx.x < first)
+    finish_at(p.dw, (int64_t)blockIdx.x * 256 + threadIdx.x);
+  else
+    finish_at(p.dx, (int64_t)(blockIdx.x - first) * 256 + threadIdx.x);
 }
 
 // ------------------------------------------------------------- few rows
 constexpr int kSkinnyWaves = 4;
 constexpr int kSkinnyRows = 64;
-
-typedef u32x4_t u32x4_any_t __attribute__((aligned(2)));
-// 16 bytes at any even address
-__device__ __forceinline__ uint4 ld16_any(const uint16_t* p) {
-  const u32x4_t v = *reinterpret_cast<const u32x4_any_t*>(p);
-  return make_uint4(v.x, v.y, v.z, v.w);
-}
-// 8 values from k on, zeros from K on
-__device__ __forceinline__ uint4 ld8_until(const uint16_t* row, int k, int K) {
-  if (k + 8 <= K) return ld16_any(row + k);
-  uint32_t w[4];
-#pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    const uint32_t lo = k + 2 * i < K ? row[k + 2 * i] : 0, hi = k + 2 * i + 1 < K ? row[k + 2 * i + 1] : 0;
-    w[i] = lo | hi << 16;
-  }
-  return make_uint4(w[0], w[1], w[2], w[3]);
-}
+using buf::ld16_any;
+using buf::ld8_until;
 
 // MB blocks of 16 rows of x by 16 rows of W.  The weights are the first
 // operand, so a lane ends with 4 neighbouring columns of row lane & 15.
@@ -225,66 +335,65 @@ __global__ __launch_bounds__(64 * kSkinnyWaves) void linear_skinny_kernel(Linear
     const int64_t m = b * 16 + (lane & 15);
     x[b] = static_cast<const uint16_t*>(g.x) + (m < g.M ? m : g.M - 1) * g.ldx;
   }
-  f32x4_t acc[MB];
+  // row block b is finished by wavefront b: what it reads is on its way before
+  // the product starts
+  const int n = n0 + (lane >> 4) * 4;
+  const Bias<4> bias = bias_at<4>(g, n);
+  Residual<4> ahead;
+  if (wave < MB && wave * 16 + (lane & 15) < g.M) ahead = fetch<4>(g, wave * 16 + (lane & 15), n);
+  f32x4_t acc[1][MB];
 #pragma unroll
-  for (int b = 0; b < MB; ++b) acc[b] = f32x4_t{0.f, 0.f, 0.f, 0.f};
-  auto step = [&](const uint4& a, const uint4& v, f32x4_t c) {
-    return __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8_t, a), __builtin_bit_cast(bf16x8_t, v), c,
-                                                   0, 0, 0);
-  };
-  const int whole = g.K & ~127;
-#pragma unroll 2
-  for (int k = wave * 128; k < whole; k += kSkinnyWaves * 128) {
-    uint4 a[4], v[MB][4];
-#pragma unroll
-    for (int i = 0; i < 4; ++i) a[i] = ld16_any(w + k + 32 * i + at);
-#pragma unroll
-    for (int b = 0; b < MB; ++b)
-#pragma unroll
-      for (int i = 0; i < 4; ++i) v[b][i] = ld16_any(x[b] + k + 32 * i + at);
-#pragma unroll
-    for (int i = 0; i < 4; ++i)
-#pragma unroll
-      for (int b = 0; b < MB; ++b) acc[b] = step(a[i], v[b][i], acc[b]);
-  }
-  // fewer than 128 values of K are left: a block of 32 a wavefront
+  for (int b = 0; b < MB; ++b) acc[0][b] = f32x4_t{0.f, 0.f, 0.f, 0.f};
   {
-    const int k = whole + wave * 32;
+    const uint16_t* w1[1] = {w + at};
+    const uint16_t* xs[MB];
+#pragma unroll
+    for (int b = 0; b < MB; ++b) xs[b] = x[b] + at;
+    stream<kSkinnyWaves, 1, MB, false>(w1, xs, g.K / 64, acc, [](const uint16_t* p) { return ld16_any(p); });
+  }
+  // fewer than 64 values of K are left: 32 for each of the last two wavefronts
+  {
+    const int k = (g.K & ~63) + (kSkinnyWaves - 1 - wave) * 32;
     if (k < g.K) {
       const uint4 a = ld8_until(w, k + at, g.K);
 #pragma unroll
-      for (int b = 0; b < MB; ++b) acc[b] = step(a, ld8_until(x[b], k + at, g.K), acc[b]);
+      for (int b = 0; b < MB; ++b) acc[0][b] = mfma_bf16(a, ld8_until(x[b], k + at, g.K), acc[0][b]);
     }
   }
 #pragma unroll
-  for (int b = 0; b < MB; ++b) part[wave][b][lane] = acc[b];
+  for (int b = 0; b < MB; ++b) part[wave][b][lane] = acc[0][b];
   __syncthreads();
-  for (int b = wave; b < MB; b += kSkinnyWaves) {
+  if (wave < MB) {
+    const int b = wave;
     f32x4_t s = part[0][b][lane];
 #pragma unroll
     for (int j = 1; j < kSkinnyWaves; ++j) s += part[j][b][lane];
     const int m = b * 16 + (lane & 15);
     float v[4] = {s[0], s[1], s[2], s[3]};
-    if (m < g.M) finish<4>(g, m, n0 + (lane >> 4) * 4, v);
+    if (m < g.M) finish<4>(g, m, n, v, bias, ahead);
   }
 }
-static_assert(kSkinnyWaves * 32 == 128, "the rest of K is one block of 32 a wavefront");
+static_assert(kSkinnyWaves >= 2 && kSkinnyWaves * 16 >= kSkinnyRows, "the rest of K goes to two wavefronts; one wavefront a row block");
 
 // -------------------------------------------------------- copies, slopes
 // Rows [rows][cols] into rows of ldd (a multiple of 8), zeros past cols.
-__global__ __launch_bounds__(256) void pack_rows_kernel(const uint16_t* __restrict__ src, int64_t rows, int cols,
-                                                        int64_t lds, uint16_t* __restrict__ dst, int64_t ldd) {
-  const int64_t chunks = ldd / 8;
-  const int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x;
-  if (i >= rows * chunks) return;
+__device__ __forceinline__ void pack_at(const PackRows& p, int64_t i) {
+  const int64_t chunks = p.ldd / 8;
+  if (i >= p.rows * chunks) return;
   const int64_t r = i / chunks;
   const int c = (int)(i - r * chunks) * 8;
-  st16(dst + r * ldd + c, ld8_until(src + r * lds, c, cols));
+  st16(static_cast<uint16_t*>(p.dst) + r * p.ldd + c, ld8_until(static_cast<const uint16_t*>(p.src) + r * p.ld, c, p.cols));
+}
+__global__ __launch_bounds__(256) void pack_rows_kernel(PackRows a, PackRows b, unsigned first) {
+  if (blockIdx.x < first)
+    pack_at(a, (int64_t)blockIdx.x * 256 + threadIdx.x);
+  else
+    pack_at(b, (int64_t)(blockIdx.x - first) * 256 + threadIdx.x);
 }
 
 // d = dy act'(pre) as bf16 rows of ldd (zeros past N), and sums of d (before
 // its rounding) over the rows of each block of kSlopeRows: part [blocks][N].
-constexpr int kSlopeRows = 64;
+constexpr int kSlopeRows = 32;
 struct Slope {
   const void* dy;
   int64_t ldy;
@@ -297,7 +406,6 @@ struct Slope {
   uint16_t* d;     // null: only the sums
   int64_t ldd;
   float* part;     // null: no sums
-  int vec;         // rows of dy and pre start on 16 bytes
 };
 // 256 threads: 16 chunks of 8 columns x 16 row lanes
 __global__ __launch_bounds__(256) void slope_kernel(Slope p) {
@@ -306,7 +414,7 @@ __global__ __launch_bounds__(256) void slope_kernel(Slope p) {
   const int n = (blockIdx.x * 16 + cx) * 8;
   const int64_t r0 = (int64_t)blockIdx.y * kSlopeRows;
   float sum[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
-  const bool whole = p.vec && n + 8 <= p.N;
+  const bool whole = n + 8 <= p.N;
 #pragma unroll
   for (int i = 0; i < kSlopeRows / 16; ++i) {
     const int64_t m = r0 + i * 16 + ry;
@@ -344,72 +452,115 @@ __global__ __launch_bounds__(256) void slope_kernel(Slope p) {
   }
 }
 
-// db[n] = sum of part[.][n], in order: 64 columns x 4 interleaved row lanes.
-__global__ __launch_bounds__(256) void bias_grad_kernel(const float* __restrict__ part, int64_t blocks, int N,
-                                                        float* __restrict__ db) {
-  __shared__ float red[4][64];
-  const int c = threadIdx.x & 63, r = threadIdx.x >> 6;
-  const int n = blockIdx.x * 64 + c;
-  float s = 0.0f;
-  if (n < N)
-    for (int64_t b = r; b < blocks; b += 4) s += part[b * N + n];
-  red[r][c] = s;
-  __syncthreads();
-  if (r == 0 && n < N) db[n] = (red[0][c] + red[1][c]) + (red[2][c] + red[3][c]);
-}
-
 unsigned grid8(int64_t n) { return (unsigned)((n + 7) & ~int64_t(7)); }
 
-template <class TL, bool AK, bool BK>
-hipError_t launch_tiles(const Linear& g, hipStream_t s) {
-  linear_tile_kernel<TL, AK, BK><<<grid8((int64_t)g.tiles_m * g.tiles_n * g.shares), TL::THREADS, 0, s>>>(g);
-  return hipGetLastError();
+int tile_side(int cls) { return cls == TILE_BIG ? 256 : cls == TILE_SMALL ? 128 : 64; }
+
+int slots_of(int cls) { return cls == TILE_BIG ? 256 : 512; }
+
+// Microseconds of one K tile of a workgroup, as measured with every slot taken.
+double k_tile_us(int cls) { return cls == TILE_BIG ? 1.6 : cls == TILE_SMALL ? 0.9 : 0.35; }
+
+void set_tiles(Linear& g, const LinearPlan& p) {
+  const int side = tile_side(p.cls);
+  g.tiles_m = (int)cdiv64(g.M, side);
+  g.tiles_n = (int)cdiv64(g.N, side);
+  g.shares = p.shares;
+  g.share_k = p.share_k;
+  g.ldpart = (g.N + 7) & ~7;
 }
+
+unsigned finish_grid(const Linear& g) { return g.shares > 1 ? (unsigned)cdiv64(g.M * (g.ldpart / 8), 256) : 0; }
 
 }  // namespace
 
 bool linear_skinny(int64_t M) { return M <= kSkinnyRows; }
 
-// Tile and shares of K.  A big tile keeps a CU busy by itself, two small ones
-// share one; the K of few tiles is shared so that every CU has work, with at
-// least 4 K tiles a share.
-LinearPlan linear_plan(int64_t M, int64_t N, int64_t K) {
+// The largest tile of which there are enough for the chip: 192 big ones keep
+// three quarters of the CUs busy, 256 of the middle size all of them.
+int linear_class(int64_t M0, int64_t N0, int64_t M1, int64_t N1) {
+  auto tiles = [&](int64_t side) { return cdiv64(M0, side) * cdiv64(N0, side) + cdiv64(M1, side) * cdiv64(N1, side); };
+  return tiles(256) >= 192 ? TILE_BIG : tiles(128) >= 256 ? TILE_SMALL : TILE_DEEP;
+}
+
+double linear_units(int cls, int64_t M, int64_t N, int64_t K) {
+  return (double)cdiv64(M, tile_side(cls)) * (double)cdiv64(N, tile_side(cls)) * (double)cdiv64(K, 64);
+}
+
+// Shares of K: the number with which the product's own rounds of the chip, and
+// the launch that joins the shares (about 4 us and their sums' way through
+// memory), take the least time.  Only K longer than an even part of all the K
+// tiles of the launch (`units`) is looked at.
+LinearPlan linear_plan(int cls, int64_t M, int64_t N, int64_t K, double units) {
   LinearPlan p{};
-  const int64_t big = cdiv64(M, 256) * cdiv64(N, 256), small = cdiv64(M, 128) * cdiv64(N, 128);
-  p.big = big >= 192;
+  p.cls = cls;
+  const int64_t kt = cdiv64(K, 64), slots = slots_of(cls);
+  const int64_t tiles = cdiv64(M, tile_side(cls)) * cdiv64(N, tile_side(cls));
+  const double sums = (double)M * (double)N * 8.0 / 5.0e6;  // us to write and read one share's sums
   p.shares = 1;
-  if (!p.big) {
-    const int64_t kt = cdiv64(K, 64);
-    int64_t want = 512 / small;
-    if (want > kt / 4) want = kt / 4;
-    if (want > 1) p.shares = (int)want;
+  if (kt > 8 && (double)kt > units / (double)slots) {
+    double best = (double)(cdiv64(tiles, slots) * kt) * k_tile_us(cls);
+    for (int64_t s = 2; s <= kt / 4 && s <= 64; ++s) {
+      const double t = (double)(cdiv64(tiles * s, slots) * cdiv64(kt, s)) * k_tile_us(cls) + 4.0 + sums * (double)s;
+      if (t < 0.95 * best) {
+        best = t;
+        p.shares = (int)s;
+      }
+    }
   }
-  p.share_k = (int)(cdiv64(cdiv64(K, 64), p.shares) * 64);
-  p.shares = (int)cdiv64(K > 0 ? K : 1, p.share_k > 0 ? p.share_k : 1);
-  if (p.share_k < 1) p.share_k = 64;
+  const int64_t each = kt > 0 ? cdiv64(kt, p.shares) : 1;
+  p.share_k = (int)(each * 64);
+  p.shares = kt > 0 ? (int)cdiv64(kt, each) : 1;
   p.part_bytes = p.shares > 1 ? (int64_t)p.shares * M * ((N + 7) & ~int64_t(7)) * 4 : 0;
   return p;
 }
 
-hipError_t launch_linear_tiles(const Linear& in, bool a_kmajor, bool b_kmajor, hipStream_t s) {
+hipError_t launch_linear_tiles(const Linear& in, const LinearPlan& p, bool regs, hipStream_t s) {
   if (in.M <= 0 || in.N <= 0) return hipSuccess;
   Linear g = in;
-  const LinearPlan p = linear_plan(g.M, g.N, g.K);
-  const int bm = p.big ? 256 : 128;
-  g.tiles_m = (int)cdiv64(g.M, bm);
-  g.tiles_n = (int)cdiv64(g.N, bm);
-  g.shares = p.shares;
-  g.share_k = p.share_k;
-  g.ldpart = (g.N + 7) & ~int64_t(7);
-  hipError_t e;
-  if (p.big)
-    e = a_kmajor ? launch_tiles<BigTile, true, true>(g, s)
-        : b_kmajor ? launch_tiles<BigTile, false, true>(g, s) : launch_tiles<BigTile, false, false>(g, s);
+  set_tiles(g, p);
+  const unsigned grid = grid8((int64_t)g.tiles_m * g.tiles_n * g.shares);
+  if (p.cls == TILE_BIG)
+    linear_tile_kernel<BigTile, false><<<grid, BigTile::THREADS, 0, s>>>(g);
+  else if (p.cls == TILE_SMALL)
+    linear_tile_kernel<SmallTile, false><<<grid, SmallTile::THREADS, 0, s>>>(g);
+  else if (!regs)
+    linear_tile_kernel<DeepTile, false><<<grid, DeepTile::THREADS, 0, s>>>(g);
   else
-    e = a_kmajor ? launch_tiles<SmallTile, true, true>(g, s)
-        : b_kmajor ? launch_tiles<SmallTile, false, true>(g, s) : launch_tiles<SmallTile, false, false>(g, s);
+    linear_tile_kernel<DeepTile, true><<<grid, DeepTile::THREADS, 0, s>>>(g);
+  const hipError_t e = hipGetLastError();
   if (e != hipSuccess || g.shares == 1) return e;
-  linear_finish_kernel<<<(unsigned)cdiv64(g.M * (g.ldpart / 8), 256), 256, 0, s>>>(g);
+  linear_finish_kernel<<<finish_grid(g), 256, 0, s>>>(g);
+  return hipGetLastError();
+}
+
+hipError_t launch_linear_grads(const LinearGrads& in, const LinearPlan& pw, const LinearPlan& px, bool regs,
+                               hipStream_t s) {
+  LinearGrads p = in;
+  auto range = [](Linear& g, const LinearPlan& q) {
+    if (g.M <= 0 || g.N <= 0 || !g.y) {
+      g.shares = 1;
+      return 0;
+    }
+    set_tiles(g, q);
+    return (int)grid8((int64_t)g.tiles_m * g.tiles_n * g.shares);
+  };
+  p.grid_dw = range(p.dw, pw);
+  p.grid_dx = range(p.dx, px);
+  const unsigned grid = (unsigned)(p.grid_dw + p.grid_dx + (p.db ? cdiv64(p.N, 64) : 0));
+  if (grid == 0) return hipSuccess;
+  if (pw.cls == TILE_BIG)
+    linear_grads_kernel<BigTile, false><<<grid, BigTile::THREADS, 0, s>>>(p);
+  else if (pw.cls == TILE_SMALL)
+    linear_grads_kernel<SmallTile, false><<<grid, SmallTile::THREADS, 0, s>>>(p);
+  else if (!regs)
+    linear_grads_kernel<DeepTile, false><<<grid, DeepTile::THREADS, 0, s>>>(p);
+  else
+    linear_grads_kernel<DeepTile, true><<<grid, DeepTile::THREADS, 0, s>>>(p);
+  const hipError_t e = hipGetLastError();
+  const unsigned fw = p.grid_dw ? finish_grid(p.dw) : 0, fx = p.grid_dx ? finish_grid(p.dx) : 0;
+  if (e != hipSuccess || fw + fx == 0) return e;
+  linear_grads_finish_kernel<<<fw + fx, 256, 0, s>>>(p, (int)fw);
   return hipGetLastError();
 }
 
@@ -425,41 +576,32 @@ hipError_t launch_linear_skinny(const Linear& g, hipStream_t s) {
   return hipGetLastError();
 }
 
-hipError_t launch_pack_rows(const void* src, int64_t rows, int cols, int64_t ld, void* dst, int64_t ldd,
-                            hipStream_t s) {
-  if (rows <= 0 || ldd <= 0) return hipSuccess;
-  pack_rows_kernel<<<(unsigned)cdiv64(rows * (ldd / 8), 256), 256, 0, s>>>(
-      static_cast<const uint16_t*>(src), rows, cols, ld, static_cast<uint16_t*>(dst), ldd);
+hipError_t launch_pack_rows(const PackRows& a, const PackRows& b, hipStream_t s) {
+  auto blocks = [](const PackRows& p) { return p.dst ? (unsigned)cdiv64(p.rows * (p.ldd / 8), 256) : 0u; };
+  const unsigned first = blocks(a), second = blocks(b);
+  if (first + second == 0) return hipSuccess;
+  pack_rows_kernel<<<first + second, 256, 0, s>>>(a, b, first);
   return hipGetLastError();
 }
 
 int64_t slope_blocks(int64_t M) { return cdiv64(M, kSlopeRows); }
 
 hipError_t launch_slope(const void* dy, int64_t ldy, int dy_dt, const void* pre, int64_t ldp, int act, int64_t M,
-                        int N, void* d, int64_t ldd, float* part, float* db, hipStream_t s) {
-  if (N <= 0) return hipSuccess;
-  auto on16 = [](const void* p, int64_t ld, int64_t size) {
-    return reinterpret_cast<uintptr_t>(p) % 16 == 0 && ld * size % 16 == 0;
-  };
-  if (M > 0) {
-    Slope p{};
-    p.dy = dy;
-    p.ldy = ldy;
-    p.dy_dt = dy_dt;
-    p.pre = static_cast<const uint16_t*>(pre);
-    p.ldp = ldp;
-    p.act = act;
-    p.M = M;
-    p.N = N;
-    p.d = static_cast<uint16_t*>(d);
-    p.ldd = ldd;
-    p.part = part;
-    p.vec = on16(dy, ldy, dy_dt == DT_F32 ? 4 : 2) && (act == ACT_NONE || on16(pre, ldp, 2));
-    slope_kernel<<<dim3((unsigned)cdiv64(N, 128), (unsigned)slope_blocks(M)), 256, 0, s>>>(p);
-    const hipError_t e = hipGetLastError();
-    if (e != hipSuccess) return e;
-  }
-  if (db) bias_grad_kernel<<<(unsigned)cdiv64(N, 64), 256, 0, s>>>(part, M > 0 ? slope_blocks(M) : 0, N, db);
+                        int N, void* d, int64_t ldd, float* part, hipStream_t s) {
+  if (N <= 0 || M <= 0) return hipSuccess;
+  Slope p{};
+  p.dy = dy;
+  p.ldy = ldy;
+  p.dy_dt = dy_dt;
+  p.pre = static_cast<const uint16_t*>(pre);
+  p.ldp = ldp;
+  p.act = act;
+  p.M = M;
+  p.N = N;
+  p.d = static_cast<uint16_t*>(d);
+  p.ldd = ldd;
+  p.part = part;
+  slope_kernel<<<dim3((unsigned)cdiv64(N, 128), (unsigned)slope_blocks(M)), 256, 0, s>>>(p);
   return hipGetLastError();
 }
 

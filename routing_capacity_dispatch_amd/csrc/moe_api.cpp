@@ -2007,7 +2007,7 @@ namespace {
 
 constexpr int64_t kMaxLd = int64_t(1) << 22;  // 256 rows of 2 bytes stay below 2^31
 constexpr int64_t kMaxLinearRows = int64_t(1) << 30;
-constexpr int64_t kMaxSlopeRows = 65535 * 64;  // one grid row for 64 rows of d
+constexpr int64_t kMaxSlopeRows = 65535 * 32;  // one grid row for 32 rows of d
 
 int64_t align8(int64_t x) { return (x + 7) & ~int64_t(7); }
 
@@ -2050,19 +2050,27 @@ moe_status check_linear(const moe_linear_args* a) {
 }
 
 struct LinearWs {
-  void* x;  // copies in whole 16 bytes, or null
+  moe::LinearPlan plan;
+  bool regs;  // the operands are taken as they lie, by way of registers
+  void* x;    // copies in whole 16 bytes, or null
   void* w;
   void* part;
 };
 int64_t carve_linear(const moe_linear_args* a, void* ws, LinearWs* w) {
   Carver cv{static_cast<char*>(ws), 0};
   *w = LinearWs{};
-  if (moe::linear_skinny(a->M) || a->N == 0 || a->K == 0) return 0;
+  if (moe::linear_skinny(a->M) || a->N == 0) return 0;
   const int64_t K8 = align8(a->K);
-  if (!tile_rows(a->x, a->ldx) || a->K % 8) w->x = cv.take(a->M * K8 * 2);
-  if (!tile_rows(a->w, a->ldw) || a->K % 8) w->w = cv.take(a->N * K8 * 2);
-  const int64_t part = moe::linear_plan(a->M, a->N, K8).part_bytes;
-  if (part) w->part = cv.take(part);
+  const int cls = moe::linear_class(a->M, a->N, 0, 0);
+  w->plan = moe::linear_plan(cls, a->M, a->N, K8, moe::linear_units(cls, a->M, a->N, K8));
+  const bool whole = a->K % 8 == 0, x = whole && tile_rows(a->x, a->ldx), y = whole && tile_rows(a->w, a->ldw);
+  if (cls == moe::TILE_DEEP) {
+    w->regs = !(x && y);
+  } else if (a->K > 0) {
+    if (!x) w->x = cv.take(a->M * K8 * 2);
+    if (!y) w->w = cv.take(a->N * K8 * 2);
+  }
+  if (w->plan.part_bytes) w->part = cv.take(w->plan.part_bytes);
   return cv.used;
 }
 
@@ -2106,26 +2114,21 @@ MOE_API moe_status moe_linear(const moe_linear_args* args, void* ws, size_t ws_b
   g.pre = a.pre;
   g.ldp = a.ldp;
   g.act = a.act;
-  const int64_t per16 = a.out_dtype == MOE_F32 ? 4 : 8;
-  g.vec = aligned16(a.y) && a.ldy % per16 == 0 && (!a.residual || (aligned16(a.residual) && a.ldr % per16 == 0)) &&
-          (!a.pre || (aligned16(a.pre) && a.ldp % 8 == 0));
   if (moe::linear_skinny(a.M)) return hip_status(moe::launch_linear_skinny(g, s));
   const int64_t K8 = align8(a.K);
-  hipError_t e = hipSuccess;
+  const moe::PackRows px{a.x, a.M, g.K, a.ldx, w.x, K8}, pw{a.w, a.N, g.K, a.ldw, w.w, K8};
+  const hipError_t e = moe::launch_pack_rows(px, pw, s);
+  if (e != hipSuccess) return MOE_ERR_HIP;
   if (w.x) {
-    e = moe::launch_pack_rows(a.x, a.M, g.K, a.ldx, w.x, K8, s);
     g.x = w.x;
     g.ldx = K8;
   }
-  if (e == hipSuccess && w.w) {
-    e = moe::launch_pack_rows(a.w, a.N, g.K, a.ldw, w.w, K8, s);
+  if (w.w) {
     g.w = w.w;
     g.ldw = K8;
   }
-  g.K = (int)K8;
   g.part = static_cast<float*>(w.part);
-  if (e == hipSuccess) e = moe::launch_linear_tiles(g, false, false, s);
-  return hip_status(e);
+  return hip_status(moe::launch_linear_tiles(g, w.plan, w.regs, s));
 }
 
 namespace {
@@ -2149,31 +2152,40 @@ moe_status check_linear_grad(const moe_linear_grad* a) {
 }
 
 struct LinearGradWs {
+  moe::LinearPlan dw, dx;
+  bool regs;    // x and w are taken as they lie, by way of registers
   void* d;      // bf16 [M][N rounded up to 8], or null: dy itself
   float* sums;  // partial sums of db
   void* x;      // copies in whole 16 bytes, or null
   void* w;
-  void* part;
+  void* part_dw;
+  void* part_dx;
 };
 int64_t carve_linear_grad(const moe_linear_grad* a, void* ws, LinearGradWs* w) {
   Carver cv{static_cast<char*>(ws), 0};
   *w = LinearGradWs{};
   const int64_t N8 = align8(a->N), K8 = align8(a->K);
-  const bool products = (a->dx || a->dw) && a->M > 0 && a->N > 0 && a->K > 0;
+  const bool dx = a->dx != nullptr, dw = a->dw != nullptr;
+  const int cls = moe::linear_class(dw ? a->N : 0, a->K, dx ? a->M : 0, a->K);
+  const double units = (dw ? moe::linear_units(cls, a->N, a->K, a->M) : 0.0) +
+                       (dx ? moe::linear_units(cls, a->M, a->K, a->N) : 0.0);
+  w->dw = moe::linear_plan(cls, a->N, a->K, a->M, units);
+  w->dx = moe::linear_plan(cls, a->M, a->K, a->N, units);
+  const bool products = (dx || dw) && a->M > 0 && a->N > 0 && a->K > 0;
   // dy as it is serves as d where no slope and no rounding is due
   const bool own = a->act == MOE_ACT_NONE && a->dy_dtype == MOE_BF16 && tile_rows(a->dy, a->lddy) &&
-                   (!a->dx || a->N % 8 == 0);
+                   (!dx || a->N % 8 == 0);
   if (products && !own) w->d = cv.take(a->M * N8 * 2);
   if (a->db && a->M > 0) w->sums = static_cast<float*>(cv.take(moe::slope_blocks(a->M) * a->N * 4));
-  if (products && a->dw && !tile_rows(a->x, a->ldx)) w->x = cv.take(a->M * K8 * 2);
-  if (products && a->dx && !tile_rows(a->w, a->ldw)) w->w = cv.take(a->N * K8 * 2);
-  int64_t part = 0;
-  if (a->dx) part = moe::linear_plan(a->M, a->K, N8).part_bytes;
-  if (a->dw) {
-    const int64_t q = moe::linear_plan(a->N, a->K, a->M).part_bytes;
-    part = q > part ? q : part;
+  const bool x = dw && !tile_rows(a->x, a->ldx), y = dx && !tile_rows(a->w, a->ldw);
+  // by way of registers a k-row has at least 8 values
+  w->regs = cls == moe::TILE_DEEP && (x || y) && (!dw || a->ldx >= 8) && (!dx || a->ldw >= 8);
+  if (products && !w->regs) {
+    if (x) w->x = cv.take(a->M * K8 * 2);
+    if (y) w->w = cv.take(a->N * K8 * 2);
   }
-  if (products && part) w->part = cv.take(part);
+  if (dw && w->dw.part_bytes) w->part_dw = cv.take(w->dw.part_bytes);
+  if (dx && w->dx.part_bytes) w->part_dx = cv.take(w->dx.part_bytes);
   return cv.used;
 }
 
@@ -2203,50 +2215,47 @@ MOE_API moe_status moe_linear_backward(const moe_linear_grad* args, void* ws, si
   hipStream_t s = static_cast<hipStream_t>(stream);
   const int64_t N8 = align8(a.N), K8 = align8(a.K);
   hipError_t e = hipSuccess;
-  if (w.d || a.db)
-    e = moe::launch_slope(a.dy, a.lddy, a.dy_dtype, a.pre, a.ldp, a.act, a.M, (int)a.N, w.d, N8, w.sums, a.db, s);
+  if (w.d || w.sums)
+    e = moe::launch_slope(a.dy, a.lddy, a.dy_dtype, a.pre, a.ldp, a.act, a.M, (int)a.N, w.d, N8, w.sums, s);
+  const moe::PackRows px{a.x, a.M, (int)a.K, a.ldx, w.x, K8}, pw{a.w, a.N, (int)a.K, a.ldw, w.w, K8};
+  if (e == hipSuccess) e = moe::launch_pack_rows(px, pw, s);
+  if (e != hipSuccess) return MOE_ERR_HIP;
   const void* d = w.d ? w.d : a.dy;
   const int64_t ldd = w.d ? N8 : a.lddy;
-  moe::Linear g{};
-  g.part = static_cast<float*>(w.part);
-  g.out_dt = moe::DT_BF16;
-  if (e == hipSuccess && a.dx && a.M > 0 && a.K > 0) {  // d [M][N] by W, K-major along N
-    g.x = d;
-    g.ldx = ldd;
-    g.w = a.w;
-    g.ldw = a.ldw;
-    if (w.w) {
-      e = moe::launch_pack_rows(a.w, a.N, (int)a.K, a.ldw, w.w, K8, s);
-      g.w = w.w;
-      g.ldw = K8;
-    }
-    g.M = a.M;
-    g.N = (int)a.K;
-    g.K = (int)a.N;
-    g.y = a.dx;
-    g.ldy = a.lddx;
-    g.vec = aligned16(a.dx) && a.lddx % 8 == 0;
-    if (e == hipSuccess) e = moe::launch_linear_tiles(g, false, true, s);
+  moe::LinearGrads g{};
+  if (a.dw) {  // d and x, both K-major along M
+    moe::Linear& q = g.dw;
+    q.x = d;
+    q.ldx = ldd;
+    q.w = w.x ? w.x : a.x;
+    q.ldw = w.x ? K8 : a.ldx;
+    q.M = a.N;
+    q.N = (int)a.K;
+    q.K = (int)a.M;
+    q.y = a.dw;
+    q.ldy = a.lddw;
+    q.out_dt = moe::DT_BF16;
+    q.part = static_cast<float*>(w.part_dw);
   }
-  if (e == hipSuccess && a.dw && a.N > 0 && a.K > 0) {  // d and x, both K-major along M
-    g.x = d;
-    g.ldx = ldd;
-    g.w = a.x;
-    g.ldw = a.ldx;
-    if (w.x) {
-      e = moe::launch_pack_rows(a.x, a.M, (int)a.K, a.ldx, w.x, K8, s);
-      g.w = w.x;
-      g.ldw = K8;
-    }
-    g.M = a.N;
-    g.N = (int)a.K;
-    g.K = (int)a.M;
-    g.y = a.dw;
-    g.ldy = a.lddw;
-    g.vec = aligned16(a.dw) && a.lddw % 8 == 0;
-    if (e == hipSuccess) e = moe::launch_linear_tiles(g, true, true, s);
+  if (a.dx) {  // d by W, K-major along N
+    moe::Linear& q = g.dx;
+    q.x = d;
+    q.ldx = ldd;
+    q.w = w.w ? w.w : a.w;
+    q.ldw = w.w ? K8 : a.ldw;
+    q.M = a.M;
+    q.N = (int)a.K;
+    q.K = (int)a.N;
+    q.y = a.dx;
+    q.ldy = a.lddx;
+    q.out_dt = moe::DT_BF16;
+    q.part = static_cast<float*>(w.part_dx);
   }
-  return hip_status(e);
+  g.sums = w.sums;
+  g.sum_blocks = w.sums ? moe::slope_blocks(a.M) : 0;
+  g.N = (int)a.N;
+  g.db = a.db;
+  return hip_status(moe::launch_linear_grads(g, w.dw, w.dx, w.regs, s));
 }
 
 // ------------------------------------------------------------------ orthogonalised updates

@@ -296,9 +296,9 @@ def test_streams_and_graph():
 
 def test_workspace_of_the_caller():
     d = dev()
-    x, w = rand((100, 33), 1).to(d), rand((40, 33), 2).to(d)
+    x, w = rand((100, 4097), 1).to(d), rand((40, 4097), 2).to(d)
     ref = rcd.linear(x, w)
-    ws = torch.full((1 << 16,), 255, dtype=torch.uint8, device=d)
+    ws = torch.full((1 << 18,), 255, dtype=torch.uint8, device=d)
     assert torch.equal(rcd.linear(x, w, ws=ws), ref)
     with pytest.raises(rcd.MoeError, match="WORKSPACE"):
         rcd.linear(x, w, ws=ws[:256])

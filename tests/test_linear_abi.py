@@ -57,9 +57,11 @@ def test_linear_null_and_workspace(lib):
     # nothing to do: no pointer is looked at
     assert lib.moe_linear(C.byref(args(M=0, x=None, w=None, y=None)), None, 0, None) == OK
     assert lib.moe_linear(C.byref(args(N=0, x=None, w=None, y=None)), None, 0, None) == OK
-    # up to 64 rows: none needed; more rows that do not end on 16 bytes: copies
-    for over, some in ((dict(M=64, K=31), False), (dict(M=4096, N=4096, ldy=4096, ldr=4096, ldp=4096), False),
-                       (dict(M=100, K=31), True), (dict(ldx=36), True), (dict(w=FAKE + 2), True)):
+    # few rows or few tiles: none needed; many whose rows do not start or end on 16 bytes: copies; a long K shared: sums
+    big = dict(M=4096, N=4096, ldy=4096, ldr=4096, ldp=4096)
+    for over, some in ((dict(M=64, K=31), False), (dict(M=100, K=31), False), (big, False), (dict(big, K=31), True),
+                       (dict(big, ldx=36), True), (dict(big, w=FAKE + 2), True),
+                       (dict(M=100, K=4096, ldx=4096, ldw=4096), True)):
         a = args(**over)
         assert lib.moe_linear_ws_bytes(C.byref(a), C.byref(n)) == OK and (n.value > 0) == some, over
         if some:
@@ -71,7 +73,7 @@ def test_linear_null_and_workspace(lib):
     (dict(M=-1), INV), (dict(lddy=47), INV), (dict(ldp=47), INV), (dict(ldx=31), INV), (dict(ldw=31), INV),
     (dict(lddx=31), INV), (dict(lddw=31), INV), (dict(act=4), INV), (dict(dy_dtype=2), INV), (dict(reserved=1), INV),
     (dict(dy=FAKE + 1), INV), (dict(pre=FAKE + 1), INV), (dict(dx=FAKE + 1), INV), (dict(db=FAKE + 2), INV),
-    (dict(dy=FAKE + 2, dy_dtype=0), INV), (dict(M=4194241), UNS), (dict(lddy=(1 << 22) + 1), UNS)])
+    (dict(dy=FAKE + 2, dy_dtype=0), INV), (dict(M=2097121), UNS), (dict(lddy=(1 << 22) + 1), UNS)])
 def test_linear_backward_refusals(lib, over, status):
     n = C.c_size_t(0)
     assert lib.moe_linear_backward_ws_bytes(C.byref(grad(**over)), C.byref(n)) == status
