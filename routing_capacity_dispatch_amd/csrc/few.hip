@@ -24,13 +24,6 @@ constexpr int kThreads = 64 * kWaves;
 
 int64_t cdiv64(int64_t a, int64_t b) { return (a + b - 1) / b; }
 
-// kSets matrices by tokens held in kPlanes bf16 parts, over K values.
-template <int kSets, int kPlanes>
-__device__ __forceinline__ void product(const uint16_t* const (&w)[kSets], const uint16_t* const (&x)[kPlanes], int K,
-                                        f32x4_t (&acc)[kSets][1]) {
-  stream<kWaves, kSets, kPlanes, true>(w, x, K / 64, acc, [](const uint16_t* p) { return ld16(p); });
-}
-
 // Sum over the wavefronts; complete in wavefront 0, whose lane holds weight
 // rows 4 (lane >> 4) .. + 3 of token lane & 15.
 template <int kSets>
@@ -47,6 +40,36 @@ __device__ __forceinline__ void join(f32x4_t (&acc)[kSets][1], f32x4_t* part) {
 #pragma unroll
       for (int s = 0; s < kSets; ++s) acc[s][0] += part[(j * kSets + s) * 64 + lane];
   }
+}
+
+// Values that another workgroup of the same kernel reads.  The 8 XCDs' L2s are
+// not coherent with one another inside a kernel, so they are written through to
+// memory and read from there (agent scope), a few kilobytes beside the weights.
+template <class T>
+__device__ __forceinline__ void put(T* p, T v) {
+  __hip_atomic_store(p, v, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+}
+template <class T>
+__device__ __forceinline__ T get(const T* p) {
+  return __hip_atomic_load(p, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+}
+__device__ __forceinline__ f32x4_t get4(const float* p) {
+  const uint64_t* q = reinterpret_cast<const uint64_t*>(p);
+  const uint64_t a = get(q), b = get(q + 1);
+  return f32x4_t{__uint_as_float((uint32_t)a), __uint_as_float((uint32_t)(a >> 32)), __uint_as_float((uint32_t)b),
+                 __uint_as_float((uint32_t)(b >> 32))};
+}
+__device__ __forceinline__ void put4(float* p, f32x4_t v) {
+  uint64_t* q = reinterpret_cast<uint64_t*>(p);
+  put(q, (uint64_t)__float_as_uint(v[0]) | (uint64_t)__float_as_uint(v[1]) << 32);
+  put(q + 1, (uint64_t)__float_as_uint(v[2]) | (uint64_t)__float_as_uint(v[3]) << 32);
+}
+
+// kSets matrices by tokens held in kPlanes bf16 parts, over K values.
+template <int kSets, int kPlanes>
+__device__ __forceinline__ void product(const uint16_t* const (&w)[kSets], const uint16_t* const (&x)[kPlanes], int K,
+                                        f32x4_t (&acc)[kSets][1]) {
+  stream<kWaves, kSets, kPlanes, true>(w, x, K / 64, acc, [](const uint16_t* p) { return ld16(p); });
 }
 
 // 4 neighbouring values as kPlanes bf16 parts, planes `plane` values apart.
@@ -107,7 +130,7 @@ __device__ void router_item(const Few& f, int item, f32x4_t* part) {
 #pragma unroll
     for (int r = 0; r < 4; ++r) {
       const int e = item * 16 + (lane >> 4) * 4 + r;
-      if (e < f.E) f.logits[(int64_t)t * f.E + e] = acc[0][0][r];
+      if (e < f.E) put(&f.logits[(int64_t)t * f.E + e], acc[0][0][r]);
     }
   }
 }
@@ -144,30 +167,23 @@ __device__ void down_item(const Few& f, int a, int item, f32x4_t* part) {
   product<1, 2>(w, x, f.F, acc);
   join<1>(acc, part);
   if (threadIdx.x < 64 && (lane & 15) < n)
-    *reinterpret_cast<f32x4_t*>(f.o + (int64_t)r * f.L + item * 16 + (lane >> 4) * 4) = acc[0][0];
+    put4(f.o + (int64_t)r * f.L + item * 16 + (lane >> 4) * 4, acc[0][0]);
 }
 
 // y_lat = sum over a token's experts, in order: 4 columns a thread.
-__device__ void combine_at(const Few& f, int t, int col) {
+__device__ __forceinline__ void combine_at(const Few& f, int t, int col) {
   f32x4_t s = zero4();
   for (int j = 0; j < f.k; ++j)
-    s += f.gates[t * f.k + j] * *reinterpret_cast<const f32x4_t*>(f.o + (int64_t)(t * f.k + j) * f.L + col);
+    s += f.gates[t * f.k + j] * get4(f.o + (int64_t)(t * f.k + j) * f.L + col);
   store_parts<2>(f.ylat + (int64_t)t * f.L + col, (int64_t)f.T * f.L, s);
 }
 
-// 16 columns of y: the up-projection, the shared down-projections and the
-// residual.
-__device__ void output_item(const Few& f, int item, f32x4_t* part) {
+// 16 columns of the shared experts' part of y, in fp32.
+__device__ void shared_out_item(const Few& f, int item, f32x4_t* part) {
   const int lane = threadIdx.x & 63, at = (lane >> 4) * 8, t = min(lane & 15, f.T - 1);
   const int64_t n = item * 16 + (lane & 15);
-  f32x4_t acc[1][1] = {{zero4()}};
-  {
-    const uint16_t* w[1] = {f.w_up_proj + n * f.L + at};
-    const uint16_t* y = f.ylat + (int64_t)t * f.L + at;
-    const uint16_t* x[2] = {y, y + (int64_t)f.T * f.L};
-    product<1, 2>(w, x, f.L, acc);
-  }
   const int W = f.S * f.Fs;
+  f32x4_t acc[1][1] = {{zero4()}};
   for (int s = 0; s < f.S; ++s) {
     const uint16_t* w[1] = {f.ws_down + ((int64_t)s * f.D + n) * f.Fs + at};
     const uint16_t* h = f.hs + (int64_t)t * W + s * f.Fs + at;
@@ -175,32 +191,56 @@ __device__ void output_item(const Few& f, int item, f32x4_t* part) {
     product<1, 2>(w, x, f.Fs, acc);
   }
   join<1>(acc, part);
-  if (threadIdx.x < 64 && (lane & 15) < f.T) {
-    const int64_t o = (int64_t)t * f.D + item * 16 + (lane >> 4) * 4;
-    f32x4_t v = acc[0][0];
+  if (threadIdx.x < 64 && (lane & 15) < f.T)
+    *reinterpret_cast<f32x4_t*>(f.ypart + (int64_t)t * f.D + item * 16 + (lane >> 4) * 4) = acc[0][0];
+}
+
+// 16 columns of y: the up-projection, the shared experts' part and the residual.
+__device__ void output_item(const Few& f, int item, f32x4_t* part) {
+  const int lane = threadIdx.x & 63, at = (lane >> 4) * 8, t = min(lane & 15, f.T - 1);
+  const int64_t o = (int64_t)t * f.D + item * 16 + (lane >> 4) * 4;
+  f32x4_t add = zero4();
+  if (threadIdx.x < 64) {
+    if (f.S > 0) add = *reinterpret_cast<const f32x4_t*>(f.ypart + o);
     if (f.res) {
       const uint2 r = *reinterpret_cast<const uint2*>(f.res + o);
-      v += f32x4_t{__uint_as_float(r.x << 16), __uint_as_float(r.x & 0xFFFF0000u), __uint_as_float(r.y << 16),
-                   __uint_as_float(r.y & 0xFFFF0000u)};
+      add += f32x4_t{__uint_as_float(r.x << 16), __uint_as_float(r.x & 0xFFFF0000u), __uint_as_float(r.y << 16),
+                     __uint_as_float(r.y & 0xFFFF0000u)};
     }
+  }
+  f32x4_t acc[1][1] = {{zero4()}};
+  const uint16_t* w[1] = {f.w_up_proj + (int64_t)(item * 16 + (lane & 15)) * f.L + at};
+  const uint16_t* y = f.ylat + (int64_t)t * f.L + at;
+  const uint16_t* x[2] = {y, y + (int64_t)f.T * f.L};
+  product<1, 2>(w, x, f.L, acc);
+  join<1>(acc, part);
+  if (threadIdx.x < 64 && (lane & 15) < f.T) {
+    const f32x4_t v = acc[0][0] + add;
     *reinterpret_cast<uint2*>(f.y + o) = make_uint2(bf16_pair(v[0], v[1]), bf16_pair(v[2], v[3]));
   }
 }
 
 // Selection for every token, then the selected experts in ascending order,
 // each with its rows t k + j in token order.  One workgroup.
-__device__ void route_all(const Few& f, uint32_t* mask, int* scan) {
+struct RouteLds {
+  uint32_t mask[1024];  // of an expert: the tokens that take it (T <= 16), then its rank above them
+  uint16_t ids[1024];   // [T][k], T k <= 1024
+  int scan[kWaves];
+};
+__device__ void route_all(const Few& f, RouteLds& s) {
   const int wave = threadIdx.x >> 6, lane = threadIdx.x & 63;
-  for (int e = threadIdx.x; e < f.E; e += kThreads) mask[e] = 0;
+  for (int e = threadIdx.x; e < f.E; e += kThreads) s.mask[e] = 0;
   __syncthreads();
   for (int t = wave; t < f.T; t += kWaves) {
     int mine;
     float g;
-    select_topk(f.logits + (int64_t)t * f.E, f.bias, f.E, f.k, mine, g);
+    const float* row = f.logits + (int64_t)t * f.E;
+    select_topk([&](int e) { return get(row + e); }, f.bias, f.E, f.k, mine, g);
     if (lane < f.k) {
       f.topk[t * f.k + lane] = mine;
       f.gates[t * f.k + lane] = g;
-      atomicOr(&mask[mine], 1u << t);
+      s.ids[t * f.k + lane] = (uint16_t)mine;
+      atomicOr(&s.mask[mine], 1u << t);
     }
   }
   __syncthreads();
@@ -209,55 +249,86 @@ __device__ void route_all(const Few& f, uint32_t* mask, int* scan) {
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
     const int e = threadIdx.x * 4 + i;
-    n += e < f.E && mask[e] != 0;
+    n += e < f.E && s.mask[e] != 0;
   }
   int x = n;
   for (int d = 1; d < 64; d <<= 1) {
     const int o = __shfl_up(x, d);
     if (lane >= d) x += o;
   }
-  if (lane == 63) scan[wave] = x;
+  if (lane == 63) s.scan[wave] = x;
   __syncthreads();
   int a = x - n;
-  for (int w = 0; w < wave; ++w) a += scan[w];
+  for (int w = 0; w < wave; ++w) a += s.scan[w];
   if (threadIdx.x == kThreads - 1) *f.n_act = a + n;
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
     const int e = threadIdx.x * 4 + i;
-    if (e < f.E && mask[e] != 0) {
+    if (e < f.E && s.mask[e] != 0) {
       f.act[a] = e;
-      f.act_rows[a] = __popc(mask[e]);
-      mask[e] |= (uint32_t)a << 16;  // T <= 16: the upper half is free
+      f.act_rows[a] = __popc(s.mask[e]);
+      s.mask[e] |= (uint32_t)a << 16;
       ++a;
     }
   }
   __syncthreads();
   for (int i = threadIdx.x; i < f.T * f.k; i += kThreads) {
     const int t = i / f.k;
-    const uint32_t m = mask[f.topk[i]];
+    const uint32_t m = s.mask[s.ids[i]];
     f.rows[(m >> 16) * 16 + __popc(m & ((1u << t) - 1u))] = i;
   }
 }
 static_assert(kThreads * 4 >= 1024, "the scan covers every expert");
 
+// ------------------------------------------------------------- launches
+// Five kernels, each waiting for the whole of the one before:
+//   1  z and the shared experts' hidden values (what needs x alone)
+//   2  the router; its last workgroup to finish selects for all tokens; meanwhile
+//      the shared experts' part of y
+//   3  the selected experts' hidden rows
+//   4  their outputs; a column block's last workgroup to finish sums them to y_lat
+//   5  y
+// A step by the last of some workgroups costs two trips to memory, less than a
+// launch; a wait of all workgroups for all others costs more than one: with 2 to
+// 5 as one kernel of workgroups that take items by tickets and wait on
+// counters, a token of a small layer took 90 us instead of 25 and 4 tokens of a
+// 6144-wide one 800 instead of 400, most of it the tickets' atomics (device-wide
+// ones on one address take about 37 ns each, one after the other).
 constexpr int kPart = (kWaves - 1) * 2 * 64;
+
+// The workgroup's results have reached memory, then *p is raised: whether all
+// n have.
+__device__ __forceinline__ bool last_of(int* p, int n) {
+  __shared__ int before;
+  __builtin_amdgcn_fence(__ATOMIC_RELEASE, "workgroup");
+  wait_vm_all();
+  __syncthreads();
+  if (threadIdx.x == 0) before = __hip_atomic_fetch_add(p, 1, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+  __syncthreads();
+  return before == n - 1;
+}
 
 __global__ __launch_bounds__(kThreads) void few_first_kernel(Few f) {
   __shared__ f32x4_t part[kPart];
+  // counters of the later kernels: one for the router, one for each 16 columns of y_lat
+  const int i = blockIdx.x * kThreads + threadIdx.x;
+  if (i < 1 + f.L / 16) f.counters[i] = 0;
   const int n = f.L / 16;
   if ((int)blockIdx.x < n)
     latent_item(f, blockIdx.x, part);
   else
     shared_item(f, blockIdx.x - n, part);
 }
-__global__ __launch_bounds__(kThreads) void few_router_kernel(Few f) {
-  __shared__ f32x4_t part[kPart];
-  router_item(f, blockIdx.x, part);
-}
 __global__ __launch_bounds__(kThreads) void few_route_kernel(Few f) {
-  __shared__ uint32_t mask[1024];
-  __shared__ int scan[kWaves];
-  route_all(f, mask, scan);
+  __shared__ f32x4_t part[kPart];
+  __shared__ RouteLds route;
+  const int n = (f.E + 15) / 16;
+  if ((int)blockIdx.x < n) {
+    router_item(f, blockIdx.x, part);
+    if (last_of(f.counters, n)) route_all(f, route);
+  } else {
+    shared_out_item(f, blockIdx.x - n, part);
+  }
 }
 __global__ __launch_bounds__(kThreads) void few_hidden_kernel(Few f) {
   __shared__ f32x4_t part[kPart];
@@ -265,11 +336,11 @@ __global__ __launch_bounds__(kThreads) void few_hidden_kernel(Few f) {
 }
 __global__ __launch_bounds__(kThreads) void few_down_kernel(Few f) {
   __shared__ f32x4_t part[kPart];
-  if ((int)blockIdx.y < *f.n_act) down_item(f, blockIdx.y, blockIdx.x, part);
-}
-__global__ __launch_bounds__(kThreads) void few_combine_kernel(Few f) {
-  const int i = blockIdx.x * kThreads + threadIdx.x, per = f.L / 4;
-  if (i < f.T * per) combine_at(f, i / per, i % per * 4);
+  const int n = *f.n_act, item = blockIdx.x;
+  if ((int)blockIdx.y >= n) return;
+  down_item(f, blockIdx.y, item, part);
+  if (last_of(&f.counters[1 + item], n))
+    for (int i = threadIdx.x; i < f.T * 4; i += kThreads) combine_at(f, i >> 2, item * 16 + (i & 3) * 4);
 }
 __global__ __launch_bounds__(kThreads) void few_output_kernel(Few f) {
   __shared__ f32x4_t part[kPart];
@@ -278,15 +349,15 @@ __global__ __launch_bounds__(kThreads) void few_output_kernel(Few f) {
 
 }  // namespace
 
+int few_counter_ints(int L) { return 1 + L / 16; }
+
 hipError_t launch_few(const Few& f, hipStream_t s) {
   if (f.T <= 0) return hipSuccess;
   const unsigned most = (unsigned)(f.T * f.k < f.E ? f.T * f.k : f.E);
   few_first_kernel<<<(unsigned)(f.L / 16 + f.S * f.Fs / 16), kThreads, 0, s>>>(f);
-  few_router_kernel<<<(unsigned)cdiv64(f.E, 16), kThreads, 0, s>>>(f);
-  few_route_kernel<<<1, kThreads, 0, s>>>(f);
+  few_route_kernel<<<(unsigned)(cdiv64(f.E, 16) + (f.S > 0 ? f.D / 16 : 0)), kThreads, 0, s>>>(f);
   few_hidden_kernel<<<dim3(f.F / 16, most), kThreads, 0, s>>>(f);
   few_down_kernel<<<dim3(f.L / 16, most), kThreads, 0, s>>>(f);
-  few_combine_kernel<<<(unsigned)cdiv64(f.T * (f.L / 4), kThreads), kThreads, 0, s>>>(f);
   few_output_kernel<<<(unsigned)(f.D / 16), kThreads, 0, s>>>(f);
   return hipGetLastError();
 }

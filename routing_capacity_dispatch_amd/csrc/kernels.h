@@ -512,7 +512,10 @@ struct Few {
   uint16_t* h;               // [2][T k][F]
   float* o;                  // [T k][L]
   uint16_t* ylat;            // [2][T][L]
+  float* ypart;              // [T][D]: the shared experts' part
+  int32_t* counters;         // [few_counter_ints(L)]
 };
+int few_counter_ints(int L);
 hipError_t launch_few(const Few& f, hipStream_t s);
 
 }  // namespace moe

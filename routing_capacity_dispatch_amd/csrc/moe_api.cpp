@@ -2439,6 +2439,8 @@ int64_t carve_few(const moe_config* c, float* logits, int32_t* topk, float* gate
   f->h = static_cast<uint16_t*>(cv.take(2 * R * F * 2));
   f->o = static_cast<float*>(cv.take(R * L * 4));
   f->ylat = static_cast<uint16_t*>(cv.take(2 * T * L * 2));
+  f->ypart = static_cast<float*>(cv.take(W > 0 ? T * c->d_model * 4 : 0));
+  f->counters = static_cast<int32_t*>(cv.take(moe::few_counter_ints((int)L) * 4));
   return cv.used;
 }
 

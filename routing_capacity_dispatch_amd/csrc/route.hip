@@ -19,7 +19,8 @@ __global__ __launch_bounds__(256) void topk_gates_kernel(const float* __restrict
   if (t >= T) return;
   int mine;
   float gate;
-  select_topk_of<NPER>(logits + t * E, bias, E, k, mine, gate);
+  const float* __restrict__ row = logits + t * E;
+  select_topk_of<NPER>([&](int e) { return row[e]; }, bias, E, k, mine, gate);
   if (lane < k) {
     topk[t * k + lane] = mine;
     gates[t * k + lane] = gate;

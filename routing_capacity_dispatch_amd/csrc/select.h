@@ -73,17 +73,17 @@ __device__ __forceinline__ uint32_t score_key(float s) {
   return (u & 0x80000000u) ? ~u : (u | 0x80000000u);
 }
 
-// row: the token's E logits, E <= 64 * NPER.  Lane j < k ends with the j-th
-// selected expert in `mine` and its gate.
-template <int NPER>
-__device__ __forceinline__ void select_topk_of(const float* __restrict__ row, const float* __restrict__ bias, int E,
-                                               int k, int& mine, float& gate) {
+// row(e): the token's logit of expert e, E <= 64 * NPER.  Lane j < k ends with
+// the j-th selected expert in `mine` and its gate.
+template <int NPER, class Row>
+__device__ __forceinline__ void select_topk_of(Row&& row, const float* __restrict__ bias, int E, int k, int& mine,
+                                               float& gate) {
   const int lane = threadIdx.x & 63;
   // every lane loads every slot (past E: the last expert again, unused), so
   // no branch separates the loads and they are all in flight together
   float v[NPER], b[NPER];
 #pragma unroll
-  for (int i = 0; i < NPER; ++i) v[i] = row[min(i * 64 + lane, E - 1)];
+  for (int i = 0; i < NPER; ++i) v[i] = row(min(i * 64 + lane, E - 1));
 #pragma unroll
   for (int i = 0; i < NPER; ++i) b[i] = 0.0f;
   if (bias) {
@@ -118,7 +118,7 @@ __device__ __forceinline__ void select_topk_of(const float* __restrict__ row, co
     if (lane == j) mine = e;
   }
   const bool sel = lane < k;
-  const float l = sel ? row[mine] : -INFINITY;
+  const float l = sel ? row(mine) : -INFINITY;
   const float m = wave_max(l);
   const float ex = sel ? expf(l - m) : 0.0f;
   const float sum = wave_sum(ex);
@@ -126,8 +126,9 @@ __device__ __forceinline__ void select_topk_of(const float* __restrict__ row, co
 }
 
 // The same for any E <= 1024.
-__device__ __forceinline__ void select_topk(const float* __restrict__ row, const float* __restrict__ bias, int E, int k,
-                                            int& mine, float& gate) {
+template <class Row>
+__device__ __forceinline__ void select_topk(Row&& row, const float* __restrict__ bias, int E, int k, int& mine,
+                                            float& gate) {
   const int nper = (E + 63) / 64;
   if (nper <= 1)
     select_topk_of<1>(row, bias, E, k, mine, gate);
