@@ -810,9 +810,10 @@ moe_status moe_linear_backward(const moe_linear_grad* args, void* ws, size_t ws_
  * norm, and the smaller side first (X = G^T where M > N), `steps` times
  *   A = X X^T,  B = b A + c A A,  X = a X + B X
  * which maps every singular value s to a s + b s^3 + c s^5; the result is
- * scale X, as G lies, rounded once to bf16.  Inside, X is fp32 and the
- * products take it, and A and B off their diagonals, rounded to fp16 (11
- * bits; X to two fp16 numbers where its smaller side is below 256), with fp32
+ * scale X, as G lies, rounded once to bf16.  Inside, X is held
+ * in two fp16 numbers (22 bits) and the diagonals of A and B in fp32; the
+ * products take the first of the two (both where the smaller side is below
+ * 256), and A and B off their diagonals, rounded to fp16 (11 bits), with fp32
  * sums.  Over five steps with (3.4445, -4.7750, 2.0315) that
  * leaves the result within 1.5e-3 of its norm; its rounding to bf16 is 1.7e-3.
  * ------------------------------------------------------------------------ */

@@ -38,11 +38,16 @@ def fp16(x):
     return np.ldexp(np.ldexp(x, e).astype(np.float16).astype(np.float64), -e)
 
 
+def held(x):
+    h = fp16(x)
+    return h + fp16(x - h)
+
+
 def emulated(g, steps=5, coeffs=USUAL, eps=1e-7, scale=1.0):
-    """X in fp32; the products take X, and A and B off their diagonals, in
-    fp16, X in two fp16 numbers where
-    its smaller side is below 256; sums exact."""
-    x = start(g, eps).astype(np.float32).astype(np.float64)
+    """X in two fp16 numbers; the products take the first (both where the
+    smaller side is below 256), and A and B off their diagonals, in fp16; sums
+    exact."""
+    x = held(start(g, eps))
     for a, b, c in (coeffs if isinstance(coeffs[0], tuple) else [coeffs] * steps):
         h = fp16(x)
         low = fp16(x - h) if min(x.shape) < 256 else np.zeros_like(x)
@@ -53,5 +58,5 @@ def emulated(g, steps=5, coeffs=USUAL, eps=1e-7, scale=1.0):
         q = b * (r + np.diag(d)) + c * p2
         e = np.diag(q).copy()
         x = (a + e[:, None]) * x + fp16(q - np.diag(e)) @ (h + low)
-        x = x.astype(np.float32).astype(np.float64)
+        x = held(x)
     return scale * (x.T if np.shape(g)[0] > np.shape(g)[1] else x)

@@ -19,14 +19,16 @@
 namespace moe {
 namespace {
 
-constexpr int kWaves = 4;
-constexpr int kThreads = 64 * kWaves;
+// Wavefronts of a workgroup, which share K (8 instead of 4: 16 tokens 125 us
+// instead of 115, 4 tokens of a 6144-wide layer 382 instead of 386).  The
+// router's also select, one token each at most.
+constexpr int kWaves = 4, kThreads = 64 * kWaves, kRouteWaves = 16;
 
 int64_t cdiv64(int64_t a, int64_t b) { return (a + b - 1) / b; }
 
 // Sum over the wavefronts; complete in wavefront 0, whose lane holds weight
 // rows 4 (lane >> 4) .. + 3 of token lane & 15.
-template <int kSets>
+template <int W, int kSets>
 __device__ __forceinline__ void join(f32x4_t (&acc)[kSets][1], f32x4_t* part) {
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
   if (wave > 0) {
@@ -36,7 +38,7 @@ __device__ __forceinline__ void join(f32x4_t (&acc)[kSets][1], f32x4_t* part) {
   __syncthreads();
   if (wave == 0) {
 #pragma unroll
-    for (int j = 0; j < kWaves - 1; ++j)
+    for (int j = 0; j < W - 1; ++j)
 #pragma unroll
       for (int s = 0; s < kSets; ++s) acc[s][0] += part[(j * kSets + s) * 64 + lane];
   }
@@ -66,10 +68,10 @@ __device__ __forceinline__ void put4(float* p, f32x4_t v) {
 }
 
 // kSets matrices by tokens held in kPlanes bf16 parts, over K values.
-template <int kSets, int kPlanes>
+template <int W, int kSets, int kPlanes>
 __device__ __forceinline__ void product(const uint16_t* const (&w)[kSets], const uint16_t* const (&x)[kPlanes], int K,
                                         f32x4_t (&acc)[kSets][1]) {
-  stream<kWaves, kSets, kPlanes, true>(w, x, K / 64, acc, [](const uint16_t* p) { return ld16(p); });
+  stream<W, kSets, kPlanes, true, 4>(w, x, K / 64, acc, [](const uint16_t* p) { return ld16(p); });
 }
 
 // 4 neighbouring values as kPlanes bf16 parts, planes `plane` values apart.
@@ -87,26 +89,26 @@ __device__ __forceinline__ void store_parts(uint16_t* p, int64_t plane, f32x4_t 
 __device__ __forceinline__ f32x4_t zero4() { return f32x4_t{0.f, 0.f, 0.f, 0.f}; }
 
 // z = x W_lat^T: 16 columns.
-__device__ void latent_item(const Few& f, int item, f32x4_t* part) {
+__device__ __forceinline__ void latent_item(const Few& f, int item, f32x4_t* part) {
   const int lane = threadIdx.x & 63, at = (lane >> 4) * 8, t = min(lane & 15, f.T - 1);
   const uint16_t* w[1] = {f.w_latent + (int64_t)(item * 16 + (lane & 15)) * f.D + at};
   const uint16_t* x[1] = {f.x + (int64_t)t * f.D + at};
   f32x4_t acc[1][1] = {{zero4()}};
-  product<1, 1>(w, x, f.D, acc);
-  join<1>(acc, part);
+  product<kWaves, 1, 1>(w, x, f.D, acc);
+  join<kWaves, 1>(acc, part);
   if (threadIdx.x < 64 && (lane & 15) < f.T)
     store_parts<3>(f.z + (int64_t)t * f.L + item * 16 + (lane >> 4) * 4, (int64_t)f.T * f.L, acc[0][0]);
 }
 
 // Hidden values of the shared experts, side by side: 16 of them.
-__device__ void shared_item(const Few& f, int item, f32x4_t* part) {
+__device__ __forceinline__ void shared_item(const Few& f, int item, f32x4_t* part) {
   const int lane = threadIdx.x & 63, at = (lane >> 4) * 8, t = min(lane & 15, f.T - 1);
   const int64_t row = (int64_t)(item * 16 + (lane & 15)) * f.D + at;
   const uint16_t* w[2] = {f.ws_gate + row, f.ws_up + row};
   const uint16_t* x[1] = {f.x + (int64_t)t * f.D + at};
   f32x4_t acc[2][1] = {{zero4()}, {zero4()}};
-  product<2, 1>(w, x, f.D, acc);
-  join<2>(acc, part);
+  product<kWaves, 2, 1>(w, x, f.D, acc);
+  join<kWaves, 2>(acc, part);
   if (threadIdx.x < 64 && (lane & 15) < f.T) {
     f32x4_t h;
 #pragma unroll
@@ -117,15 +119,15 @@ __device__ void shared_item(const Few& f, int item, f32x4_t* part) {
 }
 
 // Router logits of 16 experts.
-__device__ void router_item(const Few& f, int item, f32x4_t* part) {
+__device__ __forceinline__ void router_item(const Few& f, int item, f32x4_t* part) {
   const int lane = threadIdx.x & 63, at = (lane >> 4) * 8, t = min(lane & 15, f.T - 1);
   const uint16_t* w[1] = {f.w_router + (int64_t)min(item * 16 + (lane & 15), f.E - 1) * f.L + at};
   const uint16_t* z = f.z + (int64_t)t * f.L + at;
   const int64_t plane = (int64_t)f.T * f.L;
   const uint16_t* x[3] = {z, z + plane, z + 2 * plane};
   f32x4_t acc[1][1] = {{zero4()}};
-  product<1, 3>(w, x, f.L, acc);
-  join<1>(acc, part);
+  product<kRouteWaves, 1, 3>(w, x, f.L, acc);
+  join<kRouteWaves, 1>(acc, part);
   if (threadIdx.x < 64 && (lane & 15) < f.T) {
 #pragma unroll
     for (int r = 0; r < 4; ++r) {
@@ -135,18 +137,17 @@ __device__ void router_item(const Few& f, int item, f32x4_t* part) {
   }
 }
 
-// 16 hidden values of the rows of selected expert a.
-__device__ void hidden_item(const Few& f, int a, int item, f32x4_t* part) {
+// 16 hidden values of the n rows of the a-th selected expert, e.
+__device__ __forceinline__ void hidden_item(const Few& f, int a, int e, int n, int item, f32x4_t* part) {
   const int lane = threadIdx.x & 63, at = (lane >> 4) * 8;
-  const int e = f.act[a], n = f.act_rows[a];
-  const int r = f.rows[a * 16 + min(lane & 15, n - 1)];  // t k + j
+  const int r = f.rows[a * 16 + (lane & 15)];  // t k + j
   const int64_t row = ((int64_t)e * f.F + item * 16 + (lane & 15)) * f.L + at;
   const uint16_t* w[2] = {f.w_gate + row, f.w_up + row};
   const uint16_t* z = f.z + (int64_t)(r / f.k) * f.L + at;
   const uint16_t* x[2] = {z, z + (int64_t)f.T * f.L};
   f32x4_t acc[2][1] = {{zero4()}, {zero4()}};
-  product<2, 2>(w, x, f.L, acc);
-  join<2>(acc, part);
+  product<kWaves, 2, 2>(w, x, f.L, acc);
+  join<kWaves, 2>(acc, part);
   if (threadIdx.x < 64 && (lane & 15) < n) {
     f32x4_t h;
 #pragma unroll
@@ -155,17 +156,16 @@ __device__ void hidden_item(const Few& f, int a, int item, f32x4_t* part) {
   }
 }
 
-// 16 columns of the outputs of selected expert a.
-__device__ void down_item(const Few& f, int a, int item, f32x4_t* part) {
+// 16 columns of its outputs.
+__device__ __forceinline__ void down_item(const Few& f, int a, int e, int n, int item, f32x4_t* part) {
   const int lane = threadIdx.x & 63, at = (lane >> 4) * 8;
-  const int e = f.act[a], n = f.act_rows[a];
-  const int r = f.rows[a * 16 + min(lane & 15, n - 1)];
+  const int r = f.rows[a * 16 + (lane & 15)];
   const uint16_t* w[1] = {f.w_down + ((int64_t)e * f.L + item * 16 + (lane & 15)) * f.F + at};
   const uint16_t* h = f.h + (int64_t)r * f.F + at;
   const uint16_t* x[2] = {h, h + (int64_t)f.T * f.k * f.F};
   f32x4_t acc[1][1] = {{zero4()}};
-  product<1, 2>(w, x, f.F, acc);
-  join<1>(acc, part);
+  product<kWaves, 1, 2>(w, x, f.F, acc);
+  join<kWaves, 1>(acc, part);
   if (threadIdx.x < 64 && (lane & 15) < n)
     put4(f.o + (int64_t)r * f.L + item * 16 + (lane >> 4) * 4, acc[0][0]);
 }
@@ -179,7 +179,7 @@ __device__ __forceinline__ void combine_at(const Few& f, int t, int col) {
 }
 
 // 16 columns of the shared experts' part of y, in fp32.
-__device__ void shared_out_item(const Few& f, int item, f32x4_t* part) {
+__device__ __forceinline__ void shared_out_item(const Few& f, int item, f32x4_t* part) {
   const int lane = threadIdx.x & 63, at = (lane >> 4) * 8, t = min(lane & 15, f.T - 1);
   const int64_t n = item * 16 + (lane & 15);
   const int W = f.S * f.Fs;
@@ -188,15 +188,15 @@ __device__ void shared_out_item(const Few& f, int item, f32x4_t* part) {
     const uint16_t* w[1] = {f.ws_down + ((int64_t)s * f.D + n) * f.Fs + at};
     const uint16_t* h = f.hs + (int64_t)t * W + s * f.Fs + at;
     const uint16_t* x[2] = {h, h + (int64_t)f.T * W};
-    product<1, 2>(w, x, f.Fs, acc);
+    product<kRouteWaves, 1, 2>(w, x, f.Fs, acc);
   }
-  join<1>(acc, part);
+  join<kRouteWaves, 1>(acc, part);
   if (threadIdx.x < 64 && (lane & 15) < f.T)
     *reinterpret_cast<f32x4_t*>(f.ypart + (int64_t)t * f.D + item * 16 + (lane >> 4) * 4) = acc[0][0];
 }
 
 // 16 columns of y: the up-projection, the shared experts' part and the residual.
-__device__ void output_item(const Few& f, int item, f32x4_t* part) {
+__device__ __forceinline__ void output_item(const Few& f, int item, f32x4_t* part) {
   const int lane = threadIdx.x & 63, at = (lane >> 4) * 8, t = min(lane & 15, f.T - 1);
   const int64_t o = (int64_t)t * f.D + item * 16 + (lane >> 4) * 4;
   f32x4_t add = zero4();
@@ -212,8 +212,8 @@ __device__ void output_item(const Few& f, int item, f32x4_t* part) {
   const uint16_t* w[1] = {f.w_up_proj + (int64_t)(item * 16 + (lane & 15)) * f.L + at};
   const uint16_t* y = f.ylat + (int64_t)t * f.L + at;
   const uint16_t* x[2] = {y, y + (int64_t)f.T * f.L};
-  product<1, 2>(w, x, f.L, acc);
-  join<1>(acc, part);
+  product<kWaves, 1, 2>(w, x, f.L, acc);
+  join<kWaves, 1>(acc, part);
   if (threadIdx.x < 64 && (lane & 15) < f.T) {
     const f32x4_t v = acc[0][0] + add;
     *reinterpret_cast<uint2*>(f.y + o) = make_uint2(bf16_pair(v[0], v[1]), bf16_pair(v[2], v[3]));
@@ -225,13 +225,15 @@ __device__ void output_item(const Few& f, int item, f32x4_t* part) {
 struct RouteLds {
   uint32_t mask[1024];  // of an expert: the tokens that take it (T <= 16), then its rank above them
   uint16_t ids[1024];   // [T][k], T k <= 1024
-  int scan[kWaves];
+  int scan[kRouteWaves];
+  int total;            // selected experts
 };
+constexpr int kRouteThreads = 64 * kRouteWaves;
 __device__ void route_all(const Few& f, RouteLds& s) {
   const int wave = threadIdx.x >> 6, lane = threadIdx.x & 63;
-  for (int e = threadIdx.x; e < f.E; e += kThreads) s.mask[e] = 0;
+  for (int e = threadIdx.x; e < f.E; e += kRouteThreads) s.mask[e] = 0;
   __syncthreads();
-  for (int t = wave; t < f.T; t += kWaves) {
+  for (int t = wave; t < f.T; t += kRouteWaves) {
     int mine;
     float g;
     const float* row = f.logits + (int64_t)t * f.E;
@@ -244,13 +246,9 @@ __device__ void route_all(const Few& f, RouteLds& s) {
     }
   }
   __syncthreads();
-  // rank of every selected expert among the selected: 4 neighbouring experts a thread
-  int n = 0;
-#pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    const int e = threadIdx.x * 4 + i;
-    n += e < f.E && s.mask[e] != 0;
-  }
+  // rank of every selected expert among the selected: an expert a thread
+  const int e = threadIdx.x;
+  const int n = e < f.E && s.mask[e] != 0;
   int x = n;
   for (int d = 1; d < 64; d <<= 1) {
     const int o = __shfl_up(x, d);
@@ -258,27 +256,30 @@ __device__ void route_all(const Few& f, RouteLds& s) {
   }
   if (lane == 63) s.scan[wave] = x;
   __syncthreads();
-  int a = x - n;
-  for (int w = 0; w < wave; ++w) a += s.scan[w];
-  if (threadIdx.x == kThreads - 1) *f.n_act = a + n;
-#pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    const int e = threadIdx.x * 4 + i;
-    if (e < f.E && s.mask[e] != 0) {
-      f.act[a] = e;
-      f.act_rows[a] = __popc(s.mask[e]);
-      s.mask[e] |= (uint32_t)a << 16;
-      ++a;
-    }
+  const int a = x - n + [&] {
+    int before = 0;
+    for (int w = 0; w < wave; ++w) before += s.scan[w];
+    return before;
+  }();
+  if (threadIdx.x == kRouteThreads - 1) {
+    *f.n_act = a + n;
+    s.total = a + n;
+  }
+  if (n) {
+    f.act[a] = e | __popc(s.mask[e]) << 16;
+    s.mask[e] |= (uint32_t)a << 16;
   }
   __syncthreads();
-  for (int i = threadIdx.x; i < f.T * f.k; i += kThreads) {
+  // the rest of act is empty; an expert's rows are repeated up to 16
+  for (int i = s.total + threadIdx.x; i < f.most; i += kRouteThreads) f.act[i] = -1;
+  for (int i = threadIdx.x; i < f.T * f.k; i += kRouteThreads) {
     const int t = i / f.k;
-    const uint32_t m = s.mask[s.ids[i]];
-    f.rows[(m >> 16) * 16 + __popc(m & ((1u << t) - 1u))] = i;
+    const uint32_t m = s.mask[s.ids[i]], taken = m & 0xFFFFu;
+    const int n = __popc(taken);
+    for (int r = __popc(taken & ((1u << t) - 1u)); r < 16; r += n) f.rows[(m >> 16) * 16 + r] = i;
   }
 }
-static_assert(kThreads * 4 >= 1024, "the scan covers every expert");
+static_assert(kRouteThreads >= 1024, "the scan covers every expert");
 
 // ------------------------------------------------------------- launches
 // Five kernels, each waiting for the whole of the one before:
@@ -294,7 +295,7 @@ static_assert(kThreads * 4 >= 1024, "the scan covers every expert");
 // counters, a token of a small layer took 90 us instead of 25 and 4 tokens of a
 // 6144-wide one 800 instead of 400, most of it the tickets' atomics (device-wide
 // ones on one address take about 37 ns each, one after the other).
-constexpr int kPart = (kWaves - 1) * 2 * 64;
+constexpr int part_size(int waves, int sets) { return (waves - 1) * sets * 64; }
 
 // The workgroup's results have reached memory, then *p is raised: whether all
 // n have.
@@ -309,7 +310,7 @@ __device__ __forceinline__ bool last_of(int* p, int n) {
 }
 
 __global__ __launch_bounds__(kThreads) void few_first_kernel(Few f) {
-  __shared__ f32x4_t part[kPart];
+  __shared__ f32x4_t part[part_size(kWaves, 2)];
   // counters of the later kernels: one for the router, one for each 16 columns of y_lat
   const int i = blockIdx.x * kThreads + threadIdx.x;
   if (i < 1 + f.L / 16) f.counters[i] = 0;
@@ -319,8 +320,8 @@ __global__ __launch_bounds__(kThreads) void few_first_kernel(Few f) {
   else
     shared_item(f, blockIdx.x - n, part);
 }
-__global__ __launch_bounds__(kThreads) void few_route_kernel(Few f) {
-  __shared__ f32x4_t part[kPart];
+__global__ __launch_bounds__(kRouteThreads) void few_route_kernel(Few f) {
+  __shared__ f32x4_t part[part_size(kRouteWaves, 1)];
   __shared__ RouteLds route;
   const int n = (f.E + 15) / 16;
   if ((int)blockIdx.x < n) {
@@ -331,19 +332,20 @@ __global__ __launch_bounds__(kThreads) void few_route_kernel(Few f) {
   }
 }
 __global__ __launch_bounds__(kThreads) void few_hidden_kernel(Few f) {
-  __shared__ f32x4_t part[kPart];
-  if ((int)blockIdx.y < *f.n_act) hidden_item(f, blockIdx.y, blockIdx.x, part);
+  __shared__ f32x4_t part[part_size(kWaves, 2)];
+  const int en = f.act[blockIdx.y];
+  if (en >= 0) hidden_item(f, blockIdx.y, en & 0xFFFF, en >> 16, blockIdx.x, part);
 }
 __global__ __launch_bounds__(kThreads) void few_down_kernel(Few f) {
-  __shared__ f32x4_t part[kPart];
-  const int n = *f.n_act, item = blockIdx.x;
-  if ((int)blockIdx.y >= n) return;
-  down_item(f, blockIdx.y, item, part);
-  if (last_of(&f.counters[1 + item], n))
+  __shared__ f32x4_t part[part_size(kWaves, 1)];
+  const int en = f.act[blockIdx.y], n_act = *f.n_act, item = blockIdx.x;
+  if (en < 0) return;
+  down_item(f, blockIdx.y, en & 0xFFFF, en >> 16, item, part);
+  if (last_of(&f.counters[1 + item], n_act))
     for (int i = threadIdx.x; i < f.T * 4; i += kThreads) combine_at(f, i >> 2, item * 16 + (i & 3) * 4);
 }
 __global__ __launch_bounds__(kThreads) void few_output_kernel(Few f) {
-  __shared__ f32x4_t part[kPart];
+  __shared__ f32x4_t part[part_size(kWaves, 1)];
   output_item(f, blockIdx.x, part);
 }
 
@@ -353,11 +355,10 @@ int few_counter_ints(int L) { return 1 + L / 16; }
 
 hipError_t launch_few(const Few& f, hipStream_t s) {
   if (f.T <= 0) return hipSuccess;
-  const unsigned most = (unsigned)(f.T * f.k < f.E ? f.T * f.k : f.E);
   few_first_kernel<<<(unsigned)(f.L / 16 + f.S * f.Fs / 16), kThreads, 0, s>>>(f);
-  few_route_kernel<<<(unsigned)(cdiv64(f.E, 16) + (f.S > 0 ? f.D / 16 : 0)), kThreads, 0, s>>>(f);
-  few_hidden_kernel<<<dim3(f.F / 16, most), kThreads, 0, s>>>(f);
-  few_down_kernel<<<dim3(f.L / 16, most), kThreads, 0, s>>>(f);
+  few_route_kernel<<<(unsigned)(cdiv64(f.E, 16) + (f.S > 0 ? f.D / 16 : 0)), kRouteThreads, 0, s>>>(f);
+  few_hidden_kernel<<<dim3(f.F / 16, f.most), kThreads, 0, s>>>(f);
+  few_down_kernel<<<dim3(f.L / 16, f.most), kThreads, 0, s>>>(f);
   few_output_kernel<<<(unsigned)(f.D / 16), kThreads, 0, s>>>(f);
   return hipGetLastError();
 }

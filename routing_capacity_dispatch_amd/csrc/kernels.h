@@ -460,9 +460,8 @@ struct Ortho {
   bool tall;            // M > N: X is G^T
   int m, n, mp, np;
   double* norm;         // [group][ortho_norm_chunks()]
-  float* x32;           // [group][m][np]
-  uint16_t* x16[2];     // fp16 X times sx: this step's and the next one's
-  uint16_t* lo16[2];    // ortho_split(m): what that rounding leaves, in fp16
+  uint16_t* x16[2];     // [group][m][np]: X times sx in fp16, this step's and the next one's
+  uint16_t* lo16[2];    // and what that rounding leaves, in fp16
   uint16_t* a16;        // [group][m][mp] fp16, zero diagonals
   uint16_t* b16;
   float* da;            // [group][m]: their diagonals
@@ -470,6 +469,7 @@ struct Ortho {
   // set by the launcher
   int64_t b0;
   bool split;
+  int chunks;           // shares of a norm
   int count, cur, gram_tiles, tiles_m, tiles_n;
   float ca, cb, cc, sx, inv_sx, sa, inv_sa, sb, inv_sb, sx_next;
 };
@@ -505,10 +505,10 @@ struct Few {
   float* logits;             // [T][E]
   int32_t* topk;             // [T][k]
   float* gates;              // [T][k]
+  int most;                  // most experts that can have rows
   int32_t* n_act;            // experts that have rows
-  int32_t* act;              // their numbers, ascending
-  int32_t* act_rows;         // and rows, 1 .. T
-  int32_t* rows;             // [.][16]: t k + j of each
+  int32_t* act;              // [most]: their numbers, ascending, with their rows (1 .. T) from bit 16 on; -1
+  int32_t* rows;             // [most][16]: t k + j of each row, repeated
   uint16_t* h;               // [2][T k][F]
   float* o;                  // [T k][L]
   uint16_t* ylat;            // [2][T][L]

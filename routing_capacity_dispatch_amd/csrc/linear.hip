@@ -349,7 +349,7 @@ __global__ __launch_bounds__(64 * kSkinnyWaves) void linear_skinny_kernel(Linear
     const uint16_t* xs[MB];
 #pragma unroll
     for (int b = 0; b < MB; ++b) xs[b] = x[b] + at;
-    stream<kSkinnyWaves, 1, MB, false>(w1, xs, g.K / 64, acc, [](const uint16_t* p) { return ld16_any(p); });
+    stream<kSkinnyWaves, 1, MB, false, 8>(w1, xs, g.K / 64, acc, [](const uint16_t* p) { return ld16_any(p); });
   }
   // fewer than 64 values of K are left: 32 for each of the last two wavefronts
   {

@@ -2345,12 +2345,10 @@ int64_t carve_ortho(const moe_ortho_args* a, void* ws, moe::Ortho* p, int64_t* g
   const int64_t g = *group;
   Carver cv{static_cast<char*>(ws), 0};
   p->norm = static_cast<double*>(cv.take(g * moe::ortho_norm_chunks() * 8));
-  p->x32 = static_cast<float*>(cv.take(g * m * np * 4));
   p->x16[0] = static_cast<uint16_t*>(cv.take(g * m * np * 2));
   p->x16[1] = static_cast<uint16_t*>(cv.take(a->steps > 1 ? g * m * np * 2 : 0));
-  const bool split = moe::ortho_split(m);
-  p->lo16[0] = static_cast<uint16_t*>(cv.take(split ? g * m * np * 2 : 0));
-  p->lo16[1] = static_cast<uint16_t*>(cv.take(split && a->steps > 1 ? g * m * np * 2 : 0));
+  p->lo16[0] = static_cast<uint16_t*>(cv.take(g * m * np * 2));
+  p->lo16[1] = static_cast<uint16_t*>(cv.take(a->steps > 1 ? g * m * np * 2 : 0));
   p->a16 = static_cast<uint16_t*>(cv.take(g * m * mp * 2));
   p->b16 = static_cast<uint16_t*>(cv.take(g * m * mp * 2));
   p->da = static_cast<float*>(cv.take(g * m * 4));
@@ -2434,7 +2432,7 @@ int64_t carve_few(const moe_config* c, float* logits, int32_t* topk, float* gate
   f->gates = static_cast<float*>(pick(gates, R * 4));
   f->n_act = static_cast<int32_t*>(cv.take(4));
   f->act = static_cast<int32_t*>(cv.take(most * 4));
-  f->act_rows = static_cast<int32_t*>(cv.take(most * 4));
+  f->most = (int)most;
   f->rows = static_cast<int32_t*>(cv.take(most * 16 * 4));
   f->h = static_cast<uint16_t*>(cv.take(2 * R * F * 2));
   f->o = static_cast<float*>(cv.take(R * L * 4));

@@ -4,17 +4,16 @@
 // transposed where it is taller than wide).
 //
 // The three products run on fp16 matrix instructions (gemm_buf.h) with fp32
-// sums.  X itself stays in fp32, and the diagonals of A and B, where their
-// weight is, in fp32 as well; the products see X, and A and B off their
-// diagonals, rounded to fp16 (11 bits).  Then the rounding touches neither the
-// a X + diag(B) X that carries small singular values nor the cancellation
+// sums.  X itself is held in two fp16 numbers, h + l (22 bits), and the diagonals
+// of A and B, where their weight is, in fp32; the products see h, and A and B off
+// their diagonals, rounded to fp16 (11 bits).  Then the rounding touches neither
+// the a X + diag(B) X that carries small singular values nor the cancellation
 // between a and diag(B), and the result is off by 3e-4 to 1.5e-3 of its norm
 // over five steps of the usual coefficients, whatever the spectrum, less than
-// its final rounding to bf16.  (fp16 X alone: 1.2e-3 to 0.12, for a matrix of
-// nearly rank one; bf16 products: 1.4e-3 to 2e-2 with X in fp32.)  Matrices
-// with a side below kSplitSide, where one direction of a few is a large part of
-// A's rows (up to 1e-2), also take what X's rounding leaves, as a second fp16
-// number, in both products with X: 1e-3 at most.
+// its final rounding to bf16.  (h alone: 1.2e-3 to 0.12, for a matrix of nearly
+// rank one; bf16 products: 1.4e-3 to 2e-2.)  Matrices with a side below
+// kSplitSide, where one direction of a few is a large part of A's rows (up to
+// 1e-2), take l as well in both products with X: 1e-3 at most.
 // fp16's range is no matter: the host bounds the singular values of every
 // step and scales X, A and B by powers of two to fill it.
 //
@@ -34,8 +33,11 @@ using core::xcd_order;
 
 using BigTile = core::Tile<256, 256, 4, 2, 64, 2, 3>;
 using SmallTile = core::Tile<128, 128, 2, 2, 64, 2, 2>;
+using DeepTile = core::Tile<64, 64, 2, 2, 64, 5>;
 
 int64_t cdiv64(int64_t a, int64_t b) { return (a + b - 1) / b; }
+
+constexpr int kNormChunks = 256;  // most shares of a matrix's norm
 
 __device__ __forceinline__ uint32_t f16_pair(float lo, float hi) {
   typedef _Float16 f16x2_t __attribute__((ext_vector_type(2)));
@@ -45,8 +47,22 @@ __device__ __forceinline__ float f16_at(uint32_t pair, int hi) {
   return (float)__builtin_bit_cast(_Float16, (uint16_t)(hi ? pair >> 16 : pair & 0xFFFF));
 }
 
-__device__ __forceinline__ float load_in(const void* p, int64_t i, int dt) {
-  return dt == DT_F32 ? static_cast<const float*>(p)[i] : bf16_to_f32(static_cast<const uint16_t*>(p)[i]);
+// 8 values of G from element i on, of which n (at least 1) are there; zeros after them
+__device__ __forceinline__ void load_in(const void* p, int64_t i, int n, int dt, float* v) {
+  if (n >= 8) {
+    if (dt == DT_F32) {
+      const uint16_t* q = reinterpret_cast<const uint16_t*>(static_cast<const float*>(p) + i);
+      unpack(buf::ld16_any(q), v, float{});
+      unpack(buf::ld16_any(q + 8), v + 4, float{});
+    } else {
+      unpack(buf::ld16_any(static_cast<const uint16_t*>(p) + i), v, bf16_t{});
+    }
+  } else {
+#pragma unroll
+    for (int c = 0; c < 8; ++c)
+      v[c] = c >= n ? 0.0f
+             : dt == DT_F32 ? static_cast<const float*>(p)[i + c] : bf16_to_f32(static_cast<const uint16_t*>(p)[i + c]);
+  }
 }
 
 // Sum over a workgroup of 256 threads, in every thread, in a fixed order.
@@ -57,72 +73,105 @@ __device__ __forceinline__ double block_sum(double v, double* part) {
   return (part[0] + part[1]) + (part[2] + part[3]);
 }
 
-// part[matrix][chunk] = sum of squares of kNormRows rows' share of G, in fp64
-// (squares of small or large gradients leave fp32's range).
-constexpr int kNormChunks = 64;
+// norm[matrix][chunk] = sum of squares of a share of G, in fp64 (squares of
+// small or large gradients leave fp32's range).
 __global__ __launch_bounds__(256) void ortho_norm_kernel(Ortho p) {
   __shared__ double part[4];
-  const int64_t b = blockIdx.x / kNormChunks;
-  const int chunk = blockIdx.x % kNormChunks;
+  const int64_t b = blockIdx.x / p.chunks;
+  const int chunk = blockIdx.x % p.chunks;
   const int64_t base = (p.b0 + b) * p.stride_g;
-  const int64_t total = (int64_t)p.M * p.N;
-  const int64_t per = (total + kNormChunks - 1) / kNormChunks;
-  const int64_t first = chunk * per, end = first + per < total ? first + per : total;
+  const uint32_t per_row = (p.N + 7) / 8;
+  const uint32_t total = (uint32_t)p.M * per_row;  // at most 2^29
+  const uint32_t per = (total + p.chunks - 1) / p.chunks;
+  const uint32_t first = chunk * per, end = min(first + per, total);
   double s = 0.0;
-  int64_t i = first + threadIdx.x;
-  int64_t r = i / p.N;
-  int c = (int)(i - r * p.N);
-  for (; i < end; i += 256) {
-    const double v = load_in(p.g, base + r * p.ldg + c, p.dt);
-    s = fma(v, v, s);
-    c += 256;
-    while (c >= p.N) {
-      c -= p.N;
-      ++r;
-    }
+#pragma unroll 4
+  for (uint32_t u = first + threadIdx.x; u < end; u += 256) {
+    const uint32_t r = u / per_row, c = (u - r * per_row) * 8;
+    float v[8];
+    load_in(p.g, base + (int64_t)r * p.ldg + c, p.N - (int)c, p.dt, v);
+#pragma unroll
+    for (int i = 0; i < 8; ++i) s = fma((double)v[i], (double)v[i], s);
   }
   s = block_sum(s, part);
   if (threadIdx.x == 0) p.norm[b * kNormChunks + chunk] = s;
 }
 
-// X = G / (|G| + eps) in fp32 and scaled fp16, 64 x 64 values a workgroup,
-// zeros in columns n .. np.
+// 8 neighbouring values of X (times its scale) as h and l.
+__device__ __forceinline__ uint4 f16_pack(const float* v) {
+  return make_uint4(f16_pair(v[0], v[1]), f16_pair(v[2], v[3]), f16_pair(v[4], v[5]), f16_pair(v[6], v[7]));
+}
+__device__ __forceinline__ void f16_unpack(const uint4& q, float* v) {
+  const uint32_t w[4] = {q.x, q.y, q.z, q.w};
+#pragma unroll
+  for (int i = 0; i < 8; ++i) v[i] = f16_at(w[i / 2], i & 1);
+}
+__device__ __forceinline__ void store_x(uint16_t* h, uint16_t* l, float* v) {
+  const uint4 q = f16_pack(v);
+  st16(h, q);
+  float r[8];
+  f16_unpack(q, r);
+#pragma unroll
+  for (int i = 0; i < 8; ++i) v[i] -= r[i];
+  st16(l, f16_pack(v));
+}
+
+// X = G / (|G| + eps), 64 x 64 values a workgroup, zeros in columns n .. np.
 __global__ __launch_bounds__(256) void ortho_init_kernel(Ortho p) {
   __shared__ float tile[64][65];
+  __shared__ double part[4];
   const int cols = p.np / 64, tiles = cols * ((p.m + 63) / 64);
   const int64_t b = blockIdx.x / tiles;
   const int t = blockIdx.x % tiles;
   const int r0 = t / cols * 64, c0 = t % cols * 64;
-  double ss = 0.0;
-  for (int i = 0; i < kNormChunks; ++i) ss += p.norm[b * kNormChunks + i];
+  const double ss = block_sum((int)threadIdx.x < p.chunks ? p.norm[b * kNormChunks + threadIdx.x] : 0.0, part);
   const double den = sqrt(ss) + (double)p.eps;
-  const double inv = den > 0.0 ? 1.0 / den : 0.0;
+  const double scale = den > 0.0 ? 1.0 / den : 0.0;
   const int64_t gbase = (p.b0 + b) * p.stride_g;
-  const int lx = threadIdx.x & 63, ly = threadIdx.x >> 6;
-  // read along G's rows
-  for (int i = ly; i < 64; i += 4) {
-    const int x_r = p.tall ? r0 + lx : r0 + i, x_c = p.tall ? c0 + i : c0 + lx;  // place in X
-    float v = 0.0f;
-    if (x_r < p.m && x_c < p.n)
-      v = (float)((double)load_in(p.g, gbase + (int64_t)(p.tall ? x_c : x_r) * p.ldg + (p.tall ? x_r : x_c), p.dt) * inv);
-    if (p.tall)
-      tile[lx][i] = v;
-    else
-      tile[i][lx] = v;
+  const int64_t xbase = b * (int64_t)p.m * p.np;
+  float v[2][8];
+#pragma unroll
+  for (int i = 0; i < 2; ++i) {
+    const int row = (threadIdx.x >> 3) + 32 * i, c = (threadIdx.x & 7) * 8;
+    const int gr = (p.tall ? c0 : r0) + row, gc = (p.tall ? r0 : c0) + c;  // in G
+    if (gr < p.M && gc < p.N) {
+      load_in(p.g, gbase + (int64_t)gr * p.ldg + gc, p.N - gc, p.dt, v[i]);
+#pragma unroll
+      for (int q = 0; q < 8; ++q) v[i][q] = (float)((double)v[i][q] * scale);
+    } else {
+#pragma unroll
+      for (int q = 0; q < 8; ++q) v[i][q] = 0.0f;
+    }
+    if (p.tall) {
+#pragma unroll
+      for (int q = 0; q < 8; ++q) tile[c + q][row] = v[i][q];
+    }
   }
-  __syncthreads();
-  float* x32 = p.x32 + b * (int64_t)p.m * p.np;
-  uint16_t* x16 = p.x16[0] + b * (int64_t)p.m * p.np;
-  for (int i = ly; i < 64; i += 4) {
-    const int r = r0 + i;
+  if (p.tall) {
+    __syncthreads();
+#pragma unroll
+    for (int i = 0; i < 2; ++i)
+#pragma unroll
+      for (int q = 0; q < 8; ++q) v[i][q] = tile[(threadIdx.x >> 3) + 32 * i][(threadIdx.x & 7) * 8 + q];
+  }
+#pragma unroll
+  for (int i = 0; i < 2; ++i) {
+    const int r = r0 + (threadIdx.x >> 3) + 32 * i;
     if (r >= p.m) break;
-    const float v = tile[i][lx];
-    const int64_t at = (int64_t)r * p.np + c0 + lx;
-    const _Float16 h = (_Float16)(v * p.sx);
-    x32[at] = v;
-    x16[at] = __builtin_bit_cast(uint16_t, h);
-    if (p.split) p.lo16[0][b * (int64_t)p.m * p.np + at] = __builtin_bit_cast(uint16_t, (_Float16)(v * p.sx - (float)h));
+    const int64_t at = xbase + (int64_t)r * p.np + c0 + (threadIdx.x & 7) * 8;
+#pragma unroll
+    for (int q = 0; q < 8; ++q) v[i][q] *= p.sx;
+    store_x(p.x16[0] + at, p.lo16[0] + at, v[i]);
   }
+}
+
+// acc += A B^T of fp16 operands by the tile's schedule
+template <class TL, bool BK, class SA, class SB>
+__device__ __forceinline__ void products(const SA& a, const SB& b, int K, char* lds, Acc<TL>& acc) {
+  if constexpr (TL::NS == 2)
+    buf::mainloop<TL, false, BK, true>(a, b, K / 64, lds, acc);
+  else
+    buf::mainloop_pipe<TL, false, BK, true>(a, b, K / 64, lds, acc);
 }
 
 // kB false: A = X X^T, of X in one fp16 number or two (kSplit: h h^T + h l^T +
@@ -156,7 +205,7 @@ __global__ __launch_bounds__(TL::THREADS) void ortho_gram_kernel(Ortho p) {
     buf::BRows<TL, false> w;
     a.init(pass == 2 ? lo : X, m0, p.m, K, K, wave, lane);
     w.init(pass == 1 ? lo : X, n0, p.m, K, K, wave, lane);
-    buf::mainloop<TL, false, false, true>(a, w, K / 64, lds, acc);
+    products<TL, false>(a, w, K, lds, acc);
   }
   const float* dA = p.da + (int64_t)b * p.m;
   float* dOut = (kB ? p.db : p.da) + (int64_t)b * p.m;
@@ -206,8 +255,7 @@ __global__ __launch_bounds__(TL::THREADS) void ortho_gram_kernel(Ortho p) {
   if (mt == nt) return;
   // below the diagonal: rows of the tile itself (its columns are all below m)
   buf::Epilogue<TL>::run(acc, lds, min(TL::BM, p.m - m0), [&](int r, int c, float* v) {
-    st16(C + (int64_t)(m0 + r) * p.mp + n0 + c,
-         make_uint4(f16_pair(v[0], v[1]), f16_pair(v[2], v[3]), f16_pair(v[4], v[5]), f16_pair(v[6], v[7])));
+    st16(C + (int64_t)(m0 + r) * p.mp + n0 + c, f16_pack(v));
   });
 }
 
@@ -233,10 +281,11 @@ __global__ __launch_bounds__(TL::THREADS) void ortho_update_kernel(Ortho p) {
     buf::BRows<TL, true> w;
     a.init(p.b16 + (int64_t)b * p.m * p.mp, m0, p.m, p.mp, p.mp, wave, lane);
     w.init((pass == 1 ? p.lo16[p.cur] : p.x16[p.cur]) + xo, n0, p.np, p.np, p.m, wave, lane);
-    buf::mainloop<TL, false, true, true>(a, w, p.mp / 64, lds, acc);
+    products<TL, true>(a, w, p.mp, lds, acc);
   }
   const float* dB = p.db + (int64_t)b * p.m;
-  const float* x32 = p.x32 + xo;
+  const uint16_t* xh = p.x16[p.cur] + xo;
+  const uint16_t* xl = p.lo16[p.cur] + xo;
   const float inv = p.inv_sb * p.inv_sx;
   if constexpr (kLast == 2) {
     // a lane holds 4 neighbouring values of a row of the transposed result
@@ -247,15 +296,17 @@ __global__ __launch_bounds__(TL::THREADS) void ortho_update_kernel(Ortho p) {
       const int row = m0 + acc_row<TL>(wm, mi, lane, 0);
       float d[4];
 #pragma unroll
-      for (int r = 0; r < 4; ++r) d[r] = p.ca + dB[min(row + r, p.m - 1)];
+      for (int r = 0; r < 4; ++r) d[r] = (p.ca + dB[min(row + r, p.m - 1)]) * p.inv_sx;
 #pragma unroll
       for (int ni = 0; ni < TL::NI; ++ni) {
         const int col = n0 + acc_col<TL>(wn, ni, lane);
         if (col >= p.n || row >= p.m) continue;
         float v[4];
 #pragma unroll
-        for (int r = 0; r < 4; ++r)
-          v[r] = p.scale * fmaf(d[r], x32[(int64_t)min(row + r, p.m - 1) * p.np + col], acc.v[mi][ni][r] * inv);
+        for (int r = 0; r < 4; ++r) {
+          const int64_t at = (int64_t)min(row + r, p.m - 1) * p.np + col;
+          v[r] = p.scale * fmaf(d[r], f16_at(xh[at], 0) + f16_at(xl[at], 0), acc.v[mi][ni][r] * inv);
+        }
         uint16_t* o = out + (int64_t)col * p.ldo + row;
         if (p.vec_out && row + 4 <= p.m) {
           *reinterpret_cast<uint2*>(o) = make_uint2(bf16_pair(v[0], v[1]), bf16_pair(v[2], v[3]));
@@ -267,61 +318,79 @@ __global__ __launch_bounds__(TL::THREADS) void ortho_update_kernel(Ortho p) {
       }
     }
   } else {
-    buf::Epilogue<TL>::run(acc, lds, min(TL::BM, p.m - m0), [&](int r, int c, float* v) {
-      const int row = m0 + r, col = n0 + c;
-      if (col >= p.np) return;
-      const int64_t at = (int64_t)row * p.np + col;
-      const float d = p.ca + dB[row];
-      float x[8];
-      unpack(ld16(x32 + at), x, float{});
-      unpack(ld16(x32 + at + 4), x + 4, float{});
+    struct Ahead {
+      uint4 h, l;
+      float d;
+    };
+    buf::Epilogue<TL>::template run<Ahead>(
+        acc, lds, min(TL::BM, p.m - m0),
+        [&](int r, int c) {
+          const int64_t at = (int64_t)(m0 + r) * p.np + min(n0 + c, p.np - 8);
+          return Ahead{ld16(xh + at), ld16(xl + at), dB[m0 + r]};
+        },
+        [&](int r, int c, float* v, const Ahead& q) {
+          const int row = m0 + r, col = n0 + c;
+          if (col >= p.np) return;
+          const float d = (p.ca + q.d) * p.inv_sx;
+          float x[8], y[8];
+          f16_unpack(q.h, x);
+          f16_unpack(q.l, y);
 #pragma unroll
-      for (int i = 0; i < 8; ++i) x[i] = fmaf(d, x[i], v[i] * inv);
-      if constexpr (kLast == 0) {
-        st16(p.x32 + xo + at, pack(x, float{}));
-        st16(p.x32 + xo + at + 4, pack(x + 4, float{}));
+          for (int i = 0; i < 8; ++i) x[i] = fmaf(d, x[i] + y[i], v[i] * inv);
+          if constexpr (kLast == 0) {
+            const int64_t at = xo + (int64_t)row * p.np + col;
 #pragma unroll
-        for (int i = 0; i < 8; ++i) x[i] *= p.sx_next;
-        const uint4 h = make_uint4(f16_pair(x[0], x[1]), f16_pair(x[2], x[3]), f16_pair(x[4], x[5]), f16_pair(x[6], x[7]));
-        st16(p.x16[1 - p.cur] + xo + at, h);
-        if constexpr (kSplit) {
-          const uint32_t w4[4] = {h.x, h.y, h.z, h.w};
+            for (int i = 0; i < 8; ++i) x[i] *= p.sx_next;
+            store_x(p.x16[1 - p.cur] + at, p.lo16[1 - p.cur] + at, x);
+          } else {
+            if (col >= p.n) return;
+            uint16_t* o = p.out + (p.b0 + b) * p.stride_o + (int64_t)row * p.ldo + col;
 #pragma unroll
-          for (int i = 0; i < 8; ++i) x[i] -= f16_at(w4[i / 2], i & 1);
-          st16(p.lo16[1 - p.cur] + xo + at,
-               make_uint4(f16_pair(x[0], x[1]), f16_pair(x[2], x[3]), f16_pair(x[4], x[5]), f16_pair(x[6], x[7])));
-        }
-      } else {
-        if (col >= p.n) return;
-        uint16_t* o = p.out + (p.b0 + b) * p.stride_o + (int64_t)row * p.ldo + col;
+            for (int i = 0; i < 8; ++i) x[i] *= p.scale;
+            if (p.vec_out && col + 8 <= p.n) {
+              st16(o, pack(x, bf16_t{}));
+            } else {
 #pragma unroll
-        for (int i = 0; i < 8; ++i) x[i] *= p.scale;
-        if (p.vec_out && col + 8 <= p.n) {
-          st16(o, pack(x, bf16_t{}));
-        } else {
-#pragma unroll
-          for (int i = 0; i < 8; ++i)
-            if (col + i < p.n) o[i] = f32_to_bf16(x[i]);
-        }
-      }
-    });
+              for (int i = 0; i < 8; ++i)
+                if (col + i < p.n) o[i] = f32_to_bf16(x[i]);
+            }
+          }
+        });
   }
 }
 
 unsigned grid8(int64_t n) { return (unsigned)((n + 7) & ~int64_t(7)); }
 
-template <class TL, bool kSplit>
-hipError_t run_step(const Ortho& p, bool last, hipStream_t s) {
-  const unsigned gram = grid8((int64_t)p.gram_tiles * p.count), all = grid8((int64_t)p.tiles_m * p.tiles_n * p.count);
-  ortho_gram_kernel<TL, false, kSplit><<<gram, TL::THREADS, 0, s>>>(p);
-  ortho_gram_kernel<TL, true, false><<<gram, TL::THREADS, 0, s>>>(p);
-  if (!last)
-    ortho_update_kernel<TL, 0, kSplit><<<all, TL::THREADS, 0, s>>>(p);
-  else if (!p.tall)
-    ortho_update_kernel<TL, 1, kSplit><<<all, TL::THREADS, 0, s>>>(p);
+template <class TL>
+void run_gram(Ortho p, hipStream_t s) {
+  const int64_t t = cdiv64(p.m, TL::BM);
+  p.gram_tiles = (int)(t * (t + 1) / 2);
+  const unsigned grid = grid8((int64_t)p.gram_tiles * p.count);
+  if (TL::BM < 256 && p.split)
+    ortho_gram_kernel<TL, false, TL::BM < 256><<<grid, TL::THREADS, 0, s>>>(p);
   else
-    ortho_update_kernel<TL, 2, kSplit><<<all, TL::THREADS, 0, s>>>(p);
-  return hipGetLastError();
+    ortho_gram_kernel<TL, false, false><<<grid, TL::THREADS, 0, s>>>(p);
+  ortho_gram_kernel<TL, true, false><<<grid, TL::THREADS, 0, s>>>(p);
+}
+
+template <class TL, bool kSplit>
+void run_update_of(const Ortho& p, bool last, hipStream_t s) {
+  const unsigned grid = grid8((int64_t)p.tiles_m * p.tiles_n * p.count);
+  if (!last)
+    ortho_update_kernel<TL, 0, kSplit><<<grid, TL::THREADS, 0, s>>>(p);
+  else if (!p.tall)
+    ortho_update_kernel<TL, 1, kSplit><<<grid, TL::THREADS, 0, s>>>(p);
+  else
+    ortho_update_kernel<TL, 2, kSplit><<<grid, TL::THREADS, 0, s>>>(p);
+}
+template <class TL>
+void run_update(Ortho p, bool last, hipStream_t s) {
+  p.tiles_m = (int)cdiv64(p.m, TL::BM);
+  p.tiles_n = (int)cdiv64(p.np, TL::BN);
+  if (TL::BM < 256 && p.split)
+    run_update_of<TL, TL::BM < 256>(p, last, s);
+  else
+    run_update_of<TL, false>(p, last, s);
 }
 
 }  // namespace
@@ -330,6 +399,21 @@ int ortho_norm_chunks() { return kNormChunks; }
 
 constexpr int kSplitSide = 256;
 bool ortho_split(int64_t m) { return m < kSplitSide; }
+
+namespace {
+// Tile sizes: the largest of which there are enough.
+int class_of(int64_t big, int64_t small, bool split) {
+  return big >= 192 && !split ? TILE_BIG : small >= 256 ? TILE_SMALL : TILE_DEEP;
+}
+int gram_class(const Ortho& p) {
+  auto tiles = [&](int64_t side) { return cdiv64(p.m, side) * (cdiv64(p.m, side) + 1) / 2 * p.count; };
+  return class_of(tiles(256), tiles(128), p.split);
+}
+int update_class(const Ortho& p) {
+  auto tiles = [&](int64_t side) { return cdiv64(p.m, side) * cdiv64(p.np, side) * p.count; };
+  return class_of(tiles(256), tiles(128), p.split);
+}
+}  // namespace
 
 // Matrices at a time: enough tiles of the update for several rounds of the
 // chip, so that more would only need more workspace.
@@ -348,14 +432,10 @@ hipError_t launch_orthogonalize(const Ortho& in, const OrthoStep* step, int step
     p.count = (int)(batch - b0 < group ? batch - b0 : group);
     p.sx = step[0].sx;
     p.split = ortho_split(p.m);
-    ortho_norm_kernel<<<(unsigned)(p.count * kNormChunks), 256, 0, s>>>(p);
+    p.chunks = p.count > 1024 / kNormChunks ? (p.count > 1024 / 16 ? 16 : 1024 / p.count) : kNormChunks;
+    ortho_norm_kernel<<<(unsigned)(p.count * p.chunks), 256, 0, s>>>(p);
     ortho_init_kernel<<<(unsigned)((int64_t)p.count * (p.np / 64) * cdiv64(p.m, 64)), 256, 0, s>>>(p);
-    const bool big = !p.split && (int64_t)cdiv64(p.m, 256) * cdiv64(p.m, 256) * p.count >= 256;
-    const int tile = big ? 256 : 128;
-    const int64_t tm = cdiv64(p.m, tile);
-    p.gram_tiles = (int)(tm * (tm + 1) / 2);
-    p.tiles_m = (int)tm;
-    p.tiles_n = (int)cdiv64(p.np, tile);
+    int gram = gram_class(p), update = update_class(p);
     for (int k = 0; k < steps; ++k) {
       const OrthoStep& c = step[k];
       p.cur = k & 1;
@@ -370,8 +450,19 @@ hipError_t launch_orthogonalize(const Ortho& in, const OrthoStep* step, int step
       p.inv_sb = 1.0f / c.sb;
       p.sx_next = k + 1 < steps ? step[k + 1].sx : 1.0f;
       const bool last = k + 1 == steps;
-      const hipError_t e = big ? run_step<BigTile, false>(p, last, s)
-                           : p.split ? run_step<SmallTile, true>(p, last, s) : run_step<SmallTile, false>(p, last, s);
+      if (gram == TILE_BIG)
+        run_gram<BigTile>(p, s);
+      else if (gram == TILE_SMALL)
+        run_gram<SmallTile>(p, s);
+      else
+        run_gram<DeepTile>(p, s);
+      if (update == TILE_BIG)
+        run_update<BigTile>(p, last, s);
+      else if (update == TILE_SMALL)
+        run_update<SmallTile>(p, last, s);
+      else
+        run_update<DeepTile>(p, last, s);
+      const hipError_t e = hipGetLastError();
       if (e != hipSuccess) return e;
     }
   }

@@ -19,11 +19,11 @@ __device__ __forceinline__ f32x4_t mfma_bf16(const uint4& a, const uint4& b, f32
 // by kX row blocks (or bf16 parts of one).  w and x: this lane's row of each, 8
 // (lane >> 4) values in; units: 64-value units of K in all.  load(p): 16 bytes
 // from p on.  kJoin: all x are parts of the same rows, summed into acc[s][0].
-template <int kWaves, int kSets, int kX, bool kJoin, int kAcc, class Load>
+template <int kWaves, int kSets, int kX, bool kJoin, int kDepth, int kAcc, class Load>
 __device__ __forceinline__ void stream(const uint16_t* const (&w)[kSets], const uint16_t* const (&x)[kX], int units,
                                        f32x4_t (&acc)[kSets][kAcc], Load&& load) {
   static_assert(kAcc == (kJoin ? 1 : kX), "one sum a row block");
-  constexpr int U = 8 / (kSets + kX) > 0 ? 8 / (kSets + kX) : 1;  // units a group: about 64 registers
+  constexpr int U = kDepth / (kSets + kX) > 0 ? kDepth / (kSets + kX) : 1;  // units a group: 8 kDepth registers
   struct Group {
     uint4 a[U][kSets][2], b[U][kX][2];
   };
