@@ -177,14 +177,11 @@ __device__ __forceinline__ void products(const SA& a, const SB& b, int K, char* 
 // kB false: A = X X^T, of X in one fp16 number or two (kSplit: h h^T + h l^T +
 // l h^T);  true: B = b A + c A A, from A off its diagonal (R) and its diagonal
 // d: A A = R R + (d_i + d_j) R_ij + [i = j] d_i^2.
+// t: number of the tile among those of all matrices.
 template <class TL, bool kB, bool kSplit>
-__global__ __launch_bounds__(TL::THREADS) void ortho_gram_kernel(Ortho p) {
+__device__ __forceinline__ void gram_tile(const Ortho& p, int t, char* lds) {
   static_assert(TL::BM == TL::BN, "square tiles of a symmetric product");
-  constexpr int kLds = TL::MAIN_LDS > buf::Epilogue<TL>::kBytes ? TL::MAIN_LDS : buf::Epilogue<TL>::kBytes;
-  __shared__ __attribute__((aligned(1024))) char lds[kLds];
-  const int t = xcd_order(blockIdx.x, gridDim.x);
   const int b = t / p.gram_tiles;
-  if (b >= p.count) return;
   // tile (mt, nt), nt <= mt, number mt (mt + 1) / 2 + nt
   const int q = t - b * p.gram_tiles;
   int mt = __builtin_amdgcn_readfirstlane((int)((sqrtf(8.0f * q + 1.0f) - 1.0f) * 0.5f));
@@ -262,13 +259,9 @@ __global__ __launch_bounds__(TL::THREADS) void ortho_gram_kernel(Ortho p) {
 // X = a X + B X = (a + d_i) X_i + (R X)_i, R being B off its diagonal d.
 // kLast 0: into X; 1: the result, as G lies; 2: the result, transposed.
 template <class TL, int kLast, bool kSplit>
-__global__ __launch_bounds__(TL::THREADS) void ortho_update_kernel(Ortho p) {
-  constexpr int kLds = TL::MAIN_LDS > buf::Epilogue<TL>::kBytes ? TL::MAIN_LDS : buf::Epilogue<TL>::kBytes;
-  __shared__ __attribute__((aligned(1024))) char lds[kLds];
-  const int t = xcd_order(blockIdx.x, gridDim.x);
+__device__ __forceinline__ void update_tile(const Ortho& p, int t, char* lds) {
   const int tiles = p.tiles_m * p.tiles_n;
   const int b = t / tiles;
-  if (b >= p.count) return;
   int mt, nt;
   core::dense_tile(t - b * tiles, p.tiles_m, p.tiles_n, mt, nt);
   const int m0 = mt * TL::BM, n0 = nt * TL::BN;
@@ -359,38 +352,121 @@ __global__ __launch_bounds__(TL::THREADS) void ortho_update_kernel(Ortho p) {
   }
 }
 
+// One phase of a step on some matrices.
+enum Phase : int { PHASE_A = 0, PHASE_B = 1, PHASE_X = 2, PHASE_OUT = 3, PHASE_OUT_T = 4 };
+
+template <class TL, int kPhase, bool kSplit>
+__device__ __forceinline__ void phase_tile(const Ortho& p, int t, char* lds) {
+  if constexpr (kPhase == PHASE_A)
+    gram_tile<TL, false, kSplit>(p, t, lds);
+  else if constexpr (kPhase == PHASE_B)
+    gram_tile<TL, true, kSplit>(p, t, lds);
+  else
+    update_tile<TL, kPhase - PHASE_X, kSplit>(p, t, lds);
+}
+__host__ __device__ inline int phase_tiles(const Ortho& p, int phase) {
+  return (phase <= PHASE_B ? p.gram_tiles : p.tiles_m * p.tiles_n) * p.count;
+}
+
+template <class TL>
+constexpr int tile_lds() {
+  return TL::MAIN_LDS > buf::Epilogue<TL>::kBytes ? TL::MAIN_LDS : buf::Epilogue<TL>::kBytes;
+}
+
+template <class TL, int kPhase, bool kSplit>
+__global__ __launch_bounds__(TL::THREADS) void ortho_phase_kernel(Ortho p) {
+  __shared__ __attribute__((aligned(1024))) char lds[tile_lds<TL>()];
+  const int t = xcd_order(blockIdx.x, gridDim.x);
+  if (t < phase_tiles(p, kPhase)) phase_tile<TL, kPhase, kSplit>(p, t, lds);
+}
+
+// Two phases of different matrices in one launch: on every XCD an eighth of the
+// tiles of the first, the longer ones, then an eighth of the second's.
+template <class TL, int kPhase0, int kPhase1>
+__global__ __launch_bounds__(TL::THREADS) void ortho_pair_kernel(Ortho p0, Ortho p1) {
+  __shared__ __attribute__((aligned(1024))) char lds[tile_lds<TL>()];
+  const int xcd = blockIdx.x & 7, i = blockIdx.x >> 3;
+  const int n0 = phase_tiles(p0, kPhase0), each0 = (n0 + 7) >> 3, n1 = phase_tiles(p1, kPhase1), each1 = (n1 + 7) >> 3;
+  if (i < each0) {
+    const int t = xcd * each0 + i;
+    if (t < n0) phase_tile<TL, kPhase0, false>(p0, t, lds);
+  } else {
+    const int t = xcd * each1 + i - each0;
+    if (t < n1) phase_tile<TL, kPhase1, false>(p1, t, lds);
+  }
+}
+
 unsigned grid8(int64_t n) { return (unsigned)((n + 7) & ~int64_t(7)); }
 
 template <class TL>
-void run_gram(Ortho p, hipStream_t s) {
+void set_tiles(Ortho& p) {
   const int64_t t = cdiv64(p.m, TL::BM);
   p.gram_tiles = (int)(t * (t + 1) / 2);
-  const unsigned grid = grid8((int64_t)p.gram_tiles * p.count);
-  if (TL::BM < 256 && p.split)
-    ortho_gram_kernel<TL, false, TL::BM < 256><<<grid, TL::THREADS, 0, s>>>(p);
-  else
-    ortho_gram_kernel<TL, false, false><<<grid, TL::THREADS, 0, s>>>(p);
-  ortho_gram_kernel<TL, true, false><<<grid, TL::THREADS, 0, s>>>(p);
+  p.tiles_m = (int)t;
+  p.tiles_n = (int)cdiv64(p.np, TL::BN);
 }
 
-template <class TL, bool kSplit>
-void run_update_of(const Ortho& p, bool last, hipStream_t s) {
-  const unsigned grid = grid8((int64_t)p.tiles_m * p.tiles_n * p.count);
-  if (!last)
-    ortho_update_kernel<TL, 0, kSplit><<<grid, TL::THREADS, 0, s>>>(p);
-  else if (!p.tall)
-    ortho_update_kernel<TL, 1, kSplit><<<grid, TL::THREADS, 0, s>>>(p);
-  else
-    ortho_update_kernel<TL, 2, kSplit><<<grid, TL::THREADS, 0, s>>>(p);
+template <class TL, int kPhase, bool kSplit>
+void run_phase_of(const Ortho& p, hipStream_t s) {
+  ortho_phase_kernel<TL, kPhase, kSplit><<<grid8(phase_tiles(p, kPhase)), TL::THREADS, 0, s>>>(p);
 }
 template <class TL>
-void run_update(Ortho p, bool last, hipStream_t s) {
-  p.tiles_m = (int)cdiv64(p.m, TL::BM);
-  p.tiles_n = (int)cdiv64(p.np, TL::BN);
-  if (TL::BM < 256 && p.split)
-    run_update_of<TL, TL::BM < 256>(p, last, s);
+void run_phase(Ortho p, int phase, hipStream_t s) {
+  constexpr bool kSplit = TL::BM < 256;
+  set_tiles<TL>(p);
+  const bool split = kSplit && p.split;
+  if (phase == PHASE_A)
+    split ? run_phase_of<TL, PHASE_A, kSplit>(p, s) : run_phase_of<TL, PHASE_A, false>(p, s);
+  else if (phase == PHASE_B)
+    run_phase_of<TL, PHASE_B, false>(p, s);
+  else if (phase == PHASE_X)
+    split ? run_phase_of<TL, PHASE_X, kSplit>(p, s) : run_phase_of<TL, PHASE_X, false>(p, s);
+  else if (phase == PHASE_OUT)
+    split ? run_phase_of<TL, PHASE_OUT, kSplit>(p, s) : run_phase_of<TL, PHASE_OUT, false>(p, s);
   else
-    run_update_of<TL, false>(p, last, s);
+    split ? run_phase_of<TL, PHASE_OUT_T, kSplit>(p, s) : run_phase_of<TL, PHASE_OUT_T, false>(p, s);
+}
+void run_class(const Ortho& p, int cls, int phase, hipStream_t s) {
+  if (cls == TILE_BIG)
+    run_phase<BigTile>(p, phase, s);
+  else if (cls == TILE_SMALL)
+    run_phase<SmallTile>(p, phase, s);
+  else
+    run_phase<DeepTile>(p, phase, s);
+}
+
+// Phase `phase` of lead with the one before it of p.
+void run_pair(Ortho lead, Ortho p, int phase, hipStream_t s) {
+  using TL = BigTile;
+  set_tiles<TL>(lead);
+  set_tiles<TL>(p);
+  const int other = phase == PHASE_A ? PHASE_X : phase == PHASE_B ? PHASE_A : PHASE_B;
+  const unsigned grid = grid8(phase_tiles(lead, phase)) + grid8(phase_tiles(p, other));
+  if (phase == PHASE_A)
+    ortho_pair_kernel<TL, PHASE_A, PHASE_X><<<grid, TL::THREADS, 0, s>>>(lead, p);
+  else if (phase == PHASE_B)
+    ortho_pair_kernel<TL, PHASE_A, PHASE_B><<<grid, TL::THREADS, 0, s>>>(p, lead);
+  else if (phase == PHASE_X)
+    ortho_pair_kernel<TL, PHASE_X, PHASE_B><<<grid, TL::THREADS, 0, s>>>(lead, p);
+  else if (phase == PHASE_OUT)
+    ortho_pair_kernel<TL, PHASE_OUT, PHASE_B><<<grid, TL::THREADS, 0, s>>>(lead, p);
+  else
+    ortho_pair_kernel<TL, PHASE_OUT_T, PHASE_B><<<grid, TL::THREADS, 0, s>>>(lead, p);
+}
+
+void set_step(Ortho& p, const OrthoStep* step, int steps, int k) {
+  const OrthoStep& c = step[k];
+  p.cur = k & 1;
+  p.ca = c.a;
+  p.cb = c.b;
+  p.cc = c.c;
+  p.sx = c.sx;
+  p.inv_sx = 1.0f / c.sx;
+  p.sa = c.sa;
+  p.inv_sa = 1.0f / c.sa;
+  p.sb = c.sb;
+  p.inv_sb = 1.0f / c.sb;
+  p.sx_next = k + 1 < steps ? step[k + 1].sx : 1.0f;
 }
 
 }  // namespace
@@ -412,6 +488,24 @@ int gram_class(const Ortho& p) {
 int update_class(const Ortho& p) {
   auto tiles = [&](int64_t side) { return cdiv64(p.m, side) * cdiv64(p.np, side) * p.count; };
   return class_of(tiles(256), tiles(128), p.split);
+}
+// Two phases a launch pay where each has several rounds of the chip: the
+// matrix instructions of one then run under the other's traffic (an update
+// moves 8 bytes a value in its epilogue), and rounds end in common.
+bool pays_to_pair(const Ortho& p) {
+  return p.count >= 2 && cdiv64(p.m, 256) * cdiv64(p.np, 256) * p.count >= 512;
+}
+void skip_matrices(Ortho& p, int64_t n) {
+  const int64_t x = n * p.m * p.np, a = n * p.m * p.mp;
+  p.b0 += n;
+  for (int i = 0; i < 2; ++i) {
+    p.x16[i] += x;
+    p.lo16[i] += x;
+  }
+  p.a16 += a;
+  p.b16 += a;
+  p.da += n * p.m;
+  p.db += n * p.m;
 }
 }  // namespace
 
@@ -435,36 +529,35 @@ hipError_t launch_orthogonalize(const Ortho& in, const OrthoStep* step, int step
     p.chunks = p.count > 1024 / kNormChunks ? (p.count > 1024 / 16 ? 16 : 1024 / p.count) : kNormChunks;
     ortho_norm_kernel<<<(unsigned)(p.count * p.chunks), 256, 0, s>>>(p);
     ortho_init_kernel<<<(unsigned)((int64_t)p.count * (p.np / 64) * cdiv64(p.m, 64)), 256, 0, s>>>(p);
-    int gram = gram_class(p), update = update_class(p);
-    for (int k = 0; k < steps; ++k) {
-      const OrthoStep& c = step[k];
-      p.cur = k & 1;
-      p.ca = c.a;
-      p.cb = c.b;
-      p.cc = c.c;
-      p.sx = c.sx;
-      p.inv_sx = 1.0f / c.sx;
-      p.sa = c.sa;
-      p.inv_sa = 1.0f / c.sa;
-      p.sb = c.sb;
-      p.inv_sb = 1.0f / c.sb;
-      p.sx_next = k + 1 < steps ? step[k + 1].sx : 1.0f;
-      const bool last = k + 1 == steps;
-      if (gram == TILE_BIG)
-        run_gram<BigTile>(p, s);
-      else if (gram == TILE_SMALL)
-        run_gram<SmallTile>(p, s);
-      else
-        run_gram<DeepTile>(p, s);
-      if (update == TILE_BIG)
-        run_update<BigTile>(p, last, s);
-      else if (update == TILE_SMALL)
-        run_update<SmallTile>(p, last, s);
-      else
-        run_update<DeepTile>(p, last, s);
-      const hipError_t e = hipGetLastError();
-      if (e != hipSuccess) return e;
+    const int gram = gram_class(p), update = update_class(p);
+    const int out = p.tall ? PHASE_OUT_T : PHASE_OUT;
+    if (gram == TILE_BIG && update == TILE_BIG && pays_to_pair(p)) {
+      // the second half of the matrices one phase behind the first
+      Ortho q[2] = {p, p};
+      q[0].count = (p.count + 1) / 2;
+      q[1].count = p.count - q[0].count;
+      skip_matrices(q[1], q[0].count);
+      auto phase_of = [&](int i) { return i % 3 < 2 ? i % 3 : i / 3 + 1 < steps ? PHASE_X : out; };
+      for (int i = 0; i <= 3 * steps; ++i) {
+        if (i < 3 * steps) set_step(q[0], step, steps, i / 3);
+        if (i > 0) set_step(q[1], step, steps, (i - 1) / 3);
+        if (i == 0)
+          run_class(q[0], TILE_BIG, PHASE_A, s);
+        else if (i < 3 * steps)
+          run_pair(q[0], q[1], phase_of(i), s);
+        else
+          run_class(q[1], TILE_BIG, out, s);
+      }
+    } else {
+      for (int k = 0; k < steps; ++k) {
+        set_step(p, step, steps, k);
+        run_class(p, gram, PHASE_A, s);
+        run_class(p, gram, PHASE_B, s);
+        run_class(p, update, k + 1 < steps ? PHASE_X : out, s);
+      }
     }
+    const hipError_t e = hipGetLastError();
+    if (e != hipSuccess) return e;
   }
   return hipGetLastError();
 }
