@@ -207,41 +207,51 @@ __device__ __forceinline__ void gram_tile(const Ortho& p, int t, char* lds) {
   const float* dA = p.da + (int64_t)b * p.m;
   float* dOut = (kB ? p.db : p.da) + (int64_t)b * p.m;
   uint16_t* C = (kB ? p.b16 : p.a16) + (int64_t)b * p.m * p.mp;
-  // a lane holds rows row .. row + 3 of one column: the transposed place,
-  // 4 neighbouring values
+  // a lane holds rows row .. row + 3 of one column: the transposed place, 4
+  // neighbouring values.  What it reads of A is fetched a column ahead, before
+  // the stores that the compiler would not move loads across.
+  float dr[TL::MI][4], dc[TL::NI];
+  uint2 ahead[2][TL::MI];
+  auto fetch = [&](int ni, uint2 (&to)[TL::MI]) {
+    const int col = min(n0 + acc_col<TL>(wn, ni, lane), p.m - 1);
+#pragma unroll
+    for (int mi = 0; mi < TL::MI; ++mi) {
+      const int row = min(m0 + acc_row<TL>(wm, mi, lane, 0), p.mp - 4);
+      to[mi] = *reinterpret_cast<const uint2*>(p.a16 + ((int64_t)b * p.m + col) * p.mp + row);
+    }
+  };
+  if constexpr (kB) {
+#pragma unroll
+    for (int mi = 0; mi < TL::MI; ++mi)
+#pragma unroll
+      for (int r = 0; r < 4; ++r) dr[mi][r] = dA[min(m0 + acc_row<TL>(wm, mi, lane, r), p.m - 1)];
+#pragma unroll
+    for (int ni = 0; ni < TL::NI; ++ni) dc[ni] = dA[min(n0 + acc_col<TL>(wn, ni, lane), p.m - 1)];
+    fetch(0, ahead[0]);
+  }
 #pragma unroll
   for (int ni = 0; ni < TL::NI; ++ni) {
+    if constexpr (kB) {
+      if (ni + 1 < TL::NI) fetch(ni + 1, ahead[(ni + 1) & 1]);
+    }
     const int col = n0 + acc_col<TL>(wn, ni, lane);
     const bool in_c = col < p.m;
-    float dc = 0.0f;
-    if constexpr (kB) dc = dA[min(col, p.m - 1)];
 #pragma unroll
     for (int mi = 0; mi < TL::MI; ++mi) {
       const int row = m0 + acc_row<TL>(wm, mi, lane, 0);  // a multiple of 4, as mp is
       f32x4_t& v = acc.v[mi][ni];
-      if constexpr (kB) {
-        uint2 rw = make_uint2(0, 0);
-        f32x4_t dr = {0.f, 0.f, 0.f, 0.f};
-        if (in_c && row < p.mp) {
-          rw = *reinterpret_cast<const uint2*>(p.a16 + ((int64_t)b * p.m + col) * p.mp + row);
-#pragma unroll
-          for (int r = 0; r < 4; ++r) dr[r] = dA[min(row + r, p.m - 1)];
-        }
-#pragma unroll
-        for (int r = 0; r < 4; ++r) {
-          const float R = f16_at(r < 2 ? rw.x : rw.y, r & 1) * p.inv_sa;
-          const bool diag = row + r == col;
-          const float A = diag ? dc : R;
-          const float A2 = v[r] * (p.inv_sa * p.inv_sa) + (diag ? dc * dc : (dc + dr[r]) * R);
-          v[r] = p.cb * A + p.cc * A2;
-        }
-      } else {
-#pragma unroll
-        for (int r = 0; r < 4; ++r) v[r] *= p.inv_sx * p.inv_sx;
-      }
 #pragma unroll
       for (int r = 0; r < 4; ++r) {
         const bool diag = row + r == col;
+        if constexpr (kB) {
+          const uint2 rw = ahead[ni & 1][mi];
+          const float R = f16_at(r < 2 ? rw.x : rw.y, r & 1) * p.inv_sa;
+          const float A = diag ? dc[ni] : R;
+          const float A2 = v[r] * (p.inv_sa * p.inv_sa) + (diag ? dc[ni] * dc[ni] : (dc[ni] + dr[mi][r]) * R);
+          v[r] = p.cb * A + p.cc * A2;
+        } else {
+          v[r] *= p.inv_sx * p.inv_sx;
+        }
         if (diag && in_c) dOut[col] = v[r];
         v[r] = diag ? 0.0f : v[r] * (kB ? p.sb : p.sa);
       }
