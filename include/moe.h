@@ -768,7 +768,7 @@ typedef struct {
   int32_t reserved;     /* must be 0                                         */
 } moe_linear_args;
 
-/* Bytes of workspace (may be 0: then ws may be NULL; always 0 up to 64 rows);
+/* Bytes of workspace (may be 0: then ws may be NULL; always 0 up to 16 rows);
    sizes, leading dimensions, types and the pointers' alignment are read.  All
    pointers device; ws 256-byte aligned. */
 moe_status moe_linear_ws_bytes(const moe_linear_args* args, size_t* bytes);

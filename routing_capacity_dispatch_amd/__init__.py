@@ -558,18 +558,27 @@ _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or \
     (lambda index: torch.cuda.current_stream(index).cuda_stream)
 
 
-def _launch(name, dev, *args):
-    """Call a C entry point on the tensors' device (made current for the call
-    where it is not) and its current stream."""
+# index of the current device: likewise (valid once a tensor is on a GPU)
+_current_device = getattr(torch._C, "_cuda_getDevice", None) or torch.cuda.current_device
+
+
+def _status(name, dev, *args):
+    """Status of a C entry point called on the tensors' device (made current for
+    the call where it is not) and its current stream."""
     index = dev.index
-    prev = torch.cuda.current_device()
-    if prev != index:
-        torch.cuda.set_device(index)
+    prev = _current_device()
+    if prev == index:
+        return getattr(abi.load(), name)(*args, _raw_stream(index))
+    torch.cuda.set_device(index)
     try:
-        status = getattr(library(), name)(*args, _raw_stream(index))
+        return getattr(abi.load(), name)(*args, _raw_stream(index))
     finally:
-        if prev != index:
-            torch.cuda.set_device(prev)
+        torch.cuda.set_device(prev)
+
+
+def _launch(name, dev, *args):
+    """The same, raising its error."""
+    status = _status(name, dev, *args)
     if status:
         raise MoeError(name, status)
 
@@ -793,26 +802,33 @@ class ForwardDroplessQuant:
 # ------------------------------------------------------------- linear layers
 def _matrix(t, shape, dtypes, what, dev=None):
     """Leading dimension of a two-dimensional tensor of this shape with contiguous columns (rows may be strided)."""
-    if not (isinstance(t, torch.Tensor) and t.shape == shape and t.dtype in dtypes and t.is_cuda
-            and (dev is None or t.device == dev) and (shape[1] <= 1 or t.stride(1) == 1)
-            and (shape[0] <= 1 or t.stride(0) >= shape[1])):
-        raise ValueError(f"{what} must be a {' or '.join(str(d) for d in dtypes)} tensor of shape {tuple(shape)} with "
-                         f"contiguous columns" + (f" on {dev}" if dev is not None else " on a GPU"))
-    return t.stride(0) if shape[0] > 1 else max(shape[1], 1)
+    if isinstance(t, torch.Tensor) and t.shape == shape and t.dtype in dtypes and \
+            (t.is_cuda if dev is None else t.device == dev):
+        ld, one = t.stride()
+        rows, cols = shape
+        if (one == 1 or cols <= 1) and (ld >= cols or rows <= 1):
+            return ld if rows > 1 else max(cols, 1)
+    raise ValueError(f"{what} must be a {' or '.join(str(d) for d in dtypes)} tensor of shape {tuple(shape)} with "
+                     f"contiguous columns" + (f" on {dev}" if dev is not None else " on a GPU"))
 
 
-def _with_workspace(name, dev, args, ws):
-    """Call `name`(args, workspace): with none first where the caller has none, and one of the size asked for if it needs one."""
-    if ws is None:
-        try:
-            return _launch(name, dev, C.byref(args), None, 0)
-        except MoeError as e:
-            if e.status != abi.MOE_ERR_WORKSPACE:
-                raise
+def _with_workspace(name, dev, args, ws, likely=True):
+    """Call `name`(args, workspace) with the caller's workspace, or a new one of
+    the size asked for.  likely: whether one is asked for mostly; else the call is
+    made without first."""
+    ref = C.byref(args)
+    if ws is None and not likely:
+        status = _status(name, dev, ref, None, 0)
+        if status != abi.MOE_ERR_WORKSPACE:
+            if status:
+                raise MoeError(name, status)
+            return
     n = C.c_size_t(0)
-    abi.check(name + "_ws_bytes", getattr(library(), name + "_ws_bytes")(C.byref(args), C.byref(n)))
+    abi.check(name + "_ws_bytes", getattr(abi.load(), name + "_ws_bytes")(ref, C.byref(n)))
+    if ws is None and n.value == 0:
+        return _launch(name, dev, ref, None, 0)
     ws = _workspace(ws, n.value, dev)
-    _launch(name, dev, C.byref(args), ws.data_ptr(), ws.numel())
+    _launch(name, dev, ref, ws.data_ptr(), ws.numel())
 
 
 _BF16 = (torch.bfloat16,)
@@ -847,7 +863,7 @@ def linear(x, w, bias=None, act: str = "none", residual=None, out_dtype=torch.bf
                           None if pre is None else pre.data_ptr(), max(N, 1), abi.ACTS[act],
                           abi.MOE_F32 if bias is not None and bias.dtype == torch.float32 else abi.MOE_BF16,
                           _DT[out_dtype], 0)
-    _with_workspace("moe_linear", dev, a, ws)
+    _with_workspace("moe_linear", dev, a, ws, likely=False)
     return (out, pre) if save_pre else out
 
 

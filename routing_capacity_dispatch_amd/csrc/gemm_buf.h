@@ -212,7 +212,8 @@ __device__ __forceinline__ void mainloop(const SA& a, const SB& b, int ktiles, c
 // are read among the matrix instructions of this one.
 template <class TL, bool AK, bool BK, bool kHalf, class SA, class SB>
 __device__ __forceinline__ void mainloop_pipe(const SA& a, const SB& b, int ktiles, char* lds, Acc<TL>& acc) {
-  static_assert(TL::NSB == TL::NS, "as many stages of B as of A");
+  static_assert(TL::NSB == TL::NS && (TL::NS - 1) * (TL::A_INS + TL::B_INS) < 64,
+                "as many stages of B as of A, and loads that the wait can count");
   constexpr int P = TL::A_INS + TL::B_INS, NS = TL::NS, KS = TL::KS;
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
   const int wm = wave / TL::WGN, wn = wave % TL::WGN;
@@ -359,7 +360,8 @@ __device__ __forceinline__ void mainloop_regs(const SA& a, const SB& b, int ktil
       for (int i = 0; i < TL::B_INS; ++i) rb[s][i] = b.template load<true>(j, i);
     }
   };
-  auto step = [&](int j, int s) {
+  // tile j's registers to LDS, and the loads of tile j + D into them
+  auto stage = [&](int j, int s) {
     char* sa = lds_a + (s & 1) * TL::A_BYTES;
     char* sb = lds_b + (s & 1) * TL::B_BYTES;
 #pragma unroll
@@ -367,20 +369,29 @@ __device__ __forceinline__ void mainloop_regs(const SA& a, const SB& b, int ktil
 #pragma unroll
     for (int i = 0; i < TL::B_INS; ++i) st16(sb + (i * TL::NW + wave) * 1024 + lane * 16, rb[s][i]);
     load(j + D, s);
+  };
+  Frags<TL> f[TL::KS];
+  auto read = [&](int s) {
     __syncthreads();
 #pragma unroll
-    for (int ks = 0; ks < TL::KS; ++ks) {
-      Frags<TL> f;
-      core::read_frags<TL, AK, BK>(sa, sb, ks, f, wm, wn, lane);
-      mfma_frags<TL, kHalf>(f, acc);
-    }
+    for (int ks = 0; ks < TL::KS; ++ks)
+      core::read_frags<TL, AK, BK>(lds_a + (s & 1) * TL::A_BYTES, lds_b + (s & 1) * TL::B_BYTES, ks, f[ks], wm, wn, lane);
   };
+  if (ktiles <= 0) return;
 #pragma unroll
   for (int s = 0; s < D; ++s) load(s, s);
+  stage(0, 0);
+  read(0);
   for (int j = 0; j < ktiles; j += D) {
 #pragma unroll
     for (int s = 0; s < D; ++s)
-      if (j + s < ktiles) step(j + s, s);
+      if (j + s < ktiles) {
+        // the next tile goes to the other stage while this one's products run
+        if (j + s + 1 < ktiles) stage(j + s + 1, (s + 1) % D);
+#pragma unroll
+        for (int ks = 0; ks < TL::KS; ++ks) mfma_frags<TL, kHalf>(f[ks], acc);
+        if (j + s + 1 < ktiles) read((s + 1) % D);
+      }
   }
   __syncthreads();
 }

@@ -414,6 +414,10 @@ LinearPlan linear_plan(int cls, int64_t M, int64_t N, int64_t K, double units);
 // Rows of x and w on 16 bytes, with zeros from K to a multiple of 8, or (regs,
 // TILE_DEEP only) at any alignment; g.part of p.part_bytes.
 hipError_t launch_linear_tiles(const Linear& g, const LinearPlan& p, bool regs, hipStream_t s);
+// The same without tiles, where linear_streams(M, N, K): operands row-major, any
+// alignment and K, no workspace.
+bool linear_streams(int64_t M, int64_t N, int64_t K);
+hipError_t launch_linear_stream(const Linear& g, hipStream_t s);
 // dw = x^T w with both operands K-major ([K][ldx], [K][ldw]), dx = x w with w
 // K-major (y null: not computed), db[n] = sum of sums[.][n] (null: none).
 struct LinearGrads {
@@ -426,9 +430,6 @@ struct LinearGrads {
 };
 hipError_t launch_linear_grads(const LinearGrads& g, const LinearPlan& dw, const LinearPlan& dx, bool regs,
                                hipStream_t s);
-// At most 64 rows, both operands row-major, any alignment and K.
-bool linear_skinny(int64_t M);
-hipError_t launch_linear_skinny(const Linear& g, hipStream_t s);
 // bf16 rows into rows of ldd (a multiple of 8) with zeros past cols; dst null: none.
 struct PackRows {
   const void* src;

@@ -2,12 +2,11 @@
 // dx = d W, dW = d^T x, db = sum of d over rows, d = dy act'(pre).  bf16
 // operands, fp32 accumulation, each result rounded once.
 //
-// Up to kSkinnyRows rows the product is bound by the weights' bytes: they go
-// straight from memory into matrix instructions, the wavefronts of a workgroup
-// sharing K.  More rows take the tiles of gemm_buf.h, in three sizes (below),
-// the K of tiles that are few or long shared by several workgroups.  Both
-// products of a backward run in one launch, so that one fills the compute units
-// that the other leaves idle.
+// Few rows, and small products, go straight from memory into matrix
+// instructions, the wavefronts of a workgroup sharing K.  The rest takes the
+// tiles of gemm_buf.h, in three sizes (below), the K of tiles that are few or
+// long shared by several workgroups.  Both products of a backward run in one
+// launch, so that one fills the compute units that the other leaves idle.
 #include "common.h"
 #include "gemm_buf.h"
 #include "kernels.h"
@@ -26,17 +25,43 @@ using BigTile = core::Tile<256, 256, 4, 2, 64, 2, 3>;
 // Two workgroups a CU (2048 x 2048 x 2048: 33 us, big 59, 64 x 64 36)
 using SmallTile = core::Tile<128, 128, 2, 2, 64, 2, 2>;
 // Two workgroups a CU, five K tiles in flight each: for few tiles, whose time
-// is the loads' (512 x 2048 x 2048: 15 us, 128 x 128 30, or 26 with K shared)
+// is the loads' (512 x 2048 x 2048: 15 us, 128 x 128 30, or 26 with K shared;
+// nine K tiles in flight: the same)
 using DeepTile = core::Tile<64, 64, 2, 2, 64, 5>;
 
 int64_t cdiv64(int64_t a, int64_t b) { return (a + b - 1) / b; }
 
 // ------------------------------------------------------------- epilogue
+// Phi(u), the normal distribution's integral up to u, and e = exp(-u^2 / 2):
+// Phi(-|u|) = erfc(z) / 2, z = |u| / sqrt 2, and erfc(z) exp(z^2) is smooth in
+// t = 1 / (1 + 0.32 z): a polynomial of degree 8 fitted to it (weighted least
+// squares towards the least relative error over 0 <= z <= 10) is off by 6e-8 of
+// it.  A quarter of erff's instructions, and no cancellation for negative u.
+__device__ __forceinline__ float normal_cdf(float u, float& e) {
+  const float z = fabsf(u) * 0.70710678118654752f;
+  const float t = __builtin_amdgcn_rcpf(fmaf(0.32f, z, 1.0f));
+  float q = -1.768869357629155e-01f;
+  q = fmaf(q, t, 7.061705589258108e-01f);
+  q = fmaf(q, t, -7.767581516428086e-01f);
+  q = fmaf(q, t, 8.161300437402584e-01f);
+  q = fmaf(q, t, -1.918512878265418e-01f);
+  q = fmaf(q, t, 2.817898999523091e-01f);
+  q = fmaf(q, t, 1.584962424419372e-01f);
+  q = fmaf(q, t, 1.830312881592669e-01f);
+  q = fmaf(q, t, -1.216013331140874e-04f);
+  e = __expf(-0.5f * u * u);
+  const float tail = 0.5f * q * e;
+  return u < 0.0f ? tail : 1.0f - tail;
+}
+
 __device__ __forceinline__ float act_of(float u, int act) {
   switch (act) {
     case ACT_RELU: return u < 0.0f ? 0.0f : u;  // a NaN stays one
     case ACT_SILU: return silu(u);
-    case ACT_GELU: return 0.5f * u * (1.0f + erff(u * 0.70710678118654752f));
+    case ACT_GELU: {
+      float e;
+      return u * normal_cdf(u, e);
+    }
     default: return u;
   }
 }
@@ -47,8 +72,11 @@ __device__ __forceinline__ float act_slope(float u, int act) {
       const float p = sigmoid(u);
       return p * (1.0f + u * (1.0f - p));
     }
-    case ACT_GELU:  // Phi(u) + u phi(u)
-      return 0.5f * (1.0f + erff(u * 0.70710678118654752f)) + u * __expf(-0.5f * u * u) * 0.39894228040143268f;
+    case ACT_GELU: {  // Phi(u) + u phi(u)
+      float e;
+      const float p = normal_cdf(u, e);
+      return fmaf(u * 0.39894228040143268f, e, p);
+    }
     default: return 1.0f;
   }
 }
@@ -215,6 +243,11 @@ __device__ __forceinline__ void linear_tile(const Linear& g, int t, char* lds) {
   const int k0 = share * g.share_k, kn = min(g.share_k, g.K - k0), ktiles = (kn + TL::BK - 1) / TL::BK;
   const uint16_t* x = static_cast<const uint16_t*>(g.x) + (AK ? k0 * g.ldx : k0);
   const uint16_t* w = static_cast<const uint16_t*>(g.w) + (BK ? k0 * g.ldw : k0);
+  // a lane's columns are the same in every row; their bias is on its way while
+  // the product runs (the big tile has no registers left for it)
+  Bias<8> bias;
+  const int c0 = n0 + buf::Epilogue<TL>::column();
+  if constexpr (TL::BM < 256) bias = bias_at<8>(g, c0);
   Acc<TL> acc;
   acc.zero();
   if constexpr (kRegs) {
@@ -240,8 +273,7 @@ __device__ __forceinline__ void linear_tile(const Linear& g, int t, char* lds) {
       if (n0 + c < g.N) st_vec<8>(part, (int64_t)(m0 + r) * g.ldpart + n0 + c, DT_F32, v);
     });
   } else {
-    // a lane's columns are the same in every row
-    const Bias<8> bias = bias_at<8>(g, n0 + buf::Epilogue<TL>::column());
+    if constexpr (TL::BM == 256) bias = bias_at<8>(g, c0);
     buf::Epilogue<TL>::template run<Residual<8>>(
         acc, lds, rows, [&](int r, int c) { return fetch<8>(g, m0 + r, n0 + c); },
         [&](int r, int c, float* v, const Residual<8>& x) { finish<8, TL::BM == 256>(g, m0 + r, n0 + c, v, bias, x); });
@@ -322,66 +354,83 @@ __global__ __launch_bounds__(256) void linear_grads_finish_kernel(LinearGrads p,
     finish_at(p.dx, (int64_t)(blockIdx.x - first) * 256 + threadIdx.x);
 }
 
-// ------------------------------------------------------------- few rows
-constexpr int kSkinnyWaves = 4;
-constexpr int kSkinnyRows = 64;
+// ----------------------------------------------- straight from memory
+constexpr int kStreamWaves = 4;
 using buf::ld16_any;
 using buf::ld8_until;
 
-// MB blocks of 16 rows of x by 16 rows of W.  The weights are the first
-// operand, so a lane ends with 4 neighbouring columns of row lane & 15.
-template <int MB>
-__global__ __launch_bounds__(64 * kSkinnyWaves) void linear_skinny_kernel(Linear g) {
-  __shared__ f32x4_t part[kSkinnyWaves][MB][64];
+// 16 MB rows of x by 16 SB rows of W, operands of any alignment, the wavefronts
+// of the workgroup sharing K: nothing passes through LDS but their sums, and no
+// wavefront waits for another until the end.  The weights are the first operand,
+// so a lane ends with 4 neighbouring columns of row lane & 15 of each block.
+// Its loads take 64 bytes of a row at a time, which streams few rows' weights as
+// well as tiles do, and many rows' worse: 1 x 6144 x 2048 7.7 us (DeepTile 10.1),
+// 64 x 1024 x 1024 4.8 (9.0), 333 x 1001 x 1250 10 (12), but 64 x 6144 x 2048 20
+// (13.5) and 512 x 2048 x 2048 26 (15).
+template <int SB, int MB>
+__global__ __launch_bounds__(64 * kStreamWaves) void linear_stream_kernel(Linear g) {
+  constexpr int kBlocks = SB * MB, kOwn = (kBlocks + kStreamWaves - 1) / kStreamWaves;
+  __shared__ f32x4_t part[kStreamWaves][kBlocks][64];
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-  const int n0 = blockIdx.x * 16;
-  const int at = (lane >> 4) * 8;
-  const uint16_t* w = static_cast<const uint16_t*>(g.w) + (int64_t)min(n0 + (lane & 15), g.N - 1) * g.ldw;
+  const int m0 = blockIdx.y * 16 * MB, n0 = blockIdx.x * 16 * SB, at = (lane >> 4) * 8;
+  const uint16_t* w[SB];
   const uint16_t* x[MB];
 #pragma unroll
-  for (int b = 0; b < MB; ++b) {
-    const int64_t m = b * 16 + (lane & 15);
-    x[b] = static_cast<const uint16_t*>(g.x) + (m < g.M ? m : g.M - 1) * g.ldx;
-  }
-  // row block b is finished by wavefront b: what it reads is on its way before
-  // the product starts
-  const int n = n0 + (lane >> 4) * 4;
-  const Bias<4> bias = bias_at<4>(g, n);
-  Residual<4> ahead;
-  if (wave < MB && wave * 16 + (lane & 15) < g.M) ahead = fetch<4>(g, wave * 16 + (lane & 15), n);
-  f32x4_t acc[1][MB];
+  for (int s = 0; s < SB; ++s)
+    w[s] = static_cast<const uint16_t*>(g.w) + (int64_t)min(n0 + s * 16 + (lane & 15), g.N - 1) * g.ldw + at;
 #pragma unroll
-  for (int b = 0; b < MB; ++b) acc[0][b] = f32x4_t{0.f, 0.f, 0.f, 0.f};
-  {
-    const uint16_t* w1[1] = {w + at};
-    const uint16_t* xs[MB];
+  for (int b = 0; b < MB; ++b)
+    x[b] = static_cast<const uint16_t*>(g.x) + (int64_t)min(m0 + b * 16 + (lane & 15), (int)g.M - 1) * g.ldx + at;
+  // block q = (q / MB, q % MB) is finished by wavefront q % kStreamWaves: what it
+  // reads is on its way before the product starts
+  Bias<4> bias[kOwn];
+  Residual<4> ahead[kOwn];
+  auto row = [&](int q) { return m0 + q % MB * 16 + (lane & 15); };
+  auto col = [&](int q) { return n0 + q / MB * 16 + (lane >> 4) * 4; };
 #pragma unroll
-    for (int b = 0; b < MB; ++b) xs[b] = x[b] + at;
-    stream<kSkinnyWaves, 1, MB, false, 8>(w1, xs, g.K / 64, acc, [](const uint16_t* p) { return ld16_any(p); });
+  for (int i = 0; i < kOwn; ++i) {
+    const int q = i * kStreamWaves + wave;
+    if (q < kBlocks) bias[i] = bias_at<4>(g, col(q));
+    if (q < kBlocks && row(q) < g.M) ahead[i] = fetch<4>(g, row(q), col(q));
   }
+  f32x4_t acc[SB][MB];
+#pragma unroll
+  for (int s = 0; s < SB; ++s)
+#pragma unroll
+    for (int b = 0; b < MB; ++b) acc[s][b] = f32x4_t{0.f, 0.f, 0.f, 0.f};
+  stream<kStreamWaves, SB, MB, false, 8>(w, x, g.K / 64, acc, [](const uint16_t* p) { return ld16_any(p); });
   // fewer than 64 values of K are left: 32 for each of the last two wavefronts
   {
-    const int k = (g.K & ~63) + (kSkinnyWaves - 1 - wave) * 32;
+    const int k = (g.K & ~63) + (kStreamWaves - 1 - wave) * 32;
     if (k < g.K) {
-      const uint4 a = ld8_until(w, k + at, g.K);
+      uint4 v[MB];
 #pragma unroll
-      for (int b = 0; b < MB; ++b) acc[0][b] = mfma_bf16(a, ld8_until(x[b], k + at, g.K), acc[0][b]);
+      for (int b = 0; b < MB; ++b) v[b] = ld8_until(x[b] - at, k + at, g.K);
+#pragma unroll
+      for (int s = 0; s < SB; ++s) {
+        const uint4 a = ld8_until(w[s] - at, k + at, g.K);
+#pragma unroll
+        for (int b = 0; b < MB; ++b) acc[s][b] = mfma_bf16(a, v[b], acc[s][b]);
+      }
     }
   }
 #pragma unroll
-  for (int b = 0; b < MB; ++b) part[wave][b][lane] = acc[0][b];
-  __syncthreads();
-  if (wave < MB) {
-    const int b = wave;
-    f32x4_t s = part[0][b][lane];
+  for (int s = 0; s < SB; ++s)
 #pragma unroll
-    for (int j = 1; j < kSkinnyWaves; ++j) s += part[j][b][lane];
-    const int m = b * 16 + (lane & 15);
-    float v[4] = {s[0], s[1], s[2], s[3]};
-    if (m < g.M) finish<4>(g, m, n, v, bias, ahead);
+    for (int b = 0; b < MB; ++b) part[wave][s * MB + b][lane] = acc[s][b];
+  __syncthreads();
+#pragma unroll
+  for (int i = 0; i < kOwn; ++i) {
+    const int q = i * kStreamWaves + wave;
+    if (q >= kBlocks) break;
+    f32x4_t sum = part[0][q][lane];
+#pragma unroll
+    for (int j = 1; j < kStreamWaves; ++j) sum += part[j][q][lane];
+    float v[4] = {sum[0], sum[1], sum[2], sum[3]};
+    if (row(q) < g.M) finish<4>(g, row(q), col(q), v, bias[i], ahead[i]);
   }
 }
-static_assert(kSkinnyWaves >= 2 && kSkinnyWaves * 16 >= kSkinnyRows, "the rest of K goes to two wavefronts; one wavefront a row block");
+static_assert(kStreamWaves >= 2, "the rest of K goes to two wavefronts");
 
 // -------------------------------------------------------- copies, slopes
 // Rows [rows][cols] into rows of ldd (a multiple of 8), zeros past cols.
@@ -482,7 +531,6 @@ unsigned finish_grid(const Linear& g) { return g.shares > 1 ? (unsigned)cdiv64(g
 
 }  // namespace
 
-bool linear_skinny(int64_t M) { return M <= kSkinnyRows; }
 
 // The largest tile of which there are enough for the chip: 192 big ones keep
 // three quarters of the CUs busy, 256 of the middle size all of them.
@@ -542,6 +590,31 @@ hipError_t launch_linear_tiles(const Linear& in, const LinearPlan& p, bool regs,
   return hipGetLastError();
 }
 
+// Few rows, or operands that the L2s hold and a few hundred workgroups take.
+// blocks: 16 x 16 blocks a workgroup, 0: tiles are better.
+static int stream_blocks(int64_t M, int64_t N, int64_t K) {
+  if (M <= 16) return 1;
+  if ((M + N) * K > int64_t(3) << 20) return 0;
+  const int64_t m = cdiv64(M, 16), n = cdiv64(N, 16);
+  if (m * n <= 400) return 1;
+  if (cdiv64(m, 2) * cdiv64(n, 2) <= 400) return 4;
+  return cdiv64(m, 4) * cdiv64(n, 2) <= 400 ? 8 : 0;
+}
+bool linear_streams(int64_t M, int64_t N, int64_t K) { return stream_blocks(M, N, K) > 0; }
+
+hipError_t launch_linear_stream(const Linear& g, hipStream_t s) {
+  if (g.M <= 0 || g.N <= 0) return hipSuccess;
+  const unsigned m = (unsigned)cdiv64(g.M, 16), n = (unsigned)cdiv64(g.N, 16);
+  const int blocks = stream_blocks(g.M, g.N, g.K);
+  if (blocks == 1)
+    linear_stream_kernel<1, 1><<<dim3(n, m), 64 * kStreamWaves, 0, s>>>(g);
+  else if (blocks == 4)
+    linear_stream_kernel<2, 2><<<dim3((n + 1) / 2, (m + 1) / 2), 64 * kStreamWaves, 0, s>>>(g);
+  else
+    linear_stream_kernel<2, 4><<<dim3((n + 1) / 2, (m + 3) / 4), 64 * kStreamWaves, 0, s>>>(g);
+  return hipGetLastError();
+}
+
 hipError_t launch_linear_grads(const LinearGrads& in, const LinearPlan& pw, const LinearPlan& px, bool regs,
                                hipStream_t s) {
   LinearGrads p = in;
@@ -569,18 +642,6 @@ hipError_t launch_linear_grads(const LinearGrads& in, const LinearPlan& pw, cons
   const unsigned fw = p.grid_dw ? finish_grid(p.dw) : 0, fx = p.grid_dx ? finish_grid(p.dx) : 0;
   if (e != hipSuccess || fw + fx == 0) return e;
   linear_grads_finish_kernel<<<fw + fx, 256, 0, s>>>(p, (int)fw);
-  return hipGetLastError();
-}
-
-hipError_t launch_linear_skinny(const Linear& g, hipStream_t s) {
-  if (g.M <= 0 || g.N <= 0) return hipSuccess;
-  const dim3 grid((unsigned)cdiv64(g.N, 16));
-  if (g.M <= 16)
-    linear_skinny_kernel<1><<<grid, 64 * kSkinnyWaves, 0, s>>>(g);
-  else if (g.M <= 32)
-    linear_skinny_kernel<2><<<grid, 64 * kSkinnyWaves, 0, s>>>(g);
-  else
-    linear_skinny_kernel<4><<<grid, 64 * kSkinnyWaves, 0, s>>>(g);
   return hipGetLastError();
 }
 

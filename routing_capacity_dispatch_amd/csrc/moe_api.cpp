@@ -2059,7 +2059,7 @@ struct LinearWs {
 int64_t carve_linear(const moe_linear_args* a, void* ws, LinearWs* w) {
   Carver cv{static_cast<char*>(ws), 0};
   *w = LinearWs{};
-  if (moe::linear_skinny(a->M) || a->N == 0) return 0;
+  if (a->M == 0 || a->N == 0 || moe::linear_streams(a->M, a->N, a->K)) return 0;
   const int64_t K8 = align8(a->K);
   const int cls = moe::linear_class(a->M, a->N, 0, 0);
   w->plan = moe::linear_plan(cls, a->M, a->N, K8, moe::linear_units(cls, a->M, a->N, K8));
@@ -2114,7 +2114,7 @@ MOE_API moe_status moe_linear(const moe_linear_args* args, void* ws, size_t ws_b
   g.pre = a.pre;
   g.ldp = a.ldp;
   g.act = a.act;
-  if (moe::linear_skinny(a.M)) return hip_status(moe::launch_linear_skinny(g, s));
+  if (moe::linear_streams(a.M, a.N, a.K)) return hip_status(moe::launch_linear_stream(g, s));
   const int64_t K8 = align8(a.K);
   const moe::PackRows px{a.x, a.M, g.K, a.ldx, w.x, K8}, pw{a.w, a.N, g.K, a.ldw, w.w, K8};
   const hipError_t e = moe::launch_pack_rows(px, pw, s);

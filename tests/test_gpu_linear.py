@@ -108,7 +108,8 @@ def check_linear(M, N, K, act="none", bias=None, res=False, out=BF, pre=False, s
 @pytest.mark.parametrize("M,N,K", [
     (1, 1, 1), (1, 64, 128), (1, 1000, 2048), (3, 17, 5), (15, 100, 129), (16, 48, 64), (17, 33, 1000), (33, 250, 96),
     (64, 128, 256), (65, 128, 64), (65, 1, 7), (100, 129, 8), (127, 255, 65), (128, 128, 128), (130, 300, 1250),
-    (257, 513, 72), (300, 40, 4000), (1000, 1000, 31)])
+    (257, 513, 72), (300, 40, 4000), (1000, 1000, 31), (17, 6144, 700), (40, 2048, 1600), (640, 640, 1300),
+    (500, 900, 2050)])
 @pytest.mark.parametrize("out", [BF, F32])
 def test_linear_sizes(M, N, K, out):
     check_linear(M, N, K, "silu", BF, True, out, True, seed=M + N + K)
@@ -132,7 +133,8 @@ def test_linear_strides(shift, pad, M, out):
 
 
 # whole rounds of large tiles, with ends inside a tile, and K shared by many workgroups
-@pytest.mark.parametrize("M,N,K", [(3500, 3601, 200), (4096, 3328, 64), (72, 64, 8192), (200, 136, 5003)])
+@pytest.mark.parametrize("M,N,K", [(3500, 3601, 200), (4096, 3328, 64), (72, 64, 40000),
+                                   (200, 136, 20003), (2100, 2000, 130)])
 def test_linear_large_and_shared(M, N, K):
     check_linear(M, N, K, "relu", BF, True, BF, True, seed=3)
 
@@ -296,9 +298,9 @@ def test_streams_and_graph():
 
 def test_workspace_of_the_caller():
     d = dev()
-    x, w = rand((100, 4097), 1).to(d), rand((40, 4097), 2).to(d)
+    x, w = rand((100, 30001), 1).to(d), rand((40, 30001), 2).to(d)
     ref = rcd.linear(x, w)
-    ws = torch.full((1 << 18,), 255, dtype=torch.uint8, device=d)
+    ws = torch.full((1 << 20,), 255, dtype=torch.uint8, device=d)
     assert torch.equal(rcd.linear(x, w, ws=ws), ref)
     with pytest.raises(rcd.MoeError, match="WORKSPACE"):
         rcd.linear(x, w, ws=ws[:256])

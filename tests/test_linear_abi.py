@@ -57,11 +57,11 @@ def test_linear_null_and_workspace(lib):
     # nothing to do: no pointer is looked at
     assert lib.moe_linear(C.byref(args(M=0, x=None, w=None, y=None)), None, 0, None) == OK
     assert lib.moe_linear(C.byref(args(N=0, x=None, w=None, y=None)), None, 0, None) == OK
-    # few rows or few tiles: none needed; many whose rows do not start or end on 16 bytes: copies; a long K shared: sums
+    # few rows or a small product: none needed; many whose rows do not start or end on 16 bytes: copies; a long K shared: sums
     big = dict(M=4096, N=4096, ldy=4096, ldr=4096, ldp=4096)
-    for over, some in ((dict(M=64, K=31), False), (dict(M=100, K=31), False), (big, False), (dict(big, K=31), True),
+    for over, some in ((dict(M=16, N=1 << 20, K=31, ldy=1 << 20, ldr=1 << 20, ldp=1 << 20), False), (dict(M=100, K=31), False), (big, False), (dict(big, K=31), True),
                        (dict(big, ldx=36), True), (dict(big, w=FAKE + 2), True),
-                       (dict(M=100, K=4096, ldx=4096, ldw=4096), True)):
+                       (dict(M=100, K=32768, ldx=32768, ldw=32768), True)):
         a = args(**over)
         assert lib.moe_linear_ws_bytes(C.byref(a), C.byref(n)) == OK and (n.value > 0) == some, over
         if some:
