@@ -907,8 +907,8 @@ def linear_backward(dy, x, w, pre=None, act: str = "none", bias: bool = True, ne
 @functools.lru_cache(maxsize=64)
 def _coefficients(coeffs, steps):
     """[steps][3] fp32 on the host of one (a, b, c), or of one for each step."""
-    rows = [coeffs] * steps if not isinstance(coeffs[0], tuple) else list(coeffs)
-    _check(len(rows) == steps and all(len(r) == 3 for r in rows), "coeffs is (a, b, c), or one of them for each step")
+    rows = [coeffs] * steps if not any(isinstance(c, tuple) for c in coeffs) else list(coeffs)
+    _check(len(rows) == steps and all(isinstance(r, tuple) and len(r) == 3 for r in rows), "coeffs is (a, b, c), or one of them for each step")
     return (C.c_float * (3 * steps))(*[float(v) for r in rows for v in r])
 
 
@@ -950,7 +950,8 @@ def orthogonalize(g, steps: int = 5, coeffs=(3.4445, -4.7750, 2.0315), eps: floa
 # ------------------------------------------------------- a few tokens
 class ForwardFew:
     """Reusable dropless forward for at most 16 tokens (moe_forward_few): the
-    weights of ForwardDropless, workspace and outputs bound once."""
+    weights of ForwardDropless, workspace and outputs bound once.  One call at a
+    time: calls on two streams need an object each."""
 
     def __init__(self, cfg, weights: Dict[str, torch.Tensor], device, taps=False):
         device = torch.device(device)

@@ -292,8 +292,8 @@ static_assert(kRouteThreads >= 1024, "the scan covers every expert");
 // A step by the last of some workgroups costs two trips to memory, less than a
 // launch; a wait of all workgroups for all others costs more than one: with 2 to
 // 5 as one kernel of workgroups that take items by tickets and wait on
-// counters, a token of a small layer took 90 us instead of 25 and 4 tokens of a
-// 6144-wide one 800 instead of 400, most of it the tickets' atomics (device-wide
+// counters, a token of a small layer took 90 us instead of 26 and 4 tokens of a
+// 6144-wide one 800 instead of 385, most of it the tickets' atomics (device-wide
 // ones on one address take about 37 ns each, one after the other).
 constexpr int part_size(int waves, int sets) { return (waves - 1) * sets * 64; }
 

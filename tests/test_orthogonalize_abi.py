@@ -89,3 +89,6 @@ def test_binding_refusals():
         rcd.orthogonalize(torch.zeros(4, 4))
     with pytest.raises(ValueError, match="coeffs"):
         rcd._coefficients(((1.0, 2.0, 3.0),) * 3, 4)
+    for bad in ((), (1.0, 2.0), ((1.0, 2.0, 3.0), 4.0)):
+        with pytest.raises(ValueError, match="coeffs"):
+            rcd._coefficients(bad, 2)
