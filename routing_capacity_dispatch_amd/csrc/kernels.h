@@ -407,6 +407,8 @@ struct LinearPlan {
   int shares, share_k;
   int64_t part_bytes;
 };
+// Of a launch with so many tiles of 256 and 128 a side.
+int tile_class(int64_t big, int64_t small);
 // For one product of M0 x N0 results, or two in one launch.
 int linear_class(int64_t M0, int64_t N0, int64_t M1, int64_t N1);
 double linear_units(int cls, int64_t M, int64_t N, int64_t K);

@@ -167,8 +167,6 @@ __device__ __forceinline__ Residual<C> fetch(const Linear& g, int64_t m, int n) 
   return r;
 }
 
-// C neighbouring sums of row m from column n on: bias, pre-activation out,
-// activation, residual, result.
 template <int C>
 struct Bias {
   float v[C];
@@ -181,6 +179,8 @@ __device__ __forceinline__ Bias<C> bias_at(const Linear& g, int n) {
   return b;
 }
 
+// C neighbouring sums of row m from column n on: bias, pre-activation out,
+// activation, residual, result.
 // kStream: results of many large tiles, written past the caches, which the
 // operands then keep (16384 x 6144 x 2048 with everything: 506 -> 479 us).
 template <int C, bool kStream = false>
@@ -531,12 +531,22 @@ unsigned finish_grid(const Linear& g) { return g.shares > 1 ? (unsigned)cdiv64(g
 
 }  // namespace
 
-
 // The largest tile of which there are enough for the chip: 192 big ones keep
-// three quarters of the CUs busy, 256 of the middle size all of them.
+// three quarters of the CUs busy, 256 of the middle size all of them.  But not big
+// ones whose last round is nearly empty, or that lie in large part outside the
+// product: 256 of the middle size, a CU's first or second, take 0.35 of the time of
+// 256 big ones (4608 x 4096 x 2048, 288 big ones: 120 us, 109 with 1152 of the
+// middle size; 6144 x 4096 x 2048, 384 of them: 119 and 126).
+int tile_class(int64_t big, int64_t small) {
+  if (big >= 192 && 20 * cdiv64(big, 256) <= 7 * cdiv64(small, 256)) return TILE_BIG;
+  return small >= 256 ? TILE_SMALL : TILE_DEEP;
+}
+// (The rounds of two products are of different lengths, and fill one another's:
+// 5000 x 2500 x 2500 with 300 big tiles 188 us, with 1200 of the middle size 198.)
 int linear_class(int64_t M0, int64_t N0, int64_t M1, int64_t N1) {
   auto tiles = [&](int64_t side) { return cdiv64(M0, side) * cdiv64(N0, side) + cdiv64(M1, side) * cdiv64(N1, side); };
-  return tiles(256) >= 192 ? TILE_BIG : tiles(128) >= 256 ? TILE_SMALL : TILE_DEEP;
+  const bool two = M0 > 0 && M1 > 0;
+  return two && tiles(256) >= 192 ? TILE_BIG : tile_class(tiles(256), tiles(128));
 }
 
 double linear_units(int cls, int64_t M, int64_t N, int64_t K) {
