@@ -156,18 +156,27 @@ __device__ __forceinline__ void hidden_item(const Few& f, int a, int e, int n, i
   }
 }
 
-// 16 columns of its outputs.
+// 16 kC columns of its outputs.
+template <int kC>
 __device__ __forceinline__ void down_item(const Few& f, int a, int e, int n, int item, f32x4_t* part) {
   const int lane = threadIdx.x & 63, at = (lane >> 4) * 8;
   const int r = f.rows[a * 16 + (lane & 15)];
-  const uint16_t* w[1] = {f.w_down + ((int64_t)e * f.L + item * 16 + (lane & 15)) * f.F + at};
+  const uint16_t* w[kC];
+  f32x4_t acc[kC][1];
+#pragma unroll
+  for (int c = 0; c < kC; ++c) {
+    w[c] = f.w_down + ((int64_t)e * f.L + (item * kC + c) * 16 + (lane & 15)) * f.F + at;
+    acc[c][0] = zero4();
+  }
   const uint16_t* h = f.h + (int64_t)r * f.F + at;
   const uint16_t* x[2] = {h, h + (int64_t)f.T * f.k * f.F};
-  f32x4_t acc[1][1] = {{zero4()}};
-  product<kWaves, 1, 2>(w, x, f.F, acc);
-  join<kWaves, 1>(acc, part);
-  if (threadIdx.x < 64 && (lane & 15) < n)
-    put4(f.o + (int64_t)r * f.L + item * 16 + (lane >> 4) * 4, acc[0][0]);
+  product<kWaves, kC, 2>(w, x, f.F, acc);
+  join<kWaves, kC>(acc, part);
+  if (threadIdx.x < 64 && (lane & 15) < n) {
+#pragma unroll
+    for (int c = 0; c < kC; ++c)
+      put4(f.o + (int64_t)r * f.L + (item * kC + c) * 16 + (lane >> 4) * 4, acc[c][0]);
+  }
 }
 
 // y_lat = sum over a token's experts, in order: 4 columns a thread.
@@ -311,7 +320,7 @@ __device__ __forceinline__ bool last_of(int* p, int n) {
 
 __global__ __launch_bounds__(kThreads) void few_first_kernel(Few f) {
   __shared__ f32x4_t part[part_size(kWaves, 2)];
-  // counters of the later kernels: one for the router, one for each 16 columns of y_lat
+  // counters of the later kernels: one for the router, one for each 16 (or 32) columns of y_lat
   const int i = blockIdx.x * kThreads + threadIdx.x;
   if (i < 1 + f.L / 16) f.counters[i] = 0;
   const int n = f.L / 16;
@@ -336,13 +345,15 @@ __global__ __launch_bounds__(kThreads) void few_hidden_kernel(Few f) {
   const int en = f.act[blockIdx.y];
   if (en >= 0) hidden_item(f, blockIdx.y, en & 0xFFFF, en >> 16, blockIdx.x, part);
 }
+template <int kC>
 __global__ __launch_bounds__(kThreads) void few_down_kernel(Few f) {
-  __shared__ f32x4_t part[part_size(kWaves, 1)];
+  __shared__ f32x4_t part[part_size(kWaves, kC)];
   const int en = f.act[blockIdx.y], n_act = *f.n_act, item = blockIdx.x;
   if (en < 0) return;
-  down_item(f, blockIdx.y, en & 0xFFFF, en >> 16, item, part);
+  down_item<kC>(f, blockIdx.y, en & 0xFFFF, en >> 16, item, part);
   if (last_of(&f.counters[1 + item], n_act))
-    for (int i = threadIdx.x; i < f.T * 4; i += kThreads) combine_at(f, i >> 2, item * 16 + (i & 3) * 4);
+    for (int i = threadIdx.x; i < f.T * 4 * kC; i += kThreads)
+      combine_at(f, i / (4 * kC), (item * 4 * kC + i % (4 * kC)) * 4);
 }
 __global__ __launch_bounds__(kThreads) void few_output_kernel(Few f) {
   __shared__ f32x4_t part[part_size(kWaves, 1)];
@@ -358,7 +369,15 @@ hipError_t launch_few(const Few& f, hipStream_t s) {
   few_first_kernel<<<(unsigned)(f.L / 16 + f.S * f.Fs / 16), kThreads, 0, s>>>(f);
   few_route_kernel<<<(unsigned)(cdiv64(f.E, 16) + (f.S > 0 ? f.D / 16 : 0)), kRouteThreads, 0, s>>>(f);
   few_hidden_kernel<<<dim3(f.F / 16, f.most), kThreads, 0, s>>>(f);
-  few_down_kernel<<<dim3(f.L / 16, f.most), kThreads, 0, s>>>(f);
+  // 32 columns a workgroup where that leaves two for every CU: the hidden rows, in
+  // two parts and for any number of rows as much as 32 rows of weights, are read
+  // half as often (16 tokens by 960 columns, 60 experts 108 us, 115 with 16
+  // columns; 64 columns: the same, and 267 instead of 258 where 16 tokens pick
+  // from 128 experts.  The hidden kernel with 32 values a workgroup: 262).
+  if ((int64_t)f.L / 32 * f.most >= 512)  // L is a multiple of 64
+    few_down_kernel<2><<<dim3(f.L / 32, f.most), kThreads, 0, s>>>(f);
+  else
+    few_down_kernel<1><<<dim3(f.L / 16, f.most), kThreads, 0, s>>>(f);
   few_output_kernel<<<(unsigned)(f.D / 16), kThreads, 0, s>>>(f);
   return hipGetLastError();
 }

@@ -144,6 +144,20 @@ def test_as_the_dropless_forward():
     assert float(((a - b).abs().amax(1) / b.abs().amax(1)).max()) <= 2e-2
 
 
+def test_columns_of_a_workgroup():
+    """Enough columns and experts for 32 columns of the experts' outputs a
+    workgroup; a token's bits do not depend on it."""
+    d = dev()
+    T, D, L, E, k, F, S, Fs = 16, 128, 704, 48, 8, 192, 0, 0
+    w = weights(D, L, E, F, S, Fs, 11)
+    f, y = check(T, D, L, E, k, F, S, Fs, seed=11, w=w)
+    x = torch.randn((T, D), generator=torch.Generator().manual_seed(12)).to(torch.bfloat16).to(d)
+    one = rcd.ForwardFew(rcd.make_config(1, D, L, E, 1, k, F, S, Fs, 1), f.w, d)
+    y = f(x).clone()
+    for t in (0, 7, 15):
+        assert torch.equal(one(x[t:t + 1]), y[t:t + 1])
+
+
 def test_tokens_do_not_see_each_other():
     """A token's output is the same bits alone and among others, in any place."""
     d = dev()
