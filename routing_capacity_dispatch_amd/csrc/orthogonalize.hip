@@ -500,9 +500,16 @@ int update_class(const Ortho& p) {
 }
 // Two phases a launch pay where each has several rounds of the chip: the
 // matrix instructions of one then run under the other's traffic (an update
-// moves 8 bytes a value in its epilogue), and rounds end in common.
+// moves 8 bytes a value in its epilogue), and rounds end in common.  With four
+// rounds of updates a nearly empty last round of A's and B's tiles is no matter
+// (8 x 2048 x 4096: 3028 us, 3287 with middle-size tiles of A and B and no pairs;
+// with two, 2 x 4096 x 4096, 3440 and 3350), but tiles outside the matrix are
+// (100 x 300 x 3000: 2297 and 2150).
 bool pays_to_pair(const Ortho& p) {
-  return p.count >= 2 && cdiv64(p.m, 256) * cdiv64(p.np, 256) * p.count >= 512;
+  const int64_t m = cdiv64(p.m, 256), update = m * cdiv64(p.np, 256) * p.count, gram = m * (m + 1) / 2 * p.count;
+  if (p.count < 2 || update < 512 || update_class(p) != TILE_BIG) return false;
+  const int64_t s = cdiv64(p.m, 128), inside = s * (s + 1) / 2 * p.count;
+  return gram_class(p) == TILE_BIG || (update >= 1024 && gram >= 192 && 3 * gram <= inside);
 }
 void skip_matrices(Ortho& p, int64_t n) {
   const int64_t x = n * p.m * p.np, a = n * p.m * p.mp;
@@ -540,7 +547,7 @@ hipError_t launch_orthogonalize(const Ortho& in, const OrthoStep* step, int step
     ortho_init_kernel<<<(unsigned)((int64_t)p.count * (p.np / 64) * cdiv64(p.m, 64)), 256, 0, s>>>(p);
     const int gram = gram_class(p), update = update_class(p);
     const int out = p.tall ? PHASE_OUT_T : PHASE_OUT;
-    if (gram == TILE_BIG && update == TILE_BIG && pays_to_pair(p)) {
+    if (pays_to_pair(p)) {
       // the second half of the matrices one phase behind the first
       Ortho q[2] = {p, p};
       q[0].count = (p.count + 1) / 2;

@@ -110,6 +110,29 @@ def test_coefficients_that_diverge_are_refused():
         rcd.orthogonalize(g, steps=4, coeffs=(40.0, -3.0, 0.1))
 
 
+# two halves of many large matrices, one phase apart: even and odd numbers, wide
+# and tall, one step (its first phase is its last but two)
+@pytest.mark.parametrize("B,shape,steps", [(52, (1000, 1100), 5), (47, (1100, 1000), 5), (40, (1024, 1100), 1),
+                                           (45, (1100, 1024), 2)])
+def test_halves(B, shape, steps):
+    d = dev()
+    say("orthogonalize halves", B, shape, steps)
+    g = torch.randn((B, *shape), generator=torch.Generator(device=d).manual_seed(6), device=d)
+    got = rcd.orthogonalize(g, steps=steps)
+    torch.cuda.synchronize()
+    for i in sorted({0, B // 2 - 1, B // 2, (B + 1) // 2, B - 1}):
+        x = g[i].double()
+        x = x.t() if shape[0] > shape[1] else x
+        x = x / (torch.linalg.vector_norm(x) + 1e-7)
+        for _ in range(steps):
+            a, b, c = ns.USUAL
+            p = x @ x.t()
+            x = a * x + (b * p + c * (p @ p)) @ x
+        x = x.t() if shape[0] > shape[1] else x
+        err = float(torch.linalg.vector_norm(got[i].double() - x) / torch.linalg.vector_norm(x))
+        assert err <= FLIPS + ARITHMETIC + ROUND, err
+
+
 @pytest.mark.parametrize("scale", [1e-30, 1e-20, 1e15, 3e30])
 def test_magnitudes(scale):
     """Sums of squares that leave fp32's range."""
