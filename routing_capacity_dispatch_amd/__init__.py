@@ -5,7 +5,9 @@ Thin torch binding over the C ABI in include/moe.h (libmoe.so).  torch only
 provides device memory and the current stream; every step of the branch runs
 in the HIP kernels of the library.  The same names as the C entry points:
 route, dispatch, experts, combine, forward, their *_backward transposes and
-BackwardRouted (moe_backward_routed), plus make_config / plan.
+BackwardRouted (moe_backward_routed), plus make_config / plan; and the layers
+around it: linear and linear_backward, orthogonalize (the update made of a
+weight's gradient) and ForwardFew (at most 16 tokens).
 """
 from __future__ import annotations
 
