@@ -399,9 +399,9 @@ struct Linear {
   int64_t ldpart;
   int tiles_m, tiles_n, shares, share_k;
 };
-// Tile sizes of a launch (256, 128 or 64 a side), and the shares of K of one
+// Tiles of a launch (256, 128, 128 or 64 a side), and the shares of K of one
 // of its products.
-enum TileClass : int { TILE_BIG = 0, TILE_SMALL = 1, TILE_DEEP = 2 };
+enum TileClass : int { TILE_BIG = 0, TILE_SMALL = 1, TILE_MID = 2, TILE_DEEP = 3 };
 struct LinearPlan {
   int cls;
   int shares, share_k;
@@ -410,7 +410,7 @@ struct LinearPlan {
 // Of a launch with so many tiles of 256 and 128 a side.
 int tile_class(int64_t big, int64_t small);
 // For one product of M0 x N0 results, or two in one launch.
-int linear_class(int64_t M0, int64_t N0, int64_t M1, int64_t N1);
+int linear_class(int64_t M0, int64_t N0, int64_t K0, int64_t M1, int64_t N1, int64_t K1);
 double linear_units(int cls, int64_t M, int64_t N, int64_t K);
 LinearPlan linear_plan(int cls, int64_t M, int64_t N, int64_t K, double units);
 // Rows of x and w on 16 bytes, with zeros from K to a multiple of 8, or (regs,

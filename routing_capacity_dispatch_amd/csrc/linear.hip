@@ -4,7 +4,7 @@
 //
 // Few rows, and small products, go straight from memory into matrix
 // instructions, the wavefronts of a workgroup sharing K.  The rest takes the
-// tiles of gemm_buf.h, in three sizes (below), the K of tiles that are few or
+// tiles of gemm_buf.h, in four kinds (below), the K of tiles that are few or
 // long shared by several workgroups.  Both products of a backward run in one
 // launch, so that one fills the compute units that the other leaves idle.
 #include "common.h"
@@ -19,11 +19,16 @@ using core::Acc;
 using core::dense_tile;
 using core::xcd_order;
 
-// All 160 KB of LDS, one workgroup a CU: the fastest where every CU has a
-// tile (16384 x 6144 x 6144: 1.02 ms, 128 x 128 tiles 1.35, 64 x 64 2.1)
+// All 160 KB of LDS, one workgroup a CU: the fastest where there are several
+// rounds of them (16384 x 6144 x 2048: 360 us, 128 x 128 tiles 400)
 using BigTile = core::Tile<256, 256, 4, 2, 64, 2, 3>;
-// Two workgroups a CU (2048 x 2048 x 2048: 33 us, big 59, 64 x 64 36)
-using SmallTile = core::Tile<128, 128, 2, 2, 64, 2, 2>;
+// Two workgroups of 8 wavefronts a CU, one's epilogue under the other's loop (6144 x
+// 4096 x 2048 with everything: 120 us, big tiles 145; with 4 wavefronts 4608 x 4096
+// x 2048 takes 107 instead of 89)
+using SmallTile = core::Tile<128, 128, 4, 2, 64, 2, 2>;
+// For at most one a CU, five K tiles in flight (2048 x 2048 x 2048: 24.5 us,
+// 28 with two; with 4 wavefronts 28)
+using MidTile = core::Tile<128, 128, 4, 2, 64, 5>;
 // Two workgroups a CU, five K tiles in flight each: for few tiles, whose time
 // is the loads' (512 x 2048 x 2048: 15 us, 128 x 128 30, or 26 with K shared;
 // nine K tiles in flight: the same)
@@ -511,12 +516,12 @@ __global__ __launch_bounds__(256) void slope_kernel(Slope p) {
 
 unsigned grid8(int64_t n) { return (unsigned)((n + 7) & ~int64_t(7)); }
 
-int tile_side(int cls) { return cls == TILE_BIG ? 256 : cls == TILE_SMALL ? 128 : 64; }
+int tile_side(int cls) { return cls == TILE_BIG ? 256 : cls == TILE_DEEP ? 64 : 128; }
 
-int slots_of(int cls) { return cls == TILE_BIG ? 256 : 512; }
+int slots_of(int cls) { return cls == TILE_BIG || cls == TILE_MID ? 256 : 512; }
 
 // Microseconds of one K tile of a workgroup, as measured with every slot taken.
-double k_tile_us(int cls) { return cls == TILE_BIG ? 1.6 : cls == TILE_SMALL ? 0.9 : 0.35; }
+double k_tile_us(int cls) { return cls == TILE_BIG ? 1.6 : cls == TILE_SMALL ? 0.9 : cls == TILE_MID ? 0.7 : 0.35; }
 
 void set_tiles(Linear& g, const LinearPlan& p) {
   const int side = tile_side(p.cls);
@@ -531,22 +536,38 @@ unsigned finish_grid(const Linear& g) { return g.shares > 1 ? (unsigned)cdiv64(g
 
 }  // namespace
 
-// The largest tile of which there are enough for the chip: 192 big ones keep
-// three quarters of the CUs busy, 256 of the middle size all of them.  But not big
-// ones whose last round is nearly empty, or that lie in large part outside the
-// product: 256 of the middle size, a CU's first or second, take 0.35 of the time of
-// 256 big ones (4608 x 4096 x 2048, 288 big ones: 120 us, 109 with 1152 of the
-// middle size; 6144 x 4096 x 2048, 384 of them: 119 and 126).
-int tile_class(int64_t big, int64_t small) {
-  if (big >= 192 && 20 * cdiv64(big, 256) <= 7 * cdiv64(small, 256)) return TILE_BIG;
-  return small >= 256 ? TILE_SMALL : TILE_DEEP;
+namespace {
+// Length in K tiles of n0 tiles of K k0 and n1 of k1 <= k0 on 256 CUs, the longer
+// ones first, the shorter ones beside those of the last round.
+int64_t rounds(int64_t n0, int64_t k0, int64_t n1, int64_t k1) {
+  const int64_t last = n0 % 256;
+  int64_t t = cdiv64(n0, 256) * k0;
+  if (last && k1 > 0) n1 -= (256 - last) * (k0 / k1);
+  return t + (n1 > 0 ? cdiv64(n1, 256) * k1 : 0);
 }
-// (The rounds of two products are of different lengths, and fill one another's:
-// 5000 x 2500 x 2500 with 300 big tiles 188 us, with 1200 of the middle size 198.)
-int linear_class(int64_t M0, int64_t N0, int64_t M1, int64_t N1) {
-  auto tiles = [&](int64_t side) { return cdiv64(M0, side) * cdiv64(N0, side) + cdiv64(M1, side) * cdiv64(N1, side); };
-  const bool two = M0 > 0 && M1 > 0;
-  return two && tiles(256) >= 192 ? TILE_BIG : tile_class(tiles(256), tiles(128));
+// 256 tiles of 128 a side, a CU's first or second, take 0.28 of the time of 256
+// of 256 a side (0.26 to 0.31 over 300 to 16384 rows).
+bool big_is_faster(int64_t big, int64_t small) { return 25 * big <= 7 * small; }
+int class_of(int64_t big, int64_t small, bool faster) {
+  return big >= 192 && faster ? TILE_BIG : small > 256 ? TILE_SMALL : small > 128 ? TILE_MID : TILE_DEEP;
+}
+}  // namespace
+
+// Big tiles where there are enough of them and their rounds of the chip come out
+// shorter: a last round that is nearly empty, and tiles that lie in large part
+// outside the product, count (gradients of 4096 x 2048 x 2048, 192 big tiles: 111
+// us, 72 with 768 of 128 a side; of 8192 x 2048 x 4096: 256 and 282).  Up to 256
+// of 128 a side have a CU each; down to 129 that is faster than twice as many
+// rounds of 64 a side (1536 x 2048 x 2048 24 and 30 us, 1024 x 2048 x 2048 24 and 20).
+int tile_class(int64_t big, int64_t small) {
+  return class_of(big, small, big_is_faster(rounds(big, 1, 0, 0), rounds(small, 1, 0, 0)));
+}
+int linear_class(int64_t M0, int64_t N0, int64_t K0, int64_t M1, int64_t N1, int64_t K1) {
+  if (K0 < K1) return linear_class(M1, N1, K1, M0, N0, K0);
+  auto tiles = [](int64_t M, int64_t N, int64_t side) { return cdiv64(M, side) * cdiv64(N, side); };
+  const int64_t b0 = tiles(M0, N0, 256), b1 = tiles(M1, N1, 256), s0 = tiles(M0, N0, 128), s1 = tiles(M1, N1, 128);
+  const int64_t k0 = cdiv64(K0, 64), k1 = cdiv64(K1, 64);
+  return class_of(b0 + b1, s0 + s1, big_is_faster(rounds(b0, k0, b1, k1), rounds(s0, k0, s1, k1)));
 }
 
 double linear_units(int cls, int64_t M, int64_t N, int64_t K) {
@@ -590,6 +611,8 @@ hipError_t launch_linear_tiles(const Linear& in, const LinearPlan& p, bool regs,
     linear_tile_kernel<BigTile, false><<<grid, BigTile::THREADS, 0, s>>>(g);
   else if (p.cls == TILE_SMALL)
     linear_tile_kernel<SmallTile, false><<<grid, SmallTile::THREADS, 0, s>>>(g);
+  else if (p.cls == TILE_MID)
+    linear_tile_kernel<MidTile, false><<<grid, MidTile::THREADS, 0, s>>>(g);
   else if (!regs)
     linear_tile_kernel<DeepTile, false><<<grid, DeepTile::THREADS, 0, s>>>(g);
   else
@@ -644,6 +667,8 @@ hipError_t launch_linear_grads(const LinearGrads& in, const LinearPlan& pw, cons
     linear_grads_kernel<BigTile, false><<<grid, BigTile::THREADS, 0, s>>>(p);
   else if (pw.cls == TILE_SMALL)
     linear_grads_kernel<SmallTile, false><<<grid, SmallTile::THREADS, 0, s>>>(p);
+  else if (pw.cls == TILE_MID)
+    linear_grads_kernel<MidTile, false><<<grid, MidTile::THREADS, 0, s>>>(p);
   else if (!regs)
     linear_grads_kernel<DeepTile, false><<<grid, DeepTile::THREADS, 0, s>>>(p);
   else

@@ -2061,7 +2061,7 @@ int64_t carve_linear(const moe_linear_args* a, void* ws, LinearWs* w) {
   *w = LinearWs{};
   if (a->M == 0 || a->N == 0 || moe::linear_streams(a->M, a->N, a->K)) return 0;
   const int64_t K8 = align8(a->K);
-  const int cls = moe::linear_class(a->M, a->N, 0, 0);
+  const int cls = moe::linear_class(a->M, a->N, a->K, 0, 0, 0);
   w->plan = moe::linear_plan(cls, a->M, a->N, K8, moe::linear_units(cls, a->M, a->N, K8));
   const bool whole = a->K % 8 == 0, x = whole && tile_rows(a->x, a->ldx), y = whole && tile_rows(a->w, a->ldw);
   if (cls == moe::TILE_DEEP) {
@@ -2166,7 +2166,7 @@ int64_t carve_linear_grad(const moe_linear_grad* a, void* ws, LinearGradWs* w) {
   *w = LinearGradWs{};
   const int64_t N8 = align8(a->N), K8 = align8(a->K);
   const bool dx = a->dx != nullptr, dw = a->dw != nullptr;
-  const int cls = moe::linear_class(dw ? a->N : 0, a->K, dx ? a->M : 0, a->K);
+  const int cls = moe::linear_class(dw ? a->N : 0, a->K, a->M, dx ? a->M : 0, a->K, a->N);
   const double units = (dw ? moe::linear_units(cls, a->N, a->K, a->M) : 0.0) +
                        (dx ? moe::linear_units(cls, a->M, a->K, a->N) : 0.0);
   w->dw = moe::linear_plan(cls, a->N, a->K, a->M, units);

@@ -32,7 +32,8 @@ using core::acc_row;
 using core::xcd_order;
 
 using BigTile = core::Tile<256, 256, 4, 2, 64, 2, 3>;
-using SmallTile = core::Tile<128, 128, 2, 2, 64, 2, 2>;
+using SmallTile = core::Tile<128, 128, 4, 2, 64, 2, 2>;
+using MidTile = core::Tile<128, 128, 4, 2, 64, 5>;
 using DeepTile = core::Tile<64, 64, 2, 2, 64, 5>;
 
 int64_t cdiv64(int64_t a, int64_t b) { return (a + b - 1) / b; }
@@ -441,6 +442,8 @@ void run_class(const Ortho& p, int cls, int phase, hipStream_t s) {
     run_phase<BigTile>(p, phase, s);
   else if (cls == TILE_SMALL)
     run_phase<SmallTile>(p, phase, s);
+  else if (cls == TILE_MID)
+    run_phase<MidTile>(p, phase, s);
   else
     run_phase<DeepTile>(p, phase, s);
 }
