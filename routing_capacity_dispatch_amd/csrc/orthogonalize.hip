@@ -490,7 +490,7 @@ constexpr int kSplitSide = 256;
 bool ortho_split(int64_t m) { return m < kSplitSide; }
 
 namespace {
-// Tile sizes as of other products (100 matrices of 300 x 300: 361 us, 571 with
+// Tile sizes as of other products (100 matrices of 300 x 300: 330 us, 571 with
 // big tiles); the big one is not for two fp16 numbers of X.
 int class_of(int64_t big, int64_t small, bool split) { return tile_class(split ? 0 : big, small); }
 int gram_class(const Ortho& p) {
@@ -501,18 +501,15 @@ int update_class(const Ortho& p) {
   auto tiles = [&](int64_t side) { return cdiv64(p.m, side) * cdiv64(p.np, side) * p.count; };
   return class_of(tiles(256), tiles(128), p.split);
 }
-// Two phases a launch pay where each has several rounds of the chip: the
-// matrix instructions of one then run under the other's traffic (an update
-// moves 8 bytes a value in its epilogue), and rounds end in common.  With four
-// rounds of updates a nearly empty last round of A's and B's tiles is no matter
-// (8 x 2048 x 4096: 3028 us, 3287 with middle-size tiles of A and B and no pairs;
-// with two, 2 x 4096 x 4096, 3440 and 3350), but tiles outside the matrix are
-// (100 x 300 x 3000: 2297 and 2150).
+// Two phases a launch: the matrix instructions of one run under the other's
+// traffic (an update moves 8 bytes a value in its epilogue), and rounds end in
+// common.  That pays for wide matrices, whose update is the longest phase, with
+// four rounds of big tiles of it (12 x 2048 x 4096: 4300 us, 4630 one by one; 8 of
+// them 3075 and 3200; 32 x 1024 x 3000: 2735 and 2885), and not for square or
+// small ones (64 x 1024 x 1024: 2490 and 2420; 100 x 512 x 2048: 2200 and 2135).
 bool pays_to_pair(const Ortho& p) {
-  const int64_t m = cdiv64(p.m, 256), update = m * cdiv64(p.np, 256) * p.count, gram = m * (m + 1) / 2 * p.count;
-  if (p.count < 2 || update < 512 || update_class(p) != TILE_BIG) return false;
-  const int64_t s = cdiv64(p.m, 128), inside = s * (s + 1) / 2 * p.count;
-  return gram_class(p) == TILE_BIG || (update >= 1024 && gram >= 192 && 3 * gram <= inside);
+  const int64_t m = cdiv64(p.m, 256), n = cdiv64(p.np, 256);
+  return p.count >= 2 && m >= 4 && n >= 2 * m && m * n * p.count >= 1024 && update_class(p) == TILE_BIG;
 }
 void skip_matrices(Ortho& p, int64_t n) {
   const int64_t x = n * p.m * p.np, a = n * p.m * p.mp;

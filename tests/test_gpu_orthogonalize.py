@@ -113,7 +113,8 @@ def test_coefficients_that_diverge_are_refused():
 # two halves of many large matrices, one phase apart: even and odd numbers, wide
 # and tall, one step (its first phase is its last but two)
 @pytest.mark.parametrize("B,shape,steps", [(52, (1000, 1100), 5), (47, (1100, 1000), 5), (40, (1024, 1100), 1),
-                                           (45, (1100, 1024), 2)])
+                                           (45, (1100, 1024), 2), (32, (1024, 2048), 5), (35, (1000, 2000), 5),
+                                           (35, (2000, 1000), 1), (32, (2048, 1024), 2)])
 def test_halves(B, shape, steps):
     d = dev()
     say("orthogonalize halves", B, shape, steps)
