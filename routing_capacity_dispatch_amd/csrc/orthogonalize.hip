@@ -497,9 +497,11 @@ int gram_class(const Ortho& p) {
   auto tiles = [&](int64_t side) { return cdiv64(p.m, side) * (cdiv64(p.m, side) + 1) / 2 * p.count; };
   return class_of(tiles(256), tiles(128), p.split);
 }
+// (Up to 8 K tiles an update is mostly its epilogue, which two workgroups a CU hide:
+// 64 x 512 x 512 441 us, 459 with big tiles; 64 x 1024 x 1024 2415 and 2370.)
 int update_class(const Ortho& p) {
   auto tiles = [&](int64_t side) { return cdiv64(p.m, side) * cdiv64(p.np, side) * p.count; };
-  return class_of(tiles(256), tiles(128), p.split);
+  return class_of(tiles(256), tiles(128), p.split || p.mp <= 512);
 }
 // Two phases a launch: the matrix instructions of one run under the other's
 // traffic (an update moves 8 bytes a value in its epilogue), and rounds end in
