@@ -815,7 +815,9 @@ moe_status moe_linear_backward(const moe_linear_grad* args, void* ws, size_t ws_
  * products take the first of the two (both where the smaller side is below
  * 256), and A and B off their diagonals, rounded to fp16 (11 bits), with fp32
  * sums.  Over five steps with (3.4445, -4.7750, 2.0315) that
- * leaves the result within 1.5e-3 of its norm; its rounding to bf16 is 1.7e-3.
+ * leaves the result within 2e-3 of its norm, 3.5e-3 where a few rows or values
+ * of one magnitude carry the matrix, and 5e-3 where a handful of values do; its
+ * rounding to bf16 is 1.7e-3.
  * ------------------------------------------------------------------------ */
 typedef struct {
   int64_t batch, M, N;

@@ -474,11 +474,12 @@ struct Ortho {
   bool split;
   int chunks;           // shares of a norm
   int count, cur, gram_tiles, tiles_m, tiles_n;
-  float ca, cb, cc, sx, inv_sx, sa, inv_sa, sb, inv_sb, sx_next;
+  float ca, cb, cc, sx, inv_sx, sa, inv_sa, sb, inv_sb, sx_next, low;
 };
 struct OrthoStep {
   float a, b, c;        // coefficients
   float sx, sa, sb;     // powers of two that X, A and B are held in fp16 with
+  float low;            // share of B's diagonal that X's second fp16 number is given
 };
 int ortho_norm_chunks();
 bool ortho_split(int64_t m);

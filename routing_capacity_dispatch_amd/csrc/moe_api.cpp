@@ -2281,15 +2281,20 @@ float fp16_scale(double most) {
 // roundings of a step.
 moe_status ortho_steps(const moe_ortho_args* a, moe::OrthoStep* out) {
   double m = 1.0;
+  double gain[kMaxOrthoSteps];  // most that a step multiplies a singular value by
   for (int k = 0; k < a->steps; ++k) {
     const double ca = a->coeffs[3 * k], cb = a->coeffs[3 * k + 1], cc = a->coeffs[3 * k + 2];
     if (!isfinite(ca) || !isfinite(cb) || !isfinite(cc)) return MOE_ERR_INVALID_ARG;
     const double y = m * m;
-    // |b y + c y^2| on [0, m^2], and |a s + b s^3 + c s^5| on [0, m]
+    // |b t + c t^2| and |a + b t + c t^2| on [0, m^2], and |a s + b s^3 + c s^5| on [0, m]
     double q = fabs(cb * y + cc * y * y);
+    gain[k] = fmax(fabs(ca), fabs(ca + cb * y + cc * y * y));
     if (cc != 0.0) {
-      const double t = -cb / (2.0 * cc);
-      if (t > 0.0 && t < y && fabs(cb * t + cc * t * t) > q) q = fabs(cb * t + cc * t * t);
+      const double t = -cb / (2.0 * cc), v = cb * t + cc * t * t;
+      if (t > 0.0 && t < y) {
+        q = fmax(q, fabs(v));
+        gain[k] = fmax(gain[k], fabs(ca + v));
+      }
     }
     auto poly = [&](double s) { return fabs(s * (ca + s * s * (cb + cc * s * s))); };
     double p = poly(m);
@@ -2317,6 +2322,12 @@ moe_status ortho_steps(const moe_ortho_args* a, moe::OrthoStep* out) {
     out[k].sb = fp16_scale(q * slack);
     m = p * slack;
     if (!(m < kMaxSingular) || !(q < kMaxSingular * kMaxSingular)) return MOE_ERR_UNSUPPORTED;
+  }
+  // what a step leaves behind grows by the gains of those after it
+  double later = 1.0;
+  for (int k = a->steps - 1; k >= 0; --k) {
+    out[k].low = later > 1.0 ? (float)(1.0 / later) : 1.0f;
+    later = fmin(later * gain[k], 1e30);
   }
   return MOE_OK;
 }

@@ -6,14 +6,23 @@
 // The three products run on fp16 matrix instructions (gemm_buf.h) with fp32
 // sums.  X itself is held in two fp16 numbers, h + l (22 bits), and the diagonals
 // of A and B, where their weight is, in fp32; the products see h, and A and B off
-// their diagonals, rounded to fp16 (11 bits).  Then the rounding touches neither
-// the a X + diag(B) X that carries small singular values nor the cancellation
-// between a and diag(B), and the result is off by 3e-4 to 1.5e-3 of its norm
-// over five steps of the usual coefficients, whatever the spectrum, less than
-// its final rounding to bf16.  (h alone: 1.2e-3 to 0.12, for a matrix of nearly
-// rank one; bf16 products: 1.4e-3 to 2e-2.)  Matrices with a side below
-// kSplitSide, where one direction of a few is a large part of A's rows (up to
-// 1e-2), take l as well in both products with X: 1e-3 at most.
+// their diagonals, rounded to fp16 (11 bits).
+//
+// An update is a (h + l) + B h: the polynomial of h and a times l.  h = X - l has
+// singular values of l's size where X has none; they grow by a as l's own do, and
+// the two cancel.  A part of B times a part of l only, as its diagonal (which would
+// spare a full-rank X the rounding: there B is mostly diagonal), breaks that, and
+// what is left grows by `a` in every later step: up to 4e-2 of the result's norm
+// where a few rows carry the matrix.  So l's diagonal term has the weight 1 / (the
+// later steps' gains), which keeps what it leaves at the last step's size.  The
+// result is off by 2e-4 to 2e-3 of its norm over five steps of the usual
+// coefficients, up to 3.5e-3 where a few rows or values of one magnitude carry the
+// matrix and 5e-3 where a handful of values do; its final rounding to bf16 is
+// 1.7e-3.  (h alone: 1.2e-3 to 0.12, for a matrix of nearly rank one; bf16 products:
+// 1.4e-3 to 2e-2.)  Matrices with a side below kSplitSide, where one direction of a
+// few is a large part of A's rows, take l as well in both products with X: 3.5e-3
+// at most.  Larger ones would come to half of the above by that, for about twice
+// the matrix instructions.
 // fp16's range is no matter: the host bounds the singular values of every
 // step and scales X, A and B by powers of two to fill it.
 //
@@ -267,7 +276,8 @@ __device__ __forceinline__ void gram_tile(const Ortho& p, int t, char* lds) {
   });
 }
 
-// X = a X + B X = (a + d_i) X_i + (R X)_i, R being B off its diagonal d.
+// X = a X + B X = (a + d_i) h_i + (a + w d_i) l_i + (R X)_i, R being B off its
+// diagonal d; R X of h and l and w = 1 with kSplit, else of h and w as above.
 // kLast 0: into X; 1: the result, as G lies; 2: the result, transposed.
 template <class TL, int kLast, bool kSplit>
 __device__ __forceinline__ void update_tile(const Ortho& p, int t, char* lds) {
@@ -298,9 +308,13 @@ __device__ __forceinline__ void update_tile(const Ortho& p, int t, char* lds) {
 #pragma unroll
     for (int mi = 0; mi < TL::MI; ++mi) {
       const int row = m0 + acc_row<TL>(wm, mi, lane, 0);
-      float d[4];
+      float dh[4], dl[4];
 #pragma unroll
-      for (int r = 0; r < 4; ++r) d[r] = (p.ca + dB[min(row + r, p.m - 1)]) * p.inv_sx;
+      for (int r = 0; r < 4; ++r) {
+        const float d = dB[min(row + r, p.m - 1)];
+        dh[r] = (p.ca + d) * p.inv_sx;
+        dl[r] = fmaf(p.low, d, p.ca) * p.inv_sx;
+      }
 #pragma unroll
       for (int ni = 0; ni < TL::NI; ++ni) {
         const int col = n0 + acc_col<TL>(wn, ni, lane);
@@ -309,7 +323,7 @@ __device__ __forceinline__ void update_tile(const Ortho& p, int t, char* lds) {
 #pragma unroll
         for (int r = 0; r < 4; ++r) {
           const int64_t at = (int64_t)min(row + r, p.m - 1) * p.np + col;
-          v[r] = p.scale * fmaf(d[r], f16_at(xh[at], 0) + f16_at(xl[at], 0), acc.v[mi][ni][r] * inv);
+          v[r] = p.scale * fmaf(dh[r], f16_at(xh[at], 0), fmaf(dl[r], f16_at(xl[at], 0), acc.v[mi][ni][r] * inv));
         }
         uint16_t* o = out + (int64_t)col * p.ldo + row;
         if (p.vec_out && row + 4 <= p.m) {
@@ -335,12 +349,12 @@ __device__ __forceinline__ void update_tile(const Ortho& p, int t, char* lds) {
         [&](int r, int c, float* v, const Ahead& q) {
           const int row = m0 + r, col = n0 + c;
           if (col >= p.np) return;
-          const float d = (p.ca + q.d) * p.inv_sx;
+          const float dh = (p.ca + q.d) * p.inv_sx, dl = fmaf(p.low, q.d, p.ca) * p.inv_sx;
           float x[8], y[8];
           f16_unpack(q.h, x);
           f16_unpack(q.l, y);
 #pragma unroll
-          for (int i = 0; i < 8; ++i) x[i] = fmaf(d, x[i] + y[i], v[i] * inv);
+          for (int i = 0; i < 8; ++i) x[i] = fmaf(dh, x[i], fmaf(dl, y[i], v[i] * inv));
           if constexpr (kLast == 0) {
             const int64_t at = xo + (int64_t)row * p.np + col;
 #pragma unroll
@@ -480,6 +494,7 @@ void set_step(Ortho& p, const OrthoStep* step, int steps, int k) {
   p.sb = c.sb;
   p.inv_sb = 1.0f / c.sb;
   p.sx_next = k + 1 < steps ? step[k + 1].sx : 1.0f;
+  p.low = p.split ? 1.0f : c.low;
 }
 
 }  // namespace
