@@ -906,12 +906,24 @@ def linear_backward(dy, x, w, pre=None, act: str = "none", bias: bool = True, ne
 
 
 # --------------------------------------------------- orthogonalised updates
+_COEFFS = "coeffs is (a, b, c), or one of them for each step"
+
+
 @functools.lru_cache(maxsize=64)
+def _coefficient_array(coeffs, steps):
+    rows = list(coeffs) if any(isinstance(c, tuple) for c in coeffs) else [coeffs] * steps
+    _check(len(rows) == steps and all(isinstance(r, tuple) and len(r) == 3 for r in rows), _COEFFS)
+    return (C.c_float * (3 * steps))(*[v for r in rows for v in r])
+
+
 def _coefficients(coeffs, steps):
-    """[steps][3] fp32 on the host of one (a, b, c), or of one for each step."""
-    rows = [coeffs] * steps if not any(isinstance(c, tuple) for c in coeffs) else list(coeffs)
-    _check(len(rows) == steps and all(isinstance(r, tuple) and len(r) == 3 for r in rows), "coeffs is (a, b, c), or one of them for each step")
-    return (C.c_float * (3 * steps))(*[float(v) for r in rows for v in r])
+    """[steps][3] fp32 on the host of one (a, b, c), or of one for each step.
+    What is kept between calls is kept for their values: any number is read anew."""
+    try:
+        values = tuple(tuple(map(float, c)) if isinstance(c, (list, tuple)) else float(c) for c in coeffs)
+    except (TypeError, ValueError, RuntimeError):
+        raise ValueError(_COEFFS) from None
+    return _coefficient_array(values, steps)
 
 
 def _batch(t, what):
@@ -943,7 +955,7 @@ def orthogonalize(g, steps: int = 5, coeffs=(3.4445, -4.7750, 2.0315), eps: floa
     ldg, sg = _batch(g3, "g")
     ldo, so = _batch(o3, "out")
     _check(1 <= steps <= 64, "steps is 1 to 64")
-    co = _coefficients(tuple(tuple(c) if isinstance(c, (list, tuple)) else c for c in coeffs), steps)
+    co = _coefficients(coeffs, steps)
     a = abi.MoeOrthoArgs(B, M, N, g.data_ptr(), ldg, sg, out.data_ptr(), ldo, so, co, steps, _DT[g.dtype], eps, scale, 0)
     _with_workspace("moe_orthogonalize", dev, a, ws)
     return out
