@@ -739,7 +739,9 @@ moe_status moe_forward_dropless_quant(const moe_config* cfg, const moe_scoring* 
  * each result rounded once.  Rows may be strided (ld in elements, at least
  * the row's length, at most 2^22), at any alignment; sizes are any, 0
  * included.  M up to 2^30, N and K up to 2^22; MOE_ERR_UNSUPPORTED past that
- * or past 2^23 - 8 tiles of 128 x 128.
+ * or past 2^23 - 8 tiles of 128 x 128 (both gradients' together, less N / 64),
+ * and where 2^35 values or more of x and w have to be copied first: rows off 16
+ * bytes, or K no multiple of 8, in a product of more than 128 tiles.
  * ------------------------------------------------------------------------ */
 typedef enum {
   MOE_ACT_NONE = 0,

@@ -2011,6 +2011,11 @@ constexpr int64_t kMaxSlopeRows = 65535 * 32;  // one grid row for 32 rows of d
 
 int64_t align8(int64_t x) { return (x + 7) & ~int64_t(7); }
 
+// a launch has fewer than 2^32 threads: one of every 8 values that are copied
+bool copies_fit(int64_t x_rows, int64_t w_rows, int64_t K8) {
+  return ceil_div(x_rows * (K8 / 8), 256) + ceil_div(w_rows * (K8 / 8), 256) < (int64_t(1) << 24);
+}
+
 // rows can be read by the tiles as they are
 bool tile_rows(const void* p, int64_t ld) { return aligned16(p) && ld % 8 == 0; }
 
@@ -2052,6 +2057,7 @@ moe_status check_linear(const moe_linear_args* a) {
 struct LinearWs {
   moe::LinearPlan plan;
   bool regs;  // the operands are taken as they lie, by way of registers
+  bool fits;  // the copies' launch
   void* x;    // copies in whole 16 bytes, or null
   void* w;
   void* part;
@@ -2059,6 +2065,7 @@ struct LinearWs {
 int64_t carve_linear(const moe_linear_args* a, void* ws, LinearWs* w) {
   Carver cv{static_cast<char*>(ws), 0};
   *w = LinearWs{};
+  w->fits = true;
   if (a->M == 0 || a->N == 0 || moe::linear_streams(a->M, a->N, a->K)) return 0;
   const int64_t K8 = align8(a->K);
   const int cls = moe::linear_class(a->M, a->N, a->K, 0, 0, 0);
@@ -2069,6 +2076,7 @@ int64_t carve_linear(const moe_linear_args* a, void* ws, LinearWs* w) {
   } else if (a->K > 0) {
     if (!x) w->x = cv.take(a->M * K8 * 2);
     if (!y) w->w = cv.take(a->N * K8 * 2);
+    w->fits = copies_fit(x ? 0 : a->M, y ? 0 : a->N, K8);
   }
   if (w->plan.part_bytes) w->part = cv.take(w->plan.part_bytes);
   return cv.used;
@@ -2081,7 +2089,9 @@ MOE_API moe_status moe_linear_ws_bytes(const moe_linear_args* args, size_t* byte
   if (st != MOE_OK) return st;
   if (!bytes) return MOE_ERR_INVALID_ARG;
   LinearWs w;
-  *bytes = (size_t)carve_linear(args, nullptr, &w);
+  const int64_t need = carve_linear(args, nullptr, &w);
+  if (!w.fits) return MOE_ERR_UNSUPPORTED;
+  *bytes = (size_t)need;
   return MOE_OK;
 }
 
@@ -2093,6 +2103,7 @@ MOE_API moe_status moe_linear(const moe_linear_args* args, void* ws, size_t ws_b
   if (!a.y || (a.K > 0 && (!a.x || !a.w))) return MOE_ERR_INVALID_ARG;
   LinearWs w;
   const int64_t need = carve_linear(args, nullptr, &w);
+  if (!w.fits) return MOE_ERR_UNSUPPORTED;
   if (need > 0 && (!ws || !aligned256(ws) || (int64_t)ws_bytes < need)) return MOE_ERR_WORKSPACE;
   carve_linear(args, need > 0 ? ws : nullptr, &w);
   hipStream_t s = static_cast<hipStream_t>(stream);
@@ -2138,6 +2149,10 @@ moe_status check_linear_grad(const moe_linear_grad* a) {
   if (!valid_dtype(a->dy_dtype) || !valid_act(a->act) || a->reserved != 0) return MOE_ERR_INVALID_ARG;
   moe_status st = check_linear_sizes(a->M, a->N, a->K);
   if (st == MOE_OK && a->M > kMaxSlopeRows) st = MOE_ERR_UNSUPPORTED;
+  // both products and the sums of db are one launch
+  if (st == MOE_OK &&
+      (ceil_div(a->N, 128) + ceil_div(a->M, 128)) * ceil_div(a->K, 128) + ceil_div(a->N, 64) > kMaxListEntries - 16)
+    st = MOE_ERR_UNSUPPORTED;
   if (st == MOE_OK) st = check_ld(a->lddy, a->N);
   if (st == MOE_OK && a->act != MOE_ACT_NONE) st = check_ld(a->ldp, a->N);
   if (st == MOE_OK && a->dw) st = check_ld(a->ldx, a->K);
@@ -2154,6 +2169,7 @@ moe_status check_linear_grad(const moe_linear_grad* a) {
 struct LinearGradWs {
   moe::LinearPlan dw, dx;
   bool regs;    // x and w are taken as they lie, by way of registers
+  bool fits;    // the copies' launch
   void* d;      // bf16 [M][N rounded up to 8], or null: dy itself
   float* sums;  // partial sums of db
   void* x;      // copies in whole 16 bytes, or null
@@ -2184,6 +2200,7 @@ int64_t carve_linear_grad(const moe_linear_grad* a, void* ws, LinearGradWs* w) {
     if (x) w->x = cv.take(a->M * K8 * 2);
     if (y) w->w = cv.take(a->N * K8 * 2);
   }
+  w->fits = !products || w->regs || copies_fit(x ? a->M : 0, y ? a->N : 0, K8);
   if (dw && w->dw.part_bytes) w->part_dw = cv.take(w->dw.part_bytes);
   if (dx && w->dx.part_bytes) w->part_dx = cv.take(w->dx.part_bytes);
   return cv.used;
@@ -2196,7 +2213,9 @@ MOE_API moe_status moe_linear_backward_ws_bytes(const moe_linear_grad* args, siz
   if (st != MOE_OK) return st;
   if (!bytes) return MOE_ERR_INVALID_ARG;
   LinearGradWs w;
-  *bytes = (size_t)carve_linear_grad(args, nullptr, &w);
+  const int64_t need = carve_linear_grad(args, nullptr, &w);
+  if (!w.fits) return MOE_ERR_UNSUPPORTED;
+  *bytes = (size_t)need;
   return MOE_OK;
 }
 
@@ -2210,6 +2229,7 @@ MOE_API moe_status moe_linear_backward(const moe_linear_grad* args, void* ws, si
   }
   LinearGradWs w;
   const int64_t need = carve_linear_grad(args, nullptr, &w);
+  if (!w.fits) return MOE_ERR_UNSUPPORTED;
   if (need > 0 && (!ws || !aligned256(ws) || (int64_t)ws_bytes < need)) return MOE_ERR_WORKSPACE;
   carve_linear_grad(args, need > 0 ? ws : nullptr, &w);
   hipStream_t s = static_cast<hipStream_t>(stream);
