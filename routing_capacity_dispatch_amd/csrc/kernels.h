@@ -483,6 +483,12 @@ struct OrthoStep {
 };
 int ortho_norm_chunks();
 bool ortho_split(int64_t m);
+// What the matrices of one group take.
+struct OrthoForm {
+  int gram, update;  // TileClass
+  bool split, paired;
+};
+OrthoForm ortho_form(const Ortho& p, int64_t count);
 int64_t ortho_group(int64_t batch, int64_t m, int64_t n);
 hipError_t launch_orthogonalize(const Ortho& p, const OrthoStep* step, int steps, int64_t batch, int64_t group,
                                 hipStream_t s);

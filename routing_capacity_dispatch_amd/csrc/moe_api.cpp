@@ -2528,3 +2528,43 @@ MOE_API moe_status moe_forward_few(const moe_config* cfg, const moe_weights* w, 
   f.ws_down = bf16(w->ws_down);
   return hip_status(moe::launch_few(f, static_cast<hipStream_t>(stream)));
 }
+
+// ------------------------------------------------------------------ which kernels a call takes
+// For tests (no part of moe.h): tests that are to reach a kernel ask here
+// whether their sizes still do.  -1: refused.
+//   linear    bits 0-2: 0 nothing, 1 + tile class, 5 straight from memory; 3: operands by way of registers; 4, 5: x, w
+//             copied; 6: K shared
+//   backward  bits 0-2: 1 + tile class; 3-5 likewise; 6, 7: K of dw, of dx shared; 8: d made
+//   updates   of the first group: bits 0-2, 3-5: 1 + tile class of A and B, of X; 6: both fp16 numbers in the products;
+//             7: two halves
+namespace {
+void* const kAnyWs = reinterpret_cast<void*>(uintptr_t(256));
+}
+MOE_API int moe_linear_form(const moe_linear_args* args) {
+  if (check_linear(args) != MOE_OK) return -1;
+  if (args->M == 0 || args->N == 0) return 0;
+  if (moe::linear_streams(args->M, args->N, args->K)) return 5;
+  LinearWs w;
+  carve_linear(args, kAnyWs, &w);
+  return !w.fits ? -1
+                 : (1 + w.plan.cls) | w.regs << 3 | (w.x != nullptr) << 4 | (w.w != nullptr) << 5 |
+                       (w.plan.shares > 1) << 6;
+}
+MOE_API int moe_linear_backward_form(const moe_linear_grad* args) {
+  if (check_linear_grad(args) != MOE_OK) return -1;
+  LinearGradWs w;
+  carve_linear_grad(args, kAnyWs, &w);
+  return !w.fits ? -1
+                 : (1 + w.dw.cls) | w.regs << 3 | (w.x != nullptr) << 4 | (w.w != nullptr) << 5 |
+                       (w.part_dw != nullptr) << 6 | (w.part_dx != nullptr) << 7 | (w.d != nullptr) << 8;
+}
+MOE_API int moe_orthogonalize_form(const moe_ortho_args* args) {
+  moe::OrthoStep steps[kMaxOrthoSteps];
+  if (check_ortho(args, steps) != MOE_OK) return -1;
+  if (args->batch == 0 || args->M == 0 || args->N == 0) return 0;
+  moe::Ortho p{};
+  int64_t group;
+  carve_ortho(args, kAnyWs, &p, &group);
+  const moe::OrthoForm f = moe::ortho_form(p, group);
+  return (1 + f.gram) | (1 + f.update) << 3 | f.split << 6 | f.paired << 7;
+}

@@ -542,6 +542,13 @@ void skip_matrices(Ortho& p, int64_t n) {
 }
 }  // namespace
 
+OrthoForm ortho_form(const Ortho& in, int64_t count) {
+  Ortho p = in;
+  p.count = (int)count;
+  p.split = ortho_split(p.m);
+  return OrthoForm{gram_class(p), update_class(p), p.split, pays_to_pair(p)};
+}
+
 // Matrices at a time: enough tiles of the update for several rounds of the
 // chip, so that more would only need more workspace.
 int64_t ortho_group(int64_t batch, int64_t m, int64_t n) {
@@ -558,13 +565,13 @@ hipError_t launch_orthogonalize(const Ortho& in, const OrthoStep* step, int step
     p.b0 = b0;
     p.count = (int)(batch - b0 < group ? batch - b0 : group);
     p.sx = step[0].sx;
-    p.split = ortho_split(p.m);
+    const OrthoForm form = ortho_form(p, p.count);
+    p.split = form.split;
     p.chunks = p.count > 1024 / kNormChunks ? (p.count > 1024 / 16 ? 16 : 1024 / p.count) : kNormChunks;
     ortho_norm_kernel<<<(unsigned)(p.count * p.chunks), 256, 0, s>>>(p);
     ortho_init_kernel<<<(unsigned)((int64_t)p.count * (p.np / 64) * cdiv64(p.m, 64)), 256, 0, s>>>(p);
-    const int gram = gram_class(p), update = update_class(p);
     const int out = p.tall ? PHASE_OUT_T : PHASE_OUT;
-    if (pays_to_pair(p)) {
+    if (form.paired) {
       // the second half of the matrices one phase behind the first
       Ortho q[2] = {p, p};
       q[0].count = (p.count + 1) / 2;
@@ -584,9 +591,9 @@ hipError_t launch_orthogonalize(const Ortho& in, const OrthoStep* step, int step
     } else {
       for (int k = 0; k < steps; ++k) {
         set_step(p, step, steps, k);
-        run_class(p, gram, PHASE_A, s);
-        run_class(p, gram, PHASE_B, s);
-        run_class(p, update, k + 1 < steps ? PHASE_X : out, s);
+        run_class(p, form.gram, PHASE_A, s);
+        run_class(p, form.gram, PHASE_B, s);
+        run_class(p, form.update, k + 1 < steps ? PHASE_X : out, s);
       }
     }
     const hipError_t e = hipGetLastError();
