@@ -486,7 +486,7 @@ bool ortho_split(int64_t m);
 // What the matrices of one group take.
 struct OrthoForm {
   int gram, update;  // TileClass
-  bool split, paired;
+  bool split;
 };
 OrthoForm ortho_form(const Ortho& p, int64_t count);
 int64_t ortho_group(int64_t batch, int64_t m, int64_t n);

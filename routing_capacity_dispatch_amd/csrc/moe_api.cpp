@@ -2535,8 +2535,7 @@ MOE_API moe_status moe_forward_few(const moe_config* cfg, const moe_weights* w, 
 //   linear    bits 0-2: 0 nothing, 1 + tile class, 5 straight from memory; 3: operands by way of registers; 4, 5: x, w
 //             copied; 6: K shared
 //   backward  bits 0-2: 1 + tile class; 3-5 likewise; 6, 7: K of dw, of dx shared; 8: d made
-//   updates   of the first group: bits 0-2, 3-5: 1 + tile class of A and B, of X; 6: both fp16 numbers in the products;
-//             7: two halves
+//   updates   of the first group: bits 0-2, 3-5: 1 + tile class of A and B, of X; 6: both fp16 numbers in the products
 namespace {
 void* const kAnyWs = reinterpret_cast<void*>(uintptr_t(256));
 }
@@ -2566,5 +2565,5 @@ MOE_API int moe_orthogonalize_form(const moe_ortho_args* args) {
   int64_t group;
   carve_ortho(args, kAnyWs, &p, &group);
   const moe::OrthoForm f = moe::ortho_form(p, group);
-  return (1 + f.gram) | (1 + f.update) << 3 | f.split << 6 | f.paired << 7;
+  return (1 + f.gram) | (1 + f.update) << 3 | f.split << 6;
 }

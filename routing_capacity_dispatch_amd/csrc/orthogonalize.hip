@@ -405,22 +405,6 @@ __global__ __launch_bounds__(TL::THREADS) void ortho_phase_kernel(Ortho p) {
   if (t < phase_tiles(p, kPhase)) phase_tile<TL, kPhase, kSplit>(p, t, lds);
 }
 
-// Two phases of different matrices in one launch: on every XCD an eighth of the
-// tiles of the first, the longer ones, then an eighth of the second's.
-template <class TL, int kPhase0, int kPhase1>
-__global__ __launch_bounds__(TL::THREADS) void ortho_pair_kernel(Ortho p0, Ortho p1) {
-  __shared__ __attribute__((aligned(1024))) char lds[tile_lds<TL>()];
-  const int xcd = blockIdx.x & 7, i = blockIdx.x >> 3;
-  const int n0 = phase_tiles(p0, kPhase0), each0 = (n0 + 7) >> 3, n1 = phase_tiles(p1, kPhase1), each1 = (n1 + 7) >> 3;
-  if (i < each0) {
-    const int t = xcd * each0 + i;
-    if (t < n0) phase_tile<TL, kPhase0, false>(p0, t, lds);
-  } else {
-    const int t = xcd * each1 + i - each0;
-    if (t < n1) phase_tile<TL, kPhase1, false>(p1, t, lds);
-  }
-}
-
 unsigned grid8(int64_t n) { return (unsigned)((n + 7) & ~int64_t(7)); }
 
 template <class TL>
@@ -462,25 +446,6 @@ void run_class(const Ortho& p, int cls, int phase, hipStream_t s) {
     run_phase<DeepTile>(p, phase, s);
 }
 
-// Phase `phase` of lead with the one before it of p.
-void run_pair(Ortho lead, Ortho p, int phase, hipStream_t s) {
-  using TL = BigTile;
-  set_tiles<TL>(lead);
-  set_tiles<TL>(p);
-  const int other = phase == PHASE_A ? PHASE_X : phase == PHASE_B ? PHASE_A : PHASE_B;
-  const unsigned grid = grid8(phase_tiles(lead, phase)) + grid8(phase_tiles(p, other));
-  if (phase == PHASE_A)
-    ortho_pair_kernel<TL, PHASE_A, PHASE_X><<<grid, TL::THREADS, 0, s>>>(lead, p);
-  else if (phase == PHASE_B)
-    ortho_pair_kernel<TL, PHASE_A, PHASE_B><<<grid, TL::THREADS, 0, s>>>(p, lead);
-  else if (phase == PHASE_X)
-    ortho_pair_kernel<TL, PHASE_X, PHASE_B><<<grid, TL::THREADS, 0, s>>>(lead, p);
-  else if (phase == PHASE_OUT)
-    ortho_pair_kernel<TL, PHASE_OUT, PHASE_B><<<grid, TL::THREADS, 0, s>>>(lead, p);
-  else
-    ortho_pair_kernel<TL, PHASE_OUT_T, PHASE_B><<<grid, TL::THREADS, 0, s>>>(lead, p);
-}
-
 void set_step(Ortho& p, const OrthoStep* step, int steps, int k) {
   const OrthoStep& c = step[k];
   p.cur = k & 1;
@@ -518,35 +483,13 @@ int update_class(const Ortho& p) {
   auto tiles = [&](int64_t side) { return cdiv64(p.m, side) * cdiv64(p.np, side) * p.count; };
   return class_of(tiles(256), tiles(128), p.split || p.mp <= 512);
 }
-// Two phases a launch: the matrix instructions of one run under the other's
-// traffic (an update moves 8 bytes a value in its epilogue), and rounds end in
-// common.  That pays for wide matrices, whose update is the longest phase, with
-// four rounds of big tiles of it (12 x 2048 x 4096: 4300 us, 4630 one by one; 8 of
-// them 3075 and 3200; 32 x 1024 x 3000: 2735 and 2885), and not for square or
-// small ones (64 x 1024 x 1024: 2490 and 2420; 100 x 512 x 2048: 2200 and 2135).
-bool pays_to_pair(const Ortho& p) {
-  const int64_t m = cdiv64(p.m, 256), n = cdiv64(p.np, 256);
-  return p.count >= 2 && m >= 4 && n >= 2 * m && m * n * p.count >= 1024 && update_class(p) == TILE_BIG;
-}
-void skip_matrices(Ortho& p, int64_t n) {
-  const int64_t x = n * p.m * p.np, a = n * p.m * p.mp;
-  p.b0 += n;
-  for (int i = 0; i < 2; ++i) {
-    p.x16[i] += x;
-    p.lo16[i] += x;
-  }
-  p.a16 += a;
-  p.b16 += a;
-  p.da += n * p.m;
-  p.db += n * p.m;
-}
 }  // namespace
 
 OrthoForm ortho_form(const Ortho& in, int64_t count) {
   Ortho p = in;
   p.count = (int)count;
   p.split = ortho_split(p.m);
-  return OrthoForm{gram_class(p), update_class(p), p.split, pays_to_pair(p)};
+  return OrthoForm{gram_class(p), update_class(p), p.split};
 }
 
 // Matrices at a time: enough tiles of the update for several rounds of the
@@ -558,6 +501,12 @@ int64_t ortho_group(int64_t batch, int64_t m, int64_t n) {
   return batch < g ? batch : g;
 }
 
+// One phase a launch.  Two of them in one, two halves of the matrices a phase
+// apart, so that one's traffic would run under the other's matrix instructions, is
+// slower mostly: its rounds of the chip are others, by chance fewer or more (12 x
+// 2048 x 3584: 3951 us, 4378 one by one; 8 x 2048 x 4096 3035 and 3123; 32 x 1024 x
+// 2048 2020 and 2040; but 7 x 2048 x 4096 2722 and 2559, 64 x 1024 x 1024 2445 and
+// 2390, 58 x 1024 x 2560 4919 and 4228, 4 x 2048 x 8192 3406 and 2945).
 hipError_t launch_orthogonalize(const Ortho& in, const OrthoStep* step, int steps, int64_t batch, int64_t group,
                                 hipStream_t s) {
   for (int64_t b0 = 0; b0 < batch; b0 += group) {
@@ -571,30 +520,11 @@ hipError_t launch_orthogonalize(const Ortho& in, const OrthoStep* step, int step
     ortho_norm_kernel<<<(unsigned)(p.count * p.chunks), 256, 0, s>>>(p);
     ortho_init_kernel<<<(unsigned)((int64_t)p.count * (p.np / 64) * cdiv64(p.m, 64)), 256, 0, s>>>(p);
     const int out = p.tall ? PHASE_OUT_T : PHASE_OUT;
-    if (form.paired) {
-      // the second half of the matrices one phase behind the first
-      Ortho q[2] = {p, p};
-      q[0].count = (p.count + 1) / 2;
-      q[1].count = p.count - q[0].count;
-      skip_matrices(q[1], q[0].count);
-      auto phase_of = [&](int i) { return i % 3 < 2 ? i % 3 : i / 3 + 1 < steps ? PHASE_X : out; };
-      for (int i = 0; i <= 3 * steps; ++i) {
-        if (i < 3 * steps) set_step(q[0], step, steps, i / 3);
-        if (i > 0) set_step(q[1], step, steps, (i - 1) / 3);
-        if (i == 0)
-          run_class(q[0], TILE_BIG, PHASE_A, s);
-        else if (i < 3 * steps)
-          run_pair(q[0], q[1], phase_of(i), s);
-        else
-          run_class(q[1], TILE_BIG, out, s);
-      }
-    } else {
-      for (int k = 0; k < steps; ++k) {
-        set_step(p, step, steps, k);
-        run_class(p, form.gram, PHASE_A, s);
-        run_class(p, form.gram, PHASE_B, s);
-        run_class(p, form.update, k + 1 < steps ? PHASE_X : out, s);
-      }
+    for (int k = 0; k < steps; ++k) {
+      set_step(p, step, steps, k);
+      run_class(p, form.gram, PHASE_A, s);
+      run_class(p, form.gram, PHASE_B, s);
+      run_class(p, form.update, k + 1 < steps ? PHASE_X : out, s);
     }
     const hipError_t e = hipGetLastError();
     if (e != hipSuccess) return e;

@@ -47,7 +47,7 @@ def definition(x, steps):
     return x.t() if tall else x
 
 
-# small, two kinds of medium and large tiles, and two halves one phase apart, wide and tall
+# every size of tiles, wide and tall
 @pytest.mark.parametrize("B,shape", [(3, (700, 900)), (6, (1000, 1000)), (6, (1000, 1300)), (4, (2048, 2048)),
                                      (4, (2100, 2000)), (8, (2048, 4096)), (9, (4090, 2000))])
 @pytest.mark.parametrize("steps", [5, 2])
