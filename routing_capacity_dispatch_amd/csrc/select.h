@@ -96,7 +96,7 @@ __device__ __forceinline__ void select_topk_of(Row&& row, const float* __restric
     // at least 1 (only one NaN pattern maps to 0), so with k <= E every
     // round finds a present expert
     key[i] = i * 64 + lane < E ? max(score_key(v[i] + b[i]), 1u) : 0u;
-  mine = -1;
+  int own = -1;
   for (int j = 0; j < k; ++j) {
     uint32_t best = 0;
 #pragma unroll
@@ -115,13 +115,14 @@ __device__ __forceinline__ void select_topk_of(Row&& row, const float* __restric
       for (int i = 0; i < NPER; ++i)
         if (i == (e >> 6)) key[i] = 0;
     }
-    if (lane == j) mine = e;
+    if (lane == j) own = e;
   }
   const bool sel = lane < k;
-  const float l = sel ? row(mine) : -INFINITY;
+  const float l = sel ? row(own) : -INFINITY;
   const float m = wave_max(l);
   const float ex = sel ? expf(l - m) : 0.0f;
   const float sum = wave_sum(ex);
+  mine = own;
   gate = ex / sum;
 }
 
