@@ -2151,7 +2151,8 @@ moe_status check_linear_grad(const moe_linear_grad* a) {
   if (st == MOE_OK && a->M > kMaxSlopeRows) st = MOE_ERR_UNSUPPORTED;
   // both products and the sums of db are one launch
   if (st == MOE_OK &&
-      (ceil_div(a->N, 128) + ceil_div(a->M, 128)) * ceil_div(a->K, 128) + ceil_div(a->N, 64) > kMaxListEntries - 16)
+      ((a->dw ? ceil_div(a->N, 128) : 0) + (a->dx ? ceil_div(a->M, 128) : 0)) * ceil_div(a->K, 128) +
+              (a->db ? ceil_div(a->N, 64) : 0) > kMaxListEntries - 16)
     st = MOE_ERR_UNSUPPORTED;
   if (st == MOE_OK) st = check_ld(a->lddy, a->N);
   if (st == MOE_OK && a->act != MOE_ACT_NONE) st = check_ld(a->ldp, a->N);

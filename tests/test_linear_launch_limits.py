@@ -35,6 +35,8 @@ def test_forward(lib, over, status):
     (dict(M=1 << 20, K=1 << 15, ldx=(1 << 15) + 1, dw=None), WS),
     # dx and dw in one launch, each alone below the limit
     (dict(M=1 << 15, N=1 << 15, K=1 << 21, lddy=1 << 15, ldp=1 << 15), UNS),
+    (dict(M=1 << 15, N=1 << 15, K=1 << 21, lddy=1 << 15, ldp=1 << 15, dw=None), WS),
+    (dict(M=1 << 15, N=1 << 15, K=1 << 21, lddy=1 << 15, ldp=1 << 15, dx=None), WS),
     (dict(M=1 << 14, N=1 << 15, K=1 << 21, lddy=1 << 15, ldp=1 << 15), WS)])
 def test_backward(lib, over, status):
     K = over["K"]
