@@ -329,7 +329,8 @@ def combine_dropless(cfg, expert_out, row_of, gates, y_latent=None):
 
 
 class ForwardDropless:
-    """Reusable dropless forward call (weights, workspace and outputs bound once)."""
+    """Reusable dropless forward call (weights, workspace and outputs bound once).
+    For at most 16 tokens ForwardFew is faster."""
 
     def __init__(self, cfg, weights: Dict[str, torch.Tensor], device, taps=False):
         self.cfg = cfg

@@ -455,6 +455,9 @@ __global__ __launch_bounds__(256) void pack_rows_kernel(PackRows a, PackRows b, 
 
 // d = dy act'(pre) as bf16 rows of ldd (zeros past N), and sums of d (before
 // its rounding) over the rows of each block of kSlopeRows: part [blocks][N].
+// bf16 is what the matrix instructions take beside x and W: the rounding is as
+// large as that of the results (together 0.0024 of their norm, 0.0017 without it);
+// d in two bf16 numbers would be without it for twice the matrix instructions.
 constexpr int kSlopeRows = 32;
 struct Slope {
   const void* dy;
